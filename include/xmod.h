@@ -401,6 +401,125 @@ XMOD_API int xmod_router_topk_noalloc(const xmod_dims* dims, int K, const void* 
                                       const void* w_r, const float* bias, int32_t* idx,
                                       float* r_sel, int* status_out, void* stream);
 
+/* ---------------------------------------------------------------- generation
+ * Operators of a generation step around the layers above, for callers that produce one
+ * token at a time: a key/value cache per layer, attention over it, and the log
+ * probabilities at the end of the stack. The pages have no counterpart; the rules that
+ * shape them are theirs: a sparse layer under the causal threshold rule (xmod_routing)
+ * caches the tokens it routed only, so a sequence's length differs from layer to layer
+ * and a token's index in a layer's cache (its slot) is not its position.
+ *
+ * Format of a cache's values. NATIVE: dims->dtype. E4M3 (with dims->dtype bf16): 8-bit
+ * floating point (4 exponent bits, 3 mantissa bits, largest value 448) with one fp32
+ * scale per slot and KV head; a code stands for code * scale. */
+typedef enum { XMOD_CACHE_NATIVE = 0, XMOD_CACHE_E4M3 = 1 } xmod_cache_format;
+
+/* One layer's paged key/value cache (device pointers, 16-byte aligned, caller-owned).
+ *   k, v      [n_pages, n_kv_heads, page_size, head_dim]
+ *   k_scale, v_scale  [n_pages, n_kv_heads, page_size] fp32 for E4M3, else NULL
+ *   table     [n_seqs, max_pages] int32: slot i of sequence s lies in page
+ *             table[s, i / page_size] at row i % page_size. Entries that no used slot
+ *             needs are never read (they may hold anything).
+ * page_size must be a multiple of 16, max_pages * page_size below 2^31. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  const int32_t* table;
+  int n_pages, page_size, n_seqs, max_pages;
+  int format;
+} xmod_kv_cache;
+
+/* Append M new tokens to the cache. Row m of qkv holds a token's projections q | k | v
+ * (q heads from column 0, k heads from n_heads * head_dim, v heads after them; row stride
+ * ldqkv elements). Every q and k head is QK-normalised and rotated as in the layers
+ * (w->q_norm, w->k_norm, w->rope_theta; the other weights are not read; w NULL: neither)
+ * at position pos[m]; k and v are written to slot slot[m] of sequence seq[m], q to q_out.
+ * Everything is computed in fp32 and rounded once, to the type it is stored in; E4M3
+ * stores scale = max|x| / 448 over the head's values and the codes nearest to x / scale
+ * (ties to even). A head of zeros gets scale 0 (as do values below 2^-117, which are
+ * stored as zeros); a head with an infinity or NaN gets a NaN scale and NaN codes.
+ *   seq     [M] int32, or NULL (row m belongs to sequence m). A negative entry skips
+ *           its row: nothing of it is read or written (q_out's row keeps its values).
+ *   slot    [M] int32; the rows of one call must address distinct slots
+ *   pos     [M] int32, or NULL (pos = slot)
+ *   q_out   [M, n_heads * head_dim], row stride ldq (dtype), or NULL (q is not wanted);
+ *           may be qkv itself with ldq = ldqkv (q in place), else must not overlap it
+ * A row whose sequence is not below n_seqs, whose slot is outside [0, max_pages *
+ * page_size) or whose page is outside [0, n_pages) is skipped and reported through
+ * status_out (a device int, or NULL) as for xmod_gather. Row strides must be multiples
+ * of 8. head_dim must be 32, 64 or 128. M = 0 does nothing. */
+XMOD_API int xmod_cache_append(const xmod_dims* dims, const xmod_kv_cache* cache, int M,
+                               const void* qkv, int ldqkv, const xmod_layer_weights* w,
+                               const int32_t* seq, const int32_t* slot, const int32_t* pos,
+                               void* q_out, int ldq, int* status_out, void* stream);
+
+/* Bytes of workspace xmod_cache_attention needs for up to M rows (0 for invalid dims or
+ * M < 0). The lengths do not enter. */
+XMOD_API size_t xmod_cache_attention_workspace_bytes(const xmod_dims* dims, int M);
+
+/* Attention of one query token per row over the cache:
+ *   o[m, h] = sum_i p_i V[i, g],  p = softmax over i < len[m] of q[m, h] . K[i, g] / sqrt(head_dim)
+ * with i the slots of sequence seq[m] and g = h / (n_heads / n_kv_heads).
+ *   q       [M, n_heads * head_dim], row stride ldq (dtype): rotated queries, as
+ *           xmod_cache_append writes them
+ *   seq     [M] int32, or NULL (row m reads sequence m). A negative entry skips its row:
+ *           o and lse keep their values there. Rows may share a sequence (several new
+ *           tokens of it, each with its own len).
+ *   len     [M] int32: slots the row attends to, 0 .. max_pages * page_size. With 0 the
+ *           row of o is zero and lse is -infinity.
+ *   o       [M, n_heads * head_dim] (dtype)
+ *   lse     [M, n_heads] fp32: ln sum_i exp(q . K_i / sqrt(head_dim)), or NULL
+ * Slots at or after len[m] have no influence, whatever their pages hold. The cache is
+ * read in fp32-accumulated products; the probabilities are not rounded below 16 bits of
+ * mantissa with at most 8 query heads per KV head (11 bits for E4M3, or with more heads).
+ * Device checks (status word of ws): a sequence not below n_seqs skips its row; a len
+ * outside its range is clamped into it; a page outside [0, n_pages) is read as page 0.
+ * The result does not depend on the other rows of the call beyond fp32 rounding, and two
+ * calls with the same arguments give the same bits.
+ *   ws      xmod_cache_attention_workspace_bytes(dims, M) bytes; concurrent calls need one
+ *           each. head_dim must be 32, 64 or 128. M = 0 does nothing. */
+XMOD_API int xmod_cache_attention(const xmod_dims* dims, const xmod_kv_cache* cache, int M,
+                                  const void* q, int ldq, const int32_t* seq,
+                                  const int32_t* len, void* o, float* lse, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Log probabilities of given tokens under logits [N, V] (dtype; row stride ld >= V, any
+ * value), in natural logarithms, from one reading of the logits:
+ *   lse     [N] fp32: ln sum_v exp(x_v)
+ *   logp    [N] fp32: x_target - lse; 0 where target is negative (no token)
+ *   entropy [N] fp32: -sum_v p_v ln p_v (a token at -infinity contributes 0)
+ *   top_idx, top_logp [N, top_k]: the top_k largest logits in descending order, ties to
+ *           the lower token (-0 equals +0), and their log probabilities
+ * Every output may be NULL (logp and target go together; top_idx and top_logp too;
+ * top_k = 0 without them). top_k is at most min(V, XMOD_MAX_TOP_K). The sums are fp32.
+ * Checked on the device and reported through status_out (a device int, or NULL; see
+ * xmod_gather): a target not below V gives a NaN logp; a row that holds a NaN or
+ * +infinity, or nothing above -infinity, has no distribution: its lse, logp, entropy and
+ * top_logp are NaN (its top_idx rank a NaN above +infinity). logits and the outputs must be
+ * 16-byte aligned, rows need not be. N = 0 does nothing. */
+#define XMOD_MAX_TOP_K 64
+
+XMOD_API int xmod_token_logprobs(xmod_dtype dtype, int64_t N, int V, const void* logits,
+                                 int64_t ld, const int32_t* target, float* logp,
+                                 float* entropy, float* lse, int top_k, int32_t* top_idx,
+                                 float* top_logp, int* status_out, void* stream);
+
+/* Gradient of sum_n g_logp[n] logp[n] + g_entropy[n] entropy[n] at the logits:
+ *   dlogits[n, v] = g_logp (1[v = target] - p_v) - g_entropy p_v (ln p_v + entropy)
+ * p_v = exp(x_v - lse[n]), with lse and entropy as xmod_token_logprobs wrote them.
+ *   target     [N], negative: no token, g_logp[n] counts as 0
+ *   g_logp     [N] fp32, or NULL (zeros; target is then not read and may be NULL)
+ *   g_entropy  [N] fp32, or NULL (zeros; entropy is then not read and may be NULL)
+ *   dlogits    [N, V] (dtype), row stride ldd >= V; may be logits itself (ldd = ld), else
+ *              must not overlap it. Columns from V to ldd are not written.
+ * A row whose two gradients are zero (or absent) gets zeros, whatever its logits. A
+ * target not below V counts as negative and is reported through status_out. */
+XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const void* logits,
+                                     int64_t ld, const int32_t* target, const float* lse,
+                                     const float* entropy, const float* g_logp,
+                                     const float* g_entropy, void* dlogits, int64_t ldd,
+                                     int* status_out, void* stream);
+
 /* ---------------------------------------------------------------- failure detection
  * Not part of the method. Every wait inside the library's tcgen05 kernels (on an
  * mbarrier, or on a flag another CTA sets) gives up after 2 s without progress: the

@@ -28,6 +28,8 @@ inline size_t esize(xmod_dtype dt) { return dt == XMOD_BF16 ? 2 : 4; }
 inline bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
 inline bool aligned16_or_null(const void* p) { return !p || ((uintptr_t)p & 15u) == 0; }
 
+}  // namespace
+
 bool dims_ok(const xmod_dims* dm) {
   if (!dm) return false;
   if (dm->dtype != XMOD_BF16 && dm->dtype != XMOD_FP32) return false;
@@ -43,6 +45,8 @@ bool dims_ok(const xmod_dims* dm) {
 }
 
 bool head_dim_supported(int hd) { return hd == 32 || hd == 64 || hd == 128; }
+
+namespace {
 
 // Row stride (elements) of the transposed values for n tokens: 16-byte multiple.
 inline int vt_ld(int n) { return (n + 7) / 8 * 8; }

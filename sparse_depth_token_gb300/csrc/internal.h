@@ -40,6 +40,12 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// ---------------------------------------------------------------- argument checks
+
+// Sizes, type and eps valid (the widths multiples of 8, the query heads of the KV heads).
+bool dims_ok(const xmod_dims* dm);
+bool head_dim_supported(int hd);
+
 // ---------------------------------------------------------------- TMA tensor maps
 
 bool tma_available();
@@ -66,6 +72,18 @@ class ProfScope {
   cudaStream_t stream_;
   cudaEvent_t start_ = nullptr;
 };
+
+// One kernel launch of an entry point on context c: counted, optionally timed, checked.
+#define XMOD_LAUNCH(c, kind, expr)               \
+  do {                                           \
+    cudaError_t _e;                              \
+    {                                            \
+      ::xmod::ProfScope _p(kind, (c).stream);    \
+      _e = (expr);                               \
+    }                                            \
+    ::xmod::count_launch();                      \
+    if (_e != cudaSuccess) return XMOD_ERR_CUDA; \
+  } while (0)
 
 // ---------------------------------------------------------------- routing and row kernels
 

@@ -25,7 +25,12 @@ EXPORTS = ("xmod_version", "xmod_status_string", "xmod_workspace_bytes", "xmod_r
            "xmod_profile_enable", "xmod_profile_read", "xmod_router_topk_noalloc",
            "xmod_stack_fwd_ex", "xmod_layer_fwd_threshold", "xmod_stack_fwd_sched",
            "xmod_bwd_workspace_bytes", "xmod_layer_bwd", "xmod_stack_bwd_workspace_bytes",
-           "xmod_stack_bwd", "xmod_selftest_wait_timeout")
+           "xmod_stack_bwd", "xmod_selftest_wait_timeout", "xmod_cache_append",
+           "xmod_cache_attention_workspace_bytes", "xmod_cache_attention", "xmod_token_logprobs",
+           "xmod_token_logprobs_bwd")
+
+CACHE_NATIVE, CACHE_E4M3 = 0, 1
+MAX_TOP_K = 64   # alternatives token_logprobs reports at most
 
 # Largest B*T the allocation-free router entry point accepts (its fixed scratch).
 NOALLOC_MAX_TOKENS = 2 * 1024 * 1024
@@ -63,6 +68,13 @@ ROUTE_TOPK, ROUTE_THRESHOLD = 0, 1
 class StackOpts(ctypes.Structure):
     _fields_ = [("bias_step", ctypes.c_float), ("layer_stats", ctypes.c_void_p),
                 ("update_hist", ctypes.c_void_p), ("routing", ctypes.c_int)]
+
+
+class KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("format", ctypes.c_int)]
 
 
 class KernelTime(ctypes.Structure):
@@ -141,6 +153,20 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                  ctypes.POINTER(LayerWeights), ctypes.c_int, _VP, _VP, _VP,
                                  ctypes.c_float, _VP, ctypes.POINTER(LayerGrads), _VP, _VP,
                                  ctypes.c_size_t, _VP]
+    L.xmod_cache_append.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(KVCache), ctypes.c_int,
+                                    _VP, ctypes.c_int, ctypes.POINTER(LayerWeights), _VP, _VP,
+                                    _VP, _VP, ctypes.c_int, _VP, _VP]
+    L.xmod_cache_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.xmod_cache_attention_workspace_bytes.argtypes = [ctypes.POINTER(Dims), ctypes.c_int]
+    L.xmod_cache_attention.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(KVCache),
+                                       ctypes.c_int, _VP, ctypes.c_int, _VP, _VP, _VP, _VP, _VP,
+                                       ctypes.c_size_t, _VP]
+    L.xmod_token_logprobs.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int, _VP,
+                                      ctypes.c_int64, _VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP,
+                                      _VP, _VP]
+    L.xmod_token_logprobs_bwd.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int, _VP,
+                                          ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, _VP,
+                                          ctypes.c_int64, _VP, _VP]
     _lib = L
     return L
 
@@ -344,6 +370,135 @@ def stack_bwd(dm, K, A, N0, N1, gate, layers, x, bias, dy, route_coef, dx, grads
         ctypes.byref(dm), int(K), float(A), int(N0), int(N1), int(gate), arr, len(layers), _p(x),
         _p(bias), _p(dy), float(route_coef), _p(dx), garr, _p(checkpoints), _p(ws), _wsb(ws),
         _stream(stream)))
+
+
+def kv_cache(k, v, table, k_scale=None, v_scale=None) -> KVCache:
+    """KVCache from device tensors: k, v [n_pages, n_kv_heads, page_size, head_dim]
+    contiguous (with k_scale / v_scale [n_pages, n_kv_heads, page_size] fp32: e4m3 codes,
+    one byte each), table [n_seqs, max_pages] int32 contiguous. The struct keeps the
+    tensors, so their memory outlives every call using it."""
+    e4m3 = k_scale is not None
+    ts = (k, v, table) + ((k_scale, v_scale) if e4m3 else ())
+    if (any(t is None or not t.is_cuda or not t.is_contiguous() for t in ts) or k.dim() != 4 or table.dim() != 2
+            or k.shape != v.shape or k.dtype != v.dtype or _dtype_name(table) != "int32"
+            or (e4m3 and (k.element_size() != 1 or k_scale.shape != k.shape[:3]
+                          or v_scale.shape != k.shape[:3] or _dtype_name(k_scale) != "float32"
+                          or _dtype_name(v_scale) != "float32"))):
+        raise XmodError("kv_cache", ERR_INVALID_ARG)
+    c = KVCache(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(table), k.shape[0], k.shape[2],
+                table.shape[0], table.shape[1], CACHE_E4M3 if e4m3 else CACHE_NATIVE)
+    c._keep = ts
+    c._layout = (k.shape[1], k.shape[3], "e4m3" if e4m3 else _dtype_name(k))
+    return c
+
+
+_NAMES = {}
+
+
+def _dtype_name(t) -> str:
+    """"bfloat16", "int32", ... of a tensor's dtype."""
+    name = _NAMES.get(t.dtype)
+    if name is None:
+        name = _NAMES[t.dtype] = str(t.dtype).rsplit(".", 1)[-1]
+    return name
+
+
+def _is(t, name, shape=None) -> bool:
+    """Whether an optional tensor argument is absent, or a contiguous device tensor of that
+    dtype and shape."""
+    return t is None or (t.is_cuda and _dtype_name(t) == name and t.is_contiguous()
+                         and (shape is None or tuple(t.shape) == shape))
+
+
+def _rows(t, name, width) -> bool:
+    """Whether t is a [rows, width] device tensor of that dtype with contiguous rows."""
+    return (t.is_cuda and t.dim() == 2 and _dtype_name(t) == name and t.shape[1] == width
+            and (t.stride(1) == 1 or width == 1))
+
+
+_ELEM = {BF16: "bfloat16", FP32: "float32"}
+
+
+def _ld(t) -> int:
+    """Row stride of a [rows, width] tensor (a single row's stride is its width)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def cache_append(dm, cache: KVCache, qkv, w, seq, slot, pos=None, q_out=None, status=None,
+                 stream=None):
+    """xmod_cache_append: the rows of qkv [M, (n_heads + 2 n_kv_heads) head_dim] into the
+    cache, their transformed q into q_out (None: not wanted). w: a LayerWeights (its QK-norm
+    gains and rope_theta count) or None. status: as for gather."""
+    M = qkv.shape[0]
+    el = _ELEM.get(dm.dtype)
+    qw = dm.n_heads * dm.head_dim
+    if (not _rows(qkv, el, qw + 2 * dm.n_kv_heads * dm.head_dim)
+            or not _is(seq, "int32", (M,)) or slot is None or not _is(slot, "int32", (M,))
+            or not _is(pos, "int32", (M,))
+            or (q_out is not None and not (_rows(q_out, el, qw) and q_out.shape[0] == M))
+            or cache._layout[:2] != (dm.n_kv_heads, dm.head_dim)
+            or cache._layout[2] not in ("e4m3", el)):
+        raise XmodError("xmod_cache_append", ERR_INVALID_ARG)
+    _check("xmod_cache_append", load().xmod_cache_append(
+        ctypes.byref(dm), ctypes.byref(cache), M, _p(qkv), _ld(qkv),
+        ctypes.byref(w) if w is not None else None, _p(seq), _p(slot), _p(pos), _p(q_out),
+        _ld(q_out) if q_out is not None else 0, _p(status), _stream(stream)))
+
+
+def cache_attention_workspace_bytes(dm: Dims, M: int) -> int:
+    return int(load().xmod_cache_attention_workspace_bytes(ctypes.byref(dm), int(M)))
+
+
+def cache_attention(dm, cache: KVCache, q, seq, lens, o, ws, lse=None, stream=None):
+    """xmod_cache_attention: o [M, n_heads head_dim] (and lse [M, n_heads] fp32) of the
+    queries q over the first lens[m] slots of sequence seq[m] (None: m)."""
+    M = q.shape[0]
+    el = _ELEM.get(dm.dtype)
+    qw = dm.n_heads * dm.head_dim
+    if (not _rows(q, el, qw) or lens is None or not _is(seq, "int32", (M,))
+            or not _is(lens, "int32", (M,)) or o is None or not _is(o, el, (M, qw))
+            or not _is(lse, "float32", (M, dm.n_heads))
+            or cache._layout[:2] != (dm.n_kv_heads, dm.head_dim)
+            or cache._layout[2] not in ("e4m3", el)):
+        raise XmodError("xmod_cache_attention", ERR_INVALID_ARG)
+    _check("xmod_cache_attention", load().xmod_cache_attention(
+        ctypes.byref(dm), ctypes.byref(cache), M, _p(q), _ld(q), _p(seq), _p(lens), _p(o),
+        _p(lse), _p(ws), _wsb(ws), _stream(stream)))
+
+
+_DTYPES = {"bfloat16": BF16, "float32": FP32}
+
+
+def token_logprobs(logits, target=None, logp=None, entropy=None, lse=None, top_idx=None,
+                   top_logp=None, status=None, stream=None):
+    """xmod_token_logprobs: logits [N, V] bf16 or fp32 (rows may be strided); the outputs
+    that are given are written (logp, entropy, lse [N] fp32, top_idx int32 and top_logp
+    fp32 [N, k])."""
+    N, V = logits.shape
+    k = 0 if top_idx is None else top_idx.shape[1]
+    dt = _DTYPES.get(_dtype_name(logits), -1)
+    if (not _rows(logits, _dtype_name(logits), V) or not _is(target, "int32", (N,))
+            or not all(_is(t, "float32", (N,)) for t in (logp, entropy, lse))
+            or not _is(top_idx, "int32", (N, k)) or not _is(top_logp, "float32", (N, k))):
+        raise XmodError("xmod_token_logprobs", ERR_INVALID_ARG)
+    _check("xmod_token_logprobs", load().xmod_token_logprobs(
+        dt, N, V, _p(logits), _ld(logits), _p(target), _p(logp), _p(entropy), _p(lse), k,
+        _p(top_idx), _p(top_logp), _p(status), _stream(stream)))
+
+
+def token_logprobs_bwd(logits, target, lse, g_logp, dlogits, entropy=None, g_entropy=None,
+                       status=None, stream=None):
+    """xmod_token_logprobs_bwd: dlogits [N, V] of the gradients g_logp and g_entropy [N]
+    (either may be None); dlogits may be logits itself."""
+    N, V = logits.shape
+    name = _dtype_name(logits)
+    if (not _rows(logits, name, V) or not _rows(dlogits, name, V) or dlogits.shape[0] != N
+            or not _is(target, "int32", (N,))
+            or not all(_is(t, "float32", (N,)) for t in (lse, entropy, g_logp, g_entropy))):
+        raise XmodError("xmod_token_logprobs_bwd", ERR_INVALID_ARG)
+    _check("xmod_token_logprobs_bwd", load().xmod_token_logprobs_bwd(
+        _DTYPES.get(name, -1), N, V, _p(logits), _ld(logits), _p(target), _p(lse), _p(entropy),
+        _p(g_logp), _p(g_entropy), _p(dlogits), _ld(dlogits), _p(status), _stream(stream)))
 
 
 def selftest_wait_timeout(ws, stream=None):
