@@ -469,9 +469,9 @@ XMOD_API size_t xmod_cache_attention_workspace_bytes(const xmod_dims* dims, int 
  *           row of o is zero and lse is -infinity.
  *   o       [M, n_heads * head_dim] (dtype)
  *   lse     [M, n_heads] fp32: ln sum_i exp(q . K_i / sqrt(head_dim)), or NULL
- * Slots at or after len[m] have no influence, whatever their pages hold. The cache is
- * read in fp32-accumulated products; the probabilities are not rounded below 16 bits of
- * mantissa with at most 8 query heads per KV head (11 bits for E4M3, or with more heads).
+ * Slots at or after len[m] have no influence, whatever their pages hold. Products are
+ * accumulated in fp32; the probabilities keep at least 16 bits of mantissa (11 with E4M3
+ * and more than 8 query heads per KV head) where they weight the values.
  * Device checks (status word of ws): a sequence not below n_seqs skips its row; a len
  * outside its range is clamped into it; a page outside [0, n_pages) is read as page 0.
  * The result does not depend on the other rows of the call beyond fp32 rounding, and two

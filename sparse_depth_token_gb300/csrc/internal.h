@@ -54,6 +54,10 @@ bool tma_available();
 // swizzle; reads outside the tensor return zeros.
 bool tma_map_bf16(CUtensorMap* m, const void* base, int rank, const int64_t* dims,
                   const int64_t* strides_bytes, const int* box);
+// Tensor map of contiguous rows [rows, cols] of bf16 (esize 2) or bytes (esize 1); box
+// rows of 32, 64 or 128 bytes, swizzled over their own width.
+bool tma_map_rows(CUtensorMap* m, const void* base, int esize, int64_t rows, int cols, int box_cols,
+                  int box_rows);
 
 // ---------------------------------------------------------------- measurement
 
