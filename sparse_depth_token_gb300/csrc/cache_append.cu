@@ -55,95 +55,158 @@ struct AppendArgs {
   int* status;
 };
 
-// One warp per (row, head); lane l holds dimensions l, l + 32, ...
+// Bound: memory. A token's (hq + 2 hkv) hd elements are read once and written once, the
+// arithmetic (7 operations an element) is far below what that takes. So every thread moves
+// two 16-byte vectors: V elements c .. c + V - 1 of a head and their rotation partners
+// hd/2 further, LPH = hd / (2 V) lanes to a head, and a CTA holds as many tokens as fill
+// about 256 threads, which keeps an SM's 2048 threads loading. The angles of a token are
+// the same for all its heads: HD/2 threads compute them once into shared memory while the
+// vectors are on their way.
 template <typename T, int HD, bool FP8>
-__global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a, Turns turns) {
-  constexpr int E = HD / 32;
-  const int heads = a.hq + 2 * a.hkv;
-  const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (item >= (int64_t)a.M * heads) return;
-  const int m = (int)(item / heads), h = (int)(item % heads);
-  const int seq = a.seq ? a.seq[m] : m;
-  if (seq < 0) return;
-  const int slot = a.slot[m];
+__global__ void __launch_bounds__(512, 3)
+cache_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, int rows_per_cta) {
+  constexpr int V = 16 / sizeof(T), LPH = HD / (2 * V), HALF = HD / 2;
+  __shared__ float2 angle[8][HALF];
+  const int heads = a.hq + 2 * a.hkv, units = heads * LPH;
+  const int64_t m0 = (int64_t)blockIdx.x * rows_per_cta;
+  const int rows = (int)min((int64_t)rows_per_cta, a.M - m0), total = rows * units;
   const xmod_kv_cache& c = a.cache;
-  if (seq >= c.n_seqs || slot < 0 || slot >= c.max_pages * c.page_size) {
-    if (lane == 0) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-    return;
-  }
-  const int page = c.table[(int64_t)seq * c.max_pages + slot / c.page_size];
-  if (page < 0 || page >= c.n_pages) {
-    if (lane == 0) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-    return;
-  }
-  const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
-  if (is_q && !a.q_out) return;
-  const T* src = (const T*)a.qkv + (int64_t)m * a.ldqkv + (int64_t)h * HD;
-  float v[E];
-  for (int e = 0; e < E; ++e) v[e] = Elem<T>::to_f(src[lane + 32 * e]);
-  const T* gain = is_v ? nullptr : (const T*)(is_q ? a.q_gain : a.k_gain);
-  if (gain) {
-    float ss = 0.f;
-    for (int e = 0; e < E; ++e) ss = fmaf(v[e], v[e], ss);
-    const float inv = rsqrtf(warp_sum(ss) / (float)HD + a.eps);
-    for (int e = 0; e < E; ++e) v[e] = v[e] * inv * Elem<T>::to_f(gain[lane + 32 * e]);
-  }
-  if (a.rope && !is_v) {
-    const int pos = a.pos ? a.pos[m] : slot;
-    for (int e = 0; e < E; ++e) {
-      const int d = lane + 32 * e, c2 = d % (HD / 2);
-      const float2 cs = rotation(turns.f[c2], pos);
-      float other;
-      if (HD == 32) {
-        other = __shfl_xor_sync(0xffffffffu, v[e], 16);
-        v[e] = d < HD / 2 ? v[e] * cs.x - other * cs.y : v[e] * cs.x + other * cs.y;
-      } else if (e < E / 2) {
-        other = v[(e + E / 2) % E];
-        const float lo = v[e] * cs.x - other * cs.y, hi = other * cs.x + v[e] * cs.y;
-        v[e] = lo;
-        v[(e + E / 2) % E] = hi;
+  pdl_trigger();
+  pdl_wait();
+
+  for (int u0 = 0; u0 < total; u0 += blockDim.x) {
+    const int u = u0 + threadIdx.x;
+    const int lr = min(u, total - 1) / units, un = min(u, total - 1) % units;
+    const int h = un / LPH, l = un % LPH;
+    const int64_t m = m0 + lr;
+    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
+    const int seq = a.seq ? a.seq[m] : (int)m, slot = a.slot[m];
+    bool live = u < total && seq >= 0;
+    if (live && (seq >= c.n_seqs || slot < 0 || slot >= c.max_pages * c.page_size)) {
+      report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+      live = false;
+    }
+    const T* src = (const T*)a.qkv + m * a.ldqkv + (int64_t)h * HD + l * V;
+    Vec16<T> lo, hi;
+    lo.raw = hi.raw = make_uint4(0u, 0u, 0u, 0u);
+    int page = 0;
+    if (live) {
+      page = c.table[(int64_t)seq * c.max_pages + slot / c.page_size];
+      lo = ld_vec_stream(src);
+      hi = ld_vec_stream(src + HALF);
+    }
+    if (u0 == 0 && a.rope) {
+      for (int i = threadIdx.x; i < rows * HALF; i += blockDim.x) {
+        const int64_t row = m0 + i / HALF;
+        angle[i / HALF][i % HALF] =
+            rotation(turns.f[i % HALF], a.pos ? a.pos[row] : a.slot[row]);
       }
     }
-  }
-  if (is_q) {
-    T* dst = (T*)a.q_out + (int64_t)m * a.ldq + (int64_t)h * HD;
-    for (int e = 0; e < E; ++e) dst[lane + 32 * e] = Elem<T>::from_f(v[e]);
-    return;
-  }
-  const int g = is_v ? h - a.hq - a.hkv : h - a.hq;
-  const int64_t row = ((int64_t)page * a.hkv + g) * c.page_size + slot % c.page_size;
-  if constexpr (FP8) {
-    float amax = 0.f;
-    bool bad = false;
-    for (int e = 0; e < E; ++e) {
-      amax = fmaxf(amax, fabsf(v[e]));
-      bad |= !(fabsf(v[e]) <= FLT_MAX);
+    if (u0 == 0) __syncthreads();
+    if (live && (page < 0 || page >= c.n_pages)) {
+      report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+      live = false;
     }
-    bad = __any_sync(0xffffffffu, bad);
-    float scale = warp_max(amax) / 448.0f;
-    if (scale < FLT_MIN) scale = 0.0f;
-    if (bad) scale = __int_as_float(0x7fc00000);
-    uint8_t* dst = (uint8_t*)(is_v ? c.v : c.k) + row * HD;
-    for (int e = 0; e < E; ++e) {
-      const float x = bad ? scale : scale > 0.0f ? v[e] / scale : 0.0f;
-      dst[lane + 32 * e] = (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+    float x[V], y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      x[i] = lo.get(i);
+      y[i] = hi.get(i);
     }
-    if (lane == 0) (is_v ? c.v_scale : c.k_scale)[row] = scale;
-  } else {
-    T* dst = (T*)(is_v ? c.v : c.k) + row * HD;
-    for (int e = 0; e < E; ++e) dst[lane + 32 * e] = Elem<T>::from_f(v[e]);
+    if (a.q_gain || a.k_gain) {   // uniform: the shuffles need every lane
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const T* gain = is_v ? nullptr : (const T*)(is_q ? a.q_gain : a.k_gain);
+      if (gain) {
+        const float inv = rsqrtf(ss / (float)HD + a.eps);
+        const Vec16<T> g0 = ld_vec(gain + l * V), g1 = ld_vec(gain + HALF + l * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          x[i] = x[i] * inv * g0.get(i);
+          y[i] = y[i] * inv * g1.get(i);
+        }
+      }
+    }
+    if (a.rope && !is_v) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 cs = angle[lr][l * V + i];
+        const float rx = x[i] * cs.x - y[i] * cs.y;
+        y[i] = y[i] * cs.x + x[i] * cs.y;
+        x[i] = rx;
+      }
+    }
+    const int g = is_v ? h - a.hq - a.hkv : h - a.hq;
+    const int64_t row = is_q ? 0 : ((int64_t)page * a.hkv + g) * c.page_size + slot % c.page_size;
+    if constexpr (FP8) {
+      float amax = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+        bad |= !(fabsf(x[i]) <= FLT_MAX) || !(fabsf(y[i]) <= FLT_MAX);
+      }
+      if (bad) amax = INFINITY;   // fmaxf passes over a NaN
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (live && !is_q) {
+        float scale = amax / 448.0f;
+        if (scale < FLT_MIN) scale = 0.0f;
+        if (amax == INFINITY) scale = __int_as_float(0x7fc00000);
+        uint32_t cx[V / 4], cy[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          float2 p = make_float2(0.f, 0.f), q = p;
+          if (!(scale == 0.0f)) {
+            p = make_float2(x[2 * i] / scale, x[2 * i + 1] / scale);
+            q = make_float2(y[2 * i] / scale, y[2 * i + 1] / scale);
+          }
+          const uint32_t px = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
+          const uint32_t qx = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+          cx[i / 2] = i & 1 ? cx[i / 2] | px << 16 : px;
+          cy[i / 2] = i & 1 ? cy[i / 2] | qx << 16 : qx;
+        }
+        uint8_t* dst = (uint8_t*)(is_v ? c.v : c.k) + row * HD + l * V;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(cx[0], cx[1]);
+        *reinterpret_cast<uint2*>(dst + HALF) = make_uint2(cy[0], cy[1]);
+        if (l == 0) (is_v ? c.v_scale : c.k_scale)[row] = scale;
+        continue;
+      }
+    }
+    if (live && (!is_q || a.q_out)) {
+      T* dst = is_q ? (T*)a.q_out + m * a.ldq + (int64_t)h * HD
+                    : (T*)(is_v ? c.v : c.k) + row * HD;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        lo.set(i, x[i]);
+        hi.set(i, y[i]);
+      }
+      st_vec(dst + l * V, lo);
+      st_vec(dst + l * V + HALF, hi);
+    }
   }
+}
+
+template <typename T, int HD, bool FP8>
+cudaError_t launch_append_hd(const Ctx& c, const AppendArgs& a, const Turns& turns) {
+  const int units = (a.hq + 2 * a.hkv) * (HD / 2) / (16 / (int)sizeof(T));
+  int rows = 256 / units;
+  rows = rows < 1 ? 1 : rows > 8 ? 8 : rows;
+  int threads = (rows * units + 31) / 32 * 32;
+  if (threads > 512) threads = 512;
+  return launch_pdl(cache_append_kernel<T, HD, FP8>, dim3((unsigned)((a.M + rows - 1) / rows)),
+                    dim3(threads), 0, c.stream, a, turns, rows);
 }
 
 template <typename T, bool FP8>
 cudaError_t launch_append(const Ctx& c, const AppendArgs& a, int hd, const Turns& turns) {
-  const int64_t items = (int64_t)a.M * (a.hq + 2 * a.hkv);
-  const dim3 grid((unsigned)((items + 7) / 8));
-  if (hd == 128) cache_append_kernel<T, 128, FP8><<<grid, 256, 0, c.stream>>>(a, turns);
-  else if (hd == 64) cache_append_kernel<T, 64, FP8><<<grid, 256, 0, c.stream>>>(a, turns);
-  else cache_append_kernel<T, 32, FP8><<<grid, 256, 0, c.stream>>>(a, turns);
-  return cudaGetLastError();
+  if (hd == 128) return launch_append_hd<T, 128, FP8>(c, a, turns);
+  if (hd == 64) return launch_append_hd<T, 64, FP8>(c, a, turns);
+  return launch_append_hd<T, 32, FP8>(c, a, turns);
 }
 
 }  // namespace
