@@ -436,7 +436,7 @@ typedef struct {
  * at position pos[m]; k and v are written to slot slot[m] of sequence seq[m], q to q_out.
  * Everything is computed in fp32 and rounded once, to the type it is stored in; E4M3
  * stores scale = max|x| / 448 over the head's values and the codes nearest to x / scale
- * (ties to even). A head of zeros gets scale 0 (as do values below 2^-117, which are
+ * (the quotient in fp32, ties to even). A head of zeros gets scale 0 (as do values below 2^-117, which are
  * stored as zeros); a head with an infinity or NaN gets a NaN scale and NaN codes.
  *   seq     [M] int32, or NULL (row m belongs to sequence m). A negative entry skips
  *           its row: nothing of it is read or written (q_out's row keeps its values).

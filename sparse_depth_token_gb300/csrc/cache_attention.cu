@@ -1028,19 +1028,6 @@ size_t attention_workspace(const xmod_dims* dm) {
   return 256 + round256(kMaxCtas * sizeof(Join)) + 2 * kMaxCtas * part;
 }
 
-// CTAs of the persistent grid: two per SM of the current device.
-int grid_ctas() {
-  static std::atomic<int> sms[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = sms[dev].load(std::memory_order_relaxed);
-  if (!n) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    sms[dev].store(n, std::memory_order_relaxed);
-  }
-  return 2 * n < kMaxCtas ? 2 * n : kMaxCtas;
-}
-
 // Raises a kernel's shared-memory limit once per device.
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -1117,8 +1104,9 @@ int xmod_cache_attention(const xmod_dims* dm, const xmod_kv_cache* cache, int M,
   if (!ptr16(ws) || ws_bytes < attention_workspace(dm)) return XMOD_ERR_WORKSPACE;
   const bool fp32 = dm->dtype == XMOD_FP32, fp8 = cache->format == XMOD_CACHE_E4M3;
   if (!fp32 && !tma_available()) return XMOD_ERR_UNSUPPORTED;
-  const int ctas = grid_ctas();
-  if (ctas <= 0) return XMOD_ERR_CUDA;
+  const int sms = device_sms();
+  if (sms <= 0) return XMOD_ERR_CUDA;
+  const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
   const int rows = pass_rows(dm), group = dm->n_heads / dm->n_kv_heads;
   DecodeArgs a{};
   a.M = M;

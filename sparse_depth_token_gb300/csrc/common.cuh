@@ -68,6 +68,50 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// ---------------------------------------------------------------- paired fp32 arithmetic
+//
+// Two fp32 operations an instruction, each rounded as its scalar form.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+// Elements 2i, 2i + 1 of a 16-byte vector as fp32.
+template <typename T> __device__ __forceinline__ float2 vec_pair(const uint4& v, int i) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+  if constexpr (sizeof(T) == 4)
+    return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  else
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <typename T> __device__ __forceinline__ void set_vec_pair(uint4& v, int i, float2 f) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+  if constexpr (sizeof(T) == 4) {
+    w[2 * i] = __float_as_uint(f.x);
+    w[2 * i + 1] = __float_as_uint(f.y);
+  } else {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+
 // ---------------------------------------------------------------- device status word
 
 // First error wins; later errors do not overwrite it.

@@ -77,6 +77,9 @@ class ProfScope {
   cudaEvent_t start_ = nullptr;
 };
 
+// SMs of the current device (0 if it cannot be asked).
+int device_sms();
+
 // One kernel launch of an entry point on context c: counted, optionally timed, checked.
 #define XMOD_LAUNCH(c, kind, expr)               \
   do {                                           \
