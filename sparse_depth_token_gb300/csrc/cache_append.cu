@@ -64,60 +64,152 @@ struct AppendArgs {
   const int32_t *seq, *slot, *pos;
   xmod_kv_cache cache;
   float eps;
+  int page_shift;   // log2 of the page size, -1: not a power of two
   bool rope;
   int* status;
 };
 
-// Bound: memory, once the instructions are few enough. A token's (hq + 2 hkv) hd elements
-// are read once and written once. One warp takes a token (small batches: a part of its
-// heads) by itself, without shared memory or barriers. A lane moves two 16-byte vectors of
-// a head, elements c .. c + V - 1 and their rotation partners hd/2 further, LPH = hd / (2 V)
-// lanes to a head, HPW heads of one kind (q, k or v) a pass, four passes' loads together
-// (4 KB a warp). The angles are the same for all heads: every lane computes the 1 or 2 of
-// the hd/2 that it owns, once per token, and gets its V by shuffles. The arithmetic runs on
-// pairs of fp32; v is copied as it is. Warps stay for many tokens; the next token's
-// sequence, slot, position and page are fetched a token ahead.
-constexpr int kPasses = 4;        // passes whose loads are in flight together
+// Bound: memory, once the instructions are few enough (a token's elements are read once and
+// written once, with 7 operations each). A warp takes tokens by itself, without shared
+// memory or barriers, and of every token the same part: up to four passes over the q heads,
+// or one or two over the k heads with the v heads beside them. What depends on the heads
+// (columns, gains, this lane's frequencies) is then set up once per warp. A lane moves two
+// 16-byte vectors of a head, elements c .. c + V - 1 and their rotation partners hd/2
+// further, LPH = hd / (2 V) lanes to a head, HPW heads a pass, all passes' loads together.
+// The angles are the same for all heads: every lane computes the 1 or 2 of the hd/2 that it
+// owns, once per token, and gets its V by shuffles. The arithmetic runs on pairs of fp32; v
+// is copied as it is. The next token's sequence, slot, position and page are fetched a
+// token ahead.
+constexpr int kQPasses = 4, kKvPasses = 2;
 constexpr int kAppendWarps = 4;
-constexpr int kAppendCtas = 24;   // CTAs per SM the grid is limited to
+constexpr int kAppendCtas = 48;   // CTAs per SM the grid is limited to: short-lived, so that
+                                  // the parts' different lengths even out
 
-template <typename T, int HD, bool FP8>
-__global__ void __launch_bounds__(kAppendWarps * 32)
-cache_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, int chunk) {
-  constexpr int V = 16 / sizeof(T), LPH = HD / (2 * V), HALF = HD / 2, HPW = 32 / LPH;
-  constexpr int NJ = V > HPW ? V / HPW : 1;   // angles a lane computes
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPH, hl = lane / LPH;
-  const int q_passes = (a.hq + HPW - 1) / HPW, kv_passes = (a.hkv + HPW - 1) / HPW;
-  // passes: the q heads', the k heads', the v heads'; this warp's are [first, last)
-  const int first = max((int)blockIdx.y * chunk, a.q_out ? 0 : q_passes);
-  const int last = min(((int)blockIdx.y + 1) * chunk, q_passes + 2 * kv_passes);
-  const bool rope = a.rope && first < q_passes + kv_passes;
+template <typename T, int HD> struct AppendShape {
+  static constexpr int V = 16 / sizeof(T), LPH = HD / (2 * V), HALF = HD / 2, HPW = 32 / LPH;
+  static constexpr int NJ = V > HPW ? V / HPW : 1;   // angles a lane computes
+};
+
+struct Where {
+  int seq, slot, pos, page;
+};
+
+// QK-norm (gain > 0 elements given) and rotation of a lane's vectors x, y.
+template <typename T, int HD>
+__device__ __forceinline__ void transform(float2 (&x)[AppendShape<T, HD>::V / 2],
+                                          float2 (&y)[AppendShape<T, HD>::V / 2], bool norm,
+                                          const uint4& g0, const uint4& g1, float eps, bool rope,
+                                          const float2* cs, const float2* sn) {
+  using S = AppendShape<T, HD>;
+  if (norm) {
+    float2 ss = mul2(x[0], x[0]);
+#pragma unroll
+    for (int e = 1; e < S::V / 2; ++e) ss = fma2(x[e], x[e], ss);
+#pragma unroll
+    for (int e = 0; e < S::V / 2; ++e) ss = fma2(y[e], y[e], ss);
+    float sum = ss.x + ss.y;
+#pragma unroll
+    for (int o = S::LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = rsqrtf(fmaf(sum, 1.0f / (float)HD, eps));
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int e = 0; e < S::V / 2; ++e) {
+      x[e] = mul2(mul2(x[e], inv2), vec_pair<T>(g0, e));
+      y[e] = mul2(mul2(y[e], inv2), vec_pair<T>(g1, e));
+    }
+  }
+  if (rope) {
+#pragma unroll
+    for (int e = 0; e < S::V / 2; ++e) {
+      const float2 t = mul2(x[e], cs[e]);
+      const float2 rx = make_float2(fmaf(-y[e].x, sn[e].x, t.x), fmaf(-y[e].y, sn[e].y, t.y));
+      y[e] = fma2(x[e], sn[e], mul2(y[e], cs[e]));
+      x[e] = rx;
+    }
+  }
+}
+
+template <typename T, int HD>
+__device__ __forceinline__ void store_pair(T* dst, const float2* x, const float2* y) {
+  using S = AppendShape<T, HD>;
+  uint4 w0, w1;
+#pragma unroll
+  for (int e = 0; e < S::V / 2; ++e) {
+    set_vec_pair<T>(w0, e, x[e]);
+    set_vec_pair<T>(w1, e, y[e]);
+  }
+  *reinterpret_cast<uint4*>(dst) = w0;
+  *reinterpret_cast<uint4*>(dst + S::HALF) = w1;
+}
+
+// e4m3 codes and scale of a head whose LPH lanes hold x, y.
+template <int HD>
+__device__ __forceinline__ void store_e4m3(uint8_t* dst, float* scale_at, bool live, bool writes_scale,
+                                           const float2* x, const float2* y) {
+  using S = AppendShape<__nv_bfloat16, HD>;
+  float amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < S::V / 2; ++e) {
+    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[e].x), fabsf(x[e].y)),
+                             fmaxf(fabsf(y[e].x), fabsf(y[e].y))));   // passes over a NaN
+    bad |= x[e].x != x[e].x || x[e].y != x[e].y || y[e].x != y[e].x || y[e].y != y[e].y;
+  }
+  if (bad) amax = INFINITY;
+#pragma unroll
+  for (int o = S::LPH / 2; o > 0; o >>= 1)
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  float scale = amax / 448.0f;
+  if (scale < FLT_MIN) scale = 0.0f;
+  if (amax == INFINITY) scale = __int_as_float(0x7fc00000);
+  const float inv = scale == 0.0f ? 0.0f : 1.0f / scale;   // a NaN stays
+  const float2 inv2 = make_float2(inv, inv);
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    c[e] = (uint32_t)__nv_cvt_float2_to_fp8x2(mul2(x[2 * e], inv2), __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(mul2(x[2 * e + 1], inv2), __NV_SATFINITE, __NV_E4M3) << 16;
+    c[2 + e] = (uint32_t)__nv_cvt_float2_to_fp8x2(mul2(y[2 * e], inv2), __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(mul2(y[2 * e + 1], inv2), __NV_SATFINITE, __NV_E4M3) << 16;
+  }
+  if (!live) return;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+  *reinterpret_cast<uint2*>(dst + S::HALF) = make_uint2(c[2], c[3]);
+  if (writes_scale) *scale_at = scale;
+}
+
+// The part of the tokens that one warp takes: KV, the k and v heads from head0 on; else the
+// q heads from head0 on; `passes` passes of HPW heads.
+template <typename T, int HD, bool FP8, bool KV>
+__device__ __forceinline__ void append_part(const AppendArgs& a, const Turns& turns, int head0,
+                                            int passes, int64_t m, int64_t step) {
+  using S = AppendShape<T, HD>;
+  constexpr int V = S::V, LPH = S::LPH, HALF = S::HALF, HPW = S::HPW, NJ = S::NJ;
+  constexpr int NP = KV ? kKvPasses : kQPasses;
+  const int lane = threadIdx.x & 31, l = lane % LPH, hl = lane / LPH;
   const xmod_kv_cache& c = a.cache;
   const int room = c.max_pages * c.page_size;
-  const int step = gridDim.x * kAppendWarps;
   // this lane's angles: pairs l V + i, i = hl + HPW j; pair i of a lane comes from lane
   // l + LPH (i % HPW)
   uint64_t freq[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) freq[j] = turns.f[l * V + (hl + HPW * j) % V];
-  pdl_trigger();
-  pdl_wait();
+  const T* gain = (const T*)(KV ? a.k_gain : a.q_gain);
+  const bool norm = gain != nullptr;
 
-  struct Where {
-    int seq, slot, pos, page;
-  };
-  auto locate = [&](int64_t m, Where& w) {
+  auto locate = [&](int64_t m_, Where& w) {
     w.seq = -1;
-    if (m >= a.M) return;
-    w.seq = a.seq ? a.seq[m] : (int)m;
-    w.slot = a.slot[m];
-    w.pos = a.pos ? a.pos[m] : w.slot;
+    if (m_ >= a.M) return;
+    w.seq = a.seq ? a.seq[m_] : (int)m_;
+    w.slot = a.slot[m_];
+    w.pos = a.pos ? a.pos[m_] : w.slot;
   };
   auto find_page = [&](Where& w) {   // the page of a row to append, -1: skip the row
     w.page = -1;
     if (w.seq < 0) return;
     if (w.seq < c.n_seqs && w.slot >= 0 && w.slot < room)
-      w.page = c.table[(int64_t)w.seq * c.max_pages + w.slot / c.page_size];
+      w.page = c.table[(int64_t)w.seq * c.max_pages +
+                       (a.page_shift >= 0 ? w.slot >> a.page_shift : w.slot / c.page_size)];
     if (w.page >= c.n_pages) w.page = -1;
     if (w.page < 0) {
       report_status(a.status, XMOD_ERR_DEVICE_CHECK);
@@ -125,150 +217,78 @@ cache_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, int
     }
   };
 
-  int64_t m = (int64_t)blockIdx.x * kAppendWarps + warp;
+  pdl_trigger();
+  pdl_wait();
+  uint4 g0 = make_uint4(0u, 0u, 0u, 0u), g1 = g0;
+  if (norm) {
+    g0 = *reinterpret_cast<const uint4*>(gain + l * V);
+    g1 = *reinterpret_cast<const uint4*>(gain + HALF + l * V);
+  }
+  const int heads = KV ? a.hkv : a.hq, h0 = head0 + hl;
+  const T* src0 = (const T*)a.qkv + (KV ? a.hq * HD : 0) + h0 * HD + l * V;
+  const int v_off = a.hkv * HD;   // from a k head to the v head beside it
   Where now, next;
   locate(m, now);
   find_page(now);
   for (; m < a.M; m += step) {
     locate(m + step, next);
     if (now.page >= 0) {   // the same for the whole warp
-      const T* src = (const T*)a.qkv + m * a.ldqkv + l * V;
-      const int64_t page_row = (int64_t)now.page * a.hkv * c.page_size + now.slot % c.page_size;
+      const T* src = src0 + m * a.ldqkv;
+      constexpr int NV = KV ? 2 : 1;
+      uint4 lo[NP][NV], hi[NP][NV];
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          lo[p][j] = hi[p][j] = make_uint4(0u, 0u, 0u, 0u);
+          if (p < passes && h0 + p * HPW < heads) {
+            lo[p][j] = __ldcs(reinterpret_cast<const uint4*>(src + p * HPW * HD + j * v_off));
+            hi[p][j] = __ldcs(reinterpret_cast<const uint4*>(src + p * HPW * HD + j * v_off + HALF));
+          }
+        }
       float2 cs[V / 2], sn[V / 2];
-      for (int p0 = first; p0 < last; p0 += kPasses) {
-        uint4 lo[kPasses], hi[kPasses];
+      if (a.rope) {
+        float2 own[NJ];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int p = p0 + i;
-          const int kind = p < q_passes ? 0 : p < q_passes + kv_passes ? 1 : 2;
-          const int h = (kind == 0 ? p : p - q_passes - (kind - 1) * kv_passes) * HPW + hl;
-          const int col = kind == 0 ? 0 : a.hq + (kind - 1) * a.hkv;
-          lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (p < last && h < (kind == 0 ? a.hq : a.hkv)) {
-            lo[i] = __ldcs(reinterpret_cast<const uint4*>(src + (col + h) * HD));
-            hi[i] = __ldcs(reinterpret_cast<const uint4*>(src + (col + h) * HD + HALF));
-          }
+        for (int j = 0; j < NJ; ++j) own[j] = rotation(freq[j], now.pos);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float x = __shfl_sync(0xffffffffu, own[i / HPW].x, l + LPH * (i % HPW));
+          const float y = __shfl_sync(0xffffffffu, own[i / HPW].y, l + LPH * (i % HPW));
+          (i & 1 ? cs[i / 2].y : cs[i / 2].x) = x;
+          (i & 1 ? sn[i / 2].y : sn[i / 2].x) = y;
         }
-        if (rope && p0 == first) {
-          float2 own[NJ];
+      }
+      const int off = a.page_shift >= 0 ? now.slot & (c.page_size - 1) : now.slot % c.page_size;
+      // this lane's first row of the cache
+      const int64_t row0 = ((int64_t)now.page * a.hkv + h0) * c.page_size + off;
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) own[j] = rotation(freq[j], now.pos);
+      for (int p = 0; p < NP; ++p) {
+        if (p >= passes) break;
+        const bool live = h0 + p * HPW < heads;
+        float2 x[V / 2], y[V / 2];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float x = __shfl_sync(0xffffffffu, own[i / HPW].x, l + LPH * (i % HPW));
-            const float y = __shfl_sync(0xffffffffu, own[i / HPW].y, l + LPH * (i % HPW));
-            if (i & 1) {
-              cs[i / 2].y = x;
-              sn[i / 2].y = y;
-            } else {
-              cs[i / 2].x = x;
-              sn[i / 2].x = y;
-            }
-          }
+        for (int e = 0; e < V / 2; ++e) {
+          x[e] = vec_pair<T>(lo[p][0], e);
+          y[e] = vec_pair<T>(hi[p][0], e);
         }
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int p = p0 + i;
-          if (p >= last) break;
-          const int kind = p < q_passes ? 0 : p < q_passes + kv_passes ? 1 : 2;
-          const int h = (kind == 0 ? p : p - q_passes - (kind - 1) * kv_passes) * HPW + hl;
-          const bool live = h < (kind == 0 ? a.hq : a.hkv);
-          const T* gain = (const T*)(kind == 0 ? a.q_gain : kind == 1 ? a.k_gain : nullptr);
-          T* dst;   // of the head's vectors, in q_out or a native cache
-          int64_t row = 0;
-          if (kind == 0) {
-            dst = (T*)a.q_out + m * a.ldq + h * HD + l * V;
-          } else {
-            row = page_row + (int64_t)h * c.page_size;
-            dst = (T*)(kind == 2 ? c.v : c.k) + row * HD + l * V;
-          }
-          if (kind == 2 && !FP8) {
-            if (live) {
-              *reinterpret_cast<uint4*>(dst) = lo[i];
-              *reinterpret_cast<uint4*>(dst + HALF) = hi[i];
-            }
-            continue;
-          }
-          float2 x[V / 2], y[V / 2];
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            x[e] = vec_pair<T>(lo[i], e);
-            y[e] = vec_pair<T>(hi[i], e);
-          }
-          if (gain) {
-            float2 ss = mul2(x[0], x[0]);
-#pragma unroll
-            for (int e = 1; e < V / 2; ++e) ss = fma2(x[e], x[e], ss);
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) ss = fma2(y[e], y[e], ss);
-            float sum = ss.x + ss.y;
-#pragma unroll
-            for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv = rsqrtf(fmaf(sum, 1.0f / (float)HD, a.eps));
-            const float2 inv2 = make_float2(inv, inv);
-            const uint4 g0 = *reinterpret_cast<const uint4*>(gain + l * V);
-            const uint4 g1 = *reinterpret_cast<const uint4*>(gain + HALF + l * V);
+        transform<T, HD>(x, y, norm, g0, g1, a.eps, a.rope, cs, sn);
+        if constexpr (!KV) {
+          if (live) store_pair<T, HD>((T*)a.q_out + m * a.ldq + (h0 + p * HPW) * HD + l * V, x, y);
+        } else {
+          const int64_t row = row0 + (int64_t)p * HPW * c.page_size, at = row * HD + l * V;
+          if constexpr (FP8) {
+            store_e4m3<HD>((uint8_t*)c.k + at, c.k_scale + row, live, l == 0, x, y);
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
-              x[e] = mul2(mul2(x[e], inv2), vec_pair<T>(g0, e));
-              y[e] = mul2(mul2(y[e], inv2), vec_pair<T>(g1, e));
+              x[e] = vec_pair<T>(lo[p][NV - 1], e);
+              y[e] = vec_pair<T>(hi[p][NV - 1], e);
             }
-          }
-          if (rope && kind != 2) {
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-              const float2 neg = make_float2(-sn[e].x, -sn[e].y);
-              const float2 rx = fma2(y[e], neg, mul2(x[e], cs[e]));
-              y[e] = fma2(x[e], sn[e], mul2(y[e], cs[e]));
-              x[e] = rx;
-            }
-          }
-          if (FP8 && kind != 0) {
-            if constexpr (FP8) {
-              float amax = 0.f;
-              bool bad = false;
-#pragma unroll
-              for (int e = 0; e < V / 2; ++e) {
-                const float big = fmaxf(fmaxf(fabsf(x[e].x), fabsf(x[e].y)),
-                                        fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
-                amax = fmaxf(amax, big);   // passes over a NaN
-                bad |= x[e].x != x[e].x || x[e].y != x[e].y || y[e].x != y[e].x || y[e].y != y[e].y;
-              }
-              if (bad) amax = INFINITY;
-#pragma unroll
-              for (int o = LPH / 2; o > 0; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-              float scale = amax / 448.0f;
-              if (scale < FLT_MIN) scale = 0.0f;
-              if (amax == INFINITY) scale = __int_as_float(0x7fc00000);
-              const float inv = scale == 0.0f ? 0.0f : 1.0f / scale;   // NaN stays
-              const float2 inv2 = make_float2(inv, inv);
-              uint32_t cx[V / 4], cy[V / 4];
-#pragma unroll
-              for (int e = 0; e < V / 2; ++e) {
-                const uint32_t sx =
-                    __nv_cvt_float2_to_fp8x2(mul2(x[e], inv2), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t sy =
-                    __nv_cvt_float2_to_fp8x2(mul2(y[e], inv2), __NV_SATFINITE, __NV_E4M3);
-                cx[e / 2] = e & 1 ? cx[e / 2] | sx << 16 : sx;
-                cy[e / 2] = e & 1 ? cy[e / 2] | sy << 16 : sy;
-              }
-              if (live) {
-                uint8_t* codes = (uint8_t*)(kind == 2 ? c.v : c.k) + row * HD + l * V;
-                *reinterpret_cast<uint2*>(codes) = make_uint2(cx[0], cx[1]);
-                *reinterpret_cast<uint2*>(codes + HALF) = make_uint2(cy[0], cy[1]);
-                if (l == 0) (kind == 2 ? c.v_scale : c.k_scale)[row] = scale;
-              }
-            }
+            store_e4m3<HD>((uint8_t*)c.v + at, c.v_scale + row, live, l == 0, x, y);
           } else if (live) {
-            uint4 w0, w1;
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-              set_vec_pair<T>(w0, e, x[e]);
-              set_vec_pair<T>(w1, e, y[e]);
-            }
-            *reinterpret_cast<uint4*>(dst) = w0;
-            *reinterpret_cast<uint4*>(dst + HALF) = w1;
+            store_pair<T, HD>((T*)c.k + at, x, y);
+            *reinterpret_cast<uint4*>((T*)c.v + at) = lo[p][NV - 1];
+            *reinterpret_cast<uint4*>((T*)c.v + at + HALF) = hi[p][NV - 1];
           }
         }
       }
@@ -278,22 +298,39 @@ cache_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, int
   }
 }
 
+// blockIdx.y: the kv parts first, then the q parts.
+template <typename T, int HD, bool FP8>
+__global__ void __launch_bounds__(kAppendWarps * 32)
+cache_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, int kv_parts,
+                    int kv_passes, int q_passes) {
+  constexpr int HPW = AppendShape<T, HD>::HPW;
+  const int64_t m = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const int64_t step = (int64_t)gridDim.x * kAppendWarps;
+  const int part = blockIdx.y;
+  if (part < kv_parts)
+    append_part<T, HD, FP8, true>(a, turns, part * kv_passes * HPW, kv_passes, m, step);
+  else
+    append_part<T, HD, FP8, false>(a, turns, (part - kv_parts) * q_passes * HPW, q_passes, m, step);
+}
+
 template <typename T, int HD, bool FP8>
 cudaError_t launch_append_hd(const Ctx& c, const AppendArgs& a, const Turns& turns) {
-  constexpr int HPW = 32 / (HD / 2 / (16 / (int)sizeof(T)));
-  const int total = (a.hq + HPW - 1) / HPW + 2 * ((a.hkv + HPW - 1) / HPW);
+  constexpr int HPW = AppendShape<T, HD>::HPW;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // Passes a warp does of a token: all of them (the angles once) when the tokens alone fill
-  // the GPU, one while even single passes leave it empty (latency), four in between.
-  const int64_t M = a.M;
-  const int chunk = M * total <= (int64_t)sms * 8 ? 1 : M < (int64_t)sms * 32 && total > 4 ? 4 : total;
-  const int chunks = (total + chunk - 1) / chunk;
-  const int64_t ctas = (M + kAppendWarps - 1) / kAppendWarps;
-  const int64_t most = ((int64_t)sms * kAppendCtas + chunks - 1) / chunks;
+  const int q_all = a.q_out ? (a.hq + HPW - 1) / HPW : 0, kv_all = (a.hkv + HPW - 1) / HPW;
+  // Passes a warp does of a token: as many as it holds in flight, or one while the tokens
+  // are so few that single passes leave the GPU empty (then only the latency counts).
+  const bool few = (int64_t)a.M * (q_all + kv_all) <= (int64_t)sms * 8;
+  const int kv_parts = few ? kv_all : (kv_all + kKvPasses - 1) / kKvPasses;
+  const int q_parts = few ? q_all : (q_all + kQPasses - 1) / kQPasses;
+  const int kv_passes = (kv_all + kv_parts - 1) / kv_parts;
+  const int q_passes = q_parts ? (q_all + q_parts - 1) / q_parts : 0;
+  const int64_t ctas = ((int64_t)a.M + kAppendWarps - 1) / kAppendWarps;
+  const int64_t most = ((int64_t)sms * kAppendCtas + kv_parts + q_parts - 1) / (kv_parts + q_parts);
   return launch_pdl(cache_append_kernel<T, HD, FP8>,
-                    dim3((unsigned)(ctas < most ? ctas : most), chunks), dim3(kAppendWarps * 32), 0,
-                    c.stream, a, turns, chunk);
+                    dim3((unsigned)(ctas < most ? ctas : most), kv_parts + q_parts),
+                    dim3(kAppendWarps * 32), 0, c.stream, a, turns, kv_parts, kv_passes, q_passes);
 }
 
 template <typename T, bool FP8>
@@ -342,6 +379,9 @@ int xmod_cache_append(const xmod_dims* dm, const xmod_kv_cache* cache, int M, co
   a.pos = pos;
   a.cache = *cache;
   a.eps = dm->rms_eps;
+  a.page_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (cache->page_size == 1 << i) a.page_shift = i;
   a.rope = w && w->rope_theta > 0.0f;
   a.status = status_out;
   Turns turns{};
