@@ -70,25 +70,38 @@ struct AppendArgs {
 };
 
 // Bound: memory, once the instructions are few enough (a token's elements are read once and
-// written once, with 7 operations each). A warp takes tokens by itself, without shared
-// memory or barriers, and of every token the same part: up to four passes over the q heads,
+// written once, with 7 operations each). A warp takes tokens by itself, without barriers,
+// and of every token the same part: up to four passes over the q heads,
 // or one or two over the k heads with the v heads beside them. What depends on the heads
 // (columns, gains, this lane's frequencies) is then set up once per warp. A lane moves two
 // 16-byte vectors of a head, elements c .. c + V - 1 and their rotation partners hd/2
-// further, LPH = hd / (2 V) lanes to a head, HPW heads a pass, all passes' loads together.
+// further, LPH = hd / (2 V) lanes to a head, HPW heads a pass. The vectors come by
+// asynchronous copies into the lane's own places in shared memory, two tokens ahead, so that
+// loads are in flight all the time and cost no registers (loading into registers, a token at
+// a time, left the memory idle while a token was transformed: 72 us instead of 63).
 // The angles are the same for all heads: every lane computes the 1 or 2 of the hd/2 that it
 // owns, once per token, and gets its V by shuffles. The arithmetic runs on pairs of fp32; v
-// is copied as it is. The next token's sequence, slot, position and page are fetched a
-// token ahead.
+// is copied as it is. Sequence, slot and position are fetched three tokens ahead, the page
+// one.
 constexpr int kQPasses = 4, kKvPasses = 2;
 constexpr int kAppendWarps = 4;
-constexpr int kAppendCtas = 48;   // CTAs per SM the grid is limited to: short-lived, so that
-                                  // the parts' different lengths even out
+// CTAs per SM the grid is limited to: four are resident, twice as many even out the parts'
+// lengths (32768 prompt tokens, 12 q and 4 KV heads of 128, bf16: 62 us at 4, 63 at 8, 72 at
+// 32; 5003 tokens, 32 and 8 heads, e4m3: 24.3, 22.7, 24.4).
+constexpr int kAppendCtas = 8;
+constexpr int kAppendStages = 3;  // tokens of a warp in shared memory: one at work, two coming
 
 template <typename T, int HD> struct AppendShape {
   static constexpr int V = 16 / sizeof(T), LPH = HD / (2 * V), HALF = HD / 2, HPW = 32 / LPH;
   static constexpr int NJ = V > HPW ? V / HPW : 1;   // angles a lane computes
 };
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
 
 struct Where {
   int seq, slot, pos, page;
@@ -182,7 +195,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t* dst, float* scale_at, bool l
 // q heads from head0 on; `passes` passes of HPW heads.
 template <typename T, int HD, bool FP8, bool KV>
 __device__ __forceinline__ void append_part(const AppendArgs& a, const Turns& turns, int head0,
-                                            int passes, int64_t m, int64_t step) {
+                                            int passes, int64_t m, int64_t step,
+                                            uint4* ring_base) {
   using S = AppendShape<T, HD>;
   constexpr int V = S::V, LPH = S::LPH, HALF = S::HALF, HPW = S::HPW, NJ = S::NJ;
   constexpr int NP = KV ? kKvPasses : kQPasses;
@@ -227,25 +241,42 @@ __device__ __forceinline__ void append_part(const AppendArgs& a, const Turns& tu
   const int heads = KV ? a.hkv : a.hq, h0 = head0 + hl;
   const T* src0 = (const T*)a.qkv + (KV ? a.hq * HD : 0) + h0 * HD + l * V;
   const int v_off = a.hkv * HD;   // from a k head to the v head beside it
-  Where now, next;
-  locate(m, now);
-  find_page(now);
-  for (; m < a.M; m += step) {
-    locate(m + step, next);
-    if (now.page >= 0) {   // the same for the whole warp
-      const T* src = src0 + m * a.ldqkv;
-      constexpr int NV = KV ? 2 : 1;
-      uint4 lo[NP][NV], hi[NP][NV];
+  constexpr int NV = KV ? 2 : 1;
+  // [stage][vector][lane]: a lane reads only what it copied itself
+  uint4* const ring = ring_base + (threadIdx.x >> 5) * kAppendStages * 8 * 32 + lane;
+  static_assert(2 * NP * NV == 8, "vectors of a stage");
+  auto issue = [&](int64_t m_, const Where& w, int stage) {
+    if (w.seq >= 0) {
+      const T* src = src0 + m_ * a.ldqkv;
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          lo[p][j] = hi[p][j] = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < NV; ++j)
           if (p < passes && h0 + p * HPW < heads) {
-            lo[p][j] = __ldcs(reinterpret_cast<const uint4*>(src + p * HPW * HD + j * v_off));
-            hi[p][j] = __ldcs(reinterpret_cast<const uint4*>(src + p * HPW * HD + j * v_off + HALF));
+            uint4* at = ring + (stage * 8 + (p * NV + j) * 2) * 32;
+            copy16(at, src + p * HPW * HD + j * v_off);
+            copy16(at + 32, src + p * HPW * HD + j * v_off + HALF);
           }
-        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // tokens m (at work), m + step (page on its way), m + 2 step (vectors about to be asked
+  // for), m + 3 step (sequence, slot and position on their way)
+  Where w0, w1, w2;
+  locate(m, w0);
+  locate(m + step, w1);
+  locate(m + 2 * step, w2);
+  issue(m, w0, 0);
+  issue(m + step, w1, 1);
+  find_page(w0);
+  for (int stage = 0; m < a.M; m += step, stage = stage == kAppendStages - 1 ? 0 : stage + 1) {
+    Where w3;
+    locate(m + 3 * step, w3);
+    issue(m + 2 * step, w2, stage >= 1 ? stage - 1 : kAppendStages - 1);
+    find_page(w1);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    const Where now = w0;
+    if (now.page >= 0) {   // the same for the whole warp
       float2 cs[V / 2], sn[V / 2];
       if (a.rope) {
         float2 own[NJ];
@@ -266,11 +297,13 @@ __device__ __forceinline__ void append_part(const AppendArgs& a, const Turns& tu
       for (int p = 0; p < NP; ++p) {
         if (p >= passes) break;
         const bool live = h0 + p * HPW < heads;
+        const uint4* at_p = ring + (stage * 8 + p * NV * 2) * 32;
+        const uint4 lo = at_p[0], hi = at_p[32];
         float2 x[V / 2], y[V / 2];
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
-          x[e] = vec_pair<T>(lo[p][0], e);
-          y[e] = vec_pair<T>(hi[p][0], e);
+          x[e] = vec_pair<T>(lo, e);
+          y[e] = vec_pair<T>(hi, e);
         }
         transform<T, HD>(x, y, norm, g0, g1, a.eps, a.rope, cs, sn);
         if constexpr (!KV) {
@@ -279,22 +312,24 @@ __device__ __forceinline__ void append_part(const AppendArgs& a, const Turns& tu
           const int64_t row = row0 + (int64_t)p * HPW * c.page_size, at = row * HD + l * V;
           if constexpr (FP8) {
             store_e4m3<HD>((uint8_t*)c.k + at, c.k_scale + row, live, l == 0, x, y);
+            const uint4 vlo = at_p[64], vhi = at_p[96];
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
-              x[e] = vec_pair<T>(lo[p][NV - 1], e);
-              y[e] = vec_pair<T>(hi[p][NV - 1], e);
+              x[e] = vec_pair<T>(vlo, e);
+              y[e] = vec_pair<T>(vhi, e);
             }
             store_e4m3<HD>((uint8_t*)c.v + at, c.v_scale + row, live, l == 0, x, y);
           } else if (live) {
             store_pair<T, HD>((T*)c.k + at, x, y);
-            *reinterpret_cast<uint4*>((T*)c.v + at) = lo[p][NV - 1];
-            *reinterpret_cast<uint4*>((T*)c.v + at + HALF) = hi[p][NV - 1];
+            *reinterpret_cast<uint4*>((T*)c.v + at) = at_p[64];
+            *reinterpret_cast<uint4*>((T*)c.v + at + HALF) = at_p[96];
           }
         }
       }
     }
-    now = next;
-    if (m + step < a.M) find_page(now);
+    w0 = w1;
+    w1 = w2;
+    w2 = w3;
   }
 }
 
@@ -307,10 +342,12 @@ cache_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, int
   const int64_t m = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int64_t step = (int64_t)gridDim.x * kAppendWarps;
   const int part = blockIdx.y;
+  __shared__ uint4 ring[kAppendWarps * kAppendStages * 8 * 32];
   if (part < kv_parts)
-    append_part<T, HD, FP8, true>(a, turns, part * kv_passes * HPW, kv_passes, m, step);
+    append_part<T, HD, FP8, true>(a, turns, part * kv_passes * HPW, kv_passes, m, step, ring);
   else
-    append_part<T, HD, FP8, false>(a, turns, (part - kv_parts) * q_passes * HPW, q_passes, m, step);
+    append_part<T, HD, FP8, false>(a, turns, (part - kv_parts) * q_passes * HPW, q_passes, m, step,
+                                   ring);
 }
 
 template <typename T, int HD, bool FP8>
