@@ -1028,20 +1028,6 @@ size_t attention_workspace(const xmod_dims* dm) {
   return 256 + round256(kMaxCtas * sizeof(Join)) + 2 * kMaxCtas * part;
 }
 
-// Raises a kernel's shared-memory limit once per device.
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) >> (dev & 63) & 1)) return e;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             (int)cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
-  return e;
-}
-
 template <int HD, bool FP8, int ROWS>
 int run_tc(const Ctx& c, const DecodeArgs& a, int ctas) {
   using C = Cf<HD, FP8, ROWS>;

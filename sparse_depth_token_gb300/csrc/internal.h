@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "xmod.h"
 
 namespace xmod {
@@ -79,6 +81,20 @@ class ProfScope {
 
 // SMs of the current device (0 if it cannot be asked).
 int device_sms();
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) >> (dev & 63) & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  return e;
+}
 
 // One kernel launch of an entry point on context c: counted, optionally timed, checked.
 #define XMOD_LAUNCH(c, kind, expr)               \

@@ -1,18 +1,52 @@
 // Log probabilities of given tokens with the entropy and the largest alternatives, and
 // their gradient at the logits.
 
+#include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace xmod {
 
+using namespace tc;
+
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---------------------------------------------------------------- forward
+//
+// One pass: every thread keeps a running maximum m, l = sum e^(x - m) and
+// u = sum e^(x - m) (x - m); then lse = m + ln l and the entropy is ln l - u / l, whose
+// terms all have one sign. A logit costs 5 instructions (3 without the entropy), which two
+// thirds of the issue slots hold at the full memory rate: the kernel is bound by memory, and
+// laid out to keep reading. A CTA works rows off one after the other through a ring of
+// 16 KB chunks that bulk copies fill, three ahead and across row ends, so the ends of a row
+// (reductions, the alternatives) do not stop the memory. Few rows are split over the CTAs of
+// a cluster, which join through distributed shared memory.
+//
+// The alternatives. Logits are ranked by 64-bit keys, the value's order above the inverted
+// token number: keys are distinct, so ties need no care. A row's candidates are the logits
+// above a threshold, the k-th best of the chunks before (a later logit that equals it loses
+// the tie). Where many threads of a chunk are above it (in the first chunk all are), the
+// chunk's own threshold is the k-th largest of the maxima of groups of threads: k logits are
+// at least that large, and only k groups can hold any. So the buffer cannot overflow,
+// whatever the logits' order. Candidates are ranked by counting the larger ones.
+
+constexpr int kLpThreads = 256;
+constexpr int kChunk = 16384;      // bytes
+constexpr int kLpStages = 3;
+constexpr int kVecs = kChunk / 16 / kLpThreads;   // vectors a thread takes of a chunk
+constexpr int kKeep = 512;         // candidates a chunk may start with
+
 struct LogprobArgs {
-  int V, top_k;
-  int64_t ld;
+  int V, top_k, splits;
+  int64_t N, ld;
   const void* logits;
   const int32_t* target;
   float *logp, *entropy, *lse;
@@ -21,91 +55,394 @@ struct LogprobArgs {
   int* status;
 };
 
-// Order of two logits as unsigned keys: larger value, larger key; -0 equals +0.
-__device__ __forceinline__ uint32_t order_key(float x) {
+// Order of a logit as an unsigned number: larger value, larger number; -0 equals +0, NaN on
+// top. And back.
+__device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
-  if (x != x) return 0xffffffffu;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return x != x ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float x, int token) {
+  return (uint64_t)order_of(x) << 32 | (0xffffffffu - (uint32_t)token);
+}
+__device__ __forceinline__ int token_of(uint64_t key) {
+  return (int)(0xffffffffu - (uint32_t)key);
 }
 
-// One block per row.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Maximum of two fp32, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Largest element of a 16-byte vector, NaN if there is one.
+template <typename T> __device__ __forceinline__ float vec_max(const uint4& v) {
+  if constexpr (sizeof(T) == 4) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3]));
+    const float2 f = __bfloat1622float2(m);
+    return max_nan(f.x, f.y);
+  }
+}
+template <typename T> __device__ __forceinline__ float vec_at(const uint4& v, int i) {
+  const float2 f = vec_pair<T>(v, i >> 1);
+  return i & 1 ? f.y : f.x;
+}
+template <typename T> __device__ __forceinline__ void vec_clear(uint4& v, int i) {   // to -inf
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+  if constexpr (sizeof(T) == 4)
+    w[i] = 0xff800000u;
+  else
+    w[i >> 1] = i & 1 ? (w[i >> 1] & 0x0000ffffu) | 0xff800000u : (w[i >> 1] & 0xffff0000u) | 0xff80u;
+}
+
+struct Moments {
+  float m, l, u;
+};
+// Both over the same maximum. Nothing seen: l = 0.
+__device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
+  Moments r;
+  r.m = fmaxf(a.m, b.m);
+  const float da = a.m - r.m, db = b.m - r.m;
+  const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
+  r.l = a.l * fa + b.l * fb;
+  r.u = (a.l > 0.f ? fa * (a.u + da * a.l) : 0.f) + (b.l > 0.f ? fb * (b.u + db * b.l) : 0.f);
+  return r;
+}
+
+// A row's (or a split's) logits in 16-byte vectors, aligned: `head` elements of the first
+// vector and what follows `count` elements do not belong to it.
+struct Span {
+  const uint4* vecs;
+  int head, count, nvec, full, token0;   // full: vectors wholly inside the buffer
+};
 template <typename T>
-__global__ void __launch_bounds__(256) token_logprobs_rows_kernel(LogprobArgs a) {
-  __shared__ float red[8];
-  __shared__ unsigned long long best_s[8];
-  const int64_t n = blockIdx.x;
-  const T* x = (const T*)a.logits + n * a.ld;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  float m = -INFINITY;
-  bool bad = false;
-  for (int v = tid; v < a.V; v += 256) {
-    const float f = Elem<T>::to_f(x[v]);
-    m = fmaxf(m, f);
-    bad |= !(f < INFINITY);   // NaN or +infinity
-  }
-  m = warp_max(m);
-  if (lane == 0) red[warp] = m;
-  bad = __syncthreads_or(bad);
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
-  __syncthreads();
-  bad |= m == -INFINITY;
-  float l = 0.f, u = 0.f;
-  for (int v = tid; v < a.V; v += 256) {
-    const float y = Elem<T>::to_f(x[v]) - m, e = expf(y);
-    l += e;
-    if (e > 0.f) u = fmaf(e, y, u);
-  }
-  l = warp_sum(l);
-  if (lane == 0) red[warp] = l;
-  __syncthreads();
-  l = 0.f;
-  for (int i = 0; i < 8; ++i) l += red[i];
-  __syncthreads();
-  u = warp_sum(u);
-  if (lane == 0) red[warp] = u;
-  __syncthreads();
-  u = 0.f;
-  for (int i = 0; i < 8; ++i) u += red[i];
-  const float nan = __int_as_float(0x7fc00000);
-  const float ll = logf(l);
-  if (tid == 0) {
-    if (bad) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-    if (a.lse) a.lse[n] = bad ? nan : m + ll;
-    if (a.entropy) a.entropy[n] = bad ? nan : ll - u / l;
-    if (a.logp) {
-      const int t = a.target[n];
-      if (t >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-      a.logp[n] = t < 0 ? 0.f : bad || t >= a.V ? nan : (Elem<T>::to_f(x[t]) - m) - ll;
-    }
-  }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < a.top_k; ++k) {
-    unsigned long long best = 0;
-    for (int v = tid; v < a.V; v += 256) {
-      const unsigned long long key =
-          ((unsigned long long)order_key(Elem<T>::to_f(x[v])) << 32) | (0xffffffffu - (uint32_t)v);
-      if (key < last && key > best) best = key;
-    }
-    for (int o = 16; o; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-      best = other > best ? other : best;
-    }
-    if (lane == 0) best_s[warp] = best;
-    __syncthreads();
-    for (int i = 0; i < 8; ++i) best = best_s[i] > best ? best_s[i] : best;
-    __syncthreads();
-    last = best;
-    const int v = (int)(0xffffffffu - (uint32_t)best);
-    if (tid == 0) {
-      a.top_idx[n * a.top_k + k] = v;
-      a.top_logp[n * a.top_k + k] = bad ? nan : (Elem<T>::to_f(x[v]) - m) - ll;
-    }
-  }
+__device__ __forceinline__ Span span_of(const LogprobArgs& a, int64_t row, int split) {
+  constexpr int VE = 16 / sizeof(T);
+  Span s;
+  const int per = (a.V + a.splits - 1) / a.splits;
+  s.token0 = min(a.V, split * per);
+  s.count = min(a.V, s.token0 + per) - s.token0;
+  const uintptr_t at = (uintptr_t)((const T*)a.logits + row * a.ld + s.token0);
+  s.head = (int)(at & 15) / (int)sizeof(T);
+  s.vecs = (const uint4*)(at & ~(uintptr_t)15);
+  s.full = s.count ? (s.head + s.count) / VE : 0;
+  s.nvec = s.count ? (s.head + s.count + VE - 1) / VE : 0;
+  return s;
+}
+__device__ __forceinline__ int span_chunks(const Span& s) {
+  return (s.nvec * 16 + kChunk - 1) / kChunk;
 }
 
+// Shared memory behind the ring.
+struct LpShared {
+  uint64_t full[kLpStages];
+  uint64_t best;            // the chunk's own threshold
+  int count, abort;
+  uint64_t group[kLpThreads];
+  Moments moments[kLpThreads / 32];
+  Moments total;
+  uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
+};
+
+// Threads whose maxima stand together for the chunk's own threshold: at least 4 top_k groups
+// (a looser threshold lets more candidates in, more groups cost more to rank).
+__host__ __device__ constexpr int lp_group(int top_k) {
+  return top_k <= 16 ? 4 : top_k <= 32 ? 2 : 1;
+}
+// Candidate keys the buffer holds: those kept, and those of a chunk, which come from at
+// most top_k groups (or 16 threads) of at most `per_thread` logits a thread.
+__host__ __device__ constexpr int lp_capacity(int top_k, int per_thread) {
+  const int threads = top_k * lp_group(top_k) > 16 ? top_k * lp_group(top_k) : 16;
+  return top_k == 0 ? 0 : kKeep + threads * per_thread;
+}
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const LogprobArgs a) {
+  constexpr int VE = 16 / sizeof(T);
+  extern __shared__ __align__(128) uint8_t smem[];
+  LpShared& sh = *reinterpret_cast<LpShared*>(smem + kLpStages * kChunk);
+  uint64_t* cand = reinterpret_cast<uint64_t*>(&sh + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = a.splits > 1 ? (int)cluster_ctarank() : 0;
+  const int64_t row0 = blockIdx.x / a.splits, row_step = gridDim.x / a.splits;
+  const int k = a.top_k;
+  volatile int* abort_flag = &sh.abort;
+
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < kLpStages; ++i) mbar_init(smem_u32(&sh.full[i]), 1);
+    sh.abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+
+  // the copies' place in the rows (thread 0), `kLpStages` chunks ahead of the reading
+  int64_t issue_row = row0;
+  int issue_chunk = 0, issue_stage = 0;
+  uint32_t issued = 0;
+  auto issue = [&]() {
+    while (issue_row < a.N) {
+      const Span s = span_of<T>(a, issue_row, split);
+      if (issue_chunk >= span_chunks(s)) {
+        issue_chunk = 0;
+        issue_row += row_step;
+        continue;
+      }
+      const int v0 = issue_chunk * (kChunk / 16);
+      const int bytes = max(0, min(kChunk / 16, s.full - v0)) * 16;
+      const uint32_t bar = smem_u32(&sh.full[issue_stage]);
+      mbar_arrive_expect_tx(bar, bytes);
+      if (bytes) bulk_load(smem_u32(smem) + issue_stage * kChunk, s.vecs + v0, bytes, bar);
+      issue_stage = issue_stage == kLpStages - 1 ? 0 : issue_stage + 1;
+      ++issue_chunk;
+      ++issued;
+      return;
+    }
+  };
+  if (tid == 0)
+    for (int i = 0; i < kLpStages; ++i) issue();
+
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int64_t row = row0; row < a.N; row += row_step) {
+    const Span s = span_of<T>(a, row, split);
+    const int chunks = span_chunks(s);
+    float x_t = 0.f;   // the target's logit, on its way while the row is read
+    int target = -1;
+    if (split == 0 && tid == 0 && a.logp) {
+      target = a.target[row];
+      if (target >= 0 && target < a.V) x_t = Elem<T>::to_f(((const T*)a.logits + row * a.ld)[target]);
+    }
+    // ranks the candidates: the k best to sh.top in order, and (compact) back to the buffer
+    auto rank = [&](int count, bool compact) {
+      for (int i = tid; i < count; i += kLpThreads) {
+        const uint64_t mine = cand[i];
+        int above = 0;
+        for (int j = 0; j < count; ++j) above += cand[j] > mine;
+        if (above < k) sh.top[above] = mine;
+      }
+      __syncthreads();
+      if (compact) {
+        const int kept = min(count, k);
+        if (tid < kept) cand[tid] = sh.top[tid];
+        if (tid == 0) sh.count = kept;
+        __syncthreads();
+      }
+    };
+    float m = -FLT_MAX;
+    float2 l2 = make_float2(0.f, 0.f), u2 = l2;
+    float thr = -INFINITY;   // candidates are above it
+    bool has_thr = false;
+    int bound = 0;           // at most this many candidates are in the buffer
+    if (k && tid == 0) sh.count = 0;
+    for (int c = 0; c < chunks; ++c) {
+      mbar_wait(smem_u32(&sh.full[stage]), phase, abort_flag, a.status);
+      const uint4* buf = reinterpret_cast<const uint4*>(smem + stage * kChunk);
+      const int v0 = c * (kChunk / 16);
+      uint4 x[kVecs];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int v = v0 + tid + i * kLpThreads;
+        x[i] = buf[tid + i * kLpThreads];
+        if (v >= s.full) {   // past the row, or its last elements: one by one
+          uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+          x[i] = make_uint4(ninf, ninf, ninf, ninf);
+          if (v < s.nvec) {
+            const T* p = reinterpret_cast<const T*>(s.vecs + v);
+            T* e = reinterpret_cast<T*>(&x[i]);
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+              if (v * VE + j < s.head + s.count) e[j] = p[j];
+          }
+        }
+        if (v == 0) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (j < s.head) vec_clear<T>(x[i], j);
+        }
+      }
+      float top = vec_max<T>(x[0]);
+#pragma unroll
+      for (int i = 1; i < kVecs; ++i) top = max_nan(top, vec_max<T>(x[i]));
+      if (!(top <= m)) {   // larger, or a NaN: that one makes l 0 and the row bad
+        const float m2 = top != top ? INFINITY : top;
+        const float d = m - m2, f = ex2(d * kLog2e);
+        const float2 f2 = make_float2(f, f), d2 = make_float2(d, d);
+        if (ENT) u2 = l2.x + l2.y > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
+        l2 = mul2(l2, f2);
+        m = m2;
+      }
+      const float2 neg = make_float2(-m, -m), lg = make_float2(kLog2e, kLog2e);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+#pragma unroll
+        for (int j = 0; j < VE / 2; ++j) {
+          float2 d = add2(vec_pair<T>(x[i], j), neg);
+          if (ENT) {
+            d.x = fmaxf(d.x, -1e30f);   // -infinity times 0 below would be a NaN
+            d.y = fmaxf(d.y, -1e30f);
+          }
+          const float2 t = mul2(d, lg);
+          const float2 e = make_float2(ex2(t.x), ex2(t.y));
+          l2 = add2(l2, e);
+          if (ENT) u2 = fma2(e, d, u2);
+        }
+      }
+      const bool above = k && (has_thr ? !(top <= thr) : v0 + tid < s.nvec);
+      const int active = __syncthreads_count(above);   // also: the stage is read
+      if (tid == 0 && !*abort_flag) issue();
+      if (++stage == kLpStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (active) {
+        uint64_t own = 0;   // the chunk's own threshold
+        if (active > 16) {
+          unsigned long long best = 0;
+          if (above) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+              for (int j = 0; j < VE; ++j) {
+                const int e = (v0 + tid + i * kLpThreads) * VE + j - s.head;
+                const float f = vec_at<T>(x[i], j);
+                if (e >= 0 && e < s.count && !(has_thr && f <= thr))
+                  best = max(best, (unsigned long long)key_of(f, s.token0 + e));
+              }
+          }
+          const int lanes = lp_group(k);
+          for (int o = 1; o < lanes; o <<= 1)
+            best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+          if (tid % lanes == 0) sh.group[tid / lanes] = best;
+          if (tid == 0) sh.best = 0;
+          __syncthreads();
+          const int groups = kLpThreads / lanes;
+          if (tid < groups) {
+            const uint64_t mine = sh.group[tid];
+            int larger = 0;
+            for (int j = 0; j < groups; ++j) larger += sh.group[j] > mine;
+            if (mine && larger == k - 1) sh.best = mine;
+          }
+          __syncthreads();
+          own = sh.best;   // 0 where fewer than k groups hold candidates
+        }
+        if (above) {
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+              const int e = (v0 + tid + i * kLpThreads) * VE + j - s.head;
+              const float f = vec_at<T>(x[i], j);
+              if (e >= 0 && e < s.count && !(has_thr && f <= thr)) {
+                const uint64_t key = key_of(f, s.token0 + e);
+                if (key >= own) cand[atomicAdd(&sh.count, 1)] = key;
+              }
+            }
+        }
+        bound += (active > 16 ? min(active, k * lp_group(k)) : active) * kVecs * VE;
+        if (!has_thr || bound > kKeep) {
+          __syncthreads();
+          bound = sh.count;
+          if (bound >= k && (!has_thr || bound > kKeep / 2)) {
+            rank(bound, true);
+            thr = value_of((uint32_t)(cand[k - 1] >> 32));
+            has_thr = true;
+            bound = k;
+          }
+          __syncthreads();
+        }
+      }
+    }
+    // ---- the row's end: this CTA's sums and candidates
+    Moments mo{m, l2.x + l2.y, u2.x + u2.y};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      mo = join(mo, Moments{__shfl_xor_sync(0xffffffffu, mo.m, o), __shfl_xor_sync(0xffffffffu, mo.l, o),
+                            __shfl_xor_sync(0xffffffffu, mo.u, o)});
+    if (lane == 0) sh.moments[warp] = mo;
+    __syncthreads();
+    int found = k ? sh.count : 0;
+    if (k) rank(found, false);
+    found = min(found, k);
+    mo = sh.moments[0];
+    for (int w = 1; w < kLpThreads / 32; ++w) mo = join(mo, sh.moments[w]);
+    if (a.splits > 1) {
+      if (tid == 0) {
+        sh.total = mo;
+        sh.count = found;
+      }
+      cluster_sync_all();
+      if (split == 0) {
+        int all = 0;
+        for (int r = 0; r < a.splits; ++r) {
+          const uint32_t at = mapa_shared(smem_u32(&sh.total), r);
+          Moments other;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.m) : "r"(at) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.l) : "r"(at + 4) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.u) : "r"(at + 8) : "memory");
+          mo = r ? join(mo, other) : other;
+          if (k) {
+            int n;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                         : "=r"(n)
+                         : "r"(mapa_shared(smem_u32(&sh.count), r))
+                         : "memory");
+            if (tid < n)
+              asm volatile("ld.shared::cluster.u64 %0, [%1];"
+                           : "=l"(cand[all + tid])
+                           : "r"(mapa_shared(smem_u32(&sh.top[0]), r) + 8 * tid)
+                           : "memory");
+            all += n;
+          }
+        }
+        __syncthreads();
+        if (k) rank(all, false);
+      }
+      cluster_sync_all();   // the other CTAs' shared memory has been read
+      if (split != 0) continue;
+    }
+    const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
+    const float ll = logf(mo.l), nan = __int_as_float(0x7fc00000);
+    if (tid == 0) {
+      if (bad || target >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+      if (a.lse) a.lse[row] = bad ? nan : mo.m + ll;
+      if (a.entropy) a.entropy[row] = bad ? nan : ll - mo.u / mo.l;
+      if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (x_t - mo.m) - ll;
+    }
+    if (tid < k) {
+      const uint64_t key = sh.top[tid];
+      a.top_idx[row * k + tid] = token_of(key);
+      a.top_logp[row * k + tid] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
+    }
+  }
+  // copies still in flight (after a wait that gave up) land before the CTA ends
+  if (tid == 0)
+    for (uint32_t j = issued > kLpStages ? issued - kLpStages : 0; j < issued; ++j)
+      mbar_wait(smem_u32(&sh.full[j % kLpStages]), (j / kLpStages) & 1, nullptr, a.status);
+}
+
+// ---------------------------------------------------------------- gradient
+//
+// dx_v = g (1[v = t] - p_v) - gH p_v (ln p_v + H): one reading and one writing of the
+// logits' size, 5 instructions a logit: bound by memory. A CTA takes 16 KB of a row, four
+// 16-byte vectors a thread, aligned in the output; where the logits' rows are aligned
+// differently (another row stride), their elements are loaded one by one, which the L1
+// cache makes up for.
 struct LogprobBwdArgs {
-  int V;
-  int64_t ld, ldd;
+  int V, chunks;
+  int64_t N, ld, ldd;
   const void* logits;
   const int32_t* target;
   const float *lse, *entropy, *g_logp, *g_entropy;
@@ -114,30 +451,124 @@ struct LogprobBwdArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(LogprobBwdArgs a) {
-  const int64_t n = blockIdx.x;
-  const T* x = (const T*)a.logits + n * a.ld;
-  T* d = (T*)a.dlogits + n * a.ldd;
-  int t = a.g_logp ? a.target[n] : -1;
-  if (t >= a.V) {
-    if (threadIdx.x == 0) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-    t = -1;
-  }
-  const float g = t >= 0 ? a.g_logp[n] : 0.f, gh = a.g_entropy ? a.g_entropy[n] : 0.f;
-  const float lse = a.lse[n], ent = a.g_entropy ? a.entropy[n] : 0.f;
-  for (int v = threadIdx.x; v < a.V; v += 256) {
-    float r = 0.f;
-    if (g != 0.f || gh != 0.f) {
-      const float y = Elem<T>::to_f(x[v]) - lse, p = expf(y);
-      r = -p * (p > 0.f ? fmaf(gh, y + ent, g) : g);
-      if (v == t) r += g;
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const LogprobBwdArgs a) {
+  constexpr int VE = 16 / sizeof(T);
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t item = blockIdx.x; item < a.N * a.chunks; item += gridDim.x) {
+    const int64_t row = item / a.chunks;
+    const int chunk = (int)(item - row * a.chunks);
+    const T* x = (const T*)a.logits + row * a.ld;
+    T* d = (T*)a.dlogits + row * a.ldd;
+    // element 0 of the row is element `head` of its first aligned vector
+    const int head = (int)((uintptr_t)d & 15) / (int)sizeof(T);
+    const bool same = (((uintptr_t)x ^ (uintptr_t)d) & 15) == 0;
+    const int e0 = (chunk * (kChunk / 16) + (int)threadIdx.x) * VE - head;
+    uint4 v[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int e = e0 + i * kLpThreads * VE;
+      if (same && e >= 0 && e + VE <= a.V) {
+        v[i] = *reinterpret_cast<const uint4*>(x + e);
+      } else {
+        T* w = reinterpret_cast<T*>(&v[i]);
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          w[j] = e + j >= 0 && e + j < a.V ? x[e + j] : Elem<T>::from_f(0.f);
+      }
     }
-    d[v] = Elem<T>::from_f(r);
+    int t = a.g_logp ? a.target[row] : -1;
+    if (t >= a.V) {
+      if (threadIdx.x == 0 && chunk == 0) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+      t = -1;
+    }
+    const float g = t >= 0 ? a.g_logp[row] : 0.f, gh = a.g_entropy ? a.g_entropy[row] : 0.f;
+    const bool zero = g == 0.f && gh == 0.f;
+    const float lse = a.lse[row], ent = a.g_entropy ? a.entropy[row] : 0.f;
+    const float2 neg = make_float2(-lse, -lse), lg = make_float2(kLog2e, kLog2e);
+    // -(g + gH (y + H)) = -gH y - (g + gH H)
+    const float b = -fmaf(gh, ent, g);
+    const float2 mul = make_float2(-gh, -gh), add = make_float2(b, b);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int e = e0 + i * kLpThreads * VE;
+      if (e >= a.V || e + VE <= 0) continue;
+      uint4 out;
+#pragma unroll
+      for (int j = 0; j < VE / 2; ++j) {
+        float2 y = add2(vec_pair<T>(v[i], j), neg);
+        const float2 tt = mul2(y, lg);
+        const float2 p = make_float2(ex2(tt.x), ex2(tt.y));
+        y.x = fmaxf(y.x, -1e4f);   // p is 0 long before; -infinity times 0 would be a NaN
+        y.y = fmaxf(y.y, -1e4f);
+        float2 r = mul2(p, fma2(mul, y, add));
+        if (zero) r = make_float2(0.f, 0.f);
+        if (e + 2 * j == t) r.x += g;
+        if (e + 2 * j + 1 == t) r.y += g;
+        set_vec_pair<T>(out, j, r);
+      }
+      if (e >= 0 && e + VE <= a.V) {
+        *reinterpret_cast<uint4*>(d + e) = out;
+      } else {
+        const T* w = reinterpret_cast<const T*>(&out);
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (e + j >= 0 && e + j < a.V) d[e + j] = w[j];
+      }
+    }
   }
 }
 
+// ---------------------------------------------------------------- host
+
 bool ptr16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
 bool ptr4_or_null(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+template <typename T, bool ENT>
+cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
+  LogprobArgs a = a0;
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  // CTAs of a cluster share a row while there are SMs for them and 16 KB chunks enough
+  a.splits = 1;
+  while (a.splits < 8 && a.N * a.splits * 2 <= sms && (int64_t)a.V * sizeof(T) >= 2 * a.splits * (int64_t)kChunk)
+    a.splits *= 2;
+  const int smem = kLpStages * kChunk + (int)sizeof(LpShared) +
+                   8 * lp_capacity(a.top_k, kVecs * 16 / (int)sizeof(T));
+  auto kernel = token_logprobs_kernel<T, ENT>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kernel, kLpStages * kChunk + (int)sizeof(LpShared) +
+                                         8 * lp_capacity(XMOD_MAX_TOP_K, kVecs * 8), done);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)sms * 3;   // resident: by registers, and by shared memory
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.splits > 1 ? a.N * a.splits : a.N < most ? a.N : most));
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T>
+cudaError_t launch_logprobs_bwd(const Ctx& c, const LogprobBwdArgs& a0) {
+  LogprobBwdArgs a = a0;
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int VE = 16 / (int)sizeof(T);
+  // vectors of a row at the worst alignment, in chunks
+  a.chunks = (int)(((int64_t)a.V + 2 * VE - 2) / VE / (kChunk / 16)) + 1;
+  const int64_t items = a.N * a.chunks, most = (int64_t)sms * 64;
+  return launch_pdl(token_logprobs_bwd_kernel<T>, dim3((unsigned)(items < most ? items : most)),
+                    dim3(kLpThreads), 0, c.stream, a);
+}
 
 }  // namespace
 }  // namespace xmod
@@ -159,15 +590,16 @@ int xmod_token_logprobs(xmod_dtype dt, int64_t N, int V, const void* logits, int
   const void* ps[] = {target, logp, entropy, lse, top_idx, top_logp, status_out};
   for (const void* p : ps)
     if (!ptr4_or_null(p)) return XMOD_ERR_INVALID_ARG;
-  if (top_k > XMOD_MAX_TOP_K || N > INT32_MAX) return XMOD_ERR_UNSUPPORTED;
-  const LogprobArgs a{V, top_k, ld, logits, target, logp, entropy, lse, top_idx, top_logp,
+  if (top_k > XMOD_MAX_TOP_K || N > INT32_MAX || V > INT32_MAX - 65536) return XMOD_ERR_UNSUPPORTED;
+  const LogprobArgs a{V, top_k, 1, N, ld, logits, target, logp, entropy, lse, top_idx, top_logp,
                       status_out};
   const Ctx c{(cudaStream_t)stream, status_out};
   if (dt == XMOD_BF16)
-    token_logprobs_rows_kernel<__nv_bfloat16><<<(unsigned)N, 256, 0, c.stream>>>(a);
+    XMOD_LAUNCH(c, "token_logprobs", (entropy ? launch_logprobs<__nv_bfloat16, true>(c, a)
+                                              : launch_logprobs<__nv_bfloat16, false>(c, a)));
   else
-    token_logprobs_rows_kernel<float><<<(unsigned)N, 256, 0, c.stream>>>(a);
-  XMOD_LAUNCH(c, "token_logprobs", cudaGetLastError());
+    XMOD_LAUNCH(c, "token_logprobs",
+                (entropy ? launch_logprobs<float, true>(c, a) : launch_logprobs<float, false>(c, a)));
   return XMOD_OK;
 }
 
@@ -184,15 +616,14 @@ int xmod_token_logprobs_bwd(xmod_dtype dt, int64_t N, int V, const void* logits,
   const void* ps[] = {target, lse, entropy, g_logp, g_entropy, status_out};
   for (const void* p : ps)
     if (!ptr4_or_null(p)) return XMOD_ERR_INVALID_ARG;
-  if (N > INT32_MAX) return XMOD_ERR_UNSUPPORTED;
-  const LogprobBwdArgs a{V, ld, ldd, logits, target, lse, entropy, g_logp, g_entropy, dlogits,
-                         status_out};
+  if (N > INT32_MAX || V > INT32_MAX - 65536) return XMOD_ERR_UNSUPPORTED;
+  const LogprobBwdArgs a{V, 1, N, ld, ldd, logits, target, lse, entropy, g_logp, g_entropy,
+                         dlogits, status_out};
   const Ctx c{(cudaStream_t)stream, status_out};
   if (dt == XMOD_BF16)
-    token_logprobs_bwd_kernel<__nv_bfloat16><<<(unsigned)N, 256, 0, c.stream>>>(a);
+    XMOD_LAUNCH(c, "token_logprobs_bwd", launch_logprobs_bwd<__nv_bfloat16>(c, a));
   else
-    token_logprobs_bwd_kernel<float><<<(unsigned)N, 256, 0, c.stream>>>(a);
-  XMOD_LAUNCH(c, "token_logprobs_bwd", cudaGetLastError());
+    XMOD_LAUNCH(c, "token_logprobs_bwd", launch_logprobs_bwd<float>(c, a));
   return XMOD_OK;
 }
 
