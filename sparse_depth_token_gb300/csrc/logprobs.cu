@@ -21,22 +21,25 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------- forward
 //
-// One pass: every thread keeps a running maximum m, l = sum e^(x - m) and
-// u = sum e^(x - m) (x - m); then lse = m + ln l and the entropy is ln l - u / l, whose
-// terms all have one sign. A logit costs 5 instructions (3 without the entropy), which two
-// thirds of the issue slots hold at the full memory rate: the kernel is bound by memory, and
-// laid out to keep reading. A CTA works rows off one after the other through a ring of
-// 16 KB chunks that bulk copies fill, three ahead and across row ends, so the ends of a row
-// (reductions, the alternatives) do not stop the memory. Few rows are split over the CTAs of
-// a cluster, which join through distributed shared memory.
+// One pass: every thread keeps a running maximum m, l = sum e^(x - m) and u = sum e^(x - m)
+// (x - m); then lse = m + ln l and the entropy is ln l - u / l, whose terms all have one
+// sign. A bf16 logit costs 5 instructions (4 without the entropy), half of the issue
+// slots at the full memory rate: the kernel is bound by memory, and laid out to keep
+// reading. A CTA works rows off one after the other through a ring of 16 KB chunks that bulk
+// copies fill, three ahead and across row ends, so the ends of a row (reductions, the
+// alternatives) do not stop the memory. Few rows are split over the CTAs of a cluster, which
+// join through distributed shared memory.
 //
 // The alternatives. Logits are ranked by 64-bit keys, the value's order above the inverted
 // token number: keys are distinct, so ties need no care. A row's candidates are the logits
 // above a threshold, the k-th best of the chunks before (a later logit that equals it loses
 // the tie). Where many threads of a chunk are above it (in the first chunk all are), the
-// chunk's own threshold is the k-th largest of the maxima of groups of threads: k logits are
-// at least that large, and only k groups can hold any. So the buffer cannot overflow,
-// whatever the logits' order. Candidates are ranked by counting the larger ones.
+// chunk gets a threshold of its own, the k-th largest of the maxima of groups of threads: k
+// logits are at least that large, and hardly any besides. Should ties let more threads in
+// than the buffer has room for, the groups' best keys take the place of their maxima: then
+// only k groups can hold any. So the buffer cannot overflow, whatever the logits' order. A
+// warp looks at one thread's logits of a chunk at a time, a lane each; candidates are ranked
+// by counting the larger ones.
 
 constexpr int kLpThreads = 256;
 constexpr int kChunk = 16384;      // bytes
@@ -98,6 +101,19 @@ template <typename T> __device__ __forceinline__ float vec_at(const uint4& v, in
   const float2 f = vec_pair<T>(v, i >> 1);
   return i & 1 ? f.y : f.x;
 }
+// Elements below -2^123 become -2^123; a NaN stays.
+template <typename T> __device__ __forceinline__ void vec_finite(uint4& v) {
+  if constexpr (sizeof(T) == 4) {
+    float* f = reinterpret_cast<float*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = max_nan(f[i], -1.0633824e37f);
+  } else {
+    __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&v);
+    const __nv_bfloat162_raw low{0xfd00, 0xfd00};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __hmax2_nan(b[i], __nv_bfloat162(low));
+  }
+}
 template <typename T> __device__ __forceinline__ void vec_clear(uint4& v, int i) {   // to -inf
   uint32_t* w = reinterpret_cast<uint32_t*>(&v);
   if constexpr (sizeof(T) == 4)
@@ -106,19 +122,18 @@ template <typename T> __device__ __forceinline__ void vec_clear(uint4& v, int i)
     w[i >> 1] = i & 1 ? (w[i >> 1] & 0x0000ffffu) | 0xff800000u : (w[i >> 1] & 0xffff0000u) | 0xff80u;
 }
 
+// Over a common maximum m (l, u: sums of e^(x - m) and of e^(x - m) log2(e^(x - m))).
+// Nothing seen: l = 0.
 struct Moments {
   float m, l, u;
+  // to a maximum at or above its own
+  __device__ __forceinline__ void raise(float m2) {
+    const float d = (m - m2) * kLog2e, f = ex2(d);
+    u = l > 0.f ? f * fmaf(d, l, u) : 0.f;
+    l *= f;
+    m = m2;
+  }
 };
-// Both over the same maximum. Nothing seen: l = 0.
-__device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
-  Moments r;
-  r.m = fmaxf(a.m, b.m);
-  const float da = a.m - r.m, db = b.m - r.m;
-  const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
-  r.l = a.l * fa + b.l * fb;
-  r.u = (a.l > 0.f ? fa * (a.u + da * a.l) : 0.f) + (b.l > 0.f ? fb * (b.u + db * b.l) : 0.f);
-  return r;
-}
 
 // A row's (or a split's) logits in 16-byte vectors, aligned: `head` elements of the first
 // vector and what follows `count` elements do not belong to it.
@@ -148,8 +163,10 @@ __device__ __forceinline__ int span_chunks(const Span& s) {
 struct LpShared {
   uint64_t full[kLpStages];
   uint64_t best;            // the chunk's own threshold
+  uint32_t least;           // and in values
   int count, abort;
-  uint64_t group[kLpThreads];
+  alignas(16) uint64_t group[kLpThreads];
+  alignas(16) uint32_t group_max[kLpThreads];
   Moments moments[kLpThreads / 32];
   Moments total;
   uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
@@ -230,6 +247,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
       for (int i = tid; i < count; i += kLpThreads) {
         const uint64_t mine = cand[i];
         int above = 0;
+#pragma unroll 4
         for (int j = 0; j < count; ++j) above += cand[j] > mine;
         if (above < k) sh.top[above] = mine;
       }
@@ -241,7 +259,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
         __syncthreads();
       }
     };
-    float m = -FLT_MAX;
+    Moments mo{-FLT_MAX, 0.f, 0.f};
     float2 l2 = make_float2(0.f, 0.f), u2 = l2;
     float thr = -INFINITY;   // candidates are above it
     bool has_thr = false;
@@ -253,107 +271,144 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
       const int v0 = c * (kChunk / 16);
       uint4 x[kVecs];
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int v = v0 + tid + i * kLpThreads;
-        x[i] = buf[tid + i * kLpThreads];
-        if (v >= s.full) {   // past the row, or its last elements: one by one
-          uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-          x[i] = make_uint4(ninf, ninf, ninf, ninf);
-          if (v < s.nvec) {
-            const T* p = reinterpret_cast<const T*>(s.vecs + v);
-            T* e = reinterpret_cast<T*>(&x[i]);
+      for (int i = 0; i < kVecs; ++i) x[i] = buf[tid + i * kLpThreads];
+      if (c == 0 || v0 + kChunk / 16 > s.full) {   // the row's ends
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const int v = v0 + tid + i * kLpThreads;
+          if (v >= s.full) {   // past the row, or its last elements: one by one
+            const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+            x[i] = make_uint4(ninf, ninf, ninf, ninf);
+            if (v < s.nvec) {
+              const T* p = reinterpret_cast<const T*>(s.vecs + v);
+              T* e = reinterpret_cast<T*>(&x[i]);
+#pragma unroll
+              for (int j = 0; j < VE; ++j)
+                if (v * VE + j < s.head + s.count) e[j] = p[j];
+            }
+          }
+          if (v == 0) {
 #pragma unroll
             for (int j = 0; j < VE; ++j)
-              if (v * VE + j < s.head + s.count) e[j] = p[j];
+              if (j < s.head) vec_clear<T>(x[i], j);
           }
-        }
-        if (v == 0) {
-#pragma unroll
-          for (int j = 0; j < VE; ++j)
-            if (j < s.head) vec_clear<T>(x[i], j);
         }
       }
       float top = vec_max<T>(x[0]);
 #pragma unroll
       for (int i = 1; i < kVecs; ++i) top = max_nan(top, vec_max<T>(x[i]));
-      if (!(top <= m)) {   // larger, or a NaN: that one makes l 0 and the row bad
-        const float m2 = top != top ? INFINITY : top;
-        const float d = m - m2, f = ex2(d * kLog2e);
+      if (!(top <= mo.m)) {   // larger, or a NaN: that one makes l 0 and the row bad
+        const float d = (mo.m - (top != top ? INFINITY : top)) * kLog2e, f = ex2(d);
         const float2 f2 = make_float2(f, f), d2 = make_float2(d, d);
         if (ENT) u2 = l2.x + l2.y > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
         l2 = mul2(l2, f2);
-        m = m2;
+        mo.m = top != top ? INFINITY : top;
       }
-      const float2 neg = make_float2(-m, -m), lg = make_float2(kLog2e, kLog2e);
+      if (fabsf(mo.m) < 1e36f) {
+        const float2 neg = make_float2(-mo.m, -mo.m), lg = make_float2(kLog2e, kLog2e);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
+        for (int i = 0; i < kVecs; ++i) {
+          // an infinite exponent times 0 would be a NaN: such logits become low finite ones,
+          // whose terms are 0 as well
+          if (ENT) vec_finite<T>(x[i]);
 #pragma unroll
-        for (int j = 0; j < VE / 2; ++j) {
-          float2 d = add2(vec_pair<T>(x[i], j), neg);
-          if (ENT) {
-            d.x = fmaxf(d.x, -1e30f);   // -infinity times 0 below would be a NaN
-            d.y = fmaxf(d.y, -1e30f);
+          for (int j = 0; j < VE / 2; ++j) {
+            // the difference first: exactly 0, and a term of exactly 1, at the maximum
+            const float2 t = mul2(add2(vec_pair<T>(x[i], j), neg), lg);
+            const float2 e = make_float2(ex2(t.x), ex2(t.y));
+            l2 = add2(l2, e);
+            if (ENT) u2 = fma2(e, t, u2);
           }
-          const float2 t = mul2(d, lg);
-          const float2 e = make_float2(ex2(t.x), ex2(t.y));
-          l2 = add2(l2, e);
-          if (ENT) u2 = fma2(e, d, u2);
+        }
+      } else {   // nothing above -infinity yet, or differences that could overflow
+#pragma unroll
+        for (int i = 0; i < kVecs * VE; ++i) {
+          const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
+          l2.x += e;
+          if (ENT) u2.x = fmaf(e, d, u2.x);
         }
       }
       const bool above = k && (has_thr ? !(top <= thr) : v0 + tid < s.nvec);
       const int active = __syncthreads_count(above);   // also: the stage is read
-      if (tid == 0 && !*abort_flag) issue();
-      if (++stage == kLpStages) {
-        stage = 0;
-        phase ^= 1;
-      }
       if (active) {
-        uint64_t own = 0;   // the chunk's own threshold
+        // element j of vector v: still in the chunk, but for a row's last vector
+        auto logit = [&](int v, int j) {
+          return v < s.full ? Elem<T>::to_f(reinterpret_cast<const T*>(buf + (v - v0))[j])
+                            : Elem<T>::to_f(reinterpret_cast<const T*>(s.vecs + v)[j]);
+        };
+        auto candidate = [&](int v, int j, float& f) {
+          const int e = v * VE + j - s.head;
+          if (e < 0 || e >= s.count) return false;
+          f = logit(v, j);
+          return !(has_thr && f <= thr);
+        };
+        const int lanes = lp_group(k), groups = kLpThreads / lanes, most = max(16, k * lanes);
+        uint32_t least = 0;   // the chunk's own threshold: in values,
+        uint64_t own = 0;     // and in keys
         if (active > 16) {
-          unsigned long long best = 0;
-          if (above) {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-              for (int j = 0; j < VE; ++j) {
-                const int e = (v0 + tid + i * kLpThreads) * VE + j - s.head;
-                const float f = vec_at<T>(x[i], j);
-                if (e >= 0 && e < s.count && !(has_thr && f <= thr))
-                  best = max(best, (unsigned long long)key_of(f, s.token0 + e));
-              }
-          }
-          const int lanes = lp_group(k);
-          for (int o = 1; o < lanes; o <<= 1)
-            best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-          if (tid % lanes == 0) sh.group[tid / lanes] = best;
-          if (tid == 0) sh.best = 0;
+          const uint32_t mine = above ? order_of(top) : 0u;
+          uint32_t best = mine;
+          for (int o = 1; o < lanes; o <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+          if (tid % lanes == 0) sh.group_max[tid / lanes] = best;
+          if (tid == 0) sh.least = 0;
           __syncthreads();
-          const int groups = kLpThreads / lanes;
           if (tid < groups) {
-            const uint64_t mine = sh.group[tid];
-            int larger = 0;
-            for (int j = 0; j < groups; ++j) larger += sh.group[j] > mine;
-            if (mine && larger == k - 1) sh.best = mine;
+            const uint32_t g = sh.group_max[tid];
+            int gt = 0, ge = 0;
+#pragma unroll 4
+            for (int j = 0; j < groups; j += 4) {
+              const uint4 o = *reinterpret_cast<const uint4*>(&sh.group_max[j]);
+              gt += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
+              ge += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
+            }
+            if (g && gt < k && ge >= k) sh.least = g;   // one value, whoever writes it
           }
           __syncthreads();
-          own = sh.best;   // 0 where fewer than k groups hold candidates
-        }
-        if (above) {
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-              const int e = (v0 + tid + i * kLpThreads) * VE + j - s.head;
-              const float f = vec_at<T>(x[i], j);
-              if (e >= 0 && e < s.count && !(has_thr && f <= thr)) {
-                const uint64_t key = key_of(f, s.token0 + e);
-                if (key >= own) cand[atomicAdd(&sh.count, 1)] = key;
+          least = sh.least;   // 0 where fewer than k groups hold candidates
+          if (__syncthreads_count(mine && mine >= least) > most) {   // ties: by whole keys
+            unsigned long long key = 0;
+            if (mine && mine >= least) {
+#pragma unroll 1
+              for (int i = 0; i < kVecs * VE; ++i) {
+                const int v = v0 + tid + i / VE * kLpThreads;
+                float f;
+                if (candidate(v, i % VE, f))
+                  key = max(key, (unsigned long long)key_of(f, s.token0 + v * VE + i % VE - s.head));
               }
             }
+            for (int o = 1; o < lanes; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+            if (tid % lanes == 0) sh.group[tid / lanes] = key;
+            if (tid == 0) sh.best = 0;
+            __syncthreads();
+            if (tid < groups) {
+              const uint64_t g = sh.group[tid];
+              int gt = 0;
+              for (int j = 0; j < groups; ++j) gt += sh.group[j] > g;
+              if (g && gt == k - 1) sh.best = g;
+            }
+            __syncthreads();
+            own = sh.best;
+          }
         }
-        bound += (active > 16 ? min(active, k * lp_group(k)) : active) * kVecs * VE;
+        uint32_t todo = __ballot_sync(0xffffffffu, above && order_of(top) >= least);
+        while (todo) {   // a thread's logits of the chunk, one a lane
+          const int from = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int v = v0 + warp * 32 + from + lane / VE * kLpThreads;
+          float f = 0.f;
+          uint64_t key = 0;
+          if (lane < kVecs * VE && candidate(v, lane % VE, f))
+            key = key_of(f, s.token0 + v * VE + lane % VE - s.head);
+          const bool in = key && (uint32_t)(key >> 32) >= least && key >= own;
+          const uint32_t who = __ballot_sync(0xffffffffu, in);
+          int at = 0;
+          if (lane == 0 && who) at = atomicAdd(&sh.count, __popc(who));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+          if (in) cand[at] = key;
+        }
+        bound += min(active, most) * kVecs * VE;
+        __syncthreads();   // the stage is read, the candidates are there
         if (!has_thr || bound > kKeep) {
-          __syncthreads();
           bound = sh.count;
           if (bound >= k && (!has_thr || bound > kKeep / 2)) {
             rank(bound, true);
@@ -361,23 +416,36 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
             has_thr = true;
             bound = k;
           }
-          __syncthreads();
         }
+      }
+      if (tid == 0 && !*abort_flag) issue();
+      if (++stage == kLpStages) {
+        stage = 0;
+        phase ^= 1;
       }
     }
     // ---- the row's end: this CTA's sums and candidates
-    Moments mo{m, l2.x + l2.y, u2.x + u2.y};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      mo = join(mo, Moments{__shfl_xor_sync(0xffffffffu, mo.m, o), __shfl_xor_sync(0xffffffffu, mo.l, o),
-                            __shfl_xor_sync(0xffffffffu, mo.u, o)});
+    mo.l = l2.x + l2.y;
+    mo.u = u2.x + u2.y;
+    mo.raise(warp_max(mo.m));
+    mo.l = warp_sum(mo.l);
+    if (ENT) mo.u = warp_sum(mo.u);
     if (lane == 0) sh.moments[warp] = mo;
     __syncthreads();
-    int found = k ? sh.count : 0;
-    if (k) rank(found, false);
-    found = min(found, k);
-    mo = sh.moments[0];
-    for (int w = 1; w < kLpThreads / 32; ++w) mo = join(mo, sh.moments[w]);
+    int found = 0;
+    if (k) {
+      found = sh.count;
+      rank(found, false);
+      found = min(found, k);
+    }
+    // the first warp finishes the row; the others meet it again at the next row's first
+    // barrier, before anything that it reads here is written
+    if (a.splits == 1 && warp != 0) continue;
+    mo = sh.moments[lane % (kLpThreads / 32)];
+    mo.raise(warp_max(mo.m));
+    if (lane >= kLpThreads / 32) mo.l = mo.u = 0.f;
+    mo.l = warp_sum(mo.l);
+    mo.u = warp_sum(mo.u);
     if (a.splits > 1) {
       if (tid == 0) {
         sh.total = mo;
@@ -392,7 +460,15 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
           asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.m) : "r"(at) : "memory");
           asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.l) : "r"(at + 4) : "memory");
           asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.u) : "r"(at + 8) : "memory");
-          mo = r ? join(mo, other) : other;
+          if (r == 0) {
+            mo = other;
+          } else {
+            const float m2 = fmaxf(mo.m, other.m);
+            mo.raise(m2);
+            other.raise(m2);
+            mo.l += other.l;
+            mo.u += other.u;
+          }
           if (k) {
             int n;
             asm volatile("ld.shared::cluster.s32 %0, [%1];"
@@ -411,20 +487,20 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
         if (k) rank(all, false);
       }
       cluster_sync_all();   // the other CTAs' shared memory has been read
-      if (split != 0) continue;
+      if (split != 0 || warp != 0) continue;
     }
     const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
     const float ll = logf(mo.l), nan = __int_as_float(0x7fc00000);
     if (tid == 0) {
       if (bad || target >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
       if (a.lse) a.lse[row] = bad ? nan : mo.m + ll;
-      if (a.entropy) a.entropy[row] = bad ? nan : ll - mo.u / mo.l;
+      if (a.entropy) a.entropy[row] = bad ? nan : ll - 0.6931471805599453f * mo.u / mo.l;
       if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (x_t - mo.m) - ll;
     }
-    if (tid < k) {
-      const uint64_t key = sh.top[tid];
-      a.top_idx[row * k + tid] = token_of(key);
-      a.top_logp[row * k + tid] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
+    for (int i = lane; i < k; i += 32) {
+      const uint64_t key = sh.top[i];
+      a.top_idx[row * k + i] = token_of(key);
+      a.top_logp[row * k + i] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
     }
   }
   // copies still in flight (after a wait that gave up) land before the CTA ends
