@@ -25,30 +25,29 @@ constexpr float kLog2e = 1.4426950408889634f;
 // (x - m); then lse = m + ln l and the entropy is ln l - u / l, whose terms all have one
 // sign. A bf16 logit costs 5 instructions (4 without the entropy), half of the issue
 // slots at the full memory rate: the kernel is bound by memory, and laid out to keep
-// reading. A CTA works rows off one after the other through a ring of 16 KB chunks that bulk
-// copies fill, three ahead and across row ends, so the ends of a row (reductions, the
-// alternatives) do not stop the memory. Few rows are split over the CTAs of a cluster, which
-// join through distributed shared memory.
+// reading. A CTA works rows off one after the other: a producer warp keeps bulk copies into a
+// ring of 16 KB chunks going, across row ends, and eight warps consume them, each at its own
+// pace but for the first chunk and the end of a row. Few rows are split over the CTAs of a
+// cluster, which join through distributed shared memory.
 //
 // The alternatives. Logits are ranked by 64-bit keys, the value's order above the inverted
-// token number: keys are distinct, so ties need no care. A row's candidates are the logits
-// above a threshold, the k-th best of the chunks before (a later logit that equals it loses
-// the tie). Where many threads of a chunk are above it (in the first chunk all are), the
-// chunk gets a threshold of its own, the k-th largest of the maxima of groups of threads: k
-// logits are at least that large, and hardly any besides. Should ties let more threads in
-// than the buffer has room for, the groups' best keys take the place of their maxima: then
-// only k groups can hold any. So the buffer cannot overflow, whatever the logits' order. A
-// warp looks at one thread's logits of a chunk at a time, a lane each; candidates are ranked
-// by counting the larger ones.
+// token number: keys are distinct, so ties need no care. The k-th largest of the maxima of
+// groups of threads in a row's first chunk is a bound: k logits are at least that large, and
+// few are. The row's candidates are the first chunk's logits at or above it and the later
+// ones above it (one that equals it loses the tie to those k); a warp looks at one thread's
+// logits of a chunk at a time, a lane each. At the row's end they are ranked by counting the
+// larger ones. Should there be more than the buffer holds (rising or constant rows), the row
+// is read once more for every alternative; a row with fewer than k tokens above -infinity is
+// filled up from its first tokens.
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 256;    // consumers; one more warp produces
 constexpr int kChunk = 16384;      // bytes
 constexpr int kLpStages = 3;
 constexpr int kVecs = kChunk / 16 / kLpThreads;   // vectors a thread takes of a chunk
-constexpr int kKeep = 512;         // candidates a chunk may start with
+constexpr int kMaxCandidates = 2560;   // 20 KB: three CTAs an SM with the ring
 
 struct LogprobArgs {
-  int V, top_k, splits;
+  int V, top_k, splits, per, capacity;   // per: logits of a split; capacity: candidates
   int64_t N, ld;
   const void* logits;
   const int32_t* target;
@@ -145,9 +144,8 @@ template <typename T>
 __device__ __forceinline__ Span span_of(const LogprobArgs& a, int64_t row, int split) {
   constexpr int VE = 16 / sizeof(T);
   Span s;
-  const int per = (a.V + a.splits - 1) / a.splits;
-  s.token0 = min(a.V, split * per);
-  s.count = min(a.V, s.token0 + per) - s.token0;
+  s.token0 = min(a.V, split * a.per);
+  s.count = min(a.V, s.token0 + a.per) - s.token0;
   const uintptr_t at = (uintptr_t)((const T*)a.logits + row * a.ld + s.token0);
   s.head = (int)(at & 15) / (int)sizeof(T);
   s.vecs = (const uint4*)(at & ~(uintptr_t)15);
@@ -161,31 +159,27 @@ __device__ __forceinline__ int span_chunks(const Span& s) {
 
 // Shared memory behind the ring.
 struct LpShared {
-  uint64_t full[kLpStages];
-  uint64_t best;            // the chunk's own threshold
-  uint32_t least;           // and in values
+  uint64_t full[kLpStages], empty[kLpStages];
+  uint32_t least;           // the row's bound, in orders
   int count, abort;
-  alignas(16) uint64_t group[kLpThreads];
-  alignas(16) uint32_t group_max[kLpThreads];
-  Moments moments[kLpThreads / 32];
+  Moments moments[2][kLpThreads / 32];   // of even and odd rows: a warp may be a row ahead
   Moments total;
-  uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
+  alignas(16) uint32_t group_max[kLpThreads];
+  alignas(16) uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
 };
 
-// Threads whose maxima stand together for the chunk's own threshold: at least 4 top_k groups
-// (a looser threshold lets more candidates in, more groups cost more to rank).
-__host__ __device__ constexpr int lp_group(int top_k) {
-  return top_k <= 16 ? 4 : top_k <= 32 ? 2 : 1;
-}
-// Candidate keys the buffer holds: those kept, and those of a chunk, which come from at
-// most top_k groups (or 16 threads) of at most `per_thread` logits a thread.
-__host__ __device__ constexpr int lp_capacity(int top_k, int per_thread) {
-  const int threads = top_k * lp_group(top_k) > 16 ? top_k * lp_group(top_k) : 16;
-  return top_k == 0 ? 0 : kKeep + threads * per_thread;
+// Threads whose maxima stand together for the bound: at least 4 top_k groups (fewer give a
+// looser bound, more cost more to rank).
+__device__ __forceinline__ int lp_group(int top_k) { return top_k <= 16 ? 4 : top_k <= 32 ? 2 : 1; }
+
+constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-infinity)
+
+__device__ __forceinline__ void sync_consumers() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLpThreads) : "memory");
 }
 
 template <typename T, bool ENT>
-__global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(const LogprobArgs a) {
   constexpr int VE = 16 / sizeof(T);
   extern __shared__ __align__(128) uint8_t smem[];
   LpShared& sh = *reinterpret_cast<LpShared*>(smem + kLpStages * kChunk);
@@ -195,45 +189,56 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
   const int64_t row0 = blockIdx.x / a.splits, row_step = gridDim.x / a.splits;
   const int k = a.top_k;
   volatile int* abort_flag = &sh.abort;
+  const uint32_t bFull = smem_u32(&sh.full[0]), bEmpty = smem_u32(&sh.empty[0]);
 
   pdl_trigger();
   if (tid == 0) {
-    for (int i = 0; i < kLpStages; ++i) mbar_init(smem_u32(&sh.full[i]), 1);
+    for (int i = 0; i < kLpStages; ++i) {
+      mbar_init(bFull + 8 * i, 1);
+      mbar_init(bEmpty + 8 * i, kLpThreads / 32);
+    }
     sh.abort = 0;
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait();
 
-  // the copies' place in the rows (thread 0), `kLpStages` chunks ahead of the reading
-  int64_t issue_row = row0;
-  int issue_chunk = 0, issue_stage = 0;
-  uint32_t issued = 0;
-  auto issue = [&]() {
-    while (issue_row < a.N) {
-      const Span s = span_of<T>(a, issue_row, split);
-      if (issue_chunk >= span_chunks(s)) {
-        issue_chunk = 0;
-        issue_row += row_step;
-        continue;
+  if (warp == kLpThreads / 32) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t row = row0; ok && row < a.N; row += row_step) {
+        const Span s = span_of<T>(a, row, split);
+        const int chunks = span_chunks(s);
+        for (int c = 0; c < chunks; ++c, ++n) {
+          const uint32_t st = n % kLpStages, use = n / kLpStages;
+          if (use && !(ok = mbar_wait(bEmpty + 8 * st, (use - 1) & 1, abort_flag, a.status))) break;
+          const int v0 = c * (kChunk / 16);
+          const int bytes = max(0, min(kChunk / 16, s.full - v0)) * 16;
+          mbar_arrive_expect_tx(bFull + 8 * st, bytes);
+          if (bytes) bulk_load(smem_u32(smem) + st * kChunk, s.vecs + v0, bytes, bFull + 8 * st);
+        }
       }
-      const int v0 = issue_chunk * (kChunk / 16);
-      const int bytes = max(0, min(kChunk / 16, s.full - v0)) * 16;
-      const uint32_t bar = smem_u32(&sh.full[issue_stage]);
-      mbar_arrive_expect_tx(bar, bytes);
-      if (bytes) bulk_load(smem_u32(smem) + issue_stage * kChunk, s.vecs + v0, bytes, bar);
-      issue_stage = issue_stage == kLpStages - 1 ? 0 : issue_stage + 1;
-      ++issue_chunk;
-      ++issued;
-      return;
+      // the copies still in flight land before the CTA can end
+      for (uint32_t j = n > kLpStages ? n - kLpStages : 0; j < n; ++j)
+        mbar_wait(bFull + 8 * (j % kLpStages), (j / kLpStages) & 1, nullptr, a.status);
     }
-  };
-  if (tid == 0)
-    for (int i = 0; i < kLpStages; ++i) issue();
+    __syncwarp();
+    if (a.splits > 1) {   // the consumers' two, for the cluster's one row
+      cluster_sync_all();
+      cluster_sync_all();
+    }
+    return;
+  }
 
+  // -------------------------------------------------------------- consumers
+  // A wait that gives up (abort) lets the loops run on over what the ring holds: every warp
+  // still meets the others' barriers.
   int stage = 0;
   uint32_t phase = 0;
-  for (int64_t row = row0; row < a.N; row += row_step) {
+  int parity = 0;
+  for (int64_t row = row0; row < a.N; row += row_step, parity ^= 1) {
     const Span s = span_of<T>(a, row, split);
     const int chunks = span_chunks(s);
     float x_t = 0.f;   // the target's logit, on its way while the row is read
@@ -242,37 +247,19 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
       target = a.target[row];
       if (target >= 0 && target < a.V) x_t = Elem<T>::to_f(((const T*)a.logits + row * a.ld)[target]);
     }
-    // ranks the candidates: the k best to sh.top in order, and (compact) back to the buffer
-    auto rank = [&](int count, bool compact) {
-      for (int i = tid; i < count; i += kLpThreads) {
-        const uint64_t mine = cand[i];
-        int above = 0;
-#pragma unroll 4
-        for (int j = 0; j < count; ++j) above += cand[j] > mine;
-        if (above < k) sh.top[above] = mine;
-      }
-      __syncthreads();
-      if (compact) {
-        const int kept = min(count, k);
-        if (tid < kept) cand[tid] = sh.top[tid];
-        if (tid == 0) sh.count = kept;
-        __syncthreads();
-      }
-    };
     Moments mo{-FLT_MAX, 0.f, 0.f};
     float2 l2 = make_float2(0.f, 0.f), u2 = l2;
-    float thr = -INFINITY;   // candidates are above it
-    bool has_thr = false;
-    int bound = 0;           // at most this many candidates are in the buffer
-    if (k && tid == 0) sh.count = 0;
+    uint32_t limit = kOrderNone;   // candidates are above it
+    float thr = -INFINITY;         // the same as a value
     for (int c = 0; c < chunks; ++c) {
-      mbar_wait(smem_u32(&sh.full[stage]), phase, abort_flag, a.status);
+      mbar_wait(bFull + 8 * stage, phase, abort_flag, a.status);
       const uint4* buf = reinterpret_cast<const uint4*>(smem + stage * kChunk);
       const int v0 = c * (kChunk / 16);
       uint4 x[kVecs];
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) x[i] = buf[tid + i * kLpThreads];
-      if (c == 0 || v0 + kChunk / 16 > s.full) {   // the row's ends
+      const bool whole = c > 0 && v0 + kChunk / 16 <= s.full;
+      if (!whole) {   // the row's ends
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
           const int v = v0 + tid + i * kLpThreads;
@@ -308,6 +295,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
         const float2 neg = make_float2(-mo.m, -mo.m), lg = make_float2(kLog2e, kLog2e);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
+          if (!whole && v0 + warp * 32 + i * kLpThreads >= s.nvec) break;   // nothing left
           // an infinite exponent times 0 would be a NaN: such logits become low finite ones,
           // whose terms are 0 as well
           if (ENT) vec_finite<T>(x[i]);
@@ -320,7 +308,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
             if (ENT) u2 = fma2(e, t, u2);
           }
         }
-      } else {   // nothing above -infinity yet, or differences that could overflow
+      } else if (mo.m > -FLT_MAX) {   // differences that could overflow
 #pragma unroll
         for (int i = 0; i < kVecs * VE; ++i) {
           const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
@@ -328,30 +316,18 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
           if (ENT) u2.x = fmaf(e, d, u2.x);
         }
       }
-      const bool above = k && (has_thr ? !(top <= thr) : v0 + tid < s.nvec);
-      const int active = __syncthreads_count(above);   // also: the stage is read
-      if (active) {
-        // element j of vector v: still in the chunk, but for a row's last vector
-        auto logit = [&](int v, int j) {
-          return v < s.full ? Elem<T>::to_f(reinterpret_cast<const T*>(buf + (v - v0))[j])
-                            : Elem<T>::to_f(reinterpret_cast<const T*>(s.vecs + v)[j]);
-        };
-        auto candidate = [&](int v, int j, float& f) {
-          const int e = v * VE + j - s.head;
-          if (e < 0 || e >= s.count) return false;
-          f = logit(v, j);
-          return !(has_thr && f <= thr);
-        };
-        const int lanes = lp_group(k), groups = kLpThreads / lanes, most = max(16, k * lanes);
-        uint32_t least = 0;   // the chunk's own threshold: in values,
-        uint64_t own = 0;     // and in keys
-        if (active > 16) {
-          const uint32_t mine = above ? order_of(top) : 0u;
-          uint32_t best = mine;
+      if (k) {
+        const bool live = v0 + tid < s.nvec;
+        if (c == 0) {   // the row's bound
+          const int lanes = lp_group(k), groups = kLpThreads / lanes;
+          uint32_t best = live ? order_of(top) : 0u;
           for (int o = 1; o < lanes; o <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
           if (tid % lanes == 0) sh.group_max[tid / lanes] = best;
-          if (tid == 0) sh.least = 0;
-          __syncthreads();
+          if (tid == 0) {
+            sh.least = 0;
+            sh.count = 0;
+          }
+          sync_consumers();
           if (tid < groups) {
             const uint32_t g = sh.group_max[tid];
             int gt = 0, ge = 0;
@@ -363,62 +339,36 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
             }
             if (g && gt < k && ge >= k) sh.least = g;   // one value, whoever writes it
           }
-          __syncthreads();
-          least = sh.least;   // 0 where fewer than k groups hold candidates
-          if (__syncthreads_count(mine && mine >= least) > most) {   // ties: by whole keys
-            unsigned long long key = 0;
-            if (mine && mine >= least) {
-#pragma unroll 1
-              for (int i = 0; i < kVecs * VE; ++i) {
-                const int v = v0 + tid + i / VE * kLpThreads;
-                float f;
-                if (candidate(v, i % VE, f))
-                  key = max(key, (unsigned long long)key_of(f, s.token0 + v * VE + i % VE - s.head));
-              }
-            }
-            for (int o = 1; o < lanes; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-            if (tid % lanes == 0) sh.group[tid / lanes] = key;
-            if (tid == 0) sh.best = 0;
-            __syncthreads();
-            if (tid < groups) {
-              const uint64_t g = sh.group[tid];
-              int gt = 0;
-              for (int j = 0; j < groups; ++j) gt += sh.group[j] > g;
-              if (g && gt == k - 1) sh.best = g;
-            }
-            __syncthreads();
-            own = sh.best;
-          }
+          sync_consumers();
+          const uint32_t least = sh.least;   // 0 where fewer than k groups have logits
+          limit = max(least, kOrderNone + 1) - 1;
         }
-        uint32_t todo = __ballot_sync(0xffffffffu, above && order_of(top) >= least);
+        uint32_t todo = __ballot_sync(0xffffffffu, live && (c ? !(top <= thr) : order_of(top) > limit));
         while (todo) {   // a thread's logits of the chunk, one a lane
           const int from = __ffs(todo) - 1;
           todo &= todo - 1;
-          const int v = v0 + warp * 32 + from + lane / VE * kLpThreads;
-          float f = 0.f;
+          const int v = v0 + warp * 32 + from + lane / VE * kLpThreads, j = lane % VE;
+          const int e = v * VE + j - s.head;
           uint64_t key = 0;
-          if (lane < kVecs * VE && candidate(v, lane % VE, f))
-            key = key_of(f, s.token0 + v * VE + lane % VE - s.head);
-          const bool in = key && (uint32_t)(key >> 32) >= least && key >= own;
+          if (lane < kVecs * VE && e >= 0 && e < s.count) {
+            const T* at = v < s.full ? reinterpret_cast<const T*>(buf + (v - v0))
+                                     : reinterpret_cast<const T*>(s.vecs + v);
+            key = key_of(Elem<T>::to_f(at[j]), s.token0 + e);
+          }
+          const bool in = (uint32_t)(key >> 32) > limit;
           const uint32_t who = __ballot_sync(0xffffffffu, in);
           int at = 0;
           if (lane == 0 && who) at = atomicAdd(&sh.count, __popc(who));
           at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
-          if (in) cand[at] = key;
+          if (in && at < a.capacity) cand[at] = key;
         }
-        bound += min(active, most) * kVecs * VE;
-        __syncthreads();   // the stage is read, the candidates are there
-        if (!has_thr || bound > kKeep) {
-          bound = sh.count;
-          if (bound >= k && (!has_thr || bound > kKeep / 2)) {
-            rank(bound, true);
-            thr = value_of((uint32_t)(cand[k - 1] >> 32));
-            has_thr = true;
-            bound = k;
-          }
+        if (c == 0) {   // from here on a logit equal to the bound loses to the k that reach it
+          limit = max(sh.least, kOrderNone);
+          thr = value_of(limit);
         }
       }
-      if (tid == 0 && !*abort_flag) issue();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bEmpty + 8 * stage);
       if (++stage == kLpStages) {
         stage = 0;
         phase ^= 1;
@@ -430,18 +380,57 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
     mo.raise(warp_max(mo.m));
     mo.l = warp_sum(mo.l);
     if (ENT) mo.u = warp_sum(mo.u);
-    if (lane == 0) sh.moments[warp] = mo;
-    __syncthreads();
+    if (lane == 0) sh.moments[parity][warp] = mo;
+    sync_consumers();
     int found = 0;
+    // the k best of the candidates to sh.top, in order
+    auto rank = [&](int count) {
+      for (int i = tid; i < count; i += kLpThreads) {
+        const uint64_t mine = cand[i];
+        int above = 0;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) above += cand[j] > mine;
+        if (above < k) sh.top[above] = mine;
+      }
+      sync_consumers();
+    };
     if (k) {
       found = sh.count;
-      rank(found, false);
-      found = min(found, k);
+      if (found < k) {
+        // the rest are tokens at -infinity: the lowest, among the first 2 k
+        sync_consumers();
+        const T* p = (const T*)a.logits + row * a.ld + s.token0;
+        if (tid < min(2 * k, s.count) && order_of(Elem<T>::to_f(p[tid])) == kOrderNone)
+          cand[atomicAdd(&sh.count, 1)] = key_of(-INFINITY, s.token0 + tid);
+        sync_consumers();
+        found = sh.count;
+      }
+      if (found <= a.capacity) {
+        rank(found);
+      } else {   // too many: one reading for each alternative, the largest key below the last
+        const T* p = (const T*)a.logits + row * a.ld + s.token0;
+        uint64_t last = ~0ull;
+        for (int i = 0; i < min(k, s.count); ++i) {
+          unsigned long long best = 0;
+          for (int e = tid; e < s.count; e += kLpThreads) {
+            const uint64_t key = key_of(Elem<T>::to_f(p[e]), s.token0 + e);
+            if (key < last && key > best) best = key;
+          }
+          for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+          if (lane == 0) cand[warp] = best;
+          sync_consumers();
+          for (int w = 0; w < kLpThreads / 32; ++w) best = max(best, (unsigned long long)cand[w]);
+          last = best;
+          if (tid == 0) sh.top[i] = best;
+          sync_consumers();
+        }
+      }
+      found = min(found, min(k, s.count));
     }
-    // the first warp finishes the row; the others meet it again at the next row's first
-    // barrier, before anything that it reads here is written
+    // the first warp finishes the row; the others meet it again at the next row's barriers,
+    // before anything that it reads here is written
     if (a.splits == 1 && warp != 0) continue;
-    mo = sh.moments[lane % (kLpThreads / 32)];
+    mo = sh.moments[parity][lane % (kLpThreads / 32)];
     mo.raise(warp_max(mo.m));
     if (lane >= kLpThreads / 32) mo.l = mo.u = 0.f;
     mo.l = warp_sum(mo.l);
@@ -483,8 +472,8 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
             all += n;
           }
         }
-        __syncthreads();
-        if (k) rank(all, false);
+        sync_consumers();
+        if (k) rank(all);
       }
       cluster_sync_all();   // the other CTAs' shared memory has been read
       if (split != 0 || warp != 0) continue;
@@ -503,10 +492,6 @@ __global__ void __launch_bounds__(kLpThreads, 3) token_logprobs_kernel(const Log
       a.top_logp[row * k + i] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
     }
   }
-  // copies still in flight (after a wait that gave up) land before the CTA ends
-  if (tid == 0)
-    for (uint32_t j = issued > kLpStages ? issued - kLpStages : 0; j < issued; ++j)
-      mbar_wait(smem_u32(&sh.full[j % kLpStages]), (j / kLpStages) & 1, nullptr, a.status);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -609,17 +594,20 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
   a.splits = 1;
   while (a.splits < 8 && a.N * a.splits * 2 <= sms && (int64_t)a.V * sizeof(T) >= 2 * a.splits * (int64_t)kChunk)
     a.splits *= 2;
-  const int smem = kLpStages * kChunk + (int)sizeof(LpShared) +
-                   8 * lp_capacity(a.top_k, kVecs * 16 / (int)sizeof(T));
+  a.per = (a.V + a.splits - 1) / a.splits;
+  // about top_k logits of every chunk's size are above a bound from one chunk
+  const int64_t want = 1024 + 2 * (int64_t)a.top_k * ((int64_t)a.per * sizeof(T) / kChunk + 1);
+  a.capacity = a.top_k ? (int)(want < kMaxCandidates ? want : kMaxCandidates) : 0;
+  const int smem = kLpStages * kChunk + (int)sizeof(LpShared) + 8 * a.capacity;
   auto kernel = token_logprobs_kernel<T, ENT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kernel, kLpStages * kChunk + (int)sizeof(LpShared) +
-                                         8 * lp_capacity(XMOD_MAX_TOP_K, kVecs * 8), done);
+  cudaError_t e = allow_smem(kernel, kLpStages * kChunk + (int)sizeof(LpShared) + 8 * kMaxCandidates,
+                             done);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)sms * 3;   // resident: by registers, and by shared memory
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.splits > 1 ? a.N * a.splits : a.N < most ? a.N : most));
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(kLpThreads + 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[2];
@@ -667,7 +655,7 @@ int xmod_token_logprobs(xmod_dtype dt, int64_t N, int V, const void* logits, int
   for (const void* p : ps)
     if (!ptr4_or_null(p)) return XMOD_ERR_INVALID_ARG;
   if (top_k > XMOD_MAX_TOP_K || N > INT32_MAX || V > INT32_MAX - 65536) return XMOD_ERR_UNSUPPORTED;
-  const LogprobArgs a{V, top_k, 1, N, ld, logits, target, logp, entropy, lse, top_idx, top_logp,
+  const LogprobArgs a{V, top_k, 1, V, 0, N, ld, logits, target, logp, entropy, lse, top_idx, top_logp,
                       status_out};
   const Ctx c{(cudaStream_t)stream, status_out};
   if (dt == XMOD_BF16)
