@@ -44,7 +44,7 @@ constexpr int kLpThreads = 256;    // consumers; one more warp produces
 constexpr int kChunk = 16384;      // bytes
 constexpr int kLpStages = 3;
 constexpr int kVecs = kChunk / 16 / kLpThreads;   // vectors a thread takes of a chunk
-constexpr int kMaxCandidates = 2560;   // 20 KB: three CTAs an SM with the ring
+constexpr int kMaxCandidates = 1296;   // 2 x 10 KB: three CTAs an SM with the ring
 
 struct LogprobArgs {
   int V, top_k, splits, per, capacity;   // per: logits of a split; capacity: candidates
@@ -158,10 +158,11 @@ __device__ __forceinline__ int span_chunks(const Span& s) {
 }
 
 // Shared memory behind the ring.
-struct LpShared {
+struct alignas(16) LpShared {
   uint64_t full[kLpStages], empty[kLpStages];
   uint32_t least;           // the row's bound, in orders
-  int count, abort;
+  int found, abort;
+  int counts[kLpThreads / 32 + 1];   // candidates of the warps, and those filled up
   Moments moments[2][kLpThreads / 32];   // of even and odd rows: a warp may be a row ahead
   Moments total;
   alignas(16) uint32_t group_max[kLpThreads];
@@ -170,7 +171,9 @@ struct LpShared {
 
 // Threads whose maxima stand together for the bound: at least 4 top_k groups (fewer give a
 // looser bound, more cost more to rank).
-__device__ __forceinline__ int lp_group(int top_k) { return top_k <= 16 ? 4 : top_k <= 32 ? 2 : 1; }
+__device__ __forceinline__ int lp_group(int top_k) {
+  return top_k <= 8 ? 8 : top_k <= 16 ? 4 : top_k <= 32 ? 2 : 1;
+}
 
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-infinity)
 
@@ -183,11 +186,12 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
   constexpr int VE = 16 / sizeof(T);
   extern __shared__ __align__(128) uint8_t smem[];
   LpShared& sh = *reinterpret_cast<LpShared*>(smem + kLpStages * kChunk);
-  uint64_t* cand = reinterpret_cast<uint64_t*>(&sh + 1);
+  uint64_t* cand = reinterpret_cast<uint64_t*>(&sh + 1);   // the warps' lists, the filled up
+  uint64_t* joined = cand + a.capacity;                    // and all together
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = a.splits > 1 ? (int)cluster_ctarank() : 0;
   const int64_t row0 = blockIdx.x / a.splits, row_step = gridDim.x / a.splits;
-  const int k = a.top_k;
+  const int k = a.top_k, capw = a.capacity / (kLpThreads / 32 + 1);   // candidates of a warp
   volatile int* abort_flag = &sh.abort;
   const uint32_t bFull = smem_u32(&sh.full[0]), bEmpty = smem_u32(&sh.empty[0]);
 
@@ -238,19 +242,25 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
   int stage = 0;
   uint32_t phase = 0;
   int parity = 0;
+  const bool has_target = split == 0 && tid == 0 && a.logp;
+  int next_target = has_target && row0 < a.N ? a.target[row0] : -1;
   for (int64_t row = row0; row < a.N; row += row_step, parity ^= 1) {
     const Span s = span_of<T>(a, row, split);
     const int chunks = span_chunks(s);
-    float x_t = 0.f;   // the target's logit, on its way while the row is read
-    int target = -1;
-    if (split == 0 && tid == 0 && a.logp) {
-      target = a.target[row];
-      if (target >= 0 && target < a.V) x_t = Elem<T>::to_f(((const T*)a.logits + row * a.ld)[target]);
-    }
+    // the target's logit, on its way while the row is read; the next row's target too
+    float x_t = 0.f;
+    const int target = next_target;
+    if (target >= 0 && target < a.V) x_t = Elem<T>::to_f(((const T*)a.logits + row * a.ld)[target]);
+    if (has_target && row + row_step < a.N) next_target = a.target[row + row_step];
+    int mine_n = 0;   // this warp's candidates
     Moments mo{-FLT_MAX, 0.f, 0.f};
     float2 l2 = make_float2(0.f, 0.f), u2 = l2;
-    uint32_t limit = kOrderNone;   // candidates are above it
-    float thr = -INFINITY;         // the same as a value
+    uint32_t bound = kOrderNone;
+    float thr = -INFINITY;   // candidates are above it
+    const int lane_vec = lane / VE * kLpThreads;   // from a thread's first vector to the lane's
+    auto tail_index = [&](int v) {   // the lane's element of vector v, the row's last at most
+      return min(v * VE + lane % VE, s.head + s.count - 1);
+    };
     for (int c = 0; c < chunks; ++c) {
       mbar_wait(bFull + 8 * stage, phase, abort_flag, a.status);
       const uint4* buf = reinterpret_cast<const uint4*>(smem + stage * kChunk);
@@ -317,19 +327,16 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
         }
       }
       if (k) {
-        const bool live = v0 + tid < s.nvec;
         if (c == 0) {   // the row's bound
           const int lanes = lp_group(k), groups = kLpThreads / lanes;
-          uint32_t best = live ? order_of(top) : 0u;
+          uint32_t best = tid < s.nvec ? order_of(top) : 0u;
           for (int o = 1; o < lanes; o <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
           if (tid % lanes == 0) sh.group_max[tid / lanes] = best;
-          if (tid == 0) {
-            sh.least = 0;
-            sh.count = 0;
-          }
+          if (tid == 0) sh.least = 0;
           sync_consumers();
-          if (tid < groups) {
-            const uint32_t g = sh.group_max[tid];
+          uint32_t g = 0;
+          if (groups == 32 || tid < groups) {   // 32 groups: every warp for itself
+            g = sh.group_max[groups == 32 ? lane : tid];
             int gt = 0, ge = 0;
 #pragma unroll 4
             for (int j = 0; j < groups; j += 4) {
@@ -337,35 +344,40 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
               gt += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
               ge += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
             }
-            if (g && gt < k && ge >= k) sh.least = g;   // one value, whoever writes it
+            if (gt >= k || ge < k) g = 0;
           }
-          sync_consumers();
-          const uint32_t least = sh.least;   // 0 where fewer than k groups have logits
-          limit = max(least, kOrderNone + 1) - 1;
+          if (groups == 32) {
+            g = __reduce_max_sync(0xffffffffu, g);
+          } else {
+            if (g) sh.least = g;   // one value, whoever writes it
+            sync_consumers();
+            g = sh.least;
+          }
+          // later logits have to be above the bound (one equal to it loses to the k that reach
+          // it), this chunk's at it; none at -infinity is in. g 0: fewer than k groups hold any
+          bound = max(g, kOrderNone);
+          const uint32_t below = bound - (bound == 0x80000000u ? 2 : 1);   // 0: -0 equals it
+          thr = value_of(max(below, kOrderNone));
         }
-        uint32_t todo = __ballot_sync(0xffffffffu, live && (c ? !(top <= thr) : order_of(top) > limit));
+        uint32_t todo = __ballot_sync(0xffffffffu, !(top <= thr));
         while (todo) {   // a thread's logits of the chunk, one a lane
-          const int from = __ffs(todo) - 1;
+          const int from = warp * 32 + __ffs(todo) - 1;
           todo &= todo - 1;
-          const int v = v0 + warp * 32 + from + lane / VE * kLpThreads, j = lane % VE;
-          const int e = v * VE + j - s.head;
-          uint64_t key = 0;
-          if (lane < kVecs * VE && e >= 0 && e < s.count) {
-            const T* at = v < s.full ? reinterpret_cast<const T*>(buf + (v - v0))
-                                     : reinterpret_cast<const T*>(s.vecs + v);
-            key = key_of(Elem<T>::to_f(at[j]), s.token0 + e);
+          float f = -INFINITY;
+          if (lane < kVecs * VE) {
+            if (whole || v0 + from + lane_vec < s.full)
+              f = Elem<T>::to_f(reinterpret_cast<const T*>(buf + from)[lane_vec * VE + lane % VE]);
+            else if (v0 + from + lane_vec < s.nvec)
+              f = Elem<T>::to_f(reinterpret_cast<const T*>(s.vecs)[tail_index(v0 + from + lane_vec)]);
           }
-          const bool in = (uint32_t)(key >> 32) > limit;
+          const int e = (v0 + from + lane_vec) * VE + lane % VE - s.head;
+          const bool in = !(f <= thr) && (whole || (e >= 0 && e < s.count));
           const uint32_t who = __ballot_sync(0xffffffffu, in);
-          int at = 0;
-          if (lane == 0 && who) at = atomicAdd(&sh.count, __popc(who));
-          at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
-          if (in && at < a.capacity) cand[at] = key;
+          const int at = mine_n + __popc(who & ((1u << lane) - 1u));
+          mine_n += __popc(who);
+          if (in && at < capw) cand[warp * capw + at] = key_of(f, s.token0 + e);
         }
-        if (c == 0) {   // from here on a logit equal to the bound loses to the k that reach it
-          limit = max(sh.least, kOrderNone);
-          thr = value_of(limit);
-        }
+        if (c == 0) thr = value_of(bound);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bEmpty + 8 * stage);
@@ -380,35 +392,53 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
     mo.raise(warp_max(mo.m));
     mo.l = warp_sum(mo.l);
     if (ENT) mo.u = warp_sum(mo.u);
-    if (lane == 0) sh.moments[parity][warp] = mo;
+    if (lane == 0) {
+      sh.moments[parity][warp] = mo;
+      sh.counts[warp] = mine_n;
+      if (warp == 0) sh.counts[kLpThreads / 32] = 0;
+    }
     sync_consumers();
-    int found = 0;
-    // the k best of the candidates to sh.top, in order
-    auto rank = [&](int count) {
+    // the k best of `count` candidates to sh.top, in order: those in the lists of counts[],
+    // `stride` apart, are put together and ranked by counting the larger ones
+    auto rank = [&](int lists, int stride, int count) {
       for (int i = tid; i < count; i += kLpThreads) {
-        const uint64_t mine = cand[i];
+        int list = 0, j = i;
+        while (j >= sh.counts[list]) j -= sh.counts[list++];
+        joined[i] = cand[list * stride + j];
+      }
+      if (tid == 0) joined[count] = 0;   // pairs below
+      sync_consumers();
+      for (int i = tid; i < count; i += kLpThreads) {
+        const uint64_t mine = joined[i];
         int above = 0;
 #pragma unroll 4
-        for (int j = 0; j < count; ++j) above += cand[j] > mine;
+        for (int j = 0; j < count; j += 2) {
+          const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&joined[j]);
+          above += (o.x > mine) + (o.y > mine);
+        }
         if (above < k) sh.top[above] = mine;
       }
       sync_consumers();
     };
+    int found = 0;
     if (k) {
-      found = sh.count;
+      constexpr int W = kLpThreads / 32;
+      bool full = false;
+      for (int w = 0; w < W; ++w) {
+        found += sh.counts[w];
+        full |= sh.counts[w] > capw;
+      }
+      const T* p = (const T*)a.logits + row * a.ld + s.token0;
       if (found < k) {
         // the rest are tokens at -infinity: the lowest, among the first 2 k
-        sync_consumers();
-        const T* p = (const T*)a.logits + row * a.ld + s.token0;
         if (tid < min(2 * k, s.count) && order_of(Elem<T>::to_f(p[tid])) == kOrderNone)
-          cand[atomicAdd(&sh.count, 1)] = key_of(-INFINITY, s.token0 + tid);
+          cand[W * capw + atomicAdd(&sh.counts[W], 1)] = key_of(-INFINITY, s.token0 + tid);
         sync_consumers();
-        found = sh.count;
+        found += sh.counts[W];
       }
-      if (found <= a.capacity) {
-        rank(found);
+      if (!full) {
+        rank(W + 1, capw, found);
       } else {   // too many: one reading for each alternative, the largest key below the last
-        const T* p = (const T*)a.logits + row * a.ld + s.token0;
         uint64_t last = ~0ull;
         for (int i = 0; i < min(k, s.count); ++i) {
           unsigned long long best = 0;
@@ -419,7 +449,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
           for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
           if (lane == 0) cand[warp] = best;
           sync_consumers();
-          for (int w = 0; w < kLpThreads / 32; ++w) best = max(best, (unsigned long long)cand[w]);
+          for (int w = 0; w < W; ++w) best = max(best, (unsigned long long)cand[w]);
           last = best;
           if (tid == 0) sh.top[i] = best;
           sync_consumers();
@@ -438,7 +468,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
     if (a.splits > 1) {
       if (tid == 0) {
         sh.total = mo;
-        sh.count = found;
+        sh.found = found;
       }
       cluster_sync_all();
       if (split == 0) {
@@ -462,18 +492,19 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
             int n;
             asm volatile("ld.shared::cluster.s32 %0, [%1];"
                          : "=r"(n)
-                         : "r"(mapa_shared(smem_u32(&sh.count), r))
+                         : "r"(mapa_shared(smem_u32(&sh.found), r))
                          : "memory");
             if (tid < n)
               asm volatile("ld.shared::cluster.u64 %0, [%1];"
-                           : "=l"(cand[all + tid])
+                           : "=l"(cand[r * XMOD_MAX_TOP_K + tid])
                            : "r"(mapa_shared(smem_u32(&sh.top[0]), r) + 8 * tid)
                            : "memory");
+            if (tid == 0) sh.counts[r] = n;
             all += n;
           }
         }
         sync_consumers();
-        if (k) rank(all);
+        if (k) rank(a.splits, XMOD_MAX_TOP_K, all);
       }
       cluster_sync_all();   // the other CTAs' shared memory has been read
       if (split != 0 || warp != 0) continue;
@@ -596,13 +627,15 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
     a.splits *= 2;
   a.per = (a.V + a.splits - 1) / a.splits;
   // about top_k logits of every chunk's size are above a bound from one chunk
-  const int64_t want = 1024 + 2 * (int64_t)a.top_k * ((int64_t)a.per * sizeof(T) / kChunk + 1);
-  a.capacity = a.top_k ? (int)(want < kMaxCandidates ? want : kMaxCandidates) : 0;
-  const int smem = kLpStages * kChunk + (int)sizeof(LpShared) + 8 * a.capacity;
+  const int64_t want = 2 * (int64_t)a.top_k * ((int64_t)a.per * sizeof(T) / kChunk + 1);
+  const int lists = kLpThreads / 32 + 1;   // of at least 128: a list may fill up 2 top_k
+  a.capacity = !a.top_k ? 0 : want < 128 * lists ? 128 * lists : want < kMaxCandidates ? (int)want / lists * lists : kMaxCandidates;
+  a.capacity += a.capacity & 1;
+  const int smem = kLpStages * kChunk + (int)sizeof(LpShared) + 16 * a.capacity + 16;
   auto kernel = token_logprobs_kernel<T, ENT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kernel, kLpStages * kChunk + (int)sizeof(LpShared) + 8 * kMaxCandidates,
-                             done);
+  cudaError_t e = allow_smem(kernel, kLpStages * kChunk + (int)sizeof(LpShared) +
+                                         16 * kMaxCandidates + 16, done);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)sms * 3;   // resident: by registers, and by shared memory
   cudaLaunchConfig_t cfg = {};
