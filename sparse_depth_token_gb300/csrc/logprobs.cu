@@ -25,29 +25,33 @@ constexpr float kLog2e = 1.4426950408889634f;
 // (x - m); then lse = m + ln l and the entropy is ln l - u / l, whose terms all have one
 // sign. A bf16 logit costs 5 instructions (4 without the entropy), half of the issue
 // slots at the full memory rate: the kernel is bound by memory, and laid out to keep
-// reading. A CTA works rows off one after the other: a producer warp keeps bulk copies into a
-// ring of 16 KB chunks going, across row ends, and eight warps consume them, each at its own
-// pace but for the first chunk and the end of a row. Few rows are split over the CTAs of a
-// cluster, which join through distributed shared memory.
+// reading. A CTA works rows off one after the other, in three roles that meet at mbarriers
+// only: a producer warp keeps bulk copies into a ring of 16 KB chunks going, across row
+// ends; four consumer warps sum, each at its own pace; a finisher warp joins a row's sums,
+// finds its alternatives and writes its results while the consumers are at the next row.
+// Few rows are split over the CTAs of a cluster, which join through distributed shared
+// memory.
 //
 // The alternatives. Logits are ranked by 64-bit keys, the value's order above the inverted
-// token number: keys are distinct, so ties need no care. The k-th largest of the maxima of
-// groups of threads in a row's first chunk is a bound: k logits are at least that large, and
-// few are. The row's candidates are the first chunk's logits at or above it and the later
-// ones above it (one that equals it loses the tie to those k); a warp looks at one thread's
-// logits of a chunk at a time, a lane each. At the row's end they are ranked by counting the
-// larger ones. Should there be more than the buffer holds (rising or constant rows), the row
-// is read once more for every alternative; a row with fewer than k tokens above -infinity is
-// filled up from its first tokens.
+// token number: keys are distinct, so ties need no care. All that the consumers do for them
+// is to leave every thread's maximum of every chunk. The k-th largest of the threads' maxima
+// over the row is a bound that k logits reach and few besides; the finisher reads the
+// vectors behind the chunk maxima that reach it once more (from L2), and ranks the logits
+// that do by counting the larger ones. Should they be more than its buffer holds (many equal
+// ones), it reads the row once for every alternative; a row with fewer than k tokens above
+// -infinity is filled up from its first tokens.
 
-constexpr int kLpThreads = 256;    // consumers; one more warp produces
+constexpr int kLpThreads = 128;    // consumers; then the finisher's warp and the producer's
+constexpr int kLpAll = kLpThreads + 64;
 constexpr int kChunk = 16384;      // bytes
-constexpr int kLpStages = 3;
+constexpr int kLpStages = 2;
+constexpr int kLpCtas = 4;         // an SM
 constexpr int kVecs = kChunk / 16 / kLpThreads;   // vectors a thread takes of a chunk
-constexpr int kMaxCandidates = 1296;   // 2 x 10 KB: three CTAs an SM with the ring
+constexpr int kSlots = 8;          // maxima a thread leaves of a row, each of `step` chunks
+constexpr int kCandidates = 512;   // k - 1 threads' logits of a short row, at least
 
 struct LogprobArgs {
-  int V, top_k, splits, per, capacity;   // per: logits of a split; capacity: candidates
+  int V, top_k, splits, per;   // per: logits of a split
   int64_t N, ld;
   const void* logits;
   const int32_t* target;
@@ -157,57 +161,231 @@ __device__ __forceinline__ int span_chunks(const Span& s) {
   return (s.nvec * 16 + kChunk - 1) / kChunk;
 }
 
-// Shared memory behind the ring.
+// Shared memory behind the ring. Two of what a row leaves: the consumers may be a row ahead.
 struct alignas(16) LpShared {
   uint64_t full[kLpStages], empty[kLpStages];
-  uint32_t least;           // the row's bound, in orders
-  int found, abort;
-  int counts[kLpThreads / 32 + 1];   // candidates of the warps, and those filled up
-  Moments moments[2][kLpThreads / 32];   // of even and odd rows: a warp may be a row ahead
+  uint64_t done[2], freed[2];     // a row's maxima and sums are there; have been read
+  Moments moments[2][kLpThreads / 32];
   Moments total;
-  alignas(16) uint32_t group_max[kLpThreads];
-  alignas(16) uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
+  int found, abort;
+  alignas(16) float tops[2][kSlots][kLpThreads];
+  alignas(16) uint64_t cand[kCandidates + 2];
+  uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
+  uint16_t hits[kSlots * kLpThreads];
 };
-
-// Threads whose maxima stand together for the bound: at least 4 top_k groups (fewer give a
-// looser bound, more cost more to rank).
-__device__ __forceinline__ int lp_group(int top_k) {
-  return top_k <= 8 ? 8 : top_k <= 16 ? 4 : top_k <= 32 ? 2 : 1;
-}
 
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-infinity)
 
-__device__ __forceinline__ void sync_consumers() {
-  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLpThreads) : "memory");
+// The `k` best of `count` candidates to sh.top, in order; one warp.
+__device__ __forceinline__ void rank_candidates(LpShared& sh, int count, int k, int lane) {
+  if (lane == 0) sh.cand[count] = 0;   // the last pair's other half
+  __syncwarp();
+  for (int i = lane; i < count; i += 32) {
+    const uint64_t mine = sh.cand[i];
+    int above = 0;
+#pragma unroll 4
+    for (int j = 0; j < count; j += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.cand[j]);
+      above += (o.x > mine) + (o.y > mine);
+    }
+    if (above < k) sh.top[above] = mine;
+  }
+  __syncwarp();
+}
+
+// Finisher: the k best of the row to sh.top; how many there are (all of a short span).
+template <typename T>
+__device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared& sh, const Span& s,
+                                        int64_t row, int parity, int chunks, int step, int k,
+                                        int lane) {
+  constexpr int VE = 16 / sizeof(T), Q = kLpThreads / 32;
+  constexpr int BITS = 8 * sizeof(T), SHIFT = 32 - BITS;   // of an order that differ by type
+  const int slots = (chunks + step - 1) / step;
+  const T* p = (const T*)a.logits + row * a.ld + s.token0;
+  // what threads lane, lane + 32, ... left, and their orders over the row
+  float tops[Q][kSlots];
+  uint32_t best[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      tops[q][i] = i < slots ? sh.tops[parity][i][lane + 32 * q] : -INFINITY;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    float m = tops[q][0];
+#pragma unroll
+    for (int i = 1; i < kSlots; ++i) m = max_nan(m, tops[q][i]);
+    best[q] = lane + 32 * q < s.nvec ? order_of(m) : 0u;
+  }
+  // the k-th largest of the threads' orders: a few by taking the largest away, more by the
+  // largest bound that k threads reach, bit by bit
+  uint32_t bound = 0;
+  if (k <= 12) {
+    uint32_t left[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) left[q] = best[q];
+    for (int i = 0; i < k; ++i) {
+      uint32_t mine = left[0];
+#pragma unroll
+      for (int q = 1; q < Q; ++q) mine = max(mine, left[q]);
+      bound = __reduce_max_sync(0xffffffffu, mine);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, mine == bound)) - 1) {
+        bool taken = false;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          if (!taken && left[q] == bound) {
+            left[q] = 0;
+            taken = true;
+          }
+      }
+    }
+  } else {
+    for (int bit = BITS - 1; bit >= 0; --bit) {
+      const uint32_t next = bound | 1u << bit;
+      int n = 0;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) n += __popc(__ballot_sync(0xffffffffu, best[q] >> SHIFT >= next));
+      if (n >= k) bound = next;
+    }
+    bound <<= SHIFT;
+  }
+  // none at -infinity (see below); 0 stands for -0 too
+  bound = max(bound, kOrderNone + 1);
+  const float least = value_of(bound);
+  // the threads' chunks whose maxima reach it: first vectors of them
+  uint32_t mask = 0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (!(tops[q][i] < least)) mask |= 1u << (q * kSlots + i);
+  int at = __popc(mask), hits = at;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, hits, o);
+    if (lane >= o) hits += up;
+  }
+  at = hits - at;
+  hits = __shfl_sync(0xffffffffu, hits, 31);
+  for (; mask; mask &= mask - 1) {
+    const int i = __ffs(mask) - 1;
+    sh.hits[at++] = (i % kSlots * kLpThreads) + lane + i / kSlots * 32;
+  }
+  __syncwarp();
+  // their vectors, a lane each, four readings under way
+  int count = 0;
+  constexpr int HPW = 32 / kVecs, AHEAD = 4;
+  static_assert(32 % kVecs == 0, "");
+  for (int h0 = 0; h0 < hits; h0 += HPW * AHEAD) {
+    for (int c = 0; c < step; ++c) {
+      uint4 x[AHEAD];
+      int e0[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int h = h0 + i * HPW + lane / kVecs;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        e0[i] = s.count;
+        if (h < hits) {
+          const int hit = sh.hits[h];
+          const int v = (hit / kLpThreads * step + c) * (kChunk / 16) + hit % kLpThreads +
+                        lane % kVecs * kLpThreads;
+          if (v < s.nvec) {
+            e0[i] = v * VE - s.head;
+            if (v < s.full) {
+              x[i] = s.vecs[v];
+            } else {
+              T* e = reinterpret_cast<T*>(&x[i]);
+#pragma unroll
+              for (int j = 0; j < VE; ++j)
+                if (e0[i] + j >= 0 && e0[i] + j < s.count) e[j] = p[e0[i] + j];
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (h0 + i * HPW >= hits) break;
+        uint32_t in = 0;
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (!(vec_at<T>(x[i], j) < least)) in |= 1u << j;
+        // elements before the row's first and past its last
+        if (e0[i] < 0) in &= ~0u << -e0[i];
+        if (e0[i] + VE > s.count) in &= (1u << max(0, s.count - e0[i])) - 1u;
+        for (uint32_t who; (who = __ballot_sync(0xffffffffu, in != 0)) != 0; in &= in - 1) {
+          if (in) {
+            const int j = __ffs(in) - 1, n = count + __popc(who & ((1u << lane) - 1u));
+            float f = vec_at<T>(x[i], 0);
+#pragma unroll
+            for (int jj = 1; jj < VE; ++jj) f = jj == j ? vec_at<T>(x[i], jj) : f;
+            if (n < kCandidates) sh.cand[n] = key_of(f, s.token0 + e0[i] + j);
+          }
+          count += __popc(who);
+        }
+      }
+    }
+  }
+  const int want = min(k, s.count);
+  if (count < want) {   // the rest are tokens at -infinity: the lowest, among the first 2 k
+    for (int t0 = 0; t0 < min(2 * k, s.count); t0 += 32) {
+      const int t = t0 + lane;
+      const bool in = t < min(2 * k, s.count) && order_of(Elem<T>::to_f(p[t])) == kOrderNone;
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      if (in) sh.cand[count + __popc(who & ((1u << lane) - 1u))] = key_of(-INFINITY, s.token0 + t);
+      count += __popc(who);
+    }
+  }
+  if (count <= kCandidates) {
+    rank_candidates(sh, count, k, lane);
+  } else {   // too many: one reading for each alternative, the largest key below the last
+    uint64_t last = ~0ull;
+    for (int i = 0; i < want; ++i) {
+      unsigned long long top = 0;
+#pragma unroll 4
+      for (int e = lane; e < s.count; e += 32) {
+        const uint64_t key = key_of(Elem<T>::to_f(p[e]), s.token0 + e);
+        if (key < last && key > top) top = key;
+      }
+      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      last = top;
+      if (lane == 0) sh.top[i] = top;
+    }
+    __syncwarp();
+  }
+  return want;
 }
 
 template <typename T, bool ENT>
-__global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(const LogprobArgs a) {
-  constexpr int VE = 16 / sizeof(T);
+__global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const LogprobArgs a) {
+  constexpr int VE = 16 / sizeof(T), W = kLpThreads / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   LpShared& sh = *reinterpret_cast<LpShared*>(smem + kLpStages * kChunk);
-  uint64_t* cand = reinterpret_cast<uint64_t*>(&sh + 1);   // the warps' lists, the filled up
-  uint64_t* joined = cand + a.capacity;                    // and all together
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = a.splits > 1 ? (int)cluster_ctarank() : 0;
   const int64_t row0 = blockIdx.x / a.splits, row_step = gridDim.x / a.splits;
-  const int k = a.top_k, capw = a.capacity / (kLpThreads / 32 + 1);   // candidates of a warp
+  const int k = a.top_k;
   volatile int* abort_flag = &sh.abort;
   const uint32_t bFull = smem_u32(&sh.full[0]), bEmpty = smem_u32(&sh.empty[0]);
+  const uint32_t bDone = smem_u32(&sh.done[0]), bFreed = smem_u32(&sh.freed[0]);
 
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < kLpStages; ++i) {
       mbar_init(bFull + 8 * i, 1);
-      mbar_init(bEmpty + 8 * i, kLpThreads / 32);
+      mbar_init(bEmpty + 8 * i, W);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bDone + 8 * i, W);
+      mbar_init(bFreed + 8 * i, 1);
     }
     sh.abort = 0;
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait();
+  // a wait that gives up ends its warp's work; the other warps' waits end by the abort flag
 
-  if (warp == kLpThreads / 32) {
+  if (warp == W + 1) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t n = 0;
@@ -229,299 +407,197 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) token_logprobs_kernel(cons
         mbar_wait(bFull + 8 * (j % kLpStages), (j / kLpStages) & 1, nullptr, a.status);
     }
     __syncwarp();
-    if (a.splits > 1) {   // the consumers' two, for the cluster's one row
-      cluster_sync_all();
-      cluster_sync_all();
-    }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
-  // A wait that gives up (abort) lets the loops run on over what the ring holds: every warp
-  // still meets the others' barriers.
-  int stage = 0;
-  uint32_t phase = 0;
-  int parity = 0;
-  const bool has_target = split == 0 && tid == 0 && a.logp;
-  int next_target = has_target && row0 < a.N ? a.target[row0] : -1;
-  for (int64_t row = row0; row < a.N; row += row_step, parity ^= 1) {
-    const Span s = span_of<T>(a, row, split);
-    const int chunks = span_chunks(s);
-    // the target's logit, on its way while the row is read; the next row's target too
-    float x_t = 0.f;
-    const int target = next_target;
-    if (target >= 0 && target < a.V) x_t = Elem<T>::to_f(((const T*)a.logits + row * a.ld)[target]);
-    if (has_target && row + row_step < a.N) next_target = a.target[row + row_step];
-    int mine_n = 0;   // this warp's candidates
-    Moments mo{-FLT_MAX, 0.f, 0.f};
-    float2 l2 = make_float2(0.f, 0.f), u2 = l2;
-    uint32_t bound = kOrderNone;
-    float thr = -INFINITY;   // candidates are above it
-    const int lane_vec = lane / VE * kLpThreads;   // from a thread's first vector to the lane's
-    auto tail_index = [&](int v) {   // the lane's element of vector v, the row's last at most
-      return min(v * VE + lane % VE, s.head + s.count - 1);
-    };
-    for (int c = 0; c < chunks; ++c) {
-      mbar_wait(bFull + 8 * stage, phase, abort_flag, a.status);
-      const uint4* buf = reinterpret_cast<const uint4*>(smem + stage * kChunk);
-      const int v0 = c * (kChunk / 16);
-      uint4 x[kVecs];
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) x[i] = buf[tid + i * kLpThreads];
-      const bool whole = c > 0 && v0 + kChunk / 16 <= s.full;
-      if (!whole) {   // the row's ends
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          const int v = v0 + tid + i * kLpThreads;
-          if (v >= s.full) {   // past the row, or its last elements: one by one
-            const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-            x[i] = make_uint4(ninf, ninf, ninf, ninf);
-            if (v < s.nvec) {
-              const T* p = reinterpret_cast<const T*>(s.vecs + v);
-              T* e = reinterpret_cast<T*>(&x[i]);
-#pragma unroll
-              for (int j = 0; j < VE; ++j)
-                if (v * VE + j < s.head + s.count) e[j] = p[j];
-            }
-          }
-          if (v == 0) {
-#pragma unroll
-            for (int j = 0; j < VE; ++j)
-              if (j < s.head) vec_clear<T>(x[i], j);
-          }
-        }
-      }
-      float top = vec_max<T>(x[0]);
-#pragma unroll
-      for (int i = 1; i < kVecs; ++i) top = max_nan(top, vec_max<T>(x[i]));
-      if (!(top <= mo.m)) {   // larger, or a NaN: that one makes l 0 and the row bad
-        const float d = (mo.m - (top != top ? INFINITY : top)) * kLog2e, f = ex2(d);
-        const float2 f2 = make_float2(f, f), d2 = make_float2(d, d);
-        if (ENT) u2 = l2.x + l2.y > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
-        l2 = mul2(l2, f2);
-        mo.m = top != top ? INFINITY : top;
-      }
-      if (fabsf(mo.m) < 1e36f) {
-        const float2 neg = make_float2(-mo.m, -mo.m), lg = make_float2(kLog2e, kLog2e);
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          if (!whole && v0 + warp * 32 + i * kLpThreads >= s.nvec) break;   // nothing left
-          // an infinite exponent times 0 would be a NaN: such logits become low finite ones,
-          // whose terms are 0 as well
-          if (ENT) vec_finite<T>(x[i]);
-#pragma unroll
-          for (int j = 0; j < VE / 2; ++j) {
-            // the difference first: exactly 0, and a term of exactly 1, at the maximum
-            const float2 t = mul2(add2(vec_pair<T>(x[i], j), neg), lg);
-            const float2 e = make_float2(ex2(t.x), ex2(t.y));
-            l2 = add2(l2, e);
-            if (ENT) u2 = fma2(e, t, u2);
-          }
-        }
-      } else if (mo.m > -FLT_MAX) {   // differences that could overflow
-#pragma unroll
-        for (int i = 0; i < kVecs * VE; ++i) {
-          const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
-          l2.x += e;
-          if (ENT) u2.x = fmaf(e, d, u2.x);
-        }
-      }
-      if (k) {
-        if (c == 0) {   // the row's bound
-          const int lanes = lp_group(k), groups = kLpThreads / lanes;
-          uint32_t best = tid < s.nvec ? order_of(top) : 0u;
-          for (int o = 1; o < lanes; o <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-          if (tid % lanes == 0) sh.group_max[tid / lanes] = best;
-          if (tid == 0) sh.least = 0;
-          sync_consumers();
-          uint32_t g = 0;
-          if (groups == 32 || tid < groups) {   // 32 groups: every warp for itself
-            g = sh.group_max[groups == 32 ? lane : tid];
-            int gt = 0, ge = 0;
-#pragma unroll 4
-            for (int j = 0; j < groups; j += 4) {
-              const uint4 o = *reinterpret_cast<const uint4*>(&sh.group_max[j]);
-              gt += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
-              ge += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
-            }
-            if (gt >= k || ge < k) g = 0;
-          }
-          if (groups == 32) {
-            g = __reduce_max_sync(0xffffffffu, g);
-          } else {
-            if (g) sh.least = g;   // one value, whoever writes it
-            sync_consumers();
-            g = sh.least;
-          }
-          // later logits have to be above the bound (one equal to it loses to the k that reach
-          // it), this chunk's at it; none at -infinity is in. g 0: fewer than k groups hold any
-          bound = max(g, kOrderNone);
-          const uint32_t below = bound - (bound == 0x80000000u ? 2 : 1);   // 0: -0 equals it
-          thr = value_of(max(below, kOrderNone));
-        }
-        uint32_t todo = __ballot_sync(0xffffffffu, !(top <= thr));
-        while (todo) {   // a thread's logits of the chunk, one a lane
-          const int from = warp * 32 + __ffs(todo) - 1;
-          todo &= todo - 1;
-          float f = -INFINITY;
-          if (lane < kVecs * VE) {
-            if (whole || v0 + from + lane_vec < s.full)
-              f = Elem<T>::to_f(reinterpret_cast<const T*>(buf + from)[lane_vec * VE + lane % VE]);
-            else if (v0 + from + lane_vec < s.nvec)
-              f = Elem<T>::to_f(reinterpret_cast<const T*>(s.vecs)[tail_index(v0 + from + lane_vec)]);
-          }
-          const int e = (v0 + from + lane_vec) * VE + lane % VE - s.head;
-          const bool in = !(f <= thr) && (whole || (e >= 0 && e < s.count));
-          const uint32_t who = __ballot_sync(0xffffffffu, in);
-          const int at = mine_n + __popc(who & ((1u << lane) - 1u));
-          mine_n += __popc(who);
-          if (in && at < capw) cand[warp * capw + at] = key_of(f, s.token0 + e);
-        }
-        if (c == 0) thr = value_of(bound);
-      }
+  } else if (warp == W) {
+    // ------------------------------------------------------------ finisher
+    int parity = 0;
+    uint32_t phase = 0;
+    bool met = false;   // the cluster's barriers are behind it
+    int next_target = a.logp && split == 0 && row0 < a.N ? a.target[row0] : -1;
+    for (int64_t row = row0; row < a.N; row += row_step) {
+      const Span s = span_of<T>(a, row, split);
+      const int chunks = span_chunks(s), step = (chunks + kSlots - 1) / kSlots;
+      // the target's logit, on its way while the row is read; the next row's target too
+      const int target = next_target;
+      float x_t = 0.f;
+      if (target >= 0 && target < a.V) x_t = Elem<T>::to_f(((const T*)a.logits + row * a.ld)[target]);
+      if (a.logp && split == 0 && row + row_step < a.N) next_target = a.target[row + row_step];
+      if (!mbar_wait(bDone + 8 * parity, phase, abort_flag, a.status)) break;
+      Moments mo = sh.moments[parity][lane % W];
+      int found = 0;
+      if (k) found = find_top<T>(a, sh, s, row, parity, chunks, step, k, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bEmpty + 8 * stage);
-      if (++stage == kLpStages) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
-    // ---- the row's end: this CTA's sums and candidates
-    mo.l = l2.x + l2.y;
-    mo.u = u2.x + u2.y;
-    mo.raise(warp_max(mo.m));
-    mo.l = warp_sum(mo.l);
-    if (ENT) mo.u = warp_sum(mo.u);
-    if (lane == 0) {
-      sh.moments[parity][warp] = mo;
-      sh.counts[warp] = mine_n;
-      if (warp == 0) sh.counts[kLpThreads / 32] = 0;
-    }
-    sync_consumers();
-    // the k best of `count` candidates to sh.top, in order: those in the lists of counts[],
-    // `stride` apart, are put together and ranked by counting the larger ones
-    auto rank = [&](int lists, int stride, int count) {
-      for (int i = tid; i < count; i += kLpThreads) {
-        int list = 0, j = i;
-        while (j >= sh.counts[list]) j -= sh.counts[list++];
-        joined[i] = cand[list * stride + j];
-      }
-      if (tid == 0) joined[count] = 0;   // pairs below
-      sync_consumers();
-      for (int i = tid; i < count; i += kLpThreads) {
-        const uint64_t mine = joined[i];
-        int above = 0;
-#pragma unroll 4
-        for (int j = 0; j < count; j += 2) {
-          const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&joined[j]);
-          above += (o.x > mine) + (o.y > mine);
+      if (lane == 0) mbar_arrive(bFreed + 8 * parity);
+      mo.raise(warp_max(mo.m));
+      if (lane >= W) mo.l = mo.u = 0.f;
+      mo.l = warp_sum(mo.l);
+      mo.u = warp_sum(mo.u);
+      if (a.splits > 1) {   // the cluster's only row
+        if (lane == 0) {
+          sh.total = mo;
+          sh.found = found;
         }
-        if (above < k) sh.top[above] = mine;
-      }
-      sync_consumers();
-    };
-    int found = 0;
-    if (k) {
-      constexpr int W = kLpThreads / 32;
-      bool full = false;
-      for (int w = 0; w < W; ++w) {
-        found += sh.counts[w];
-        full |= sh.counts[w] > capw;
-      }
-      const T* p = (const T*)a.logits + row * a.ld + s.token0;
-      if (found < k) {
-        // the rest are tokens at -infinity: the lowest, among the first 2 k
-        if (tid < min(2 * k, s.count) && order_of(Elem<T>::to_f(p[tid])) == kOrderNone)
-          cand[W * capw + atomicAdd(&sh.counts[W], 1)] = key_of(-INFINITY, s.token0 + tid);
-        sync_consumers();
-        found += sh.counts[W];
-      }
-      if (!full) {
-        rank(W + 1, capw, found);
-      } else {   // too many: one reading for each alternative, the largest key below the last
-        uint64_t last = ~0ull;
-        for (int i = 0; i < min(k, s.count); ++i) {
-          unsigned long long best = 0;
-          for (int e = tid; e < s.count; e += kLpThreads) {
-            const uint64_t key = key_of(Elem<T>::to_f(p[e]), s.token0 + e);
-            if (key < last && key > best) best = key;
-          }
-          for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-          if (lane == 0) cand[warp] = best;
-          sync_consumers();
-          for (int w = 0; w < W; ++w) best = max(best, (unsigned long long)cand[w]);
-          last = best;
-          if (tid == 0) sh.top[i] = best;
-          sync_consumers();
-        }
-      }
-      found = min(found, min(k, s.count));
-    }
-    // the first warp finishes the row; the others meet it again at the next row's barriers,
-    // before anything that it reads here is written
-    if (a.splits == 1 && warp != 0) continue;
-    mo = sh.moments[parity][lane % (kLpThreads / 32)];
-    mo.raise(warp_max(mo.m));
-    if (lane >= kLpThreads / 32) mo.l = mo.u = 0.f;
-    mo.l = warp_sum(mo.l);
-    mo.u = warp_sum(mo.u);
-    if (a.splits > 1) {
-      if (tid == 0) {
-        sh.total = mo;
-        sh.found = found;
-      }
-      cluster_sync_all();
-      if (split == 0) {
-        int all = 0;
-        for (int r = 0; r < a.splits; ++r) {
-          const uint32_t at = mapa_shared(smem_u32(&sh.total), r);
-          Moments other;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.m) : "r"(at) : "memory");
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.l) : "r"(at + 4) : "memory");
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.u) : "r"(at + 8) : "memory");
-          if (r == 0) {
-            mo = other;
-          } else {
-            const float m2 = fmaxf(mo.m, other.m);
-            mo.raise(m2);
-            other.raise(m2);
-            mo.l += other.l;
-            mo.u += other.u;
-          }
-          if (k) {
+        cluster_sync_all();
+        if (split == 0) {
+          int all = 0;
+          for (int r = 0; r < a.splits; ++r) {
+            const uint32_t at = mapa_shared(smem_u32(&sh.total), r);
+            Moments other;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.m) : "r"(at) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.l) : "r"(at + 4) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.u) : "r"(at + 8) : "memory");
+            if (r == 0) {
+              mo = other;
+            } else {
+              const float m2 = fmaxf(mo.m, other.m);
+              mo.raise(m2);
+              other.raise(m2);
+              mo.l += other.l;
+              mo.u += other.u;
+            }
             int n;
             asm volatile("ld.shared::cluster.s32 %0, [%1];"
                          : "=r"(n)
                          : "r"(mapa_shared(smem_u32(&sh.found), r))
                          : "memory");
-            if (tid < n)
+            for (int i = lane; i < n; i += 32)
               asm volatile("ld.shared::cluster.u64 %0, [%1];"
-                           : "=l"(cand[r * XMOD_MAX_TOP_K + tid])
-                           : "r"(mapa_shared(smem_u32(&sh.top[0]), r) + 8 * tid)
+                           : "=l"(sh.cand[all + i])
+                           : "r"(mapa_shared(smem_u32(&sh.top[0]), r) + 8 * i)
                            : "memory");
-            if (tid == 0) sh.counts[r] = n;
             all += n;
           }
+          __syncwarp();
+          if (k) rank_candidates(sh, all, k, lane);
         }
-        sync_consumers();
-        if (k) rank(a.splits, XMOD_MAX_TOP_K, all);
+        cluster_sync_all();   // the other CTAs' shared memory has been read
+        if (split != 0) return;
+        met = true;
       }
-      cluster_sync_all();   // the other CTAs' shared memory has been read
-      if (split != 0 || warp != 0) continue;
+      const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
+      const float ll = logf(mo.l), nan = __int_as_float(0x7fc00000);
+      if (lane == 0) {
+        if (bad || target >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+        if (a.lse) a.lse[row] = bad ? nan : mo.m + ll;
+        if (a.entropy) a.entropy[row] = bad ? nan : ll - 0.6931471805599453f * mo.u / mo.l;
+        if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (x_t - mo.m) - ll;
+      }
+      for (int i = lane; i < k; i += 32) {
+        const uint64_t key = sh.top[i];
+        a.top_idx[row * k + i] = token_of(key);
+        a.top_logp[row * k + i] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
+      }
+      __syncwarp();
+      parity ^= 1;
+      if (!parity) phase ^= 1;
     }
-    const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
-    const float ll = logf(mo.l), nan = __int_as_float(0x7fc00000);
-    if (tid == 0) {
-      if (bad || target >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-      if (a.lse) a.lse[row] = bad ? nan : mo.m + ll;
-      if (a.entropy) a.entropy[row] = bad ? nan : ll - 0.6931471805599453f * mo.u / mo.l;
-      if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (x_t - mo.m) - ll;
+    if (met) return;
+  } else {
+    // ------------------------------------------------------------ consumers
+    int stage = 0, parity = 0;
+    uint32_t phase = 0, row_phase = 1;   // the first two rows find their places free
+    for (int64_t row = row0; row < a.N; row += row_step) {
+      const Span s = span_of<T>(a, row, split);
+      const int chunks = span_chunks(s), step = (chunks + kSlots - 1) / kSlots;
+      Moments mo{-FLT_MAX, 0.f, 0.f};
+      float2 l2 = make_float2(0.f, 0.f), u2 = l2;
+      float slot_top = -INFINITY;
+      int slot = 0, in_slot = 0;
+      if (!mbar_wait(bFreed + 8 * parity, row_phase, abort_flag, a.status)) break;
+      bool ok = true;
+      for (int c = 0; c < chunks; ++c) {
+        if (!(ok = mbar_wait(bFull + 8 * stage, phase, abort_flag, a.status))) break;
+        const uint4* buf = reinterpret_cast<const uint4*>(smem + stage * kChunk);
+        const int v0 = c * (kChunk / 16);
+        uint4 x[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) x[i] = buf[tid + i * kLpThreads];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bEmpty + 8 * stage);
+        if (++stage == kLpStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        const bool whole = c > 0 && v0 + kChunk / 16 <= s.full;
+        if (!whole) {   // the row's ends
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i) {
+            const int v = v0 + tid + i * kLpThreads;
+            if (v >= s.full) {   // past the row, or its last elements: one by one
+              const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+              x[i] = make_uint4(ninf, ninf, ninf, ninf);
+              if (v < s.nvec) {
+                const T* p = reinterpret_cast<const T*>(s.vecs + v);
+                T* e = reinterpret_cast<T*>(&x[i]);
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                  if (v * VE + j < s.head + s.count) e[j] = p[j];
+              }
+            }
+            if (v == 0) {
+#pragma unroll
+              for (int j = 0; j < VE; ++j)
+                if (j < s.head) vec_clear<T>(x[i], j);
+            }
+          }
+        }
+        float top = vec_max<T>(x[0]);
+#pragma unroll
+        for (int i = 1; i < kVecs; ++i) top = max_nan(top, vec_max<T>(x[i]));
+        if (!(top <= mo.m)) {   // larger, or a NaN: that one makes l 0 and the row bad
+          const float d = (mo.m - (top != top ? INFINITY : top)) * kLog2e, f = ex2(d);
+          const float2 f2 = make_float2(f, f), d2 = make_float2(d, d);
+          if (ENT) u2 = l2.x + l2.y > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
+          l2 = mul2(l2, f2);
+          mo.m = top != top ? INFINITY : top;
+        }
+        slot_top = max_nan(slot_top, top);
+        if (++in_slot == step || c + 1 == chunks) {
+          sh.tops[parity][slot++][tid] = slot_top;
+          slot_top = -INFINITY;
+          in_slot = 0;
+        }
+        if (fabsf(mo.m) < 1e36f) {
+          const float2 neg = make_float2(-mo.m, -mo.m), lg = make_float2(kLog2e, kLog2e);
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i) {
+            if (!whole && v0 + warp * 32 + i * kLpThreads >= s.nvec) break;   // nothing left
+            // an infinite exponent times 0 would be a NaN: such logits become low finite ones,
+            // whose terms are 0 as well
+            if (ENT) vec_finite<T>(x[i]);
+#pragma unroll
+            for (int j = 0; j < VE / 2; ++j) {
+              // the difference first: exactly 0, and a term of exactly 1, at the maximum
+              const float2 t = mul2(add2(vec_pair<T>(x[i], j), neg), lg);
+              const float2 e = make_float2(ex2(t.x), ex2(t.y));
+              l2 = add2(l2, e);
+              if (ENT) u2 = fma2(e, t, u2);
+            }
+          }
+        } else if (mo.m > -FLT_MAX) {   // differences that could overflow
+#pragma unroll
+          for (int i = 0; i < kVecs * VE; ++i) {
+            const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
+            l2.x += e;
+            if (ENT) u2.x = fmaf(e, d, u2.x);
+          }
+        }
+      }
+      if (!ok) break;
+      mo.l = l2.x + l2.y;
+      mo.u = u2.x + u2.y;
+      mo.raise(warp_max(mo.m));
+      mo.l = warp_sum(mo.l);
+      if (ENT) mo.u = warp_sum(mo.u);
+      if (lane == 0) sh.moments[parity][warp] = mo;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bDone + 8 * parity);
+      parity ^= 1;
+      if (!parity) row_phase ^= 1;
     }
-    for (int i = lane; i < k; i += 32) {
-      const uint64_t key = sh.top[i];
-      a.top_idx[row * k + i] = token_of(key);
-      a.top_logp[row * k + i] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
-    }
+  }
+  if (a.splits > 1) {   // the finishers' two, for the cluster's one row
+    cluster_sync_all();
+    cluster_sync_all();
   }
 }
 
@@ -542,8 +618,10 @@ struct LogprobBwdArgs {
   int* status;
 };
 
+constexpr int kBwdThreads = 256, kBwdVecs = kChunk / 16 / kBwdThreads;
+
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const LogprobBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const LogprobBwdArgs a) {
   constexpr int VE = 16 / sizeof(T);
   pdl_trigger();
   pdl_wait();
@@ -556,10 +634,10 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const Lo
     const int head = (int)((uintptr_t)d & 15) / (int)sizeof(T);
     const bool same = (((uintptr_t)x ^ (uintptr_t)d) & 15) == 0;
     const int e0 = (chunk * (kChunk / 16) + (int)threadIdx.x) * VE - head;
-    uint4 v[kVecs];
+    uint4 v[kBwdVecs];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int e = e0 + i * kLpThreads * VE;
+    for (int i = 0; i < kBwdVecs; ++i) {
+      const int e = e0 + i * kBwdThreads * VE;
       if (same && e >= 0 && e + VE <= a.V) {
         v[i] = *reinterpret_cast<const uint4*>(x + e);
       } else {
@@ -582,8 +660,8 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const Lo
     const float b = -fmaf(gh, ent, g);
     const float2 mul = make_float2(-gh, -gh), add = make_float2(b, b);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int e = e0 + i * kLpThreads * VE;
+    for (int i = 0; i < kBwdVecs; ++i) {
+      const int e = e0 + i * kBwdThreads * VE;
       if (e >= a.V || e + VE <= 0) continue;
       uint4 out;
 #pragma unroll
@@ -626,21 +704,16 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
   while (a.splits < 8 && a.N * a.splits * 2 <= sms && (int64_t)a.V * sizeof(T) >= 2 * a.splits * (int64_t)kChunk)
     a.splits *= 2;
   a.per = (a.V + a.splits - 1) / a.splits;
-  // about top_k logits of every chunk's size are above a bound from one chunk
-  const int64_t want = 2 * (int64_t)a.top_k * ((int64_t)a.per * sizeof(T) / kChunk + 1);
-  const int lists = kLpThreads / 32 + 1;   // of at least 128: a list may fill up 2 top_k
-  a.capacity = !a.top_k ? 0 : want < 128 * lists ? 128 * lists : want < kMaxCandidates ? (int)want / lists * lists : kMaxCandidates;
-  a.capacity += a.capacity & 1;
-  const int smem = kLpStages * kChunk + (int)sizeof(LpShared) + 16 * a.capacity + 16;
+  constexpr int smem = kLpStages * kChunk + (int)sizeof(LpShared);
+  static_assert(kLpCtas * (smem + 1024) <= 228 * 1024, "");
   auto kernel = token_logprobs_kernel<T, ENT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kernel, kLpStages * kChunk + (int)sizeof(LpShared) +
-                                         16 * kMaxCandidates + 16, done);
+  cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t most = (int64_t)sms * 3;   // resident: by registers, and by shared memory
+  const int64_t most = (int64_t)sms * kLpCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.splits > 1 ? a.N * a.splits : a.N < most ? a.N : most));
-  cfg.blockDim = dim3(kLpThreads + 32);
+  cfg.blockDim = dim3(kLpAll);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[2];
@@ -664,7 +737,7 @@ cudaError_t launch_logprobs_bwd(const Ctx& c, const LogprobBwdArgs& a0) {
   a.chunks = (int)(((int64_t)a.V + 2 * VE - 2) / VE / (kChunk / 16)) + 1;
   const int64_t items = a.N * a.chunks, most = (int64_t)sms * 64;
   return launch_pdl(token_logprobs_bwd_kernel<T>, dim3((unsigned)(items < most ? items : most)),
-                    dim3(kLpThreads), 0, c.stream, a);
+                    dim3(kBwdThreads), 0, c.stream, a);
 }
 
 }  // namespace
@@ -688,7 +761,7 @@ int xmod_token_logprobs(xmod_dtype dt, int64_t N, int V, const void* logits, int
   for (const void* p : ps)
     if (!ptr4_or_null(p)) return XMOD_ERR_INVALID_ARG;
   if (top_k > XMOD_MAX_TOP_K || N > INT32_MAX || V > INT32_MAX - 65536) return XMOD_ERR_UNSUPPORTED;
-  const LogprobArgs a{V, top_k, 1, V, 0, N, ld, logits, target, logp, entropy, lse, top_idx, top_logp,
+  const LogprobArgs a{V, top_k, 1, V, N, ld, logits, target, logp, entropy, lse, top_idx, top_logp,
                       status_out};
   const Ctx c{(cudaStream_t)stream, status_out};
   if (dt == XMOD_BF16)
