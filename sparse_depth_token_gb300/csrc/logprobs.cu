@@ -508,78 +508,89 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
         if (!(ok = mbar_wait(bFull + 8 * stage, phase, abort_flag, a.status))) break;
         const uint4* buf = reinterpret_cast<const uint4*>(smem + stage * kChunk);
         const int v0 = c * (kChunk / 16);
-        uint4 x[kVecs];
+        auto absorb = [&](auto& x) {   // takes vectors into the sums
+          constexpr int N = sizeof(x) / sizeof(uint4);
+          float top = vec_max<T>(x[0]);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) x[i] = buf[tid + i * kLpThreads];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bEmpty + 8 * stage);
+          for (int i = 1; i < N; ++i) top = max_nan(top, vec_max<T>(x[i]));
+          if (!(top <= mo.m)) {   // larger, or a NaN: that one makes l 0 and the row bad
+            const float d = (mo.m - (top != top ? INFINITY : top)) * kLog2e, f = ex2(d);
+            const float2 f2 = make_float2(f, f), d2 = make_float2(d, d);
+            if (ENT) u2 = l2.x + l2.y > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
+            l2 = mul2(l2, f2);
+            mo.m = top != top ? INFINITY : top;
+          }
+          slot_top = max_nan(slot_top, top);
+          if (fabsf(mo.m) < 1e36f) {
+            const float2 neg = make_float2(-mo.m, -mo.m), lg = make_float2(kLog2e, kLog2e);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              // an infinite exponent times 0 would be a NaN: such logits become low finite
+              // ones, whose terms are 0 as well
+              if (ENT) vec_finite<T>(x[i]);
+#pragma unroll
+              for (int j = 0; j < VE / 2; ++j) {
+                // the difference first: exactly 0, and a term of exactly 1, at the maximum
+                const float2 t = mul2(add2(vec_pair<T>(x[i], j), neg), lg);
+                const float2 e = make_float2(ex2(t.x), ex2(t.y));
+                l2 = add2(l2, e);
+                if (ENT) u2 = fma2(e, t, u2);
+              }
+            }
+          } else if (mo.m > -FLT_MAX) {   // differences that could overflow
+#pragma unroll
+            for (int i = 0; i < N * VE; ++i) {
+              const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
+              l2.x += e;
+              if (ENT) u2.x = fmaf(e, d, u2.x);
+            }
+          }
+        };
+        if (v0 + kChunk / 16 <= s.full) {
+          uint4 x[kVecs];
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i) x[i] = buf[tid + i * kLpThreads];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bEmpty + 8 * stage);
+          if (v0 + tid == 0) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+              if (j < s.head) vec_clear<T>(x[0], j);
+          }
+          absorb(x);
+        } else {   // the row's last chunk: what there is of it, a vector at a time
+#pragma unroll 1
+          for (int i = 0; v0 + warp * 32 + i * kLpThreads < s.nvec; ++i) {
+            const int v = v0 + tid + i * kLpThreads;
+            const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+            uint4 x[1] = {make_uint4(ninf, ninf, ninf, ninf)};
+            if (v < s.full) {
+              x[0] = buf[tid + i * kLpThreads];
+              if (v == 0) {
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                  if (j < s.head) vec_clear<T>(x[0], j);
+              }
+            } else if (v < s.nvec) {   // the last elements, one by one
+              const T* p = reinterpret_cast<const T*>(s.vecs + v);
+              T* e = reinterpret_cast<T*>(&x[0]);
+#pragma unroll
+              for (int j = 0; j < VE; ++j)
+                if (v * VE + j >= s.head && v * VE + j < s.head + s.count) e[j] = p[j];
+            }
+            absorb(x);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bEmpty + 8 * stage);
+        }
         if (++stage == kLpStages) {
           stage = 0;
           phase ^= 1;
         }
-        const bool whole = c > 0 && v0 + kChunk / 16 <= s.full;
-        if (!whole) {   // the row's ends
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i) {
-            const int v = v0 + tid + i * kLpThreads;
-            if (v >= s.full) {   // past the row, or its last elements: one by one
-              const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-              x[i] = make_uint4(ninf, ninf, ninf, ninf);
-              if (v < s.nvec) {
-                const T* p = reinterpret_cast<const T*>(s.vecs + v);
-                T* e = reinterpret_cast<T*>(&x[i]);
-#pragma unroll
-                for (int j = 0; j < VE; ++j)
-                  if (v * VE + j < s.head + s.count) e[j] = p[j];
-              }
-            }
-            if (v == 0) {
-#pragma unroll
-              for (int j = 0; j < VE; ++j)
-                if (j < s.head) vec_clear<T>(x[i], j);
-            }
-          }
-        }
-        float top = vec_max<T>(x[0]);
-#pragma unroll
-        for (int i = 1; i < kVecs; ++i) top = max_nan(top, vec_max<T>(x[i]));
-        if (!(top <= mo.m)) {   // larger, or a NaN: that one makes l 0 and the row bad
-          const float d = (mo.m - (top != top ? INFINITY : top)) * kLog2e, f = ex2(d);
-          const float2 f2 = make_float2(f, f), d2 = make_float2(d, d);
-          if (ENT) u2 = l2.x + l2.y > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
-          l2 = mul2(l2, f2);
-          mo.m = top != top ? INFINITY : top;
-        }
-        slot_top = max_nan(slot_top, top);
         if (++in_slot == step || c + 1 == chunks) {
           sh.tops[parity][slot++][tid] = slot_top;
           slot_top = -INFINITY;
           in_slot = 0;
-        }
-        if (fabsf(mo.m) < 1e36f) {
-          const float2 neg = make_float2(-mo.m, -mo.m), lg = make_float2(kLog2e, kLog2e);
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i) {
-            if (!whole && v0 + warp * 32 + i * kLpThreads >= s.nvec) break;   // nothing left
-            // an infinite exponent times 0 would be a NaN: such logits become low finite ones,
-            // whose terms are 0 as well
-            if (ENT) vec_finite<T>(x[i]);
-#pragma unroll
-            for (int j = 0; j < VE / 2; ++j) {
-              // the difference first: exactly 0, and a term of exactly 1, at the maximum
-              const float2 t = mul2(add2(vec_pair<T>(x[i], j), neg), lg);
-              const float2 e = make_float2(ex2(t.x), ex2(t.y));
-              l2 = add2(l2, e);
-              if (ENT) u2 = fma2(e, t, u2);
-            }
-          }
-        } else if (mo.m > -FLT_MAX) {   // differences that could overflow
-#pragma unroll
-          for (int i = 0; i < kVecs * VE; ++i) {
-            const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
-            l2.x += e;
-            if (ENT) u2.x = fmaf(e, d, u2.x);
-          }
         }
       }
       if (!ok) break;
