@@ -180,10 +180,21 @@ def _p(t):
     return t.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        _torch_module = torch
+    return _torch_module
+
+
+def _stream(stream):
+    if stream is None:   # the raw handle: a Stream object costs as much as a launch
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -377,51 +388,46 @@ def kv_cache(k, v, table, k_scale=None, v_scale=None) -> KVCache:
     contiguous (with k_scale / v_scale [n_pages, n_kv_heads, page_size] fp32: e4m3 codes,
     one byte each), table [n_seqs, max_pages] int32 contiguous. The struct keeps the
     tensors, so their memory outlives every call using it."""
+    T = _torch()
     e4m3 = k_scale is not None
     ts = (k, v, table) + ((k_scale, v_scale) if e4m3 else ())
-    if (any(t is None or not t.is_cuda or not t.is_contiguous() for t in ts) or k.dim() != 4 or table.dim() != 2
-            or k.shape != v.shape or k.dtype != v.dtype or _dtype_name(table) != "int32"
-            or (e4m3 and (k.element_size() != 1 or k_scale.shape != k.shape[:3]
-                          or v_scale.shape != k.shape[:3] or _dtype_name(k_scale) != "float32"
-                          or _dtype_name(v_scale) != "float32"))):
+    if (any(t is None or not t.is_cuda or not t.is_contiguous() for t in ts) or k.dim() != 4
+            or table.dim() != 2 or k.shape != v.shape or k.dtype is not v.dtype
+            or table.dtype is not T.int32 or (v_scale is not None) != e4m3
+            or (e4m3 and (k.element_size() != 1 or any(
+                t.shape != k.shape[:3] or t.dtype is not T.float32 for t in ts[3:])))):
         raise XmodError("kv_cache", ERR_INVALID_ARG)
     c = KVCache(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(table), k.shape[0], k.shape[2],
                 table.shape[0], table.shape[1], CACHE_E4M3 if e4m3 else CACHE_NATIVE)
     c._keep = ts
-    c._layout = (k.shape[1], k.shape[3], "e4m3" if e4m3 else _dtype_name(k))
+    c.n_kv_heads, c.head_dim, c.dtype = k.shape[1], k.shape[3], k.dtype
     return c
 
 
-_NAMES = {}
+def _vec(fn, t, dtype, n):
+    """Device pointer of an optional contiguous tensor of n elements of that dtype."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise XmodError(fn, ERR_INVALID_ARG)
+    return t.data_ptr()
 
 
-def _dtype_name(t) -> str:
-    """"bfloat16", "int32", ... of a tensor's dtype."""
-    name = _NAMES.get(t.dtype)
-    if name is None:
-        name = _NAMES[t.dtype] = str(t.dtype).rsplit(".", 1)[-1]
-    return name
+def _mat(fn, t, dtype, rows, width):
+    """(device pointer, row stride) of a [rows, width] tensor with contiguous rows."""
+    if (t.dtype is not dtype or not t.is_cuda or t.shape != (rows, width)
+            or (width > 1 and t.stride(1) != 1)):
+        raise XmodError(fn, ERR_INVALID_ARG)
+    return t.data_ptr(), t.stride(0) if rows > 1 else width
 
 
-def _is(t, name, shape=None) -> bool:
-    """Whether an optional tensor argument is absent, or a contiguous device tensor of that
-    dtype and shape."""
-    return t is None or (t.is_cuda and _dtype_name(t) == name and t.is_contiguous()
-                         and (shape is None or tuple(t.shape) == shape))
-
-
-def _rows(t, name, width) -> bool:
-    """Whether t is a [rows, width] device tensor of that dtype with contiguous rows."""
-    return (t.is_cuda and t.dim() == 2 and _dtype_name(t) == name and t.shape[1] == width
-            and (t.stride(1) == 1 or width == 1))
-
-
-_ELEM = {BF16: "bfloat16", FP32: "float32"}
-
-
-def _ld(t) -> int:
-    """Row stride of a [rows, width] tensor (a single row's stride is its width)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _elem(fn, dm, cache):
+    """torch dtype of the dims' elements; the cache has to be of these dims."""
+    el = _torch().bfloat16 if dm.dtype == BF16 else _torch().float32
+    if (cache.n_kv_heads != dm.n_kv_heads or cache.head_dim != dm.head_dim
+            or (cache.format == CACHE_NATIVE and cache.dtype is not el)):
+        raise XmodError(fn, ERR_INVALID_ARG)
+    return el
 
 
 def cache_append(dm, cache: KVCache, qkv, w, seq, slot, pos=None, q_out=None, status=None,
@@ -429,20 +435,20 @@ def cache_append(dm, cache: KVCache, qkv, w, seq, slot, pos=None, q_out=None, st
     """xmod_cache_append: the rows of qkv [M, (n_heads + 2 n_kv_heads) head_dim] into the
     cache, their transformed q into q_out (None: not wanted). w: a LayerWeights (its QK-norm
     gains and rope_theta count) or None. status: as for gather."""
+    fn = "xmod_cache_append"
     M = qkv.shape[0]
-    el = _ELEM.get(dm.dtype)
+    el = _elem(fn, dm, cache)
+    i32 = _torch().int32
     qw = dm.n_heads * dm.head_dim
-    if (not _rows(qkv, el, qw + 2 * dm.n_kv_heads * dm.head_dim)
-            or not _is(seq, "int32", (M,)) or slot is None or not _is(slot, "int32", (M,))
-            or not _is(pos, "int32", (M,))
-            or (q_out is not None and not (_rows(q_out, el, qw) and q_out.shape[0] == M))
-            or cache._layout[:2] != (dm.n_kv_heads, dm.head_dim)
-            or cache._layout[2] not in ("e4m3", el)):
-        raise XmodError("xmod_cache_append", ERR_INVALID_ARG)
-    _check("xmod_cache_append", load().xmod_cache_append(
-        ctypes.byref(dm), ctypes.byref(cache), M, _p(qkv), _ld(qkv),
-        ctypes.byref(w) if w is not None else None, _p(seq), _p(slot), _p(pos), _p(q_out),
-        _ld(q_out) if q_out is not None else 0, _p(status), _stream(stream)))
+    qkv_p, ld = _mat(fn, qkv, el, M, qw + 2 * dm.n_kv_heads * dm.head_dim)
+    q_p, ldq = _mat(fn, q_out, el, M, qw) if q_out is not None else (None, 0)
+    st = load().xmod_cache_append(
+        ctypes.byref(dm), ctypes.byref(cache), M, qkv_p, ld,
+        ctypes.byref(w) if w is not None else None, _vec(fn, seq, i32, M),
+        _vec(fn, slot, i32, M), _vec(fn, pos, i32, M), q_p, ldq, _vec(fn, status, i32, 1),
+        _stream(stream))
+    if st:
+        raise XmodError(fn, st)
 
 
 def cache_attention_workspace_bytes(dm: Dims, M: int) -> int:
@@ -452,21 +458,28 @@ def cache_attention_workspace_bytes(dm: Dims, M: int) -> int:
 def cache_attention(dm, cache: KVCache, q, seq, lens, o, ws, lse=None, stream=None):
     """xmod_cache_attention: o [M, n_heads head_dim] (and lse [M, n_heads] fp32) of the
     queries q over the first lens[m] slots of sequence seq[m] (None: m)."""
+    fn = "xmod_cache_attention"
     M = q.shape[0]
-    el = _ELEM.get(dm.dtype)
+    el = _elem(fn, dm, cache)
+    t = _torch()
     qw = dm.n_heads * dm.head_dim
-    if (not _rows(q, el, qw) or lens is None or not _is(seq, "int32", (M,))
-            or not _is(lens, "int32", (M,)) or o is None or not _is(o, el, (M, qw))
-            or not _is(lse, "float32", (M, dm.n_heads))
-            or cache._layout[:2] != (dm.n_kv_heads, dm.head_dim)
-            or cache._layout[2] not in ("e4m3", el)):
-        raise XmodError("xmod_cache_attention", ERR_INVALID_ARG)
-    _check("xmod_cache_attention", load().xmod_cache_attention(
-        ctypes.byref(dm), ctypes.byref(cache), M, _p(q), _ld(q), _p(seq), _p(lens), _p(o),
-        _p(lse), _p(ws), _wsb(ws), _stream(stream)))
+    q_p, ldq = _mat(fn, q, el, M, qw)
+    st = load().xmod_cache_attention(
+        ctypes.byref(dm), ctypes.byref(cache), M, q_p, ldq, _vec(fn, seq, t.int32, M),
+        _vec(fn, lens, t.int32, M), _vec(fn, o, el, M * qw),
+        _vec(fn, lse, t.float32, M * dm.n_heads), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _stream(stream))
+    if st:
+        raise XmodError(fn, st)
 
 
-_DTYPES = {"bfloat16": BF16, "float32": FP32}
+def _logits_dtype(fn, t):
+    T = _torch()
+    if t.dtype is T.bfloat16:
+        return BF16
+    if t.dtype is T.float32:
+        return FP32
+    raise XmodError(fn, ERR_INVALID_ARG)
 
 
 def token_logprobs(logits, target=None, logp=None, entropy=None, lse=None, top_idx=None,
@@ -474,31 +487,36 @@ def token_logprobs(logits, target=None, logp=None, entropy=None, lse=None, top_i
     """xmod_token_logprobs: logits [N, V] bf16 or fp32 (rows may be strided); the outputs
     that are given are written (logp, entropy, lse [N] fp32, top_idx int32 and top_logp
     fp32 [N, k])."""
+    fn = "xmod_token_logprobs"
     N, V = logits.shape
-    k = 0 if top_idx is None else top_idx.shape[1]
-    dt = _DTYPES.get(_dtype_name(logits), -1)
-    if (not _rows(logits, _dtype_name(logits), V) or not _is(target, "int32", (N,))
-            or not all(_is(t, "float32", (N,)) for t in (logp, entropy, lse))
-            or not _is(top_idx, "int32", (N, k)) or not _is(top_logp, "float32", (N, k))):
-        raise XmodError("xmod_token_logprobs", ERR_INVALID_ARG)
-    _check("xmod_token_logprobs", load().xmod_token_logprobs(
-        dt, N, V, _p(logits), _ld(logits), _p(target), _p(logp), _p(entropy), _p(lse), k,
-        _p(top_idx), _p(top_logp), _p(status), _stream(stream)))
+    k = top_idx.shape[1] if top_idx is not None else 0
+    dt = _logits_dtype(fn, logits)
+    i32, f32 = _torch().int32, _torch().float32
+    x, ld = _mat(fn, logits, logits.dtype, N, V)
+    st = load().xmod_token_logprobs(
+        dt, N, V, x, ld, _vec(fn, target, i32, N), _vec(fn, logp, f32, N),
+        _vec(fn, entropy, f32, N), _vec(fn, lse, f32, N), k, _vec(fn, top_idx, i32, N * k),
+        _vec(fn, top_logp, f32, N * k), _vec(fn, status, i32, 1), _stream(stream))
+    if st:
+        raise XmodError(fn, st)
 
 
 def token_logprobs_bwd(logits, target, lse, g_logp, dlogits, entropy=None, g_entropy=None,
                        status=None, stream=None):
     """xmod_token_logprobs_bwd: dlogits [N, V] of the gradients g_logp and g_entropy [N]
     (either may be None); dlogits may be logits itself."""
+    fn = "xmod_token_logprobs_bwd"
     N, V = logits.shape
-    name = _dtype_name(logits)
-    if (not _rows(logits, name, V) or not _rows(dlogits, name, V) or dlogits.shape[0] != N
-            or not _is(target, "int32", (N,))
-            or not all(_is(t, "float32", (N,)) for t in (lse, entropy, g_logp, g_entropy))):
-        raise XmodError("xmod_token_logprobs_bwd", ERR_INVALID_ARG)
-    _check("xmod_token_logprobs_bwd", load().xmod_token_logprobs_bwd(
-        _DTYPES.get(name, -1), N, V, _p(logits), _ld(logits), _p(target), _p(lse), _p(entropy),
-        _p(g_logp), _p(g_entropy), _p(dlogits), _ld(dlogits), _p(status), _stream(stream)))
+    dt = _logits_dtype(fn, logits)
+    i32, f32 = _torch().int32, _torch().float32
+    x, ld = _mat(fn, logits, logits.dtype, N, V)
+    d, ldd = _mat(fn, dlogits, logits.dtype, N, V)
+    st = load().xmod_token_logprobs_bwd(
+        dt, N, V, x, ld, _vec(fn, target, i32, N), _vec(fn, lse, f32, N),
+        _vec(fn, entropy, f32, N), _vec(fn, g_logp, f32, N), _vec(fn, g_entropy, f32, N), d, ldd,
+        _vec(fn, status, i32, 1), _stream(stream))
+    if st:
+        raise XmodError(fn, st)
 
 
 def selftest_wait_timeout(ws, stream=None):
