@@ -963,12 +963,14 @@ __global__ void __launch_bounds__(128, 2) cache_attention_f32_kernel(const Decod
 // ---------------------------------------------------------------- join
 
 // Segment of CTA blockIdx.x that later CTAs' ranges continue, query head blockIdx.y: the
-// parts' maxima, then their sums and outputs at the common maximum. Four warps take every
-// fourth part each; their sums are added in order.
+// parts' maxima and sums, and their outputs weighted to the common maximum. Eight warps take
+// every eighth part each, four of them under way at a time; their sums are added in order.
+constexpr int kJoinWarps = 8;
+
 template <typename T, int HD, int ROWS>
-__global__ void __launch_bounds__(128) cache_attention_join_kernel(const DecodeArgs a) {
-  constexpr int E = HD / 32;
-  __shared__ float sm_top[4], sm_l[4], sm_o[4][HD];
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_attention_join_kernel(const DecodeArgs a) {
+  constexpr int E = HD / 32, AHEAD = 4;
+  __shared__ float sm_w[kMaxCtas], sm_red[2][kJoinWarps], sm_o[kJoinWarps][HD];
   pdl_trigger();
   pdl_wait();
   const Join j = a.join[blockIdx.x];
@@ -980,33 +982,67 @@ __global__ void __launch_bounds__(128) cache_attention_join_kernel(const DecodeA
   const int parts = j.last - j.first + 1;
   // part 0 is the starting CTA's second slot, the others their CTAs' first
   auto part = [&](int p) { return part_at<HD, ROWS>(a, 2 * (j.first + p) + (p == 0 ? 1 : 0)); };
-  float top = -INFINITY;
-  for (int p = threadIdx.x; p < parts; p += 128) top = fmaxf(top, part(p)[row]);
+  float v[AHEAD][E];   // this warp's first parts, on their way with the maxima
+  auto fetch = [&](int p0) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int p = p0 + i * kJoinWarps;
+      const float* at = part(min(p, parts - 1)) + 2 * ROWS + row * HD + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = p < parts ? at[e] : 0.f;
+    }
+  };
+  fetch(warp);
+  float m[2], s[2], top = -INFINITY;   // at most kMaxCtas parts: two a thread
+  static_assert(kMaxCtas <= 2 * kJoinWarps * 32, "");
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = threadIdx.x + i * kJoinWarps * 32;
+    m[i] = p < parts ? part(p)[row] : -INFINITY;
+    s[i] = p < parts ? part(p)[ROWS + row] : 0.f;
+    top = fmaxf(top, m[i]);
+  }
   top = warp_max(top);
-  if (lane == 0) sm_top[warp] = top;
+  if (lane == 0) sm_red[0][warp] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(sm_top[0], sm_top[1]), fmaxf(sm_top[2], sm_top[3]));
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sm_red[0][w]);
   const float low = top == -INFINITY ? 0.f : top;
-  float l = 0.f, o[E];
+  float l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = threadIdx.x + i * kJoinWarps * 32;
+    const float f = exp2f(m[i] - low);
+    if (p < parts) sm_w[p] = f;
+    l = fmaf(s[i], f, l);
+  }
+  l = warp_sum(l);
+  if (lane == 0) sm_red[1][warp] = l;
+  __syncthreads();
+  float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int p = warp; p < parts; p += 4) {
-    const float* at = part(p);
-    const float f = exp2f(at[row] - low);
-    l = fmaf(at[ROWS + row], f, l);
+  for (int p0 = warp; p0 < parts; p0 += AHEAD * kJoinWarps) {
+    if (p0 != warp) fetch(p0);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(at[2 * ROWS + row * HD + lane + 32 * e], f, o[e]);
+    for (int i = 0; i < AHEAD; ++i) {
+      const int p = p0 + i * kJoinWarps;
+      if (p < parts) {
+        const float f = sm_w[p];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(v[i][e], f, o[e]);
+      }
+    }
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane + 32 * e] = o[e];
-  if (lane == 0) sm_l[warp] = l;
+  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
   __syncthreads();
-  l = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
+  l = 0.f;
+  for (int w = 0; w < kJoinWarps; ++w) l += sm_red[1][w];
   const int64_t head = (int64_t)j.row * a.hq + g * group + h0 + row;
-  for (int d = threadIdx.x; d < HD; d += 128) {
-    const float v = (sm_o[0][d] + sm_o[1][d]) + (sm_o[2][d] + sm_o[3][d]);
-    st_f((T*)a.o + head * HD + d, l > 0.f || l != l ? v / l : 0.f);
+  for (int d = threadIdx.x; d < HD; d += kJoinWarps * 32) {
+    float x = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) x += sm_o[w][d];
+    st_f((T*)a.o + head * HD + d, l > 0.f || l != l ? x / l : 0.f);
   }
   if (a.lse && threadIdx.x == 0) a.lse[head] = (top + log2f(l)) * 0.6931471805599453f;
 }
@@ -1044,7 +1080,8 @@ int run_tc(const Ctx& c, const DecodeArgs& a, int ctas) {
   const int group = a.hq / a.hkv;
   XMOD_LAUNCH(c, "cache_attn_join",
               launch_pdl(cache_attention_join_kernel<__nv_bfloat16, HD, ROWS>,
-                         dim3(ctas, group < ROWS ? group : ROWS), dim3(128), 0, c.stream, a));
+                         dim3(ctas, group < ROWS ? group : ROWS), dim3(kJoinWarps * 32), 0,
+                         c.stream, a));
   return XMOD_OK;
 }
 
@@ -1057,7 +1094,8 @@ int run_hd(const Ctx& c, const DecodeArgs& a, int ctas, bool fp32, bool fp8, int
     const int group = a.hq / a.hkv;
     XMOD_LAUNCH(c, "cache_attn_join",
                 launch_pdl(cache_attention_join_kernel<float, HD, ROWS>,
-                           dim3(ctas, group < ROWS ? group : ROWS), dim3(128), 0, c.stream, a));
+                           dim3(ctas, group < ROWS ? group : ROWS), dim3(kJoinWarps * 32), 0,
+                         c.stream, a));
     return XMOD_OK;
   }
   if (rows == 8) return fp8 ? run_tc<HD, true, 8>(c, a, ctas) : run_tc<HD, false, 8>(c, a, ctas);

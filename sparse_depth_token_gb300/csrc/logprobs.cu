@@ -166,13 +166,21 @@ struct alignas(16) LpShared {
   uint64_t full[kLpStages], empty[kLpStages];
   uint64_t done[2], freed[2];     // a row's maxima and sums are there; have been read
   Moments moments[2][kLpThreads / 32];
-  Moments total;
-  int found, abort;
+  Moments parts[8];               // of a cluster's CTAs, in the first one
+  int abort;
   alignas(16) float tops[2][kSlots][kLpThreads];
   alignas(16) uint64_t cand[kCandidates + 2];
   uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
+  uint64_t lists[8 * XMOD_MAX_TOP_K];   // the cluster's
   uint16_t hits[kSlots * kLpThreads];
 };
+
+__device__ __forceinline__ void st_cluster(uint32_t at, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster64(uint32_t at, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
 
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-infinity)
 
@@ -381,7 +389,10 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
     sh.abort = 0;
     fence_barrier_init();
   }
-  __syncthreads();
+  if (a.splits > 1)
+    cluster_sync_all();   // also: the cluster's CTAs run, their shared memory may be written
+  else
+    __syncthreads();
   pdl_wait();
   // a wait that gives up ends its warp's work; the other warps' waits end by the abort flag
 
@@ -411,7 +422,7 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
     // ------------------------------------------------------------ finisher
     int parity = 0;
     uint32_t phase = 0;
-    bool met = false;   // the cluster's barriers are behind it
+    bool met = false;   // the cluster's barrier is behind it
     int next_target = a.logp && split == 0 && row0 < a.N ? a.target[row0] : -1;
     for (int64_t row = row0; row < a.N; row += row_step) {
       const Span s = span_of<T>(a, row, split);
@@ -431,47 +442,30 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
       if (lane >= W) mo.l = mo.u = 0.f;
       mo.l = warp_sum(mo.l);
       mo.u = warp_sum(mo.u);
-      if (a.splits > 1) {   // the cluster's only row
+      if (a.splits > 1) {   // the cluster's only row: everything to the first CTA
         if (lane == 0) {
-          sh.total = mo;
-          sh.found = found;
+          const uint32_t at = mapa_shared(smem_u32(&sh.parts[split]), 0);
+          st_cluster(at, __float_as_uint(mo.m));
+          st_cluster(at + 4, __float_as_uint(mo.l));
+          st_cluster(at + 8, __float_as_uint(mo.u));
         }
+        const int before = split * min(k, a.per);   // all splits but the last are full
+        for (int i = lane; i < found; i += 32)
+          st_cluster64(mapa_shared(smem_u32(&sh.lists[before + i]), 0), sh.top[i]);
         cluster_sync_all();
-        if (split == 0) {
-          int all = 0;
-          for (int r = 0; r < a.splits; ++r) {
-            const uint32_t at = mapa_shared(smem_u32(&sh.total), r);
-            Moments other;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.m) : "r"(at) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.l) : "r"(at + 4) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.u) : "r"(at + 8) : "memory");
-            if (r == 0) {
-              mo = other;
-            } else {
-              const float m2 = fmaxf(mo.m, other.m);
-              mo.raise(m2);
-              other.raise(m2);
-              mo.l += other.l;
-              mo.u += other.u;
-            }
-            int n;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                         : "=r"(n)
-                         : "r"(mapa_shared(smem_u32(&sh.found), r))
-                         : "memory");
-            for (int i = lane; i < n; i += 32)
-              asm volatile("ld.shared::cluster.u64 %0, [%1];"
-                           : "=l"(sh.cand[all + i])
-                           : "r"(mapa_shared(smem_u32(&sh.top[0]), r) + 8 * i)
-                           : "memory");
-            all += n;
-          }
-          __syncwarp();
-          if (k) rank_candidates(sh, all, k, lane);
-        }
-        cluster_sync_all();   // the other CTAs' shared memory has been read
-        if (split != 0) return;
         met = true;
+        if (split != 0) return;
+        mo = sh.parts[min(lane, a.splits - 1)];
+        mo.raise(warp_max(mo.m));
+        if (lane >= a.splits) mo.l = mo.u = 0.f;
+        mo.l = warp_sum(mo.l);
+        mo.u = warp_sum(mo.u);
+        if (k) {
+          const int last = a.V - (a.splits - 1) * a.per;
+          const int all = (a.splits - 1) * min(k, a.per) + min(k, last);
+          for (int i = lane; i < all; i += 32) sh.cand[i] = sh.lists[i];
+          rank_candidates(sh, all, k, lane);
+        }
       }
       const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
       const float ll = logf(mo.l), nan = __int_as_float(0x7fc00000);
@@ -606,10 +600,7 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
       if (!parity) row_phase ^= 1;
     }
   }
-  if (a.splits > 1) {   // the finishers' two, for the cluster's one row
-    cluster_sync_all();
-    cluster_sync_all();
-  }
+  if (a.splits > 1) cluster_sync_all();   // the finishers' one, for the cluster's one row
 }
 
 // ---------------------------------------------------------------- gradient
