@@ -195,13 +195,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Two e4m3 codes (16 bits) to two f16, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
-      : "=r"(r)
+// Four e4m3 codes to two pairs of f16, exactly.
+__device__ __forceinline__ void e4m3x4_f16x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(codes));
-  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -530,10 +529,11 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t c = b[2 * kk + j];
+                uint32_t b0, b1;
+                e4m3x4_f16x2(b[2 * kk + j], b0, b1);
                 mma16816<FP8>(s[2 * u + j], qf[k + kk][0], PAIR ? 0u : qf[k + kk][1 % (PAIR ? 2 : 4)],
                               qf[k + kk][PAIR ? 1 : 2], PAIR ? 0u : qf[k + kk][3 % (PAIR ? 2 : 4)],
-                              e4m3x2_f16x2(c), e4m3x2_f16x2(c >> 16));
+                              b0, b1);
               }
           }
         }
@@ -649,16 +649,18 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             accumulate(o[2 * c], b[0], b[1]);
             accumulate(o[2 * c + 1], b[2], b[3]);
           } else if ((c & 1) == 0) {
-            // transposed as pairs of codes: a register holds dimensions 2r, 2r + 1 of keys
-            // 2t and 2t + 1; the even dimensions make one column group, the odd ones the next
+            // transposed as pairs of codes: a register holds dimensions 2r, 2r + 1 of key 2t
+            // and of key 2t + 1; with the middle two exchanged, the pair of keys of the even
+            // dimension and that of the odd one, which make two column groups
             uint32_t b[4];   // chunk c: keys 0-7, 8-15; chunk c + 1: the same
             ldsm4_t(b, vS + tile_off<C>(key0 + (((lane >> 3) & 1) << 3) + (lane & 7), c + (lane >> 4)));
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
-              const uint32_t x0 = e4m3x2_f16x2(b[2 * cc]), x1 = e4m3x2_f16x2(b[2 * cc] >> 16);
-              const uint32_t y0 = e4m3x2_f16x2(b[2 * cc + 1]), y1 = e4m3x2_f16x2(b[2 * cc + 1] >> 16);
-              accumulate(o[2 * (c + cc)], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
-              accumulate(o[2 * (c + cc) + 1], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+              uint32_t x0, x1, y0, y1;
+              e4m3x4_f16x2(__byte_perm(b[2 * cc], 0, 0x3120), x0, x1);
+              e4m3x4_f16x2(__byte_perm(b[2 * cc + 1], 0, 0x3120), y0, y1);
+              accumulate(o[2 * (c + cc)], x0, y0);
+              accumulate(o[2 * (c + cc) + 1], x1, y1);
             }
           }
         }
@@ -826,12 +828,18 @@ __global__ void __launch_bounds__(128, 2) cache_attention_f32_kernel(const Decod
       const float4* kp = reinterpret_cast<const float4*>((const float*)a.k + row0 * HD) + l8;
       const float4* vp = reinterpret_cast<const float4*>((const float*)a.v + row0 * HD) + l8;
       float s[4][ROWS];
-      float4 kv[4][CH];
+      float4 kk[4][CH], vv[4][CH];   // the values on their way with the keys
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-          kv[j][c] = key0 + 4 * j + sub < n ? __ldg(kp + j * HD + c * 8)
+          kk[j][c] = key0 + 4 * j + sub < n ? __ldg(kp + j * HD + c * 8)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          vv[j][c] = key0 + 4 * j + sub < n ? __ldg(vp + j * HD + c * 8)
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -840,10 +848,10 @@ __global__ void __launch_bounds__(128, 2) cache_attention_f32_kernel(const Decod
           float d = 0.f;
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
-            d = fmaf(q[i][c].x, kv[j][c].x, d);
-            d = fmaf(q[i][c].y, kv[j][c].y, d);
-            d = fmaf(q[i][c].z, kv[j][c].z, d);
-            d = fmaf(q[i][c].w, kv[j][c].w, d);
+            d = fmaf(q[i][c].x, kk[j][c].x, d);
+            d = fmaf(q[i][c].y, kk[j][c].y, d);
+            d = fmaf(q[i][c].z, kk[j][c].z, d);
+            d = fmaf(q[i][c].w, kk[j][c].w, d);
           }
           d += __shfl_xor_sync(0xffffffffu, d, 1);
           d += __shfl_xor_sync(0xffffffffu, d, 2);
@@ -851,12 +859,6 @@ __global__ void __launch_bounds__(128, 2) cache_attention_f32_kernel(const Decod
           s[j][i] = key0 + 4 * j + sub < n ? d * to_log2 : -INFINITY;
         }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-          kv[j][c] = key0 + 4 * j + sub < n ? __ldg(vp + j * HD + c * 8)
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {   // each eight lanes keep the softmax of their keys
         const float top = fmaxf(fmaxf(fmaxf(s[0][i], s[1][i]), fmaxf(s[2][i], s[3][i])), mx[i]);
@@ -877,10 +879,10 @@ __global__ void __launch_bounds__(128, 2) cache_attention_f32_kernel(const Decod
           sum[i] += p;
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
-            o[i][c].x = fmaf(p, kv[j][c].x, o[i][c].x);
-            o[i][c].y = fmaf(p, kv[j][c].y, o[i][c].y);
-            o[i][c].z = fmaf(p, kv[j][c].z, o[i][c].z);
-            o[i][c].w = fmaf(p, kv[j][c].w, o[i][c].w);
+            o[i][c].x = fmaf(p, vv[j][c].x, o[i][c].x);
+            o[i][c].y = fmaf(p, vv[j][c].y, o[i][c].y);
+            o[i][c].z = fmaf(p, vv[j][c].z, o[i][c].z);
+            o[i][c].w = fmaf(p, vv[j][c].w, o[i][c].w);
           }
         }
       }
