@@ -540,26 +540,40 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       }
       // ---- scaling and mask; running maximum
       float vs[2 * C::SUB][2], top[2] = {mx[0], mx[1]}, vtop = 0.f;
+      const float* sc = reinterpret_cast<const float*>(gbase + (sScale - base) + st * C::SC);
 #pragma unroll
       for (int j = 0; j < 2 * C::SUB; ++j) {
         const int key = ((j >> 1) * 4 + warp) * 16 + (j & 1) * 8 + 2 * t;
         float2 ks = make_float2(1.f, 1.f);
         if constexpr (FP8) {
-          const float* sc = reinterpret_cast<const float*>(gbase + (sScale - base) + st * C::SC);
           ks = *reinterpret_cast<const float2*>(sc + key);
           const float2 v2 = *reinterpret_cast<const float2*>(sc + KT + key);
-          vs[j][0] = key < info.valid ? v2.x : 0.f;
-          vs[j][1] = key + 1 < info.valid ? v2.y : 0.f;
-          vtop = fmaxf(vtop, fmaxf(vs[j][0], vs[j][1]));
+          vs[j][0] = v2.x;
+          vs[j][1] = v2.y;
         }
 #pragma unroll
         for (int i = 0; i < (PAIR ? 1 : 2); ++i) {
-          const float x = s[j][2 * i] * (FP8 ? q_mul[i] * ks.x : q_mul[i]);
-          const float y = s[j][2 * i + 1] * (FP8 ? q_mul[i] * ks.y : q_mul[i]);
-          s[j][2 * i] = key < info.valid ? x : -INFINITY;
-          s[j][2 * i + 1] = key + 1 < info.valid ? y : -INFINITY;
-          top[i] = fmaxf(top[i], fmaxf(s[j][2 * i], s[j][2 * i + 1]));
+          s[j][2 * i] *= FP8 ? q_mul[i] * ks.x : q_mul[i];
+          s[j][2 * i + 1] *= FP8 ? q_mul[i] * ks.y : q_mul[i];
         }
+      }
+      if (info.valid < KT) {   // slots past the length
+#pragma unroll
+        for (int j = 0; j < 2 * C::SUB; ++j) {
+          const int key = ((j >> 1) * 4 + warp) * 16 + (j & 1) * 8 + 2 * t;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (key + e >= info.valid) {
+              s[j][e] = s[j][2 + e] = -INFINITY;
+              vs[j][e] = 0.f;
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * C::SUB; ++j) {
+#pragma unroll
+        for (int i = 0; i < (PAIR ? 1 : 2); ++i) top[i] = fmaxf(top[i], fmaxf(s[j][2 * i], s[j][2 * i + 1]));
+        if constexpr (FP8) vtop = fmaxf(vtop, fmaxf(vs[j][0], vs[j][1]));
       }
       float keep[2], floor2[2];
 #pragma unroll
@@ -635,7 +649,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         }
         auto accumulate = [&](float (&c)[4], uint32_t b0, uint32_t b1) {
           if constexpr (PAIR) {
-            mma16816<FP8>(c, hi[0], lo[0], hi[2], lo[2], b0, b1);
+            mma16816<FP8>(c, hi[0], FP8 ? 0u : lo[0], hi[2], FP8 ? 0u : lo[2], b0, b1);
           } else {
             mma16816<FP8>(c, hi[0], hi[1], hi[2], hi[3], b0, b1);
             if (!FP8) mma16816<FP8>(c, lo[0], lo[1], lo[2], lo[3], b0, b1);
