@@ -218,17 +218,11 @@ __device__ __forceinline__ void append_part(const AppendArgs& a, const Turns& tu
     w.slot = a.slot[m_];
     w.pos = a.pos ? a.pos[m_] : w.slot;
   };
-  auto find_page = [&](Where& w) {   // the page of a row to append, -1: skip the row
+  auto find_page = [&](Where& w) {   // looked at an iteration later, when it has arrived
     w.page = -1;
-    if (w.seq < 0) return;
-    if (w.seq < c.n_seqs && w.slot >= 0 && w.slot < room)
+    if (w.seq >= 0 && w.seq < c.n_seqs && w.slot >= 0 && w.slot < room)
       w.page = c.table[(int64_t)w.seq * c.max_pages +
                        (a.page_shift >= 0 ? w.slot >> a.page_shift : w.slot / c.page_size)];
-    if (w.page >= c.n_pages) w.page = -1;
-    if (w.page < 0) {
-      report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-      w.page = -1;
-    }
   };
 
   pdl_trigger();
@@ -276,7 +270,9 @@ __device__ __forceinline__ void append_part(const AppendArgs& a, const Turns& tu
     find_page(w1);
     asm volatile("cp.async.wait_group 2;" ::: "memory");
     const Where now = w0;
-    if (now.page >= 0) {   // the same for the whole warp
+    const bool found = now.page >= 0 && now.page < c.n_pages;   // the same for the whole warp
+    if (now.seq >= 0 && !found) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+    if (now.seq >= 0 && found) {
       float2 cs[V / 2], sn[V / 2];
       if (a.rope) {
         float2 own[NJ];

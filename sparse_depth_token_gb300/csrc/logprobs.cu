@@ -423,15 +423,23 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
     int parity = 0;
     uint32_t phase = 0;
     bool met = false;   // the cluster's barrier is behind it
-    int next_target = a.logp && split == 0 && row0 < a.N ? a.target[row0] : -1;
+    // the target's logit is fetched a row ahead (and kept as it is stored until it is used),
+    // the target two rows ahead
+    const bool targets = a.logp && split == 0;
+    auto target_of = [&](int64_t r) { return targets && r < a.N ? a.target[r] : -1; };
+    auto logit_of = [&](int64_t r, int t) {
+      return t >= 0 && t < a.V ? ((const T*)a.logits + r * a.ld)[t] : Elem<T>::from_f(0.f);
+    };
+    int target_1 = target_of(row0), target_2 = target_of(row0 + row_step);
+    T x_1 = logit_of(row0, target_1);
     for (int64_t row = row0; row < a.N; row += row_step) {
       const Span s = span_of<T>(a, row, split);
       const int chunks = span_chunks(s), step = (chunks + kSlots - 1) / kSlots;
-      // the target's logit, on its way while the row is read; the next row's target too
-      const int target = next_target;
-      float x_t = 0.f;
-      if (target >= 0 && target < a.V) x_t = Elem<T>::to_f(((const T*)a.logits + row * a.ld)[target]);
-      if (a.logp && split == 0 && row + row_step < a.N) next_target = a.target[row + row_step];
+      const int target = target_1;
+      const T x_t = x_1;
+      target_1 = target_2;
+      x_1 = logit_of(row + row_step, target_1);
+      target_2 = target_of(row + 2 * row_step);
       if (!mbar_wait(bDone + 8 * parity, phase, abort_flag, a.status)) break;
       Moments mo = sh.moments[parity][lane % W];
       int found = 0;
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
         if (bad || target >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
         if (a.lse) a.lse[row] = bad ? nan : mo.m + ll;
         if (a.entropy) a.entropy[row] = bad ? nan : ll - 0.6931471805599453f * mo.u / mo.l;
-        if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (x_t - mo.m) - ll;
+        if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (Elem<T>::to_f(x_t) - mo.m) - ll;
       }
       for (int i = lane; i < k; i += 32) {
         const uint64_t key = sh.top[i];
