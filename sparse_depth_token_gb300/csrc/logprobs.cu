@@ -709,9 +709,12 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
   LogprobArgs a = a0;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // CTAs of a cluster share a row while there are SMs for them and 16 KB chunks enough
+  // CTAs of a cluster share a row while there are SMs for them, two 16 KB chunks for each, and
+  // not too many candidates to join (8 rows of 50257, bf16, one, two, four CTAs a row: without
+  // alternatives 6.3, 5.0, 4.5 us; 5 of them 8.9, 8.3, 8.1; 20 of them 10.6, 10.5, 11.5)
   a.splits = 1;
-  while (a.splits < 8 && a.N * a.splits * 2 <= sms && (int64_t)a.V * sizeof(T) >= 2 * a.splits * (int64_t)kChunk)
+  while (a.splits < 8 && a.N * a.splits * 2 <= sms && a.splits * 2 * a.top_k <= 48 &&
+         (int64_t)a.V * sizeof(T) >= 2 * a.splits * (int64_t)kChunk)
     a.splits *= 2;
   a.per = (a.V + a.splits - 1) / a.splits;
   constexpr int smem = kLpStages * kChunk + (int)sizeof(LpShared);
