@@ -33,7 +33,7 @@ using namespace tc;
 
 namespace {
 
-constexpr int kMaxCtas = 384;        // CTAs the workspace has room for
+constexpr int kMaxCtas = 512;        // CTAs the workspace has room for
 constexpr int kThreads = 160;        // 4 consumer warps, 1 producer warp
 constexpr int kConsumers = 4;
 
@@ -790,9 +790,12 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
 // reading of the keys (32 registers of q, 32 of output). The cache's tiles, ranges and joins
 // are the tensor-core kernel's.
 template <int HD> constexpr int f32_rows() { return 256 / HD; }
+// CTAs an SM: as many as the registers allow (24 rows of up to 1000 slots, 4 KV heads of 64:
+// two 12.0, three 11.4 us; 64 rows of up to 8192: 113, 95 us; heads of 128 spill at three).
+template <int HD> constexpr int f32_ctas() { return HD == 128 ? 2 : 3; }
 
 template <int HD>
-__global__ void __launch_bounds__(128, 2) cache_attention_f32_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(128, f32_ctas<HD>()) cache_attention_f32_kernel(const DecodeArgs a) {
   constexpr int KT = 64, ROWS = f32_rows<HD>(), CH = HD / 32;
   __shared__ Plan plan_s;
   __shared__ long long scratch[4];
@@ -1146,7 +1149,8 @@ int xmod_cache_attention(const xmod_dims* dm, const xmod_kv_cache* cache, int M,
   if (!fp32 && !tma_available()) return XMOD_ERR_UNSUPPORTED;
   const int sms = device_sms();
   if (sms <= 0) return XMOD_ERR_CUDA;
-  const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  const int per_sm = fp32 && dm->head_dim != 128 ? 3 : 2;   // f32_ctas, Cf: two
+  const int ctas = per_sm * sms < kMaxCtas ? per_sm * sms : kMaxCtas;
   const int rows = pass_rows(dm), group = dm->n_heads / dm->n_kv_heads;
   DecodeArgs a{};
   a.M = M;
