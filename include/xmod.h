@@ -470,8 +470,8 @@ XMOD_API size_t xmod_cache_attention_workspace_bytes(const xmod_dims* dims, int 
  *   o       [M, n_heads * head_dim] (dtype)
  *   lse     [M, n_heads] fp32: ln sum_i exp(q . K_i / sqrt(head_dim)), or NULL
  * Slots at or after len[m] have no influence, whatever their pages hold. Products are
- * accumulated in fp32; the probabilities keep at least 16 bits of mantissa (11 with E4M3
- * and more than 8 query heads per KV head) where they weight the values.
+ * accumulated in fp32; the probabilities keep at least 16 bits of mantissa (11 with E4M3)
+ * where they weight the values.
  * Device checks (status word of ws): a sequence not below n_seqs skips its row; a len
  * outside its range is clamped into it; a page outside [0, n_pages) is read as page 0.
  * The result does not depend on the other rows of the call beyond fp32 rounding, and two
@@ -495,8 +495,8 @@ XMOD_API int xmod_cache_attention(const xmod_dims* dims, const xmod_kv_cache* ca
  * Checked on the device and reported through status_out (a device int, or NULL; see
  * xmod_gather): a target not below V gives a NaN logp; a row that holds a NaN or
  * +infinity, or nothing above -infinity, has no distribution: its lse, logp, entropy and
- * top_logp are NaN (its top_idx rank a NaN above +infinity). logits and the outputs must be
- * 16-byte aligned, rows need not be. N = 0 does nothing. */
+ * top_logp are NaN (its top_idx rank a NaN above +infinity). Pointers need only their
+ * elements' alignment (rows of an odd V begin anywhere). N = 0 does nothing. */
 #define XMOD_MAX_TOP_K 64
 
 XMOD_API int xmod_token_logprobs(xmod_dtype dtype, int64_t N, int V, const void* logits,
@@ -513,7 +513,8 @@ XMOD_API int xmod_token_logprobs(xmod_dtype dtype, int64_t N, int V, const void*
  *   dlogits    [N, V] (dtype), row stride ldd >= V; may be logits itself (ldd = ld), else
  *              must not overlap it. Columns from V to ldd are not written.
  * A row whose two gradients are zero (or absent) gets zeros, whatever its logits. A
- * target not below V counts as negative and is reported through status_out. */
+ * target not below V counts as negative and is reported through status_out. Alignment as
+ * for xmod_token_logprobs. */
 XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const void* logits,
                                      int64_t ld, const int32_t* target, const float* lse,
                                      const float* entropy, const float* g_logp,

@@ -132,7 +132,7 @@ struct Moments {
   // to a maximum at or above its own
   __device__ __forceinline__ void raise(float m2) {
     const float d = (m - m2) * kLog2e, f = ex2(d);
-    u = l > 0.f ? f * fmaf(d, l, u) : 0.f;
+    u = f > 0.f ? f * fmaf(d, l, u) : 0.f;   // d may be infinite where f is 0
     l *= f;
     m = m2;
   }
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
           if (!(top <= mo.m)) {   // larger, or a NaN: that one makes l 0 and the row bad
             const float d = (mo.m - (top != top ? INFINITY : top)) * kLog2e, f = ex2(d);
             const float2 f2 = make_float2(f, f), d2 = make_float2(d, d);
-            if (ENT) u2 = l2.x + l2.y > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
+            if (ENT) u2 = f > 0.f ? mul2(f2, fma2(d2, l2, u2)) : make_float2(0.f, 0.f);
             l2 = mul2(l2, f2);
             mo.m = top != top ? INFINITY : top;
           }
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
                 if (ENT) u2 = fma2(e, t, u2);
               }
             }
-          } else if (mo.m > -FLT_MAX) {   // differences that could overflow
+          } else if (top > -INFINITY) {   // differences that could overflow
 #pragma unroll
             for (int i = 0; i < N * VE; ++i) {
               const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
@@ -701,7 +701,10 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const L
 
 // ---------------------------------------------------------------- host
 
-bool ptr16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
+// Logits: any element of an array (vector accesses stay inside its aligned 16 bytes).
+bool elem_ptr(const void* p, xmod_dtype dt) {
+  return p && ((uintptr_t)p & (dt == XMOD_BF16 ? 1u : 3u)) == 0;
+}
 bool ptr4_or_null(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 template <typename T, bool ENT>
@@ -769,7 +772,7 @@ int xmod_token_logprobs(xmod_dtype dt, int64_t N, int V, const void* logits, int
       (target != nullptr) != (logp != nullptr))
     return XMOD_ERR_INVALID_ARG;
   if (N == 0) return XMOD_OK;
-  if (!ptr16(logits)) return XMOD_ERR_INVALID_ARG;
+  if (!elem_ptr(logits, dt)) return XMOD_ERR_INVALID_ARG;
   const void* ps[] = {target, logp, entropy, lse, top_idx, top_logp, status_out};
   for (const void* p : ps)
     if (!ptr4_or_null(p)) return XMOD_ERR_INVALID_ARG;
@@ -793,7 +796,7 @@ int xmod_token_logprobs_bwd(xmod_dtype dt, int64_t N, int V, const void* logits,
   if ((dt != XMOD_BF16 && dt != XMOD_FP32) || N < 0 || V <= 0 || ld < V || ldd < V)
     return XMOD_ERR_INVALID_ARG;
   if (N == 0) return XMOD_OK;
-  if (!ptr16(logits) || !ptr16(dlogits) || !lse || (g_logp && !target) ||
+  if (!elem_ptr(logits, dt) || !elem_ptr(dlogits, dt) || !lse || (g_logp && !target) ||
       (g_entropy && !entropy) || (dlogits == logits && ldd != ld))
     return XMOD_ERR_INVALID_ARG;
   const void* ps[] = {target, lse, entropy, g_logp, g_entropy, status_out};

@@ -391,7 +391,8 @@ def kv_cache(k, v, table, k_scale=None, v_scale=None) -> KVCache:
     T = _torch()
     e4m3 = k_scale is not None
     ts = (k, v, table) + ((k_scale, v_scale) if e4m3 else ())
-    if (any(t is None or not t.is_cuda or not t.is_contiguous() for t in ts) or k.dim() != 4
+    if (any(t is None or not t.is_cuda or t.device != k.device or not t.is_contiguous()
+            for t in ts) or k.dim() != 4
             or table.dim() != 2 or k.shape != v.shape or k.dtype is not v.dtype
             or table.dtype is not T.int32 or (v_scale is not None) != e4m3
             or (e4m3 and (k.element_size() != 1 or any(
@@ -400,31 +401,39 @@ def kv_cache(k, v, table, k_scale=None, v_scale=None) -> KVCache:
     c = KVCache(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(table), k.shape[0], k.shape[2],
                 table.shape[0], table.shape[1], CACHE_E4M3 if e4m3 else CACHE_NATIVE)
     c._keep = ts
-    c.n_kv_heads, c.head_dim, c.dtype = k.shape[1], k.shape[3], k.dtype
+    c.n_kv_heads, c.head_dim, c.dtype, c.device = k.shape[1], k.shape[3], k.dtype, k.get_device()
     return c
 
 
-def _vec(fn, t, dtype, n):
-    """Device pointer of an optional contiguous tensor of n elements of that dtype."""
+def _device(fn, t):
+    """Device index of a tensor; it has to be the current device."""
+    dev = t.get_device()
+    if dev < 0 or dev != _torch()._C._cuda_getDevice():
+        raise XmodError(fn, ERR_INVALID_ARG)
+    return dev
+
+
+def _vec(fn, t, dtype, n, dev):
+    """Pointer of an optional contiguous tensor of n elements of that dtype on device dev."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
         raise XmodError(fn, ERR_INVALID_ARG)
     return t.data_ptr()
 
 
-def _mat(fn, t, dtype, rows, width):
-    """(device pointer, row stride) of a [rows, width] tensor with contiguous rows."""
-    if (t.dtype is not dtype or not t.is_cuda or t.shape != (rows, width)
+def _mat(fn, t, dtype, rows, width, dev):
+    """(pointer, row stride) of a [rows, width] tensor with contiguous rows on device dev."""
+    if (t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, width)
             or (width > 1 and t.stride(1) != 1)):
         raise XmodError(fn, ERR_INVALID_ARG)
     return t.data_ptr(), t.stride(0) if rows > 1 else width
 
 
-def _elem(fn, dm, cache):
-    """torch dtype of the dims' elements; the cache has to be of these dims."""
+def _elem(fn, dm, cache, dev):
+    """torch dtype of the dims' elements; the cache has to be of these dims and there."""
     el = _torch().bfloat16 if dm.dtype == BF16 else _torch().float32
-    if (cache.n_kv_heads != dm.n_kv_heads or cache.head_dim != dm.head_dim
+    if (cache.n_kv_heads != dm.n_kv_heads or cache.head_dim != dm.head_dim or cache.device != dev
             or (cache.format == CACHE_NATIVE and cache.dtype is not el)):
         raise XmodError(fn, ERR_INVALID_ARG)
     return el
@@ -436,17 +445,21 @@ def cache_append(dm, cache: KVCache, qkv, w, seq, slot, pos=None, q_out=None, st
     cache, their transformed q into q_out (None: not wanted). w: a LayerWeights (its QK-norm
     gains and rope_theta count) or None. status: as for gather."""
     fn = "xmod_cache_append"
-    M = qkv.shape[0]
-    el = _elem(fn, dm, cache)
+    M, dev = qkv.shape[0], _device(fn, qkv)
+    el = _elem(fn, dm, cache, dev)
     i32 = _torch().int32
     qw = dm.n_heads * dm.head_dim
-    qkv_p, ld = _mat(fn, qkv, el, M, qw + 2 * dm.n_kv_heads * dm.head_dim)
-    q_p, ldq = _mat(fn, q_out, el, M, qw) if q_out is not None else (None, 0)
+    qkv_p, ld = _mat(fn, qkv, el, M, qw + 2 * dm.n_kv_heads * dm.head_dim, dev)
+    q_p, ldq = _mat(fn, q_out, el, M, qw, dev) if q_out is not None else (None, 0)
+    if w is not None:
+        keep = getattr(w, "_keep", {})
+        _vec(fn, keep.get("q_norm"), el, dm.head_dim, dev)
+        _vec(fn, keep.get("k_norm"), el, dm.head_dim, dev)
     st = load().xmod_cache_append(
         ctypes.byref(dm), ctypes.byref(cache), M, qkv_p, ld,
-        ctypes.byref(w) if w is not None else None, _vec(fn, seq, i32, M),
-        _vec(fn, slot, i32, M), _vec(fn, pos, i32, M), q_p, ldq, _vec(fn, status, i32, 1),
-        _stream(stream))
+        ctypes.byref(w) if w is not None else None, _vec(fn, seq, i32, M, dev),
+        _vec(fn, slot, i32, M, dev), _vec(fn, pos, i32, M, dev), q_p, ldq,
+        _vec(fn, status, i32, 1, dev), _stream(stream))
     if st:
         raise XmodError(fn, st)
 
@@ -459,27 +472,29 @@ def cache_attention(dm, cache: KVCache, q, seq, lens, o, ws, lse=None, stream=No
     """xmod_cache_attention: o [M, n_heads head_dim] (and lse [M, n_heads] fp32) of the
     queries q over the first lens[m] slots of sequence seq[m] (None: m)."""
     fn = "xmod_cache_attention"
-    M = q.shape[0]
-    el = _elem(fn, dm, cache)
+    M, dev = q.shape[0], _device(fn, q)
+    el = _elem(fn, dm, cache, dev)
     t = _torch()
     qw = dm.n_heads * dm.head_dim
-    q_p, ldq = _mat(fn, q, el, M, qw)
+    q_p, ldq = _mat(fn, q, el, M, qw, dev)
     st = load().xmod_cache_attention(
-        ctypes.byref(dm), ctypes.byref(cache), M, q_p, ldq, _vec(fn, seq, t.int32, M),
-        _vec(fn, lens, t.int32, M), _vec(fn, o, el, M * qw),
-        _vec(fn, lse, t.float32, M * dm.n_heads), ws.data_ptr(), ws.numel() * ws.element_size(),
-        _stream(stream))
+        ctypes.byref(dm), ctypes.byref(cache), M, q_p, ldq, _vec(fn, seq, t.int32, M, dev),
+        _vec(fn, lens, t.int32, M, dev), _vec(fn, o, el, M * qw, dev),
+        _vec(fn, lse, t.float32, M * dm.n_heads, dev),
+        _vec(fn, ws, ws.dtype, ws.numel(), dev), ws.numel() * ws.element_size(), _stream(stream))
     if st:
         raise XmodError(fn, st)
 
 
-def _logits_dtype(fn, t):
+def _logits(fn, t):
+    """(dtype code, rows, width, pointer, row stride, device) of logits."""
     T = _torch()
-    if t.dtype is T.bfloat16:
-        return BF16
-    if t.dtype is T.float32:
-        return FP32
-    raise XmodError(fn, ERR_INVALID_ARG)
+    dt = BF16 if t.dtype is T.bfloat16 else FP32 if t.dtype is T.float32 else None
+    if dt is None or t.dim() != 2:
+        raise XmodError(fn, ERR_INVALID_ARG)
+    N, V = t.shape
+    dev = _device(fn, t)
+    return (dt, N, V) + _mat(fn, t, t.dtype, N, V, dev) + (dev,)
 
 
 def token_logprobs(logits, target=None, logp=None, entropy=None, lse=None, top_idx=None,
@@ -488,15 +503,14 @@ def token_logprobs(logits, target=None, logp=None, entropy=None, lse=None, top_i
     that are given are written (logp, entropy, lse [N] fp32, top_idx int32 and top_logp
     fp32 [N, k])."""
     fn = "xmod_token_logprobs"
-    N, V = logits.shape
+    dt, N, V, x, ld, dev = _logits(fn, logits)
     k = top_idx.shape[1] if top_idx is not None else 0
-    dt = _logits_dtype(fn, logits)
     i32, f32 = _torch().int32, _torch().float32
-    x, ld = _mat(fn, logits, logits.dtype, N, V)
     st = load().xmod_token_logprobs(
-        dt, N, V, x, ld, _vec(fn, target, i32, N), _vec(fn, logp, f32, N),
-        _vec(fn, entropy, f32, N), _vec(fn, lse, f32, N), k, _vec(fn, top_idx, i32, N * k),
-        _vec(fn, top_logp, f32, N * k), _vec(fn, status, i32, 1), _stream(stream))
+        dt, N, V, x, ld, _vec(fn, target, i32, N, dev), _vec(fn, logp, f32, N, dev),
+        _vec(fn, entropy, f32, N, dev), _vec(fn, lse, f32, N, dev), k,
+        _vec(fn, top_idx, i32, N * k, dev), _vec(fn, top_logp, f32, N * k, dev),
+        _vec(fn, status, i32, 1, dev), _stream(stream))
     if st:
         raise XmodError(fn, st)
 
@@ -506,15 +520,13 @@ def token_logprobs_bwd(logits, target, lse, g_logp, dlogits, entropy=None, g_ent
     """xmod_token_logprobs_bwd: dlogits [N, V] of the gradients g_logp and g_entropy [N]
     (either may be None); dlogits may be logits itself."""
     fn = "xmod_token_logprobs_bwd"
-    N, V = logits.shape
-    dt = _logits_dtype(fn, logits)
+    dt, N, V, x, ld, dev = _logits(fn, logits)
     i32, f32 = _torch().int32, _torch().float32
-    x, ld = _mat(fn, logits, logits.dtype, N, V)
-    d, ldd = _mat(fn, dlogits, logits.dtype, N, V)
+    d, ldd = _mat(fn, dlogits, logits.dtype, N, V, dev)
     st = load().xmod_token_logprobs_bwd(
-        dt, N, V, x, ld, _vec(fn, target, i32, N), _vec(fn, lse, f32, N),
-        _vec(fn, entropy, f32, N), _vec(fn, g_logp, f32, N), _vec(fn, g_entropy, f32, N), d, ldd,
-        _vec(fn, status, i32, 1), _stream(stream))
+        dt, N, V, x, ld, _vec(fn, target, i32, N, dev), _vec(fn, lse, f32, N, dev),
+        _vec(fn, entropy, f32, N, dev), _vec(fn, g_logp, f32, N, dev),
+        _vec(fn, g_entropy, f32, N, dev), d, ldd, _vec(fn, status, i32, 1, dev), _stream(stream))
     if st:
         raise XmodError(fn, st)
 

@@ -479,3 +479,90 @@ def test_token_by_token_equals_the_threshold_layer(X):
     ref = from_dev(full, "bf16")
     # both sides round their stream once: half a spacing each, as for a stored output
     U.assert_close(got.reshape(ref.shape), ref, "bf16", "y", stored_ref=2 * ref)
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_attention_of_many_short_rows(X, kind):
+    """More rows than a CTA plans at once, short and empty ones, some skipped."""
+    M = 4100
+    lens = [(m * 7) % 23 for m in range(M)]
+    seq = [m if m % 11 else -1 for m in range(M)]
+    c, q, o, lse, ws, call = _attention(X, kind, 4, 2, 64, 16, lens, seq)
+    call()
+    assert X.sync_status(ws) == X.OK
+    sample = list(range(0, 40)) + list(range(40, M, 97)) + [M - 1]
+    _check_attention(c, kind, q[sample], [seq[m] for m in sample], [lens[m] for m in sample], o[sample], lse[sample],
+                     4, 64)
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_two_streams_at_once(X, kind):
+    """Attention of two caches on two streams at the same time, each with its workspace,
+    while a third appends: the same bits as one after the other."""
+    a = _attention(X, kind, 12, 4, 128, 16, [3000, 5, 900, 64], seed=3)
+    b = _attention(X, kind, 16, 1, 64, 32, [77, 2500, 1, 0, 640], seed=4)
+    for s in (a, b):
+        s[5]()
+    torch.cuda.synchronize()
+    want = [(s[2].clone(), s[3].clone()) for s in (a, b)]
+    dtype, c, qkv, seq, slot, pos, gains, w = _append_case(X, kind, 12, 4, 128, 16, 200, True, THETA)
+    q_out = torch.empty(200, 12 * 128, dtype=C.DT[dtype], device="cuda")
+    dm = C.dims(X, 12, 4, 128, dtype)
+    seq_t, slot_t = ints(seq.tolist()), ints(slot.tolist())
+    X.cache_append(dm, c.handle, qkv, w, seq_t, slot_t, pos, q_out)
+    held = [t.clone() for t in c.tensors()] + [q_out.clone()]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                s[5]()
+        with torch.cuda.stream(streams[2]):
+            X.cache_append(dm, c.handle, qkv, w, seq_t, slot_t, pos, q_out)
+    torch.cuda.synchronize()
+    for s, (o, lse) in zip((a, b), want):
+        assert torch.equal(s[2], o) and torch.equal(s[3], lse)
+    for t, h in zip(c.tensors() + [q_out], held):
+        assert torch.equal(t.view(torch.uint8), h.view(torch.uint8))
+
+
+def test_binding_refusals(X):
+    """Types, shapes, layouts and caches that do not belong together are refused."""
+    hq, hkv, hd, M = 4, 2, 64, 3
+    dm = C.dims(X, hq, hkv, hd, "bf16")
+    c = C.Cache(X, [16] * M, hkv, hd, 16, "bf16")
+    qkv = torch.zeros(M, (hq + 2 * hkv) * hd, dtype=torch.bfloat16, device="cuda")
+    q, o = torch.zeros(M, hq * hd, dtype=torch.bfloat16, device="cuda"), torch.zeros(M, hq * hd, dtype=torch.bfloat16, device="cuda")
+    i, ws = ints([1] * M), torch.zeros(X.cache_attention_workspace_bytes(dm, M), dtype=torch.uint8, device="cuda")
+    w32 = X.layer_weights({"q_norm": torch.ones(hd, device="cuda")})
+    odd = torch.zeros(M, (hq + 2 * hkv) * hd + 4, dtype=torch.bfloat16, device="cuda")
+    other = C.dims(X, hq, hkv, 32, "bf16")
+    bad = [lambda: X.cache_append(dm, c.handle, qkv.float(), None, None, i),
+           lambda: X.cache_append(dm, c.handle, qkv[:, :-8], None, None, i),
+           lambda: X.cache_append(dm, c.handle, odd[:, 4:], None, None, i),
+           lambda: X.cache_append(dm, c.handle, odd[:, :-4], None, None, i),
+           lambda: X.cache_append(dm, c.handle, qkv, None, None, i.long()),
+           lambda: X.cache_append(dm, c.handle, qkv, None, None, i[:2]),
+           lambda: X.cache_append(dm, c.handle, qkv, None, None, None),
+           lambda: X.cache_append(dm, c.handle, qkv, None, i.cpu(), i),
+           lambda: X.cache_append(dm, c.handle, qkv, w32, None, i),
+           lambda: X.cache_append(dm, c.handle, qkv, None, None, i, None, q[:2]),
+           lambda: X.cache_append(other, c.handle, qkv, None, None, i),
+           lambda: X.cache_append(C.dims(X, hq, hkv, hd, "fp32"), c.handle, qkv.float(), None, None, i),
+           lambda: X.cache_attention(dm, c.handle, q, None, i, o.float(), ws),
+           lambda: X.cache_attention(dm, c.handle, q, None, i.float(), o, ws),
+           lambda: X.cache_attention(dm, c.handle, q, None, None, o, ws),
+           lambda: X.cache_attention(dm, c.handle, q.t(), None, i, o, ws),
+           lambda: X.cache_attention(dm, c.handle, q, None, i, o, ws.cpu()),
+           lambda: X.cache_attention(dm, c.handle, q, None, i, o, ws, lse=torch.zeros(M, device="cuda")),
+           lambda: X.kv_cache(c.k, c.v.float(), c.table), lambda: X.kv_cache(c.k, c.v, c.table.long()),
+           lambda: X.kv_cache(c.k.transpose(1, 2), c.v.transpose(1, 2), c.table),
+           lambda: X.kv_cache(c.k, c.v, c.table, torch.zeros(1, device="cuda")),
+           lambda: X.kv_cache(c.k, c.v, c.table, None, torch.zeros(1, device="cuda"))]
+    for n, call in enumerate(bad):
+        with pytest.raises(X.XmodError) as e:
+            call()
+        assert e.value.status == X.ERR_INVALID_ARG, n
+    with pytest.raises(X.XmodError) as e:
+        X.cache_attention(dm, c.handle, q, None, i, o, ws[:256])
+    assert e.value.status == X.ERR_WORKSPACE

@@ -343,3 +343,92 @@ def test_loss_gradient_chains_into_a_layer(X):
         # fp32 losses of 16 tokens near 6: 16 * 6 * 2^-20 over 2 eps = 6e-3; third order
         # below eps^2 |v|^3 ~ 6e-5 * 16; both on a derivative of order |dx| |v| ~ 1
         assert abs(num - ana) <= 6e-3 + 1e-3 + 1e-2 * abs(ana)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("first_row,first_token", [(1, 0), (3, 5), (2, 1)])
+def test_slices_that_begin_anywhere(X, dtype, first_row, first_token):
+    """Rows and tokens cut out of a larger array of odd rows: bases and rows at any element,
+    forward, gradient and gradient in place."""
+    full, _ = _logits(9, 5003, dtype, 0, 31)
+    x = full[first_row:, first_token:]
+    N, V = x.shape
+    t = torch.randint(0, V, (N,), generator=torch.Generator().manual_seed(7)).to(torch.int32).cuda()
+    small = x.contiguous()
+    out = _forward(X, x, t, 9)
+    _check(small, t, out, 9)
+    g = torch.randn(N, generator=torch.Generator().manual_seed(8)).cuda()
+    d = torch.empty_like(small)
+    X.token_logprobs_bwd(small, t, out["lse"], g, d, entropy=out["entropy"], g_entropy=g)
+    wide = torch.full((9, 5010), -3.0, dtype=x.dtype, device="cuda")
+    part = wide[first_row:, 7:7 + V]
+    X.token_logprobs_bwd(x, t, out["lse"], g, part, entropy=out["entropy"], g_entropy=g)
+    assert torch.equal(part.contiguous(), d)
+    part.fill_(-3.0)
+    assert bool((wide == -3).all()), "a value outside the slice changed"
+    before = full.clone()
+    X.token_logprobs_bwd(x, t, out["lse"], g, x, entropy=out["entropy"], g_entropy=g)
+    assert torch.equal(x.contiguous(), d)
+    x.copy_(before[first_row:, first_token:])
+    assert torch.equal(full, before), "a value outside the slice changed"
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("N,V", [(2, 50257), (700, 5000), (3, 131)])
+@pytest.mark.parametrize("mask", ["inf", "lowest"])
+def test_few_allowed_tokens(X, dtype, N, V, mask):
+    """A grammar that leaves fewer tokens than alternatives are asked for: the rest are ruled
+    out tokens in order, at -infinity or at the type's lowest value."""
+    low = -math.inf if mask == "inf" else torch.finfo(DT[dtype]).min
+    gen = torch.Generator().manual_seed(V)
+    x = torch.full((N, V), low, dtype=DT[dtype], device="cuda")
+    t = torch.randint(0, V, (N,), generator=gen).cuda()
+    for i in range(3):
+        at = torch.randint(0, V, (N,), generator=gen).cuda()
+        x[torch.arange(N, device="cuda"), at] = 1.0 + i
+    x[torch.arange(N, device="cuda"), t] = 0.5
+    out = _forward(X, x, t.to(torch.int32), 20)
+    d = x.double()
+    idx = torch.sort(d, dim=1, descending=True, stable=True).indices[:, :20]
+    assert torch.equal(out["top_idx"].long(), idx)
+    lp = torch.log_softmax(d, 1)
+    assert bool(((out["logp"].double() - lp.gather(1, t[:, None])[:, 0]).abs() <= 2.0 ** -18).all())
+    assert bool(((out["entropy"].double() - torch.special.entr(lp.exp()).sum(1)).abs() <= 2.0 ** -18).all())
+    want = lp.gather(1, idx)
+    live = want > -1e30
+    assert bool(((out["top_logp"].double() - want).abs()[live] <= 2.0 ** -18).all())
+    assert bool((out["top_logp"][~live] < -1e30).all())
+
+
+def test_all_tokens_at_the_lowest_value(X):
+    """Finite logits, however low, are a distribution: the uniform one."""
+    for dtype, t in DT.items():
+        x = torch.full((2, 3000), torch.finfo(t).min, dtype=t, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = _forward(X, x, torch.zeros(2, dtype=torch.int32, device="cuda"), 4, status=status)
+        assert int(status) == 0
+        assert out["top_idx"].tolist() == [[0, 1, 2, 3]] * 2
+        assert bool(((out["entropy"] - math.log(3000)).abs() < 1e-5).all())
+        assert bool(((out["logp"] + math.log(3000)).abs() < 1e-5).all())
+
+
+def test_binding_refusals(X):
+    """Types, shapes and layouts that the call cannot take are refused by the binding."""
+    x, t = _logits(4, 50, "bf16")
+    f = torch.empty(4, device="cuda")
+    idx, lp = torch.empty(4, 3, dtype=torch.int32, device="cuda"), torch.empty(4, 3, device="cuda")
+    bad = [lambda: X.token_logprobs(x.double(), None, lse=f), lambda: X.token_logprobs(x.half(), None, lse=f),
+           lambda: X.token_logprobs(x.t(), None, lse=f), lambda: X.token_logprobs(x[0], None, lse=f),
+           lambda: X.token_logprobs(x[:1].expand(4, 50), None, lse=f),
+           lambda: X.token_logprobs(x, t.long(), logp=f), lambda: X.token_logprobs(x, t, logp=f[:3]),
+           lambda: X.token_logprobs(x, t.cpu(), logp=f), lambda: X.token_logprobs(x, t, logp=f.double()),
+           lambda: X.token_logprobs(x, t), lambda: X.token_logprobs(x, None, logp=f),
+           lambda: X.token_logprobs(x, None, top_idx=idx), lambda: X.token_logprobs(x, None, top_idx=idx, top_logp=lp[:, :2]),
+           lambda: X.token_logprobs(x, None, lse=f, status=f),
+           lambda: X.token_logprobs_bwd(x, t, f, f, x.float()), lambda: X.token_logprobs_bwd(x, None, f, f, x),
+           lambda: X.token_logprobs_bwd(x, t, f, f, x, g_entropy=f),
+           lambda: X.token_logprobs_bwd(x, t, f[:2], f, x)]
+    for i, call in enumerate(bad):
+        with pytest.raises(X.XmodError) as e:
+            call()
+        assert e.value.status == X.ERR_INVALID_ARG, i

@@ -92,7 +92,7 @@ def _logprobs_bwd(dt=X.BF16, N=3, V=100, x=FAKE, ld=100, t=FAKE, lse=FAKE, h=FAK
 
 
 def test_logprob_arguments():
-    for bad in (dict(dt=5), dict(N=-1), dict(V=0), dict(ld=99), dict(x=None), dict(x=FAKE + 8), dict(k=-1),
+    for bad in (dict(dt=5), dict(N=-1), dict(V=0), dict(ld=99), dict(x=None), dict(x=FAKE + 1), dict(k=-1),
                 dict(k=101), dict(k=0), dict(ti=None), dict(tl=None), dict(t=None), dict(lp=None), dict(lp=FAKE + 2),
                 dict(h=FAKE + 1), dict(st=FAKE + 2)):
         assert _logprobs(**bad) == X.ERR_INVALID_ARG, bad
@@ -101,8 +101,8 @@ def test_logprob_arguments():
 
 
 def test_logprob_gradient_arguments():
-    for bad in (dict(dt=5), dict(N=-1), dict(V=0), dict(ld=99), dict(ldd=99), dict(x=None), dict(x=FAKE + 8),
-                dict(d=None), dict(d=FAKE + 4), dict(lse=None), dict(t=None), dict(h=None), dict(g=FAKE + 2),
+    for bad in (dict(dt=5), dict(N=-1), dict(V=0), dict(ld=99), dict(ldd=99), dict(x=None), dict(x=FAKE + 1),
+                dict(d=None), dict(d=FAKE + 3), dict(dt=X.FP32, x=FAKE + 2), dict(lse=None), dict(t=None), dict(h=None), dict(g=FAKE + 2),
                 dict(d=FAKE, ldd=128), dict(st=FAKE + 1)):
         assert _logprobs_bwd(**bad) == X.ERR_INVALID_ARG, bad
     assert _logprobs_bwd(N=0) == X.OK
