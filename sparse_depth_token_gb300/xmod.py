@@ -191,10 +191,17 @@ def _torch():
     return _torch_module
 
 
+def _raw_stream(stream, dev):
+    """A stream's handle; None: the current one's (a Stream object costs as much to build as
+    a kernel to launch)."""
+    if stream is None:
+        return _torch_module._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
 def _stream(stream):
-    if stream is None:   # the raw handle: a Stream object costs as much as a launch
-        c = _torch()._C
-        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    if stream is None:
+        return _torch().cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -225,6 +232,8 @@ def layer_weights(tensors: dict, varsigma: float = 1.0, rope_theta: float = 0.0)
     lw = LayerWeights(*[_p(tensors.get(n)) for n in LayerWeights.NAMES], float(varsigma),
                       _p(tensors.get("q_norm")), _p(tensors.get("k_norm")), float(rope_theta))
     lw._keep = dict(tensors)
+    lw._gains = [(t.dtype, t.numel(), t.get_device())
+                 for t in (tensors.get("q_norm"), tensors.get("k_norm")) if hasattr(t, "dtype")]
     return lw
 
 
@@ -408,7 +417,7 @@ def kv_cache(k, v, table, k_scale=None, v_scale=None) -> KVCache:
 def _device(fn, t):
     """Device index of a tensor; it has to be the current device."""
     dev = t.get_device()
-    if dev < 0 or dev != _torch()._C._cuda_getDevice():
+    if dev < 0 or dev != (_torch_module or _torch())._C._cuda_getDevice():
         raise XmodError(fn, ERR_INVALID_ARG)
     return dev
 
@@ -432,7 +441,7 @@ def _mat(fn, t, dtype, rows, width, dev):
 
 def _elem(fn, dm, cache, dev):
     """torch dtype of the dims' elements; the cache has to be of these dims and there."""
-    el = _torch().bfloat16 if dm.dtype == BF16 else _torch().float32
+    el = _torch_module.bfloat16 if dm.dtype == BF16 else _torch_module.float32
     if (cache.n_kv_heads != dm.n_kv_heads or cache.head_dim != dm.head_dim or cache.device != dev
             or (cache.format == CACHE_NATIVE and cache.dtype is not el)):
         raise XmodError(fn, ERR_INVALID_ARG)
@@ -446,20 +455,17 @@ def cache_append(dm, cache: KVCache, qkv, w, seq, slot, pos=None, q_out=None, st
     gains and rope_theta count) or None. status: as for gather."""
     fn = "xmod_cache_append"
     M, dev = qkv.shape[0], _device(fn, qkv)
-    el = _elem(fn, dm, cache, dev)
-    i32 = _torch().int32
+    el, i32 = _elem(fn, dm, cache, dev), _torch_module.int32
     qw = dm.n_heads * dm.head_dim
     qkv_p, ld = _mat(fn, qkv, el, M, qw + 2 * dm.n_kv_heads * dm.head_dim, dev)
     q_p, ldq = _mat(fn, q_out, el, M, qw, dev) if q_out is not None else (None, 0)
-    if w is not None:
-        keep = getattr(w, "_keep", {})
-        _vec(fn, keep.get("q_norm"), el, dm.head_dim, dev)
-        _vec(fn, keep.get("k_norm"), el, dm.head_dim, dev)
+    for g in getattr(w, "_gains", ()):
+        if g != (el, dm.head_dim, dev):
+            raise XmodError(fn, ERR_INVALID_ARG)
     st = load().xmod_cache_append(
-        ctypes.byref(dm), ctypes.byref(cache), M, qkv_p, ld,
-        ctypes.byref(w) if w is not None else None, _vec(fn, seq, i32, M, dev),
-        _vec(fn, slot, i32, M, dev), _vec(fn, pos, i32, M, dev), q_p, ldq,
-        _vec(fn, status, i32, 1, dev), _stream(stream))
+        dm, cache, M, qkv_p, ld, w, _vec(fn, seq, i32, M, dev), _vec(fn, slot, i32, M, dev),
+        _vec(fn, pos, i32, M, dev), q_p, ldq, _vec(fn, status, i32, 1, dev),
+        _raw_stream(stream, dev))
     if st:
         raise XmodError(fn, st)
 
@@ -473,15 +479,14 @@ def cache_attention(dm, cache: KVCache, q, seq, lens, o, ws, lse=None, stream=No
     queries q over the first lens[m] slots of sequence seq[m] (None: m)."""
     fn = "xmod_cache_attention"
     M, dev = q.shape[0], _device(fn, q)
-    el = _elem(fn, dm, cache, dev)
-    t = _torch()
+    el, i32 = _elem(fn, dm, cache, dev), _torch_module.int32
     qw = dm.n_heads * dm.head_dim
     q_p, ldq = _mat(fn, q, el, M, qw, dev)
     st = load().xmod_cache_attention(
-        ctypes.byref(dm), ctypes.byref(cache), M, q_p, ldq, _vec(fn, seq, t.int32, M, dev),
-        _vec(fn, lens, t.int32, M, dev), _vec(fn, o, el, M * qw, dev),
-        _vec(fn, lse, t.float32, M * dm.n_heads, dev),
-        _vec(fn, ws, ws.dtype, ws.numel(), dev), ws.numel() * ws.element_size(), _stream(stream))
+        dm, cache, M, q_p, ldq, _vec(fn, seq, i32, M, dev), _vec(fn, lens, i32, M, dev),
+        _vec(fn, o, el, M * qw, dev), _vec(fn, lse, _torch_module.float32, M * dm.n_heads, dev),
+        _vec(fn, ws, ws.dtype, ws.numel(), dev), ws.numel() * ws.element_size(),
+        _raw_stream(stream, dev))
     if st:
         raise XmodError(fn, st)
 
@@ -504,13 +509,13 @@ def token_logprobs(logits, target=None, logp=None, entropy=None, lse=None, top_i
     fp32 [N, k])."""
     fn = "xmod_token_logprobs"
     dt, N, V, x, ld, dev = _logits(fn, logits)
+    i32, f32 = _torch_module.int32, _torch_module.float32
     k = top_idx.shape[1] if top_idx is not None else 0
-    i32, f32 = _torch().int32, _torch().float32
     st = load().xmod_token_logprobs(
         dt, N, V, x, ld, _vec(fn, target, i32, N, dev), _vec(fn, logp, f32, N, dev),
         _vec(fn, entropy, f32, N, dev), _vec(fn, lse, f32, N, dev), k,
         _vec(fn, top_idx, i32, N * k, dev), _vec(fn, top_logp, f32, N * k, dev),
-        _vec(fn, status, i32, 1, dev), _stream(stream))
+        _vec(fn, status, i32, 1, dev), _raw_stream(stream, dev))
     if st:
         raise XmodError(fn, st)
 
@@ -521,12 +526,13 @@ def token_logprobs_bwd(logits, target, lse, g_logp, dlogits, entropy=None, g_ent
     (either may be None); dlogits may be logits itself."""
     fn = "xmod_token_logprobs_bwd"
     dt, N, V, x, ld, dev = _logits(fn, logits)
-    i32, f32 = _torch().int32, _torch().float32
+    i32, f32 = _torch_module.int32, _torch_module.float32
     d, ldd = _mat(fn, dlogits, logits.dtype, N, V, dev)
     st = load().xmod_token_logprobs_bwd(
         dt, N, V, x, ld, _vec(fn, target, i32, N, dev), _vec(fn, lse, f32, N, dev),
         _vec(fn, entropy, f32, N, dev), _vec(fn, g_logp, f32, N, dev),
-        _vec(fn, g_entropy, f32, N, dev), d, ldd, _vec(fn, status, i32, 1, dev), _stream(stream))
+        _vec(fn, g_entropy, f32, N, dev), d, ldd, _vec(fn, status, i32, 1, dev),
+        _raw_stream(stream, dev))
     if st:
         raise XmodError(fn, st)
 
