@@ -25,7 +25,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // (x - m); then lse = m + ln l and the entropy is ln l - u / l, whose terms all have one
 // sign. A bf16 logit costs 5 instructions (4 without the entropy), half of the issue
 // slots at the full memory rate: the kernel is bound by memory, and laid out to keep
-// reading. A CTA works rows off one after the other, in three roles that meet at mbarriers
+// reading (4096 rows of 50257, bf16, 412 MB: 67 us, 6.2 TB/s, 0.91 of what a copy reaches; with
+// 5 alternatives 79 us, 0.77; fp32, 823 MB, with 5 alternatives 126 us, 0.96; 8 rows with 20
+// alternatives 10.5 us). A CTA works rows off one after the other, in three roles that meet at mbarriers
 // only: a producer warp keeps bulk copies into a ring of 16 KB chunks going, across row
 // ends; four consumer warps sum, each at its own pace; a finisher warp joins a row's sums,
 // finds its alternatives and writes its results while the consumers are at the next row.
@@ -614,7 +616,8 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
 // ---------------------------------------------------------------- gradient
 //
 // dx_v = g (1[v = t] - p_v) - gH p_v (ln p_v + H): one reading and one writing of the
-// logits' size, 5 instructions a logit: bound by memory. A CTA takes 16 KB of a row, four
+// logits' size, 5 instructions a logit: bound by memory (4096 rows of 50257, bf16, 823 MB:
+// 127 us, 6.5 TB/s, 0.96 of what a copy reaches). A CTA takes 16 KB of a row, four
 // 16-byte vectors a thread, aligned in the output; where the logits' rows are aligned
 // differently (another row stride), their elements are loaded one by one, which the L1
 // cache makes up for.
