@@ -29,8 +29,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 5 alternatives 79 us, 0.77; fp32, 823 MB, with 5 alternatives 126 us, 0.96; 8 rows with 20
 // alternatives 10.5 us). A CTA works rows off one after the other, in three roles that meet at mbarriers
 // only: a producer warp keeps bulk copies into a ring of 16 KB chunks going, across row
-// ends; four consumer warps sum, each at its own pace; a finisher warp joins a row's sums,
-// finds its alternatives and writes its results while the consumers are at the next row.
+// ends; four consumer warps sum, each at its own pace; a finisher warp (or two, taking
+// turns) joins a row's sums, finds its alternatives and writes its results while the
+// consumers are at the next rows.
 // Few rows are split over the CTAs of a cluster, which join through distributed shared
 // memory.
 //
@@ -43,8 +44,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ones), it reads the row once for every alternative; a row with fewer than k tokens above
 // -infinity is filled up from its first tokens.
 
-constexpr int kLpThreads = 128;    // consumers; then the finisher's warp and the producer's
-constexpr int kLpAll = kLpThreads + 64;
+constexpr int kLpThreads = 128;    // consumers; then the finishers' warps and the producer's
 constexpr int kChunk = 16384;      // bytes
 constexpr int kLpStages = 2;
 constexpr int kLpCtas = 4;         // an SM
@@ -171,10 +171,11 @@ struct alignas(16) LpShared {
   Moments parts[8];               // of a cluster's CTAs, in the first one
   int abort;
   alignas(16) float tops[2][kSlots][kLpThreads];
-  alignas(16) uint64_t cand[kCandidates + 2];
-  uint64_t top[XMOD_MAX_TOP_K];   // this CTA's best, in order
-  uint64_t lists[8 * XMOD_MAX_TOP_K];   // the cluster's
-  uint16_t hits[kSlots * kLpThreads];
+  struct Finisher {
+    alignas(16) uint64_t cand[kCandidates + 2];
+    uint64_t top[XMOD_MAX_TOP_K];   // the row's (or this CTA's) best, in order
+    uint16_t hits[kSlots * kLpThreads];
+  } fin[2];
 };
 
 __device__ __forceinline__ void st_cluster(uint32_t at, uint32_t v) {
@@ -187,7 +188,7 @@ __device__ __forceinline__ void st_cluster64(uint32_t at, uint64_t v) {
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-infinity)
 
 // The `k` best of `count` candidates to sh.top, in order; one warp.
-__device__ __forceinline__ void rank_candidates(LpShared& sh, int count, int k, int lane) {
+__device__ __forceinline__ void rank_candidates(LpShared::Finisher& sh, int count, int k, int lane) {
   if (lane == 0) sh.cand[count] = 0;   // the last pair's other half
   __syncwarp();
   for (int i = lane; i < count; i += 32) {
@@ -205,8 +206,9 @@ __device__ __forceinline__ void rank_candidates(LpShared& sh, int count, int k, 
 
 // Finisher: the k best of the row to sh.top; how many there are (all of a short span).
 template <typename T>
-__device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared& sh, const Span& s,
-                                        int64_t row, int parity, int chunks, int step, int k,
+__device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared::Finisher& sh,
+                                        const float (*row_tops)[kLpThreads], const Span& s,
+                                        int64_t row, int chunks, int step, int k,
                                         int lane) {
   constexpr int VE = 16 / sizeof(T), Q = kLpThreads / 32;
   constexpr int BITS = 8 * sizeof(T), SHIFT = 32 - BITS;   // of an order that differ by type
@@ -219,7 +221,7 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared& sh, cons
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int i = 0; i < kSlots; ++i)
-      tops[q][i] = i < slots ? sh.tops[parity][i][lane + 32 * q] : -INFINITY;
+      tops[q][i] = i < slots ? row_tops[i][lane + 32 * q] : -INFINITY;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     float m = tops[q][0];
@@ -282,9 +284,9 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared& sh, cons
     sh.hits[at++] = (i % kSlots * kLpThreads) + lane + i / kSlots * 32;
   }
   __syncwarp();
-  // their vectors, a lane each, four readings under way
+  // their vectors, a lane each, two readings under way
   int count = 0;
-  constexpr int HPW = 32 / kVecs, AHEAD = 4;
+  constexpr int HPW = 32 / kVecs, AHEAD = 2;
   static_assert(32 % kVecs == 0, "");
   for (int h0 = 0; h0 < hits; h0 += HPW * AHEAD) {
     for (int c = 0; c < step; ++c) {
@@ -365,8 +367,9 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared& sh, cons
   return want;
 }
 
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const LogprobArgs a) {
+template <typename T, bool ENT, int FIN>
+__global__ void __launch_bounds__(kLpThreads + 32 * FIN + 32, kLpCtas)
+token_logprobs_kernel(const LogprobArgs a) {
   constexpr int VE = 16 / sizeof(T), W = kLpThreads / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   LpShared& sh = *reinterpret_cast<LpShared*>(smem + kLpStages * kChunk);
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
   pdl_wait();
   // a wait that gives up ends its warp's work; the other warps' waits end by the abort flag
 
-  if (warp == W + 1) {
+  if (warp == W + FIN) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t n = 0;
@@ -420,9 +423,11 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
         mbar_wait(bFull + 8 * (j % kLpStages), (j / kLpStages) & 1, nullptr, a.status);
     }
     __syncwarp();
-  } else if (warp == W) {
-    // ------------------------------------------------------------ finisher
-    int parity = 0;
+  } else if (warp >= W) {
+    // ------------------------------------------------------------ finishers
+    int parity = warp - W;
+    LpShared::Finisher& fin = sh.fin[parity];
+    const int64_t first = row0 + parity * row_step, turn = FIN * row_step;
     uint32_t phase = 0;
     bool met = false;   // the cluster's barrier is behind it
     // the target's logit is fetched a row ahead (and kept as it is stored until it is used),
@@ -432,26 +437,27 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
     auto logit_of = [&](int64_t r, int t) {
       return t >= 0 && t < a.V ? ((const T*)a.logits + r * a.ld)[t] : Elem<T>::from_f(0.f);
     };
-    int target_1 = target_of(row0), target_2 = target_of(row0 + row_step);
-    T x_1 = logit_of(row0, target_1);
-    for (int64_t row = row0; row < a.N; row += row_step) {
+    int target_1 = target_of(first), target_2 = target_of(first + turn);
+    T x_1 = logit_of(first, target_1);
+    for (int64_t row = first; row < a.N; row += turn) {
       const Span s = span_of<T>(a, row, split);
       const int chunks = span_chunks(s), step = (chunks + kSlots - 1) / kSlots;
       const int target = target_1;
       const T x_t = x_1;
       target_1 = target_2;
-      x_1 = logit_of(row + row_step, target_1);
-      target_2 = target_of(row + 2 * row_step);
+      x_1 = logit_of(row + turn, target_1);
+      target_2 = target_of(row + 2 * turn);
       if (!mbar_wait(bDone + 8 * parity, phase, abort_flag, a.status)) break;
       Moments mo = sh.moments[parity][lane % W];
       int found = 0;
-      if (k) found = find_top<T>(a, sh, s, row, parity, chunks, step, k, lane);
+      if (k) found = find_top<T>(a, fin, sh.tops[parity], s, row, chunks, step, k, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(bFreed + 8 * parity);
       mo.raise(warp_max(mo.m));
       if (lane >= W) mo.l = mo.u = 0.f;
       mo.l = warp_sum(mo.l);
       mo.u = warp_sum(mo.u);
+      const uint64_t* best = fin.top;
       if (a.splits > 1) {   // the cluster's only row: everything to the first CTA
         if (lane == 0) {
           const uint32_t at = mapa_shared(smem_u32(&sh.parts[split]), 0);
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
         }
         const int before = split * min(k, a.per);   // all splits but the last are full
         for (int i = lane; i < found; i += 32)
-          st_cluster64(mapa_shared(smem_u32(&sh.lists[before + i]), 0), sh.top[i]);
+          st_cluster64(mapa_shared(smem_u32(&sh.fin[1].cand[before + i]), 0), fin.top[i]);
         cluster_sync_all();
         met = true;
         if (split != 0) return;
@@ -473,8 +479,8 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
         if (k) {
           const int last = a.V - (a.splits - 1) * a.per;
           const int all = (a.splits - 1) * min(k, a.per) + min(k, last);
-          for (int i = lane; i < all; i += 32) sh.cand[i] = sh.lists[i];
-          rank_candidates(sh, all, k, lane);
+          rank_candidates(sh.fin[1], all, k, lane);
+          best = sh.fin[1].top;   // a second finisher has no row here
         }
       }
       const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
@@ -486,13 +492,13 @@ __global__ void __launch_bounds__(kLpAll, kLpCtas) token_logprobs_kernel(const L
         if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (Elem<T>::to_f(x_t) - mo.m) - ll;
       }
       for (int i = lane; i < k; i += 32) {
-        const uint64_t key = sh.top[i];
+        const uint64_t key = best[i];
         a.top_idx[row * k + i] = token_of(key);
         a.top_logp[row * k + i] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
       }
       __syncwarp();
-      parity ^= 1;
-      if (!parity) phase ^= 1;
+      if (FIN == 1) parity ^= 1;
+      if (FIN == 2 || !parity) phase ^= 1;
     }
     if (met) return;
   } else {
@@ -710,8 +716,8 @@ bool elem_ptr(const void* p, xmod_dtype dt) {
 }
 bool ptr4_or_null(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
-template <typename T, bool ENT>
-cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
+template <typename T, bool ENT, int FIN>
+cudaError_t launch_logprobs_fin(const Ctx& c, const LogprobArgs& a0) {
   LogprobArgs a = a0;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -725,14 +731,14 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
   a.per = (a.V + a.splits - 1) / a.splits;
   constexpr int smem = kLpStages * kChunk + (int)sizeof(LpShared);
   static_assert(kLpCtas * (smem + 1024) <= 228 * 1024, "");
-  auto kernel = token_logprobs_kernel<T, ENT>;
+  auto kernel = token_logprobs_kernel<T, ENT, FIN>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)sms * kLpCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.splits > 1 ? a.N * a.splits : a.N < most ? a.N : most));
-  cfg.blockDim = dim3(kLpAll);
+  cfg.blockDim = dim3(kLpThreads + 32 * FIN + 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[2];
@@ -744,6 +750,17 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a0) {
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// A second finisher where one would hold the rows up: short rows, or many alternatives (it
+// costs the others registers and issue slots). 4096 rows, bf16, one and two finishers: 50257
+// logits with 5 alternatives 77.7 and 78.8 us, with 64 of them 174 and 141; 1000 logits with 5
+// alternatives 26 and 18 us.
+template <typename T, bool ENT>
+cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
+  return a.top_k > 32 || (a.top_k && (int64_t)a.V * sizeof(T) <= 2 * kChunk)
+             ? launch_logprobs_fin<T, ENT, 2>(c, a)
+             : launch_logprobs_fin<T, ENT, 1>(c, a);
 }
 
 template <typename T>
