@@ -424,10 +424,9 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   // -------------------------------------------------------------- consumers
   // Warp w takes the keys w, w + 4, ... (in groups of 16) of every tile. Scores and
   // probabilities live in MMA fragments: thread (r = lane / 4, t = lane % 4) holds query
-  // heads r and r + 8. With at most 8 query heads rows 8 to 15 of the probabilities carry
-  // what rounding rows 0 to 7 to 16 bits left over, so that the outputs see 16 bits of
-  // mantissa (22 for f16) at no cost; with more, bf16 takes a second MMA for the remainder
-  // and f16's 11 bits stand (the codes they weight have 4).
+  // heads r and r + 8. bf16 probabilities go in as two bf16 parts, 16 bits of mantissa: with
+  // at most 8 query heads rows 8 to 15 carry what rounding rows 0 to 7 left over, at no cost;
+  // with more a second MMA does. For e4m3 values f16's 11 bits stand (the codes have 4).
   constexpr bool PAIR = ROWS == 8;
   const int r = lane >> 2, t = lane & 3;
   const float to_log2 = 1.4426950408889634f * rsqrtf((float)HD);
@@ -460,7 +459,9 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       if (info.valid > 0) {
         // query fragments: bf16 as they are; for e4m3 caches in f16 (the type the codes
         // convert to), each row scaled by a power of two to a largest value in [1, 2)
+        // (rows past the query heads are zero: their maxima never move)
         const uint32_t qs = sQ + st * C::QB;
+        const int rows = min(ROWS, group - (info.pass % a.passes) * ROWS);
 #pragma unroll
         for (int i = 0; i < (PAIR ? 1 : 2); ++i) {
           const uint32_t row = qs + (r + 8 * i) * C::QROW;
@@ -472,6 +473,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             const uint32_t at = row + k * 32 + (FP8 ? t * 8 : t * 4);
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[k][0]) : "r"(at));
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[k][1]) : "r"(at + (FP8 ? 4 : 16)));
+            if (r + 8 * i >= rows) w[k][0] = w[k][1] = 0u;
           }
           q_mul[i] = to_log2;
           if constexpr (FP8) {
