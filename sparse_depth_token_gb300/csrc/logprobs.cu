@@ -26,7 +26,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // sign. A bf16 logit costs 5 instructions (4 without the entropy), half of the issue
 // slots at the full memory rate: the kernel is bound by memory, and laid out to keep
 // reading (4096 rows of 50257, bf16, 412 MB: 67 us, 6.2 TB/s, 0.91 of what a copy reaches; with
-// 5 alternatives 79 us, 0.77; fp32, 823 MB, with 5 alternatives 126 us, 0.96; 8 rows with 20
+// 5 alternatives 78 us, 0.78; fp32, 823 MB, with 5 alternatives 126 us, 0.96; 8 rows with 20
 // alternatives 10.5 us). A CTA works rows off one after the other, in three roles that meet at mbarriers
 // only: a producer warp keeps bulk copies into a ring of 16 KB chunks going, across row
 // ends; four consumer warps sum, each at its own pace; a finisher warp (or two, taking
@@ -163,6 +163,13 @@ __device__ __forceinline__ int span_chunks(const Span& s) {
   return (s.nvec * 16 + kChunk - 1) / kChunk;
 }
 
+// What a warp needs to find a row's alternatives.
+struct Finisher {
+  alignas(16) uint64_t cand[kCandidates + 2];
+  uint64_t top[XMOD_MAX_TOP_K];   // the row's (or this CTA's) best, in order
+  uint16_t hits[kSlots * kLpThreads];
+};
+
 // Shared memory behind the ring. Two of what a row leaves: the consumers may be a row ahead.
 struct alignas(16) LpShared {
   uint64_t full[kLpStages], empty[kLpStages];
@@ -171,11 +178,7 @@ struct alignas(16) LpShared {
   Moments parts[8];               // of a cluster's CTAs, in the first one
   int abort;
   alignas(16) float tops[2][kSlots][kLpThreads];
-  struct Finisher {
-    alignas(16) uint64_t cand[kCandidates + 2];
-    uint64_t top[XMOD_MAX_TOP_K];   // the row's (or this CTA's) best, in order
-    uint16_t hits[kSlots * kLpThreads];
-  } fin[2];
+  Finisher fin[2];
 };
 
 __device__ __forceinline__ void st_cluster(uint32_t at, uint32_t v) {
@@ -188,7 +191,7 @@ __device__ __forceinline__ void st_cluster64(uint32_t at, uint64_t v) {
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-infinity)
 
 // The `k` best of `count` candidates to sh.top, in order; one warp.
-__device__ __forceinline__ void rank_candidates(LpShared::Finisher& sh, int count, int k, int lane) {
+__device__ __forceinline__ void rank_candidates(Finisher& sh, int count, int k, int lane) {
   if (lane == 0) sh.cand[count] = 0;   // the last pair's other half
   __syncwarp();
   for (int i = lane; i < count; i += 32) {
@@ -204,29 +207,23 @@ __device__ __forceinline__ void rank_candidates(LpShared::Finisher& sh, int coun
   __syncwarp();
 }
 
-// Finisher: the k best of the row to sh.top; how many there are (all of a short span).
-template <typename T>
-__device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared::Finisher& sh,
-                                        const float (*row_tops)[kLpThreads], const Span& s,
-                                        int64_t row, int chunks, int step, int k,
-                                        int lane) {
-  constexpr int VE = 16 / sizeof(T), Q = kLpThreads / 32;
+// One warp: the k best of a row (or split) to sh.top, in order; how many there are (all of a
+// short one). The row's vectors were read by 32 Q threads: thread t took the vectors
+// t + 32 Q j, and its slot i holds the maximum of EACH * step of them from j = i EACH step on;
+// tops: those of threads lane, lane + 32, ...
+template <typename T, int Q, int S, int EACH>
+__device__ __forceinline__ int find_top(const LogprobArgs& a, Finisher& sh,
+                                        const float (&tops)[Q][S], const Span& s, int64_t row,
+                                        int step, int k, int lane) {
+  constexpr int VE = 16 / sizeof(T), THREADS = 32 * Q;
   constexpr int BITS = 8 * sizeof(T), SHIFT = 32 - BITS;   // of an order that differ by type
-  const int slots = (chunks + step - 1) / step;
   const T* p = (const T*)a.logits + row * a.ld + s.token0;
-  // what threads lane, lane + 32, ... left, and their orders over the row
-  float tops[Q][kSlots];
-  uint32_t best[Q];
-#pragma unroll
-  for (int q = 0; q < Q; ++q)
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      tops[q][i] = i < slots ? row_tops[i][lane + 32 * q] : -INFINITY;
+  uint32_t best[Q];   // the threads' orders over the row
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     float m = tops[q][0];
 #pragma unroll
-    for (int i = 1; i < kSlots; ++i) m = max_nan(m, tops[q][i]);
+    for (int i = 1; i < S; ++i) m = max_nan(m, tops[q][i]);
     best[q] = lane + 32 * q < s.nvec ? order_of(m) : 0u;
   }
   // the k-th largest of the threads' orders: a few by taking the largest away, more by the
@@ -269,8 +266,8 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared::Finisher
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (!(tops[q][i] < least)) mask |= 1u << (q * kSlots + i);
+    for (int i = 0; i < S; ++i)
+      if (!(tops[q][i] < least)) mask |= 1u << (q * S + i);
   int at = __popc(mask), hits = at;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -281,26 +278,25 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared::Finisher
   hits = __shfl_sync(0xffffffffu, hits, 31);
   for (; mask; mask &= mask - 1) {
     const int i = __ffs(mask) - 1;
-    sh.hits[at++] = (i % kSlots * kLpThreads) + lane + i / kSlots * 32;
+    sh.hits[at++] = i % S * THREADS + lane + i / S * 32;
   }
   __syncwarp();
   // their vectors, a lane each, two readings under way
   int count = 0;
-  constexpr int HPW = 32 / kVecs, AHEAD = 2;
-  static_assert(32 % kVecs == 0, "");
+  constexpr int HPW = 32 / EACH, AHEAD = 2;
+  static_assert(32 % EACH == 0 && Q * S <= 32, "");
   for (int h0 = 0; h0 < hits; h0 += HPW * AHEAD) {
     for (int c = 0; c < step; ++c) {
       uint4 x[AHEAD];
       int e0[AHEAD];
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
-        const int h = h0 + i * HPW + lane / kVecs;
+        const int h = h0 + i * HPW + lane / EACH;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         e0[i] = s.count;
         if (h < hits) {
           const int hit = sh.hits[h];
-          const int v = (hit / kLpThreads * step + c) * (kChunk / 16) + hit % kLpThreads +
-                        lane % kVecs * kLpThreads;
+          const int v = ((hit / THREADS * step + c) * EACH + lane % EACH) * THREADS + hit % THREADS;
           if (v < s.nvec) {
             e0[i] = v * VE - s.head;
             if (v < s.full) {
@@ -367,6 +363,107 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, LpShared::Finisher
   return want;
 }
 
+// One warp: a row's results from its sums, its target's logit and its alternatives' keys.
+template <typename T>
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const Moments& mo,
+                                          int target, T x_t, const uint64_t* top, int lane) {
+  const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
+  const float ll = logf(mo.l), nan = __int_as_float(0x7fc00000);
+  if (lane == 0) {
+    if (bad || target >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+    if (a.lse) a.lse[row] = bad ? nan : mo.m + ll;
+    if (a.entropy) a.entropy[row] = bad ? nan : ll - 0.6931471805599453f * mo.u / mo.l;
+    if (a.logp)
+      a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (Elem<T>::to_f(x_t) - mo.m) - ll;
+  }
+  for (int i = lane; i < a.top_k; i += 32) {
+    const uint64_t key = top[i];
+    a.top_idx[row * a.top_k + i] = token_of(key);
+    a.top_logp[row * a.top_k + i] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
+  }
+}
+
+// Rows of at most 256 vectors (4 KB): a warp holds one in registers, eight vectors a lane, so
+// the maximum comes first and nothing is read twice but the few vectors behind the bound.
+// 4096 rows of 1000 logits, bf16, with 5 alternatives: 7.0 us, 18 us by the ring.
+constexpr int kShortVecs = 8, kShortWarps = 4, kShortTopK = 32;
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kShortWarps * 32)
+token_logprobs_short_kernel(const LogprobArgs a) {
+  constexpr int VE = 16 / sizeof(T);
+  __shared__ Finisher fin[kShortWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t row = (int64_t)blockIdx.x * kShortWarps + warp; row < a.N;
+       row += (int64_t)gridDim.x * kShortWarps) {
+    const Span s = span_of<T>(a, row, 0);
+    const int target = a.logp ? a.target[row] : -1;
+    uint4 x[kShortVecs];
+#pragma unroll
+    for (int i = 0; i < kShortVecs; ++i) {
+      const int v = lane + 32 * i;
+      const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+      x[i] = make_uint4(ninf, ninf, ninf, ninf);
+      if (v < s.full) {
+        x[i] = s.vecs[v];
+        if (v == 0) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (j < s.head) vec_clear<T>(x[i], j);
+        }
+      } else if (v < s.nvec) {
+        const T* p = reinterpret_cast<const T*>(s.vecs + v);
+        T* e = reinterpret_cast<T*>(&x[i]);
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (v * VE + j >= s.head && v * VE + j < s.head + s.count) e[j] = p[j];
+      }
+    }
+    const T x_t = target >= 0 && target < a.V ? ((const T*)a.logits + row * a.ld)[target]
+                                              : Elem<T>::from_f(0.f);
+    float tops[1][kShortVecs], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kShortVecs; ++i) {
+      tops[0][i] = vec_max<T>(x[i]);
+      top = max_nan(top, tops[0][i]);
+    }
+    // a NaN makes the maximum +infinity, the sum 0 or NaN and the row bad
+    const bool nan = __any_sync(0xffffffffu, top != top);
+    Moments mo{nan ? INFINITY : warp_max(top), 0.f, 0.f};
+    float2 l2 = make_float2(0.f, 0.f), u2 = l2;
+    if (fabsf(mo.m) < 1e36f) {
+      const float2 neg = make_float2(-mo.m, -mo.m), lg = make_float2(kLog2e, kLog2e);
+#pragma unroll
+      for (int i = 0; i < kShortVecs; ++i) {
+        if (32 * i >= s.nvec) break;
+        if (ENT) vec_finite<T>(x[i]);
+#pragma unroll
+        for (int j = 0; j < VE / 2; ++j) {
+          const float2 t = mul2(add2(vec_pair<T>(x[i], j), neg), lg);
+          const float2 e = make_float2(ex2(t.x), ex2(t.y));
+          l2 = add2(l2, e);
+          if (ENT) u2 = fma2(e, t, u2);
+        }
+      }
+    } else if (mo.m > -INFINITY) {   // differences that could overflow
+#pragma unroll
+      for (int i = 0; i < kShortVecs * VE; ++i) {
+        const float d = fmaxf(vec_at<T>(x[i / VE], i % VE) - mo.m, -1e30f) * kLog2e, e = ex2(d);
+        l2.x += e;
+        if (ENT) u2.x = fmaf(e, d, u2.x);
+      }
+    }
+    mo.l = warp_sum(l2.x + l2.y);
+    if (ENT) mo.u = warp_sum(u2.x + u2.y);
+    if (a.top_k)
+      find_top<T, 1, kShortVecs, 1>(a, fin[warp], tops, s, row, 1, a.top_k, lane);
+    write_row<T>(a, row, mo, target, x_t, fin[warp].top, lane);
+    __syncwarp();
+  }
+}
+
 template <typename T, bool ENT, int FIN>
 __global__ void __launch_bounds__(kLpThreads + 32 * FIN + 32, kLpCtas)
 token_logprobs_kernel(const LogprobArgs a) {
@@ -426,7 +523,7 @@ token_logprobs_kernel(const LogprobArgs a) {
   } else if (warp >= W) {
     // ------------------------------------------------------------ finishers
     int parity = warp - W;
-    LpShared::Finisher& fin = sh.fin[parity];
+    Finisher& fin = sh.fin[parity];
     const int64_t first = row0 + parity * row_step, turn = FIN * row_step;
     uint32_t phase = 0;
     bool met = false;   // the cluster's barrier is behind it
@@ -450,7 +547,16 @@ token_logprobs_kernel(const LogprobArgs a) {
       if (!mbar_wait(bDone + 8 * parity, phase, abort_flag, a.status)) break;
       Moments mo = sh.moments[parity][lane % W];
       int found = 0;
-      if (k) found = find_top<T>(a, fin, sh.tops[parity], s, row, chunks, step, k, lane);
+      if (k) {
+        const int slots = (chunks + step - 1) / step;
+        float tops[W][kSlots];
+#pragma unroll
+        for (int q = 0; q < W; ++q)
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i)
+            tops[q][i] = i < slots ? sh.tops[parity][i][lane + 32 * q] : -INFINITY;
+        found = find_top<T, W, kSlots, kVecs>(a, fin, tops, s, row, step, k, lane);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bFreed + 8 * parity);
       mo.raise(warp_max(mo.m));
@@ -483,19 +589,7 @@ token_logprobs_kernel(const LogprobArgs a) {
           best = sh.fin[1].top;   // a second finisher has no row here
         }
       }
-      const bool bad = !(mo.l > 0.f);   // nothing above -infinity, a NaN or +infinity
-      const float ll = logf(mo.l), nan = __int_as_float(0x7fc00000);
-      if (lane == 0) {
-        if (bad || target >= a.V) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-        if (a.lse) a.lse[row] = bad ? nan : mo.m + ll;
-        if (a.entropy) a.entropy[row] = bad ? nan : ll - 0.6931471805599453f * mo.u / mo.l;
-        if (a.logp) a.logp[row] = target < 0 ? 0.f : bad || target >= a.V ? nan : (Elem<T>::to_f(x_t) - mo.m) - ll;
-      }
-      for (int i = lane; i < k; i += 32) {
-        const uint64_t key = best[i];
-        a.top_idx[row * k + i] = token_of(key);
-        a.top_logp[row * k + i] = bad ? nan : (value_of((uint32_t)(key >> 32)) - mo.m) - ll;
-      }
+      write_row<T>(a, row, mo, target, x_t, best, lane);
       __syncwarp();
       if (FIN == 1) parity ^= 1;
       if (FIN == 2 || !parity) phase ^= 1;
@@ -627,8 +721,9 @@ token_logprobs_kernel(const LogprobArgs a) {
 // 16-byte vectors a thread, aligned in the output; where the logits' rows are aligned
 // differently (another row stride), their elements are loaded one by one, which the L1
 // cache makes up for.
+// Short rows (at most 256 vectors) are taken by warps instead of CTAs, 2 KB at a time.
 struct LogprobBwdArgs {
-  int V, chunks;
+  int V, chunks;   // chunks: pieces of a row
   int64_t N, ld, ldd;
   const void* logits;
   const int32_t* target;
@@ -637,14 +732,17 @@ struct LogprobBwdArgs {
   int* status;
 };
 
-constexpr int kBwdThreads = 256, kBwdVecs = kChunk / 16 / kBwdThreads;
+constexpr int kBwdThreads = 256, kBwdVecs = 4;
 
-template <typename T>
+// GROUP threads take a piece of GROUP * kBwdVecs vectors of a row.
+template <typename T, int GROUP>
 __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const LogprobBwdArgs a) {
-  constexpr int VE = 16 / sizeof(T);
+  constexpr int VE = 16 / sizeof(T), GROUPS = kBwdThreads / GROUP;
+  const int t_in = threadIdx.x % GROUP;
   pdl_trigger();
   pdl_wait();
-  for (int64_t item = blockIdx.x; item < a.N * a.chunks; item += gridDim.x) {
+  for (int64_t item = (int64_t)blockIdx.x * GROUPS + threadIdx.x / GROUP; item < a.N * a.chunks;
+       item += (int64_t)gridDim.x * GROUPS) {
     const int64_t row = item / a.chunks;
     const int chunk = (int)(item - row * a.chunks);
     const T* x = (const T*)a.logits + row * a.ld;
@@ -652,11 +750,11 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const L
     // element 0 of the row is element `head` of its first aligned vector
     const int head = (int)((uintptr_t)d & 15) / (int)sizeof(T);
     const bool same = (((uintptr_t)x ^ (uintptr_t)d) & 15) == 0;
-    const int e0 = (chunk * (kChunk / 16) + (int)threadIdx.x) * VE - head;
+    const int e0 = (chunk * GROUP * kBwdVecs + t_in) * VE - head;
     uint4 v[kBwdVecs];
 #pragma unroll
     for (int i = 0; i < kBwdVecs; ++i) {
-      const int e = e0 + i * kBwdThreads * VE;
+      const int e = e0 + i * GROUP * VE;
       if (same && e >= 0 && e + VE <= a.V) {
         v[i] = *reinterpret_cast<const uint4*>(x + e);
       } else {
@@ -668,7 +766,7 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const L
     }
     int t = a.g_logp ? a.target[row] : -1;
     if (t >= a.V) {
-      if (threadIdx.x == 0 && chunk == 0) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+      if (t_in == 0 && chunk == 0) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
       t = -1;
     }
     const float g = t >= 0 ? a.g_logp[row] : 0.f, gh = a.g_entropy ? a.g_entropy[row] : 0.f;
@@ -680,7 +778,7 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const L
     const float2 mul = make_float2(-gh, -gh), add = make_float2(b, b);
 #pragma unroll
     for (int i = 0; i < kBwdVecs; ++i) {
-      const int e = e0 + i * kBwdThreads * VE;
+      const int e = e0 + i * GROUP * VE;
       if (e >= a.V || e + VE <= 0) continue;
       uint4 out;
 #pragma unroll
@@ -752,28 +850,43 @@ cudaError_t launch_logprobs_fin(const Ctx& c, const LogprobArgs& a0) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// A second finisher where one would hold the rows up: short rows, or many alternatives (it
-// costs the others registers and issue slots). 4096 rows, bf16, one and two finishers: 50257
-// logits with 5 alternatives 77.7 and 78.8 us, with 64 of them 174 and 141; 1000 logits with 5
-// alternatives 26 and 18 us.
+// Short rows go to warps. Else a second finisher where one would hold the rows up: rows of one
+// or two chunks, or many alternatives (it costs the others registers and issue slots). 4096
+// rows, bf16, one and two finishers: 50257 logits with 5 alternatives 77.7 and 78.8 us, with
+// 64 of them 174 and 141; 1000 logits with 5 alternatives (now a warp's) 26 and 18 us.
 template <typename T, bool ENT>
 cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
+  const int VE = 16 / (int)sizeof(T);
+  if (((int64_t)a.V + 2 * VE - 2) / VE <= 32 * kShortVecs && a.top_k <= kShortTopK) {
+    const int sms = device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int64_t ctas = (a.N + kShortWarps - 1) / kShortWarps, most = (int64_t)sms * 16;
+    return launch_pdl(token_logprobs_short_kernel<T, ENT>, dim3((unsigned)(ctas < most ? ctas : most)),
+                      dim3(kShortWarps * 32), 0, c.stream, a);
+  }
   return a.top_k > 32 || (a.top_k && (int64_t)a.V * sizeof(T) <= 2 * kChunk)
              ? launch_logprobs_fin<T, ENT, 2>(c, a)
              : launch_logprobs_fin<T, ENT, 1>(c, a);
 }
 
-template <typename T>
-cudaError_t launch_logprobs_bwd(const Ctx& c, const LogprobBwdArgs& a0) {
+template <typename T, int GROUP>
+cudaError_t launch_logprobs_bwd_group(const Ctx& c, const LogprobBwdArgs& a0, int64_t vecs) {
   LogprobBwdArgs a = a0;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int VE = 16 / (int)sizeof(T);
-  // vectors of a row at the worst alignment, in chunks
-  a.chunks = (int)(((int64_t)a.V + 2 * VE - 2) / VE / (kChunk / 16)) + 1;
-  const int64_t items = a.N * a.chunks, most = (int64_t)sms * 64;
-  return launch_pdl(token_logprobs_bwd_kernel<T>, dim3((unsigned)(items < most ? items : most)),
+  a.chunks = (int)((vecs + GROUP * kBwdVecs - 1) / (GROUP * kBwdVecs));
+  const int64_t items = a.N * a.chunks, groups = kBwdThreads / GROUP;
+  const int64_t ctas = (items + groups - 1) / groups, most = (int64_t)sms * 64;
+  return launch_pdl(token_logprobs_bwd_kernel<T, GROUP>, dim3((unsigned)(ctas < most ? ctas : most)),
                     dim3(kBwdThreads), 0, c.stream, a);
+}
+
+template <typename T>
+cudaError_t launch_logprobs_bwd(const Ctx& c, const LogprobBwdArgs& a) {
+  const int VE = 16 / (int)sizeof(T);
+  const int64_t vecs = ((int64_t)a.V + 2 * VE - 2) / VE;   // of a row at the worst alignment
+  return vecs <= 256 ? launch_logprobs_bwd_group<T, 32>(c, a, vecs)
+                     : launch_logprobs_bwd_group<T, kBwdThreads>(c, a, vecs);
 }
 
 }  // namespace

@@ -432,3 +432,20 @@ def test_binding_refusals(X):
         with pytest.raises(X.XmodError) as e:
             call()
         assert e.value.status == X.ERR_INVALID_ARG, i
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("V", [1009, 1021, 1022, 1024, 2033, 2041, 2042, 2048, 4096])
+def test_row_lengths_around_the_kernels_borders(X, dtype, V):
+    """Rows that a warp, a CTA's first chunk or more just hold, at any alignment."""
+    x, t = _logits(11, V, dtype, 1, V)
+    for k in (1, 31, 33):
+        out = _forward(X, x, t, k)
+        _check(x, t, out, k)
+    g = torch.randn(11, generator=torch.Generator().manual_seed(9)).cuda()
+    d = torch.empty(11, V, dtype=x.dtype, device="cuda")
+    X.token_logprobs_bwd(x, t, out["lse"], g, d, entropy=out["entropy"], g_entropy=g)
+    ref = _grad_ref(x, t, g, g)[0]
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    # the bound of the formula's test with |g| (1 + |ln p| + H) below 64
+    assert bool(((d.double() - ref).abs() <= half * ref.abs() + 64 * 2.0 ** -17 * ref.abs() + 2.0 ** -17).all())
