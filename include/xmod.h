@@ -491,13 +491,16 @@ XMOD_API int xmod_cache_attention(const xmod_dims* dims, const xmod_kv_cache* ca
  *   top_idx, top_logp [N, top_k]: the top_k largest logits in descending order, ties to
  *           the lower token (-0 equals +0), and their log probabilities
  * Every output may be NULL (logp and target go together; top_idx and top_logp too;
- * top_k = 0 without them). top_k is at most min(V, XMOD_MAX_TOP_K). The sums are fp32.
+ * top_k = 0 without them). top_k is at most min(V, XMOD_MAX_TOP_K), V at most
+ * XMOD_MAX_VOCAB (a row's finisher works within the kernel's bounded waits, whatever the
+ * order of its logits). The sums are fp32.
  * Checked on the device and reported through status_out (a device int, or NULL; see
  * xmod_gather): a target not below V gives a NaN logp; a row that holds a NaN or
  * +infinity, or nothing above -infinity, has no distribution: its lse, logp, entropy and
  * top_logp are NaN (its top_idx rank a NaN above +infinity). Pointers need only their
  * elements' alignment (rows of an odd V begin anywhere). N = 0 does nothing. */
 #define XMOD_MAX_TOP_K 64
+#define XMOD_MAX_VOCAB (1 << 22)
 
 XMOD_API int xmod_token_logprobs(xmod_dtype dtype, int64_t N, int V, const void* logits,
                                  int64_t ld, const int32_t* target, float* logp,
@@ -513,8 +516,8 @@ XMOD_API int xmod_token_logprobs(xmod_dtype dtype, int64_t N, int V, const void*
  *   dlogits    [N, V] (dtype), row stride ldd >= V; may be logits itself (ldd = ld), else
  *              must not overlap it. Columns from V to ldd are not written.
  * A row whose two gradients are zero (or absent) gets zeros, whatever its logits. A
- * target not below V counts as negative and is reported through status_out. Alignment as
- * for xmod_token_logprobs. */
+ * target not below V counts as negative and is reported through status_out. Alignment and
+ * V as for xmod_token_logprobs. */
 XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const void* logits,
                                      int64_t ld, const int32_t* target, const float* lse,
                                      const float* entropy, const float* g_logp,

@@ -3,6 +3,7 @@
 
 #include <cuda_bf16.h>
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 
 #include <atomic>
@@ -23,25 +24,26 @@ constexpr float kLog2e = 1.4426950408889634f;
 //
 // One pass: every thread keeps a running maximum m, l = sum e^(x - m) and u = sum e^(x - m)
 // (x - m); then lse = m + ln l and the entropy is ln l - u / l, whose terms all have one
-// sign. A bf16 logit costs 5 instructions (4 without the entropy), half of the issue
-// slots at the full memory rate: the kernel is bound by memory, and laid out to keep
-// reading (4096 rows of 50257, bf16, 412 MB: 67 us, 6.2 TB/s, 0.91 of what a copy reaches; with
-// 5 alternatives 78 us, 0.78; fp32, 823 MB, with 5 alternatives 126 us, 0.96; 8 rows with 20
-// alternatives 10.5 us). A CTA works rows off one after the other, in three roles that meet at mbarriers
-// only: a producer warp keeps bulk copies into a ring of 16 KB chunks going, across row
-// ends; four consumer warps sum, each at its own pace; a finisher warp (or two, taking
-// turns) joins a row's sums, finds its alternatives and writes its results while the
-// consumers are at the next rows.
-// Few rows are split over the CTAs of a cluster, which join through distributed shared
-// memory.
+// sign. A bf16 logit costs 5 instructions (4 without the entropy), half of the issue slots
+// at the full memory rate: the kernel is bound by memory, and laid out to keep reading. A
+// CTA works rows off one after the other, in three roles that meet at mbarriers only: a
+// producer warp keeps bulk copies into a ring of 16 KB chunks going, across row ends; four
+// consumer warps sum, each at its own pace; a finisher warp (or two, taking turns) joins a
+// row's sums, finds its alternatives and writes its results while the consumers are at the
+// next rows. Few rows are split over the CTAs of a cluster, which join through distributed
+// shared memory; short rows go to single warps (below).
+//
+// Measured: 4096 rows of 50257, bf16 (412 MB): 67 us, 6.2 TB/s, 0.91 of what a copy reaches;
+// with 5 alternatives 78 us, 0.78 (the finisher takes issue slots); fp32 (823 MB), with 5
+// alternatives 126 us, 0.96; 8 rows with 20 alternatives 10.5 us, without 4.4.
 //
 // The alternatives. Logits are ranked by 64-bit keys, the value's order above the inverted
 // token number: keys are distinct, so ties need no care. All that the consumers do for them
 // is to leave every thread's maximum of every chunk. The k-th largest of the threads' maxima
 // over the row is a bound that k logits reach and few besides; the finisher reads the
 // vectors behind the chunk maxima that reach it once more (from L2), and ranks the logits
-// that do by counting the larger ones. Should they be more than its buffer holds (many equal
-// ones), it reads the row once for every alternative; a row with fewer than k tokens above
+// that do by counting the larger ones. Whenever they fill its buffer (many equal ones, a row
+// in rising order), only the k best so far stay; a row with fewer than k tokens above
 // -infinity is filled up from its first tokens.
 
 constexpr int kLpThreads = 128;    // consumers; then the finishers' warps and the producer's
@@ -50,7 +52,10 @@ constexpr int kLpStages = 2;
 constexpr int kLpCtas = 4;         // an SM
 constexpr int kVecs = kChunk / 16 / kLpThreads;   // vectors a thread takes of a chunk
 constexpr int kSlots = 8;          // maxima a thread leaves of a row, each of `step` chunks
-constexpr int kCandidates = 512;   // k - 1 threads' logits of a short row, at least
+// Logits that a finisher keeps while it looks. 8 rows of 50257 bf16 logits with 20
+// alternatives, all but three at the type's lowest value: 99 us (192: 112, 512: 300; reading
+// the row once for every alternative instead, 1030); ordinary rows do not fill it.
+constexpr int kCandidates = 256;
 
 struct LogprobArgs {
   int V, top_k, splits, per;   // per: logits of a split
@@ -160,7 +165,7 @@ __device__ __forceinline__ Span span_of(const LogprobArgs& a, int64_t row, int s
   return s;
 }
 __device__ __forceinline__ int span_chunks(const Span& s) {
-  return (s.nvec * 16 + kChunk - 1) / kChunk;
+  return (s.nvec + kChunk / 16 - 1) / (kChunk / 16);
 }
 
 // What a warp needs to find a row's alternatives.
@@ -260,7 +265,7 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, Finisher& sh,
   }
   // none at -infinity (see below); 0 stands for -0 too
   bound = max(bound, kOrderNone + 1);
-  const float least = value_of(bound);
+  float least = value_of(bound);
   // the threads' chunks whose maxima reach it: first vectors of them
   uint32_t mask = 0;
 #pragma unroll
@@ -283,6 +288,9 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, Finisher& sh,
   __syncwarp();
   // their vectors, a lane each, two readings under way
   int count = 0;
+  uint64_t low = 0;   // keys below it are known not to be among the k best
+  float above = least;   // from token `last` on, the least value that can be
+  int last = INT_MAX;
   constexpr int HPW = 32 / EACH, AHEAD = 2;
   static_assert(32 % EACH == 0 && Q * S <= 32, "");
   for (int h0 = 0; h0 < hits; h0 += HPW * AHEAD) {
@@ -313,21 +321,35 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, Finisher& sh,
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         if (h0 + i * HPW >= hits) break;
+        const float at_least = s.token0 + e0[i] >= last ? above : least;
         uint32_t in = 0;
 #pragma unroll
         for (int j = 0; j < VE; ++j)
-          if (!(vec_at<T>(x[i], j) < least)) in |= 1u << j;
+          if (!(vec_at<T>(x[i], j) < at_least)) in |= 1u << j;
         // elements before the row's first and past its last
         if (e0[i] < 0) in &= ~0u << -e0[i];
         if (e0[i] + VE > s.count) in &= (1u << max(0, s.count - e0[i])) - 1u;
         for (uint32_t who; (who = __ballot_sync(0xffffffffu, in != 0)) != 0; in &= in - 1) {
+          if (count > kCandidates - 32) {   // keep the k best
+            rank_candidates(sh, count, k, lane);
+            for (int j = lane; j < k; j += 32) sh.cand[j] = sh.top[j];
+            count = k;
+            low = sh.top[k - 1];
+            least = value_of((uint32_t)(low >> 32));
+            above = value_of((uint32_t)(low >> 32) + 1);
+            last = token_of(low);
+            __syncwarp();
+          }
+          uint64_t key = 0;
           if (in) {
-            const int j = __ffs(in) - 1, n = count + __popc(who & ((1u << lane) - 1u));
+            const int j = __ffs(in) - 1;
             float f = vec_at<T>(x[i], 0);
 #pragma unroll
             for (int jj = 1; jj < VE; ++jj) f = jj == j ? vec_at<T>(x[i], jj) : f;
-            if (n < kCandidates) sh.cand[n] = key_of(f, s.token0 + e0[i] + j);
+            key = key_of(f, s.token0 + e0[i] + j);
           }
+          if (low) who = __ballot_sync(0xffffffffu, key > low);
+          if (who >> lane & 1) sh.cand[count + __popc(who & ((1u << lane) - 1u))] = key;
           count += __popc(who);
         }
       }
@@ -343,23 +365,7 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, Finisher& sh,
       count += __popc(who);
     }
   }
-  if (count <= kCandidates) {
-    rank_candidates(sh, count, k, lane);
-  } else {   // too many: one reading for each alternative, the largest key below the last
-    uint64_t last = ~0ull;
-    for (int i = 0; i < want; ++i) {
-      unsigned long long top = 0;
-#pragma unroll 4
-      for (int e = lane; e < s.count; e += 32) {
-        const uint64_t key = key_of(Elem<T>::to_f(p[e]), s.token0 + e);
-        if (key < last && key > top) top = key;
-      }
-      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      last = top;
-      if (lane == 0) sh.top[i] = top;
-    }
-    __syncwarp();
-  }
+  rank_candidates(sh, count, k, lane);
   return want;
 }
 
@@ -909,7 +915,7 @@ int xmod_token_logprobs(xmod_dtype dt, int64_t N, int V, const void* logits, int
   const void* ps[] = {target, logp, entropy, lse, top_idx, top_logp, status_out};
   for (const void* p : ps)
     if (!ptr4_or_null(p)) return XMOD_ERR_INVALID_ARG;
-  if (top_k > XMOD_MAX_TOP_K || N > INT32_MAX || V > INT32_MAX - 65536) return XMOD_ERR_UNSUPPORTED;
+  if (top_k > XMOD_MAX_TOP_K || N > INT32_MAX || V > XMOD_MAX_VOCAB) return XMOD_ERR_UNSUPPORTED;
   const LogprobArgs a{V, top_k, 1, V, N, ld, logits, target, logp, entropy, lse, top_idx, top_logp,
                       status_out};
   const Ctx c{(cudaStream_t)stream, status_out};
@@ -935,7 +941,7 @@ int xmod_token_logprobs_bwd(xmod_dtype dt, int64_t N, int V, const void* logits,
   const void* ps[] = {target, lse, entropy, g_logp, g_entropy, status_out};
   for (const void* p : ps)
     if (!ptr4_or_null(p)) return XMOD_ERR_INVALID_ARG;
-  if (N > INT32_MAX || V > INT32_MAX - 65536) return XMOD_ERR_UNSUPPORTED;
+  if (N > INT32_MAX || V > XMOD_MAX_VOCAB) return XMOD_ERR_UNSUPPORTED;
   const LogprobBwdArgs a{V, 1, N, ld, ldd, logits, target, lse, entropy, g_logp, g_entropy,
                          dlogits, status_out};
   const Ctx c{(cudaStream_t)stream, status_out};

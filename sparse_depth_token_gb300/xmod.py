@@ -31,6 +31,7 @@ EXPORTS = ("xmod_version", "xmod_status_string", "xmod_workspace_bytes", "xmod_r
 
 CACHE_NATIVE, CACHE_E4M3 = 0, 1
 MAX_TOP_K = 64   # alternatives token_logprobs reports at most
+MAX_VOCAB = 1 << 22   # logits of a row of token_logprobs and its gradient at most
 
 # Largest B*T the allocation-free router entry point accepts (its fixed scratch).
 NOALLOC_MAX_TOKENS = 2 * 1024 * 1024

@@ -449,3 +449,39 @@ def test_row_lengths_around_the_kernels_borders(X, dtype, V):
     half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
     # the bound of the formula's test with |g| (1 + |ln p| + H) below 64
     assert bool(((d.double() - ref).abs() <= half * ref.abs() + 64 * 2.0 ** -17 * ref.abs() + 2.0 ** -17).all())
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("shape", ["equal", "ascending", "random"])
+def test_longest_rows(X, dtype, shape):
+    """Rows at the vocabulary's limit with the most alternatives, in orders that make the
+    alternatives' search as long as it gets."""
+    V = X.MAX_VOCAB
+    i = torch.arange(V, dtype=torch.float32)
+    x = {"equal": torch.full((V,), -2.0), "ascending": i * 2.0 ** -18,
+         "random": torch.randn(V, generator=torch.Generator().manual_seed(4))}[shape]
+    x = torch.stack([x, x.flip(0)]).cuda().to(DT[dtype])
+    t = torch.tensor([5, V - 1], dtype=torch.int32, device="cuda")
+    for k in (64, 3):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = _forward(X, x, t, k, status=status)
+        assert status.item() == 0
+        _check(x, t, out, k)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("V,k", [(600, 20), (2040, 32), (30000, 64), (50257, 40)])
+def test_more_equal_logits_than_are_kept(X, dtype, V, k):
+    """A few tokens above a plateau of equal ones, in many rows at once; and rows of which
+    each logit is a new best."""
+    gen = torch.Generator().manual_seed(V + k)
+    N = 301
+    x = torch.full((N, V), torch.finfo(DT[dtype]).min, dtype=DT[dtype])
+    t = torch.randint(0, V, (N,), generator=gen)
+    x[torch.arange(N), t] = 0.5
+    x[1::7] = (torch.arange(V) / 64).to(DT[dtype])
+    x[2::7, : V // 2] = -3.0
+    x = x.cuda()
+    out = _forward(X, x, t.to(torch.int32).cuda(), k)
+    idx = torch.sort(x.double(), dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(out["top_idx"].long(), idx)

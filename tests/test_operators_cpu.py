@@ -115,6 +115,18 @@ def test_top_k_limit_matches_the_header():
     assert int(re.search(r"#define\s+XMOD_MAX_TOP_K\s+(\d+)", open(header).read()).group(1)) == X.MAX_TOP_K
 
 
+def test_vocabulary_limit():
+    """Rows past the limit are refused before anything is launched."""
+    import os
+    import re
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "xmod.h")
+    assert re.search(r"#define\s+XMOD_MAX_VOCAB\s+\(1 << 22\)", open(header).read())
+    V = X.MAX_VOCAB + 1
+    assert V == 2 ** 22 + 1
+    assert _logprobs(V=V, ld=V) == X.ERR_UNSUPPORTED
+    assert _logprobs_bwd(V=V, ld=V, ldd=V) == X.ERR_UNSUPPORTED
+
+
 def test_binding_refuses_host_tensors():
     """Host memory is refused before any pointer is taken."""
     k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
