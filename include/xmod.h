@@ -436,14 +436,16 @@ typedef struct {
  * at position pos[m]; k and v are written to slot slot[m] of sequence seq[m], q to q_out.
  * Everything is computed in fp32 and rounded once, to the type it is stored in; E4M3
  * stores scale = max|x| / 448 over the head's values and the codes nearest to x / scale
- * (the quotient in fp32, ties to even). A head of zeros gets scale 0 (as do values below 2^-117, which are
- * stored as zeros); a head with an infinity or NaN gets a NaN scale and NaN codes.
+ * (the quotient in fp32, ties to even). A head of zeros gets scale 0 (as do values below
+ * 2^-117, which are stored as zeros); a head with an infinity or NaN gets a NaN scale and
+ * NaN codes.
  *   seq     [M] int32, or NULL (row m belongs to sequence m). A negative entry skips
  *           its row: nothing of it is read or written (q_out's row keeps its values).
  *   slot    [M] int32; the rows of one call must address distinct slots
  *   pos     [M] int32, or NULL (pos = slot)
  *   q_out   [M, n_heads * head_dim], row stride ldq (dtype), or NULL (q is not wanted);
- *           may be qkv itself with ldq = ldqkv (q in place), else must not overlap it
+ *           may be qkv itself with ldq = ldqkv (q in place; of one row any ldq), else must
+ *           not overlap it
  * A row whose sequence is not below n_seqs, whose slot is outside [0, max_pages *
  * page_size) or whose page is outside [0, n_pages) is skipped and reported through
  * status_out (a device int, or NULL) as for xmod_gather. Row strides must be multiples

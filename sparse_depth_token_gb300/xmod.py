@@ -432,12 +432,16 @@ def _vec(fn, t, dtype, n, dev):
     return t.data_ptr()
 
 
-def _mat(fn, t, dtype, rows, width, dev):
-    """(pointer, row stride) of a [rows, width] tensor with contiguous rows on device dev."""
+def _mat(fn, t, dtype, rows, width, dev, most=2 ** 31 - 1):
+    """(pointer, row stride) of a [rows, width] tensor with contiguous rows on device dev;
+    strides up to `most`."""
     if (t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, width)
             or (width > 1 and t.stride(1) != 1)):
         raise XmodError(fn, ERR_INVALID_ARG)
-    return t.data_ptr(), t.stride(0) if rows > 1 else width
+    ld = t.stride(0) if rows > 1 else width
+    if ld > most:
+        raise XmodError(fn, ERR_UNSUPPORTED)
+    return t.data_ptr(), ld
 
 
 def _elem(fn, dm, cache, dev):
@@ -499,8 +503,10 @@ def _logits(fn, t):
     if dt is None or t.dim() != 2:
         raise XmodError(fn, ERR_INVALID_ARG)
     N, V = t.shape
+    if V > MAX_VOCAB:
+        raise XmodError(fn, ERR_UNSUPPORTED)
     dev = _device(fn, t)
-    return (dt, N, V) + _mat(fn, t, t.dtype, N, V, dev) + (dev,)
+    return (dt, N, V) + _mat(fn, t, t.dtype, N, V, dev, 2 ** 62) + (dev,)
 
 
 def token_logprobs(logits, target=None, logp=None, entropy=None, lse=None, top_idx=None,
@@ -528,7 +534,7 @@ def token_logprobs_bwd(logits, target, lse, g_logp, dlogits, entropy=None, g_ent
     fn = "xmod_token_logprobs_bwd"
     dt, N, V, x, ld, dev = _logits(fn, logits)
     i32, f32 = _torch_module.int32, _torch_module.float32
-    d, ldd = _mat(fn, dlogits, logits.dtype, N, V, dev)
+    d, ldd = _mat(fn, dlogits, logits.dtype, N, V, dev, 2 ** 62)
     st = load().xmod_token_logprobs_bwd(
         dt, N, V, x, ld, _vec(fn, target, i32, N, dev), _vec(fn, lse, f32, N, dev),
         _vec(fn, entropy, f32, N, dev), _vec(fn, g_logp, f32, N, dev),

@@ -566,3 +566,38 @@ def test_binding_refusals(X):
     with pytest.raises(X.XmodError) as e:
         X.cache_attention(dm, c.handle, q, None, i, o, ws[:256])
     assert e.value.status == X.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_append_one_token_in_place(X, kind):
+    """A single row has no row stride of its own: its q may lie in place all the same."""
+    hq, hkv, hd, page = 4, 2, 64, 16
+    dtype, c, qkv, seq, slot, pos, gains, w = _append_case(X, kind, hq, hkv, hd, page, 1, True, THETA)
+    before = [t.clone() for t in c.tensors()]
+    x = qkv.clone()
+    X.cache_append(C.dims(X, hq, hkv, hd, dtype), c.handle, x, w, ints(seq.tolist()), ints(slot.tolist()),
+                   pos, q_out=x[:, :hq * hd])
+    _check_append(c, dtype, qkv, seq, slot, pos, gains, THETA, x[:, :hq * hd].contiguous(), hq, hkv, hd,
+                  [True], before)
+    assert torch.equal(x[:, hq * hd:], qkv[:, hq * hd:])
+
+
+def test_row_strides_past_32_bits_are_refused(X):
+    """The calls that take row strides as 32-bit numbers do not cut a longer one short."""
+    hq, hkv, hd = 4, 2, 64
+    c = C.Cache(X, [16, 16], hkv, hd, 16, "bf16", fill=0.5)
+    dm, width = C.dims(X, hq, hkv, hd, "bf16"), (hq + 2 * hkv) * hd
+    buf = torch.empty(2 ** 32 + 2 * width, dtype=torch.bfloat16, device="cuda")
+    far = buf.as_strided((2, width), (2 ** 32 + width, 1))
+    near = buf[:2 * width].view(2, width)
+    slot = ints([0, 1])
+    ws = torch.zeros(X.cache_attention_workspace_bytes(dm, 2), dtype=torch.uint8, device="cuda")
+    o = torch.empty(2, hq * hd, dtype=torch.bfloat16, device="cuda")
+    held = [t.clone() for t in c.tensors()]
+    for call in (lambda: X.cache_append(dm, c.handle, far, None, None, slot),
+                 lambda: X.cache_append(dm, c.handle, near, None, None, slot, q_out=far[:, :hq * hd]),
+                 lambda: X.cache_attention(dm, c.handle, far[:, :hq * hd], None, slot, o, ws)):
+        with pytest.raises(X.XmodError) as e:
+            call()
+        assert e.value.status == X.ERR_UNSUPPORTED
+    assert all(torch.equal(a, b) for a, b in zip(held, c.tensors()))

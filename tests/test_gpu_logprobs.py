@@ -485,3 +485,15 @@ def test_more_equal_logits_than_are_kept(X, dtype, V, k):
     out = _forward(X, x, t.to(torch.int32).cuda(), k)
     idx = torch.sort(x.double(), dim=1, descending=True, stable=True).indices[:, :k]
     assert torch.equal(out["top_idx"].long(), idx)
+
+
+def test_rows_past_the_vocabulary_limit_are_refused(X):
+    """Also one whose length is past 32 bits, which the call's number would cut short."""
+    buf = torch.empty(2 ** 32 + 100, dtype=torch.bfloat16, device="cuda")
+    f = torch.empty(1, device="cuda")
+    for V in (X.MAX_VOCAB + 1, 2 ** 32 + 100):
+        x = buf[:V].view(1, V)
+        for call in (lambda: X.token_logprobs(x, None, lse=f), lambda: X.token_logprobs_bwd(x, None, f, None, x)):
+            with pytest.raises(X.XmodError) as e:
+                call()
+            assert e.value.status == X.ERR_UNSUPPORTED
