@@ -34,8 +34,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // shared memory; short rows go to single warps (below).
 //
 // Measured: 4096 rows of 50257, bf16 (412 MB): 67 us, 6.2 TB/s, 0.91 of what a copy reaches;
-// with 5 alternatives 78 us, 0.78 (the finisher takes issue slots); fp32 (823 MB), with 5
-// alternatives 126 us, 0.96; 8 rows with 20 alternatives 10.5 us, without 4.4.
+// with 5 alternatives 76 us, 0.80 (the finisher takes issue slots); fp32 (823 MB), with 5
+// alternatives 124 us, 0.98; 8 rows with 20 alternatives 10.7 us, without 4.1.
 //
 // The alternatives. Logits are ranked by 64-bit keys, the value's order above the inverted
 // token number: keys are distinct, so ties need no care. All that the consumers do for them
@@ -51,6 +51,7 @@ constexpr int kChunk = 16384;      // bytes
 constexpr int kLpStages = 2;
 constexpr int kLpCtas = 4;         // an SM
 constexpr int kVecs = kChunk / 16 / kLpThreads;   // vectors a thread takes of a chunk
+constexpr int kTail = 2;            // vectors at a time of a row's last chunk
 constexpr int kSlots = 8;          // maxima a thread leaves of a row, each of `step` chunks
 // Logits that a finisher keeps while it looks. 8 rows of 50257 bf16 logits with 20
 // alternatives, all but three at the type's lowest value: 99 us (192: 112, 512: 300; reading
@@ -232,7 +233,8 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, Finisher& sh,
     best[q] = lane + 32 * q < s.nvec ? order_of(m) : 0u;
   }
   // the k-th largest of the threads' orders: a few by taking the largest away, more by the
-  // largest bound that k threads reach, bit by bit
+  // largest bound that k threads reach, bit by bit (4096 rows of 50257, bf16, either way: 5
+  // alternatives 76.5 and 78.8 us, 20 of them 101 and 96)
   uint32_t bound = 0;
   if (k <= 12) {
     uint32_t left[Q];
@@ -391,7 +393,7 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
 
 // Rows of at most 256 vectors (4 KB): a warp holds one in registers, eight vectors a lane, so
 // the maximum comes first and nothing is read twice but the few vectors behind the bound.
-// 4096 rows of 1000 logits, bf16, with 5 alternatives: 7.0 us, 18 us by the ring.
+// 4096 rows of 1000 logits, bf16, with 5 alternatives: 7.3 us, 18 us by the ring.
 constexpr int kShortVecs = 8, kShortWarps = 4, kShortTopK = 32;
 
 template <typename T, bool ENT>
@@ -668,25 +670,32 @@ token_logprobs_kernel(const LogprobArgs a) {
               if (j < s.head) vec_clear<T>(x[0], j);
           }
           absorb(x);
-        } else {   // the row's last chunk: what there is of it, a vector at a time
-#pragma unroll 1
-          for (int i = 0; v0 + warp * 32 + i * kLpThreads < s.nvec; ++i) {
-            const int v = v0 + tid + i * kLpThreads;
-            const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-            uint4 x[1] = {make_uint4(ninf, ninf, ninf, ninf)};
-            if (v < s.full) {
-              x[0] = buf[tid + i * kLpThreads];
-              if (v == 0) {
+        } else {   // the row's last chunk: what there is of it, two vectors at a time
+          // (4096 rows of 16000 logits, bf16: 29.0 us; one by one 31.9, four 27.7, but those
+          // cost 81 instead of 76 where 50257 logits with 5 alternatives are wanted)
+          const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+          // the last vector, not wholly inside the buffer, by elements
+          uint4 part = make_uint4(ninf, ninf, ninf, ninf);
+          if (s.full < s.nvec && (s.full - v0) % kLpThreads == tid) {
+            const T* p = reinterpret_cast<const T*>(s.vecs + s.full);
+            T* e = reinterpret_cast<T*>(&part);
 #pragma unroll
-                for (int j = 0; j < VE; ++j)
-                  if (j < s.head) vec_clear<T>(x[0], j);
-              }
-            } else if (v < s.nvec) {   // the last elements, one by one
-              const T* p = reinterpret_cast<const T*>(s.vecs + v);
-              T* e = reinterpret_cast<T*>(&x[0]);
+            for (int j = 0; j < VE; ++j)
+              if (s.full * VE + j >= s.head && s.full * VE + j < s.head + s.count) e[j] = p[j];
+          }
+#pragma unroll 1
+          for (int v = v0 + tid; v - lane < s.nvec; v += kTail * kLpThreads) {
+            uint4 x[kTail];
+#pragma unroll
+            for (int i = 0; i < kTail; ++i) {
+              const int vi = v + i * kLpThreads;
+              x[i] = vi == s.full ? part : make_uint4(ninf, ninf, ninf, ninf);
+              if (vi < s.full) x[i] = buf[vi - v0];
+            }
+            if (v == 0) {
 #pragma unroll
               for (int j = 0; j < VE; ++j)
-                if (v * VE + j >= s.head && v * VE + j < s.head + s.count) e[j] = p[j];
+                if (j < s.head) vec_clear<T>(x[0], j);
             }
             absorb(x);
           }
@@ -858,8 +867,9 @@ cudaError_t launch_logprobs_fin(const Ctx& c, const LogprobArgs& a0) {
 
 // Short rows go to warps. Else a second finisher where one would hold the rows up: rows of one
 // or two chunks, or many alternatives (it costs the others registers and issue slots). 4096
-// rows, bf16, one and two finishers: 50257 logits with 5 alternatives 77.7 and 78.8 us, with
-// 64 of them 174 and 141; 1000 logits with 5 alternatives (now a warp's) 26 and 18 us.
+// rows, bf16, one and two finishers: 50257 logits with 5 alternatives 76.4 and 80.5 us, with
+// 64 of them 184 and 146; 8191 logits with 5 alternatives 37.8 and 33.8, 16000 44.5 and 41.0,
+// 20000 47.6 and 46.9.
 template <typename T, bool ENT>
 cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
   const int VE = 16 / (int)sizeof(T);
