@@ -853,18 +853,20 @@ __global__ void __launch_bounds__(128, f32_ctas<HD>()) cache_attention_f32_kerne
       const float4* kp = reinterpret_cast<const float4*>((const float*)a.k + row0 * HD) + l8;
       const float4* vp = reinterpret_cast<const float4*>((const float*)a.v + row0 * HD) + l8;
       float s[4][ROWS];
-      float4 kk[4][CH], vv[4][CH];   // the values on their way with the keys
+      // the values on their way with the keys (plain loads: the launch may begin while the
+      // kernel before it still writes the cache, so it is not read-only to this one)
+      float4 kk[4][CH], vv[4][CH];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-          kk[j][c] = key0 + 4 * j + sub < n ? __ldg(kp + j * HD + c * 8)
+          kk[j][c] = key0 + 4 * j + sub < n ? kp[j * HD + c * 8]
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-          vv[j][c] = key0 + 4 * j + sub < n ? __ldg(vp + j * HD + c * 8)
+          vv[j][c] = key0 + 4 * j + sub < n ? vp[j * HD + c * 8]
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

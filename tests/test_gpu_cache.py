@@ -601,3 +601,35 @@ def test_row_strides_past_32_bits_are_refused(X):
             call()
         assert e.value.status == X.ERR_UNSUPPORTED
     assert all(torch.equal(a, b) for a, b in zip(held, c.tensors()))
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_rewritten_slots_are_read_anew(X, kind):
+    """Slots that a call reads, the next overwrites and the one after reads again, queued
+    without a pause: the same bits as with one after each call."""
+    dtype, e4m3 = KINDS[kind]
+    hq, hkv, hd, page, M, n = 8, 4, 64, 16, 6, 200
+    dm = C.dims(X, hq, hkv, hd, dtype)
+    gen = torch.Generator().manual_seed(11)
+    qkv = torch.randn(24, M, (hq + 2 * hkv) * hd, generator=gen).cuda().to(C.DT[dtype])
+    slots = [ints([(37 * i + 5 * m) % n for m in range(M)]) for i in range(3)]
+    lens = ints([n - m for m in range(M)])
+    ws = torch.zeros(X.cache_attention_workspace_bytes(dm, M), dtype=torch.uint8, device="cuda")
+    runs = []
+    for pause in (True, False):
+        c = C.Cache(X, [208] * M, hkv, hd, page, dtype, e4m3)
+        for s in range(M):
+            c.fill(s, n, s)
+        o = torch.empty(24, M, hq * hd, dtype=C.DT[dtype], device="cuda")
+        torch.cuda.synchronize()
+        for i in range(24):
+            X.cache_append(dm, c.handle, qkv[i], None, None, slots[i % 3])
+            if pause:
+                torch.cuda.synchronize()
+            X.cache_attention(dm, c.handle, qkv[i, :, :hq * hd], None, lens, o[i], ws)
+            if pause:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        runs.append(o)
+    assert torch.equal(*(r.view(torch.uint8) for r in runs))
+    assert bool(runs[0].float().isfinite().all())
