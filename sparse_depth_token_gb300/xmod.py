@@ -233,7 +233,7 @@ def layer_weights(tensors: dict, varsigma: float = 1.0, rope_theta: float = 0.0)
     lw = LayerWeights(*[_p(tensors.get(n)) for n in LayerWeights.NAMES], float(varsigma),
                       _p(tensors.get("q_norm")), _p(tensors.get("k_norm")), float(rope_theta))
     lw._keep = dict(tensors)
-    lw._gains = [(t.dtype, t.numel(), t.get_device())
+    lw._gains = [(t.dtype, t.numel(), t.is_contiguous(), t.get_device())
                  for t in (tensors.get("q_norm"), tensors.get("k_norm")) if hasattr(t, "dtype")]
     return lw
 
@@ -444,6 +444,14 @@ def _mat(fn, t, dtype, rows, width, dev, most=2 ** 31 - 1):
     return t.data_ptr(), ld
 
 
+def _check_gains(fn, w, dtype, n, dev):
+    """The QK-norm gains that a LayerWeights was made of are read as n elements of that dtype
+    on end, on device dev."""
+    for g in getattr(w, "_gains", ()):
+        if g != (dtype, n, True, dev):
+            raise XmodError(fn, ERR_INVALID_ARG)
+
+
 def _elem(fn, dm, cache, dev):
     """torch dtype of the dims' elements; the cache has to be of these dims and there."""
     el = _torch_module.bfloat16 if dm.dtype == BF16 else _torch_module.float32
@@ -464,9 +472,7 @@ def cache_append(dm, cache: KVCache, qkv, w, seq, slot, pos=None, q_out=None, st
     qw = dm.n_heads * dm.head_dim
     qkv_p, ld = _mat(fn, qkv, el, M, qw + 2 * dm.n_kv_heads * dm.head_dim, dev)
     q_p, ldq = _mat(fn, q_out, el, M, qw, dev) if q_out is not None else (None, 0)
-    for g in getattr(w, "_gains", ()):
-        if g != (el, dm.head_dim, dev):
-            raise XmodError(fn, ERR_INVALID_ARG)
+    _check_gains(fn, w, el, dm.head_dim, dev)
     st = load().xmod_cache_append(
         dm, cache, M, qkv_p, ld, w, _vec(fn, seq, i32, M, dev), _vec(fn, slot, i32, M, dev),
         _vec(fn, pos, i32, M, dev), q_p, ldq, _vec(fn, status, i32, 1, dev),
