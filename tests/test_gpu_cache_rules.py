@@ -57,3 +57,42 @@ def test_gains_that_are_not_contiguous_are_refused(X, which, layout):
                        ints([0] * M), None, q)
     assert e.value.status == X.ERR_INVALID_ARG
     assert bool((q == -3).all()) and all(torch.equal(a, b) for a, b in zip(before, c.tensors()))
+
+
+# ------------------------------------------------------------------ code bytes
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_e4m3_codes_are_the_quotients(X, hd):
+    """Code bytes and scales of k and v (copied: no norm, no rotation) equal amax / 448 and
+    the fp32 quotient x / scale rounded to e4m3, both computed on the host. bf16 values over
+    a scale often lie exactly between two codes, where any other rounding of the quotient
+    shows; heads from the smallest scales to the largest."""
+    hkv, M = 4, 600
+    g = torch.Generator().manual_seed(hd)
+    x = torch.randn(M, 2 * hkv, hd, generator=g)
+    x[:, :, 0] *= 1 + 2 * torch.rand(M, 2 * hkv, generator=g)
+    # scales down to the smallest normal number and below it, and up to the largest
+    size = torch.tensor([0.0] * 8 + [-121, -119.5, -118, -110, -90, -60, 60, 110, 123.0])
+    x *= torch.exp2(size[torch.arange(M) % len(size)])[:, None, None]
+    x[0, :, :] = 1.3671875      # 200 times the scale of 3.0625: between 192 and 208
+    x[0, :, 1] = 3.0625
+    x[1] = -0.0
+    x = x.bfloat16()
+    c = C.Cache(X, [M], hkv, hd, 16, "bf16", True, fill=1.0)
+    qkv = torch.cat([torch.zeros(M, hkv, hd, dtype=torch.bfloat16), x], 1).reshape(M, -1).cuda()
+    X.cache_append(C.dims(X, hkv, hkv, hd, "bf16"), c.handle, qkv, None, ints([0] * M), ints(list(range(M))))
+    x = x.float()
+    scale = x.abs().amax(-1) / torch.tensor(448.0)
+    scale = torch.where(scale < 2.0 ** -126, torch.zeros_like(scale), scale)
+    by = torch.where(scale == 0, torch.full_like(scale, math.inf), scale)
+    want = (x / by[..., None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert want[0, 0, 2] == torch.tensor(192.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert 0 < int((scale == 0).sum()) < scale.numel() // 2
+    pages = torch.tensor([c.place(0, i)[0] for i in range(M)]).cuda()
+    offs = torch.arange(M).cuda() % c.page
+    for n, name in enumerate(("k", "v")):
+        code = getattr(c, name).view(torch.uint8)[pages, :, offs].cpu()
+        sc = getattr(c, name + "_scale")[pages, :, offs].cpu()
+        assert torch.equal(sc, scale[:, n * hkv:(n + 1) * hkv])
+        off = code != want[:, n * hkv:(n + 1) * hkv]
+        assert not bool(off.any()), (name, int(off.sum()), off.nonzero()[:4].tolist())
