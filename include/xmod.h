@@ -411,7 +411,7 @@ XMOD_API int xmod_router_topk_noalloc(const xmod_dims* dims, int K, const void* 
  *
  * Format of a cache's values. NATIVE: dims->dtype. E4M3 (with dims->dtype bf16): 8-bit
  * floating point (4 exponent bits, 3 mantissa bits, largest value 448) with one fp32
- * scale per slot and KV head; a code stands for code * scale. */
+ * scale per slot and KV head; a code stands for code * scale, whatever the scale's sign. */
 typedef enum { XMOD_CACHE_NATIVE = 0, XMOD_CACHE_E4M3 = 1 } xmod_cache_format;
 
 /* One layer's paged key/value cache (device pointers, 16-byte aligned, caller-owned).

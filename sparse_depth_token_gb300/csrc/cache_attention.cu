@@ -581,7 +581,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       for (int j = 0; j < 2 * C::SUB; ++j) {
 #pragma unroll
         for (int i = 0; i < (PAIR ? 1 : 2); ++i) top[i] = fmaxf(top[i], fmaxf(s[j][2 * i], s[j][2 * i + 1]));
-        if constexpr (FP8) vtop = fmaxf(vtop, fmaxf(vs[j][0], vs[j][1]));
+        if constexpr (FP8) vtop = fmaxf(vtop, fmaxf(fabsf(vs[j][0]), fabsf(vs[j][1])));
       }
       float keep[2], floor2[2];
 #pragma unroll

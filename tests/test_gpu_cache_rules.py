@@ -96,3 +96,51 @@ def test_e4m3_codes_are_the_quotients(X, hd):
         assert torch.equal(sc, scale[:, n * hkv:(n + 1) * hkv])
         off = code != want[:, n * hkv:(n + 1) * hkv]
         assert not bool(off.any()), (name, int(off.sum()), off.nonzero()[:4].tolist())
+
+
+# ------------------------------------------------------------------ scales of e4m3 values
+
+def _check_e4m3_rows(c, q, lens, o, lse, hq, hd):
+    """Rows m over sequence m against 64 bits. Beside the errors of attention_ref, a weight
+    p |scale| below 2^-28 of the row's largest (or of 2^-112) is held to half of f16's last
+    step there: 2^-39 of a power of two at most twice the largest, times the codes."""
+    for m, n in enumerate(lens):
+        ref, rl, bound, dz = C.attention_ref(c, q[m].reshape(hq, hd), m, n, P_ROUND["e4m3"])
+        spread = bound / (2 * dz + 2.0 ** -18 + P_ROUND["e4m3"])[:, None]
+        rep = hq // c.hkv
+        k = c.rows("k", m, n).repeat_interleave(rep, 0)
+        qm = q[m].reshape(hq, hd).double()
+        z = torch.einsum("hd,hnd->hn", qm, k) / math.sqrt(hd)
+        w = torch.exp(z - z.amax(1, keepdim=True))
+        # the error of the scores that count (attention_ref's is that of all)
+        dz = torch.where(w > 2.0 ** -60, torch.einsum("hd,hnd->hn", qm.abs(), k.abs()), torch.zeros_like(w))
+        dz = dz.amax(1) * math.sqrt(hd) * 2.0 ** -24
+        pages = torch.from_numpy(c.table_np[m, :-(-n // c.page)].astype(np.int64)).cuda()
+        sc = c.v_scale[pages].double().permute(1, 0, 2).reshape(c.hkv, -1)[:, :n].repeat_interleave(rep, 0)
+        codes = c.v.view(torch.uint8)[pages].view(torch.float8_e4m3fn).double().abs()
+        codes = codes.permute(1, 0, 2, 3).reshape(c.hkv, -1, hd)[:, :n].sum(1).repeat_interleave(rep, 0)
+        largest = (w * sc.abs()).amax(1).clamp(min=2.0 ** -113)
+        bound = spread * (2 * dz + 2.0 ** -18 + P_ROUND["e4m3"])[:, None] + (
+            2.0 ** -38 * largest / w.sum(1))[:, None] * codes
+        err = (o[m].view(hq, hd).double() - ref).abs() - bound - C.HALF["bf16"] * (ref.abs() + bound)
+        assert float(err.max()) <= 0, (m, n, float(err.max()), float(ref.abs().max()))
+        le = (lse[m].double() - rl).abs() - 2 * dz - 2.0 ** -18 - 2.0 ** -22 * rl.abs()
+        assert float(le.max()) <= 0, (m, n, float(le.max()))
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(12, 4, 128), (16, 1, 64), (2, 2, 32)])
+@pytest.mark.parametrize("sign", ["all", "some"])
+def test_negative_scales(X, hq, hkv, hd, sign):
+    """A code stands for code * scale, whatever the scale's sign."""
+    lens = [1, 64, 300, 1000]
+    c = C.Cache(X, lens, hkv, hd, 16, "bf16", True)
+    g = torch.Generator().manual_seed(5)
+    for m, n in enumerate(lens):
+        c.fill(m, n, m)
+        for name in ("k_scale", "v_scale"):
+            s = getattr(c, name)
+            s *= -1.0 if sign == "all" else torch.where(torch.rand(s.shape, generator=g) < 0.5, -1.0, 1.0).cuda()
+    q = torch.randn(len(lens), hq * hd, generator=g).cuda().bfloat16()
+    o, lse, status = attend(X, c, q, range(len(lens)), lens, hq, hd, "bf16")
+    assert status == X.OK
+    _check_e4m3_rows(c, q, lens, o, lse, hq, hd)
