@@ -144,3 +144,37 @@ def test_negative_scales(X, hq, hkv, hd, sign):
     o, lse, status = attend(X, c, q, range(len(lens)), lens, hq, hd, "bf16")
     assert status == X.OK
     _check_e4m3_rows(c, q, lens, o, lse, hq, hd)
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(12, 4, 128), (16, 1, 64), (2, 2, 32)])
+@pytest.mark.parametrize("pattern", ["rising", "falling", "outlier first", "outlier inside", "outlier last", "tiny",
+                                     "huge", "mixed"])
+def test_scales_of_all_sizes(X, hq, hkv, hd, pattern):
+    """Value scales that span many powers of two along a sequence, and one key of nearly no
+    probability (about 2^-200) with a scale 2^60 times the others': its scale must not cost
+    the other keys' weights their bits."""
+    lens = [70, 400, 2600]
+    c = C.Cache(X, lens, hkv, hd, 32, "bf16", True)
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(len(lens), hq * hd, generator=g).abs().cuda().bfloat16()
+    for m, n in enumerate(lens):
+        c.fill(m, n, m)
+        jitter = 0.5 + torch.rand(hkv, n, generator=g, dtype=torch.float64)
+        steps = {"rising": lambda i: 60 * i / n - 30, "falling": lambda i: 30 - 60 * i / n,
+                 "tiny": lambda i: 0 * i - 119, "huge": lambda i: 0 * i + 112,
+                 "mixed": lambda i: 20 * torch.sin(i / 7)}.get(pattern, lambda i: 0 * i - 7)
+        pages = torch.from_numpy(c.table_np[m, :-(-n // c.page)].astype(np.int64)).cuda()
+        sc = torch.full((hkv, len(pages) * c.page), math.nan, dtype=torch.float64)
+        sc[:, :n] = torch.exp2(steps(torch.arange(n, dtype=torch.float64))) * jitter
+        c.v_scale[pages] = sc.view(hkv, -1, c.page).permute(1, 0, 2).float().cuda()
+        if pattern.startswith("outlier"):
+            at = {"first": 0, "inside": n // 2 + 3, "last": n - 1}[pattern.split()[1]]
+            p, off = c.place(m, at)
+            c.k[p, :, off] = torch.full((hkv, hd), -448.0, device="cuda").to(torch.float8_e4m3fn)
+            # scores of about -150: the mean |q| is 0.8
+            c.k_scale[p, :, off] = 150 / 448 / (0.8 * math.sqrt(hd))
+            c.v_scale[p, :, off] = 2.0 ** 53
+    o, lse, status = attend(X, c, q, range(len(lens)), lens, hq, hd, "bf16")
+    assert status == X.OK
+    assert bool(o.isfinite().all())
+    _check_e4m3_rows(c, q, lens, o, lse, hq, hd)
