@@ -474,7 +474,9 @@ XMOD_API size_t xmod_cache_attention_workspace_bytes(const xmod_dims* dims, int 
  * Slots at or after len[m] have no influence, whatever their pages hold. Products are
  * accumulated in fp32; the probabilities keep at least 16 bits of mantissa where they
  * weight the values. With E4M3 they go in times the values' scales and keep 11 bits, down to
- * 2^-28 of the largest |p * scale| (or of 2^-112, if that is larger); below, 2^-39 of it.
+ * 2^-28 of the row's largest |p * scale| (or of 2^-112, if that is larger); smaller ones are
+ * off by at most 2^-38 of it. E4M3 rounds query elements below 2^-17 of
+ * their head's largest one, by at most 2^-25 of it. Scores beyond fp32's range give NaN.
  * Device checks (status word of ws): a sequence not below n_seqs skips its row; a len
  * outside its range is clamped into it; a page outside [0, n_pages) is read as page 0.
  * The result does not depend on the other rows of the call beyond fp32 rounding, and two

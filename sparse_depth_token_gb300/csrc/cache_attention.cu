@@ -498,7 +498,9 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             float p2 = __uint_as_float(__float_as_uint(big) & 0x7f800000u);   // its power of two
-            if (!(p2 >= 1e-30f && p2 <= 1e30f)) p2 = 1.f;   // zeros, infinities, NaN: as they are
+            // zeros and tiny rows: 2^-120, whose product with to_log2 is a normal number; rows with
+            // an infinity: as they are
+            p2 = p2 == INFINITY ? 1.f : fmaxf(p2, 0x1p-120f);
             const float inv = 1.f / p2;
             q_mul[i] *= p2;
 #pragma unroll

@@ -178,3 +178,42 @@ def test_scales_of_all_sizes(X, hq, hkv, hd, pattern):
     assert status == X.OK
     assert bool(o.isfinite().all())
     _check_e4m3_rows(c, q, lens, o, lse, hq, hd)
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(12, 4, 128), (16, 1, 64), (2, 2, 32)])
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_queries_of_all_sizes(X, kind, hq, hkv, hd):
+    """Queries from 2^-126 to 2^122, one element each: scores are one product, so that the
+    largest of far apart ones takes all the weight, and tiny ones weight all keys alike."""
+    dtype, e4m3 = KINDS[kind]
+    n = 100
+    lens = [n] * 6
+    c = C.Cache(X, lens, hkv, hd, 16, dtype, e4m3)
+    q = torch.zeros(len(lens), hq, hd)
+    for m, size in enumerate((2.0 ** -126, 2.0 ** -104, 1.0, 2.0 ** 98, 2.0 ** 101, 2.0 ** 122)):
+        c.fill(m, n, m)
+        q[m, :, 5] = size
+    for t in c.tensors():       # the keys' element 5: codes far apart, one scale
+        if t is c.k:
+            for m in range(len(lens)):
+                for i in range(n):
+                    p, off = c.place(m, i)
+                    v = (8 + (i * 7 % n) // 8) * (1.0 if e4m3 else 0.125) if i % 8 == 0 else 1.0
+                    c.k[p, :, off, 5] = torch.full((hkv,), v, device="cuda").to(c.k.dtype)
+        elif t is c.k_scale:
+            t.fill_(0.125)
+    qd = q.view(len(lens), -1).cuda().to(C.DT[dtype])
+    o, lse, status = attend(X, c, qd, range(len(lens)), lens, hq, hd, dtype)
+    assert status == X.OK
+    for m in range(len(lens)):
+        ref, rl, bound, dz = C.attention_ref(c, qd[m].reshape(hq, hd), m, n, P_ROUND[kind])
+        big = float(q[m].max()) > 2
+        # one product: a score's relative error is that of its factors (rsqrt's 2 ulp, log2 e's
+        # and ln 2's roundings and the products', 2^-21 in all); where the scores are far apart
+        # none of it reaches the weights
+        z = float(rl.abs().max())
+        bound = bound / (2 * dz + 2.0 ** -18 + P_ROUND[kind])[:, None] * (
+            2.0 ** -18 + P_ROUND[kind] + (0.0 if big else 2.0 ** -20))
+        err = (o[m].view(hq, hd).double() - ref).abs() - bound - C.HALF[dtype] * (ref.abs() + bound)
+        assert float(err.max()) <= 0, (m, float(err.max()))
+        assert float((lse[m].double() - rl).abs().max()) <= 2.0 ** -17 + 2.0 ** -20 * z, m
