@@ -396,8 +396,8 @@ def stack_bwd(dm, K, A, N0, N1, gate, layers, x, bias, dy, route_coef, dx, grads
 def kv_cache(k, v, table, k_scale=None, v_scale=None) -> KVCache:
     """KVCache from device tensors: k, v [n_pages, n_kv_heads, page_size, head_dim]
     contiguous (with k_scale / v_scale [n_pages, n_kv_heads, page_size] fp32: e4m3 codes,
-    one byte each), table [n_seqs, max_pages] int32 contiguous. The struct keeps the
-    tensors, so their memory outlives every call using it."""
+    as float8_e4m3fn or plain bytes), table [n_seqs, max_pages] int32 contiguous. The struct
+    keeps the tensors, so their memory outlives every call using it."""
     T = _torch()
     e4m3 = k_scale is not None
     ts = (k, v, table) + ((k_scale, v_scale) if e4m3 else ())
@@ -405,7 +405,7 @@ def kv_cache(k, v, table, k_scale=None, v_scale=None) -> KVCache:
             for t in ts) or k.dim() != 4
             or table.dim() != 2 or k.shape != v.shape or k.dtype is not v.dtype
             or table.dtype is not T.int32 or (v_scale is not None) != e4m3
-            or (e4m3 and (k.element_size() != 1 or any(
+            or (e4m3 and (k.dtype not in (T.float8_e4m3fn, T.uint8, T.int8) or any(
                 t.shape != k.shape[:3] or t.dtype is not T.float32 for t in ts[3:])))):
         raise XmodError("kv_cache", ERR_INVALID_ARG)
     c = KVCache(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(table), k.shape[0], k.shape[2],

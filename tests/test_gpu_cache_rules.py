@@ -217,3 +217,18 @@ def test_queries_of_all_sizes(X, kind, hq, hkv, hd):
         err = (o[m].view(hq, hd).double() - ref).abs() - bound - C.HALF[dtype] * (ref.abs() + bound)
         assert float(err.max()) <= 0, (m, float(err.max()))
         assert float((lse[m].double() - rl).abs().max()) <= 2.0 ** -17 + 2.0 ** -20 * z, m
+
+
+def test_codes_of_another_8_bit_type_are_refused(X):
+    """Codes are e4m3 or plain bytes of them; other 8-bit floating types would be misread."""
+    shape = (4, 2, 16, 64)
+    scale = torch.ones(shape[:3], device="cuda")
+    table = ints([[0, 1], [2, 3]])
+    for t in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz):
+        x = torch.zeros(shape, dtype=torch.uint8, device="cuda").view(t)
+        with pytest.raises(X.XmodError) as e:
+            X.kv_cache(x, x.clone(), table, scale, scale.clone())
+        assert e.value.status == X.ERR_INVALID_ARG
+    for t in (torch.float8_e4m3fn, torch.uint8, torch.int8):
+        x = torch.zeros(shape, dtype=torch.uint8, device="cuda").view(t)
+        X.kv_cache(x, x.clone(), table, scale, scale.clone())
