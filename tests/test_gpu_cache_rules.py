@@ -232,3 +232,64 @@ def test_codes_of_another_8_bit_type_are_refused(X):
     for t in (torch.float8_e4m3fn, torch.uint8, torch.int8):
         x = torch.zeros(shape, dtype=torch.uint8, device="cuda").view(t)
         X.kv_cache(x, x.clone(), table, scale, scale.clone())
+
+
+# ------------------------------------------------------------------ places
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_append_past_32_bit_offsets(X, kind):
+    """The slot that the append writes held NaN; k and v (copied), or their codes and scales,
+    stand there afterwards and nothing beside them has changed."""
+    dtype, e4m3 = KINDS[kind]
+    hkv, hd, page, hq = 8, 128, 64, 16
+    c = C.Cache(X, [200], hkv, hd, page, dtype, e4m3, first_page=(2 ** 32 + 2 ** 20) // (hkv * hd * page))
+    assert c.k.numel() > 2 ** 32
+    c.fill(0, 199, 7)
+    pages = torch.from_numpy(c.table_np[0].astype(np.int64)).cuda()
+    raw = lambda t: t.view(torch.uint8) if t.element_size() == 1 else t  # noqa: E731
+    bits = lambda t: t.contiguous().view(torch.uint8)  # noqa: E731
+    before = [raw(t)[pages].clone() for t in c.tensors()]
+    p, off = c.place(0, 199)
+    assert not bool(c.k[p, :, off].double().isfinite().any())
+    qkv = torch.randn(1, (hq + 2 * hkv) * hd, generator=torch.Generator().manual_seed(6)).cuda().to(C.DT[dtype])
+    X.cache_append(C.dims(X, hq, hkv, hd, dtype), c.handle, qkv, None, None, ints([199]))
+    for i, name in enumerate(("k", "v")):
+        x = qkv[0, (hq + i * hkv) * hd:(hq + (i + 1) * hkv) * hd].view(hkv, hd)
+        got = getattr(c, name)[p, :, off]
+        if e4m3:
+            x = x.float().cpu()
+            scale = x.abs().amax(-1) / torch.tensor(448.0)
+            assert torch.equal(getattr(c, name + "_scale")[p, :, off].cpu(), scale)
+            x = (x / scale[:, None]).to(torch.float8_e4m3fn)
+        assert torch.equal(bits(got.cpu()), bits(x.cpu()))
+    at = c.table_np[0].tolist().index(p)
+    for t, b in zip(c.tensors(), before):
+        now = raw(t)[pages].clone()
+        now[at, :, off] = b[at, :, off]
+        assert torch.equal(bits(now), bits(b))
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("page", [16, 64])
+def test_pages_outside_the_cache_are_read_as_page_0(X, kind, page):
+    """The same bits as with the entry 0 in the table, and a report; rows that do not need
+    the entry are not touched by it."""
+    dtype, e4m3 = KINDS[kind]
+    hq, hkv, hd, n = 8, 2, 64, 3 * page - 5
+    c = C.Cache(X, [3 * page, 3 * page], hkv, hd, page, dtype, e4m3)
+    for s in range(2):
+        c.fill(s, 3 * page, s)
+    first = int(c.table_np[0, 0])       # its place becomes page 0's: every page read holds numbers
+    for t in c.tensors():
+        t = t.view(torch.uint8) if t.element_size() == 1 else t
+        t[0] = t[first]
+    q = torch.randn(2, hq * hd, generator=torch.Generator().manual_seed(5)).cuda().to(C.DT[dtype])
+    c.table[0, 1] = 0
+    want = attend(X, c, q, [0, 1], [n, n], hq, hd, dtype)
+    assert want[2] == X.OK and bool(want[0].isfinite().all())
+    for bad in (-1, c.n_pages, 2 ** 31 - 1, -2 ** 31):
+        c.table[0, 1] = bad
+        got = attend(X, c, q, [0, 1], [n, n], hq, hd, dtype)
+        assert got[2] == X.ERR_DEVICE_CHECK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert attend(X, c, q, [0, 1], [page, n], hq, hd, dtype)[2] == X.OK
