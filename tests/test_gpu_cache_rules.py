@@ -293,3 +293,35 @@ def test_pages_outside_the_cache_are_read_as_page_0(X, kind, page):
         assert got[2] == X.ERR_DEVICE_CHECK
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert attend(X, c, q, [0, 1], [page, n], hq, hd, dtype)[2] == X.OK
+
+
+# ------------------------------------------------------------------ alone and in a batch
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("hq,hkv,hd", [(12, 4, 128), (16, 1, 64)])
+def test_rows_alone_and_in_batches(X, kind, hq, hkv, hd):
+    """The other rows of a call move the borders of the split, and with them the maximum that
+    a weight is rounded against: the same row alone and in batches differs by the weights'
+    stated rounding on both sides (and fp32's) at most."""
+    dtype, e4m3 = KINDS[kind]
+    lens = [700, 64, 3000, 129, 1, 1500]
+    M = len(lens)
+    c = C.Cache(X, lens, hkv, hd, 16, dtype, e4m3)
+    for m, n in enumerate(lens):
+        c.fill(m, n, m, 2.0)
+    q = torch.randn(M, hq * hd, generator=torch.Generator().manual_seed(9)).cuda().to(C.DT[dtype])
+    runs = []
+    for rows in [[m] for m in range(M)] + [[0, 1], [2, 3], [4, 5], [1, 2, 3], list(range(M)), [2] * 9 + [0, 5] * 4]:
+        o, lse, status = attend(X, c, q[rows], rows, [lens[m] for m in rows], hq, hd, dtype)
+        assert status == X.OK
+        runs.append((rows, o.double(), lse.double()))
+    for m, n in enumerate(lens):
+        ref, rl, bound, dz = C.attention_ref(c, q[m].reshape(hq, hd), m, n, P_ROUND[kind])
+        spread = bound / (2 * dz + 2.0 ** -18 + P_ROUND[kind])[:, None]
+        seen = [(o[i].view(hq, hd), lse[i]) for rows, o, lse in runs for i, r in enumerate(rows) if r == m]
+        assert len(seen) >= 3
+        for o, lse in seen[1:]:
+            # fp32's part: exp and the sums, 2^-18 on either side; the scores are the same bits
+            tol = spread * 2 * (P_ROUND[kind] + 2.0 ** -18) + C.HALF[dtype] * (o.abs() + seen[0][0].abs())
+            assert bool(((o - seen[0][0]).abs() <= tol).all()), m
+            assert float((lse - seen[0][1]).abs().max()) <= 2.0 ** -17 + 2.0 ** -22 * float(rl.abs().max()), m
