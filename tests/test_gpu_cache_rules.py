@@ -325,3 +325,41 @@ def test_rows_alone_and_in_batches(X, kind, hq, hkv, hd):
             tol = spread * 2 * (P_ROUND[kind] + 2.0 ** -18) + C.HALF[dtype] * (o.abs() + seen[0][0].abs())
             assert bool(((o - seen[0][0]).abs() <= tol).all()), m
             assert float((lse - seen[0][1]).abs().max()) <= 2.0 ** -17 + 2.0 ** -22 * float(rl.abs().max()), m
+
+
+# ------------------------------------------------------------------ rotation
+
+def _turns(theta, hd, pos):
+    """pos theta^(-2c/hd) / 2 pi modulo 1 for c < hd / 2, from 60-digit arithmetic."""
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        pi = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+        out = []
+        for c in range(hd // 2):
+            f = (decimal.Decimal(-2 * c) / hd * decimal.Decimal(theta).ln()).exp() / (2 * pi)
+            out.append([float(pos_ * f % 1) for pos_ in map(decimal.Decimal, pos)])
+    return torch.tensor(out, dtype=torch.float64).T
+
+
+@pytest.mark.parametrize("theta", [1.0, 10.0, 1e4, 1e6])
+@pytest.mark.parametrize("hd", [32, 128])
+def test_rotation_against_long_arithmetic(X, theta, hd):
+    """Angles are within 2^-52 turns times the position of the definition's, beside fp32."""
+    pos = [0, 1, 3, 4097, 131071, 2 ** 24 - 1, 99999989, 2 ** 31 - 1]
+    M, hq = len(pos), 2
+    c = C.Cache(X, [16] * M, 1, hd, 16, "fp32", fill=0.5)
+    x = torch.randn(M, (hq + 2) * hd, generator=torch.Generator().manual_seed(4))
+    q = torch.empty(M, hq * hd, device="cuda")
+    X.cache_append(C.dims(X, hq, 1, hd, "fp32"), c.handle, x.cuda(), X.layer_weights({}, rope_theta=theta), None,
+                   ints([3] * M), ints(pos), q)
+    turns = _turns(theta, hd, pos) * (2 * math.pi)
+    cs, sn = turns.cos()[:, None], turns.sin()[:, None]
+    h = x.double().view(M, hq + 2, hd)[:, :hq]
+    a, b = h[..., :hd // 2], h[..., hd // 2:]
+    want = torch.cat([a * cs - b * sn, b * cs + a * sn], -1)
+    size = (a.abs() + b.abs()).repeat(1, 1, 2)
+    off = 2 * math.pi * 2.0 ** -52 * torch.tensor(pos, dtype=torch.float64)[:, None, None]
+    # fp32: the angle, its sine and cosine, two products and their sum (8 steps of the pair)
+    tol = size * (8 * 2.0 ** -24 + off) + C.HALF["fp32"] * want.abs()
+    err = (q.view(M, hq, hd).double().cpu() - want).abs() - tol
+    assert float(err.max()) <= 0, (err.amax((1, 2)).tolist())
