@@ -473,16 +473,18 @@ XMOD_API size_t xmod_cache_attention_workspace_bytes(const xmod_dims* dims, int 
  *   lse     [M, n_heads] fp32: ln sum_i exp(q . K_i / sqrt(head_dim)), or NULL
  * Slots at or after len[m] have no influence, whatever their pages hold. Products are
  * accumulated in fp32; the probabilities keep at least 16 bits of mantissa where they
- * weight the values. With E4M3 they go in times the values' scales and keep 11 bits, down to
- * 2^-28 of the row's largest |p * scale| (or of 2^-112, if that is larger); smaller ones are
- * off by at most 2^-38 of it. E4M3 rounds query elements below 2^-17 of their head's
- * largest one, by at most 2^-25 of it. Scores beyond fp32's range give NaN.
+ * weight the values. With E4M3 they go in times the values' scales and keep 22 bits with at
+ * most 8 query heads per KV head and 11 with more, but are off by up to 2^-38 of the row's
+ * largest |p * scale| (or of 2^-112, if that is larger) where that is more. E4M3 rounds query
+ * elements below 2^-17 of their head's largest one, by at most 2^-25 of it. Scores beyond
+ * fp32's range give NaN.
  * Device checks (status word of ws): a sequence not below n_seqs skips its row; a len
  * outside its range is clamped into it; a page outside [0, n_pages) is read as page 0.
  * Two calls with the same arguments give the same bits. The other rows of a call move the
  * borders at which a row's slots are split and so the maximum that a weight is rounded
  * against: a row alone and in a batch differ by that rounding on both sides (relative to
- * sum p |V|: 2 * 2^-16 in bf16, 2 * 2^-11 with E4M3), by fp32's, and by o's own.
+ * sum p |V|: 2 * 2^-16 in bf16, 2 * 2^-11 with E4M3 and more than 8 query heads per KV head),
+ * by fp32's, and by o's own.
  *   ws      xmod_cache_attention_workspace_bytes(dims, M) bytes; concurrent calls need one
  *           each. head_dim must be 32, 64 or 128. M = 0 does nothing. */
 XMOD_API int xmod_cache_attention(const xmod_dims* dims, const xmod_kv_cache* cache, int M,

@@ -233,8 +233,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 // f16 weights of e4m3 values (probability times the value's scale) are scaled up to 2^14 (f16
-// ends at 65504, its full precision at 2^-14): they keep 11 bits down to 2^-28 of the largest
-// weight so far, a power of two at or above it being the reference. The largest weight, not
+// ends at 65504, its last step is 2^-24): one part keeps 11 bits, two keep 22, and either is off
+// by 2^-39 of the reference where that is more, a power of two at or above the largest weight so
+// far. The largest weight, not
 // the largest scale: a key of little probability with a large scale costs the others nothing.
 // (32 rows of up to 16384, 16 and 4 heads: 54.7 us, by the largest scale 54.4; 64 rows of up to
 // 8192 with 16 query heads a KV head 42.5 and 41.7.)
@@ -432,9 +433,11 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   // -------------------------------------------------------------- consumers
   // Warp w takes the keys w, w + 4, ... (in groups of 16) of every tile. Scores and
   // probabilities live in MMA fragments: thread (r = lane / 4, t = lane % 4) holds query
-  // heads r and r + 8. bf16 probabilities go in as two bf16 parts, 16 bits of mantissa: with
+  // heads r and r + 8. Probabilities go in as two parts, 16 bits of mantissa in bf16, 22 in f16
+  // (e4m3 values; 32 rows of up to 16384, 16 and 4 heads: 54.5 us, by one part 54.4): with
   // at most 8 query heads rows 8 to 15 carry what rounding rows 0 to 7 left over, at no cost;
-  // with more a second MMA does. For e4m3 values f16's 11 bits stand (the codes have 4).
+  // with more a second MMA does, for bf16; over e4m3 values f16's 11 bits stand there (64 rows
+  // of up to 8192, 16 query heads a KV head: 42.4 us, 46.4 with the second).
   constexpr bool PAIR = ROWS == 8;
   const int r = lane >> 2, t = lane & 3;
   const float to_log2 = 1.4426950408889634f * rsqrtf((float)HD);
@@ -675,7 +678,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         }
         auto accumulate = [&](float (&c)[4], uint32_t b0, uint32_t b1) {
           if constexpr (PAIR) {
-            mma16816<FP8>(c, hi[0], FP8 ? 0u : lo[0], hi[2], FP8 ? 0u : lo[2], b0, b1);
+            mma16816<FP8>(c, hi[0], lo[0], hi[2], lo[2], b0, b1);
           } else {
             mma16816<FP8>(c, hi[0], hi[1], hi[2], hi[3], b0, b1);
             if (!FP8) mma16816<FP8>(c, lo[0], lo[1], lo[2], lo[3], b0, b1);

@@ -363,3 +363,38 @@ def test_rotation_against_long_arithmetic(X, theta, hd):
     tol = size * (8 * 2.0 ** -24 + off) + C.HALF["fp32"] * want.abs()
     err = (q.view(M, hq, hd).double().cpu() - want).abs() - tol
     assert float(err.max()) <= 0, (err.amax((1, 2)).tolist())
+
+
+# ------------------------------------------------------------------ bits of the weights
+
+@pytest.mark.parametrize("hq,hkv,hd", [(4, 4, 128), (8, 1, 64), (6, 2, 32)])
+def test_e4m3_weights_keep_22_bits(X, hq, hkv, hd):
+    """Two keys whose weighted values cancel: codes 8 and -9 (and multiples), with the second
+    value's scale set so that p1 s1 8 = p2 s2 9 to fp32. What is left of o is the weights'
+    rounding, 2^-22 each with at most 8 query heads per KV head, and fp32's."""
+    M, rep = 150, hq // hkv
+    g = torch.Generator().manual_seed(hd)
+    c = C.Cache(X, [2] * M, hkv, hd, 16, "bf16", True)
+    k = torch.zeros(M, hkv, 2, hd)
+    k[..., 3] = torch.randint(8, 16, (M, hkv, 2), generator=g).float()
+    v = torch.exp2(torch.randint(-3, 4, (M, hkv, 1, hd), generator=g).float()) * torch.tensor([8.0, -9.0])[:, None]
+    v = v * torch.where(torch.rand(M, hkv, 1, hd, generator=g) < 0.5, -1.0, 1.0)
+    ks = 0.05 + 0.1 * torch.rand(M, hkv, 2, generator=g)
+    q = torch.zeros(M, hkv, 1, hd)
+    q[..., 3] = (0.5 + torch.rand(M, hkv, 1, generator=g)).bfloat16().float() * math.sqrt(hd) / 8
+    q = q.expand(M, hkv, rep, hd).reshape(M, hq * hd).cuda().bfloat16()
+    z = q.view(M, hkv, rep, hd)[:, :, 0, 3].double().cpu()[..., None] * k[..., 3].double() * ks.double() / math.sqrt(hd)
+    p = torch.softmax(z, -1)
+    vs = torch.rand(M, hkv, 2, generator=g, dtype=torch.float64) + 0.5
+    vs[..., 1] = vs[..., 0] * p[..., 0] * 8 / (p[..., 1] * 9)
+    for m in range(M):
+        page, off = c.place(m, 0)
+        for name, x, s in (("k", k, ks), ("v", v, vs)):
+            getattr(c, name)[page, :, off:off + 2] = x[m].cuda().to(torch.float8_e4m3fn)
+            getattr(c, name + "_scale")[page, :, off:off + 2] = s[m].float().cuda()
+    o, lse, status = attend(X, c, q, range(M), [2] * M, hq, hd, "bf16")
+    assert status == X.OK
+    for m in range(M):
+        ref, rl, bound, dz = C.attention_ref(c, q[m].reshape(hq, hd), m, 2, 2.0 ** -22)
+        err = (o[m].view(hq, hd).double() - ref).abs() - bound - C.HALF["bf16"] * (ref.abs() + bound)
+        assert float(err.max()) <= 0, (m, float(err.max()), float(bound.max()))
