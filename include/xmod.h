@@ -436,9 +436,9 @@ typedef struct {
  * at position pos[m]; k and v are written to slot slot[m] of sequence seq[m], q to q_out.
  * Everything is computed in fp32 and rounded once, to the type it is stored in; E4M3
  * stores scale = max|x| / 448 over the head's values and the codes nearest to x / scale
- * (the quotient in fp32, ties to even). A head of zeros gets scale 0 (as do values below
- * 2^-117, which are stored as zeros); a head with an infinity or NaN gets a NaN scale and
- * NaN codes.
+ * (both quotients in fp32, ties to even). A head of zeros gets scale 0, and so does one whose
+ * scale would be below 2^-126: its values are stored as zeros. A head with an infinity or NaN
+ * gets a NaN scale and NaN codes.
  *   seq     [M] int32, or NULL (row m belongs to sequence m). A negative entry skips
  *           its row: nothing of it is read or written (q_out's row keeps its values).
  *   slot    [M] int32; the rows of one call must address distinct slots
@@ -526,7 +526,7 @@ XMOD_API int xmod_token_logprobs(xmod_dtype dtype, int64_t N, int V, const void*
  *              must not overlap it. Columns from V to ldd are not written.
  * A row whose two gradients are zero (or absent) gets zeros, whatever its logits. A
  * target not below V counts as negative and is reported through status_out. Alignment and
- * V as for xmod_token_logprobs. */
+ * V as for xmod_token_logprobs, whose lse and entropy it takes. */
 XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const void* logits,
                                      int64_t ld, const int32_t* target, const float* lse,
                                      const float* entropy, const float* g_logp,

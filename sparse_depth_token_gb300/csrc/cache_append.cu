@@ -86,12 +86,15 @@ struct AppendArgs {
 // is copied as it is. Sequence, slot and position are fetched three tokens ahead, the page
 // one (and looked at only when its token's turn comes: 64 us with a check as it is fetched).
 // Measured: 32768 tokens of 12 q and 4 KV heads of 128, bf16 (336 MB): 58 us, 5.8 TB/s, 0.85
-// of what a copy reaches; 5003 tokens of 32 and 8 heads to e4m3 (99 MB): 22.5 us; 8 tokens: 2.1 us.
+// of what a copy reaches, fp32 (672 MB) 134 us; 5003 tokens of 32 and 8 heads to e4m3 (99 MB):
+// 22.5 us, with neither memory (32 %) nor issue (35 %) full: 122 registers leave four CTAs an SM,
+// too few to hide their latencies; 8 tokens: 2.0 us.
 constexpr int kQPasses = 4, kKvPasses = 2;
 constexpr int kAppendWarps = 4;
 // CTAs per SM the grid is limited to: four are resident, twice as many even out the parts'
-// lengths (measured before the last step, 32768 tokens of 12 q and 4 KV heads of 128, bf16: 62 us
-// at 4, 63 at 8, 72 at 32; 5003 tokens of 32 and 8 heads to e4m3: 24.3, 22.7, 24.4).
+// lengths. In us at 4, 8, 16 and 32: 32768 tokens of 12 q and 4 KV heads of 128, bf16 55.8, 58.0,
+// 61.5, 67.8, to e4m3 59.8, 62.8, 67.2, 74.5, fp32 167, 134, 115, 115; 5003 tokens of 32 and 8
+// heads, bf16 23.6, 20.8, 20.4, 22.7, to e4m3 24.7, 22.3, 22.7, 24.9, fp32 45.6, 38.6, 36.1, 35.7.
 constexpr int kAppendCtas = 8;
 constexpr int kAppendStages = 3;  // tokens of a warp in shared memory: one at work, two coming
 

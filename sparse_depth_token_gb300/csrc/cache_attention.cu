@@ -13,8 +13,8 @@
 // Measured: 64 rows of up to 8192 slots (32 query and 8 KV heads of 128, bf16, 1.10 GB)
 // 171 us, 6.4 TB/s, 0.95 of what a copy reaches; one row of 131079 (16 and 4 heads, 268 MB)
 // 49 us, of which 10 are the launch, the plan, the first tile and the join; 32 rows of up to
-// 16384 in e4m3 (285 MB) 55 us: the codes stream at 6.4 TB/s (their conversions to f16 take
-// most issue slots) after 9.5 us of the same latency; 8 rows of up to 512 8.4 us.
+// 16384 in e4m3 (285 MB) 55 us: the codes stream at 6.3 TB/s (their conversions to f16 double
+// the instructions a byte) after 9.5 us of the same latency; 8 rows of up to 512 8.3 us.
 //
 // Split. The tiles of all rows and KV heads form one list, cut into equal ranges, one per
 // CTA, so a single long sequence fills the GPU as well as a batch of ragged ones. A CTA

@@ -233,8 +233,9 @@ __device__ __forceinline__ int find_top(const LogprobArgs& a, Finisher& sh,
     best[q] = lane + 32 * q < s.nvec ? order_of(m) : 0u;
   }
   // the k-th largest of the threads' orders: a few by taking the largest away, more by the
-  // largest bound that k threads reach, bit by bit (4096 rows of 50257, bf16, either way: 5
-  // alternatives 76.5 and 78.8 us, 20 of them 101 and 96)
+  // largest bound that k threads reach, bit by bit (4096 rows of 50257, bf16, either way, in us:
+  // 5 alternatives 76.4 and 78.9, 8 of them 81.9 and 84.0, 12 86.8 and 87.4, 16 96.4 and 94.3,
+  // 20 101 and 97.9; rows of 16000: 5 of them 41.1 and 42.9, 12 46.4 and 45.9, 20 53.3 and 48.9)
   uint32_t bound = 0;
   if (k <= 12) {
     uint32_t left[Q];
@@ -867,9 +868,10 @@ cudaError_t launch_logprobs_fin(const Ctx& c, const LogprobArgs& a0) {
 
 // Short rows go to warps. Else a second finisher where one would hold the rows up: rows of one
 // or two chunks, or many alternatives (it costs the others registers and issue slots). 4096
-// rows, bf16, one and two finishers: 50257 logits with 5 alternatives 76.4 and 80.5 us, with
-// 64 of them 184 and 146; 8191 logits with 5 alternatives 37.8 and 33.8, 16000 44.5 and 41.0,
-// 20000 47.6 and 46.9.
+// rows, bf16, one and two finishers, in us: 5 alternatives of 5000 logits 32.5 and 26.5, of 8191
+// 38.1 and 34.1, of 16000 44.8 and 41.2, of 20000 47.9 and 47.1, of 24000 51.6 and 52.0, of 32000
+// 59.1 and 61.7, of 50257 76.6 and 80.7; of 50257 20 alternatives 96.8 and 97.9, 32 113 and 108,
+// 40 127 and 116, 64 184 and 147.
 template <typename T, bool ENT>
 cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
   const int VE = 16 / (int)sizeof(T);
