@@ -492,6 +492,121 @@ XMOD_API int xmod_cache_attention(const xmod_dims* dims, const xmod_kv_cache* ca
                                   const int32_t* len, void* o, float* lse, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* Bytes of workspace xmod_cache_attention_chunk needs for up to n_chunks chunks of up to M
+ * rows together (0 for invalid dims, n_chunks < 0 or M < 0). The lengths do not enter. */
+XMOD_API size_t xmod_cache_attention_chunk_workspace_bytes(const xmod_dims* dims, int n_chunks,
+                                                           int M);
+
+/* Attention of a chunk of new tokens of each sequence over the cache that holds them (after
+ * xmod_cache_append) and what came before: pieces of prompts, whole prompts packed one after
+ * the other, proposed tokens to be verified. Chunk c is rows start[c] .. start[c + 1] - 1 of
+ * q, in the order of their slots; its last row attends to the first len[c] slots of its
+ * sequence, the row before it to one less, and so on:
+ *   o[m, h] = sum_i p_i V[i, g],  p = softmax over i < lim(m) of q[m, h] . K[i, g] / sqrt(head_dim)
+ *   lim(m) = len[c] - (start[c + 1] - 1 - m),  g = h / (n_heads / n_kv_heads)
+ *   M       rows of q, o and lse; those of no chunk keep their values in o and lse
+ *   q       [M, n_heads * head_dim], row stride ldq (dtype): rotated queries
+ *   start   [n_chunks + 1] int32, not descending, within 0 .. M; a chunk may be empty
+ *   seq     [n_chunks] int32, or NULL (chunk c reads sequence c). A negative entry skips its
+ *           chunk: o and lse keep their values there.
+ *   len     [n_chunks] int32, 0 .. max_pages * page_size. A row with lim(m) <= 0 attends to
+ *           nothing: its o is zero and its lse -infinity.
+ *   o       [M, n_heads * head_dim] (dtype), must not overlap q
+ *   lse     [M, n_heads] fp32: ln sum_i exp(q . K_i / sqrt(head_dim)), or NULL
+ * Slots at or after lim(m) have no influence on row m, whatever they hold (NaN and infinities
+ * included; tokens of the chunk after row m among them). Products are accumulated in fp32 and
+ * the softmax's sums are fp32. In bf16 and over E4M3 the weights of the values (with E4M3 times
+ * the values' scales) are rounded to bf16. Scores beyond fp32's range give NaN.
+ * Device checks (status word of ws): a chunk whose sequence is not below n_seqs, or whose start
+ * entries lie outside 0 .. M or descend, is skipped; a len outside its range is clamped into
+ * it; a page outside [0, n_pages) is read as page 0.
+ * Two calls with the same arguments give the same bits; a chunk alone and among others may
+ * differ by the roundings above.
+ *   ws      xmod_cache_attention_chunk_workspace_bytes(dims, n_chunks, M) bytes; concurrent
+ *           calls need one each. head_dim must be 32, 64 or 128. M = 0 or n_chunks = 0 does
+ *           nothing. */
+XMOD_API int xmod_cache_attention_chunk(const xmod_dims* dims, const xmod_kv_cache* cache,
+                                        int n_chunks, int M, const void* q, int ldq,
+                                        const int32_t* start, const int32_t* seq,
+                                        const int32_t* len, void* o, float* lse, void* ws,
+                                        size_t ws_bytes, void* stream);
+
+/* Rotary positions beyond the layers' own (whole heads, halves paired): which dimensions
+ * turn, in which pairs, how fast. A host structure, copied by every call that takes it.
+ *   rot_dim      the first rot_dim dimensions of every head turn, the others do not; a
+ *                multiple of 8, 8 .. head_dim
+ *   interleaved  0: dimension c is paired with c + rot_dim / 2; 1: 2c with 2c + 1
+ *   amplitude    factor of cosine and sine
+ *   freq         [rot_dim / 2] radians per position of pair c (any finite numbers) */
+typedef struct {
+  int rot_dim, interleaved;
+  float amplitude;
+  double freq[64];
+} xmod_rope;
+
+/* How frequencies are scaled for contexts longer than the trained one, f_c =
+ * theta^(-2c / rot_dim) before:
+ *   PLAIN   f_c
+ *   LINEAR  f_c / factor (positions interpolated)
+ *   BASE    theta becomes theta * factor^(rot_dim / (rot_dim - 2)): the slowest pair is slowed
+ *           down by factor, the fastest not (rot_dim 8 or more)
+ *   PARTS   by parts of the spectrum (Peng et al., "YaRN: Efficient Context Window Extension
+ *           of Large Language Models", 2023): with e(t) = rot_dim ln(trained / (2 pi t)) /
+ *           (2 ln theta) the pair that turns t times in the trained context, lo =
+ *           max(0, floor(e(32))), hi = min(rot_dim - 1, ceil(e(1))) and g_c = (c - lo) /
+ *           max(hi - lo, 0.001) clamped to [0, 1]: f_c (1 - g_c) + f_c / factor g_c, amplitude
+ *           0.1 ln(factor) + 1 (1 in the other scalings) */
+typedef enum {
+  XMOD_ROPE_PLAIN = 0,
+  XMOD_ROPE_LINEAR = 1,
+  XMOD_ROPE_BASE = 2,
+  XMOD_ROPE_PARTS = 3
+} xmod_rope_scaling;
+
+/* Fill `rope` (host only, nothing is launched). theta > 1, factor >= 1 (not read by PLAIN),
+ * trained > 0 positions (read by PARTS). */
+XMOD_API int xmod_rope_init(xmod_rope* rope, int rot_dim, int interleaved, double theta,
+                            xmod_rope_scaling scaling, double factor, int trained);
+
+/* QK-norm and rotary positions of the q and k heads of M tokens' projections q | k | v (as
+ * for xmod_cache_append, which can then be called with w NULL), in one pass:
+ *   n = x / sqrt(mean(x^2) + rms_eps) * gain   (w->q_norm, w->k_norm; either may be NULL, and
+ *                                               w too: n = x; w's other members are not read)
+ *   out: (a, b) of pair c becomes amplitude * (a cos t - b sin t, b cos t + a sin t),
+ *        t = pos * freq[c]; dimensions from rot_dim on are n
+ * computed in fp32 and rounded once. The angle is off by at most |pos| * (|freq| 2^-53 + 2^-62)
+ * and 2e-9 radians, cosine and sine by 1e-7 more.
+ *   qkv   [M, >= (n_heads + n_kv_heads) * head_dim], row stride ldqkv; v is not read
+ *   pos   [M] int32, or NULL (row m is at position m mod dims->T). A negative position skips
+ *         its row: out keeps its values there.
+ *   out   [M, (n_heads + n_kv_heads) * head_dim], row stride ldo; may be qkv itself with ldo =
+ *         ldqkv, else must not overlap it
+ * Row strides must be multiples of 8, head_dim 32, 64 or 128. M = 0 does nothing. */
+XMOD_API int xmod_qk_rope(const xmod_dims* dims, int M, const void* qkv, int ldqkv,
+                          const xmod_layer_weights* w, const xmod_rope* rope, const int32_t* pos,
+                          void* out, int ldo, void* stream);
+
+/* Bytes of workspace xmod_qk_rope_bwd needs with gains (0 for invalid dims or M < 0). */
+XMOD_API size_t xmod_qk_rope_bwd_workspace_bytes(const xmod_dims* dims, int M);
+
+/* Gradient of sum(dout * out) of xmod_qk_rope at qkv and at the gains.
+ *   qkv      as in the forward; not read (may be NULL) where there are no gains
+ *   dout     [M, (n_heads + n_kv_heads) * head_dim], row stride lddo (dtype)
+ *   din      the same shape, row stride lddi (dtype): the gradient at the q and k projections;
+ *            may be dout itself with lddi = lddo, else must not overlap dout or qkv
+ *   dq_norm, dk_norm  [head_dim] fp32, overwritten: the gains' gradients; NULL: not wanted
+ *            (must be NULL without that gain)
+ * Rows of negative positions are skipped: din keeps its values, the gains' gradients leave
+ * them out. Two calls with the same arguments give the same bits.
+ *   ws       xmod_qk_rope_bwd_workspace_bytes(dims, M) bytes; concurrent calls need one each;
+ *            may be NULL where no gain's gradient is wanted
+ * M = 0 zeroes the gains' gradients. */
+XMOD_API int xmod_qk_rope_bwd(const xmod_dims* dims, int M, const void* qkv, int ldqkv,
+                              const xmod_layer_weights* w, const xmod_rope* rope,
+                              const int32_t* pos, const void* dout, int lddo, void* din,
+                              int lddi, float* dq_norm, float* dk_norm, void* ws,
+                              size_t ws_bytes, void* stream);
+
 /* Log probabilities of given tokens under logits [N, V] (dtype; row stride ld >= V, any
  * value), in natural logarithms, from one reading of the logits:
  *   lse     [N] fp32: ln sum_v exp(x_v)
@@ -532,6 +647,36 @@ XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const v
                                      const float* entropy, const float* g_logp,
                                      const float* g_entropy, void* dlogits, int64_t ldd,
                                      int* status_out, void* stream);
+
+/* A token for each row of logits [N, V] (dtype; row stride ld >= V, any value) from a given
+ * uniform number. With x the row, m its maximum and T its temperature, token v has the weight
+ * w_v = exp((x_v - m) / T). Tokens are ranked by descending logit, ties to the lower token
+ * (-0 equals +0). Kept are
+ *   - with T <= 0 the first token alone,
+ *   - the first top_k (0 or less: all),
+ *   - of these the shortest run from the first whose weights reach top_p times their sum, at
+ *     least one (top_p >= 1: all),
+ *   - of all tokens those with w_v >= min_p (above 1 counts as 1; 0 or less: all),
+ * and of the kept tokens, taken in the order of their numbers, the first is chosen at which
+ * the running sum of weights exceeds u times the whole sum.
+ *   temperature, top_p, min_p [N] fp32, top_k [N] int32: each may be NULL (1; off)
+ *   u       [N] fp32 in [0, 1)
+ *   token   [N] int32
+ *   logp    [N] fp32: ln of the probability with which the token was chosen, w_token over the
+ *           kept weights' sum; or NULL
+ * Weights are integers in units of at most 2^-39 (2^(bits of V) - 62), computed to a relative
+ * error of 2^-33, and sums are exact: the choice depends on neither order nor launch, and
+ * differs from the real numbers' only where u, top_p or min_p lies that close to a border.
+ * Weights below the unit count as 0.
+ * Checked on the device and reported through status_out (a device int, or NULL; see
+ * xmod_gather): a row that holds a NaN or +infinity, or nothing above -infinity, has no
+ * distribution: token -1 and logp NaN; so does a row whose u, temperature, top_p or min_p is
+ * NaN or whose u is outside [0, 1). Pointers need only their elements' alignment. V is at most
+ * XMOD_MAX_VOCAB. N = 0 does nothing. */
+XMOD_API int xmod_sample_tokens(xmod_dtype dtype, int64_t N, int V, const void* logits,
+                                int64_t ld, const float* temperature, const int32_t* top_k,
+                                const float* top_p, const float* min_p, const float* u,
+                                int32_t* token, float* logp, int* status_out, void* stream);
 
 /* ---------------------------------------------------------------- failure detection
  * Not part of the method. Every wait inside the library's tcgen05 kernels (on an

@@ -1,0 +1,134 @@
+// Attention of a chunk of new tokens over the paged cache: the entry point, and the join of
+// segments that several CTAs worked on.
+
+#include <math.h>
+
+#include "cache_chunk.cuh"
+
+namespace xmod {
+
+namespace {
+
+// Segment of CTA blockIdx.x that later CTAs' ranges continue: a warp a row, the parts' outputs
+// weighted to the common maximum, in CTA order.
+constexpr int kJoinWarps = 8;
+
+template <typename T, int HD, int QR>
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_chunk_join_kernel(const ChunkArgs a) {
+  constexpr int E = HD / 32;
+  pdl_trigger();
+  pdl_wait();
+  const ChunkJoin j = a.join[blockIdx.x];
+  if (j.chunk < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = blockIdx.y * kJoinWarps + warp;
+  const ChunkRow row = chunk_row(a, read_chunk(a, j.chunk), j.hp, j.t, R);
+  if (row.m < 0) return;
+  float top = -INFINITY;
+  for (int p = j.first + lane; p <= j.last; p += 32)
+    top = fmaxf(top, chunk_part<QR, HD>(a, p, p > j.first)[R]);
+  top = warp_max(top);
+  const float low = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int p = j.first; p <= j.last; ++p) {
+    const float* part = chunk_part<QR, HD>(a, p, p > j.first);
+    const float f = exp2f(part[R] - low);
+    sum = fmaf(part[QR + R], f, sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(part[2 * QR + R * HD + e * 32 + lane], f, o[e]);
+  }
+  const int64_t head = row.m * a.hq + row.head;
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) st_f((T*)a.o + head * HD + e * 32 + lane, o[e] * inv);
+  if (a.lse && lane == 0) a.lse[head] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <typename T, int QR> int launch_join(const Ctx& c, const ChunkArgs& a, int hd, int ctas) {
+  const dim3 grid(ctas, QR / kJoinWarps), block(kJoinWarps * 32);
+  if (hd == 128)
+    XMOD_LAUNCH(c, "cache_chunk_join", launch_pdl(cache_chunk_join_kernel<T, 128, QR>, grid, block, 0, c.stream, a));
+  else if (hd == 64)
+    XMOD_LAUNCH(c, "cache_chunk_join", launch_pdl(cache_chunk_join_kernel<T, 64, QR>, grid, block, 0, c.stream, a));
+  else
+    XMOD_LAUNCH(c, "cache_chunk_join", launch_pdl(cache_chunk_join_kernel<T, 32, QR>, grid, block, 0, c.stream, a));
+  return XMOD_OK;
+}
+
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+constexpr int kQueryRows = 64;   // of a segment
+
+size_t chunk_workspace(const xmod_dims* dm) {
+  const size_t part = (size_t)kQueryRows * (dm->head_dim + 2) * 4;
+  return 256 + round256(kChunkMaxCtas * sizeof(ChunkJoin)) + 2 * kChunkMaxCtas * part;
+}
+
+}  // namespace
+}  // namespace xmod
+
+using namespace xmod;
+
+extern "C" {
+
+size_t xmod_cache_attention_chunk_workspace_bytes(const xmod_dims* dm, int n_chunks, int M) {
+  if (!dims_ok(dm) || n_chunks < 0 || M < 0 || !head_dim_supported(dm->head_dim)) return 0;
+  return chunk_workspace(dm);
+}
+
+int xmod_cache_attention_chunk(const xmod_dims* dm, const xmod_kv_cache* cache, int n_chunks, int M,
+                               const void* q, int ldq, const int32_t* start, const int32_t* seq,
+                               const int32_t* len, void* o, float* lse, void* ws, size_t ws_bytes,
+                               void* stream) {
+  const int st = cache_status(dm, cache);
+  if (st) return st;
+  if (n_chunks < 0 || M < 0) return XMOD_ERR_INVALID_ARG;
+  if (n_chunks == 0 || M == 0) return XMOD_OK;
+  const int qw = dm->n_heads * dm->head_dim;
+  if (!ptr16(q) || ldq < qw || ldq % 8 || !start || !ptr4_or_null(start) || !ptr4_or_null(seq) || !len ||
+      !ptr4_or_null(len) || !ptr16(o) || o == q || !ptr4_or_null(lse))
+    return XMOD_ERR_INVALID_ARG;
+  if (!ptr16(ws) || ws_bytes < chunk_workspace(dm)) return XMOD_ERR_WORKSPACE;
+  const bool fp32 = dm->dtype == XMOD_FP32, fp8 = cache->format == XMOD_CACHE_E4M3;
+  const int sms = device_sms();
+  if (sms <= 0) return XMOD_ERR_CUDA;
+  const int ctas = 2 * sms < kChunkMaxCtas ? 2 * sms : kChunkMaxCtas;
+  const int group = dm->n_heads / dm->n_kv_heads;
+  ChunkArgs a{};
+  a.n_chunks = n_chunks;
+  a.M = M;
+  a.hq = dm->n_heads;
+  a.hkv = dm->n_kv_heads;
+  a.ldq = ldq;
+  a.q = q;
+  a.start = start;
+  a.seq = seq;
+  a.len = len;
+  a.o = o;
+  a.lse = lse;
+  a.table = cache->table;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.n_pages = cache->n_pages;
+  a.page_size = cache->page_size;
+  a.n_seqs = cache->n_seqs;
+  a.max_pages = cache->max_pages;
+  a.hpt = group < kQueryRows ? group : kQueryRows;
+  a.tpt = kQueryRows / a.hpt;
+  a.passes = (group + a.hpt - 1) / a.hpt;
+  a.box = cache->page_size % 64 == 0 ? 64 : cache->page_size % 32 == 0 ? 32 : 16;
+  a.join = (ChunkJoin*)((char*)ws + 256);
+  a.part = (float*)((char*)ws + 256 + round256(kChunkMaxCtas * sizeof(ChunkJoin)));
+  a.status = (int*)ws;
+  const Ctx c{(cudaStream_t)stream, a.status};
+  const int r = launch_chunk_f32(c, a, dm->head_dim, fp8, !fp32, ctas);
+  if (r) return r;
+  if (fp32) return launch_join<float, kQueryRows>(c, a, dm->head_dim, ctas);
+  return launch_join<__nv_bfloat16, kQueryRows>(c, a, dm->head_dim, ctas);
+}
+
+}  // extern "C"

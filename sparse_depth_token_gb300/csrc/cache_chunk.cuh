@@ -1,0 +1,273 @@
+// What the kernels of a chunk's attention over the paged cache share: the chunks' shapes, the
+// division of the work over the CTAs, and the partial results where a division cuts it.
+//
+// A segment is up to QR query rows of one chunk and KV head: tpt tokens with hpt query heads of
+// the KV head each (row R: token R / hpt, head R % hpt), so that a key tile read once serves
+// them all. A segment's key tiles are those below its last token's limit. The tiles of all
+// segments form one list (order: chunk, KV head and pass of heads, tokens, keys), cut into
+// equal ranges, one per CTA: a single long sequence fills the GPU as well as a batch of ragged
+// ones, and causal segments of all lengths even out. Where a segment lies in several CTAs'
+// ranges each leaves its maximum, sum and unnormalised output in the workspace, and a second
+// kernel joins them in CTA order: the result is the same bits at every call.
+#pragma once
+
+#include "cache.h"
+#include "common.cuh"
+
+namespace xmod {
+
+constexpr int kChunkKeys = 64;        // keys of a tile
+constexpr int kChunkMaxCtas = 512;    // CTAs the workspace has room for
+
+// A segment that starts in a CTA's range and ends in a later one's.
+struct ChunkJoin {
+  int chunk, hp, t, first, last;   // CTAs first .. last hold it; chunk < 0: none
+};
+
+struct ChunkArgs {
+  int n_chunks, M, hq, hkv, ldq;
+  const void* q;
+  const int32_t *start, *seq, *len;
+  void* o;
+  float* lse;
+  const int32_t* table;
+  const void *k, *v;
+  const float *k_scale, *v_scale;
+  int n_pages, page_size, n_seqs, max_pages;
+  int hpt, tpt, passes;   // heads and tokens of a segment, passes over a KV head's query heads
+  int box;                // rows of a TMA box: divides the page size and a tile
+  float* part;            // partial results, two per CTA
+  ChunkJoin* join;        // what each CTA leaves to be joined
+  int* status;
+};
+
+struct Chunk {
+  int first, n, len, seq;   // first row, tokens (0: nothing to do), slots, sequence
+};
+
+__device__ __forceinline__ Chunk read_chunk(const ChunkArgs& a, int c) {
+  Chunk k;
+  k.first = a.start[c];
+  const int end = a.start[c + 1];
+  k.seq = a.seq ? a.seq[c] : c;
+  k.len = 0;
+  k.n = 0;
+  if (k.seq < 0) return k;
+  if (k.seq >= a.n_seqs || k.first < 0 || end < k.first || end > a.M) {
+    report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+    return k;
+  }
+  k.n = end - k.first;
+  if (k.n == 0) return k;
+  const int n = a.len[c], most = a.max_pages * a.page_size;
+  if (n < 0 || n > most) report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+  k.len = min(max(n, 0), most);
+  return k;
+}
+
+__device__ __forceinline__ int chunk_segments(const ChunkArgs& a, const Chunk& k) {
+  return (k.n + a.tpt - 1) / a.tpt;
+}
+// Slots that the last token of segment t attends to (may be 0 or less).
+__device__ __forceinline__ int segment_limit(const ChunkArgs& a, const Chunk& k, int t) {
+  const int64_t end = min((int64_t)k.n, (int64_t)(t + 1) * a.tpt);
+  return (int)(k.len - k.n + end);
+}
+// A segment without keys counts as one tile: its zeros have to be written.
+__device__ __forceinline__ int segment_tiles(int limit) {
+  return limit <= 0 ? 1 : (limit - 1) / kChunkKeys + 1;
+}
+
+// Tiles of the first t segments of a chunk, in closed form. Segment i has ceil((b + (i + 1) tpt)
+// / 64) tiles with b = len - n, at least one, the last one ceil(len / 64).
+__device__ __forceinline__ long long tiles_before(const ChunkArgs& a, const Chunk& k, int t) {
+  long long sum = 0;
+  const int nt = chunk_segments(a, k);
+  if (t == nt && nt > 0) {
+    sum += segment_tiles(k.len);
+    --t;
+  }
+  const long long b = (long long)k.len - k.n;
+  const int empty = b < 0 ? (int)min((long long)t, -b / a.tpt) : 0;
+  sum += empty;
+  const int n = t - empty;
+  if (n <= 0) return sum;
+  // sum over j < n of floor((tpt j + c) / 64)
+  const long long c = b + kChunkKeys - 1 + (long long)a.tpt * (empty + 1);
+  const int qa = a.tpt / kChunkKeys, ra = a.tpt % kChunkKeys;
+  const long long qc = c / kChunkKeys;
+  const int rc = (int)(c % kChunkKeys);
+  sum += (long long)qa * n * (n - 1) / 2 + qc * n;
+  if (ra == 0) return sum;
+  // j = 64 u + v: floor((ra j + rc) / 64) = ra u + floor((ra v + rc) / 64)
+  const long long u = n / kChunkKeys;
+  const int w = n % kChunkKeys;
+  int whole = 0, part = 0;
+#pragma unroll 8
+  for (int v = 0; v < kChunkKeys; ++v) {
+    const int f = (ra * v + rc) / kChunkKeys;
+    whole += f;
+    if (v < w) part += f;
+  }
+  return sum + ra * (kChunkKeys * (u * (u - 1) / 2) + u * w) + u * whole + part;
+}
+
+// This CTA's range [begin, end) of the tile list and where it starts: chunk, KV head and pass,
+// segment, and `tile` tiles into it.
+struct ChunkPlan {
+  long long begin, end, total, off;
+  int chunk, hp, t, tile, ctas;
+};
+
+// All threads of the CTA; scratch: one int64 per warp.
+__device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* plan, long long* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
+  const int per = (a.n_chunks + nthreads - 1) / nthreads;
+  const int c0 = min(a.n_chunks, tid * per), c1 = min(a.n_chunks, c0 + per);
+  const long long P = (long long)a.hkv * a.passes;
+  long long mine = 0;
+  for (int c = c0; c < c1; ++c) {
+    const Chunk k = read_chunk(a, c);
+    mine += P * tiles_before(a, k, chunk_segments(a, k));
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < nthreads / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  const int ctas = (int)min((long long)gridDim.x, total);
+  const int g = blockIdx.x;
+  const long long begin = g < ctas ? total * g / ctas : total;
+  const long long end = g < ctas ? total * (g + 1) / ctas : total;
+  if (tid == 0) {
+    plan->begin = begin;
+    plan->end = end;
+    plan->total = total;
+    plan->ctas = ctas;
+    plan->t = 0;
+  }
+  if (begin < end && begin >= before && begin < before + mine) {
+    long long at = before;
+    for (int c = c0; c < c1; ++c) {
+      const Chunk k = read_chunk(a, c);
+      const long long n = P * tiles_before(a, k, chunk_segments(a, k));
+      if (begin < at + n) {
+        plan->chunk = c;
+        plan->off = begin - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  if (begin >= end) return;
+  // the segment: the last one with tiles_before <= rem, by as many guesses at once as threads
+  const Chunk k = read_chunk(a, plan->chunk);
+  const int nt = chunk_segments(a, k);
+  const long long off = plan->off, each = tiles_before(a, k, nt), rem = off % each;
+  int lo = 0, hi = nt;   // within lo .. hi - 1
+  while (hi - lo > 1) {
+    const int step = (hi - lo + nthreads - 1) / nthreads, t = lo + tid * step;
+    if (t < hi && tiles_before(a, k, t) <= rem) atomicMax(&plan->t, t);
+    __syncthreads();
+    lo = plan->t;
+    hi = min(hi, lo + step);
+    __syncthreads();
+  }
+  if (tid == 0) {
+    plan->t = lo;
+    plan->hp = (int)(off / each);
+    plan->tile = (int)(rem - tiles_before(a, k, lo));
+  }
+  __syncthreads();
+}
+
+// A CTA's way along its range, segment by segment.
+struct ChunkWalk {
+  Chunk k;
+  int chunk, segments, hp, t, tile, tiles, limit;   // tile: the next one, of `tiles`
+
+  __device__ __forceinline__ void set_segment(const ChunkArgs& a) {
+    limit = segment_limit(a, k, t);
+    tiles = segment_tiles(limit);
+  }
+  __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkPlan& p) {
+    chunk = p.chunk;
+    k = read_chunk(a, chunk);
+    segments = chunk_segments(a, k);
+    hp = p.hp;
+    t = p.t;
+    tile = p.tile;
+    set_segment(a);
+  }
+  __device__ __forceinline__ void next_segment(const ChunkArgs& a) {
+    tile = 0;
+    if (++t == segments) {
+      t = 0;
+      if (++hp == a.hkv * a.passes) {
+        hp = 0;
+        do {
+          if (++chunk >= a.n_chunks) {   // the list ends here
+            chunk = a.n_chunks - 1;
+            break;
+          }
+          k = read_chunk(a, chunk);
+        } while (k.n == 0);
+        segments = chunk_segments(a, k);
+      }
+    }
+    set_segment(a);
+  }
+};
+
+// Query row R of a segment: its row of q and o (-1: none), its head and its limit.
+struct ChunkRow {
+  int64_t m;
+  int head, limit;
+};
+__device__ __forceinline__ ChunkRow chunk_row(const ChunkArgs& a, const Chunk& k, int hp, int t, int R) {
+  ChunkRow r;
+  const int g = hp / a.passes, h = (hp % a.passes) * a.hpt + R % a.hpt, group = a.hq / a.hkv;
+  const int in = R / a.hpt;
+  const int64_t token = (int64_t)t * a.tpt + in;
+  r.m = -1;
+  r.limit = 0;
+  r.head = g * group + h;
+  if (in >= a.tpt || token >= k.n || h >= group) return r;
+  r.m = k.first + token;
+  r.limit = (int)max((int64_t)0, k.len - k.n + 1 + token);
+  return r;
+}
+
+// Where a segment's part in this CTA's range goes: slot 0 if it began before the range, 1 if it
+// begins here and goes on after it.
+template <int QR, int HD>
+__device__ __forceinline__ float* chunk_part(const ChunkArgs& a, int cta, bool began_before) {
+  return a.part + ((int64_t)2 * cta + (began_before ? 0 : 1)) * QR * (HD + 2);
+}
+
+// The join of a segment that begins in this CTA's range and of which `left` tiles come after
+// it: it ends in the last CTA whose range begins at or before its last tile.
+__device__ __forceinline__ ChunkJoin chunk_join(const ChunkPlan& p, const ChunkWalk& w, long long left) {
+  ChunkJoin j;
+  j.chunk = w.chunk;
+  j.hp = w.hp;
+  j.t = w.t;
+  j.first = blockIdx.x;
+  j.last = (int)min((long long)p.ctas - 1, ((p.end + left) * p.ctas - 1) / p.total);
+  return j;
+}
+
+// Launchers of the two kernels (cache_chunk_f32.cu, cache_chunk_tc.cu); ctas as planned.
+struct Ctx;
+int launch_chunk_f32(const Ctx& c, const ChunkArgs& a, int hd, bool fp8, bool bf16, int ctas);
+
+}  // namespace xmod

@@ -1,0 +1,258 @@
+// Attention of a chunk of new tokens over the paged cache on FFMA: fp32 throughout.
+
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "cache_chunk.cuh"
+
+namespace xmod {
+
+namespace {
+
+constexpr int kRows = 64, kThreads = 256;
+
+// Keys and values of the cache as fp32: 16-byte vector of T or of e4m3 codes.
+template <typename T, bool FP8> struct Source {
+  static constexpr int ES = FP8 ? 1 : (int)sizeof(T), VE = 16 / ES;
+  static __device__ __forceinline__ void load(const void* p, float scale, float (&x)[VE]) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(p);
+    if constexpr (FP8) {
+      const __nv_fp8x2_storage_t* c = reinterpret_cast<const __nv_fp8x2_storage_t*>(&raw);
+#pragma unroll
+      for (int i = 0; i < VE / 2; ++i) {
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c[i], __NV_E4M3)));
+        x[2 * i] = f.x * scale;
+        x[2 * i + 1] = f.y * scale;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE / 2; ++i) {
+        const float2 f = vec_pair<T>(raw, i);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
+
+template <int HD> struct Smem {
+  static constexpr int QLD = HD + 4, PLD = kChunkKeys + 4;
+  float q[kRows * QLD], kv[kChunkKeys * QLD], p[kRows * PLD];
+  ChunkPlan plan;
+  long long scratch[kThreads / 32];
+};
+
+// 16 x 16 threads: thread (ty, tx) has rows 4 ty .. 4 ty + 3, keys tx + 16 j of the scores and
+// dimensions 4 tx + 64 j .. of the output.
+template <typename T, bool FP8, int HD>
+__global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const ChunkArgs a) {
+  using S = Smem<HD>;
+  using Src = Source<T, FP8>;
+  constexpr int DW = HD >= 64 ? 4 : 2, DN = HD / (16 * DW);   // DN groups of DW dimensions
+  extern __shared__ __align__(16) uint8_t smem[];
+  S& s = *reinterpret_cast<S*>(smem);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  pdl_trigger();
+  pdl_wait();
+  make_chunk_plan(a, &s.plan, s.scratch);
+  const ChunkPlan plan = s.plan;
+  if (tid == 0) a.join[blockIdx.x].chunk = -1;
+  long long left = plan.end - plan.begin;
+  if (left <= 0) return;
+  ChunkWalk w;
+  w.begin(a, plan);
+  const float to_log2 = 1.4426950408889634f * rsqrtf((float)HD);
+  while (left > 0) {
+    const int first = w.tile, last = (int)min((long long)w.tiles, first + left);
+    left -= last - first;
+    ChunkRow row[4];
+    float mx[4], sum[4], o[4][DN * DW];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      row[i] = chunk_row(a, w.k, w.hp, w.t, 4 * ty + i);
+      mx[i] = -INFINITY;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DN * DW; ++d) o[i][d] = 0.f;
+    }
+    __syncthreads();   // the segment before is done with the queries
+    for (int i = tid; i < kRows * (HD / 4); i += kThreads) {
+      const int R = i / (HD / 4), d = i % (HD / 4) * 4;
+      const ChunkRow r = chunk_row(a, w.k, w.hp, w.t, R);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r.m >= 0) {
+        const T* p = (const T*)a.q + r.m * a.ldq + r.head * HD + d;
+        x = make_float4(ld_f(p) * to_log2, ld_f(p + 1) * to_log2, ld_f(p + 2) * to_log2, ld_f(p + 3) * to_log2);
+      }
+      *reinterpret_cast<float4*>(&s.q[R * S::QLD + d]) = x;
+    }
+    // slots of the cache into shared memory; those at and after the segment's limit as zeros
+    auto fill = [&](const void* base, const float* scales, int key0) {
+      constexpr int CH = HD / Src::VE;
+      const int g = w.hp / a.passes;
+      for (int i = tid; i < kChunkKeys * CH; i += kThreads) {
+        const int key = i / CH, c = i % CH, slot = key0 + key;
+        float x[Src::VE];
+        if (slot < w.limit) {
+          int page = a.table[(int64_t)w.k.seq * a.max_pages + slot / a.page_size];
+          if (page < 0 || page >= a.n_pages) {
+            report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+            page = 0;
+          }
+          const int64_t at = ((int64_t)page * a.hkv + g) * a.page_size + slot % a.page_size;
+          Src::load((const uint8_t*)base + (at * HD + c * Src::VE) * Src::ES, FP8 ? scales[at] : 1.f, x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < Src::VE; ++e) x[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < Src::VE; e += 4)
+          *reinterpret_cast<float4*>(&s.kv[key * S::QLD + c * Src::VE + e]) =
+              make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+      }
+    };
+    for (int tile = first; tile < last; ++tile) {
+      const int key0 = tile * kChunkKeys;
+      fill(a.k, a.k_scale, key0);
+      __syncthreads();
+      float sc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < HD; d += 4) {
+        float4 qv[4], kv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&s.q[(4 * ty + i) * S::QLD + d]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&s.kv[(tx + 16 * j) * S::QLD + d]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[i][j] = fmaf(qv[i].x, kv[j].x, sc[i][j]);
+            sc[i][j] = fmaf(qv[i].y, kv[j].y, sc[i][j]);
+            sc[i][j] = fmaf(qv[i].z, kv[j].z, sc[i][j]);
+            sc[i][j] = fmaf(qv[i].w, kv[j].w, sc[i][j]);
+          }
+      }
+      bool masked = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float top = mx[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (key0 + tx + 16 * j >= row[i].limit) sc[i][j] = -INFINITY;
+          top = fmaxf(top, sc[i][j]);
+        }
+        masked |= key0 + kChunkKeys > row[i].limit;
+#pragma unroll
+        for (int of = 8; of > 0; of >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, of));
+        const float low = top == -INFINITY ? 0.f : top, keep = exp2f(mx[i] - low);
+        mx[i] = top;
+        float part = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(sc[i][j] - low);
+          part += p;
+          s.p[(4 * ty + i) * S::PLD + tx + 16 * j] = p;
+        }
+        sum[i] = sum[i] * keep + part;   // this thread's keys; joined at the end
+#pragma unroll
+        for (int d = 0; d < DN * DW; ++d) o[i][d] *= keep;
+      }
+      __syncthreads();
+      fill(a.v, a.v_scale, key0);
+      __syncthreads();
+      // a key past a row's limit may hold anything: its product is left out, not weighted by 0
+      const bool guard = __any_sync(0xffffffffu, masked);
+#pragma unroll 4
+      for (int key = 0; key < kChunkKeys; ++key) {
+        float v[DN * DW];
+#pragma unroll
+        for (int g = 0; g < DN; ++g) {
+          const float* at = &s.kv[key * S::QLD + (g * 16 + tx) * DW];
+          if constexpr (DW == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(at);
+            v[4 * g] = f.x;
+            v[4 * g + 1] = f.y;
+            v[4 * g + 2] = f.z;
+            v[4 * g + 3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(at);
+            v[2 * g] = f.x;
+            v[2 * g + 1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = s.p[(4 * ty + i) * S::PLD + key];
+          if (!guard || key0 + key < row[i].limit) {
+#pragma unroll
+            for (int d = 0; d < DN * DW; ++d) o[i][d] = fmaf(p, v[d], o[i][d]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    const bool whole = first == 0 && last == w.tiles;
+    float* part = chunk_part<kRows, HD>(a, blockIdx.x, first > 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int of = 8; of > 0; of >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], of);
+      const int R = 4 * ty + i;
+      if (row[i].m < 0) continue;
+      const int64_t head = row[i].m * a.hq + row[i].head;
+      if (whole) {
+        const float inv = sum[i] > 0.f || sum[i] != sum[i] ? 1.f / sum[i] : 0.f;
+#pragma unroll
+        for (int g = 0; g < DN; ++g)
+#pragma unroll
+          for (int e = 0; e < DW; ++e)
+            st_f((T*)a.o + head * HD + (g * 16 + tx) * DW + e, o[i][g * DW + e] * inv);
+        if (a.lse && tx == 0) a.lse[head] = (mx[i] + log2f(sum[i])) * 0.6931471805599453f;
+      } else {
+#pragma unroll
+        for (int g = 0; g < DN; ++g)
+#pragma unroll
+          for (int e = 0; e < DW; ++e)
+            part[2 * kRows + R * HD + (g * 16 + tx) * DW + e] = o[i][g * DW + e];
+        if (tx == 0) {
+          part[R] = mx[i];
+          part[kRows + R] = sum[i];
+        }
+      }
+    }
+    if (tid == 0 && first == 0 && !whole) a.join[blockIdx.x] = chunk_join(plan, w, w.tiles - last);
+    if (left > 0) w.next_segment(a);
+  }
+}
+
+template <typename T, bool FP8, int HD> int launch_f32(const Ctx& c, const ChunkArgs& a, int ctas) {
+  static std::atomic<uint64_t> done{0};
+  auto k = cache_chunk_f32_kernel<T, FP8, HD>;
+  if (allow_smem(k, (int)sizeof(Smem<HD>), done) != cudaSuccess) return XMOD_ERR_CUDA;
+  XMOD_LAUNCH(c, "cache_chunk",
+              launch_pdl(k, dim3(ctas), dim3(kThreads), sizeof(Smem<HD>), c.stream, a));
+  return XMOD_OK;
+}
+
+template <typename T, bool FP8> int launch_f32_hd(const Ctx& c, const ChunkArgs& a, int hd, int ctas) {
+  if (hd == 128) return launch_f32<T, FP8, 128>(c, a, ctas);
+  if (hd == 64) return launch_f32<T, FP8, 64>(c, a, ctas);
+  return launch_f32<T, FP8, 32>(c, a, ctas);
+}
+
+}  // namespace
+
+int launch_chunk_f32(const Ctx& c, const ChunkArgs& a, int hd, bool fp8, bool bf16, int ctas) {
+  if (fp8) return launch_f32_hd<__nv_bfloat16, true>(c, a, hd, ctas);
+  if (bf16) return launch_f32_hd<__nv_bfloat16, false>(c, a, hd, ctas);
+  return launch_f32_hd<float, false>(c, a, hd, ctas);
+}
+
+}  // namespace xmod

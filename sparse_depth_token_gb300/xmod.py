@@ -27,9 +27,12 @@ EXPORTS = ("xmod_version", "xmod_status_string", "xmod_workspace_bytes", "xmod_r
            "xmod_bwd_workspace_bytes", "xmod_layer_bwd", "xmod_stack_bwd_workspace_bytes",
            "xmod_stack_bwd", "xmod_selftest_wait_timeout", "xmod_cache_append",
            "xmod_cache_attention_workspace_bytes", "xmod_cache_attention", "xmod_token_logprobs",
-           "xmod_token_logprobs_bwd")
+           "xmod_token_logprobs_bwd", "xmod_cache_attention_chunk_workspace_bytes",
+           "xmod_cache_attention_chunk", "xmod_rope_init", "xmod_qk_rope",
+           "xmod_qk_rope_bwd_workspace_bytes", "xmod_qk_rope_bwd", "xmod_sample_tokens")
 
 CACHE_NATIVE, CACHE_E4M3 = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3
 MAX_TOP_K = 64   # alternatives token_logprobs reports at most
 MAX_VOCAB = 1 << 22   # logits of a row of token_logprobs and its gradient at most
 
@@ -76,6 +79,11 @@ class KVCache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_seqs", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("amplitude", ctypes.c_float), ("freq", ctypes.c_double * 64)]
 
 
 class KernelTime(ctypes.Structure):
@@ -168,6 +176,25 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.xmod_token_logprobs_bwd.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int, _VP,
                                           ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, _VP,
                                           ctypes.c_int64, _VP, _VP]
+    L.xmod_cache_attention_chunk_workspace_bytes.restype = ctypes.c_size_t
+    L.xmod_cache_attention_chunk_workspace_bytes.argtypes = [ctypes.POINTER(Dims), ctypes.c_int,
+                                                             ctypes.c_int]
+    L.xmod_cache_attention_chunk.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(KVCache),
+                                             ctypes.c_int, ctypes.c_int, _VP, ctypes.c_int, _VP,
+                                             _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]
+    L.xmod_rope_init.argtypes = [ctypes.POINTER(Rope), ctypes.c_int, ctypes.c_int,
+                                 ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_int]
+    L.xmod_qk_rope.argtypes = [ctypes.POINTER(Dims), ctypes.c_int, _VP, ctypes.c_int,
+                               ctypes.POINTER(LayerWeights), ctypes.POINTER(Rope), _VP, _VP,
+                               ctypes.c_int, _VP]
+    L.xmod_qk_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+    L.xmod_qk_rope_bwd_workspace_bytes.argtypes = [ctypes.POINTER(Dims), ctypes.c_int]
+    L.xmod_qk_rope_bwd.argtypes = [ctypes.POINTER(Dims), ctypes.c_int, _VP, ctypes.c_int,
+                                   ctypes.POINTER(LayerWeights), ctypes.POINTER(Rope), _VP, _VP,
+                                   ctypes.c_int, _VP, ctypes.c_int, _VP, _VP, _VP,
+                                   ctypes.c_size_t, _VP]
+    L.xmod_sample_tokens.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int, _VP,
+                                     ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]
     _lib = L
     return L
 
@@ -444,6 +471,17 @@ def _mat(fn, t, dtype, rows, width, dev, most=2 ** 31 - 1):
     return t.data_ptr(), ld
 
 
+def _cols(fn, t, dtype, rows, width, dev):
+    """(pointer, row stride) of the first `width` columns of a matrix with `rows` rows."""
+    if (t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] != rows
+            or t.shape[1] < width or t.stride(1) != 1):
+        raise XmodError(fn, ERR_INVALID_ARG)
+    ld = t.stride(0) if rows > 1 else width
+    if ld > 2 ** 31 - 1:
+        raise XmodError(fn, ERR_UNSUPPORTED)
+    return t.data_ptr(), ld
+
+
 def _check_gains(fn, w, dtype, n, dev):
     """The QK-norm gains that a LayerWeights was made of are read as n elements of that dtype
     on end, on device dev."""
@@ -502,6 +540,87 @@ def cache_attention(dm, cache: KVCache, q, seq, lens, o, ws, lse=None, stream=No
         raise XmodError(fn, st)
 
 
+def cache_attention_chunk_workspace_bytes(dm: Dims, n_chunks: int, M: int) -> int:
+    return int(load().xmod_cache_attention_chunk_workspace_bytes(ctypes.byref(dm), int(n_chunks),
+                                                                 int(M)))
+
+
+def cache_attention_chunk(dm, cache: KVCache, q, start, seq, lens, o, ws, lse=None, stream=None):
+    """xmod_cache_attention_chunk: o [M, n_heads head_dim] (and lse [M, n_heads] fp32) of the
+    queries q, whose rows start[c] .. start[c + 1] - 1 are the last tokens of the first lens[c]
+    slots of sequence seq[c] (None: c)."""
+    fn = "xmod_cache_attention_chunk"
+    M, n, dev = q.shape[0], lens.numel(), _device(fn, q)
+    el, i32 = _elem(fn, dm, cache, dev), _torch_module.int32
+    qw = dm.n_heads * dm.head_dim
+    q_p, ldq = _mat(fn, q, el, M, qw, dev)
+    st = load().xmod_cache_attention_chunk(
+        dm, cache, n, M, q_p, ldq, _vec(fn, start, i32, n + 1, dev), _vec(fn, seq, i32, n, dev),
+        _vec(fn, lens, i32, n, dev), _vec(fn, o, el, M * qw, dev),
+        _vec(fn, lse, _torch_module.float32, M * dm.n_heads, dev),
+        _vec(fn, ws, ws.dtype, ws.numel(), dev), ws.numel() * ws.element_size(),
+        _raw_stream(stream, dev))
+    if st:
+        raise XmodError(fn, st)
+
+
+def rope(head_dim, theta=10000.0, rot_dim=None, interleaved=False, scaling=ROPE_PLAIN, factor=1.0,
+         trained=0) -> Rope:
+    """xmod_rope_init: rotary positions that turn the first rot_dim (None: all) of head_dim
+    dimensions. The structure's freq and amplitude may be changed afterwards."""
+    r = Rope()
+    rot = head_dim if rot_dim is None else rot_dim
+    if not 0 < rot <= head_dim:
+        raise XmodError("xmod_rope_init", ERR_INVALID_ARG)
+    _check("xmod_rope_init", load().xmod_rope_init(
+        ctypes.byref(r), int(rot), 1 if interleaved else 0, float(theta), int(scaling),
+        float(factor), int(trained)))
+    return r
+
+
+def qk_rope(dm, qkv, w, rope: Rope, out, pos=None, stream=None):
+    """xmod_qk_rope: the q and k heads of qkv [M, >= (n_heads + n_kv_heads) head_dim], normed (w: a
+    LayerWeights, whose QK-norm gains count, or None) and turned at pos [M] (None: m mod T),
+    into out [M, (n_heads + n_kv_heads) head_dim] (qkv itself, or its first columns: in place)."""
+    fn = "xmod_qk_rope"
+    M, dev = qkv.shape[0], _device(fn, qkv)
+    el = _torch_module.bfloat16 if dm.dtype == BF16 else _torch_module.float32
+    width = (dm.n_heads + dm.n_kv_heads) * dm.head_dim
+    x, ldx = _cols(fn, qkv, el, M, width, dev)
+    y, ldy = _cols(fn, out, el, M, width, dev)
+    _check_gains(fn, w, el, dm.head_dim, dev)
+    st = load().xmod_qk_rope(dm, M, x, ldx, w, rope, _vec(fn, pos, _torch_module.int32, M, dev), y,
+                             ldy, _raw_stream(stream, dev))
+    if st:
+        raise XmodError(fn, st)
+
+
+def qk_rope_bwd_workspace_bytes(dm: Dims, M: int) -> int:
+    return int(load().xmod_qk_rope_bwd_workspace_bytes(ctypes.byref(dm), int(M)))
+
+
+def qk_rope_bwd(dm, qkv, w, rope: Rope, dout, din, pos=None, dq_norm=None, dk_norm=None, ws=None,
+                stream=None):
+    """xmod_qk_rope_bwd: din of the gradient dout (both [M, (n_heads + n_kv_heads) head_dim]; may
+    be one tensor) and, with gains, dq_norm and dk_norm [head_dim] fp32; qkv and ws may be None
+    without gains."""
+    fn = "xmod_qk_rope_bwd"
+    M, dev = dout.shape[0], _device(fn, dout)
+    el = _torch_module.bfloat16 if dm.dtype == BF16 else _torch_module.float32
+    width, f32 = (dm.n_heads + dm.n_kv_heads) * dm.head_dim, _torch_module.float32
+    x, ldx = _cols(fn, qkv, el, M, width, dev) if qkv is not None else (None, 0)
+    d, ldd = _cols(fn, dout, el, M, width, dev)
+    y, ldy = _cols(fn, din, el, M, width, dev)
+    _check_gains(fn, w, el, dm.head_dim, dev)
+    st = load().xmod_qk_rope_bwd(
+        dm, M, x, ldx, w, rope, _vec(fn, pos, _torch_module.int32, M, dev), d, ldd, y, ldy,
+        _vec(fn, dq_norm, f32, dm.head_dim, dev), _vec(fn, dk_norm, f32, dm.head_dim, dev),
+        _vec(fn, ws, ws.dtype, ws.numel(), dev) if ws is not None else None, _wsb(ws),
+        _raw_stream(stream, dev))
+    if st:
+        raise XmodError(fn, st)
+
+
 def _logits(fn, t):
     """(dtype code, rows, width, pointer, row stride, device) of logits."""
     T = _torch()
@@ -545,6 +664,24 @@ def token_logprobs_bwd(logits, target, lse, g_logp, dlogits, entropy=None, g_ent
         dt, N, V, x, ld, _vec(fn, target, i32, N, dev), _vec(fn, lse, f32, N, dev),
         _vec(fn, entropy, f32, N, dev), _vec(fn, g_logp, f32, N, dev),
         _vec(fn, g_entropy, f32, N, dev), d, ldd, _vec(fn, status, i32, 1, dev),
+        _raw_stream(stream, dev))
+    if st:
+        raise XmodError(fn, st)
+
+
+def sample_tokens(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None,
+                  logp=None, status=None, stream=None):
+    """xmod_sample_tokens: a token of each row of logits [N, V] (bf16 or fp32; rows may be
+    strided) for u [N] fp32 in [0, 1); temperature, top_p, min_p [N] fp32 and top_k [N] int32
+    may each be None (1; off). token [N] int32 and logp [N] fp32 (None: not wanted) are
+    written."""
+    fn = "xmod_sample_tokens"
+    dt, N, V, x, ld, dev = _logits(fn, logits)
+    i32, f32 = _torch_module.int32, _torch_module.float32
+    st = load().xmod_sample_tokens(
+        dt, N, V, x, ld, _vec(fn, temperature, f32, N, dev), _vec(fn, top_k, i32, N, dev),
+        _vec(fn, top_p, f32, N, dev), _vec(fn, min_p, f32, N, dev), _vec(fn, u, f32, N, dev),
+        _vec(fn, token, i32, N, dev), _vec(fn, logp, f32, N, dev), _vec(fn, status, i32, 1, dev),
         _raw_stream(stream, dev))
     if st:
         raise XmodError(fn, st)
