@@ -59,11 +59,11 @@ template <typename T, int QR> int launch_join(const Ctx& c, const ChunkArgs& a, 
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
-constexpr int kQueryRows = 64;   // of a segment
-
 size_t chunk_workspace(const xmod_dims* dm) {
-  const size_t part = (size_t)kQueryRows * (dm->head_dim + 2) * 4;
-  return 256 + round256(kChunkMaxCtas * sizeof(ChunkJoin)) + 2 * kChunkMaxCtas * part;
+  const bool fp32 = dm->dtype == XMOD_FP32;
+  const size_t part = (size_t)(fp32 ? kChunkF32Rows : kChunkTcRows) * (dm->head_dim + 2) * 4;
+  return 256 + round256(kChunkMaxCtas * sizeof(ChunkJoin)) +
+         2 * (size_t)(fp32 ? kChunkMaxCtas : kChunkTcMaxCtas) * part;
 }
 
 }  // namespace
@@ -92,9 +92,11 @@ int xmod_cache_attention_chunk(const xmod_dims* dm, const xmod_kv_cache* cache, 
     return XMOD_ERR_INVALID_ARG;
   if (!ptr16(ws) || ws_bytes < chunk_workspace(dm)) return XMOD_ERR_WORKSPACE;
   const bool fp32 = dm->dtype == XMOD_FP32, fp8 = cache->format == XMOD_CACHE_E4M3;
+  if (!fp32 && !tma_available()) return XMOD_ERR_UNSUPPORTED;
   const int sms = device_sms();
   if (sms <= 0) return XMOD_ERR_CUDA;
-  const int ctas = 2 * sms < kChunkMaxCtas ? 2 * sms : kChunkMaxCtas;
+  const int want = fp32 ? 2 * sms : sms, most = fp32 ? kChunkMaxCtas : kChunkTcMaxCtas;
+  const int ctas = want < most ? want : most, rows = fp32 ? kChunkF32Rows : kChunkTcRows;
   const int group = dm->n_heads / dm->n_kv_heads;
   ChunkArgs a{};
   a.n_chunks = n_chunks;
@@ -117,18 +119,20 @@ int xmod_cache_attention_chunk(const xmod_dims* dm, const xmod_kv_cache* cache, 
   a.page_size = cache->page_size;
   a.n_seqs = cache->n_seqs;
   a.max_pages = cache->max_pages;
-  a.hpt = group < kQueryRows ? group : kQueryRows;
-  a.tpt = kQueryRows / a.hpt;
+  a.hpt = group < rows ? group : rows;
+  a.tpt = rows / a.hpt;
   a.passes = (group + a.hpt - 1) / a.hpt;
   a.box = cache->page_size % 64 == 0 ? 64 : cache->page_size % 32 == 0 ? 32 : 16;
   a.join = (ChunkJoin*)((char*)ws + 256);
   a.part = (float*)((char*)ws + 256 + round256(kChunkMaxCtas * sizeof(ChunkJoin)));
   a.status = (int*)ws;
   const Ctx c{(cudaStream_t)stream, a.status};
-  const int r = launch_chunk_f32(c, a, dm->head_dim, fp8, !fp32, ctas);
-  if (r) return r;
-  if (fp32) return launch_join<float, kQueryRows>(c, a, dm->head_dim, ctas);
-  return launch_join<__nv_bfloat16, kQueryRows>(c, a, dm->head_dim, ctas);
+  if (fp32) {
+    const int r = launch_chunk_f32(c, a, dm->head_dim, ctas);
+    return r ? r : launch_join<float, kChunkF32Rows>(c, a, dm->head_dim, ctas);
+  }
+  const int r = launch_chunk_tc(c, a, dm->head_dim, fp8, ctas);
+  return r ? r : launch_join<__nv_bfloat16, kChunkTcRows>(c, a, dm->head_dim, ctas);
 }
 
 }  // extern "C"

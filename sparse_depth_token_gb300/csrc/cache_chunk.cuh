@@ -18,6 +18,9 @@ namespace xmod {
 
 constexpr int kChunkKeys = 64;        // keys of a tile
 constexpr int kChunkMaxCtas = 512;    // CTAs the workspace has room for
+constexpr int kChunkTcRows = 256;     // query rows of a segment: tensor cores, one CTA an SM
+constexpr int kChunkTcMaxCtas = 192;
+constexpr int kChunkF32Rows = 64;     // FFMA, two CTAs an SM
 
 // A segment that starts in a CTA's range and ends in a later one's.
 struct ChunkJoin {
@@ -268,6 +271,7 @@ __device__ __forceinline__ ChunkJoin chunk_join(const ChunkPlan& p, const ChunkW
 
 // Launchers of the two kernels (cache_chunk_f32.cu, cache_chunk_tc.cu); ctas as planned.
 struct Ctx;
-int launch_chunk_f32(const Ctx& c, const ChunkArgs& a, int hd, bool fp8, bool bf16, int ctas);
+int launch_chunk_f32(const Ctx& c, const ChunkArgs& a, int hd, int ctas);
+int launch_chunk_tc(const Ctx& c, const ChunkArgs& a, int hd, bool fp8, int ctas);
 
 }  // namespace xmod

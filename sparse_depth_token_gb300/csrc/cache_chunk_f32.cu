@@ -1,6 +1,5 @@
 // Attention of a chunk of new tokens over the paged cache on FFMA: fp32 throughout.
 
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include <atomic>
@@ -11,31 +10,7 @@ namespace xmod {
 
 namespace {
 
-constexpr int kRows = 64, kThreads = 256;
-
-// Keys and values of the cache as fp32: 16-byte vector of T or of e4m3 codes.
-template <typename T, bool FP8> struct Source {
-  static constexpr int ES = FP8 ? 1 : (int)sizeof(T), VE = 16 / ES;
-  static __device__ __forceinline__ void load(const void* p, float scale, float (&x)[VE]) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p);
-    if constexpr (FP8) {
-      const __nv_fp8x2_storage_t* c = reinterpret_cast<const __nv_fp8x2_storage_t*>(&raw);
-#pragma unroll
-      for (int i = 0; i < VE / 2; ++i) {
-        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c[i], __NV_E4M3)));
-        x[2 * i] = f.x * scale;
-        x[2 * i + 1] = f.y * scale;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE / 2; ++i) {
-        const float2 f = vec_pair<T>(raw, i);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    }
-  }
-};
+constexpr int kRows = kChunkF32Rows, kThreads = 256;
 
 template <int HD> struct Smem {
   static constexpr int QLD = HD + 4, PLD = kChunkKeys + 4;
@@ -46,10 +21,9 @@ template <int HD> struct Smem {
 
 // 16 x 16 threads: thread (ty, tx) has rows 4 ty .. 4 ty + 3, keys tx + 16 j of the scores and
 // dimensions 4 tx + 64 j .. of the output.
-template <typename T, bool FP8, int HD>
+template <int HD>
 __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const ChunkArgs a) {
   using S = Smem<HD>;
-  using Src = Source<T, FP8>;
   constexpr int DW = HD >= 64 ? 4 : 2, DN = HD / (16 * DW);   // DN groups of DW dimensions
   extern __shared__ __align__(16) uint8_t smem[];
   S& s = *reinterpret_cast<S*>(smem);
@@ -83,18 +57,18 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
       const ChunkRow r = chunk_row(a, w.k, w.hp, w.t, R);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r.m >= 0) {
-        const T* p = (const T*)a.q + r.m * a.ldq + r.head * HD + d;
+        const float* p = (const float*)a.q + r.m * a.ldq + r.head * HD + d;
         x = make_float4(ld_f(p) * to_log2, ld_f(p + 1) * to_log2, ld_f(p + 2) * to_log2, ld_f(p + 3) * to_log2);
       }
       *reinterpret_cast<float4*>(&s.q[R * S::QLD + d]) = x;
     }
     // slots of the cache into shared memory; those at and after the segment's limit as zeros
-    auto fill = [&](const void* base, const float* scales, int key0) {
-      constexpr int CH = HD / Src::VE;
+    auto fill = [&](const float* cache, int key0) {
+      constexpr int CH = HD / 4;
       const int g = w.hp / a.passes;
       for (int i = tid; i < kChunkKeys * CH; i += kThreads) {
         const int key = i / CH, c = i % CH, slot = key0 + key;
-        float x[Src::VE];
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (slot < w.limit) {
           int page = a.table[(int64_t)w.k.seq * a.max_pages + slot / a.page_size];
           if (page < 0 || page >= a.n_pages) {
@@ -102,20 +76,14 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
             page = 0;
           }
           const int64_t at = ((int64_t)page * a.hkv + g) * a.page_size + slot % a.page_size;
-          Src::load((const uint8_t*)base + (at * HD + c * Src::VE) * Src::ES, FP8 ? scales[at] : 1.f, x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < Src::VE; ++e) x[e] = 0.f;
+          x = *reinterpret_cast<const float4*>(cache + at * HD + c * 4);
         }
-#pragma unroll
-        for (int e = 0; e < Src::VE; e += 4)
-          *reinterpret_cast<float4*>(&s.kv[key * S::QLD + c * Src::VE + e]) =
-              make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        *reinterpret_cast<float4*>(&s.kv[key * S::QLD + c * 4]) = x;
       }
     };
     for (int tile = first; tile < last; ++tile) {
       const int key0 = tile * kChunkKeys;
-      fill(a.k, a.k_scale, key0);
+      fill((const float*)a.k, key0);
       __syncthreads();
       float sc[4][4];
 #pragma unroll
@@ -165,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
         for (int d = 0; d < DN * DW; ++d) o[i][d] *= keep;
       }
       __syncthreads();
-      fill(a.v, a.v_scale, key0);
+      fill((const float*)a.v, key0);
       __syncthreads();
       // a key past a row's limit may hold anything: its product is left out, not weighted by 0
       const bool guard = __any_sync(0xffffffffu, masked);
@@ -213,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
         for (int g = 0; g < DN; ++g)
 #pragma unroll
           for (int e = 0; e < DW; ++e)
-            st_f((T*)a.o + head * HD + (g * 16 + tx) * DW + e, o[i][g * DW + e] * inv);
+            ((float*)a.o)[head * HD + (g * 16 + tx) * DW + e] = o[i][g * DW + e] * inv;
         if (a.lse && tx == 0) a.lse[head] = (mx[i] + log2f(sum[i])) * 0.6931471805599453f;
       } else {
 #pragma unroll
@@ -232,27 +200,21 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
   }
 }
 
-template <typename T, bool FP8, int HD> int launch_f32(const Ctx& c, const ChunkArgs& a, int ctas) {
+template <int HD> int launch_f32(const Ctx& c, const ChunkArgs& a, int ctas) {
   static std::atomic<uint64_t> done{0};
-  auto k = cache_chunk_f32_kernel<T, FP8, HD>;
+  auto k = cache_chunk_f32_kernel<HD>;
   if (allow_smem(k, (int)sizeof(Smem<HD>), done) != cudaSuccess) return XMOD_ERR_CUDA;
   XMOD_LAUNCH(c, "cache_chunk",
               launch_pdl(k, dim3(ctas), dim3(kThreads), sizeof(Smem<HD>), c.stream, a));
   return XMOD_OK;
 }
 
-template <typename T, bool FP8> int launch_f32_hd(const Ctx& c, const ChunkArgs& a, int hd, int ctas) {
-  if (hd == 128) return launch_f32<T, FP8, 128>(c, a, ctas);
-  if (hd == 64) return launch_f32<T, FP8, 64>(c, a, ctas);
-  return launch_f32<T, FP8, 32>(c, a, ctas);
-}
-
 }  // namespace
 
-int launch_chunk_f32(const Ctx& c, const ChunkArgs& a, int hd, bool fp8, bool bf16, int ctas) {
-  if (fp8) return launch_f32_hd<__nv_bfloat16, true>(c, a, hd, ctas);
-  if (bf16) return launch_f32_hd<__nv_bfloat16, false>(c, a, hd, ctas);
-  return launch_f32_hd<float, false>(c, a, hd, ctas);
+int launch_chunk_f32(const Ctx& c, const ChunkArgs& a, int hd, int ctas) {
+  if (hd == 128) return launch_f32<128>(c, a, ctas);
+  if (hd == 64) return launch_f32<64>(c, a, ctas);
+  return launch_f32<32>(c, a, ctas);
 }
 
 }  // namespace xmod

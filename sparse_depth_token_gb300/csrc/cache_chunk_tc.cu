@@ -1,0 +1,840 @@
+// Attention of a chunk of new tokens over the paged cache on the tcgen05 tensor cores: bf16
+// queries over a bf16 or an e4m3 cache.
+//
+//   o = sum_i p_i V_i,  p = softmax_i(q . K_i / sqrt(hd)),  i < the row's limit
+//
+// One persistent CTA per SM takes its range of the tile list (cache_chunk.cuh). A segment is two
+// MMA tiles, A and B, of 128 query rows each (a row is a token and a query head of one KV head),
+// which share every 64-key tile of K and V. Roles:
+//   warp 0        TMA of K and V (pages gathered box by box) into rings of stages, K a tile ahead
+//   warp 1        owner of the tensor memory; one lane issues S = Q K^T (two buffers for each of
+//                 A and B) and O += P V, each as soon as its inputs are there
+//   warp 2        the segments' descriptions and query rows, the next segment's as soon as the
+//                 last S of this one has been computed
+//   warps 4..7    softmax of A, a row a thread: scores from tensor memory, running maximum and
+//   warps 8..11   sum, P back over the scores as bf16; the same for B
+//   warps 12..15  (e4m3) codes to bf16, exactly
+// The running maximum only moves when it grows by more than 2^8 (weights stay below 256 and
+// keep their relative rounding in bf16); O is then rescaled in tensor memory.
+//
+// V is used as the cache stores it, [slot, dimension], as an MN-major operand: nothing is
+// transposed. A slot that a row does not see must not touch it even if it holds an infinity or
+// NaN, which a weight of 0 does not ensure. So in the tiles that some row of the segment sees
+// only in part, the softmax warps look at V first: slots past the segment's end become zeros;
+// and if another slot that some row does not see holds such a value, those values are added by
+// hand to the rows that see them and then replaced by zeros.
+
+#include <cuda.h>
+#include <float.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "cache_chunk.cuh"
+#include "tc_common.cuh"
+
+namespace xmod {
+
+namespace {
+
+using namespace tc;
+
+constexpr int KB = kChunkKeys;
+constexpr int QR = kChunkTcRows;
+constexpr float kRescale = 8.0f;   // log2 units
+
+template <int HD, bool FP8> struct Tc {
+  static constexpr int RB = HD >= 64 ? 128 : 64;            // bytes of a swizzled row
+  static constexpr int HALVES = HD * 2 / RB;                // of a head's dimensions
+  static constexpr int Q_HALF = 128 * RB, Q_TILE = HALVES * Q_HALF;
+  static constexpr int K_HALF = KB * RB, K_TILE = HALVES * K_HALF;
+  static constexpr int NK = FP8 ? 3 : HD == 128 ? 4 : HD == 64 ? 6 : 8;   // stages of K, and of V
+  static constexpr int CRB = HD >= 128 ? 128 : HD;          // bytes of a row of codes
+  static constexpr int CODES = FP8 ? KB * HD : 0;           // of K, and of V
+  static constexpr int NC = FP8 ? 3 : 0;
+  static constexpr int SCALES = FP8 ? 2 * KB * 4 : 0;
+  static constexpr int DATA = 2 * Q_TILE + 2 * NK * K_TILE + NC * (2 * CODES + SCALES) + NK * SCALES;
+  static constexpr int MISC = 2048;
+  static constexpr int SMEM = DATA + MISC + 1024;
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int TMEM_COLS = 512;                     // S: 4 x 64, O: 2 x HD
+  static constexpr int SW = RB == 128 ? 2 : 4;              // descriptor's swizzle code
+  static_assert(SMEM <= 227 * 1024, "");
+};
+
+// A segment in a CTA's range, as the loader describes it to the softmax warps.
+struct Segment {
+  Chunk k;
+  int chunk, hp, t, tiles, limit, first, last;   // tiles first .. last - 1 are this CTA's
+  int both;                                      // B has rows
+};
+constexpr int kSegments = 4;
+enum { kSegFirst = 1, kSegLast = 2, kSegBoth = 4 };   // what the MMA warp is told about a tile
+
+__device__ __forceinline__ bool segment_both(const ChunkArgs& a, const Chunk& k, int t) {
+  return (int64_t)min(a.tpt, k.n - t * a.tpt) * a.hpt > 128;
+}
+
+// K-major operand: rows of RB bytes, groups of 8 rows RB * 8 bytes apart.
+template <int RB, int SW> __device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)((8 * RB) >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)SW << 61;
+}
+// MN-major operand: atoms of RB bytes (MN) x 8 rows (K), the atoms along K 8 * RB bytes apart,
+// those along MN `stride`.
+template <int RB, int SW> __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((stride >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((8 * RB) >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)SW << 61;
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of `rows` rows.
+template <int RB> __device__ __forceinline__ uint32_t swizzled(int r, int c, int rows) {
+  constexpr int CH = RB / 16;
+  const int x = RB == 128 ? (r & 7) : RB == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+  return (uint32_t)((c / CH) * rows * RB + r * RB + (((c % CH) ^ x) << 4));
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Nonzero if one of the two bf16 of w is an infinity or NaN.
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// Four e4m3 codes to bf16, exactly: exponent and mantissa moved to their places make the value
+// times 2^-120 (subnormals too); a code of NaN is put in by hand.
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // codes in the high bytes
+  uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
+  uint32_t y = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+  const uint32_t up = 0x7b807b80u;   // 2^120
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(up));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(up));
+  if ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
+    if ((w & 0x7fu) == 0x7fu) lo |= 0x00007fffu;
+    if ((w & 0x7f00u) == 0x7f00u) lo |= 0x7fff0000u;
+    if ((w & 0x7f0000u) == 0x7f0000u) hi |= 0x00007fffu;
+    if ((w & 0x7f000000u) == 0x7f000000u) hi |= 0x7fff0000u;
+  }
+}
+
+template <int HD, bool FP8>
+__global__ void __launch_bounds__((Tc<HD, FP8>::THREADS), 1)
+cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                      const ChunkArgs a) {
+  using C = Tc<HD, FP8>;
+  constexpr int NK = C::NK, RB = C::RB;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const uint32_t sQ = base, sK = sQ + 2 * C::Q_TILE, sV = sK + NK * C::K_TILE;
+  const uint32_t sCode = sV + NK * C::K_TILE;                       // stages: K codes, V codes
+  const uint32_t sCodeScale = sCode + C::NC * 2 * C::CODES;         // stages: K scales, V scales
+  const uint32_t sScale = sCodeScale + C::NC * C::SCALES;           // the same beside the V stages
+  uint8_t* const misc = gbase + C::DATA;
+  const uint32_t sMisc = base + C::DATA;
+  // misc: barriers, then what the roles tell one another
+  uint32_t bar = sMisc;
+  auto take = [&](int n) {
+    const uint32_t b = bar;
+    bar += 8 * n;
+    return b;
+  };
+  const uint32_t K_FULL = take(NK), K_EMPTY = take(NK), V_FULL = take(NK), V_EMPTY = take(NK);
+  const uint32_t S_FULL = take(4), S_EMPTY = take(4), P_FULL = take(4), P_EMPTY = take(4);   // [A, B][2]
+  const uint32_t Q_FULL = take(1), Q_EMPTY = take(1), SEG_FULL = take(kSegments), SEG_EMPTY = take(kSegments);
+  const uint32_t LOOK = take(2), C_FULL = take(C::NC), C_EMPTY = take(C::NC);
+  constexpr int kBarBytes = 8 * (4 * NK + 16 + 2 + 2 * kSegments + 2 + 2 * C::NC);
+  static_assert(kBarBytes <= 640, "");
+  ChunkPlan* const plan = reinterpret_cast<ChunkPlan*>(misc + 640);
+  long long* const scratch = reinterpret_cast<long long*>(misc + 640 + 64);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc + 832);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 840);
+  unsigned long long* const bad_keys = reinterpret_cast<unsigned long long*>(misc + 848);   // [2][3]
+  volatile int* const tile_info = reinterpret_cast<volatile int*>(misc + 896);              // [NK]
+  volatile int* const code_info = reinterpret_cast<volatile int*>(misc + 928);              // [NC]
+  Segment* const segs = reinterpret_cast<Segment*>(misc + 944);
+  static_assert(sizeof(ChunkPlan) <= 64 && 944 + kSegments * sizeof(Segment) <= C::MISC && NK <= 8, "");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(K_FULL + 8 * i, FP8 ? 128 : 1);
+      mbar_init(K_EMPTY + 8 * i, 1);
+      mbar_init(V_FULL + 8 * i, FP8 ? 128 : 1);
+      mbar_init(V_EMPTY + 8 * i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(S_FULL + 8 * i, 1);
+      mbar_init(S_EMPTY + 8 * i, 128);
+      mbar_init(P_FULL + 8 * i, 128);
+      mbar_init(P_EMPTY + 8 * i, 1);
+    }
+    mbar_init(Q_FULL, 32);
+    mbar_init(Q_EMPTY, 1);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(SEG_FULL + 8 * i, 1);
+      mbar_init(SEG_EMPTY + 8 * i, 8);
+    }
+    mbar_init(LOOK, 4);       // A's warps alone
+    mbar_init(LOOK + 8, 8);   // A's and B's
+    for (int i = 0; i < C::NC; ++i) {
+      mbar_init(C_FULL + 8 * i, 1);
+      mbar_init(C_EMPTY + 8 * i, 128);
+    }
+    *abort_flag = 0;
+    for (int i = 0; i < 6; ++i) bad_keys[i] = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&mK);
+    prefetch_tensormap(&mV);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;   // S of A, S of B (two buffers each), O of A, O of B
+  pdl_wait();
+  make_chunk_plan(a, plan, scratch);
+  const int ntiles = (int)(plan->end - plan->begin);
+  if (tid == 0) a.join[blockIdx.x].chunk = -1;
+
+  if (ntiles <= 0) {
+    // nothing to do
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ TMA
+    ChunkWalk w;
+    w.begin(a, *plan);
+    int left = ntiles, it = 0;
+    const int nbox = KB / a.box;
+    int page = 0, y_prev = 0, boxes_prev = 0;
+    auto page_of = [&](int tile) {   // lane b: the page of box b
+      const int key = tile * KB + lane * a.box;
+      return lane < nbox && key < w.limit ? a.table[(int64_t)w.k.seq * a.max_pages + key / a.page_size] : 0;
+    };
+    auto load_v = [&](int i, int y, int boxes) {   // V of the i-th tile of the range
+      const int st = i % NK;
+      const uint32_t full = V_FULL + 8 * st;
+      if (i >= NK && !mbar_wait(V_EMPTY + 8 * st, ((i / NK) & 1) ^ 1, abort_flag, a.status)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * HD * 2);
+      __syncwarp();
+      if (lane < boxes) {
+#pragma unroll
+        for (int h = 0; h < C::HALVES; ++h)
+          tma_load_2d(sV + st * C::K_TILE + h * C::K_HALF + lane * a.box * RB, &mV, full, h * 64, y);
+      }
+      return true;
+    };
+    bool ok = true;
+    while (left > 0 && ok) {
+      const int first = w.tile, last = min(w.tiles, first + left);
+      const int both = segment_both(a, w.k, w.t) ? kSegBoth : 0, g = w.hp / a.passes;
+      left -= last - first;
+      page = page_of(first);
+      for (int tile = first; tile < last && ok; ++tile, ++it) {
+        const int next = tile + 1 < last ? page_of(tile + 1) : 0;
+        const int valid = max(0, min(KB, w.limit - tile * KB)), boxes = (valid + a.box - 1) / a.box;
+        const int info = (tile == first ? kSegFirst : 0) | (tile == last - 1 ? kSegLast : 0) | both;
+        int pg = page;
+        if (lane < boxes && (pg < 0 || pg >= a.n_pages)) {
+          report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+          pg = 0;
+        }
+        const int key = tile * KB + lane * a.box;
+        const int y = (int)(((int64_t)pg * a.hkv + g) * a.page_size + key % a.page_size);
+        if constexpr (!FP8) {
+          const int st = it % NK;
+          const uint32_t full = K_FULL + 8 * st;
+          ok = it < NK || mbar_wait(K_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            tile_info[st] = info;
+            mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * HD * 2);
+          }
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_load_2d(sK + st * C::K_TILE + h * C::K_HALF + lane * a.box * RB, &mK, full, h * 64, y);
+          }
+          if (it > 0) ok = __all_sync(0xffffffffu, load_v(it - 1, y_prev, boxes_prev));
+        } else {
+          const int st = it % C::NC;
+          const uint32_t full = C_FULL + 8 * st;
+          ok = it < C::NC || mbar_wait(C_EMPTY + 8 * st, ((it / C::NC) & 1) ^ 1, abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            code_info[st] = info;
+            mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * (2 * HD + 8));
+          }
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t k = sCode + st * 2 * C::CODES + lane * a.box * C::CRB;
+            tma_load_2d(k, &mK, full, 0, y);
+            tma_load_2d(k + C::CODES, &mV, full, 0, y);
+            const uint32_t s = sCodeScale + st * C::SCALES + lane * a.box * 4;
+            bulk_load(s, a.k_scale + y, a.box * 4, full);
+            bulk_load(s + KB * 4, a.v_scale + y, a.box * 4, full);
+          }
+        }
+        y_prev = y;
+        boxes_prev = boxes;
+        page = next;
+      }
+      if (left > 0) w.next_segment(a);
+    }
+    if (!FP8 && ok) load_v(it - 1, y_prev, boxes_prev);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, KB);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | kIdescBMajorMN;
+      // next tile of the range for S and for P V of A and B; how many of them were theirs; the
+      // tiles' has-B flags by their last bits
+      int is[2] = {0, 0}, ip[2] = {0, 0}, cs[2] = {0, 0}, cp[2] = {0, 0}, segments = 0;
+      uint32_t both_bits = 0;
+      uint64_t t0 = global_timer_ns();
+      uint32_t spins = 0;
+      auto s_done = [&](int i, int info) {   // S of tile i issued for A and B
+        mma_commit(K_EMPTY + 8 * (i % NK));
+        if (info & kSegLast) mma_commit(Q_EMPTY);
+      };
+      while (ip[0] < ntiles || ip[1] < ntiles) {
+        bool progressed = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          // ---- S
+          const int i = is[x];
+          // B does not run ahead of A, which looks after the segment's beginning
+          if (i < ntiles && (x == 0 || i < is[0])) {
+            if (x == 0) {
+              if (cs[0] <= cp[0] + 1 && i <= is[1] + NK - 1 &&
+                  mbar_test_wait(K_FULL + 8 * (i % NK), (uint32_t)(i / NK) & 1u)) {
+                const int info = tile_info[i % NK];
+                const int b = cs[0] & 1;
+                if ((!(info & kSegFirst) || mbar_test_wait(Q_FULL, (uint32_t)segments & 1u)) &&
+                    mbar_test_wait(S_EMPTY + 8 * b, ((uint32_t)(cs[0] >> 1) & 1u) ^ 1u)) {
+                  if (info & kSegFirst) ++segments;
+                  tc_fence_after();
+                  const uint32_t k = sK + (i % NK) * C::K_TILE;
+#pragma unroll
+                  for (int kk = 0; kk < HD / 16; ++kk) {
+                    constexpr int PER = RB / 32;   // 16-deep steps of a half
+                    mma_bf16(tmem + b * KB, desc_k<RB, C::SW>(sQ + (kk / PER) * C::Q_HALF) + 2ull * (kk % PER),
+                             desc_k<RB, C::SW>(k + (kk / PER) * C::K_HALF) + 2ull * (kk % PER), idesc_s, kk != 0);
+                  }
+                  mma_commit(S_FULL + 8 * b);
+                  ++cs[0];
+                  ++is[0];
+                  const uint32_t bit = 1u << (i & 31);
+                  both_bits = info & kSegBoth ? both_bits | bit : both_bits & ~bit;
+                  progressed = true;
+                }
+              }
+            } else {
+              const int info = tile_info[i % NK];
+              if (!(info & kSegBoth)) {
+                s_done(i, info);
+                ++is[1];
+                progressed = true;
+              } else if (cs[1] <= cp[1] + 1) {
+                const int b = cs[1] & 1;
+                if (mbar_test_wait(S_EMPTY + 16 + 8 * b, ((uint32_t)(cs[1] >> 1) & 1u) ^ 1u)) {
+                  tc_fence_after();
+                  const uint32_t k = sK + (i % NK) * C::K_TILE;
+#pragma unroll
+                  for (int kk = 0; kk < HD / 16; ++kk) {
+                    constexpr int PER = RB / 32;
+                    mma_bf16(tmem + (2 + b) * KB,
+                             desc_k<RB, C::SW>(sQ + C::Q_TILE + (kk / PER) * C::Q_HALF) + 2ull * (kk % PER),
+                             desc_k<RB, C::SW>(k + (kk / PER) * C::K_HALF) + 2ull * (kk % PER), idesc_s, kk != 0);
+                  }
+                  mma_commit(S_FULL + 16 + 8 * b);
+                  s_done(i, info);
+                  ++cs[1];
+                  ++is[1];
+                  progressed = true;
+                }
+              }
+            }
+          }
+          // ---- O += P V; B's after A's, which frees the stage
+          const int j = ip[x];
+          if (j < is[x] && (x == 0 || j < ip[0])) {
+            const bool mine = x == 0 || (both_bits >> (j & 31) & 1);
+            const int b = cp[x] & 1, vs = j % NK;
+            if (!mine) {
+              mma_commit(V_EMPTY + 8 * vs);
+              ++ip[x];
+              progressed = true;
+            } else if (mbar_test_wait(P_FULL + 16 * x + 8 * b, (uint32_t)(cp[x] >> 1) & 1u) &&
+                       mbar_test_wait(V_FULL + 8 * vs, (uint32_t)(j / NK) & 1u)) {
+              tc_fence_after();
+              const uint32_t tp = tmem + (2 * x + b) * KB, to = tmem + 4 * KB + x * HD;
+              const uint32_t v = sV + vs * C::K_TILE;
+#pragma unroll
+              for (int kk = 0; kk < KB / 16; ++kk)   // 16 keys: 8 columns of P, 2 groups of 8 rows of V
+                mma_bf16_tmem_a(to, tp + 8 * kk, desc_mn<RB, C::SW>(v + kk * 16 * RB, C::K_HALF), idesc_o, 1u);
+              mma_commit(P_EMPTY + 16 * x + 8 * b);
+              if (x == 1) mma_commit(V_EMPTY + 8 * vs);
+              ++cp[x];
+              ++ip[x];
+              progressed = true;
+            }
+          }
+        }
+        if (progressed) {
+          t0 = global_timer_ns();
+          spins = 0;
+          continue;
+        }
+        if ((++spins & 255u) == 0u) {
+          if (*abort_flag) break;
+          if (global_timer_ns() - t0 > kWaitLimitNs) {
+            report_status(a.status, XMOD_ERR_TIMEOUT);
+            *abort_flag = 1;
+            break;
+          }
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ segments and their queries
+    ChunkWalk w;
+    w.begin(a, *plan);
+    int left = ntiles, s = 0;
+    bool ok = true;
+    for (;; ++s) {
+      const int e = s % kSegments;
+      ok = s < kSegments || mbar_wait(SEG_EMPTY + 8 * e, ((s / kSegments) & 1) ^ 1, abort_flag, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int first = w.tile, last = min(w.tiles, first + left);
+      const bool both = left > 0 && segment_both(a, w.k, w.t);
+      if (lane == 0) {
+        Segment& g = segs[e];
+        g.k = w.k;
+        g.chunk = w.chunk;
+        g.hp = w.hp;
+        g.t = w.t;
+        g.tiles = w.tiles;
+        g.limit = w.limit;
+        g.first = left > 0 ? first : -1;   // the end of the range
+        g.last = last;
+        g.both = both;
+        mbar_arrive(SEG_FULL + 8 * e);
+      }
+      __syncwarp();
+      if (left <= 0) break;
+      ok = s == 0 || mbar_wait(Q_EMPTY, (s - 1) & 1, abort_flag, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      constexpr int CH = HD / 8;   // 16-byte chunks of a row
+      for (int R0 = 0; R0 < (both ? QR : 128); R0 += 32) {
+        const ChunkRow mine = chunk_row(a, w.k, w.hp, w.t, R0 + lane);
+        const int64_t at = mine.m < 0 ? -1 : mine.m * a.ldq + (int64_t)mine.head * HD;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+          const int64_t from = __shfl_sync(0xffffffffu, at, r);
+          const int R = R0 + r;
+          const uint32_t dst = sQ + (R >> 7) * C::Q_TILE + swizzled<RB>(R & 127, c, 128);
+          if (from >= 0)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                         "l"((const __nv_bfloat16*)a.q + from + c * 8)
+                         : "memory");
+          else
+            sts128(dst, make_uint4(0u, 0u, 0u, 0u));
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(Q_FULL);
+      left -= last - first;
+      if (left > 0) w.next_segment(a);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------ softmax
+    const int x = (warp - 4) >> 2, quad = warp & 3, row128 = quad * 32 + lane, R = x * 128 + row128;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + 2 * x * KB, tO = tmem + lane_off + 4 * KB + x * HD;
+    const uint32_t bSF = S_FULL + 16 * x, bSE = S_EMPTY + 16 * x, bPF = P_FULL + 16 * x, bPE = P_EMPTY + 16 * x;
+    const float scale_log2 = 1.4426950408889634f * rsqrtf((float)HD);
+    int n = 0, i0 = 0;            // tiles this group has worked on; tiles before the segment
+    int looks[2] = {0, 0};        // looks at V, by A's warps alone and by all
+    uint32_t look_phase = 0;      // of the two barriers
+    bool ok = true;
+    // all softmax warps that work on the segment
+    auto meet = [&](int both) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(LOOK + 8 * both);
+      const bool r = mbar_wait(LOOK + 8 * both, (look_phase >> both) & 1u, abort_flag, a.status);
+      look_phase ^= 1u << both;
+      return __all_sync(0xffffffffu, r);
+    };
+    for (int s = 0; ok; ++s) {
+      const int e = s % kSegments;
+      if (!__all_sync(0xffffffffu, mbar_wait(SEG_FULL + 8 * e, (s / kSegments) & 1, abort_flag, a.status))) break;
+      const Segment g = segs[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(SEG_EMPTY + 8 * e);
+      if (g.first < 0) break;
+      const int count = g.last - g.first;
+      const int least = (int)max((int64_t)0, g.k.len - g.k.n + 1 + (int64_t)g.t * a.tpt);   // the first row's limit
+      if (x == 1 && !g.both) {
+        i0 += count;
+        continue;
+      }
+      ChunkRow row = chunk_row(a, g.k, g.hp, g.t, R);
+      const int limit = row.m < 0 ? g.limit : row.limit;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        float zero[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zero[i] = 0.f;
+        tmem_st32(tO + c * 32, zero);
+      }
+      tmem_st_wait();
+      for (int tile = g.first; tile < g.last; ++tile, ++n) {
+        const int b = n & 1, it = i0 + tile - g.first, vs = it % NK, key0 = tile * KB;
+        if (!__all_sync(0xffffffffu, mbar_wait(bSF + 8 * b, (uint32_t)(n >> 1) & 1u, abort_flag, a.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float v[KB];
+        tmem_ld64(tS + b * KB, v);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(bSE + 8 * b);
+        const float* sc = reinterpret_cast<const float*>(gbase + (sScale - base) + vs * C::SCALES);
+        if constexpr (FP8) {
+          // the scales lie there since K's codes were converted
+          if (!__all_sync(0xffffffffu, mbar_wait(K_FULL + 8 * vs, (uint32_t)(it / NK) & 1u, abort_flag, a.status))) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < KB; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + i);
+            v[i] *= f.x;
+            v[i + 1] *= f.y;
+            v[i + 2] *= f.z;
+            v[i + 3] *= f.w;
+          }
+        }
+        const bool masked = key0 + KB > least;   // some row of the segment does not see all of it
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < KB; ++i)
+            if (key0 + i >= limit) v[i] = -INFINITY;
+        }
+        float mc[KB / 16];
+#pragma unroll
+        for (int r = 0; r < KB / 16; ++r) {
+          const float* u = v + 16 * r;
+          float t = max3(u[0], u[1], u[2]);
+#pragma unroll
+          for (int i = 3; i < 15; i += 2) t = max3(t, u[i], u[i + 1]);
+          mc[r] = fmaxf(t, u[15]);
+        }
+        const float m_cand = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]) * scale_log2;
+        const bool grow = m_cand > m + kRescale;
+        const float m_new = grow ? m_cand : m;
+        const float alpha = grow ? exp2f(m - m_new) : 1.0f;
+        if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+          // O holds the tiles before: the last of their products has to have landed
+          const int q = n - 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float f = m == -INFINITY ? 1.0f : alpha;
+#pragma unroll 1
+          for (int c = 0; c < HD / 32; ++c) {
+            float ov[32];
+            tmem_ld32(tO + c * 32, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] *= f;
+            tmem_st32(tO + c * 32, ov);
+          }
+          tmem_st_wait();
+        }
+        m = m_new;
+        const float negm = m == -INFINITY ? 0.f : -m;
+        const float2 scale2 = make_float2(scale_log2, scale_log2), negm2 = make_float2(negm, negm);
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < KB; i += 2) {
+          const float2 y = fma2(make_float2(v[i], v[i + 1]), scale2, negm2);
+          const float2 p = make_float2(ex2(y.x), ex2(y.y));
+          acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], p);
+          v[i] = p.x;
+          v[i + 1] = p.y;
+        }
+        const float2 both_acc = add2(acc[0], acc[1]);
+        l = l * alpha + (both_acc.x + both_acc.y);
+        if constexpr (FP8) {
+#pragma unroll
+          for (int i = 0; i < KB; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + KB + i);
+            v[i] *= f.x;
+            v[i + 1] *= f.y;
+            v[i + 2] *= f.z;
+            v[i + 3] *= f.w;
+          }
+          if (masked) {   // a scale that is not seen may be anything
+#pragma unroll
+            for (int i = 0; i < KB; ++i)
+              if (key0 + i >= limit) v[i] = 0.f;
+          }
+        }
+        if (masked) {
+          // ---- V's slots that some row does not see
+          if (!__all_sync(0xffffffffu, mbar_wait(V_FULL + 8 * vs, (uint32_t)(it / NK) & 1u, abort_flag, a.status))) {
+            ok = false;
+            break;
+          }
+          constexpr int CH = HD / 8;
+          const uint32_t vt = sV + vs * C::K_TILE;
+          const int from = max(0, least - key0), valid = max(0, min(KB, g.limit - key0));
+          const int width = g.both ? 256 : 128;
+          unsigned long long bad = 0;
+          for (int i = from * CH + R; i < KB * CH; i += width) {
+            const int key = i / CH;
+            const uint32_t at = vt + swizzled<RB>(key, i % CH, KB);
+            if (key >= valid) {
+              sts128(at, make_uint4(0u, 0u, 0u, 0u));
+            } else {
+              const uint4 u = lds128(at);
+              if (nonfinite2(u.x) | nonfinite2(u.y) | nonfinite2(u.z) | nonfinite2(u.w)) bad |= 1ull << key;
+            }
+          }
+          // three slots in turn: the one of the look before last, which all have read before they
+          // came to this one, is cleared for the look after next
+          const int look = g.both ? looks[1]++ : looks[0]++;
+          unsigned long long* const slots = bad_keys + 3 * g.both;
+          const int slot = look % 3;
+          if (bad) atomicOr(&slots[slot], bad);
+          fence_proxy_async_smem();
+          if (!meet(g.both)) {
+            ok = false;
+            break;
+          }
+          bad = *reinterpret_cast<volatile unsigned long long*>(&slots[slot]);
+          if (R == 0) slots[(look + 2) % 3] = 0;
+          if (bad) {
+            // rare: infinities and NaN of V to the rows that see them, then zeros in their place
+            if (n > 0) {
+              const int q = n - 1;
+              if (!__all_sync(0xffffffffu, mbar_wait(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status))) {
+                ok = false;
+                break;
+              }
+            }
+            tc_fence_after();
+            float weight[KB];   // by key: local memory
+#pragma unroll
+            for (int i = 0; i < KB; ++i) weight[i] = v[i];
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+              float ov[32];
+              tmem_ld32(tO + c * 32, ov);
+              tmem_ld_wait();
+              for (unsigned long long rest = bad; rest; rest &= rest - 1) {
+                const int key = __ffsll((long long)rest) - 1;
+                if (key0 + key >= limit) continue;
+                const float p = weight[key];
+#pragma unroll
+                for (int d = 0; d < 32; d += 8) {
+                  const uint4 u = lds128(vt + swizzled<RB>(key, c * 4 + d / 8, KB));
+#pragma unroll
+                  for (int h = 0; h < 4; ++h) {
+                    const float2 f = vec_pair<__nv_bfloat16>(u, h);
+                    if (!isfinite(f.x)) ov[d + 2 * h] += p * f.x;
+                    if (!isfinite(f.y)) ov[d + 2 * h + 1] += p * f.y;
+                  }
+                }
+              }
+              __syncwarp();
+              tmem_st32(tO + c * 32, ov);
+            }
+            tmem_st_wait();
+            if (!meet(g.both)) {
+              ok = false;
+              break;
+            }
+            for (int i = from * CH + R; i < valid * CH; i += width) {
+              const uint32_t at = vt + swizzled<RB>(i / CH, i % CH, KB);
+              uint4 u = lds128(at);
+              uint32_t* h = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t f = nonfinite2(h[k]);
+                h[k] &= ~((f & 0x8000u ? 0xffffu : 0u) | (f & 0x80000000u ? 0xffff0000u : 0u));
+              }
+              sts128(at, u);
+            }
+            fence_proxy_async_smem();
+            if (!meet(g.both)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        float pk[32];
+#pragma unroll
+        for (int i = 0; i < KB; i += 2) pk[i / 2] = __uint_as_float(pack_bf16x2(v[i], v[i + 1]));
+        tmem_st32(tS + b * KB, pk);   // over the scores
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bPF + 8 * b);
+      }
+      if (!ok) break;
+      i0 += count;
+      // ---- the segment's result in this CTA's range
+      const int q = n - 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status))) break;
+      tc_fence_after();
+      const bool whole = g.first == 0 && g.last == g.tiles;
+      const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+      const int64_t head = row.m * a.hq + row.head;
+      float* part = chunk_part<QR, HD>(a, blockIdx.x, g.first > 0);
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        float ov[32];
+        tmem_ld32(tO + c * 32, ov);
+        tmem_ld_wait();
+        if (row.m >= 0) {
+          if (whole) {
+            __nv_bfloat16* dst = (__nv_bfloat16*)a.o + head * HD + c * 32;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(dst + i) =
+                  make_uint4(pack_bf16x2(ov[i] * inv, ov[i + 1] * inv), pack_bf16x2(ov[i + 2] * inv, ov[i + 3] * inv),
+                             pack_bf16x2(ov[i + 4] * inv, ov[i + 5] * inv), pack_bf16x2(ov[i + 6] * inv, ov[i + 7] * inv));
+          } else {
+            float* dst = part + 2 * QR + R * HD + c * 32;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(dst + i) = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+          }
+        }
+      }
+      if (row.m >= 0) {
+        if (whole) {
+          if (a.lse) a.lse[head] = (m + log2f(l)) * 0.6931471805599453f;
+        } else {
+          part[R] = m;
+          part[QR + R] = l;
+        }
+      }
+      if (R == 0 && g.first == 0 && !whole) {
+        ChunkWalk w;
+        w.chunk = g.chunk;
+        w.hp = g.hp;
+        w.t = g.t;
+        a.join[blockIdx.x] = chunk_join(*plan, w, g.tiles - g.last);
+      }
+    }
+  } else if (FP8 && warp >= 12) {
+    // ------------------------------------------------------------ codes to bf16
+    constexpr int CH = HD / 16;                      // 16-byte chunks of a row of codes
+    const int t = tid - 384;
+    bool ok = true;
+    for (int it = 0; it < ntiles && ok; ++it) {
+      const int cs = it % (C::NC ? C::NC : 1), st = it % NK;
+      ok = mbar_wait(C_FULL + 8 * cs, (it / (C::NC ? C::NC : 1)) & 1, abort_flag, a.status);
+      // K's and V's stages are those of the tile NK before: with V's the softmax is done with its scales
+      if (ok && it >= NK)
+        ok = mbar_wait(K_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status) &&
+             mbar_wait(V_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (t == 0) tile_info[st] = code_info[cs];
+      {
+        const float* from = reinterpret_cast<const float*>(gbase + (sCodeScale - base) + cs * C::SCALES);
+        float* to = reinterpret_cast<float*>(gbase + (sScale - base) + st * C::SCALES);
+        to[t] = from[t];   // 128: K's and V's
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t src = sCode + cs * 2 * C::CODES + kv * C::CODES;
+        const uint32_t dst = (kv ? sV : sK) + st * C::K_TILE;
+        // eight lanes take the same chunk of eight rows: their swizzled places differ
+#pragma unroll
+        for (int i = t; i < KB * CH; i += 128) {
+          const int r = (i & 7) + 8 * (i / (8 * CH)), c = (i >> 3) % CH;
+          const uint4 u = lds128(src + swizzled<C::CRB>(r, c, KB));
+          uint4 lo, hi;
+          codes_bf16(u.x, lo.x, lo.y);
+          codes_bf16(u.y, lo.z, lo.w);
+          codes_bf16(u.z, hi.x, hi.y);
+          codes_bf16(u.w, hi.z, hi.w);
+          sts128(dst + swizzled<RB>(r, 2 * c, KB), lo);
+          sts128(dst + swizzled<RB>(r, 2 * c + 1, KB), hi);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive((kv ? V_FULL : K_FULL) + 8 * st);
+      }
+      mbar_arrive(C_EMPTY + 8 * cs);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {   // copies in flight land before the CTA ends
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 20000000ull) {
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int HD, bool FP8> int launch_tc(const Ctx& c, const ChunkArgs& a, int ctas) {
+  using C = Tc<HD, FP8>;
+  CUtensorMap mk, mv;
+  const int64_t rows = (int64_t)a.n_pages * a.hkv * a.page_size;
+  const int cols = FP8 ? C::CRB : C::RB / 2;
+  if (!tma_map_rows(&mk, a.k, FP8 ? 1 : 2, rows, HD, cols, a.box) ||
+      !tma_map_rows(&mv, a.v, FP8 ? 1 : 2, rows, HD, cols, a.box))
+    return XMOD_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  auto k = cache_chunk_tc_kernel<HD, FP8>;
+  if (allow_smem(k, C::SMEM, done) != cudaSuccess) return XMOD_ERR_CUDA;
+  XMOD_LAUNCH(c, "cache_chunk", launch_pdl(k, dim3(ctas), dim3(C::THREADS), C::SMEM, c.stream, mk, mv, a));
+  return XMOD_OK;
+}
+
+template <bool FP8> int launch_tc_hd(const Ctx& c, const ChunkArgs& a, int hd, int ctas) {
+  if (hd == 128) return launch_tc<128, FP8>(c, a, ctas);
+  if (hd == 64) return launch_tc<64, FP8>(c, a, ctas);
+  return launch_tc<32, FP8>(c, a, ctas);
+}
+
+}  // namespace
+
+int launch_chunk_tc(const Ctx& c, const ChunkArgs& a, int hd, bool fp8, int ctas) {
+  return fp8 ? launch_tc_hd<true>(c, a, hd, ctas) : launch_tc_hd<false>(c, a, hd, ctas);
+}
+
+}  // namespace xmod
