@@ -9,45 +9,76 @@ namespace xmod {
 
 namespace {
 
-// Segment of CTA blockIdx.x that later CTAs' ranges continue: a warp a row, the parts' outputs
-// weighted to the common maximum, in CTA order.
+// Segment of CTA blockIdx.x that later CTAs' ranges continue, 32 rows a block: a lane has a row,
+// a warp every eighth group of four dimensions; the parts' outputs are weighted to the common
+// maximum, in CTA order, four parts on their way at a time.
 constexpr int kJoinWarps = 8;
 
 template <typename T, int HD, int QR>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_chunk_join_kernel(const ChunkArgs a) {
-  constexpr int E = HD / 32;
+  constexpr int G = HD / 4, E = G / kJoinWarps, AHEAD = 4;
   pdl_trigger();
   pdl_wait();
   const ChunkJoin j = a.join[blockIdx.x];
   if (j.chunk < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = blockIdx.y * kJoinWarps + warp;
-  const ChunkRow row = chunk_row(a, read_chunk(a, j.chunk), j.hp, j.t, R);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = blockIdx.y * 32 + lane;
+  constexpr int BLOCK = QR < 128 ? QR : 128;
+  const ChunkRow row = chunk_row(a, read_chunk(a, j.chunk), j.hp, j.t, R / BLOCK, R % BLOCK);
   if (row.m < 0) return;
   float top = -INFINITY;
-  for (int p = j.first + lane; p <= j.last; p += 32)
-    top = fmaxf(top, chunk_part<QR, HD>(a, p, p > j.first)[R]);
-  top = warp_max(top);
+#pragma unroll 8
+  for (int p = j.first; p <= j.last; ++p) top = fmaxf(top, chunk_part<QR, HD>(a, p, p > j.first)[R]);
   const float low = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, o[E];
+  float sum = 0.f;
+  float4 o[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int p = j.first; p <= j.last; ++p) {
-    const float* part = chunk_part<QR, HD>(a, p, p > j.first);
-    const float f = exp2f(part[R] - low);
-    sum = fmaf(part[QR + R], f, sum);
+  for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = j.first; p0 <= j.last; p0 += AHEAD) {
+    float m[AHEAD], l[AHEAD];
+    float4 v[AHEAD][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(part[2 * QR + R * HD + e * 32 + lane], f, o[e]);
+    for (int i = 0; i < AHEAD; ++i) {
+      const int p = min(p0 + i, j.last);
+      const float* part = chunk_part<QR, HD>(a, p, p > j.first);
+      m[i] = part[R];
+      l[i] = part[QR + R];
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        v[i][e] = *reinterpret_cast<const float4*>(part + 2 * QR + ((e * kJoinWarps + warp) * QR + R) * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (p0 + i > j.last) break;
+      const float f = exp2f(m[i] - low);
+      sum = fmaf(l[i], f, sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        o[e].x = fmaf(v[i][e].x, f, o[e].x);
+        o[e].y = fmaf(v[i][e].y, f, o[e].y);
+        o[e].z = fmaf(v[i][e].z, f, o[e].z);
+        o[e].w = fmaf(v[i][e].w, f, o[e].w);
+      }
+    }
   }
   const int64_t head = row.m * a.hq + row.head;
   const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) st_f((T*)a.o + head * HD + e * 32 + lane, o[e] * inv);
-  if (a.lse && lane == 0) a.lse[head] = (top + log2f(sum)) * 0.6931471805599453f;
+  for (int e = 0; e < E; ++e) {
+    T* dst = (T*)a.o + head * HD + (e * kJoinWarps + warp) * 4;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(dst) = make_float4(o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv);
+    } else {
+      uint4 w;
+      set_vec_pair<T>(w, 0, make_float2(o[e].x * inv, o[e].y * inv));
+      set_vec_pair<T>(w, 1, make_float2(o[e].z * inv, o[e].w * inv));
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w.x, w.y);
+    }
+  }
+  if (a.lse && warp == 0) a.lse[head] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int QR> int launch_join(const Ctx& c, const ChunkArgs& a, int hd, int ctas) {
-  const dim3 grid(ctas, QR / kJoinWarps), block(kJoinWarps * 32);
+  const dim3 grid(ctas, QR / 32), block(kJoinWarps * 32);
   if (hd == 128)
     XMOD_LAUNCH(c, "cache_chunk_join", launch_pdl(cache_chunk_join_kernel<T, 128, QR>, grid, block, 0, c.stream, a));
   else if (hd == 64)
@@ -119,9 +150,16 @@ int xmod_cache_attention_chunk(const xmod_dims* dm, const xmod_kv_cache* cache, 
   a.page_size = cache->page_size;
   a.n_seqs = cache->n_seqs;
   a.max_pages = cache->max_pages;
-  a.hpt = group < rows ? group : rows;
-  a.tpt = rows / a.hpt;
+  const int block = fp32 ? kChunkF32Rows : 128;
+  a.group = group;
+  a.hpt = group < block ? group : block;
+  a.block_tokens = block / a.hpt;
+  a.tpt = rows / block * a.block_tokens;
   a.passes = (group + a.hpt - 1) / a.hpt;
+  a.hpt_inverse = (65536 + a.hpt - 1) / a.hpt;
+  a.page_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (cache->page_size == 1 << i) a.page_shift = i;
   a.box = cache->page_size % 64 == 0 ? 64 : cache->page_size % 32 == 0 ? 32 : 16;
   a.join = (ChunkJoin*)((char*)ws + 256);
   a.part = (float*)((char*)ws + 256 + round256(kChunkMaxCtas * sizeof(ChunkJoin)));

@@ -1,9 +1,10 @@
 // What the kernels of a chunk's attention over the paged cache share: the chunks' shapes, the
 // division of the work over the CTAs, and the partial results where a division cuts it.
 //
-// A segment is up to QR query rows of one chunk and KV head: tpt tokens with hpt query heads of
-// the KV head each (row R: token R / hpt, head R % hpt), so that a key tile read once serves
-// them all. A segment's key tiles are those below its last token's limit. The tiles of all
+// A segment is up to QR query rows of one chunk and KV head: one block of rows (FFMA) or two of
+// 128 (tensor cores), a block `block_tokens` tokens with hpt query heads of the KV head each (row
+// r: token r / hpt, head r % hpt), so that a key tile read once serves them all. A segment's key
+// tiles are those below its last token's limit. The tiles of all
 // segments form one list (order: chunk, KV head and pass of heads, tokens, keys), cut into
 // equal ranges, one per CTA: a single long sequence fills the GPU as well as a batch of ragged
 // ones, and causal segments of all lengths even out. Where a segment lies in several CTAs'
@@ -37,7 +38,11 @@ struct ChunkArgs {
   const void *k, *v;
   const float *k_scale, *v_scale;
   int n_pages, page_size, n_seqs, max_pages;
+  int group;              // query heads of a KV head
   int hpt, tpt, passes;   // heads and tokens of a segment, passes over a KV head's query heads
+  int block_tokens;       // tokens of a block of rows
+  int hpt_inverse;        // ceil(2^16 / hpt): r / hpt for r, hpt <= 256 (their product is below 2^16)
+  int page_shift;         // log2 of the page size, -1: not a power of two
   int box;                // rows of a TMA box: divides the page size and a tile
   float* part;            // partial results, two per CTA
   ChunkJoin* join;        // what each CTA leaves to be joined
@@ -83,42 +88,57 @@ __device__ __forceinline__ int segment_tiles(int limit) {
 
 // Tiles of the first t segments of a chunk, in closed form. Segment i has ceil((b + (i + 1) tpt)
 // / 64) tiles with b = len - n, at least one, the last one ceil(len / 64).
-__device__ __forceinline__ long long tiles_before(const ChunkArgs& a, const Chunk& k, int t) {
+// Small code (a loop, not inlined): what a kernel runs once costs mostly its fetching.
+static __device__ __noinline__ long long tiles_before(int tpt, int tokens, int slots, int segments, int t) {
   long long sum = 0;
-  const int nt = chunk_segments(a, k);
-  if (t == nt && nt > 0) {
-    sum += segment_tiles(k.len);
+  if (t == segments && t > 0) {
+    sum += segment_tiles(slots);
     --t;
   }
-  const long long b = (long long)k.len - k.n;
-  const int empty = b < 0 ? (int)min((long long)t, -b / a.tpt) : 0;
+  const int b = slots - tokens;   // below 2^31 in size both
+  const int empty = b < 0 ? min(t, -b / tpt) : 0;
   sum += empty;
   const int n = t - empty;
   if (n <= 0) return sum;
   // sum over j < n of floor((tpt j + c) / 64)
-  const long long c = b + kChunkKeys - 1 + (long long)a.tpt * (empty + 1);
-  const int qa = a.tpt / kChunkKeys, ra = a.tpt % kChunkKeys;
+  const long long c = (long long)b + kChunkKeys - 1 + (long long)tpt * (empty + 1);
+  const int qa = tpt / kChunkKeys, ra = tpt % kChunkKeys;
   const long long qc = c / kChunkKeys;
   const int rc = (int)(c % kChunkKeys);
-  sum += (long long)qa * n * (n - 1) / 2 + qc * n;
+  sum += (long long)qa * ((long long)n * (n - 1) / 2) + qc * n;
   if (ra == 0) return sum;
+  if (kChunkKeys % ra == 0) {
+    // j = p u + v, p = 64 / ra: floor((ra j + rc) / 64) = u, and one more from v = z on
+    const int p = kChunkKeys / ra, z = (kChunkKeys - rc + ra - 1) / ra;
+    const long long u = n / p;
+    const int w = n % p;
+    return sum + p * (u * (u - 1) / 2) + u * w + u * max(0, p - z) + max(0, w - z);
+  }
   // j = 64 u + v: floor((ra j + rc) / 64) = ra u + floor((ra v + rc) / 64)
   const long long u = n / kChunkKeys;
   const int w = n % kChunkKeys;
   int whole = 0, part = 0;
-#pragma unroll 8
+#pragma unroll 4
   for (int v = 0; v < kChunkKeys; ++v) {
     const int f = (ra * v + rc) / kChunkKeys;
     whole += f;
-    if (v < w) part += f;
+    part += v < w ? f : 0;
   }
   return sum + ra * (kChunkKeys * (u * (u - 1) / 2) + u * w) + u * whole + part;
+}
+
+// x / y for 0 <= x, 0 < y: in 32 bits where they fit (a division in 64 is long).
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  if (x <= 0xffffffffll && y <= 0xffffffffll) return (uint32_t)x / (uint32_t)y;
+  return x / y;
 }
 
 // This CTA's range [begin, end) of the tile list and where it starts: chunk, KV head and pass,
 // segment, and `tile` tiles into it.
 struct ChunkPlan {
-  long long begin, end, total, off;
+  long long begin, end, total, off, each;   // each: tiles of a KV head and pass of the chunk
+  unsigned long long found;
+  Chunk k;
   int chunk, hp, t, tile, ctas;
 };
 
@@ -127,11 +147,14 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
   const int per = (a.n_chunks + nthreads - 1) / nthreads;
   const int c0 = min(a.n_chunks, tid * per), c1 = min(a.n_chunks, c0 + per);
-  const long long P = (long long)a.hkv * a.passes;
-  long long mine = 0;
+  const int P = a.hkv * a.passes;
+  long long mine = 0, each = 0;
+  Chunk k;
   for (int c = c0; c < c1; ++c) {
-    const Chunk k = read_chunk(a, c);
-    mine += P * tiles_before(a, k, chunk_segments(a, k));
+    k = read_chunk(a, c);
+    const int segments = chunk_segments(a, k);
+    each = tiles_before(a.tpt, k.n, k.len, segments, segments);
+    mine += P * each;
   }
   long long incl = mine;
 #pragma unroll
@@ -148,47 +171,58 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
   }
   const int ctas = (int)min((long long)gridDim.x, total);
   const int g = blockIdx.x;
-  const long long begin = g < ctas ? total * g / ctas : total;
-  const long long end = g < ctas ? total * (g + 1) / ctas : total;
+  const long long begin = g < ctas ? divide(total * g, ctas) : total;
+  const long long end = g < ctas ? divide(total * (g + 1), ctas) : total;
   if (tid == 0) {
     plan->begin = begin;
     plan->end = end;
     plan->total = total;
     plan->ctas = ctas;
-    plan->t = 0;
+    plan->found = 0;
   }
   if (begin < end && begin >= before && begin < before + mine) {
     long long at = before;
     for (int c = c0; c < c1; ++c) {
-      const Chunk k = read_chunk(a, c);
-      const long long n = P * tiles_before(a, k, chunk_segments(a, k));
-      if (begin < at + n) {
+      if (per > 1) {
+        k = read_chunk(a, c);
+        const int segments = chunk_segments(a, k);
+        each = tiles_before(a.tpt, k.n, k.len, segments, segments);
+      }
+      if (begin < at + P * each) {
         plan->chunk = c;
         plan->off = begin - at;
+        plan->each = each;
+        plan->k = k;
         break;
       }
-      at += n;
+      at += P * each;
     }
   }
   __syncthreads();
   if (begin >= end) return;
   // the segment: the last one with tiles_before <= rem, by as many guesses at once as threads
-  const Chunk k = read_chunk(a, plan->chunk);
-  const int nt = chunk_segments(a, k);
-  const long long off = plan->off, each = tiles_before(a, k, nt), rem = off % each;
-  int lo = 0, hi = nt;   // within lo .. hi - 1
+  k = plan->k;
+  const int segments = chunk_segments(a, k);
+  const long long off = plan->off;
+  each = plan->each;
+  const int hp = (int)divide(off, each);
+  const long long rem = off - hp * each;
+  int lo = 0, hi = segments;   // within lo .. hi - 1
   while (hi - lo > 1) {
     const int step = (hi - lo + nthreads - 1) / nthreads, t = lo + tid * step;
-    if (t < hi && tiles_before(a, k, t) <= rem) atomicMax(&plan->t, t);
+    if (t < hi) {
+      const long long n = tiles_before(a.tpt, k.n, k.len, segments, t);
+      if (n <= rem) atomicMax(&plan->found, (unsigned long long)t << 40 | (unsigned long long)n);
+    }
     __syncthreads();
-    lo = plan->t;
+    lo = (int)(plan->found >> 40);
     hi = min(hi, lo + step);
     __syncthreads();
   }
   if (tid == 0) {
     plan->t = lo;
-    plan->hp = (int)(off / each);
-    plan->tile = (int)(rem - tiles_before(a, k, lo));
+    plan->hp = hp;
+    plan->tile = (int)(rem - (long long)(plan->found & 0xffffffffffull));
   }
   __syncthreads();
 }
@@ -204,7 +238,7 @@ struct ChunkWalk {
   }
   __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkPlan& p) {
     chunk = p.chunk;
-    k = read_chunk(a, chunk);
+    k = p.k;
     segments = chunk_segments(a, k);
     hp = p.hp;
     t = p.t;
@@ -231,27 +265,42 @@ struct ChunkWalk {
   }
 };
 
-// Query row R of a segment: its row of q and o (-1: none), its head and its limit.
+// KV head and first query head of a KV head and pass.
+__device__ __forceinline__ int chunk_kv_head(const ChunkArgs& a, int hp) { return a.passes == 1 ? hp : hp / a.passes; }
+__device__ __forceinline__ int chunk_first_head(const ChunkArgs& a, int hp) {
+  return a.passes == 1 ? hp * a.group : hp / a.passes * a.group + hp % a.passes * a.hpt;
+}
+
+// Row r of block x of a segment: its row of q and o (-1: none), its head and its limit.
 struct ChunkRow {
   int64_t m;
   int head, limit;
 };
-__device__ __forceinline__ ChunkRow chunk_row(const ChunkArgs& a, const Chunk& k, int hp, int t, int R) {
-  ChunkRow r;
-  const int g = hp / a.passes, h = (hp % a.passes) * a.hpt + R % a.hpt, group = a.hq / a.hkv;
-  const int in = R / a.hpt;
-  const int64_t token = (int64_t)t * a.tpt + in;
-  r.m = -1;
-  r.limit = 0;
-  r.head = g * group + h;
-  if (in >= a.tpt || token >= k.n || h >= group) return r;
-  r.m = k.first + token;
-  r.limit = (int)max((int64_t)0, k.len - k.n + 1 + token);
-  return r;
+__device__ __forceinline__ ChunkRow chunk_row(const ChunkArgs& a, const Chunk& k, int hp, int t, int x, int r) {
+  ChunkRow row;
+  const int in = (r * a.hpt_inverse) >> 16, h = r - in * a.hpt;
+  const int token = t * a.tpt + x * a.block_tokens + in;
+  row.m = -1;
+  row.limit = 0;
+  row.head = chunk_first_head(a, hp) + h;
+  if (in >= a.block_tokens || token >= k.n || (a.passes > 1 && hp % a.passes * a.hpt + h >= a.group)) return row;
+  row.m = k.first + token;
+  row.limit = max(0, k.len - k.n + 1 + token);
+  return row;
+}
+
+// A slot's place in the table and in its page.
+__device__ __forceinline__ int chunk_page(const ChunkArgs& a, const Chunk& k, int slot) {
+  return a.table[(int64_t)k.seq * a.max_pages + (a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page_size)];
+}
+__device__ __forceinline__ int chunk_in_page(const ChunkArgs& a, int slot) {
+  return a.page_shift >= 0 ? slot & (a.page_size - 1) : slot % a.page_size;
 }
 
 // Where a segment's part in this CTA's range goes: slot 0 if it began before the range, 1 if it
-// begins here and goes on after it.
+// begins here and goes on after it. A part is [QR] maxima (log2 units), [QR] sums and the outputs
+// as [HD / 4][QR][4], which both the writers' and the join's threads, a row each, touch in whole
+// lines.
 template <int QR, int HD>
 __device__ __forceinline__ float* chunk_part(const ChunkArgs& a, int cta, bool began_before) {
   return a.part + ((int64_t)2 * cta + (began_before ? 0 : 1)) * QR * (HD + 2);
@@ -265,7 +314,7 @@ __device__ __forceinline__ ChunkJoin chunk_join(const ChunkPlan& p, const ChunkW
   j.hp = w.hp;
   j.t = w.t;
   j.first = blockIdx.x;
-  j.last = (int)min((long long)p.ctas - 1, ((p.end + left) * p.ctas - 1) / p.total);
+  j.last = (int)min((long long)p.ctas - 1, divide((p.end + left) * p.ctas - 1, p.total));
   return j;
 }
 

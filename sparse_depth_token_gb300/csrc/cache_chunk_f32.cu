@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
     float mx[4], sum[4], o[4][DN * DW];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      row[i] = chunk_row(a, w.k, w.hp, w.t, 4 * ty + i);
+      row[i] = chunk_row(a, w.k, w.hp, w.t, 0, 4 * ty + i);
       mx[i] = -INFINITY;
       sum[i] = 0.f;
 #pragma unroll
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
     __syncthreads();   // the segment before is done with the queries
     for (int i = tid; i < kRows * (HD / 4); i += kThreads) {
       const int R = i / (HD / 4), d = i % (HD / 4) * 4;
-      const ChunkRow r = chunk_row(a, w.k, w.hp, w.t, R);
+      const ChunkRow r = chunk_row(a, w.k, w.hp, w.t, 0, R);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r.m >= 0) {
         const float* p = (const float*)a.q + r.m * a.ldq + r.head * HD + d;
@@ -65,17 +65,17 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
     // slots of the cache into shared memory; those at and after the segment's limit as zeros
     auto fill = [&](const float* cache, int key0) {
       constexpr int CH = HD / 4;
-      const int g = w.hp / a.passes;
+      const int g = chunk_kv_head(a, w.hp);
       for (int i = tid; i < kChunkKeys * CH; i += kThreads) {
         const int key = i / CH, c = i % CH, slot = key0 + key;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (slot < w.limit) {
-          int page = a.table[(int64_t)w.k.seq * a.max_pages + slot / a.page_size];
+          int page = chunk_page(a, w.k, slot);
           if (page < 0 || page >= a.n_pages) {
             report_status(a.status, XMOD_ERR_DEVICE_CHECK);
             page = 0;
           }
-          const int64_t at = ((int64_t)page * a.hkv + g) * a.page_size + slot % a.page_size;
+          const int64_t at = ((int64_t)page * a.hkv + g) * a.page_size + chunk_in_page(a, slot);
           x = *reinterpret_cast<const float4*>(cache + at * HD + c * 4);
         }
         *reinterpret_cast<float4*>(&s.kv[key * S::QLD + c * 4]) = x;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
         for (int g = 0; g < DN; ++g)
 #pragma unroll
           for (int e = 0; e < DW; ++e)
-            part[2 * kRows + R * HD + (g * 16 + tx) * DW + e] = o[i][g * DW + e];
+            part[2 * kRows + (((g * 16 + tx) * DW / 4) * kRows + R) * 4 + (tx * DW + e) % 4] = o[i][g * DW + e];
         if (tx == 0) {
           part[R] = mx[i];
           part[kRows + R] = sum[i];

@@ -7,10 +7,10 @@
 // MMA tiles, A and B, of 128 query rows each (a row is a token and a query head of one KV head),
 // which share every 64-key tile of K and V. Roles:
 //   warp 0        TMA of K and V (pages gathered box by box) into rings of stages, K a tile ahead
-//   warp 1        owner of the tensor memory; one lane issues S = Q K^T (two buffers for each of
-//                 A and B) and O += P V, each as soon as its inputs are there
-//   warp 2        the segments' descriptions and query rows, the next segment's as soon as the
-//                 last S of this one has been computed
+//   warps 1, 3    they issue A's and B's S = Q K^T (two buffers each, a tile ahead)
+//                 and O += P V; warp 1 owns the tensor memory
+//   warp 2        the segments' descriptions, and TMA of their query rows, the next segment's as
+//                 soon as the last S of this one has been computed
 //   warps 4..7    softmax of A, a row a thread: scores from tensor memory, running maximum and
 //   warps 8..11   sum, P back over the scores as bf16; the same for B
 //   warps 12..15  (e4m3) codes to bf16, exactly
@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "cache_chunk.cuh"
 #include "tc_common.cuh"
@@ -53,7 +54,9 @@ template <int HD, bool FP8> struct Tc {
   static constexpr int CODES = FP8 ? KB * HD : 0;           // of K, and of V
   static constexpr int NC = FP8 ? 3 : 0;
   static constexpr int SCALES = FP8 ? 2 * KB * 4 : 0;
-  static constexpr int DATA = 2 * Q_TILE + 2 * NK * K_TILE + NC * (2 * CODES + SCALES) + NK * SCALES;
+  // where a warp turns its rows of the output: 32 rows of OUT columns, padded
+  static constexpr int OUT = FP8 && HD == 128 ? 16 : 32, OUT_LD = OUT * 2 + 16, TURN = 8 * 32 * OUT_LD;
+  static constexpr int DATA = 2 * Q_TILE + 2 * NK * K_TILE + NC * (2 * CODES + SCALES) + NK * SCALES + TURN;
   static constexpr int MISC = 2048;
   static constexpr int SMEM = DATA + MISC + 1024;
   static constexpr int THREADS = FP8 ? 512 : 384;
@@ -72,7 +75,7 @@ constexpr int kSegments = 4;
 enum { kSegFirst = 1, kSegLast = 2, kSegBoth = 4 };   // what the MMA warp is told about a tile
 
 __device__ __forceinline__ bool segment_both(const ChunkArgs& a, const Chunk& k, int t) {
-  return (int64_t)min(a.tpt, k.n - t * a.tpt) * a.hpt > 128;
+  return k.n - t * a.tpt > a.block_tokens;
 }
 
 // K-major operand: rows of RB bytes, groups of 8 rows RB * 8 bytes apart.
@@ -92,6 +95,33 @@ template <int RB> __device__ __forceinline__ uint32_t swizzled(int r, int c, int
   constexpr int CH = RB / 16;
   const int x = RB == 128 ? (r & 7) : RB == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
   return (uint32_t)((c / CH) * rows * RB + r * RB + (((c % CH) ^ x) << 4));
+}
+
+// The tensor-core instructions of a whole warp, issued by one elected lane.
+__device__ __forceinline__ void mma_elected(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_tmem_a_elected(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {   // accumulates
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
@@ -130,8 +160,8 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& h
 
 template <int HD, bool FP8>
 __global__ void __launch_bounds__((Tc<HD, FP8>::THREADS), 1)
-cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                      const ChunkArgs a) {
+cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                      const __grid_constant__ CUtensorMap mV, const ChunkArgs a) {
   using C = Tc<HD, FP8>;
   constexpr int NK = C::NK, RB = C::RB;
   extern __shared__ uint8_t smem_raw[];
@@ -142,6 +172,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
   const uint32_t sCode = sV + NK * C::K_TILE;                       // stages: K codes, V codes
   const uint32_t sCodeScale = sCode + C::NC * 2 * C::CODES;         // stages: K scales, V scales
   const uint32_t sScale = sCodeScale + C::NC * C::SCALES;           // the same beside the V stages
+  const uint32_t sTurn = sScale + NK * C::SCALES;                   // a part for each softmax warp
   uint8_t* const misc = gbase + C::DATA;
   const uint32_t sMisc = base + C::DATA;
   // misc: barriers, then what the roles tell one another
@@ -152,38 +183,38 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     return b;
   };
   const uint32_t K_FULL = take(NK), K_EMPTY = take(NK), V_FULL = take(NK), V_EMPTY = take(NK);
-  const uint32_t S_FULL = take(4), S_EMPTY = take(4), P_FULL = take(4), P_EMPTY = take(4);   // [A, B][2]
+  const uint32_t S_FULL = take(4), P_FULL = take(4), P_EMPTY = take(4);   // [A, B][2]
   const uint32_t Q_FULL = take(1), Q_EMPTY = take(1), SEG_FULL = take(kSegments), SEG_EMPTY = take(kSegments);
   const uint32_t LOOK = take(2), C_FULL = take(C::NC), C_EMPTY = take(C::NC);
-  constexpr int kBarBytes = 8 * (4 * NK + 16 + 2 + 2 * kSegments + 2 + 2 * C::NC);
+  constexpr int kBarBytes = 8 * (4 * NK + 12 + 2 + 2 * kSegments + 2 + 2 * C::NC);
   static_assert(kBarBytes <= 640, "");
   ChunkPlan* const plan = reinterpret_cast<ChunkPlan*>(misc + 640);
-  long long* const scratch = reinterpret_cast<long long*>(misc + 640 + 64);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc + 832);
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 840);
-  unsigned long long* const bad_keys = reinterpret_cast<unsigned long long*>(misc + 848);   // [2][3]
-  volatile int* const tile_info = reinterpret_cast<volatile int*>(misc + 896);              // [NK]
-  volatile int* const code_info = reinterpret_cast<volatile int*>(misc + 928);              // [NC]
-  Segment* const segs = reinterpret_cast<Segment*>(misc + 944);
-  static_assert(sizeof(ChunkPlan) <= 64 && 944 + kSegments * sizeof(Segment) <= C::MISC && NK <= 8, "");
+  long long* const scratch = reinterpret_cast<long long*>(misc + 768);                      // [16]
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc + 896);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 904);
+  unsigned long long* const bad_keys = reinterpret_cast<unsigned long long*>(misc + 912);   // [2][3]
+  volatile int* const tile_info = reinterpret_cast<volatile int*>(misc + 960);              // [NK]
+  volatile int* const code_info = reinterpret_cast<volatile int*>(misc + 992);              // [NC]
+  Segment* const segs = reinterpret_cast<Segment*>(misc + 1008);
+  static_assert(sizeof(ChunkPlan) <= 128 && 1008 + kSegments * sizeof(Segment) <= C::MISC && NK <= 8, "");
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(K_FULL + 8 * i, FP8 ? 128 : 1);
-      mbar_init(K_EMPTY + 8 * i, 1);
+      mbar_init(K_EMPTY + 8 * i, 2);   // A's and B's MMAs
       mbar_init(V_FULL + 8 * i, FP8 ? 128 : 1);
-      mbar_init(V_EMPTY + 8 * i, 1);
+      mbar_init(V_EMPTY + 8 * i, 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(S_FULL + 8 * i, 1);
-      mbar_init(S_EMPTY + 8 * i, 128);
       mbar_init(P_FULL + 8 * i, 128);
       mbar_init(P_EMPTY + 8 * i, 1);
     }
-    mbar_init(Q_FULL, 32);
-    mbar_init(Q_EMPTY, 1);
+    mbar_init(Q_FULL, 1);
+    mbar_init(Q_EMPTY, 2);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(SEG_FULL + 8 * i, 1);
       mbar_init(SEG_EMPTY + 8 * i, 8);
@@ -197,6 +228,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     *abort_flag = 0;
     for (int i = 0; i < 6; ++i) bad_keys[i] = 0;
     fence_barrier_init();
+    prefetch_tensormap(&mQ);
     prefetch_tensormap(&mK);
     prefetch_tensormap(&mV);
   }
@@ -210,6 +242,87 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
   const int ntiles = (int)(plan->end - plan->begin);
   if (tid == 0) a.join[blockIdx.x].chunk = -1;
 
+  // ------------------------------------------------------------ MMA of A (X = 0), of B
+  // The whole warp runs this, with one lane elected at each instruction: control and operands
+  // stay uniform, which keeps the descriptors in uniform registers (a lane by itself moves every
+  // operand there first, on a scheduler that it shares with two softmax warps).
+  auto issue_mma = [&](auto half) {
+    constexpr int X = decltype(half)::value;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, KB);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | kIdescBMajorMN;
+    constexpr int PER = RB / 32;   // 16-deep steps of a half
+    const uint32_t bSF = S_FULL + 16 * X, bPF = P_FULL + 16 * X, bPE = P_EMPTY + 16 * X;
+    const uint32_t tS = tmem + 2 * X * KB, tO = tmem + 4 * KB + X * HD;
+    const uint64_t dQ = desc_k<RB, C::SW>(sQ + X * C::Q_TILE);
+    const uint64_t dK0 = desc_k<RB, C::SW>(sK), dV0 = desc_mn<RB, C::SW>(sV, C::K_HALF);
+    const int n = __shfl_sync(0xffffffffu, ntiles, 0);
+    int is = 0, ip = 0;                 // next tile of the range for S, for P V
+    int is_st = 0, ip_st = 0;           // their stages,
+    uint32_t is_ph = 0, ip_ph = 0;      // and the phases of those
+    int cs = 0, cp = 0, segments = 0;   // tiles of this half whose S, P V has been issued; segments begun
+    uint32_t mine_bits = 0;             // which of the last 32 tiles are this half's
+    while (ip < n) {
+      // S runs up to two tiles ahead of P V (its buffer held the P before, which that P V has
+      // taken: the MMAs of a thread run in order); but a segment's first S, which waits for its
+      // queries, comes after the last P V of the one before.
+      bool ok = true;
+      while (is < n && is < ip + 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait(K_FULL + 8 * is_st, is_ph, abort_flag, a.status));
+        if (!ok) break;
+        const int info = __shfl_sync(0xffffffffu, tile_info[is_st], 0);
+        if (info & kSegFirst) {
+          if (is > ip) break;
+          ok = __all_sync(0xffffffffu, mbar_wait(Q_FULL, (uint32_t)segments & 1u, abort_flag, a.status));
+          if (!ok) break;
+          ++segments;
+        }
+        // a tile without rows of this half: its stages are freed, but not before they are full,
+        // for a phase has one arrival of each half
+        const uint32_t bit = 1u << (is & 31);
+        if (X == 0 || (info & kSegBoth)) {
+          const int b = cs & 1;
+          tc_fence_after();
+          const uint64_t dK = dK0 + (uint32_t)(is_st * (C::K_TILE >> 4));
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_elected(tS + b * KB, dQ + (kk / PER) * (C::Q_HALF >> 4) + 2 * (kk % PER),
+                        dK + (kk / PER) * (C::K_HALF >> 4) + 2 * (kk % PER), idesc_s, kk != 0);
+          commit_elected(bSF + 8 * b);
+          ++cs;
+          mine_bits |= bit;
+        } else {
+          mine_bits &= ~bit;
+        }
+        commit_elected(K_EMPTY + 8 * is_st);
+        if (info & kSegLast) commit_elected(Q_EMPTY);
+        ++is;
+        if (++is_st == NK) {
+          is_st = 0;
+          is_ph ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(V_FULL + 8 * ip_st, ip_ph, abort_flag, a.status))) break;
+      if (mine_bits >> (ip & 31) & 1) {
+        const int b = cp & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(bPF + 8 * b, (uint32_t)(cp >> 1) & 1u, abort_flag, a.status))) break;
+        tc_fence_after();
+        const uint64_t dV = dV0 + (uint32_t)(ip_st * (C::K_TILE >> 4));
+#pragma unroll
+        for (int kk = 0; kk < KB / 16; ++kk)   // 16 keys: 8 columns of P, 2 groups of 8 rows of V
+          mma_tmem_a_elected(tO, tS + b * KB + 8 * kk, dV + kk * RB, idesc_o);
+        commit_elected(bPE + 8 * b);
+        ++cp;
+      }
+      commit_elected(V_EMPTY + 8 * ip_st);
+      ++ip;
+      if (++ip_st == NK) {
+        ip_st = 0;
+        ip_ph ^= 1;
+      }
+    }
+  };
+
   if (ntiles <= 0) {
     // nothing to do
   } else if (warp == 0) {
@@ -221,7 +334,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     int page = 0, y_prev = 0, boxes_prev = 0;
     auto page_of = [&](int tile) {   // lane b: the page of box b
       const int key = tile * KB + lane * a.box;
-      return lane < nbox && key < w.limit ? a.table[(int64_t)w.k.seq * a.max_pages + key / a.page_size] : 0;
+      return lane < nbox && key < w.limit ? chunk_page(a, w.k, key) : 0;
     };
     auto load_v = [&](int i, int y, int boxes) {   // V of the i-th tile of the range
       const int st = i % NK;
@@ -239,7 +352,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     bool ok = true;
     while (left > 0 && ok) {
       const int first = w.tile, last = min(w.tiles, first + left);
-      const int both = segment_both(a, w.k, w.t) ? kSegBoth : 0, g = w.hp / a.passes;
+      const int both = segment_both(a, w.k, w.t) ? kSegBoth : 0, g = chunk_kv_head(a, w.hp);
       left -= last - first;
       page = page_of(first);
       for (int tile = first; tile < last && ok; ++tile, ++it) {
@@ -252,7 +365,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
           pg = 0;
         }
         const int key = tile * KB + lane * a.box;
-        const int y = (int)(((int64_t)pg * a.hkv + g) * a.page_size + key % a.page_size);
+        const int y = (int)(((int64_t)pg * a.hkv + g) * a.page_size + chunk_in_page(a, key));
         if constexpr (!FP8) {
           const int st = it % NK;
           const uint32_t full = K_FULL + 8 * st;
@@ -298,119 +411,9 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     }
     if (!FP8 && ok) load_v(it - 1, y_prev, boxes_prev);
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, KB);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | kIdescBMajorMN;
-      // next tile of the range for S and for P V of A and B; how many of them were theirs; the
-      // tiles' has-B flags by their last bits
-      int is[2] = {0, 0}, ip[2] = {0, 0}, cs[2] = {0, 0}, cp[2] = {0, 0}, segments = 0;
-      uint32_t both_bits = 0;
-      uint64_t t0 = global_timer_ns();
-      uint32_t spins = 0;
-      auto s_done = [&](int i, int info) {   // S of tile i issued for A and B
-        mma_commit(K_EMPTY + 8 * (i % NK));
-        if (info & kSegLast) mma_commit(Q_EMPTY);
-      };
-      while (ip[0] < ntiles || ip[1] < ntiles) {
-        bool progressed = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          // ---- S
-          const int i = is[x];
-          // B does not run ahead of A, which looks after the segment's beginning
-          if (i < ntiles && (x == 0 || i < is[0])) {
-            if (x == 0) {
-              if (cs[0] <= cp[0] + 1 && i <= is[1] + NK - 1 &&
-                  mbar_test_wait(K_FULL + 8 * (i % NK), (uint32_t)(i / NK) & 1u)) {
-                const int info = tile_info[i % NK];
-                const int b = cs[0] & 1;
-                if ((!(info & kSegFirst) || mbar_test_wait(Q_FULL, (uint32_t)segments & 1u)) &&
-                    mbar_test_wait(S_EMPTY + 8 * b, ((uint32_t)(cs[0] >> 1) & 1u) ^ 1u)) {
-                  if (info & kSegFirst) ++segments;
-                  tc_fence_after();
-                  const uint32_t k = sK + (i % NK) * C::K_TILE;
-#pragma unroll
-                  for (int kk = 0; kk < HD / 16; ++kk) {
-                    constexpr int PER = RB / 32;   // 16-deep steps of a half
-                    mma_bf16(tmem + b * KB, desc_k<RB, C::SW>(sQ + (kk / PER) * C::Q_HALF) + 2ull * (kk % PER),
-                             desc_k<RB, C::SW>(k + (kk / PER) * C::K_HALF) + 2ull * (kk % PER), idesc_s, kk != 0);
-                  }
-                  mma_commit(S_FULL + 8 * b);
-                  ++cs[0];
-                  ++is[0];
-                  const uint32_t bit = 1u << (i & 31);
-                  both_bits = info & kSegBoth ? both_bits | bit : both_bits & ~bit;
-                  progressed = true;
-                }
-              }
-            } else {
-              const int info = tile_info[i % NK];
-              if (!(info & kSegBoth)) {
-                s_done(i, info);
-                ++is[1];
-                progressed = true;
-              } else if (cs[1] <= cp[1] + 1) {
-                const int b = cs[1] & 1;
-                if (mbar_test_wait(S_EMPTY + 16 + 8 * b, ((uint32_t)(cs[1] >> 1) & 1u) ^ 1u)) {
-                  tc_fence_after();
-                  const uint32_t k = sK + (i % NK) * C::K_TILE;
-#pragma unroll
-                  for (int kk = 0; kk < HD / 16; ++kk) {
-                    constexpr int PER = RB / 32;
-                    mma_bf16(tmem + (2 + b) * KB,
-                             desc_k<RB, C::SW>(sQ + C::Q_TILE + (kk / PER) * C::Q_HALF) + 2ull * (kk % PER),
-                             desc_k<RB, C::SW>(k + (kk / PER) * C::K_HALF) + 2ull * (kk % PER), idesc_s, kk != 0);
-                  }
-                  mma_commit(S_FULL + 16 + 8 * b);
-                  s_done(i, info);
-                  ++cs[1];
-                  ++is[1];
-                  progressed = true;
-                }
-              }
-            }
-          }
-          // ---- O += P V; B's after A's, which frees the stage
-          const int j = ip[x];
-          if (j < is[x] && (x == 0 || j < ip[0])) {
-            const bool mine = x == 0 || (both_bits >> (j & 31) & 1);
-            const int b = cp[x] & 1, vs = j % NK;
-            if (!mine) {
-              mma_commit(V_EMPTY + 8 * vs);
-              ++ip[x];
-              progressed = true;
-            } else if (mbar_test_wait(P_FULL + 16 * x + 8 * b, (uint32_t)(cp[x] >> 1) & 1u) &&
-                       mbar_test_wait(V_FULL + 8 * vs, (uint32_t)(j / NK) & 1u)) {
-              tc_fence_after();
-              const uint32_t tp = tmem + (2 * x + b) * KB, to = tmem + 4 * KB + x * HD;
-              const uint32_t v = sV + vs * C::K_TILE;
-#pragma unroll
-              for (int kk = 0; kk < KB / 16; ++kk)   // 16 keys: 8 columns of P, 2 groups of 8 rows of V
-                mma_bf16_tmem_a(to, tp + 8 * kk, desc_mn<RB, C::SW>(v + kk * 16 * RB, C::K_HALF), idesc_o, 1u);
-              mma_commit(P_EMPTY + 16 * x + 8 * b);
-              if (x == 1) mma_commit(V_EMPTY + 8 * vs);
-              ++cp[x];
-              ++ip[x];
-              progressed = true;
-            }
-          }
-        }
-        if (progressed) {
-          t0 = global_timer_ns();
-          spins = 0;
-          continue;
-        }
-        if ((++spins & 255u) == 0u) {
-          if (*abort_flag) break;
-          if (global_timer_ns() - t0 > kWaitLimitNs) {
-            report_status(a.status, XMOD_ERR_TIMEOUT);
-            *abort_flag = 1;
-            break;
-          }
-        }
-      }
-    }
+    issue_mma(std::integral_constant<int, 0>{});
+  } else if (warp == 3) {
+    issue_mma(std::integral_constant<int, 1>{});
   } else if (warp == 2) {
     // ------------------------------------------------------------ segments and their queries
     ChunkWalk w;
@@ -442,27 +445,17 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
       ok = s == 0 || mbar_wait(Q_EMPTY, (s - 1) & 1, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      constexpr int CH = HD / 8;   // 16-byte chunks of a row
-      for (int R0 = 0; R0 < (both ? QR : 128); R0 += 32) {
-        const ChunkRow mine = chunk_row(a, w.k, w.hp, w.t, R0 + lane);
-        const int64_t at = mine.m < 0 ? -1 : mine.m * a.ldq + (int64_t)mine.head * HD;
+      if (lane == 0) {
+        // rows past the chunk's end come too (zeros past q's); they are worked on but not stored
+        const int blocks = both ? 2 : 1, head = chunk_first_head(a, w.hp);
+        mbar_arrive_expect_tx(Q_FULL, (uint32_t)(blocks * C::HALVES * RB * a.hpt * a.block_tokens));
+        for (int x = 0; x < blocks; ++x)
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-          const int64_t from = __shfl_sync(0xffffffffu, at, r);
-          const int R = R0 + r;
-          const uint32_t dst = sQ + (R >> 7) * C::Q_TILE + swizzled<RB>(R & 127, c, 128);
-          if (from >= 0)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                         "l"((const __nv_bfloat16*)a.q + from + c * 8)
-                         : "memory");
-          else
-            sts128(dst, make_uint4(0u, 0u, 0u, 0u));
-        }
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(sQ + x * C::Q_TILE + h * C::Q_HALF, &mQ, Q_FULL, h * 64, head,
+                        w.k.first + w.t * a.tpt + x * a.block_tokens);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(Q_FULL);
+      __syncwarp();
       left -= last - first;
       if (left > 0) w.next_segment(a);
     }
@@ -471,7 +464,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     const int x = (warp - 4) >> 2, quad = warp & 3, row128 = quad * 32 + lane, R = x * 128 + row128;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tS = tmem + lane_off + 2 * x * KB, tO = tmem + lane_off + 4 * KB + x * HD;
-    const uint32_t bSF = S_FULL + 16 * x, bSE = S_EMPTY + 16 * x, bPF = P_FULL + 16 * x, bPE = P_EMPTY + 16 * x;
+    const uint32_t bSF = S_FULL + 16 * x, bPF = P_FULL + 16 * x, bPE = P_EMPTY + 16 * x;
     const float scale_log2 = 1.4426950408889634f * rsqrtf((float)HD);
     int n = 0, i0 = 0;            // tiles this group has worked on; tiles before the segment
     int looks[2] = {0, 0};        // looks at V, by A's warps alone and by all
@@ -498,7 +491,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
         i0 += count;
         continue;
       }
-      ChunkRow row = chunk_row(a, g.k, g.hp, g.t, R);
+      const ChunkRow row = chunk_row(a, g.k, g.hp, g.t, x, row128);
       const int limit = row.m < 0 ? g.limit : row.limit;
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -519,8 +512,6 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
         float v[KB];
         tmem_ld64(tS + b * KB, v);
         tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive(bSE + 8 * b);
         const float* sc = reinterpret_cast<const float*>(gbase + (sScale - base) + vs * C::SCALES);
         if constexpr (FP8) {
           // the scales lie there since K's codes were converted
@@ -616,11 +607,13 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
           const int from = max(0, least - key0), valid = max(0, min(KB, g.limit - key0));
           const int width = g.both ? 256 : 128;
           unsigned long long bad = 0;
+          bool wrote = false;
           for (int i = from * CH + R; i < KB * CH; i += width) {
             const int key = i / CH;
             const uint32_t at = vt + swizzled<RB>(key, i % CH, KB);
             if (key >= valid) {
               sts128(at, make_uint4(0u, 0u, 0u, 0u));
+              wrote = true;
             } else {
               const uint4 u = lds128(at);
               if (nonfinite2(u.x) | nonfinite2(u.y) | nonfinite2(u.z) | nonfinite2(u.w)) bad |= 1ull << key;
@@ -632,7 +625,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
           unsigned long long* const slots = bad_keys + 3 * g.both;
           const int slot = look % 3;
           if (bad) atomicOr(&slots[slot], bad);
-          fence_proxy_async_smem();
+          if (wrote) fence_proxy_async_smem();
           if (!meet(g.both)) {
             ok = false;
             break;
@@ -714,26 +707,51 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
       tc_fence_after();
       const bool whole = g.first == 0 && g.last == g.tiles;
       const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-      const int64_t head = row.m * a.hq + row.head;
+      const int64_t head = row.m < 0 ? -1 : row.m * a.hq + row.head;
       float* part = chunk_part<QR, HD>(a, blockIdx.x, g.first > 0);
-#pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
-        float ov[32];
-        tmem_ld32(tO + c * 32, ov);
-        tmem_ld_wait();
-        if (row.m >= 0) {
-          if (whole) {
-            __nv_bfloat16* dst = (__nv_bfloat16*)a.o + head * HD + c * 32;
+      if (whole) {
+        // through shared memory, so that lanes side by side write one row's columns: PER lanes a row
+        constexpr int PER = C::OUT / 8, STEPS = PER;   // 16 bytes a lane, 32 / PER rows a step
+        const uint32_t turn_base = sTurn + (warp - 4) * 32 * C::OUT_LD;
+        int64_t to[STEPS];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(dst + i) =
-                  make_uint4(pack_bf16x2(ov[i] * inv, ov[i + 1] * inv), pack_bf16x2(ov[i + 2] * inv, ov[i + 3] * inv),
-                             pack_bf16x2(ov[i + 4] * inv, ov[i + 5] * inv), pack_bf16x2(ov[i + 6] * inv, ov[i + 7] * inv));
-          } else {
-            float* dst = part + 2 * QR + R * HD + c * 32;
+        for (int i = 0; i < STEPS; ++i) to[i] = __shfl_sync(0xffffffffu, head, i * (32 / PER) + lane / PER);
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          float ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tmem_ld_wait();
+#pragma unroll
+          for (int part32 = 0; part32 < 32 / C::OUT; ++part32) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < C::OUT; i += 8) {
+              const float* f = ov + part32 * C::OUT + i;
+              sts128(turn_base + lane * C::OUT_LD + i * 2,
+                     make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv)));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+              const uint4 u = lds128(turn_base + (i * (32 / PER) + lane / PER) * C::OUT_LD + lane % PER * 16);
+              if (to[i] >= 0)
+                *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + to[i] * HD + c * 32 + part32 * C::OUT +
+                                          lane % PER * 8) = u;
+            }
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          float ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tmem_ld_wait();
+          if (row.m >= 0) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(dst + i) = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+              *reinterpret_cast<float4*>(part + 2 * QR + ((c * 8 + i / 4) * QR + R) * 4) =
+                  make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
           }
         }
       }
@@ -812,16 +830,17 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
 
 template <int HD, bool FP8> int launch_tc(const Ctx& c, const ChunkArgs& a, int ctas) {
   using C = Tc<HD, FP8>;
-  CUtensorMap mk, mv;
+  CUtensorMap mq, mk, mv;
   const int64_t rows = (int64_t)a.n_pages * a.hkv * a.page_size;
   const int cols = FP8 ? C::CRB : C::RB / 2;
-  if (!tma_map_rows(&mk, a.k, FP8 ? 1 : 2, rows, HD, cols, a.box) ||
+  if (!tma_map_heads(&mq, a.q, a.M, a.ldq, a.hq, HD, C::RB / 2, a.hpt, a.block_tokens) ||
+      !tma_map_rows(&mk, a.k, FP8 ? 1 : 2, rows, HD, cols, a.box) ||
       !tma_map_rows(&mv, a.v, FP8 ? 1 : 2, rows, HD, cols, a.box))
     return XMOD_ERR_CUDA;
   static std::atomic<uint64_t> done{0};
   auto k = cache_chunk_tc_kernel<HD, FP8>;
   if (allow_smem(k, C::SMEM, done) != cudaSuccess) return XMOD_ERR_CUDA;
-  XMOD_LAUNCH(c, "cache_chunk", launch_pdl(k, dim3(ctas), dim3(C::THREADS), C::SMEM, c.stream, mk, mv, a));
+  XMOD_LAUNCH(c, "cache_chunk", launch_pdl(k, dim3(ctas), dim3(C::THREADS), C::SMEM, c.stream, mq, mk, mv, a));
   return XMOD_OK;
 }
 

@@ -60,6 +60,10 @@ bool tma_map_bf16(CUtensorMap* m, const void* base, int rank, const int64_t* dim
 // rows of 32, 64 or 128 bytes, swizzled over their own width.
 bool tma_map_rows(CUtensorMap* m, const void* base, int esize, int64_t rows, int cols, int box_cols,
                   int box_rows);
+// Tensor map of bf16 [rows, heads, head_dim], rows `ld` elements apart; boxes of box_cols
+// dimensions (64 or 128 bytes, swizzled over their own width), box_heads heads, box_rows rows.
+bool tma_map_heads(CUtensorMap* m, const void* base, int64_t rows, int64_t ld, int heads, int hd,
+                   int box_cols, int box_heads, int box_rows);
 
 // ---------------------------------------------------------------- measurement
 

@@ -77,4 +77,18 @@ bool tma_map_rows(CUtensorMap* m, const void* base, int esize, int64_t rows, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_map_heads(CUtensorMap* m, const void* base, int64_t rows, int64_t ld, int heads, int hd,
+                   int box_cols, int box_heads, int box_rows) {
+  if (!tma_available() || (box_cols != 32 && box_cols != 64)) return false;
+  const cuuint64_t d[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t st[2] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t bx[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), d, st, bx, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace xmod
