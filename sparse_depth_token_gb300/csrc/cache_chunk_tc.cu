@@ -29,7 +29,6 @@
 #include <math.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "cache_chunk.cuh"
 #include "tc_common.cuh"
@@ -141,20 +140,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Nonzero if one of the two bf16 of w is an infinity or NaN.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-// Four e4m3 codes to bf16, exactly: exponent and mantissa moved to their places make the value
-// times 2^-120 (subnormals too); a code of NaN is put in by hand.
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // codes in the high bytes
-  uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-  uint32_t y = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
-  const uint32_t up = 0x7b807b80u;   // 2^120
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(up));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(up));
-  if ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-    if ((w & 0x7fu) == 0x7fu) lo |= 0x00007fffu;
-    if ((w & 0x7f00u) == 0x7f00u) lo |= 0x7fff0000u;
-    if ((w & 0x7f0000u) == 0x7f0000u) hi |= 0x00007fffu;
-    if ((w & 0x7f000000u) == 0x7f000000u) hi |= 0x7fff0000u;
+// Sixteen e4m3 codes to bf16, exactly: exponent and mantissa moved to their places make the value
+// times 2^-120 (subnormals too); codes of NaN are put in by hand.
+__device__ __forceinline__ uint32_t codes2_bf16(uint32_t w, uint32_t select) {
+  const uint32_t a = __byte_perm(w, 0, select);   // two codes in the high bytes
+  const uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));   // 2^120
+  return r;
+}
+__device__ __noinline__ uint32_t codes2_nan(uint32_t w, uint32_t at, uint32_t r) {
+  if ((w >> at & 0x7fu) == 0x7fu) r |= 0x00007fffu;
+  if ((w >> at & 0x7f00u) == 0x7f00u) r |= 0x7fff0000u;
+  return r;
+}
+__device__ __forceinline__ void codes_bf16(const uint4& u, uint4& lo, uint4& hi) {
+  lo = make_uint4(codes2_bf16(u.x, 0x1404), codes2_bf16(u.x, 0x3424), codes2_bf16(u.y, 0x1404), codes2_bf16(u.y, 0x3424));
+  hi = make_uint4(codes2_bf16(u.z, 0x1404), codes2_bf16(u.z, 0x3424), codes2_bf16(u.w, 0x1404), codes2_bf16(u.w, 0x3424));
+  auto top = [](uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; };
+  if ((top(u.x) | top(u.y) | top(u.z) | top(u.w)) & 0x80808080u) {
+    lo = make_uint4(codes2_nan(u.x, 0, lo.x), codes2_nan(u.x, 16, lo.y), codes2_nan(u.y, 0, lo.z), codes2_nan(u.y, 16, lo.w));
+    hi = make_uint4(codes2_nan(u.z, 0, hi.x), codes2_nan(u.z, 16, hi.y), codes2_nan(u.w, 0, hi.z), codes2_nan(u.w, 16, hi.w));
   }
 }
 
@@ -246,8 +252,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
   // The whole warp runs this, with one lane elected at each instruction: control and operands
   // stay uniform, which keeps the descriptors in uniform registers (a lane by itself moves every
   // operand there first, on a scheduler that it shares with two softmax warps).
-  auto issue_mma = [&](auto half) {
-    constexpr int X = decltype(half)::value;
+  auto issue_mma = [&](const int X) {
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, KB);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | kIdescBMajorMN;
     constexpr int PER = RB / 32;   // 16-deep steps of a half
@@ -410,10 +415,8 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       if (left > 0) w.next_segment(a);
     }
     if (!FP8 && ok) load_v(it - 1, y_prev, boxes_prev);
-  } else if (warp == 1) {
-    issue_mma(std::integral_constant<int, 0>{});
-  } else if (warp == 3) {
-    issue_mma(std::integral_constant<int, 1>{});
+  } else if (warp == 1 || warp == 3) {
+    issue_mma(warp == 3 ? 1 : 0);
   } else if (warp == 2) {
     // ------------------------------------------------------------ segments and their queries
     ChunkWalk w;
@@ -522,10 +525,12 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 #pragma unroll
           for (int i = 0; i < KB; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(sc + i);
-            v[i] *= f.x;
-            v[i + 1] *= f.y;
-            v[i + 2] *= f.z;
-            v[i + 3] *= f.w;
+            const float2 s0 = mul2(make_float2(v[i], v[i + 1]), make_float2(f.x, f.y));
+            const float2 s1 = mul2(make_float2(v[i + 2], v[i + 3]), make_float2(f.z, f.w));
+            v[i] = s0.x;
+            v[i + 1] = s0.y;
+            v[i + 2] = s1.x;
+            v[i + 3] = s1.y;
           }
         }
         const bool masked = key0 + KB > least;   // some row of the segment does not see all of it
@@ -585,10 +590,12 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 #pragma unroll
           for (int i = 0; i < KB; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(sc + KB + i);
-            v[i] *= f.x;
-            v[i + 1] *= f.y;
-            v[i + 2] *= f.z;
-            v[i + 3] *= f.w;
+            const float2 s0 = mul2(make_float2(v[i], v[i + 1]), make_float2(f.x, f.y));
+            const float2 s1 = mul2(make_float2(v[i + 2], v[i + 3]), make_float2(f.z, f.w));
+            v[i] = s0.x;
+            v[i + 1] = s0.y;
+            v[i + 2] = s1.x;
+            v[i + 3] = s1.y;
           }
           if (masked) {   // a scale that is not seen may be anything
 #pragma unroll
@@ -791,20 +798,22 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         float* to = reinterpret_cast<float*>(gbase + (sScale - base) + st * C::SCALES);
         to[t] = from[t];   // 128: K's and V's
       }
-#pragma unroll
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t src = sCode + cs * 2 * C::CODES + kv * C::CODES;
         const uint32_t dst = (kv ? sV : sK) + st * C::K_TILE;
-        // eight lanes take the same chunk of eight rows: their swizzled places differ
-#pragma unroll
-        for (int i = t; i < KB * CH; i += 128) {
-          const int r = (i & 7) + 8 * (i / (8 * CH)), c = (i >> 3) % CH;
-          const uint4 u = lds128(src + swizzled<C::CRB>(r, c, KB));
+        // eight lanes take the same chunk of eight rows: their swizzled places differ. Loops are
+        // kept small: unrolled, the roles' code together no longer fits the instruction cache
+        // (16 ragged chunks at 16384: ITIME us).
+        constexpr int N = KB * CH / 128;
+        auto row_of = [&](int i) { return (i & 7) + 8 * (i / (8 * CH)); };
+        uint4 u = lds128(src + swizzled<C::CRB>(row_of(t), (t >> 3) % CH, KB));
+#pragma unroll 1
+        for (int j = 0; j < N; ++j) {
+          const int i = t + 128 * j, r = row_of(i), c = (i >> 3) % CH;
           uint4 lo, hi;
-          codes_bf16(u.x, lo.x, lo.y);
-          codes_bf16(u.y, lo.z, lo.w);
-          codes_bf16(u.z, hi.x, hi.y);
-          codes_bf16(u.w, hi.z, hi.w);
+          codes_bf16(u, lo, hi);
+          if (j + 1 < N) u = lds128(src + swizzled<C::CRB>(row_of(i + 128), ((i + 128) >> 3) % CH, KB));
           sts128(dst + swizzled<RB>(r, 2 * c, KB), lo);
           sts128(dst + swizzled<RB>(r, 2 * c + 1, KB), hi);
         }
