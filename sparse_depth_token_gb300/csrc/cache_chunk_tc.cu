@@ -43,6 +43,17 @@ constexpr int KB = kChunkKeys;
 constexpr int QR = kChunkTcRows;
 constexpr float kRescale = 8.0f;   // log2 units
 
+// The bounded wait with everything but its first test out of line: it stands in every loop here,
+// whose code has to stay small.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return mbar_wait(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = wait_longer(bar, parity, abort_flag, status);
+  return __all_sync(0xffffffffu, ok);   // the whole warp calls it
+}
+
 template <int HD, bool FP8> struct Tc {
   static constexpr int RB = HD >= 64 ? 128 : 64;            // bytes of a swizzled row
   static constexpr int HALVES = HD * 2 / RB;                // of a head's dimensions
@@ -71,7 +82,6 @@ struct Segment {
   int both;                                      // B has rows
 };
 constexpr int kSegments = 4;
-enum { kSegFirst = 1, kSegLast = 2, kSegBoth = 4 };   // what the MMA warp is told about a tile
 
 __device__ __forceinline__ bool segment_both(const ChunkArgs& a, const Chunk& k, int t) {
   return k.n - t * a.tpt > a.block_tokens;
@@ -188,30 +198,27 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     bar += 8 * n;
     return b;
   };
-  const uint32_t K_FULL = take(NK), K_EMPTY = take(NK), V_FULL = take(NK), V_EMPTY = take(NK);
+  const uint32_t FULL = take(NK), K_EMPTY = take(NK), V_EMPTY = take(NK);   // of K and V together
   const uint32_t S_FULL = take(4), P_FULL = take(4), P_EMPTY = take(4);   // [A, B][2]
   const uint32_t Q_FULL = take(1), Q_EMPTY = take(1), SEG_FULL = take(kSegments), SEG_EMPTY = take(kSegments);
   const uint32_t LOOK = take(2), C_FULL = take(C::NC), C_EMPTY = take(C::NC);
-  constexpr int kBarBytes = 8 * (4 * NK + 12 + 2 + 2 * kSegments + 2 + 2 * C::NC);
+  constexpr int kBarBytes = 8 * (3 * NK + 12 + 2 + 2 * kSegments + 2 + 2 * C::NC);
   static_assert(kBarBytes <= 640, "");
   ChunkPlan* const plan = reinterpret_cast<ChunkPlan*>(misc + 640);
   long long* const scratch = reinterpret_cast<long long*>(misc + 768);                      // [16]
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc + 896);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 904);
   unsigned long long* const bad_keys = reinterpret_cast<unsigned long long*>(misc + 912);   // [2][3]
-  volatile int* const tile_info = reinterpret_cast<volatile int*>(misc + 960);              // [NK]
-  volatile int* const code_info = reinterpret_cast<volatile int*>(misc + 992);              // [NC]
-  Segment* const segs = reinterpret_cast<Segment*>(misc + 1008);
-  static_assert(sizeof(ChunkPlan) <= 128 && 1008 + kSegments * sizeof(Segment) <= C::MISC && NK <= 8, "");
+  Segment* const segs = reinterpret_cast<Segment*>(misc + 960);
+  static_assert(sizeof(ChunkPlan) <= 128 && 960 + kSegments * sizeof(Segment) <= C::MISC, "");
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
-      mbar_init(K_FULL + 8 * i, FP8 ? 128 : 1);
+      mbar_init(FULL + 8 * i, FP8 ? 128 : 1);
       mbar_init(K_EMPTY + 8 * i, 2);   // A's and B's MMAs
-      mbar_init(V_FULL + 8 * i, FP8 ? 128 : 1);
       mbar_init(V_EMPTY + 8 * i, 2);
     }
     for (int i = 0; i < 4; ++i) {
@@ -223,7 +230,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     mbar_init(Q_EMPTY, 2);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(SEG_FULL + 8 * i, 1);
-      mbar_init(SEG_EMPTY + 8 * i, 8);
+      mbar_init(SEG_EMPTY + 8 * i, 10);   // softmax and MMA warps
     }
     mbar_init(LOOK, 4);       // A's warps alone
     mbar_init(LOOK + 8, 8);   // A's and B's
@@ -251,7 +258,8 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
   // ------------------------------------------------------------ MMA of A (X = 0), of B
   // The whole warp runs this, with one lane elected at each instruction: control and operands
   // stay uniform, which keeps the descriptors in uniform registers (a lane by itself moves every
-  // operand there first, on a scheduler that it shares with two softmax warps).
+  // operand there first, on a scheduler that it shares with two softmax warps: 500 tokens at
+  // 131072 487 us, so 402). Every wait costs the issue of MMAs, so there are two a tile.
   auto issue_mma = [&](const int X) {
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, KB);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | kIdescBMajorMN;
@@ -260,71 +268,68 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     const uint32_t tS = tmem + 2 * X * KB, tO = tmem + 4 * KB + X * HD;
     const uint64_t dQ = desc_k<RB, C::SW>(sQ + X * C::Q_TILE);
     const uint64_t dK0 = desc_k<RB, C::SW>(sK), dV0 = desc_mn<RB, C::SW>(sV, C::K_HALF);
-    const int n = __shfl_sync(0xffffffffu, ntiles, 0);
-    int is = 0, ip = 0;                 // next tile of the range for S, for P V
-    int is_st = 0, ip_st = 0;           // their stages,
-    uint32_t is_ph = 0, ip_ph = 0;      // and the phases of those
-    int cs = 0, cp = 0, segments = 0;   // tiles of this half whose S, P V has been issued; segments begun
-    uint32_t mine_bits = 0;             // which of the last 32 tiles are this half's
-    while (ip < n) {
-      // S runs up to two tiles ahead of P V (its buffer held the P before, which that P V has
-      // taken: the MMAs of a thread run in order); but a segment's first S, which waits for its
-      // queries, comes after the last P V of the one before.
-      bool ok = true;
-      while (is < n && is < ip + 2) {
-        ok = __all_sync(0xffffffffu, mbar_wait(K_FULL + 8 * is_st, is_ph, abort_flag, a.status));
-        if (!ok) break;
-        const int info = __shfl_sync(0xffffffffu, tile_info[is_st], 0);
-        if (info & kSegFirst) {
-          if (is > ip) break;
-          ok = __all_sync(0xffffffffu, mbar_wait(Q_FULL, (uint32_t)segments & 1u, abort_flag, a.status));
-          if (!ok) break;
-          ++segments;
-        }
-        // a tile without rows of this half: its stages are freed, but not before they are full,
-        // for a phase has one arrival of each half
-        const uint32_t bit = 1u << (is & 31);
-        if (X == 0 || (info & kSegBoth)) {
-          const int b = cs & 1;
-          tc_fence_after();
-          const uint64_t dK = dK0 + (uint32_t)(is_st * (C::K_TILE >> 4));
+    int s_st = 0, v_st = 0;    // stages of the next S and P V,
+    uint32_t s_ph = 0;         // the phase of S's
+    int cs = 0, cp = 0;        // tiles whose S, P V has been issued
+    auto next_stage = [&](int& st) {
+      if (++st == NK) st = 0;
+    };
+    // S of the next tile, once its K and V are there
+    auto scores = [&](bool mine) {
+      if (!wait_for(FULL + 8 * s_st, s_ph, abort_flag, a.status)) return false;
+      if (mine) {
+        const int b = cs & 1;
+        tc_fence_after();
+        const uint64_t dK = dK0 + (uint32_t)(s_st * (C::K_TILE >> 4));
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            mma_elected(tS + b * KB, dQ + (kk / PER) * (C::Q_HALF >> 4) + 2 * (kk % PER),
-                        dK + (kk / PER) * (C::K_HALF >> 4) + 2 * (kk % PER), idesc_s, kk != 0);
-          commit_elected(bSF + 8 * b);
-          ++cs;
-          mine_bits |= bit;
-        } else {
-          mine_bits &= ~bit;
+        for (int kk = 0; kk < HD / 16; ++kk)
+          mma_elected(tS + b * KB, dQ + (kk / PER) * (C::Q_HALF >> 4) + 2 * (kk % PER),
+                      dK + (kk / PER) * (C::K_HALF >> 4) + 2 * (kk % PER), idesc_s, kk != 0);
+        commit_elected(bSF + 8 * b);
+        ++cs;
+      }
+      commit_elected(K_EMPTY + 8 * s_st);
+      if (++s_st == NK) {
+        s_st = 0;
+        s_ph ^= 1;
+      }
+      return true;
+    };
+    for (int s = 0;; ++s) {
+      const int e = s % kSegments;
+      if (!wait_for(SEG_FULL + 8 * e, (s / kSegments) & 1, abort_flag, a.status)) break;
+      const int first = __shfl_sync(0xffffffffu, segs[e].first, 0);
+      const int count = __shfl_sync(0xffffffffu, segs[e].last, 0) - first;
+      const bool mine = X == 0 || __shfl_sync(0xffffffffu, segs[e].both, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(SEG_EMPTY + 8 * e);
+      if (first < 0 || !wait_for(Q_FULL, s & 1, abort_flag, a.status)) break;
+      // S runs two tiles ahead of P V: its buffer held the P before, which that P V has taken (the
+      // MMAs of a thread run in order). A tile without rows of this half: its stages are freed, but
+      // not before they are full, for a phase has one arrival of each half.
+      bool ok = scores(mine) && (count == 1 || scores(mine));
+      if (count <= 2) commit_elected(Q_EMPTY);
+      for (int i = 0; i < count && ok; ++i) {
+        if (mine) {
+          const int b = cp & 1;
+          ok = wait_for(bPF + 8 * b, (uint32_t)(cp >> 1) & 1u, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dV = dV0 + (uint32_t)(v_st * (C::K_TILE >> 4));
+#pragma unroll
+          for (int kk = 0; kk < KB / 16; ++kk)   // 16 keys: 8 columns of P, 2 groups of 8 rows of V
+            mma_tmem_a_elected(tO, tS + b * KB + 8 * kk, dV + kk * RB, idesc_o);
+          commit_elected(bPE + 8 * b);
+          ++cp;
         }
-        commit_elected(K_EMPTY + 8 * is_st);
-        if (info & kSegLast) commit_elected(Q_EMPTY);
-        ++is;
-        if (++is_st == NK) {
-          is_st = 0;
-          is_ph ^= 1;
+        commit_elected(V_EMPTY + 8 * v_st);
+        next_stage(v_st);
+        if (i + 2 < count) {
+          ok = scores(mine);
+          if (i + 3 == count) commit_elected(Q_EMPTY);
         }
       }
       if (!ok) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(V_FULL + 8 * ip_st, ip_ph, abort_flag, a.status))) break;
-      if (mine_bits >> (ip & 31) & 1) {
-        const int b = cp & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(bPF + 8 * b, (uint32_t)(cp >> 1) & 1u, abort_flag, a.status))) break;
-        tc_fence_after();
-        const uint64_t dV = dV0 + (uint32_t)(ip_st * (C::K_TILE >> 4));
-#pragma unroll
-        for (int kk = 0; kk < KB / 16; ++kk)   // 16 keys: 8 columns of P, 2 groups of 8 rows of V
-          mma_tmem_a_elected(tO, tS + b * KB + 8 * kk, dV + kk * RB, idesc_o);
-        commit_elected(bPE + 8 * b);
-        ++cp;
-      }
-      commit_elected(V_EMPTY + 8 * ip_st);
-      ++ip;
-      if (++ip_st == NK) {
-        ip_st = 0;
-        ip_ph ^= 1;
-      }
     }
   };
 
@@ -343,10 +348,8 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     };
     auto load_v = [&](int i, int y, int boxes) {   // V of the i-th tile of the range
       const int st = i % NK;
-      const uint32_t full = V_FULL + 8 * st;
-      if (i >= NK && !mbar_wait(V_EMPTY + 8 * st, ((i / NK) & 1) ^ 1, abort_flag, a.status)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * HD * 2);
-      __syncwarp();
+      const uint32_t full = FULL + 8 * st;
+      if (i >= NK && !wait_for(V_EMPTY + 8 * st, ((i / NK) & 1) ^ 1, abort_flag, a.status)) return false;
       if (lane < boxes) {
 #pragma unroll
         for (int h = 0; h < C::HALVES; ++h)
@@ -357,13 +360,12 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     bool ok = true;
     while (left > 0 && ok) {
       const int first = w.tile, last = min(w.tiles, first + left);
-      const int both = segment_both(a, w.k, w.t) ? kSegBoth : 0, g = chunk_kv_head(a, w.hp);
+      const int g = chunk_kv_head(a, w.hp);
       left -= last - first;
       page = page_of(first);
       for (int tile = first; tile < last && ok; ++tile, ++it) {
         const int next = tile + 1 < last ? page_of(tile + 1) : 0;
         const int valid = max(0, min(KB, w.limit - tile * KB)), boxes = (valid + a.box - 1) / a.box;
-        const int info = (tile == first ? kSegFirst : 0) | (tile == last - 1 ? kSegLast : 0) | both;
         int pg = page;
         if (lane < boxes && (pg < 0 || pg >= a.n_pages)) {
           report_status(a.status, XMOD_ERR_DEVICE_CHECK);
@@ -373,31 +375,23 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         const int y = (int)(((int64_t)pg * a.hkv + g) * a.page_size + chunk_in_page(a, key));
         if constexpr (!FP8) {
           const int st = it % NK;
-          const uint32_t full = K_FULL + 8 * st;
-          ok = it < NK || mbar_wait(K_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status);
-          ok = __all_sync(0xffffffffu, ok);
+          const uint32_t full = FULL + 8 * st;
+          ok = it < NK || wait_for(K_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
-          if (lane == 0) {
-            tile_info[st] = info;
-            mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * HD * 2);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * HD * 4);   // V's too
           __syncwarp();
           if (lane < boxes) {
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h)
               tma_load_2d(sK + st * C::K_TILE + h * C::K_HALF + lane * a.box * RB, &mK, full, h * 64, y);
           }
-          if (it > 0) ok = __all_sync(0xffffffffu, load_v(it - 1, y_prev, boxes_prev));
+          if (it > 0) ok = load_v(it - 1, y_prev, boxes_prev);
         } else {
           const int st = it % C::NC;
           const uint32_t full = C_FULL + 8 * st;
-          ok = it < C::NC || mbar_wait(C_EMPTY + 8 * st, ((it / C::NC) & 1) ^ 1, abort_flag, a.status);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = it < C::NC || wait_for(C_EMPTY + 8 * st, ((it / C::NC) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
-          if (lane == 0) {
-            code_info[st] = info;
-            mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * (2 * HD + 8));
-          }
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)a.box * (2 * HD + 8));
           __syncwarp();
           if (lane < boxes) {
             const uint32_t k = sCode + st * 2 * C::CODES + lane * a.box * C::CRB;
@@ -425,8 +419,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     bool ok = true;
     for (;; ++s) {
       const int e = s % kSegments;
-      ok = s < kSegments || mbar_wait(SEG_EMPTY + 8 * e, ((s / kSegments) & 1) ^ 1, abort_flag, a.status);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = s < kSegments || wait_for(SEG_EMPTY + 8 * e, ((s / kSegments) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       const int first = w.tile, last = min(w.tiles, first + left);
       const bool both = left > 0 && segment_both(a, w.k, w.t);
@@ -445,8 +438,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       }
       __syncwarp();
       if (left <= 0) break;
-      ok = s == 0 || mbar_wait(Q_EMPTY, (s - 1) & 1, abort_flag, a.status);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = s == 0 || wait_for(Q_EMPTY, (s - 1) & 1, abort_flag, a.status);
       if (!ok) break;
       if (lane == 0) {
         // rows past the chunk's end come too (zeros past q's); they are worked on but not stored
@@ -477,13 +469,13 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     auto meet = [&](int both) {
       __syncwarp();
       if (lane == 0) mbar_arrive(LOOK + 8 * both);
-      const bool r = mbar_wait(LOOK + 8 * both, (look_phase >> both) & 1u, abort_flag, a.status);
+      const bool r = wait_for(LOOK + 8 * both, (look_phase >> both) & 1u, abort_flag, a.status);
       look_phase ^= 1u << both;
-      return __all_sync(0xffffffffu, r);
+      return r;
     };
     for (int s = 0; ok; ++s) {
       const int e = s % kSegments;
-      if (!__all_sync(0xffffffffu, mbar_wait(SEG_FULL + 8 * e, (s / kSegments) & 1, abort_flag, a.status))) break;
+      if (!wait_for(SEG_FULL + 8 * e, (s / kSegments) & 1, abort_flag, a.status)) break;
       const Segment g = segs[e];
       __syncwarp();
       if (lane == 0) mbar_arrive(SEG_EMPTY + 8 * e);
@@ -507,7 +499,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       tmem_st_wait();
       for (int tile = g.first; tile < g.last; ++tile, ++n) {
         const int b = n & 1, it = i0 + tile - g.first, vs = it % NK, key0 = tile * KB;
-        if (!__all_sync(0xffffffffu, mbar_wait(bSF + 8 * b, (uint32_t)(n >> 1) & 1u, abort_flag, a.status))) {
+        if (!wait_for(bSF + 8 * b, (uint32_t)(n >> 1) & 1u, abort_flag, a.status)) {
           ok = false;
           break;
         }
@@ -517,8 +509,8 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         tmem_ld_wait();
         const float* sc = reinterpret_cast<const float*>(gbase + (sScale - base) + vs * C::SCALES);
         if constexpr (FP8) {
-          // the scales lie there since K's codes were converted
-          if (!__all_sync(0xffffffffu, mbar_wait(K_FULL + 8 * vs, (uint32_t)(it / NK) & 1u, abort_flag, a.status))) {
+          // the scales lie there since the codes were converted
+          if (!wait_for(FULL + 8 * vs, (uint32_t)(it / NK) & 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
@@ -555,7 +547,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
           // O holds the tiles before: the last of their products has to have landed
           const int q = n - 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status))) {
+          if (!wait_for(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
@@ -605,7 +597,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         }
         if (masked) {
           // ---- V's slots that some row does not see
-          if (!__all_sync(0xffffffffu, mbar_wait(V_FULL + 8 * vs, (uint32_t)(it / NK) & 1u, abort_flag, a.status))) {
+          if (!wait_for(FULL + 8 * vs, (uint32_t)(it / NK) & 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
@@ -643,7 +635,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             // rare: infinities and NaN of V to the rows that see them, then zeros in their place
             if (n > 0) {
               const int q = n - 1;
-              if (!__all_sync(0xffffffffu, mbar_wait(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status))) {
+              if (!wait_for(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status)) {
                 ok = false;
                 break;
               }
@@ -710,7 +702,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       i0 += count;
       // ---- the segment's result in this CTA's range
       const int q = n - 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status))) break;
+      if (!wait_for(bPE + 8 * (q & 1), (uint32_t)(q >> 1) & 1u, abort_flag, a.status)) break;
       tc_fence_after();
       const bool whole = g.first == 0 && g.last == g.tiles;
       const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
@@ -785,14 +777,12 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     bool ok = true;
     for (int it = 0; it < ntiles && ok; ++it) {
       const int cs = it % (C::NC ? C::NC : 1), st = it % NK;
-      ok = mbar_wait(C_FULL + 8 * cs, (it / (C::NC ? C::NC : 1)) & 1, abort_flag, a.status);
+      ok = wait_for(C_FULL + 8 * cs, (it / (C::NC ? C::NC : 1)) & 1, abort_flag, a.status);
       // K's and V's stages are those of the tile NK before: with V's the softmax is done with its scales
       if (ok && it >= NK)
-        ok = mbar_wait(K_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status) &&
-             mbar_wait(V_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status);
-      ok = __all_sync(0xffffffffu, ok);
+        ok = wait_for(K_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status) &&
+             wait_for(V_EMPTY + 8 * st, ((it / NK) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
-      if (t == 0) tile_info[st] = code_info[cs];
       {
         const float* from = reinterpret_cast<const float*>(gbase + (sCodeScale - base) + cs * C::SCALES);
         float* to = reinterpret_cast<float*>(gbase + (sScale - base) + st * C::SCALES);
@@ -817,9 +807,9 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           sts128(dst + swizzled<RB>(r, 2 * c, KB), lo);
           sts128(dst + swizzled<RB>(r, 2 * c + 1, KB), hi);
         }
-        fence_proxy_async_smem();
-        mbar_arrive((kv ? V_FULL : K_FULL) + 8 * st);
       }
+      fence_proxy_async_smem();
+      mbar_arrive(FULL + 8 * st);
       mbar_arrive(C_EMPTY + 8 * cs);
     }
   }
