@@ -10,29 +10,27 @@ namespace xmod {
 namespace {
 
 // Segment of CTA blockIdx.x that later CTAs' ranges continue, 32 rows a block: a lane has a row,
-// a warp every eighth group of four dimensions; the parts' outputs are weighted to the common
-// maximum, in CTA order, four parts on their way at a time.
+// a warp every eighth group of four dimensions; the parts' outputs are weighted to the running
+// maximum, in CTA order, several parts on their way at a time. Latency: the record, the parts, the
+// stores (13 us with one part at a time and the maxima before, now JTIME).
 constexpr int kJoinWarps = 8;
 
 template <typename T, int HD, int QR>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_chunk_join_kernel(const ChunkArgs a) {
-  constexpr int G = HD / 4, E = G / kJoinWarps, AHEAD = 4;
+  constexpr int G = HD / 4, E = G / kJoinWarps, AHEAD = E >= 4 ? 4 : 8;
   pdl_trigger();
   pdl_wait();
   const ChunkJoin j = a.join[blockIdx.x];
-  if (j.chunk < 0) return;
+  if (j.first < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = blockIdx.y * 32 + lane;
   constexpr int BLOCK = QR < 128 ? QR : 128;
-  const ChunkRow row = chunk_row(a, read_chunk(a, j.chunk), j.hp, j.t, R / BLOCK, R % BLOCK);
+  const ChunkRow row = chunk_row(a, j.k, j.hp, j.t, R / BLOCK, R % BLOCK);
   if (row.m < 0) return;
-  float top = -INFINITY;
-#pragma unroll 8
-  for (int p = j.first; p <= j.last; ++p) top = fmaxf(top, chunk_part<QR, HD>(a, p, p > j.first)[R]);
-  const float low = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
+  float top = -INFINITY, sum = 0.f;
   float4 o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
   for (int p0 = j.first; p0 <= j.last; p0 += AHEAD) {
     float m[AHEAD], l[AHEAD];
     float4 v[AHEAD][E];
@@ -46,6 +44,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_chunk_join_kernel(const
       for (int e = 0; e < E; ++e)
         v[i][e] = *reinterpret_cast<const float4*>(part + 2 * QR + ((e * kJoinWarps + warp) * QR + R) * 4);
     }
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) now = fmaxf(now, m[i]);   // the last part again, perhaps
+    const float low = now == -INFINITY ? 0.f : now, keep = exp2f(top - low);
+    top = now;
+    sum *= keep;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = make_float4(o[e].x * keep, o[e].y * keep, o[e].z * keep, o[e].w * keep);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       if (p0 + i > j.last) break;
@@ -156,6 +162,7 @@ int xmod_cache_attention_chunk(const xmod_dims* dm, const xmod_kv_cache* cache, 
   a.block_tokens = block / a.hpt;
   a.tpt = rows / block * a.block_tokens;
   a.passes = (group + a.hpt - 1) / a.hpt;
+  a.lead = fp32 ? 1 : 4;
   a.hpt_inverse = (65536 + a.hpt - 1) / a.hpt;
   a.page_shift = -1;
   for (int i = 4; i < 31; ++i)

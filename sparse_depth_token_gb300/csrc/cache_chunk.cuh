@@ -6,7 +6,7 @@
 // r: token r / hpt, head r % hpt), so that a key tile read once serves them all. A segment's key
 // tiles are those below its last token's limit. The tiles of all
 // segments form one list (order: chunk, KV head and pass of heads, tokens, keys), cut into
-// equal ranges, one per CTA: a single long sequence fills the GPU as well as a batch of ragged
+// ranges of equal cost, one per CTA: a single long sequence fills the GPU as well as a batch of ragged
 // ones, and causal segments of all lengths even out. Where a segment lies in several CTAs'
 // ranges each leaves its maximum, sum and unnormalised output in the workspace, and a second
 // kernel joins them in CTA order: the result is the same bits at every call.
@@ -23,9 +23,14 @@ constexpr int kChunkTcRows = 256;     // query rows of a segment: tensor cores, 
 constexpr int kChunkTcMaxCtas = 192;
 constexpr int kChunkF32Rows = 64;     // FFMA, two CTAs an SM
 
+struct Chunk {
+  int first, n, len, seq;   // first row, tokens (0: nothing to do), slots, sequence
+};
+
 // A segment that starts in a CTA's range and ends in a later one's.
 struct ChunkJoin {
-  int chunk, hp, t, first, last;   // CTAs first .. last hold it; chunk < 0: none
+  int hp, t, first, last;   // CTAs first .. last hold it; first < 0: none
+  Chunk k;
 };
 
 struct ChunkArgs {
@@ -41,6 +46,7 @@ struct ChunkArgs {
   int group;              // query heads of a KV head
   int hpt, tpt, passes;   // heads and tokens of a segment, passes over a KV head's query heads
   int block_tokens;       // tokens of a block of rows
+  int lead;               // what a segment costs beside its tiles, in tiles
   int hpt_inverse;        // ceil(2^16 / hpt): r / hpt for r, hpt <= 256 (their product is below 2^16)
   int page_shift;         // log2 of the page size, -1: not a power of two
   int box;                // rows of a TMA box: divides the page size and a tile
@@ -49,11 +55,7 @@ struct ChunkArgs {
   int* status;
 };
 
-struct Chunk {
-  int first, n, len, seq;   // first row, tokens (0: nothing to do), slots, sequence
-};
-
-__device__ __forceinline__ Chunk read_chunk(const ChunkArgs& a, int c) {
+static __device__ __noinline__ Chunk read_chunk(const ChunkArgs& a, int c) {
   Chunk k;
   k.first = a.start[c];
   const int end = a.start[c + 1];
@@ -128,32 +130,46 @@ static __device__ __noinline__ long long tiles_before(int tpt, int tokens, int s
 }
 
 // x / y for 0 <= x, 0 < y: in 32 bits where they fit (a division in 64 is long).
-__device__ __forceinline__ long long divide(long long x, long long y) {
-  if (x <= 0xffffffffll && y <= 0xffffffffll) return (uint32_t)x / (uint32_t)y;
+static __device__ __noinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
   return x / y;
 }
 
-// This CTA's range [begin, end) of the tile list and where it starts: chunk, KV head and pass,
-// segment, and `tile` tiles into it.
+// The list's cut: positions are tiles, with `lead` more before each segment's own, so that ranges
+// of equal length take equal time. CTA g's range is each * g + min(g, more) .. .
 struct ChunkPlan {
-  long long begin, end, total, off, each;   // each: tiles of a KV head and pass of the chunk
+  long long begin, end;       // this CTA's range
+  long long each, tiles;      // of a CTA; of a KV head and pass of the chunk it begins in
+  long long off;
   unsigned long long found;
   Chunk k;
-  int chunk, hp, t, tile, ctas;
+  int more, chunk, hp, t, at;   // where the range begins: chunk, KV head and pass, segment, position in it
 };
+
+__device__ __forceinline__ int chunk_cta_of(const ChunkPlan& p, long long position) {
+  const long long big = (p.each + 1) * p.more;   // positions of the CTAs with one more
+  return (int)(position < big ? divide(position, p.each + 1) : p.more + divide(position - big, p.each));
+}
+
+// Cost of the first t segments.
+__device__ __forceinline__ long long cost_before(const ChunkArgs& a, const Chunk& k, int segments, int t) {
+  return tiles_before(a.tpt, k.n, k.len, segments, t) + (long long)a.lead * t;
+}
 
 // All threads of the CTA; scratch: one int64 per warp.
 __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* plan, long long* scratch) {
+  const int least = a.lead + 1;   // of a range: a segment of one tile is not cut
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
   const int per = (a.n_chunks + nthreads - 1) / nthreads;
   const int c0 = min(a.n_chunks, tid * per), c1 = min(a.n_chunks, c0 + per);
   const int P = a.hkv * a.passes;
   long long mine = 0, each = 0;
   Chunk k;
+#pragma unroll 1
   for (int c = c0; c < c1; ++c) {
     k = read_chunk(a, c);
     const int segments = chunk_segments(a, k);
-    each = tiles_before(a.tpt, k.n, k.len, segments, segments);
+    each = cost_before(a, k, segments, segments);
     mine += P * each;
   }
   long long incl = mine;
@@ -165,33 +181,37 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   long long before = incl - mine, total = 0;
+#pragma unroll 1
   for (int w = 0; w < nthreads / 32; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
-  const int ctas = (int)min((long long)gridDim.x, total);
+  const int ctas = total < (long long)least * gridDim.x ? ((int)total + least - 1) / least : (int)gridDim.x;
   const int g = blockIdx.x;
-  const long long begin = g < ctas ? divide(total * g, ctas) : total;
-  const long long end = g < ctas ? divide(total * (g + 1), ctas) : total;
+  const long long length = ctas > 0 ? divide(total, ctas) : 0;
+  const int more = (int)(total - length * ctas);
+  const long long begin = g < ctas ? length * g + min(g, more) : total;
+  const long long end = g < ctas ? begin + length + (g < more ? 1 : 0) : total;
   if (tid == 0) {
     plan->begin = begin;
     plan->end = end;
-    plan->total = total;
-    plan->ctas = ctas;
+    plan->each = length;
+    plan->more = more;
     plan->found = 0;
   }
   if (begin < end && begin >= before && begin < before + mine) {
     long long at = before;
+#pragma unroll 1
     for (int c = c0; c < c1; ++c) {
       if (per > 1) {
         k = read_chunk(a, c);
         const int segments = chunk_segments(a, k);
-        each = tiles_before(a.tpt, k.n, k.len, segments, segments);
+        each = cost_before(a, k, segments, segments);
       }
       if (begin < at + P * each) {
         plan->chunk = c;
         plan->off = begin - at;
-        plan->each = each;
+        plan->tiles = each;
         plan->k = k;
         break;
       }
@@ -200,18 +220,19 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
   }
   __syncthreads();
   if (begin >= end) return;
-  // the segment: the last one with tiles_before <= rem, by as many guesses at once as threads
+  // the segment: the last one that begins at or before rem, by as many guesses at once as threads
   k = plan->k;
   const int segments = chunk_segments(a, k);
   const long long off = plan->off;
-  each = plan->each;
+  each = plan->tiles;
   const int hp = (int)divide(off, each);
   const long long rem = off - hp * each;
   int lo = 0, hi = segments;   // within lo .. hi - 1
+#pragma unroll 1
   while (hi - lo > 1) {
     const int step = (hi - lo + nthreads - 1) / nthreads, t = lo + tid * step;
     if (t < hi) {
-      const long long n = tiles_before(a.tpt, k.n, k.len, segments, t);
+      const long long n = cost_before(a, k, segments, t);
       if (n <= rem) atomicMax(&plan->found, (unsigned long long)t << 40 | (unsigned long long)n);
     }
     __syncthreads();
@@ -222,7 +243,7 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
   if (tid == 0) {
     plan->t = lo;
     plan->hp = hp;
-    plan->tile = (int)(rem - (long long)(plan->found & 0xffffffffffull));
+    plan->at = (int)(rem - (long long)(plan->found & 0xffffffffffull));
   }
   __syncthreads();
 }
@@ -230,38 +251,46 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
 // A CTA's way along its range, segment by segment.
 struct ChunkWalk {
   Chunk k;
-  int chunk, segments, hp, t, tile, tiles, limit;   // tile: the next one, of `tiles`
+  long long left;                                   // positions of the range not yet taken
+  int chunk, segments, hp, t, at, tiles, limit;     // at: position in the segment
+  int first, last;                                  // the segment's tiles in this CTA's range
 
-  __device__ __forceinline__ void set_segment(const ChunkArgs& a) {
-    limit = segment_limit(a, k, t);
-    tiles = segment_tiles(limit);
-  }
   __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkPlan& p) {
     chunk = p.chunk;
     k = p.k;
     segments = chunk_segments(a, k);
     hp = p.hp;
     t = p.t;
-    tile = p.tile;
-    set_segment(a);
+    at = p.at;
+    left = p.end - p.begin;
   }
-  __device__ __forceinline__ void next_segment(const ChunkArgs& a) {
-    tile = 0;
-    if (++t == segments) {
-      t = 0;
-      if (++hp == a.hkv * a.passes) {
-        hp = 0;
-        do {
-          if (++chunk >= a.n_chunks) {   // the list ends here
-            chunk = a.n_chunks - 1;
-            break;
+  // The next segment that has tiles in the range; false: none is left.
+  __device__ __forceinline__ bool next(const ChunkArgs& a) {
+    while (left > 0) {
+      if (at < 0) {   // the segment before is done
+        at = 0;
+        if (++t == segments) {
+          t = 0;
+          if (++hp == a.hkv * a.passes) {
+            hp = 0;
+            do {
+              if (++chunk >= a.n_chunks) return false;   // the list ends here
+              k = read_chunk(a, chunk);
+            } while (k.n == 0);
+            segments = chunk_segments(a, k);
           }
-          k = read_chunk(a, chunk);
-        } while (k.n == 0);
-        segments = chunk_segments(a, k);
+        }
       }
+      limit = segment_limit(a, k, t);
+      tiles = segment_tiles(limit);
+      const int end = (int)min((long long)(tiles + a.lead), at + left);
+      left -= end - at;
+      first = max(0, at - a.lead);
+      last = max(0, end - a.lead);
+      at = -1;
+      if (last > first) return true;
     }
-    set_segment(a);
+    return false;
   }
 };
 
@@ -306,15 +335,15 @@ __device__ __forceinline__ float* chunk_part(const ChunkArgs& a, int cta, bool b
   return a.part + ((int64_t)2 * cta + (began_before ? 0 : 1)) * QR * (HD + 2);
 }
 
-// The join of a segment that begins in this CTA's range and of which `left` tiles come after
-// it: it ends in the last CTA whose range begins at or before its last tile.
-__device__ __forceinline__ ChunkJoin chunk_join(const ChunkPlan& p, const ChunkWalk& w, long long left) {
+// The join of a segment whose first tiles, but not all, are this CTA's, the range's last: it ends
+// `left` tiles on.
+__device__ __forceinline__ ChunkJoin chunk_join(const ChunkPlan& p, const Chunk& k, int hp, int t, int left) {
   ChunkJoin j;
-  j.chunk = w.chunk;
-  j.hp = w.hp;
-  j.t = w.t;
+  j.hp = hp;
+  j.t = t;
   j.first = blockIdx.x;
-  j.last = (int)min((long long)p.ctas - 1, divide((p.end + left) * p.ctas - 1, p.total));
+  j.last = chunk_cta_of(p, p.end + left - 1);
+  j.k = k;
   return j;
 }
 

@@ -31,16 +31,13 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
   pdl_trigger();
   pdl_wait();
   make_chunk_plan(a, &s.plan, s.scratch);
-  const ChunkPlan plan = s.plan;
-  if (tid == 0) a.join[blockIdx.x].chunk = -1;
-  long long left = plan.end - plan.begin;
-  if (left <= 0) return;
+  if (tid == 0) a.join[blockIdx.x].first = -1;
+  if (s.plan.begin >= s.plan.end) return;
   ChunkWalk w;
-  w.begin(a, plan);
+  w.begin(a, s.plan);
   const float to_log2 = 1.4426950408889634f * rsqrtf((float)HD);
-  while (left > 0) {
-    const int first = w.tile, last = (int)min((long long)w.tiles, first + left);
-    left -= last - first;
+  while (w.next(a)) {
+    const int first = w.first, last = w.last;
     ChunkRow row[4];
     float mx[4], sum[4], o[4][DN * DW];
 #pragma unroll
@@ -195,8 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
         }
       }
     }
-    if (tid == 0 && first == 0 && !whole) a.join[blockIdx.x] = chunk_join(plan, w, w.tiles - last);
-    if (left > 0) w.next_segment(a);
+    if (tid == 0 && first == 0 && !whole) a.join[blockIdx.x] = chunk_join(s.plan, w.k, w.hp, w.t, w.tiles - last);
   }
 }
 

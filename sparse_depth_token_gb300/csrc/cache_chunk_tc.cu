@@ -78,8 +78,8 @@ template <int HD, bool FP8> struct Tc {
 // A segment in a CTA's range, as the loader describes it to the softmax warps.
 struct Segment {
   Chunk k;
-  int chunk, hp, t, tiles, limit, first, last;   // tiles first .. last - 1 are this CTA's
-  int both;                                      // B has rows
+  int hp, t, tiles, limit, first, last;   // tiles first .. last - 1 are this CTA's; first < 0: no more
+  int both;                               // B has rows
 };
 constexpr int kSegments = 4;
 
@@ -230,7 +230,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     mbar_init(Q_EMPTY, 2);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(SEG_FULL + 8 * i, 1);
-      mbar_init(SEG_EMPTY + 8 * i, 10);   // softmax and MMA warps
+      mbar_init(SEG_EMPTY + 8 * i, FP8 ? 14 : 10);   // softmax, MMA and conversion warps
     }
     mbar_init(LOOK, 4);       // A's warps alone
     mbar_init(LOOK + 8, 8);   // A's and B's
@@ -252,8 +252,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
   const uint32_t tmem = *tmem_slot;   // S of A, S of B (two buffers each), O of A, O of B
   pdl_wait();
   make_chunk_plan(a, plan, scratch);
-  const int ntiles = (int)(plan->end - plan->begin);
-  if (tid == 0) a.join[blockIdx.x].chunk = -1;
+  if (tid == 0) a.join[blockIdx.x].first = -1;
 
   // ------------------------------------------------------------ MMA of A (X = 0), of B
   // The whole warp runs this, with one lane elected at each instruction: control and operands
@@ -333,13 +332,13 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     }
   };
 
-  if (ntiles <= 0) {
+  if (plan->begin >= plan->end) {
     // nothing to do
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA
     ChunkWalk w;
     w.begin(a, *plan);
-    int left = ntiles, it = 0;
+    int it = 0;
     const int nbox = KB / a.box;
     int page = 0, y_prev = 0, boxes_prev = 0;
     auto page_of = [&](int tile) {   // lane b: the page of box b
@@ -358,10 +357,8 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       return true;
     };
     bool ok = true;
-    while (left > 0 && ok) {
-      const int first = w.tile, last = min(w.tiles, first + left);
-      const int g = chunk_kv_head(a, w.hp);
-      left -= last - first;
+    while (ok && w.next(a)) {
+      const int first = w.first, last = w.last, g = chunk_kv_head(a, w.hp);
       page = page_of(first);
       for (int tile = first; tile < last && ok; ++tile, ++it) {
         const int next = tile + 1 < last ? page_of(tile + 1) : 0;
@@ -406,38 +403,35 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         boxes_prev = boxes;
         page = next;
       }
-      if (left > 0) w.next_segment(a);
     }
-    if (!FP8 && ok) load_v(it - 1, y_prev, boxes_prev);
+    if (!FP8 && ok && it > 0) load_v(it - 1, y_prev, boxes_prev);
   } else if (warp == 1 || warp == 3) {
     issue_mma(warp == 3 ? 1 : 0);
   } else if (warp == 2) {
     // ------------------------------------------------------------ segments and their queries
     ChunkWalk w;
     w.begin(a, *plan);
-    int left = ntiles, s = 0;
+    int s = 0;
     bool ok = true;
     for (;; ++s) {
       const int e = s % kSegments;
       ok = s < kSegments || wait_for(SEG_EMPTY + 8 * e, ((s / kSegments) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
-      const int first = w.tile, last = min(w.tiles, first + left);
-      const bool both = left > 0 && segment_both(a, w.k, w.t);
+      const bool more = w.next(a), both = more && segment_both(a, w.k, w.t);
       if (lane == 0) {
         Segment& g = segs[e];
         g.k = w.k;
-        g.chunk = w.chunk;
         g.hp = w.hp;
         g.t = w.t;
         g.tiles = w.tiles;
         g.limit = w.limit;
-        g.first = left > 0 ? first : -1;   // the end of the range
-        g.last = last;
+        g.first = more ? w.first : -1;
+        g.last = w.last;
         g.both = both;
         mbar_arrive(SEG_FULL + 8 * e);
       }
       __syncwarp();
-      if (left <= 0) break;
+      if (!more) break;
       ok = s == 0 || wait_for(Q_EMPTY, (s - 1) & 1, abort_flag, a.status);
       if (!ok) break;
       if (lane == 0) {
@@ -451,8 +445,6 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                         w.k.first + w.t * a.tpt + x * a.block_tokens);
       }
       __syncwarp();
-      left -= last - first;
-      if (left > 0) w.next_segment(a);
     }
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax
@@ -526,10 +518,15 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           }
         }
         const bool masked = key0 + KB > least;   // some row of the segment does not see all of it
+        const int seen = limit - key0;   // of this row
         if (masked) {
 #pragma unroll
-          for (int i = 0; i < KB; ++i)
-            if (key0 + i >= limit) v[i] = -INFINITY;
+          for (int c = 0; c < KB; c += 16)
+            if (__any_sync(0xffffffffu, seen < c + 16)) {
+#pragma unroll
+              for (int i = c; i < c + 16; ++i)
+                if (i >= seen) v[i] = -INFINITY;
+            }
         }
         float mc[KB / 16];
 #pragma unroll
@@ -592,7 +589,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           if (masked) {   // a scale that is not seen may be anything
 #pragma unroll
             for (int i = 0; i < KB; ++i)
-              if (key0 + i >= limit) v[i] = 0.f;
+              if (i >= seen) v[i] = 0.f;
           }
         }
         if (masked) {
@@ -607,15 +604,25 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           const int width = g.both ? 256 : 128;
           unsigned long long bad = 0;
           bool wrote = false;
-          for (int i = from * CH + R; i < KB * CH; i += width) {
-            const int key = i / CH;
-            const uint32_t at = vt + swizzled<RB>(key, i % CH, KB);
-            if (key >= valid) {
-              sts128(at, make_uint4(0u, 0u, 0u, 0u));
-              wrote = true;
-            } else {
-              const uint4 u = lds128(at);
-              if (nonfinite2(u.x) | nonfinite2(u.y) | nonfinite2(u.z) | nonfinite2(u.w)) bad |= 1ull << key;
+          // four vectors at a time
+#pragma unroll 1
+          for (int i0 = from * CH + R; i0 < KB * CH; i0 += 4 * width) {
+            uint4 u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int i = min(i0 + j * width, KB * CH - 1);
+              u[j] = lds128(vt + swizzled<RB>(i / CH, i % CH, KB));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int i = i0 + j * width, key = i / CH;
+              if (i >= KB * CH) break;
+              if (key >= valid) {
+                sts128(vt + swizzled<RB>(key, i % CH, KB), make_uint4(0u, 0u, 0u, 0u));
+                wrote = true;
+              } else if (nonfinite2(u[j].x) | nonfinite2(u[j].y) | nonfinite2(u[j].z) | nonfinite2(u[j].w)) {
+                bad |= 1ull << key;
+              }
             }
           }
           // three slots in turn: the one of the look before last, which all have read before they
@@ -763,11 +770,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         }
       }
       if (R == 0 && g.first == 0 && !whole) {
-        ChunkWalk w;
-        w.chunk = g.chunk;
-        w.hp = g.hp;
-        w.t = g.t;
-        a.join[blockIdx.x] = chunk_join(*plan, w, g.tiles - g.last);
+        a.join[blockIdx.x] = chunk_join(*plan, g.k, g.hp, g.t, g.tiles - g.last);
       }
     }
   } else if (FP8 && warp >= 12) {
@@ -775,7 +778,19 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     constexpr int CH = HD / 16;                      // 16-byte chunks of a row of codes
     const int t = tid - 384;
     bool ok = true;
-    for (int it = 0; it < ntiles && ok; ++it) {
+    int it = 0;
+    for (int s = 0, left = 0; ok; ++it, --left) {
+      while (left == 0 && ok) {   // the next segment's tiles
+        const int e = s % kSegments;
+        ok = wait_for(SEG_FULL + 8 * e, (s / kSegments) & 1, abort_flag, a.status);
+        if (!ok) break;
+        const int first = segs[e].first;
+        left = first < 0 ? -1 : segs[e].last - first;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(SEG_EMPTY + 8 * e);
+        ++s;
+      }
+      if (!ok || left < 0) break;
       const int cs = it % (C::NC ? C::NC : 1), st = it % NK;
       ok = wait_for(C_FULL + 8 * cs, (it / (C::NC ? C::NC : 1)) & 1, abort_flag, a.status);
       // K's and V's stages are those of the tile NK before: with V's the softmax is done with its scales

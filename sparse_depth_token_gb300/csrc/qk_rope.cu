@@ -295,24 +295,28 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
   }
 }
 
-// The CTAs' sums of the gains' gradients: blockIdx.x 0 q's, 1 k's; in doubles, in order.
+// The CTAs' sums of the gains' gradients, 32 dimensions a block (blockIdx.y 0: q's, 1: k's), in
+// doubles, in order. (One block for all dimensions took longer than the pass itself: 76 us.)
 constexpr int kGainThreads = 1024;
 __global__ void __launch_bounds__(kGainThreads)
 qk_rope_gain_kernel(const float* part, int hd, int ctas, int q_parts, int k_parts, float* dq, float* dk) {
   __shared__ double sm[kGainThreads];
   pdl_trigger();
   pdl_wait();
-  float* out = blockIdx.x ? dk : dq;
+  float* out = blockIdx.y ? dk : dq;
   if (!out) return;
-  const float* at = part + (blockIdx.x ? (int64_t)q_parts * ctas * hd : 0);
-  const int n = (blockIdx.x ? k_parts : q_parts) * ctas, e = threadIdx.x % hd, rows = kGainThreads / hd;
+  const int e = blockIdx.x * 32 + (threadIdx.x & 31), rows = kGainThreads / 32;
+  const float* at = part + (blockIdx.y ? (int64_t)q_parts * ctas * hd : 0) + e;
+  const int n = (blockIdx.y ? k_parts : q_parts) * ctas;
   double s = 0.0;
-  for (int i = threadIdx.x / hd; i < n; i += rows) s += at[(int64_t)i * hd + e];
+#pragma unroll 8
+  for (int i = threadIdx.x >> 5; i < n; i += rows) s += at[(int64_t)i * hd];
   sm[threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.x >= hd) return;
+  if (threadIdx.x >= 32) return;
   s = 0.0;
-  for (int i = 0; i < rows; ++i) s += sm[i * hd + e];
+#pragma unroll 8
+  for (int i = 0; i < rows; ++i) s += sm[i * 32 + threadIdx.x];
   out[e] = (float)s;
 }
 
@@ -337,7 +341,7 @@ int launch_rope(const Ctx& c, RopeArgs a, const PairTurns& turns, float* dq, flo
                                        dim3(kRopeWarps * 32), 0, c.stream, a, turns));
   if (BWD && a.part)
     XMOD_LAUNCH(c, "qk_rope_gain",
-                launch_pdl(qk_rope_gain_kernel, dim3(2), dim3(kGainThreads), 0, c.stream,
+                launch_pdl(qk_rope_gain_kernel, dim3(HD / 32, 2), dim3(kGainThreads), 0, c.stream,
                            (const float*)a.part, HD, ctas, a.q_parts, a.k_parts, dq, dk));
   return XMOD_OK;
 }
@@ -491,7 +495,7 @@ int xmod_qk_rope_bwd(const xmod_dims* dm, int M, const void* qkv, int ldqkv, con
     if (!gains) return XMOD_OK;
     const Ctx c{(cudaStream_t)stream, nullptr};
     XMOD_LAUNCH(c, "qk_rope_gain",
-                launch_pdl(qk_rope_gain_kernel, dim3(2), dim3(kGainThreads), 0, c.stream,
+                launch_pdl(qk_rope_gain_kernel, dim3(dm->head_dim / 32, 2), dim3(kGainThreads), 0, c.stream,
                            (const float*)ws, dm->head_dim, 0, 0, 0, dq_norm, dk_norm));
     return XMOD_OK;
   }
