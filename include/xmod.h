@@ -665,7 +665,7 @@ XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const v
  *   logp    [N] fp32: ln of the probability with which the token was chosen, w_token over the
  *           kept weights' sum; or NULL
  * Weights are integers in units of at most 2^-39 (2^(bits of V) - 62), computed to a relative
- * error of 2^-33, and sums are exact: the choice depends on neither order nor launch, and
+ * error of 2^-32, and sums are exact: the choice depends on neither order nor launch, and
  * differs from the real numbers' only where u, top_p or min_p lies that close to a border.
  * Weights below the unit count as 0.
  * Checked on the device and reported through status_out (a device int, or NULL; see

@@ -44,14 +44,33 @@ struct SampleArgs {
 constexpr int kBins = 4096;     // of 1/64 in log2 of the weight, or of a range of keys
 constexpr int kList = 1024;     // tokens that are ranked one by one
 
+// What stays of a row, in shared memory. bf16 (table): the table's entries of values that go are
+// zeros, `place` is that of the last value kept, of which the first `ties` tokens stay with
+// `weight` each; values beside the table stay as told. Else tokens above x stay, and those at x up
+// to `token`. Weights below `least` go.
+struct Cut {
+  bool table, small, rest;
+  unsigned place;
+  uint64_t ties, weight, least;
+  float x;
+  int token;
+};
+
 struct Shared {
-  uint64_t power[1024];     // 2^(i / 1024) in units of 2^-unit
-  float powerf[1024];       // the same times 2^40
-  unsigned mass_lo[kBins], mass_hi[kBins], count[kBins];
+  uint64_t power[1024];     // 2^(i / 1024) in units of 2^-unit, less kRound's bits
+  float powerf[1024];       // the same times 2^32
+  union {
+    struct {
+      unsigned mass_lo[kBins], mass_hi[kBins];
+    };
+    uint64_t value[kBins];  // weights of bf16 values
+  };
+  unsigned count[kBins];
   uint64_t key[kList], weight[kList];
   uint64_t scan[33], scan2[33];
   uint64_t found[4];
   int n;
+  Cut cut;
 };
 
 // Order of a logit as an unsigned number (larger value, larger number; -0 equals +0), above
@@ -75,7 +94,8 @@ struct Scale {
 // Where the weight of x lies on a grid of 1/1024 in log2 (0 at the top, descending with x), and
 // the rest z: 2^((step + z * 1024) / 1024). The difference and the product are taken with
 // their rounding errors (T. J. Dekker, A floating-point technique for extending the available
-// precision, 1971), so that the rest is good to 2^-34.
+// precision, 1971), so that the rest is good to 2^-34. kNone: the weight is 0.
+constexpr int kNone = -65536;
 __device__ __forceinline__ int step_of(const Scale& s, float x, float& z) {
   constexpr float kMagic = 12288.0f;   // its last bit is 2^-10
   const float d = x - s.top, t = d - x;
@@ -84,20 +104,21 @@ __device__ __forceinline__ int step_of(const Scale& s, float x, float& z) {
   const float e = fmaf(dd, s.hi, fmaf(d, s.lo, fmaf(d, s.hi, -p)));
   const float n = fmaxf(p, -63.0f) + kMagic;
   z = (p - (n - kMagic)) + e;
-  return p > -63.0f ? __float_as_int(n) - __float_as_int(kMagic) : -65536;   // -infinity too
+  return p > -63.0f ? __float_as_int(n) - __float_as_int(kMagic) : kNone;   // -infinity too
 }
 
 // Weight in units of 2^-unit: the table's entry for the grid point and a second-order series
-// of what is left (at most 2^-11: the next term is below 2^-37).
+// of what is left (at most 2^-11: the next term is below 2^-37), rounded to 2^-32 by adding
+// kRound, whose bits the table's entry has less.
+constexpr float kRound = 12582912.0f;
 __device__ __forceinline__ uint64_t weight_of(const Shared& sh, const Scale& s, float x) {
   float z;
   const int step = step_of(s, x, z);
-  if (step <= -64512) return 0;
-  const int j = step & 1023, shift = -(step >> 10);
+  const int j = step & 1023, shift = -(step >> 10);   // 63 at most, or none
   const float q = z * fmaf(z, 0.24022651f, 0.69314718f);
-  const int corr = __float2int_rn(sh.powerf[j] * q);
-  const int64_t w = (int64_t)sh.power[j] + (int64_t)corr * (1ll << (s.unit - 40));
-  return (uint64_t)w >> shift;
+  const int corr = __float_as_int(fmaf(sh.powerf[j], q, kRound));
+  const int64_t w = (int64_t)sh.power[j] + (int64_t)corr * (1ll << (s.unit - 32));
+  return step == kNone ? 0 : (uint64_t)w >> shift;
 }
 
 // Elements of 16-byte block v of a row, -infinity for those outside it.
@@ -111,6 +132,10 @@ template <typename T> struct Row {
     base = p - off;
     V = V_;
     blocks = (int)(((int64_t)off + V + VE - 1) / VE);
+  }
+  __device__ __forceinline__ bool whole(int v) const { return v * VE >= off && v * VE - off + VE <= V; }
+  __device__ __forceinline__ uint4 raw(int v) const {
+    return *reinterpret_cast<const uint4*>(base + (int64_t)v * VE);
   }
   __device__ __forceinline__ void load(int v, float (&x)[VE]) const {
     const int e0 = v * VE - off;   // token of the block's first element
@@ -129,6 +154,30 @@ template <typename T> struct Row {
     }
   }
 };
+
+// f(v, raw) for the 16-byte blocks v of a row that lie within it whole, threads side by side from
+// block `from` on, four loads on their way at a time; edge(v) for the others.
+template <typename T, int STEP, typename F, typename G>
+__device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, F&& f, G&& edge) {
+#pragma unroll 1
+  for (int v0 = from; v0 < to; v0 += 4 * STEP) {
+    uint4 raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int v = v0 + j * STEP;
+      if (v < to && row.whole(v)) raw[j] = row.raw(v);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int v = v0 + j * STEP;
+      if (v >= to) break;
+      if (row.whole(v))
+        f(v, raw[j]);
+      else
+        edge(v);
+    }
+  }
+}
 
 __device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
 
@@ -181,14 +230,15 @@ template <int THREADS> __device__ __forceinline__ void clear_bins(Shared& sh) {
   __syncthreads();
 }
 
-// First bin at which the running sum of counts (by_mass: masses) reaches `need`; what lies
-// before it. The sums reach it.
+// First bin at which the running sum of counts (by_mass: masses) reaches `need` (bin kBins: none),
+// what lies before it, and the whole sums.
 struct Crossing {
   int bin;
   uint64_t count, mass;   // before the bin
+  uint64_t all_count, all_mass;
 };
 template <int THREADS>
-__device__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t need, uint64_t* all_mass) {
+__device__ __noinline__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t need) {
   constexpr int PER = kBins / THREADS;
   uint64_t c = 0, m = 0, total, total_c;
   for (int i = 0; i < PER; ++i) {
@@ -198,9 +248,8 @@ __device__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t need, uint64_t* 
   }
   uint64_t cb = block_scan<THREADS>(c, sh.scan, &total_c);
   uint64_t mb = block_scan<THREADS>(m, sh.scan2, &total);
-  if (all_mass) *all_mass = total;
   if (threadIdx.x == 0) {   // what a sum that never reaches `need` would leave
-    sh.found[0] = kBins - 1;
+    sh.found[0] = kBins;
     sh.found[1] = sh.found[2] = 0;
   }
   __syncthreads();
@@ -220,7 +269,7 @@ __device__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t need, uint64_t* 
     }
   }
   __syncthreads();
-  const Crossing r{(int)sh.found[0], sh.found[1], sh.found[2]};
+  const Crossing r{(int)sh.found[0], sh.found[1], sh.found[2], total_c, total};
   __syncthreads();
   return r;
 }
@@ -228,12 +277,13 @@ __device__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t need, uint64_t* 
 // The key at which the running count (by_mass: mass) over the tokens of bin `bin` in their
 // order reaches `need`, and the mass up to it. `clobbered`: the bins were used for finer ones.
 template <typename T, int THREADS>
-__device__ uint64_t find_key(Shared& sh, const Row<T>& row, const Scale& sc, int bin, uint64_t members,
-                             bool by_mass, uint64_t need, uint64_t* mass_to, bool* clobbered) {
+__device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T>& row, const Scale& sc, int bin, bool by_mass,
+                                          uint64_t need, uint64_t* mass_to, bool* clobbered) {
   constexpr int VE = Row<T>::VE;
   uint64_t lo = 0, hi = ~0ull, before_mass = 0;
   bool ranged = false;   // members are those with keys in lo .. hi, else those of the bin
   auto visit = [&](auto&& f) {
+#pragma unroll 1
     for (int v = threadIdx.x; v < row.blocks; v += THREADS) {
       float x[VE];
       row.load(v, x);
@@ -249,7 +299,22 @@ __device__ uint64_t find_key(Shared& sh, const Row<T>& row, const Scale& sc, int
     }
   };
   // every turn leaves a 4096th of the keys: six are enough for 64 bits
-  for (int level = 0; members > kList && level < 6; ++level) {
+  for (int level = 0; level < 7; ++level) {
+    if (threadIdx.x == 0) {
+      sh.n = 0;
+      sh.found[0] = ~0ull;
+      sh.found[1] = 0;
+    }
+    __syncthreads();
+    visit([&](uint64_t key, float x) {
+      const int i = atomicAdd(&sh.n, 1);
+      if (i < kList) {
+        sh.key[i] = key;
+        sh.weight[i] = weight_of(sh, sc, x);
+      }
+    });
+    __syncthreads();
+    if (sh.n <= kList) break;
     *clobbered = true;
     if (!ranged) {   // the members' range of keys
       uint64_t mn = ~0ull, mx = 0;
@@ -257,12 +322,6 @@ __device__ uint64_t find_key(Shared& sh, const Row<T>& row, const Scale& sc, int
         mn = key < mn ? key : mn;
         mx = key > mx ? key : mx;
       });
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        sh.found[0] = ~0ull;
-        sh.found[1] = 0;
-      }
-      __syncthreads();
       atomicMin((unsigned long long*)&sh.found[0], (unsigned long long)mn);
       atomicMax((unsigned long long*)&sh.found[1], (unsigned long long)mx);
       __syncthreads();
@@ -280,32 +339,24 @@ __device__ uint64_t find_key(Shared& sh, const Row<T>& row, const Scale& sc, int
       add_mass(sh, b, weight_of(sh, sc, x));
     });
     __syncthreads();
-    const Crossing at = find_bin<THREADS>(sh, by_mass, need, nullptr);
+    const Crossing at = find_bin<THREADS>(sh, by_mass, need);
+    const int sub = min(at.bin, kBins - 1);
     need -= by_mass ? at.mass : at.count;
     before_mass += at.mass;
-    members = sh.count[at.bin];
-    hi -= (uint64_t)at.bin << shift;
+    hi -= (uint64_t)sub << shift;
     const uint64_t width = (1ull << shift) - 1;
     if (hi - lo > width) lo = hi - width;
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    sh.n = 0;
-    sh.found[0] = sh.found[1] = 0;
-  }
-  __syncthreads();
-  visit([&](uint64_t key, float x) {
-    const int i = atomicAdd(&sh.n, 1);
-    if (i < kList) {
-      sh.key[i] = key;
-      sh.weight[i] = weight_of(sh, sc, x);
-    }
-  });
-  __syncthreads();
   const int n = min(sh.n, kList);
+  __syncthreads();
+  if (threadIdx.x == 0) sh.found[0] = sh.found[1] = 0;
+  __syncthreads();
+#pragma unroll 1
   for (int i = threadIdx.x; i < n; i += THREADS) {
     const uint64_t key = sh.key[i], w = sh.weight[i];
     uint64_t above = 0, above_mass = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j)
       if (sh.key[j] > key) {
         ++above;
@@ -323,59 +374,466 @@ __device__ uint64_t find_key(Shared& sh, const Row<T>& row, const Scale& sc, int
   return key;
 }
 
+// ---------------------------------------------------------------- bf16 values
+//
+// bf16 rows have few values, so their weights come from a table that a row's CTA works out
+// once, 4096 entries for 2^-9 <= |x| < 128; the other values are worked out as they come.
+constexpr int kValues = 2048;        // of a sign
+constexpr unsigned kLeastValue = 0x3b00;   // 2^-9
+
+// Place of a bf16 value in the table, kBins and more: none. Ranked downwards: kValues - 1 .. 0,
+// then kValues .. kBins - 1.
+__device__ __forceinline__ unsigned place_of(unsigned bits) {
+  const unsigned m = (bits & 0x7fffu) - kLeastValue;
+  return m < kValues ? m + (bits >> 4 & 0x800u) : kBins;
+}
+__device__ __forceinline__ float place_value(int place) {
+  const unsigned bits = place < kValues ? kLeastValue + place : 0x8000u + kLeastValue + (place - kValues);
+  return __uint_as_float(bits << 16);
+}
+__device__ __forceinline__ int place_rank(int place) { return place < kValues ? kValues - 1 - place : place; }
+
+// Counts of the table's values and the cut by them. False: the cut lies among values beside the
+// table.
+template <int THREADS>
+__device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16>& row, const Scale& sc, int top_k,
+                                       float top_p, bool by_k, bool by_p) {
+  using R = Row<__nv_bfloat16>;
+  const int tid = threadIdx.x;
+  unsigned small_n = 0, rest_n = 0;
+  uint64_t small_mass = 0, rest_mass = 0;
+  auto beside = [&](float x) {
+    if (fabsf(x) < 1.0f) {
+      ++small_n;
+      small_mass += weight_of(sh, sc, x);
+    } else {
+      ++rest_n;
+      if (x >= -3.4e38f) rest_mass += weight_of(sh, sc, x);
+    }
+  };
+  auto meet = [&](unsigned bits) {
+    const unsigned place = place_of(bits);
+    if (place < kBins)
+      atomicAdd(&sh.count[place], 1u);
+    else
+      beside(__uint_as_float(bits << 16));
+  };
+  for_blocks<__nv_bfloat16, THREADS>(
+      row, tid, row.blocks,
+      [&](int, const uint4& raw) {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) meet(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xffffu);
+      },
+      [&](int v) {
+        float x[R::VE];
+        row.load(v, x);
+#pragma unroll
+        for (int i = 0; i < R::VE; ++i) {
+          const int token = v * R::VE - row.off + i;
+          if (token >= 0 && token < row.V) meet(__float_as_uint(x[i]) >> 16);
+        }
+      });
+  uint64_t all_small, all_rest, all_small_mass, all_rest_mass;
+  block_scan<THREADS>(small_n, sh.scan, &all_small);
+  block_scan<THREADS>(rest_n, sh.scan2, &all_rest);
+  block_scan<THREADS>(small_mass, sh.scan, &all_small_mass);
+  block_scan<THREADS>(rest_mass, sh.scan2, &all_rest_mass);
+  // running sums in rank order; the small values lie between the signs
+  constexpr int PER = kBins / THREADS;
+  const int r0 = tid * PER;
+  uint64_t c = 0, m = 0, all_c, all_m;
+  auto place_at = [&](int rank) { return rank < kValues ? kValues - 1 - rank : rank; };
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int at = place_at(r0 + i);
+    c += sh.count[at];
+    m += sh.count[at] * sh.value[at];
+  }
+  const uint64_t cb = block_scan<THREADS>(c, sh.scan, &all_c) + (r0 >= kValues ? all_small : 0);
+  const uint64_t mb = block_scan<THREADS>(m, sh.scan2, &all_m) + (r0 >= kValues ? all_small_mass : 0);
+  all_m += all_small_mass + all_rest_mass;
+  // where a sum reaches `need`: found = {place, tokens of it, sum up to it}
+  auto reach = [&](bool by_mass, uint64_t need) {
+    __syncthreads();
+    if (tid == 0) sh.found[0] = kBins;
+    __syncthreads();
+    const uint64_t before = by_mass ? mb : cb;
+    if (before < need && need <= before + (by_mass ? m : c)) {
+      uint64_t count = cb, mass = mb;
+#pragma unroll 1
+      for (int i = 0; i < PER; ++i) {
+        const int at = place_at(r0 + i);
+        const uint64_t n = sh.count[at], w = sh.value[at];
+        if (by_mass ? need <= mass + n * w : need <= count + n) {
+          const uint64_t keep = by_mass ? (need - mass + w - 1) / w : need - count;
+          sh.found[0] = at;
+          sh.found[1] = keep;
+          sh.found[2] = mass + keep * w;
+          break;
+        }
+        count += n;
+        mass += n * w;
+      }
+    }
+    __syncthreads();
+  };
+  uint64_t kept = all_m, ties = 0;
+  unsigned tie_place = kBins;
+  if (by_k) {
+    reach(false, top_k);
+    tie_place = (unsigned)sh.found[0];
+    ties = sh.found[1];
+    if (tie_place < kBins) kept = sh.found[2];
+    // it ends among the values beside the table: nothing is lost if those have no weight
+    if (tie_place == kBins && (all_rest_mass || (uint64_t)top_k <= all_c + all_small)) return false;
+  }
+  if (by_p) {
+    bool more;
+    uint64_t need = scaled(top_p, kept, &more);
+    need += more;
+    if (need == 0) need = 1;
+    reach(true, need);
+    const unsigned place = (unsigned)sh.found[0];
+    if (place == kBins) return false;
+    if (tie_place == kBins || place_rank(place) < place_rank(tie_place)) {
+      tie_place = place;
+      ties = sh.found[1];
+    } else {
+      ties = min(ties, sh.found[1]);   // the same place: p's cut is within k's
+    }
+  }
+  __syncthreads();
+  if (tie_place < kBins) {
+    const uint64_t weight = sh.value[tie_place];
+    __syncthreads();
+    if (tid == 0) {
+      sh.cut.place = tie_place;
+      sh.cut.weight = weight;
+      sh.cut.ties = weight < sh.cut.least ? 0 : ties;
+      sh.cut.small = tie_place >= kValues;
+      sh.cut.rest = false;
+    }
+    const int rank = place_rank(tie_place);
+    for (int i = tid; i < kBins; i += THREADS)
+      if (place_rank(i) >= rank) sh.value[i] = 0;
+  }
+  return true;
+}
+
+// The lowest key kept by top-k and top-p, of any values.
 template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS)
-sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem);
+__device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T>& row, const Scale& sc, int top_k, float top_p,
+                                             bool by_k, bool by_p) {
+  constexpr int VE = Row<T>::VE;
+  const int tid = threadIdx.x;
+  uint64_t cut = 0, rest_mass = 0;
+  // Tokens whose weights are below 2^-24 are summed aside, not by atomics, unless the cut lies
+  // among them.
+  auto fill = [&](int region) {
+    clear_bins<THREADS>(sh);
+    uint64_t mass = 0;
+    auto meet = [&](float x) {
+      float z;
+      const int b = min(kBins - 1, -step_of(sc, x, z) >> 4);
+      const uint64_t w = weight_of(sh, sc, x);
+      if (b < region) {
+        if (by_k) atomicAdd(&sh.count[b], 1u);
+        add_mass(sh, b, w);
+      } else {
+        mass += w;
+      }
+    };
+    for_blocks<T, THREADS>(
+        row, tid, row.blocks,
+        [&](int, const uint4& raw) {
+#pragma unroll
+          for (int i = 0; i < VE / 2; ++i) {
+            const float2 f = vec_pair<T>(raw, i);
+            meet(f.x);
+            meet(f.y);
+          }
+        },
+        [&](int v) {
+          float x[VE];
+          row.load(v, x);
+#pragma unroll 1
+          for (int i = 0; i < VE; ++i) {
+            const int token = v * VE - row.off + i;
+            if (token >= 0 && token < row.V) meet(x[i]);
+          }
+        });
+    block_scan<THREADS>(mass, sh.scan, &rest_mass);
+    __syncthreads();
+  };
+  int region = 24 * 64;
+  fill(region);
+  uint64_t kept = 0;
+  bool clobbered = false;
+  if (by_k) {
+    uint64_t to;
+    Crossing at = find_bin<THREADS>(sh, false, top_k);
+    if (at.bin == kBins) {
+      region = kBins;
+      fill(region);
+      at = find_bin<THREADS>(sh, false, top_k);
+    }
+    kept = at.mass;
+    if (at.bin < kBins - 1) {   // the last bin's weights are 0: kept or not is the same
+      cut = find_key<T, THREADS>(sh, row, sc, at.bin, false, top_k - at.count, &to, &clobbered);
+      kept += to;
+    }
+  } else {
+    kept = find_bin<THREADS>(sh, true, ~0ull).all_mass + rest_mass;
+  }
+  if (by_p) {
+    if (clobbered) fill(region);
+    bool more;
+    uint64_t need = scaled(top_p, kept, &more);
+    need += more;
+    if (need == 0) need = 1;
+    uint64_t to;
+    Crossing at = find_bin<THREADS>(sh, true, need);
+    if (at.bin == kBins && region < kBins) {
+      region = kBins;
+      fill(region);
+      at = find_bin<THREADS>(sh, true, need);
+    }
+    const uint64_t key = find_key<T, THREADS>(sh, row, sc, at.bin, true, need - at.mass, &to, &clobbered);
+    cut = key > cut ? key : cut;
+  }
+  return cut;
+}
+
+// Weights of block v's tokens that are kept for sure, and how many are of the last value kept.
+template <typename T>
+__device__ __forceinline__ unsigned block_weights(const Shared& sh, const Row<T>& row, const Scale& sc,
+                                                  const Cut& cut, int v, const float (&x)[Row<T>::VE],
+                                                  uint64_t (&w)[Row<T>::VE]) {
+  constexpr int VE = Row<T>::VE;
+  unsigned tied = 0;
+  if constexpr (sizeof(T) == 2) {
+    if (cut.table) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const unsigned place = place_of(__float_as_uint(x[i]) >> 16);
+        w[i] = 0;
+        if (place < kBins) {
+          w[i] = sh.value[place];
+          tied += place == cut.place;
+        } else if (fabsf(x[i]) < 1.0f ? cut.small : cut.rest && x[i] >= -3.4e38f) {   // not outside the row
+          const uint64_t t = weight_of(sh, sc, x[i]);
+          w[i] = t >= cut.least ? t : 0;
+        }
+      }
+      return tied;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VE; ++i) {
+    const int token = v * VE - row.off + i;
+    w[i] = 0;
+    if (x[i] > cut.x || (x[i] == cut.x && token <= cut.token)) {
+      const uint64_t t = weight_of(sh, sc, x[i]);
+      w[i] = t >= cut.least ? t : 0;
+    }
+  }
+  return tied;
+}
+
+// The choice among what stays.
+template <typename T, int THREADS>
+__device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T>& row, const Scale& sc, int64_t r,
+                                    float u, float temp) {
   constexpr int VE = Row<T>::VE, WARPS = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_trigger();
-  for (int i = tid; i < 1024; i += THREADS) {
-    const uint64_t p = __umul64hi(tables.coarse[i >> 5], tables.fine[i & 31]);   // 60-bit fraction
-    sh.power[i] = a.unit >= 60 ? p << (a.unit - 60) : p >> (60 - a.unit);
-    sh.powerf[i] = (float)(p >> 20);
+  const Cut cut = sh.cut;
+  // ---- kept weights by slices of the row, a warp each
+  const int per = (row.blocks + WARPS - 1) / WARPS;
+  uint64_t sum = 0, tied = 0;
+  auto meet = [&](int v, const float (&x)[VE]) {
+    uint64_t w[VE];
+    tied += block_weights<T>(sh, row, sc, cut, v, x, w);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) sum += w[i];
+  };
+  for_blocks<T, 32>(
+      row, warp * per + lane, min(row.blocks, (warp + 1) * per),
+      [&](int v, const uint4& raw) {
+        float x[VE];
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+          const float2 f = vec_pair<T>(raw, i);
+          x[2 * i] = f.x;
+          x[2 * i + 1] = f.y;
+        }
+        meet(v, x);
+      },
+      [&](int v) {
+        float x[VE];
+        row.load(v, x);
+        meet(v, x);
+      });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    tied += __shfl_xor_sync(0xffffffffu, tied, o);
   }
-  pdl_wait();
-  for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
-    const Row<T> row(a.logits, r * a.ld, a.V);
-    // ---- the first token in rank; a NaN
-    uint64_t best = 0;
-    bool bad = false;
-    {
-      float top = -INFINITY;
+  __syncthreads();
+  if (lane == 0) {
+    sh.scan[warp] = sum;
+    sh.scan2[warp] = tied;
+  }
+  __syncthreads();
+  uint64_t whole = 0, left = cut.ties;   // ties not yet met
+#pragma unroll 1
+  for (int w = 0; w < WARPS; ++w) {
+    const uint64_t t = min(left, sh.scan2[w]);
+    whole += sh.scan[w] + t * cut.weight;
+    left -= t;
+  }
+  bool rest;
+  uint64_t target = scaled(u, whole, &rest);   // the running sum has to exceed it
+  int slice = 0;
+  left = cut.ties;
+#pragma unroll 1
+  for (; slice < WARPS - 1; ++slice) {
+    const uint64_t t = min(left, sh.scan2[slice]), mass = sh.scan[slice] + t * cut.weight;
+    if (target < mass) break;
+    target -= mass;
+    left -= t;
+  }
+  __syncthreads();
+  // ---- the token within the slice, a block a thread
+#pragma unroll 1
+  for (int v0 = slice * per; v0 < min(row.blocks, (slice + 1) * per); v0 += THREADS) {
+    const int v = v0 + tid;
+    uint64_t w[VE], mine = 0, all, met = 0;
+    float x[VE];
+    const bool live = v < min(row.blocks, (slice + 1) * per);
+    if (live) {
+      row.load(v, x);
+      met = block_weights<T>(sh, row, sc, cut, v, x, w);
+    }
+    if (cut.ties) {   // the block's ties that stay
+      uint64_t all_met;
+      uint64_t stay = block_scan<THREADS>(met, sh.scan, &all_met);
+      stay = left > stay ? left - stay : 0;
+      left = left > all_met ? left - all_met : 0;
+      if (live && met) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (stay && place_of(__float_as_uint(x[i]) >> 16) == cut.place) {
+            w[i] = cut.weight;
+            --stay;
+          }
+      }
+    }
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) mine += w[i];
+    }
+    const uint64_t before = block_scan<THREADS>(mine, sh.scan, &all);
+    if (before <= target && target < before + mine) {
+      uint64_t cum = before;
       int at = -1;
-#pragma unroll 2
-      for (int v = tid; v < row.blocks; v += THREADS) {
+      float x_at = 0.f;
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        cum += w[i];
+        if (at < 0 && cum > target) {
+          at = i;
+          x_at = x[i];
+        }
+      }
+      a.token[r] = v * VE - row.off + at;
+      if (a.logp) {
+        const int e = 63 - __clzll(whole);
+        const float f = (float)(whole - (1ull << e)) * exp2f((float)-e);
+        a.logp[r] = (float)(((double)x_at - (double)sc.top) / (double)temp -
+                            ((double)(e - a.unit) * 0.6931471805599453 + (double)log1pf(f)));
+      }
+    }
+    if (target < all) break;
+    target -= all;
+  }
+  __syncthreads();
+}
+
+// The first token in rank as a key (0: nothing above -infinity), a NaN counts as above all.
+template <typename T, int THREADS>
+__device__ __noinline__ uint64_t first_key(Shared& sh, const Row<T>& row) {
+  constexpr int VE = Row<T>::VE;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float top = -INFINITY;
+  int at = -1;
+  bool bad = false;
+  auto meet = [&](float x, int token) {
+    if (x > top) {
+      top = x;
+      at = token;
+    }
+    bad |= x != x;
+  };
+  for_blocks<T, THREADS>(
+      row, tid, row.blocks,
+      [&](int v, const uint4& raw) {
+        if constexpr (sizeof(T) == 2) {   // eight at once, one by one only if they are above
+          const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
+          const float2 m = __bfloat1622float2(__hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3])));
+          if (m.x <= top && m.y <= top) return;
+        }
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+          const float2 f = vec_pair<T>(raw, i);
+          meet(f.x, v * VE - row.off + 2 * i);
+          meet(f.y, v * VE - row.off + 2 * i + 1);
+        }
+      },
+      [&](int v) {
         float x[VE];
         row.load(v, x);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          if (x[i] > top) {
-            top = x[i];
-            at = v * VE - row.off + i;
-          }
-          bad |= x[i] != x[i];
-        }
-      }
-      if (at >= 0) best = key_of(top, at);
-    }
+        for (int i = 0; i < VE; ++i) meet(x[i], v * VE - row.off + i);
+      });
+  uint64_t best = bad ? ~0ull : at >= 0 ? key_of(top, at) : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
-      best = other > best ? other : best;
-    }
-    __syncthreads();
-    if (lane == 0) sh.scan[warp] = best;
-    bad = __syncthreads_or(bad);
-    for (int w = 0; w < WARPS; ++w) best = sh.scan[w] > best ? sh.scan[w] : best;
-    __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
+    best = other > best ? other : best;
+  }
+  __syncthreads();
+  if (lane == 0) sh.scan[warp] = best;
+  __syncthreads();
+#pragma unroll 1
+  for (int w = 0; w < THREADS / 32; ++w) best = sh.scan[w] > best ? sh.scan[w] : best;
+  __syncthreads();
+  return best;
+}
 
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  const int tid = threadIdx.x;
+  pdl_trigger();
+  for (int i = tid; i < 1024; i += THREADS) {
+    const uint64_t p = __umul64hi(tables.coarse[i >> 5], tables.fine[i & 31]);   // 60-bit fraction
+    sh.power[i] = (a.unit >= 60 ? p << (a.unit - 60) : p >> (60 - a.unit)) -
+                  ((uint64_t)__float_as_int(kRound) << (a.unit - 32));
+    sh.powerf[i] = (float)(p >> 28);
+  }
+  pdl_wait();
+#pragma unroll 1
+  for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
+    const Row<T> row(a.logits, r * a.ld, a.V);
+    const uint64_t best = first_key<T, THREADS>(sh, row);
     const float temp = a.temperature ? a.temperature[r] : 1.0f;
     const float u = a.u[r], min_p = a.min_p ? a.min_p[r] : 0.0f, top_p = a.top_p ? a.top_p[r] : 1.0f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
     const float top = key_value(best);
-    if (bad || best == 0 || top == INFINITY || !(u >= 0.0f && u < 1.0f) || temp != temp ||
+    if (best == ~0ull || best == 0 || top == INFINITY || !(u >= 0.0f && u < 1.0f) || temp != temp ||
         min_p != min_p || top_p != top_p) {
       if (tid == 0) {
         report_status(a.status, XMOD_ERR_DEVICE_CHECK);
@@ -403,128 +861,42 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
         sc.lo = 0.0f;
       }
     }
-    // ---- the cut of top-k and top-p: the lowest key that is kept
-    uint64_t cut = 0;
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.0f;
-    if (by_k || by_p) {
-      auto fill = [&]() {
-        clear_bins<THREADS>(sh);
-        for (int v = tid; v < row.blocks; v += THREADS) {
-          float x[VE];
-          row.load(v, x);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            const int token = v * VE - row.off + i;
-            if (token < 0 || token >= a.V) continue;
-            float z;
-            const int b = min(kBins - 1, -step_of(sc, x[i], z) >> 4);
-            atomicAdd(&sh.count[b], 1u);
-            if (by_p) {
-              const uint64_t w = weight_of(sh, sc, x[i]);
-              if (w) add_mass(sh, b, w);
-            }
-          }
-        }
-        __syncthreads();
-      };
-      fill();
-      uint64_t kept = 0;
-      bool clobbered = false;
-      if (by_k) {
-        uint64_t to;
-        const Crossing at = find_bin<THREADS>(sh, false, top_k, nullptr);
-        kept = at.mass;
-        if (at.bin < kBins - 1) {   // the last bin's weights are 0: kept or not is the same
-          cut = find_key<T, THREADS>(sh, row, sc, at.bin, sh.count[at.bin], false, top_k - at.count, &to,
-                                     &clobbered);
-          kept += to;
-        }
-      }
-      if (by_p) {
-        if (clobbered) fill();
-        uint64_t all;
-        if (!by_k) {
-          find_bin<THREADS>(sh, false, 1, &all);
-          kept = all;
-        }
-        bool more;
-        uint64_t need = scaled(top_p, kept, &more);
-        need += more;
-        if (need == 0) need = 1;
-        uint64_t to;
-        const Crossing at = find_bin<THREADS>(sh, true, need, nullptr);
-        const uint64_t key = find_key<T, THREADS>(sh, row, sc, at.bin, sh.count[at.bin], true,
-                                                  need - at.mass, &to, &clobbered);
-        cut = key > cut ? key : cut;
-      }
-    }
-    const float cut_x = cut ? key_value(cut) : -INFINITY;
-    const int cut_token = cut ? key_token(cut) : a.V;
     uint64_t least = 0;
     if (min_p > 0.0f) {
       bool more;
       least = scaled(fminf(min_p, 1.0f), 1ull << a.unit, &more);
       least += more;
     }
-    auto kept_weight = [&](float x, int token) -> uint64_t {
-      if (!(x > cut_x || (x == cut_x && token <= cut_token))) return 0;
-      const uint64_t w = weight_of(sh, sc, x);
-      return w >= least ? w : 0;
-    };
-    // ---- kept weights by slices of the row, a warp each
-    const int per = (row.blocks + WARPS - 1) / WARPS;
-    uint64_t sum = 0;
-#pragma unroll 2
-    for (int v = warp * per + lane; v < min(row.blocks, (warp + 1) * per); v += 32) {
-      float x[VE];
-      row.load(v, x);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) sum += kept_weight(x[i], v * VE - row.off + i);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sh.scan[warp] = sum;
-    __syncthreads();
-    uint64_t whole = 0;
-    for (int w = 0; w < WARPS; ++w) whole += sh.scan[w];
-    bool rest;
-    uint64_t target = scaled(u, whole, &rest);   // the running sum has to exceed it
-    int slice = 0;
-    for (; slice < WARPS - 1 && target >= sh.scan[slice]; ++slice) target -= sh.scan[slice];
-    __syncthreads();
-    // ---- the token within the slice, a block a thread
-    for (int v0 = slice * per; v0 < min(row.blocks, (slice + 1) * per); v0 += THREADS) {
-      const int v = v0 + tid;
-      uint64_t w[VE], mine = 0, all;
-      float x[VE];
-      if (v < min(row.blocks, (slice + 1) * per)) {
-        row.load(v, x);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) mine += w[i] = kept_weight(x[i], v * VE - row.off + i);
-      }
-      const uint64_t before = block_scan<THREADS>(mine, sh.scan, &all);
-      if (before <= target && target < before + mine) {
-        uint64_t cum = before;
-        bool done = false;
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          cum += w[i];
-          if (!done && cum > target) {
-            done = true;
-            a.token[r] = v * VE - row.off + i;
-            if (a.logp) {
-              const int e = 63 - __clzll(whole);
-              const float f = (float)(whole - (1ull << e)) * exp2f((float)-e);
-              a.logp[r] = (float)(((double)x[i] - (double)top) / (double)temp -
-                                  ((double)(e - a.unit) * 0.6931471805599453 + (double)log1pf(f)));
-            }
-          }
+    bool table = sizeof(T) == 2 && place_of(__float_as_uint(top) >> 16) < kBins;
+    if (tid == 0) sh.cut = Cut{table, true, true, kBins, 0, 0, least, -INFINITY, a.V};
+    if constexpr (sizeof(T) == 2) {
+      if (table) {
+        for (int i = tid; i < kBins; i += THREADS) {
+          const float x = place_value(i);
+          sh.value[i] = x <= top ? weight_of(sh, sc, x) : 0;
+          sh.count[i] = 0;
+        }
+        __syncthreads();
+        if (by_k || by_p) table = table_cut<THREADS>(sh, row, sc, top_k, top_p, by_k, by_p);
+        if (table && least) {
+          __syncthreads();
+          for (int i = tid; i < kBins; i += THREADS)
+            if (sh.value[i] < least) sh.value[i] = 0;
         }
       }
-      if (target < all) break;
-      target -= all;
+    }
+    if ((by_k || by_p) && !table) {
+      __syncthreads();
+      const uint64_t cut = general_cut<T, THREADS>(sh, row, sc, top_k, top_p, by_k, by_p);
+      if (tid == 0) {
+        sh.cut.table = false;
+        sh.cut.x = cut ? key_value(cut) : -INFINITY;
+        sh.cut.token = cut ? key_token(cut) : a.V;
+      }
     }
     __syncthreads();
+    choose<T, THREADS>(a, sh, row, sc, r, u, temp);
   }
 }
 
