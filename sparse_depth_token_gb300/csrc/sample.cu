@@ -46,10 +46,10 @@ constexpr int kList = 1024;     // tokens that are ranked one by one
 
 // What stays of a row, in shared memory. bf16 (table): the table's entries of values that go are
 // zeros, `place` is that of the last value kept, of which the first `ties` tokens stay with
-// `weight` each; values beside the table stay as told. Else tokens above x stay, and those at x up
-// to `token`. Weights below `least` go.
+// `weight` each; the values too small for the table stay as told. Else tokens above x stay, and
+// those at x up to `token`. Weights below `least` go.
 struct Cut {
-  bool table, small, rest;
+  bool table, small;
   unsigned place;
   uint64_t ties, weight, least;
   float x;
@@ -69,6 +69,8 @@ struct Shared {
   uint64_t key[kList], weight[kList];
   uint64_t scan[33], scan2[33];
   uint64_t found[4];
+  unsigned long long small_mass;
+  unsigned small_n;
   int n;
   Cut cut;
 };
@@ -126,14 +128,16 @@ template <typename T> struct Row {
   static constexpr int VE = 16 / sizeof(T);
   const T* base;    // aligned
   int off, V, blocks;
+  int first, last;   // blocks that lie within the row whole: first .. last - 1
   __device__ Row(const void* logits, int64_t at, int V_) {
     const T* p = (const T*)logits + at;
     off = (int)(((uintptr_t)p & 15) / sizeof(T));
     base = p - off;
     V = V_;
-    blocks = (int)(((int64_t)off + V + VE - 1) / VE);
+    blocks = (off + V + VE - 1) / VE;
+    first = off ? 1 : 0;
+    last = (off + V) / VE;
   }
-  __device__ __forceinline__ bool whole(int v) const { return v * VE >= off && v * VE - off + VE <= V; }
   __device__ __forceinline__ uint4 raw(int v) const {
     return *reinterpret_cast<const uint4*>(base + (int64_t)v * VE);
   }
@@ -155,52 +159,69 @@ template <typename T> struct Row {
   }
 };
 
-// f(v, raw) for the 16-byte blocks v of a row that lie within it whole, threads side by side from
-// block `from` on, four loads on their way at a time; edge(v) for the others.
+// f(v, raw) for this thread's blocks v = from, from + STEP, .. below `to` that lie within the row
+// whole, four loads on their way at a time; edge(v) for those that do not (the row's first and
+// last block at most). f's code stands four times and should be short: unrolled further, or with
+// the rare cases inlined, the loops no longer fit the instruction cache.
 template <typename T, int STEP, typename F, typename G>
 __device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, F&& f, G&& edge) {
+  int v = from;
+  if (v < row.first && v < to) {
+    edge(v);
+    v += STEP;
+  }
+  const int end = min(to, row.last);
 #pragma unroll 1
-  for (int v0 = from; v0 < to; v0 += 4 * STEP) {
+  for (; v < end; v += 4 * STEP) {
     uint4 raw[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = v0 + j * STEP;
-      if (v < to && row.whole(v)) raw[j] = row.raw(v);
-    }
+    for (int j = 0; j < 4; ++j)
+      if (v + j * STEP < end) raw[j] = row.raw(v + j * STEP);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = v0 + j * STEP;
-      if (v >= to) break;
-      if (row.whole(v))
-        f(v, raw[j]);
-      else
-        edge(v);
-    }
+    for (int j = 0; j < 4; ++j)
+      if (v + j * STEP < end) f(v + j * STEP, raw[j]);
   }
+  // the block past the last whole one, if it is this thread's
+  if (row.last < to && row.last >= from && row.last < row.blocks && row.last >= row.first && (row.last - from) % STEP == 0)
+    edge(row.last);
 }
 
 __device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
 
-// Sum over the CTA of each thread's v before it; *total the whole sum.
+// Sums over the CTA of each thread's a and b before it; *total the whole sums.
 template <int THREADS>
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* scratch, uint64_t* total) {
+__device__ __noinline__ ulonglong2 block_scan2(Shared& sh, uint64_t a, uint64_t b, ulonglong2* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t incl = v;
+  uint64_t ia = a, ib = b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t up = shfl_up64(incl, o);
-    if (lane >= o) incl += up;
+    const uint64_t ua = shfl_up64(ia, o), ub = shfl_up64(ib, o);
+    if (lane >= o) {
+      ia += ua;
+      ib += ub;
+    }
   }
   __syncthreads();
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  uint64_t before = 0, sum = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    sum += scratch[w];
+  if (lane == 31) {
+    sh.scan[warp] = ia;
+    sh.scan2[warp] = ib;
   }
-  *total = sum;
-  return before + incl - v;
+  __syncthreads();
+  // a lane a warp
+  constexpr int WARPS = THREADS / 32;
+  uint64_t wa = lane < WARPS ? sh.scan[lane] : 0, wb = lane < WARPS ? sh.scan2[lane] : 0;
+  const uint64_t ma = wa, mb = wb;
+#pragma unroll
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const uint64_t ua = shfl_up64(wa, o), ub = shfl_up64(wb, o);
+    if (lane >= o) {
+      wa += ua;
+      wb += ub;
+    }
+  }
+  total->x = __shfl_sync(0xffffffffu, wa, WARPS - 1);
+  total->y = __shfl_sync(0xffffffffu, wb, WARPS - 1);
+  return make_ulonglong2(__shfl_sync(0xffffffffu, wa - ma, warp) + ia - a, __shfl_sync(0xffffffffu, wb - mb, warp) + ib - b);
 }
 
 // f * w rounded down for f >= 0, and whether something was cut off.
@@ -246,8 +267,11 @@ __device__ __noinline__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t nee
     c += sh.count[b];
     m += (uint64_t)sh.mass_hi[b] << 32 | sh.mass_lo[b];
   }
-  uint64_t cb = block_scan<THREADS>(c, sh.scan, &total_c);
-  uint64_t mb = block_scan<THREADS>(m, sh.scan2, &total);
+  ulonglong2 totals;
+  const ulonglong2 befores = block_scan2<THREADS>(sh, c, m, &totals);
+  uint64_t cb = befores.x, mb = befores.y;
+  total_c = totals.x;
+  total = totals.y;
   if (threadIdx.x == 0) {   // what a sum that never reaches `need` would leave
     sh.found[0] = kBins;
     sh.found[1] = sh.found[2] = 0;
@@ -377,82 +401,126 @@ __device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T>& row, const S
 // ---------------------------------------------------------------- bf16 values
 //
 // bf16 rows have few values, so their weights come from a table that a row's CTA works out
-// once, 4096 entries for 2^-9 <= |x| < 128; the other values are worked out as they come.
-constexpr int kValues = 2048;        // of a sign
-constexpr unsigned kLeastValue = 0x3b00;   // 2^-9
+// once, 4096 entries for 2^-9 <= |x| < 128. Smaller values are worked out as they come; logits
+// below -127.5 count as that, whose weight has to be 0 (else, as with a largest logit outside the
+// table, the row goes the general way).
+constexpr int kValues = 2048;         // of a sign
+constexpr unsigned kLeastValue = 0x3b00;   // 2^-9; the 2048 patterns from here differ in their last 11 bits
+constexpr unsigned kLowest = 0xc2ff;       // -127.5
 
-// Place of a bf16 value in the table, kBins and more: none. Ranked downwards: kValues - 1 .. 0,
-// then kValues .. kBins - 1.
-__device__ __forceinline__ unsigned place_of(unsigned bits) {
-  const unsigned m = (bits & 0x7fffu) - kLeastValue;
-  return m < kValues ? m + (bits >> 4 & 0x800u) : kBins;
-}
+__device__ __forceinline__ unsigned place_of(unsigned bits) { return (bits & 0x7ffu) | (bits >> 4 & 0x800u); }
+__device__ __forceinline__ bool in_table(unsigned bits) { return (bits & 0x7fffu) - kLeastValue < kValues; }
+__device__ __forceinline__ int place_size(int place) { return (place - (kLeastValue & 0x7ff)) & 0x7ff; }   // by |x|
 __device__ __forceinline__ float place_value(int place) {
-  const unsigned bits = place < kValues ? kLeastValue + place : 0x8000u + kLeastValue + (place - kValues);
-  return __uint_as_float(bits << 16);
+  return __uint_as_float((kLeastValue + place_size(place) | (place >= kValues ? 0x8000u : 0u)) << 16);
 }
-__device__ __forceinline__ int place_rank(int place) { return place < kValues ? kValues - 1 - place : place; }
+// Values in falling order.
+__device__ __forceinline__ int place_rank(int place) {
+  return place < kValues ? kValues - 1 - place_size(place) : kValues + place_size(place);
+}
+__device__ __noinline__ uint64_t small_weight(const Shared& sh, const Scale& sc, unsigned bits) {
+  return weight_of(sh, sc, __uint_as_float(bits << 16));
+}
+__device__ __forceinline__ int place_at(int rank) {
+  const int size = rank < kValues ? kValues - 1 - rank : rank - kValues;
+  return ((kLeastValue + size) & 0x7ff) | (rank < kValues ? 0 : kValues);
+}
+__device__ __forceinline__ uint4 clamped(const uint4& raw) {
+  uint4 r;
+  const uint32_t low = kLowest << 16 | kLowest;
+  const __nv_bfloat162 l = *reinterpret_cast<const __nv_bfloat162*>(&low);
+  const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
+  __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = __hmax2(b[i], l);
+  return r;
+}
+// Whether all eight values of a clamped block of a row below 128 lie in the table.
+__device__ __forceinline__ bool all_in_table(const uint4& u) {
+  const unsigned m = 0x7fff7fffu, least = kLeastValue << 16 | kLeastValue;
+  const unsigned x = __vminu2(__vminu2(u.x & m, u.y & m), __vminu2(u.z & m, u.w & m));
+  return __vminu2(x, least) == least;
+}
+__device__ __forceinline__ unsigned half_of(const uint4& u, int i) {
+  const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
+  return i & 1 ? w >> 16 : w & 0xffffu;
+}
+// The same block with clamped elements, those outside the row as they are told.
+__device__ __forceinline__ unsigned clamped_bits(float x) { return __float_as_uint(fmaxf(x, -127.5f)) >> 16; }
 
-// Counts of the table's values and the cut by them. False: the cut lies among values beside the
-// table.
+// Block v with elements outside the row at -infinity, and which are inside.
+template <typename T>
+__device__ __forceinline__ unsigned block_at(const Row<T>& row, int v, float (&x)[Row<T>::VE]) {
+  constexpr int VE = Row<T>::VE;
+  row.load(v, x);
+  unsigned live = 0;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) {
+    const int token = v * VE - row.off + i;
+    if (token >= 0 && token < row.V) live |= 1u << i;
+  }
+  return live;
+}
+__device__ __forceinline__ uint4 packed(const float (&x)[8]) {
+  uint4 u;
+  u.x = clamped_bits(x[0]) | clamped_bits(x[1]) << 16;
+  u.y = clamped_bits(x[2]) | clamped_bits(x[3]) << 16;
+  u.z = clamped_bits(x[4]) | clamped_bits(x[5]) << 16;
+  u.w = clamped_bits(x[6]) | clamped_bits(x[7]) << 16;
+  return u;
+}
+
+// Counts the clamped values u that `live` tells, in the table or beside it.
+__device__ __noinline__ void count_block(Shared& sh, const Scale& sc, const uint4& u, unsigned live) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    if (!(live >> i & 1)) continue;
+    const unsigned bits = half_of(u, i);
+    if (in_table(bits)) {
+      atomicAdd(&sh.count[place_of(bits)], 1u);
+    } else {
+      atomicAdd(&sh.small_n, 1u);
+      atomicAdd(&sh.small_mass, (unsigned long long)small_weight(sh, sc, bits));
+    }
+  }
+}
+
+// Counts of the table's values and the cut by them. False: the cut lies among the smaller values.
 template <int THREADS>
 __device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16>& row, const Scale& sc, int top_k,
                                        float top_p, bool by_k, bool by_p) {
-  using R = Row<__nv_bfloat16>;
   const int tid = threadIdx.x;
-  unsigned small_n = 0, rest_n = 0;
-  uint64_t small_mass = 0, rest_mass = 0;
-  auto beside = [&](float x) {
-    if (fabsf(x) < 1.0f) {
-      ++small_n;
-      small_mass += weight_of(sh, sc, x);
-    } else {
-      ++rest_n;
-      if (x >= -3.4e38f) rest_mass += weight_of(sh, sc, x);
-    }
-  };
-  auto meet = [&](unsigned bits) {
-    const unsigned place = place_of(bits);
-    if (place < kBins)
-      atomicAdd(&sh.count[place], 1u);
-    else
-      beside(__uint_as_float(bits << 16));
-  };
   for_blocks<__nv_bfloat16, THREADS>(
       row, tid, row.blocks,
       [&](int, const uint4& raw) {
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw);
+        const uint4 u = clamped(raw);
+        if (all_in_table(u)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) meet(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xffffu);
+          for (int i = 0; i < 8; ++i) atomicAdd(&sh.count[place_of(half_of(u, i))], 1u);
+        } else {
+          count_block(sh, sc, u, 0xffu);
+        }
       },
       [&](int v) {
-        float x[R::VE];
-        row.load(v, x);
-#pragma unroll
-        for (int i = 0; i < R::VE; ++i) {
-          const int token = v * R::VE - row.off + i;
-          if (token >= 0 && token < row.V) meet(__float_as_uint(x[i]) >> 16);
-        }
+        float x[8];
+        const unsigned live = block_at<__nv_bfloat16>(row, v, x);
+        count_block(sh, sc, packed(x), live);
       });
-  uint64_t all_small, all_rest, all_small_mass, all_rest_mass;
-  block_scan<THREADS>(small_n, sh.scan, &all_small);
-  block_scan<THREADS>(rest_n, sh.scan2, &all_rest);
-  block_scan<THREADS>(small_mass, sh.scan, &all_small_mass);
-  block_scan<THREADS>(rest_mass, sh.scan2, &all_rest_mass);
+  __syncthreads();
   // running sums in rank order; the small values lie between the signs
   constexpr int PER = kBins / THREADS;
   const int r0 = tid * PER;
-  uint64_t c = 0, m = 0, all_c, all_m;
-  auto place_at = [&](int rank) { return rank < kValues ? kValues - 1 - rank : rank; };
+  uint64_t c = 0, m = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int at = place_at(r0 + i);
     c += sh.count[at];
     m += sh.count[at] * sh.value[at];
   }
-  const uint64_t cb = block_scan<THREADS>(c, sh.scan, &all_c) + (r0 >= kValues ? all_small : 0);
-  const uint64_t mb = block_scan<THREADS>(m, sh.scan2, &all_m) + (r0 >= kValues ? all_small_mass : 0);
-  all_m += all_small_mass + all_rest_mass;
+  ulonglong2 all;
+  const ulonglong2 before2 = block_scan2<THREADS>(sh, c, m, &all);
+  const uint64_t cb = before2.x + (r0 >= kValues ? sh.small_n : 0);
+  const uint64_t mb = before2.y + (r0 >= kValues ? sh.small_mass : 0);
   // where a sum reaches `need`: found = {place, tokens of it, sum up to it}
   auto reach = [&](bool by_mass, uint64_t need) {
     __syncthreads();
@@ -478,15 +546,14 @@ __device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16>& row
     }
     __syncthreads();
   };
-  uint64_t kept = all_m, ties = 0;
-  unsigned tie_place = kBins;
+  uint64_t kept = all.y + sh.small_mass, ties = 0;
+  unsigned place = kBins;
   if (by_k) {
     reach(false, top_k);
-    tie_place = (unsigned)sh.found[0];
+    place = (unsigned)sh.found[0];
+    if (place == kBins) return false;
     ties = sh.found[1];
-    if (tie_place < kBins) kept = sh.found[2];
-    // it ends among the values beside the table: nothing is lost if those have no weight
-    if (tie_place == kBins && (all_rest_mass || (uint64_t)top_k <= all_c + all_small)) return false;
+    kept = sh.found[2];
   }
   if (by_p) {
     bool more;
@@ -494,30 +561,26 @@ __device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16>& row
     need += more;
     if (need == 0) need = 1;
     reach(true, need);
-    const unsigned place = (unsigned)sh.found[0];
-    if (place == kBins) return false;
-    if (tie_place == kBins || place_rank(place) < place_rank(tie_place)) {
-      tie_place = place;
+    const unsigned at = (unsigned)sh.found[0];
+    if (at == kBins) return false;
+    // of one place p's cut is within k's
+    if (place == kBins || place_rank(at) <= place_rank(place)) {
+      place = at;
       ties = sh.found[1];
-    } else {
-      ties = min(ties, sh.found[1]);   // the same place: p's cut is within k's
     }
   }
+  const uint64_t weight = sh.value[place];
   __syncthreads();
-  if (tie_place < kBins) {
-    const uint64_t weight = sh.value[tie_place];
-    __syncthreads();
-    if (tid == 0) {
-      sh.cut.place = tie_place;
-      sh.cut.weight = weight;
-      sh.cut.ties = weight < sh.cut.least ? 0 : ties;
-      sh.cut.small = tie_place >= kValues;
-      sh.cut.rest = false;
-    }
-    const int rank = place_rank(tie_place);
-    for (int i = tid; i < kBins; i += THREADS)
-      if (place_rank(i) >= rank) sh.value[i] = 0;
+  if (tid == 0) {
+    sh.cut.place = place;
+    sh.cut.weight = weight;
+    sh.cut.ties = weight < sh.cut.least ? 0 : ties;
+    sh.cut.small = place >= kValues;
   }
+  const int rank = place_rank(place);
+#pragma unroll 1
+  for (int i = tid; i < kBins; i += THREADS)
+    if (place_rank(i) >= rank) sh.value[i] = 0;
   return true;
 }
 
@@ -563,7 +626,9 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T>& row, cons
             if (token >= 0 && token < row.V) meet(x[i]);
           }
         });
-    block_scan<THREADS>(mass, sh.scan, &rest_mass);
+    ulonglong2 all;
+    block_scan2<THREADS>(sh, mass, 0, &all);
+    rest_mass = all.x;
     __syncthreads();
   };
   int region = 24 * 64;
@@ -606,41 +671,64 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T>& row, cons
 }
 
 // Weights of block v's tokens that are kept for sure, and how many are of the last value kept.
-template <typename T>
-__device__ __forceinline__ unsigned block_weights(const Shared& sh, const Row<T>& row, const Scale& sc,
-                                                  const Cut& cut, int v, const float (&x)[Row<T>::VE],
-                                                  uint64_t (&w)[Row<T>::VE]) {
-  constexpr int VE = Row<T>::VE;
+// bf16 by the table: eight clamped values u, those outside the row left out by `live`.
+__device__ __forceinline__ unsigned table_weights(const Shared& sh, const Scale& sc, const Cut& cut, const uint4& u,
+                                                  unsigned live, uint64_t (&w)[8]) {
   unsigned tied = 0;
-  if constexpr (sizeof(T) == 2) {
-    if (cut.table) {
+  if (live == 0xffu && all_in_table(u)) {
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const unsigned place = place_of(__float_as_uint(x[i]) >> 16);
-        w[i] = 0;
-        if (place < kBins) {
-          w[i] = sh.value[place];
-          tied += place == cut.place;
-        } else if (fabsf(x[i]) < 1.0f ? cut.small : cut.rest && x[i] >= -3.4e38f) {   // not outside the row
-          const uint64_t t = weight_of(sh, sc, x[i]);
-          w[i] = t >= cut.least ? t : 0;
-        }
-      }
-      return tied;
+    for (int i = 0; i < 8; ++i) {
+      const unsigned place = place_of(half_of(u, i));
+      w[i] = sh.value[place];
+      tied += place == cut.place;
     }
+    return tied;
   }
 #pragma unroll
-  for (int i = 0; i < VE; ++i) {
-    const int token = v * VE - row.off + i;
+  for (int i = 0; i < 8; ++i) {
+    const unsigned bits = half_of(u, i), place = place_of(bits);
     w[i] = 0;
-    if (x[i] > cut.x || (x[i] == cut.x && token <= cut.token)) {
-      const uint64_t t = weight_of(sh, sc, x[i]);
+    if (!(live >> i & 1)) continue;
+    if (in_table(bits)) {
+      w[i] = sh.value[place];
+      tied += place == cut.place;
+    } else if (cut.small) {
+      const uint64_t t = small_weight(sh, sc, bits);
       w[i] = t >= cut.least ? t : 0;
     }
   }
   return tied;
 }
-
+// Their sum, one by one.
+__device__ __noinline__ uint64_t sum_block(const Shared& sh, const Scale& sc, const uint4& u, unsigned live,
+                                           unsigned* tied) {
+  uint64_t sum = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    if (!(live >> i & 1)) continue;
+    const unsigned bits = half_of(u, i), place = place_of(bits);
+    if (in_table(bits)) {
+      sum += sh.value[place];
+      *tied += place == sh.cut.place;
+    } else if (sh.cut.small) {
+      const uint64_t t = small_weight(sh, sc, bits);
+      sum += t >= sh.cut.least ? t : 0;
+    }
+  }
+  return sum;
+}
+template <typename T>
+__device__ __forceinline__ void key_weights(const Shared& sh, const Scale& sc, const Cut& cut, int token0,
+                                            const float (&x)[Row<T>::VE], uint64_t (&w)[Row<T>::VE]) {
+#pragma unroll
+  for (int i = 0; i < Row<T>::VE; ++i) {
+    w[i] = 0;
+    if (x[i] > cut.x || (x[i] == cut.x && token0 + i <= cut.token)) {
+      const uint64_t t = weight_of(sh, sc, x[i]);
+      w[i] = t >= cut.least ? t : 0;
+    }
+  }
+}
 // The choice among what stays.
 template <typename T, int THREADS>
 __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T>& row, const Scale& sc, int64_t r,
@@ -650,35 +738,60 @@ __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T
   const Cut cut = sh.cut;
   // ---- kept weights by slices of the row, a warp each
   const int per = (row.blocks + WARPS - 1) / WARPS;
-  uint64_t sum = 0, tied = 0;
-  auto meet = [&](int v, const float (&x)[VE]) {
-    uint64_t w[VE];
-    tied += block_weights<T>(sh, row, sc, cut, v, x, w);
+  uint64_t sum = 0;
+  unsigned tied = 0;
+  const int slice_end = min(row.blocks, (warp + 1) * per);
+  if (sizeof(T) == 2 && cut.table) {
+    if constexpr (sizeof(T) == 2) {
+      for_blocks<T, 32>(
+          row, warp * per + lane, slice_end,
+          [&](int, const uint4& raw) {
+            const uint4 u = clamped(raw);
+            if (all_in_table(u)) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) sum += w[i];
-  };
-  for_blocks<T, 32>(
-      row, warp * per + lane, min(row.blocks, (warp + 1) * per),
-      [&](int v, const uint4& raw) {
-        float x[VE];
+              for (int i = 0; i < 8; ++i) {
+                const unsigned place = place_of(half_of(u, i));
+                sum += sh.value[place];
+                tied += place == cut.place;
+              }
+            } else {
+              sum += sum_block(sh, sc, u, 0xffu, &tied);
+            }
+          },
+          [&](int v) {
+            float x[8];
+            const unsigned live = block_at<T>(row, v, x);
+            sum += sum_block(sh, sc, packed(x), live, &tied);
+          });
+    }
+  } else {
+    for_blocks<T, 32>(
+        row, warp * per + lane, slice_end,
+        [&](int v, const uint4& raw) {
+          float x[VE];
+          uint64_t w[VE];
 #pragma unroll
-        for (int i = 0; i < VE / 2; ++i) {
-          const float2 f = vec_pair<T>(raw, i);
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
-        }
-        meet(v, x);
-      },
-      [&](int v) {
-        float x[VE];
-        row.load(v, x);
-        meet(v, x);
-      });
+          for (int i = 0; i < VE / 2; ++i) {
+            const float2 f = vec_pair<T>(raw, i);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+          }
+          key_weights<T>(sh, sc, cut, v * VE - row.off, x, w);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    tied += __shfl_xor_sync(0xffffffffu, tied, o);
+          for (int i = 0; i < VE; ++i) sum += w[i];
+        },
+        [&](int v) {
+          float x[VE];
+          uint64_t w[VE];
+          row.load(v, x);
+          key_weights<T>(sh, sc, cut, v * VE - row.off, x, w);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) sum += w[i];
+        });
   }
+  tied = __reduce_add_sync(0xffffffffu, tied);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   __syncthreads();
   if (lane == 0) {
     sh.scan[warp] = sum;
@@ -708,32 +821,38 @@ __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T
 #pragma unroll 1
   for (int v0 = slice * per; v0 < min(row.blocks, (slice + 1) * per); v0 += THREADS) {
     const int v = v0 + tid;
-    uint64_t w[VE], mine = 0, all, met = 0;
+    uint64_t w[VE], mine = 0;
+    unsigned met = 0;
     float x[VE];
     const bool live = v < min(row.blocks, (slice + 1) * per);
     if (live) {
-      row.load(v, x);
-      met = block_weights<T>(sh, row, sc, cut, v, x, w);
+      const unsigned inside = block_at<T>(row, v, x);
+      if constexpr (sizeof(T) == 2) {
+        if (cut.table) met = table_weights(sh, sc, cut, packed(x), inside, w);
+      }
+      if (sizeof(T) != 2 || !cut.table) key_weights<T>(sh, sc, cut, v * VE - row.off, x, w);
     }
+    ulonglong2 all2;
     if (cut.ties) {   // the block's ties that stay
-      uint64_t all_met;
-      uint64_t stay = block_scan<THREADS>(met, sh.scan, &all_met);
+      uint64_t stay = block_scan2<THREADS>(sh, met, 0, &all2).x;
       stay = left > stay ? left - stay : 0;
-      left = left > all_met ? left - all_met : 0;
+      left = left > all2.x ? left - all2.x : 0;
       if (live && met) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (stay && place_of(__float_as_uint(x[i]) >> 16) == cut.place) {
+        for (int i = 0; i < VE; ++i) {
+          const unsigned bits = clamped_bits(x[i]);
+          if (stay && in_table(bits) && place_of(bits) == cut.place) {
             w[i] = cut.weight;
             --stay;
           }
+        }
       }
     }
     if (live) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) mine += w[i];
     }
-    const uint64_t before = block_scan<THREADS>(mine, sh.scan, &all);
+    const uint64_t before = block_scan2<THREADS>(sh, mine, 0, &all2).x, all = all2.x;
     if (before <= target && target < before + mine) {
       uint64_t cum = before;
       int at = -1;
@@ -868,10 +987,16 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
       least = scaled(fminf(min_p, 1.0f), 1ull << a.unit, &more);
       least += more;
     }
-    bool table = sizeof(T) == 2 && place_of(__float_as_uint(top) >> 16) < kBins;
-    if (tid == 0) sh.cut = Cut{table, true, true, kBins, 0, 0, least, -INFINITY, a.V};
+    // -127.5 at (-127.5 - top) sc.hi: none of its weight is left 62 below
+    bool table = sizeof(T) == 2 && in_table(__float_as_uint(top) >> 16) && (-127.5f - top) * sc.hi < -64.0f;
+    if (tid == 0) {
+      sh.cut = Cut{table, true, kBins, 0, 0, least, -INFINITY, a.V};
+      sh.small_n = 0;
+      sh.small_mass = 0;
+    }
     if constexpr (sizeof(T) == 2) {
       if (table) {
+#pragma unroll 1
         for (int i = tid; i < kBins; i += THREADS) {
           const float x = place_value(i);
           sh.value[i] = x <= top ? weight_of(sh, sc, x) : 0;
