@@ -113,7 +113,7 @@ __device__ __forceinline__ int step_of(const Scale& s, float x, float& z) {
 // of what is left (at most 2^-11: the next term is below 2^-37), rounded to 2^-32 by adding
 // kRound, whose bits the table's entry has less.
 constexpr float kRound = 12582912.0f;
-__device__ __forceinline__ uint64_t weight_of(const Shared& sh, const Scale& s, float x) {
+__device__ __forceinline__ uint64_t weight_inline(const Shared& sh, const Scale& s, float x) {
   float z;
   const int step = step_of(s, x, z);
   const int j = step & 1023, shift = -(step >> 10);   // 63 at most, or none
@@ -121,6 +121,10 @@ __device__ __forceinline__ uint64_t weight_of(const Shared& sh, const Scale& s, 
   const int corr = __float_as_int(fmaf(sh.powerf[j], q, kRound));
   const int64_t w = (int64_t)sh.power[j] + (int64_t)corr * (1ll << (s.unit - 32));
   return step == kNone ? 0 : (uint64_t)w >> shift;
+}
+
+__device__ __noinline__ uint64_t weight_of(const Shared& sh, const Scale& s, float x) {
+  return weight_inline(sh, s, x);
 }
 
 // Elements of 16-byte block v of a row, -infinity for those outside it.
@@ -161,8 +165,8 @@ template <typename T> struct Row {
 
 // f(v, raw) for this thread's blocks v = from, from + STEP, .. below `to` that lie within the row
 // whole, four loads on their way at a time; edge(v) for those that do not (the row's first and
-// last block at most). f's code stands four times and should be short: unrolled further, or with
-// the rare cases inlined, the loops no longer fit the instruction cache.
+// last block at most). f's code stands once: with several copies, or the rare cases inlined, a
+// row's phases evict one another from the instruction cache.
 template <typename T, int STEP, typename F, typename G>
 __device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, F&& f, G&& edge) {
   int v = from;
@@ -177,9 +181,9 @@ __device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, 
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (v + j * STEP < end) raw[j] = row.raw(v + j * STEP);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (v + j * STEP < end) f(v + j * STEP, raw[j]);
+#pragma unroll 1
+    for (int j = 0; j < 4 && v + j * STEP < end; ++j)
+      f(v + j * STEP, j < 2 ? j == 0 ? raw[0] : raw[1] : j == 2 ? raw[2] : raw[3]);
   }
   // the block past the last whole one, if it is this thread's
   if (row.last < to && row.last >= from && row.last < row.blocks && row.last >= row.first && (row.last - from) % STEP == 0)
@@ -225,7 +229,7 @@ __device__ __noinline__ ulonglong2 block_scan2(Shared& sh, uint64_t a, uint64_t 
 }
 
 // f * w rounded down for f >= 0, and whether something was cut off.
-__device__ __forceinline__ uint64_t scaled(float f, uint64_t w, bool* cut) {
+__device__ __noinline__ uint64_t scaled(float f, uint64_t w, bool* cut) {
   const uint32_t b = __float_as_uint(f);
   const int ex = (int)(b >> 23);
   const uint64_t m = (b & 0x7fffffu) | (ex ? 0x800000u : 0u);
@@ -251,6 +255,19 @@ template <int THREADS> __device__ __forceinline__ void clear_bins(Shared& sh) {
   __syncthreads();
 }
 
+// Block v with elements outside the row at -infinity, and which are inside.
+template <typename T>
+__device__ __forceinline__ unsigned block_at(const Row<T>& row, int v, float (&x)[Row<T>::VE]) {
+  constexpr int VE = Row<T>::VE;
+  row.load(v, x);
+  unsigned live = 0;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) {
+    const int token = v * VE - row.off + i;
+    if (token >= 0 && token < row.V) live |= 1u << i;
+  }
+  return live;
+}
 // First bin at which the running sum of counts (by_mass: masses) reaches `need` (bin kBins: none),
 // what lies before it, and the whole sums.
 struct Crossing {
@@ -310,15 +327,22 @@ __device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T>& row, const S
 #pragma unroll 1
     for (int v = threadIdx.x; v < row.blocks; v += THREADS) {
       float x[VE];
-      row.load(v, x);
+      const unsigned live = block_at<T>(row, v, x);
+      unsigned in = 0;
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        const int token = v * VE - row.off + i;
-        if (token < 0 || token >= row.V) continue;
-        const uint64_t key = key_of(x[i], token);
+        const uint64_t key = key_of(x[i], v * VE - row.off + i);
         float z;
-        const bool in = ranged ? key >= lo && key <= hi : min(kBins - 1, -step_of(sc, x[i], z) >> 4) == bin;
-        if (in) f(key, x[i]);
+        in |= (ranged ? key >= lo && key <= hi : min(kBins - 1, -step_of(sc, x[i], z) >> 4) == bin) ? 1u << i : 0u;
+      }
+      // few are members
+#pragma unroll 1
+      for (in &= live; in; in &= in - 1) {
+        const int i = __ffs(in) - 1;
+        float y = x[0];
+#pragma unroll
+        for (int j = 1; j < VE; ++j) y = j == i ? x[j] : y;
+        f(key_of(y, v * VE - row.off + i), y);
       }
     }
   };
@@ -418,9 +442,6 @@ __device__ __forceinline__ float place_value(int place) {
 __device__ __forceinline__ int place_rank(int place) {
   return place < kValues ? kValues - 1 - place_size(place) : kValues + place_size(place);
 }
-__device__ __noinline__ uint64_t small_weight(const Shared& sh, const Scale& sc, unsigned bits) {
-  return weight_of(sh, sc, __uint_as_float(bits << 16));
-}
 __device__ __forceinline__ int place_at(int rank) {
   const int size = rank < kValues ? kValues - 1 - rank : rank - kValues;
   return ((kLeastValue + size) & 0x7ff) | (rank < kValues ? 0 : kValues);
@@ -448,19 +469,6 @@ __device__ __forceinline__ unsigned half_of(const uint4& u, int i) {
 // The same block with clamped elements, those outside the row as they are told.
 __device__ __forceinline__ unsigned clamped_bits(float x) { return __float_as_uint(fmaxf(x, -127.5f)) >> 16; }
 
-// Block v with elements outside the row at -infinity, and which are inside.
-template <typename T>
-__device__ __forceinline__ unsigned block_at(const Row<T>& row, int v, float (&x)[Row<T>::VE]) {
-  constexpr int VE = Row<T>::VE;
-  row.load(v, x);
-  unsigned live = 0;
-#pragma unroll
-  for (int i = 0; i < VE; ++i) {
-    const int token = v * VE - row.off + i;
-    if (token >= 0 && token < row.V) live |= 1u << i;
-  }
-  return live;
-}
 __device__ __forceinline__ uint4 packed(const float (&x)[8]) {
   uint4 u;
   u.x = clamped_bits(x[0]) | clamped_bits(x[1]) << 16;
@@ -480,7 +488,7 @@ __device__ __noinline__ void count_block(Shared& sh, const Scale& sc, const uint
       atomicAdd(&sh.count[place_of(bits)], 1u);
     } else {
       atomicAdd(&sh.small_n, 1u);
-      atomicAdd(&sh.small_mass, (unsigned long long)small_weight(sh, sc, bits));
+      atomicAdd(&sh.small_mass, (unsigned long long)weight_of(sh, sc, __uint_as_float(bits << 16)));
     }
   }
 }
@@ -599,10 +607,10 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T>& row, cons
     auto meet = [&](float x) {
       float z;
       const int b = min(kBins - 1, -step_of(sc, x, z) >> 4);
-      const uint64_t w = weight_of(sh, sc, x);
+      const uint64_t w = by_p ? weight_inline(sh, sc, x) : 0;
       if (b < region) {
         if (by_k) atomicAdd(&sh.count[b], 1u);
-        add_mass(sh, b, w);
+        if (w) add_mass(sh, b, w);
       } else {
         mass += w;
       }
@@ -693,7 +701,7 @@ __device__ __forceinline__ unsigned table_weights(const Shared& sh, const Scale&
       w[i] = sh.value[place];
       tied += place == cut.place;
     } else if (cut.small) {
-      const uint64_t t = small_weight(sh, sc, bits);
+      const uint64_t t = weight_of(sh, sc, __uint_as_float(bits << 16));
       w[i] = t >= cut.least ? t : 0;
     }
   }
@@ -711,23 +719,16 @@ __device__ __noinline__ uint64_t sum_block(const Shared& sh, const Scale& sc, co
       sum += sh.value[place];
       *tied += place == sh.cut.place;
     } else if (sh.cut.small) {
-      const uint64_t t = small_weight(sh, sc, bits);
+      const uint64_t t = weight_of(sh, sc, __uint_as_float(bits << 16));
       sum += t >= sh.cut.least ? t : 0;
     }
   }
   return sum;
 }
-template <typename T>
-__device__ __forceinline__ void key_weights(const Shared& sh, const Scale& sc, const Cut& cut, int token0,
-                                            const float (&x)[Row<T>::VE], uint64_t (&w)[Row<T>::VE]) {
-#pragma unroll
-  for (int i = 0; i < Row<T>::VE; ++i) {
-    w[i] = 0;
-    if (x[i] > cut.x || (x[i] == cut.x && token0 + i <= cut.token)) {
-      const uint64_t t = weight_of(sh, sc, x[i]);
-      w[i] = t >= cut.least ? t : 0;
-    }
-  }
+__device__ __forceinline__ uint64_t key_weight(const Shared& sh, const Scale& sc, const Cut& cut, int token, float x) {
+  if (!(x > cut.x || (x == cut.x && token <= cut.token))) return 0;
+  const uint64_t t = weight_inline(sh, sc, x);
+  return t >= cut.least ? t : 0;
 }
 // The choice among what stays.
 template <typename T, int THREADS>
@@ -768,25 +769,25 @@ __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T
     for_blocks<T, 32>(
         row, warp * per + lane, slice_end,
         [&](int v, const uint4& raw) {
-          float x[VE];
-          uint64_t w[VE];
+          const int token0 = v * VE - row.off;
+          if constexpr (sizeof(T) == 4) {
 #pragma unroll
-          for (int i = 0; i < VE / 2; ++i) {
-            const float2 f = vec_pair<T>(raw, i);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
+            for (int i = 0; i < VE; ++i) sum += key_weight(sh, sc, cut, token0 + i, __uint_as_float((&raw.x)[i]));
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < VE; ++i)
+              sum += key_weight(sh, sc, cut, token0 + i, __uint_as_float(half_of(raw, i) << 16));
           }
-          key_weights<T>(sh, sc, cut, v * VE - row.off, x, w);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) sum += w[i];
         },
         [&](int v) {
           float x[VE];
-          uint64_t w[VE];
-          row.load(v, x);
-          key_weights<T>(sh, sc, cut, v * VE - row.off, x, w);
+          block_at<T>(row, v, x);
 #pragma unroll
-          for (int i = 0; i < VE; ++i) sum += w[i];
+          for (int i = 0; i < VE; ++i)
+            if (x[i] > -INFINITY && x[i] >= cut.x && (x[i] > cut.x || v * VE - row.off + i <= cut.token)) {
+              const uint64_t t = weight_of(sh, sc, x[i]);
+              sum += t >= cut.least ? t : 0;
+            }
         });
   }
   tied = __reduce_add_sync(0xffffffffu, tied);
@@ -830,7 +831,16 @@ __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T
       if constexpr (sizeof(T) == 2) {
         if (cut.table) met = table_weights(sh, sc, cut, packed(x), inside, w);
       }
-      if (sizeof(T) != 2 || !cut.table) key_weights<T>(sh, sc, cut, v * VE - row.off, x, w);
+      if (sizeof(T) != 2 || !cut.table) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          w[i] = 0;
+          if (x[i] > -INFINITY && x[i] >= cut.x && (x[i] > cut.x || v * VE - row.off + i <= cut.token)) {
+            const uint64_t t = weight_of(sh, sc, x[i]);
+            w[i] = t >= cut.least ? t : 0;
+          }
+        }
+      }
     }
     ulonglong2 all2;
     if (cut.ties) {   // the block's ties that stay
@@ -867,10 +877,15 @@ __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T
       }
       a.token[r] = v * VE - row.off + at;
       if (a.logp) {
+        // (x - top) / temp - ln(whole 2^-unit), each with its rounding errors
+        const float d = x_at - sc.top, t = d - x_at, dd = (x_at - (d - t)) + (-sc.top - t);
+        const float q = d / temp, qq = (fmaf(-q, temp, d) + dd) / temp;
         const int e = 63 - __clzll(whole);
-        const float f = (float)(whole - (1ull << e)) * exp2f((float)-e);
-        a.logp[r] = (float)(((double)x_at - (double)sc.top) / (double)temp -
-                            ((double)(e - a.unit) * 0.6931471805599453 + (double)log1pf(f)));
+        const float f = (float)(whole - (1ull << e)) * __uint_as_float((unsigned)(127 - e) << 23);
+        const float n = (float)(e - a.unit);
+        constexpr float kLn2Hi = 0.693145752f, kLn2Lo = 1.42860677e-6f;   // the first of 17 bits
+        const float big = q - n * kLn2Hi, rest2 = (q - big) - n * kLn2Hi;
+        a.logp[r] = big + (rest2 + ((qq - n * kLn2Lo) - log1pf(f)));
       }
     }
     if (target < all) break;
