@@ -36,14 +36,19 @@ struct RopeArgs {
   float eps, amplitude;
   float turn_sign;    // -1: turned back
   float* part;        // [ctas, 2, hd] of the gains' gradients
-  int q_parts, k_parts, q_passes, k_passes;
+  int q_parts, k_parts;   // groups of HPW heads
 };
 
 constexpr int kRopeWarps = 4;
-constexpr int kRopePasses = 4;    // passes of heads a warp holds at a time
+// CTAs an SM, and so registers a thread, and the grid: a warp has many tokens, the next one's
+// vectors on their way while it works on one. Measured (bf16, 12 and 4 heads of 128): forward of
+// 32768 tokens 49.2 us at 5 (4: 51.7, 6: 52.7, 8: 64 with spills; four passes of heads a warp and no
+// token ahead: 56), 5.5 TB/s, 0.81 of what a copy reaches; gradient of 16384 tokens 43.3 us at 4 (3:
+// 44.9, 5: 77 with spills), 4.7 TB/s with the gains' sums, which take 8; twice the grid 52.
+template <bool BWD> constexpr int rope_ctas() { return BWD ? 4 : 5; }
 constexpr int kMaxRopeCtas = 2048;
 
-// A lane holds two vectors of V elements of a head, HD / (2 V) lanes to a head, HPW heads a
+// Bound: memory (a row's q and k heads are read and written once). A lane holds two vectors of V elements of a head, HD / (2 V) lanes to a head, HPW heads a
 // pass. Pairs never leave the lane: with halves paired a turning lane holds vector l and its
 // partner rot_dim / 2 further, the other lanes two neighbouring vectors of the rest;
 // interleaved, any two vectors will do.
@@ -138,17 +143,17 @@ __device__ __forceinline__ void turn(float2 (&x)[V / 2], float2 (&y)[V / 2], con
   }
 }
 
+// A warp takes HPW heads (one pass over 32 lanes) of every step-th token, the same heads all along.
 // BWD: the gradient with norms (the one without is the forward's with turn_sign -1).
 template <typename T, int V, int HD, bool BWD>
-__global__ void __launch_bounds__(kRopeWarps * 32)
+__global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas<BWD>())
 qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
   using S = RopeShape<T, V, HD>;
-  constexpr int LPH = S::LPH, HPW = S::HPW, NP = kRopePasses, VB = V * sizeof(T);
+  constexpr int LPH = S::LPH, HPW = S::HPW, VB = V * sizeof(T);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPH, hl = lane / LPH;
   const bool is_k = (int)blockIdx.y >= a.q_parts;
-  const int part = is_k ? blockIdx.y - a.q_parts : blockIdx.y;
-  const int passes = is_k ? a.k_passes : a.q_passes, heads = is_k ? a.hkv : a.hq;
-  const int h0 = part * passes * HPW + hl;
+  const int part = is_k ? blockIdx.y - a.q_parts : blockIdx.y, heads = is_k ? a.hkv : a.hq;
+  const int h0 = part * HPW + hl;
   const int64_t column = (int64_t)((is_k ? a.hq : 0) + h0) * HD;
   const LaneMap map = lane_map<V, HD>(l, a.rot, a.interleaved);
   uint64_t freq[S::NJ];
@@ -160,7 +165,7 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
     freq[j] = pair < a.rot / 2 ? turns.f[pair] : 0;
   }
   const T* gain = (const T*)(is_k ? a.k_gain : a.q_gain);
-  const bool norm = gain != nullptr;
+  const bool norm = gain != nullptr, live = h0 < heads;
   float2 dg0[V / 2], dg1[V / 2];
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) dg0[e] = dg1[e] = make_float2(0.f, 0.f);
@@ -173,37 +178,38 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
     g1 = load_bytes<VB>(gain + map.e1);
   }
   const int64_t step = (int64_t)gridDim.x * kRopeWarps;
-  for (int64_t m = (int64_t)blockIdx.x * kRopeWarps + warp; m < a.M; m += step) {
-    const int pos = a.pos ? a.pos[m] : (int)(m % a.T);
-    uint4 xv[NP][2], dv[BWD ? NP : 1][2];
-    const T* xp = (const T*)a.x + m * a.ldx + column;
-    const T* dp = (const T*)a.d + m * a.ldd + column;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const bool live = p < passes && h0 + p * HPW < heads && pos >= 0;
-      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-      if (!BWD || norm) {
-        xv[p][0] = live ? load_bytes<VB>(xp + p * HPW * HD + map.e0) : none;
-        xv[p][1] = live ? load_bytes<VB>(xp + p * HPW * HD + map.e1) : none;
-      }
-      if constexpr (BWD) {
-        dv[p][0] = live ? load_bytes<VB>(dp + p * HPW * HD + map.e0) : none;
-        dv[p][1] = live ? load_bytes<VB>(dp + p * HPW * HD + map.e1) : none;
-      }
+  auto position = [&](int64_t m) { return m < a.M ? a.pos ? a.pos[m] : (int)(m % a.T) : -1; };
+  // x: the projections; d: the gradient
+  auto fetch = [&](int64_t m, int pos, uint4 (&x)[2], uint4 (&d)[2]) {
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const bool in = live && pos >= 0;
+    if (!BWD || norm) {
+      const T* p = (const T*)a.x + m * a.ldx + column;
+      x[0] = in ? load_bytes<VB>(p + map.e0) : none;
+      x[1] = in ? load_bytes<VB>(p + map.e1) : none;
     }
-    if (pos < 0) continue;
-    float2 cs[V / 2], sn[V / 2];
-    lane_angles<T, V, HD>(freq, pos, a.amplitude, a.turn_sign, l, cs, sn);
-    T* op = (T*)a.out + m * a.ldo + column;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      if (p >= passes) break;
-      const bool live = h0 + p * HPW < heads;
+    if constexpr (BWD) {
+      const T* p = (const T*)a.d + m * a.ldd + column;
+      d[0] = in ? load_bytes<VB>(p + map.e0) : none;
+      d[1] = in ? load_bytes<VB>(p + map.e1) : none;
+    }
+  };
+  int64_t m = (int64_t)blockIdx.x * kRopeWarps + warp;
+  int pos = position(m), pos1 = position(m + step);
+  uint4 xv[2], dv[2];
+  fetch(m, pos, xv, dv);
+  for (; m < a.M; m += step) {
+    const int pos2 = position(m + 2 * step);
+    uint4 xn[2], dn[2];
+    fetch(m + step, pos1, xn, dn);
+    if (pos >= 0) {
+      float2 cs[V / 2], sn[V / 2];
+      lane_angles<T, V, HD>(freq, pos, a.amplitude, a.turn_sign, l, cs, sn);
       float2 x[V / 2], y[V / 2];
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) {
-        x[e] = vec_pair<T>(BWD ? dv[BWD ? p : 0][0] : xv[p][0], e);
-        y[e] = vec_pair<T>(BWD ? dv[BWD ? p : 0][1] : xv[p][1], e);
+        x[e] = vec_pair<T>(BWD ? dv[0] : xv[0], e);
+        y[e] = vec_pair<T>(BWD ? dv[1] : xv[1], e);
       }
       if constexpr (!BWD) {
         if (norm) {
@@ -227,15 +233,13 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
       } else {
         turn<V>(x, y, cs, sn, map, a.interleaved);   // the gradient at the normed head
         if (norm) {
-          float2 u[V / 2], w[V / 2];
           float2 ss = make_float2(0.f, 0.f), sd = ss;
 #pragma unroll
           for (int e = 0; e < V / 2; ++e) {
-            u[e] = vec_pair<T>(xv[p][0], e);
-            w[e] = vec_pair<T>(xv[p][1], e);
-            ss = fma2(w[e], w[e], fma2(u[e], u[e], ss));
-            sd = fma2(mul2(x[e], vec_pair<T>(g0, e)), u[e], sd);
-            sd = fma2(mul2(y[e], vec_pair<T>(g1, e)), w[e], sd);
+            const float2 u = vec_pair<T>(xv[0], e), w = vec_pair<T>(xv[1], e);
+            ss = fma2(w, w, fma2(u, u, ss));
+            sd = fma2(mul2(x[e], vec_pair<T>(g0, e)), u, sd);
+            sd = fma2(mul2(y[e], vec_pair<T>(g1, e)), w, sd);
           }
           float sum = ss.x + ss.y, dot = sd.x + sd.y;
 #pragma unroll
@@ -249,23 +253,32 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
           const float2 back2 = make_float2(back, back);
 #pragma unroll
           for (int e = 0; e < V / 2; ++e) {
-            dg0[e] = fma2(x[e], mul2(u[e], inv2), dg0[e]);
-            dg1[e] = fma2(y[e], mul2(w[e], inv2), dg1[e]);
-            x[e] = fma2(u[e], back2, mul2(mul2(x[e], vec_pair<T>(g0, e)), inv2));
-            y[e] = fma2(w[e], back2, mul2(mul2(y[e], vec_pair<T>(g1, e)), inv2));
+            const float2 u = vec_pair<T>(xv[0], e), w = vec_pair<T>(xv[1], e);
+            dg0[e] = fma2(x[e], mul2(u, inv2), dg0[e]);
+            dg1[e] = fma2(y[e], mul2(w, inv2), dg1[e]);
+            x[e] = fma2(u, back2, mul2(mul2(x[e], vec_pair<T>(g0, e)), inv2));
+            y[e] = fma2(w, back2, mul2(mul2(y[e], vec_pair<T>(g1, e)), inv2));
           }
         }
       }
       if (live) {
+        T* op = (T*)a.out + m * a.ldo + column;
         uint4 w0, w1;
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
           set_vec_pair<T>(w0, e, x[e]);
           set_vec_pair<T>(w1, e, y[e]);
         }
-        store_bytes<VB>(op + p * HPW * HD + map.e0, w0);
-        store_bytes<VB>(op + p * HPW * HD + map.e1, w1);
+        store_bytes<VB>(op + map.e0, w0);
+        store_bytes<VB>(op + map.e1, w1);
       }
+    }
+    pos = pos1;
+    pos1 = pos2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      xv[i] = xn[i];
+      dv[i] = dn[i];
     }
   }
   if constexpr (BWD) {
@@ -296,11 +309,20 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
 }
 
 // The CTAs' sums of the gains' gradients, 32 dimensions a block (blockIdx.y 0: q's, 1: k's), in
-// doubles, in order. (One block for all dimensions took longer than the pass itself: 76 us.)
+// order, each sum with its rounding errors beside it (D. E. Knuth, The Art of Computer
+// Programming 2, 4.2.2; in doubles it took 22 us of 80, one block for all dimensions 76).
 constexpr int kGainThreads = 1024;
+struct PairSum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float h, float l) {
+    const float t = hi + h, b = t - hi;
+    lo += (hi - (t - b)) + (h - b) + l;
+    hi = t;
+  }
+};
 __global__ void __launch_bounds__(kGainThreads)
 qk_rope_gain_kernel(const float* part, int hd, int ctas, int q_parts, int k_parts, float* dq, float* dk) {
-  __shared__ double sm[kGainThreads];
+  __shared__ float2 sm[kGainThreads];
   pdl_trigger();
   pdl_wait();
   float* out = blockIdx.y ? dk : dq;
@@ -308,16 +330,21 @@ qk_rope_gain_kernel(const float* part, int hd, int ctas, int q_parts, int k_part
   const int e = blockIdx.x * 32 + (threadIdx.x & 31), rows = kGainThreads / 32;
   const float* at = part + (blockIdx.y ? (int64_t)q_parts * ctas * hd : 0) + e;
   const int n = (blockIdx.y ? k_parts : q_parts) * ctas;
-  double s = 0.0;
-#pragma unroll 8
-  for (int i = threadIdx.x >> 5; i < n; i += rows) s += at[(int64_t)i * hd];
-  sm[threadIdx.x] = s;
+  PairSum s{0.f, 0.f};
+  for (int i0 = threadIdx.x >> 5; i0 < n; i0 += 8 * rows) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i0 + j * rows < n ? at[(int64_t)(i0 + j * rows) * hd] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s.add(v[j], 0.f);
+  }
+  sm[threadIdx.x] = make_float2(s.hi, s.lo);
   __syncthreads();
   if (threadIdx.x >= 32) return;
-  s = 0.0;
+  s = PairSum{0.f, 0.f};
 #pragma unroll 8
-  for (int i = 0; i < rows; ++i) s += sm[i * 32 + threadIdx.x];
-  out[e] = (float)s;
+  for (int i = 0; i < rows; ++i) s.add(sm[i * 32 + threadIdx.x].x, sm[i * 32 + threadIdx.x].y);
+  out[e] = s.hi + s.lo;
 }
 
 template <typename T, int V, int HD, bool BWD>
@@ -325,16 +352,11 @@ int launch_rope(const Ctx& c, RopeArgs a, const PairTurns& turns, float* dq, flo
   constexpr int HPW = RopeShape<T, V, HD>::HPW;
   const int sms = device_sms();
   if (sms <= 0) return XMOD_ERR_CUDA;
-  const int q_all = (a.hq + HPW - 1) / HPW, k_all = (a.hkv + HPW - 1) / HPW;
-  const bool few = (int64_t)a.M * (q_all + k_all) <= (int64_t)sms * 8;
-  const int most_passes = few ? 1 : kRopePasses;
-  a.q_parts = (q_all + most_passes - 1) / most_passes;
-  a.k_parts = (k_all + most_passes - 1) / most_passes;
-  a.q_passes = (q_all + a.q_parts - 1) / a.q_parts;
-  a.k_passes = (k_all + a.k_parts - 1) / a.k_parts;
+  a.q_parts = (a.hq + HPW - 1) / HPW;
+  a.k_parts = (a.hkv + HPW - 1) / HPW;
   const int parts = a.q_parts + a.k_parts;
   const int64_t want = ((int64_t)a.M + kRopeWarps - 1) / kRopeWarps;
-  int64_t most = ((int64_t)sms * 16 + parts - 1) / parts;
+  int64_t most = ((int64_t)sms * rope_ctas<BWD>() + parts - 1) / parts;
   if (BWD && most * parts > kMaxRopeCtas) most = kMaxRopeCtas / parts > 0 ? kMaxRopeCtas / parts : 1;
   const int ctas = (int)(want < most ? want : most);
   XMOD_LAUNCH(c, "qk_rope", launch_pdl(qk_rope_kernel<T, V, HD, BWD>, dim3(ctas, parts),
