@@ -12,7 +12,7 @@ namespace {
 // Segment of CTA blockIdx.x that later CTAs' ranges continue, 32 rows a block: a lane has a row,
 // a warp every eighth group of four dimensions; the parts' outputs are weighted to the running
 // maximum, in CTA order, several parts on their way at a time. Latency: the record, the parts, the
-// stores (13 us with one part at a time and the maxima before, now JTIME).
+// stores (13 us with one part at a time and the maxima before, now 7 for eight chunks of four tokens).
 constexpr int kJoinWarps = 8;
 
 template <typename T, int HD, int QR>

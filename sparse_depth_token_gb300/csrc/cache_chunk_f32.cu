@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "cache_chunk.cuh"
 
@@ -14,7 +15,11 @@ constexpr int kRows = kChunkF32Rows, kThreads = 256;
 
 template <int HD> struct Smem {
   static constexpr int QLD = HD + 4, PLD = kChunkKeys + 4;
-  float q[kRows * QLD], kv[kChunkKeys * QLD], p[kRows * PLD];
+  // heads of 128: keys and values share a buffer, so that two CTAs fit an SM (500 tokens at 8192 of
+  // 16 and 4 heads: 910 us; one CTA with both on their way 1574)
+  static constexpr bool kShared = HD == 128;
+  float q[kRows * QLD], k[kChunkKeys * QLD], own_v[kShared ? 4 : kChunkKeys * QLD], p[kRows * PLD];
+  __device__ __forceinline__ float* v() { return kShared ? k : own_v; }
   ChunkPlan plan;
   long long scratch[kThreads / 32];
 };
@@ -59,50 +64,64 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
       }
       *reinterpret_cast<float4*>(&s.q[R * S::QLD + d]) = x;
     }
-    // slots of the cache into shared memory; those at and after the segment's limit as zeros
-    auto fill = [&](const float* cache, int key0) {
-      constexpr int CH = HD / 4;
-      const int g = chunk_kv_head(a, w.hp);
-      for (int i = tid; i < kChunkKeys * CH; i += kThreads) {
-        const int key = i / CH, c = i % CH, slot = key0 + key;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (slot < w.limit) {
-          int page = chunk_page(a, w.k, slot);
-          if (page < 0 || page >= a.n_pages) {
-            report_status(a.status, XMOD_ERR_DEVICE_CHECK);
-            page = 0;
-          }
-          const int64_t at = ((int64_t)page * a.hkv + g) * a.page_size + chunk_in_page(a, slot);
-          x = *reinterpret_cast<const float4*>(cache + at * HD + c * 4);
-        }
-        *reinterpret_cast<float4*>(&s.kv[key * S::QLD + c * 4]) = x;
+    // A tile's slots on their way into shared memory, those at and after the segment's limit as
+    // zeros. A thread copies vector tid % CH of the keys tid / CH + STEP j; the pages of those are
+    // looked up a tile ahead.
+    constexpr int CH = HD / 4, STEP = kThreads / CH, N = kChunkKeys / STEP;
+    const int g = chunk_kv_head(a, w.hp), c4 = tid % CH * 4, key_in = tid / CH;
+    auto pages_of = [&](int tile, int (&page)[N]) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int slot = tile * kChunkKeys + key_in + STEP * j;
+        page[j] = tile < last && slot < w.limit ? chunk_page(a, w.k, slot) : 0;
       }
     };
+    auto copy = [&](const float* cache, float* to, int tile, const int (&page)[N]) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int key = key_in + STEP * j, slot = tile * kChunkKeys + key;
+        int pg = page[j];
+        if (pg < 0 || pg >= a.n_pages) {
+          report_status(a.status, XMOD_ERR_DEVICE_CHECK);
+          pg = 0;
+        }
+        const int64_t at = ((int64_t)pg * a.hkv + g) * a.page_size + chunk_in_page(a, slot);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(to + key * S::QLD + c4)),
+                     "l"(cache + (slot < w.limit ? at * HD + c4 : 0)), "r"(slot < w.limit ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int page[N], page_next[N];
+    pages_of(first, page);
+    pages_of(first + 1, page_next);
+    copy((const float*)a.k, s.k, first, page);
+    if (!S::kShared) copy((const float*)a.v, s.v(), first, page);
     for (int tile = first; tile < last; ++tile) {
       const int key0 = tile * kChunkKeys;
-      fill((const float*)a.k, key0);
+      if (S::kShared)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys; the values may be under way
       __syncthreads();
       float sc[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
       for (int d = 0; d < HD; d += 4) {
         float4 qv[4], kv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&s.q[(4 * ty + i) * S::QLD + d]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&s.kv[(tx + 16 * j) * S::QLD + d]);
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&s.k[(tx + 16 * j) * S::QLD + d]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sc[i][j] = fmaf(qv[i].x, kv[j].x, sc[i][j]);
-            sc[i][j] = fmaf(qv[i].y, kv[j].y, sc[i][j]);
-            sc[i][j] = fmaf(qv[i].z, kv[j].z, sc[i][j]);
-            sc[i][j] = fmaf(qv[i].w, kv[j].w, sc[i][j]);
-          }
+          for (int j = 0; j < 4; ++j)
+            sc[i][j] = fmaf(qv[i].x, kv[j].x, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, sc[i][j]))));
       }
       bool masked = false;
 #pragma unroll
@@ -129,39 +148,71 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
 #pragma unroll
         for (int d = 0; d < DN * DW; ++d) o[i][d] *= keep;
       }
-      __syncthreads();
-      fill((const float*)a.v, key0);
-      __syncthreads();
-      // a key past a row's limit may hold anything: its product is left out, not weighted by 0
+      if (S::kShared) {
+        __syncthreads();   // the keys are done with
+        copy((const float*)a.v, s.v(), tile, page);
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();   // the values are there, the weights too, and the keys are done with
+      if (!S::kShared && tile + 1 < last) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) page[j] = page_next[j];
+        pages_of(tile + 2, page_next);
+        copy((const float*)a.k, s.k, tile + 1, page);
+      }
+      // four keys at a time; a key past a row's limit may hold anything: its product is left out,
+      // not weighted by 0
       const bool guard = __any_sync(0xffffffffu, masked);
-#pragma unroll 4
-      for (int key = 0; key < kChunkKeys; ++key) {
-        float v[DN * DW];
+      auto add = [&](auto guarded, int key) {
+        float4 p[4];
 #pragma unroll
-        for (int g = 0; g < DN; ++g) {
-          const float* at = &s.kv[key * S::QLD + (g * 16 + tx) * DW];
-          if constexpr (DW == 4) {
-            const float4 f = *reinterpret_cast<const float4*>(at);
-            v[4 * g] = f.x;
-            v[4 * g + 1] = f.y;
-            v[4 * g + 2] = f.z;
-            v[4 * g + 3] = f.w;
-          } else {
-            const float2 f = *reinterpret_cast<const float2*>(at);
-            v[2 * g] = f.x;
-            v[2 * g + 1] = f.y;
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&s.p[(4 * ty + i) * S::PLD + key]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v[DN * DW];
+#pragma unroll
+          for (int gd = 0; gd < DN; ++gd) {
+            const float* at = &s.v()[(key + e) * S::QLD + (gd * 16 + tx) * DW];
+            if constexpr (DW == 4) {
+              const float4 f = *reinterpret_cast<const float4*>(at);
+              v[4 * gd] = f.x;
+              v[4 * gd + 1] = f.y;
+              v[4 * gd + 2] = f.z;
+              v[4 * gd + 3] = f.w;
+            } else {
+              const float2 f = *reinterpret_cast<const float2*>(at);
+              v[2 * gd] = f.x;
+              v[2 * gd + 1] = f.y;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float pe = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+            if (!decltype(guarded)::value || key0 + key + e < row[i].limit) {
+#pragma unroll
+              for (int d = 0; d < DN * DW; ++d) o[i][d] = fmaf(pe, v[d], o[i][d]);
+            }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = s.p[(4 * ty + i) * S::PLD + key];
-          if (!guard || key0 + key < row[i].limit) {
-#pragma unroll
-            for (int d = 0; d < DN * DW; ++d) o[i][d] = fmaf(p, v[d], o[i][d]);
-          }
-        }
+      };
+      if (guard) {
+#pragma unroll 1
+        for (int key = 0; key < kChunkKeys; key += 4) add(std::true_type{}, key);
+      } else {
+#pragma unroll 2
+        for (int key = 0; key < kChunkKeys; key += 4) add(std::false_type{}, key);
       }
       __syncthreads();
+      if (tile + 1 < last) {
+        if (S::kShared) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) page[j] = page_next[j];
+          pages_of(tile + 2, page_next);
+          copy((const float*)a.k, s.k, tile + 1, page);
+        } else {
+          copy((const float*)a.v, s.v(), tile + 1, page);
+        }
+      }
     }
     const bool whole = first == 0 && last == w.tiles;
     float* part = chunk_part<kRows, HD>(a, blockIdx.x, first > 0);
