@@ -123,7 +123,7 @@ __device__ __forceinline__ uint64_t weight_inline(const Shared& sh, const Scale&
   return step == kNone ? 0 : (uint64_t)w >> shift;
 }
 
-__device__ __noinline__ uint64_t weight_of(const Shared& sh, const Scale& s, float x) {
+__device__ __noinline__ uint64_t weight_of(const Shared& sh, Scale s, float x) {
   return weight_inline(sh, s, x);
 }
 
@@ -165,9 +165,9 @@ template <typename T> struct Row {
 
 // f(v, raw) for this thread's blocks v = from, from + STEP, .. below `to` that lie within the row
 // whole, four loads on their way at a time; edge(v) for those that do not (the row's first and
-// last block at most). f's code stands once: with several copies, or the rare cases inlined, a
-// row's phases evict one another from the instruction cache.
-template <typename T, int STEP, typename F, typename G>
+// last block at most). A long f stands once: with several copies, or the rare cases inlined, a
+// row's phases evict one another from the instruction cache. SHORT: four copies.
+template <typename T, int STEP, bool SHORT, typename F, typename G>
 __device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, F&& f, G&& edge) {
   int v = from;
   if (v < row.first && v < to) {
@@ -181,9 +181,15 @@ __device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, 
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (v + j * STEP < end) raw[j] = row.raw(v + j * STEP);
+    if constexpr (SHORT) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (v + j * STEP < end) f(v + j * STEP, raw[j]);
+    } else {
 #pragma unroll 1
-    for (int j = 0; j < 4 && v + j * STEP < end; ++j)
-      f(v + j * STEP, j < 2 ? j == 0 ? raw[0] : raw[1] : j == 2 ? raw[2] : raw[3]);
+      for (int j = 0; j < 4 && v + j * STEP < end; ++j)
+        f(v + j * STEP, j < 2 ? j == 0 ? raw[0] : raw[1] : j == 2 ? raw[2] : raw[3]);
+    }
   }
   // the block past the last whole one, if it is this thread's
   if (row.last < to && row.last >= from && row.last < row.blocks && row.last >= row.first && (row.last - from) % STEP == 0)
@@ -478,12 +484,35 @@ __device__ __forceinline__ uint4 packed(const float (&x)[8]) {
   return u;
 }
 
+// Byte offsets of the places of a word's two values in a table of entries of 2^SHIFT bytes.
+template <int SHIFT> __device__ __forceinline__ uint32_t offsets(uint32_t w) {
+  return (w & 0x07ff07ffu) << SHIFT | (w >> (4 - SHIFT) & 0x08000800u << SHIFT);
+}
+template <typename E> __device__ __forceinline__ E& entry(E* table, uint32_t bytes) {
+  return *reinterpret_cast<E*>(reinterpret_cast<char*>(table) + bytes);
+}
+// The values beside the table, a bit each, and the block with the lowest value in their place: its
+// weight is 0 and it ranks last, so that it may be counted without harm.
+__device__ __noinline__ unsigned beside_table(uint4 u) {
+  unsigned r = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r |= in_table(half_of(u, i)) ? 0u : 1u << i;
+  return r;
+}
+__device__ __forceinline__ uint32_t lowest_for(uint32_t w, unsigned beside) {
+  const uint32_t m = (beside & 1 ? 0xffffu : 0u) | (beside & 2 ? 0xffff0000u : 0u);
+  return (w & ~m) | ((kLowest << 16 | kLowest) & m);
+}
+__device__ __forceinline__ uint4 lowest_for(const uint4& u, unsigned beside) {
+  return make_uint4(lowest_for(u.x, beside), lowest_for(u.y, beside >> 2), lowest_for(u.z, beside >> 4),
+                    lowest_for(u.w, beside >> 6));
+}
+
 // Counts the clamped values u that `live` tells, in the table or beside it.
-__device__ __noinline__ void count_block(Shared& sh, const Scale& sc, const uint4& u, unsigned live) {
+__device__ __noinline__ void count_block(Shared& sh, Scale sc, uint4 u, unsigned live) {
 #pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    if (!(live >> i & 1)) continue;
-    const unsigned bits = half_of(u, i);
+  for (; live; live &= live - 1) {
+    const unsigned bits = half_of(u, __ffs(live) - 1);
     if (in_table(bits)) {
       atomicAdd(&sh.count[place_of(bits)], 1u);
     } else {
@@ -498,15 +527,20 @@ template <int THREADS>
 __device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16>& row, const Scale& sc, int top_k,
                                        float top_p, bool by_k, bool by_p) {
   const int tid = threadIdx.x;
-  for_blocks<__nv_bfloat16, THREADS>(
+  for_blocks<__nv_bfloat16, THREADS, true>(
       row, tid, row.blocks,
       [&](int, const uint4& raw) {
-        const uint4 u = clamped(raw);
-        if (all_in_table(u)) {
+        uint4 u = clamped(raw);
+        if (!all_in_table(u)) {
+          const unsigned beside = beside_table(u);
+          count_block(sh, sc, u, beside);
+          u = lowest_for(u, beside);
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) atomicAdd(&sh.count[place_of(half_of(u, i))], 1u);
-        } else {
-          count_block(sh, sc, u, 0xffu);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = offsets<2>((&u.x)[i]);
+          atomicAdd(&entry(sh.count, at & 0xffffu), 1u);
+          atomicAdd(&entry(sh.count, at >> 16), 1u);
         }
       },
       [&](int v) {
@@ -615,7 +649,7 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T>& row, cons
         mass += w;
       }
     };
-    for_blocks<T, THREADS>(
+    for_blocks<T, THREADS, false>(
         row, tid, row.blocks,
         [&](int, const uint4& raw) {
 #pragma unroll
@@ -708,16 +742,13 @@ __device__ __forceinline__ unsigned table_weights(const Shared& sh, const Scale&
   return tied;
 }
 // Their sum, one by one.
-__device__ __noinline__ uint64_t sum_block(const Shared& sh, const Scale& sc, const uint4& u, unsigned live,
-                                           unsigned* tied) {
+__device__ __noinline__ uint64_t sum_block(const Shared& sh, Scale sc, uint4 u, unsigned live) {
   uint64_t sum = 0;
 #pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    if (!(live >> i & 1)) continue;
-    const unsigned bits = half_of(u, i), place = place_of(bits);
+  for (; live; live &= live - 1) {
+    const unsigned bits = half_of(u, __ffs(live) - 1), place = place_of(bits);
     if (in_table(bits)) {
       sum += sh.value[place];
-      *tied += place == sh.cut.place;
     } else if (sh.cut.small) {
       const uint64_t t = weight_of(sh, sc, __uint_as_float(bits << 16));
       sum += t >= sh.cut.least ? t : 0;
@@ -744,29 +775,41 @@ __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T
   const int slice_end = min(row.blocks, (warp + 1) * per);
   if (sizeof(T) == 2 && cut.table) {
     if constexpr (sizeof(T) == 2) {
-      for_blocks<T, 32>(
+      // ties of the low and the high halves, 16 bits each; none is equal to a NaN
+      const uint32_t cut_bits = cut.place < kBins ? __float_as_uint(place_value(cut.place)) : 0x7fff0000u;
+      const uint32_t pattern = cut_bits | cut_bits >> 16;
+      unsigned ties = 0;
+      for_blocks<T, 32, true>(
           row, warp * per + lane, slice_end,
           [&](int, const uint4& raw) {
-            const uint4 u = clamped(raw);
-            if (all_in_table(u)) {
+            uint4 u = clamped(raw);
+            if (!all_in_table(u)) {
+              const unsigned beside = beside_table(u);
+              if (cut.small) sum += sum_block(sh, sc, u, beside);
+              u = lowest_for(u, beside);
+            }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const unsigned place = place_of(half_of(u, i));
-                sum += sh.value[place];
-                tied += place == cut.place;
-              }
-            } else {
-              sum += sum_block(sh, sc, u, 0xffu, &tied);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w = (&u.x)[i], at = offsets<3>(w);
+              sum += entry(sh.value, at & 0xffffu);
+              sum += entry(sh.value, at >> 16);
+              ties += __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w),
+                                  *reinterpret_cast<const __nv_bfloat162*>(&pattern)) & 0x00010001u;
             }
           },
           [&](int v) {
             float x[8];
             const unsigned live = block_at<T>(row, v, x);
-            sum += sum_block(sh, sc, packed(x), live, &tied);
+            const uint4 u = packed(x);
+            sum += sum_block(sh, sc, u, live);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              tied += (live >> i & 1) && half_of(u, i) == (pattern & 0xffffu);
           });
+      tied += (ties & 0xffffu) + (ties >> 16);
     }
   } else {
-    for_blocks<T, 32>(
+    for_blocks<T, 32, false>(
         row, warp * per + lane, slice_end,
         [&](int v, const uint4& raw) {
           const int token0 = v * VE - row.off;
@@ -894,55 +937,70 @@ __device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T
   __syncthreads();
 }
 
-// The first token in rank as a key (0: nothing above -infinity), a NaN counts as above all.
+// The largest of two, a NaN if one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+// The row's largest logit, a NaN if it holds one. Every thread has it.
 template <typename T, int THREADS>
-__device__ __noinline__ uint64_t first_key(Shared& sh, const Row<T>& row) {
+__device__ __noinline__ float row_top(Shared& sh, const Row<T>& row) {
   constexpr int VE = Row<T>::VE;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float top = -INFINITY;
-  int at = -1;
-  bool bad = false;
-  auto meet = [&](float x, int token) {
-    if (x > top) {
-      top = x;
-      at = token;
-    }
-    bad |= x != x;
-  };
-  for_blocks<T, THREADS>(
+  __nv_bfloat162 top2 = __float2bfloat162_rn(-INFINITY);
+  for_blocks<T, THREADS, true>(
       row, tid, row.blocks,
-      [&](int v, const uint4& raw) {
-        if constexpr (sizeof(T) == 2) {   // eight at once, one by one only if they are above
+      [&](int, const uint4& raw) {
+        if constexpr (sizeof(T) == 2) {
           const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
-          const float2 m = __bfloat1622float2(__hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3])));
-          if (m.x <= top && m.y <= top) return;
-        }
-#pragma unroll
-        for (int i = 0; i < VE / 2; ++i) {
-          const float2 f = vec_pair<T>(raw, i);
-          meet(f.x, v * VE - row.off + 2 * i);
-          meet(f.y, v * VE - row.off + 2 * i + 1);
+          top2 = __hmax2_nan(top2, __hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3])));
+        } else {
+          top = max_nan(top, max_nan(max_nan(__uint_as_float(raw.x), __uint_as_float(raw.y)),
+                                     max_nan(__uint_as_float(raw.z), __uint_as_float(raw.w))));
         }
       },
       [&](int v) {
         float x[VE];
         row.load(v, x);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) meet(x[i], v * VE - row.off + i);
+        for (int i = 0; i < VE; ++i) top = max_nan(top, x[i]);
       });
-  uint64_t best = bad ? ~0ull : at >= 0 ? key_of(top, at) : 0;
+  const float2 f = __bfloat1622float2(top2);
+  top = max_nan(top, max_nan(f.x, f.y));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
-    best = other > best ? other : best;
-  }
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   __syncthreads();
-  if (lane == 0) sh.scan[warp] = best;
+  float* tops = reinterpret_cast<float*>(sh.scan);
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+  top = tops[lane < THREADS / 32 ? lane : 0];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  __syncthreads();
+  return top + 0.0f;
+}
+// The first token whose logit is `top`.
+template <typename T, int THREADS>
+__device__ __noinline__ int first_token(Shared& sh, const Row<T>& row, float top) {
+  constexpr int VE = Row<T>::VE;
+  if (threadIdx.x == 0) sh.n = row.V;
   __syncthreads();
 #pragma unroll 1
-  for (int w = 0; w < THREADS / 32; ++w) best = sh.scan[w] > best ? sh.scan[w] : best;
+  for (int v = threadIdx.x; v < row.blocks; v += THREADS) {
+    float x[VE];
+    row.load(v, x);
+    unsigned at = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) at |= x[i] == top ? 1u << i : 0u;
+    if (at) {
+      atomicMin(&sh.n, v * VE - row.off + __ffs(at) - 1);
+      break;   // the thread's others come later
+    }
+  }
   __syncthreads();
-  return best;
+  return sh.n;
 }
 
 template <typename T, int THREADS>
@@ -962,12 +1020,11 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
 #pragma unroll 1
   for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
     const Row<T> row(a.logits, r * a.ld, a.V);
-    const uint64_t best = first_key<T, THREADS>(sh, row);
+    const float top = row_top<T, THREADS>(sh, row);
     const float temp = a.temperature ? a.temperature[r] : 1.0f;
     const float u = a.u[r], min_p = a.min_p ? a.min_p[r] : 0.0f, top_p = a.top_p ? a.top_p[r] : 1.0f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
-    const float top = key_value(best);
-    if (best == ~0ull || best == 0 || top == INFINITY || !(u >= 0.0f && u < 1.0f) || temp != temp ||
+    if (!(top > -INFINITY && top < INFINITY) || !(u >= 0.0f && u < 1.0f) || temp != temp ||
         min_p != min_p || top_p != top_p) {
       if (tid == 0) {
         report_status(a.status, XMOD_ERR_DEVICE_CHECK);
@@ -977,8 +1034,9 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
       continue;
     }
     if (temp <= 0.0f || top_k == 1 || top_p <= 0.0f) {
+      const int token = first_token<T, THREADS>(sh, row, top);
       if (tid == 0) {
-        a.token[r] = key_token(best);
+        a.token[r] = token;
         if (a.logp) a.logp[r] = 0.0f;
       }
       continue;
