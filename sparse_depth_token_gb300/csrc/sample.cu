@@ -324,7 +324,7 @@ __device__ __noinline__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t nee
 // The key at which the running count (by_mass: mass) over the tokens of bin `bin` in their
 // order reaches `need`, and the mass up to it. `clobbered`: the bins were used for finer ones.
 template <typename T, int THREADS>
-__device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T>& row, const Scale& sc, int bin, bool by_mass,
+__device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T> row, const Scale sc, int bin, bool by_mass,
                                           uint64_t need, uint64_t* mass_to, bool* clobbered) {
   constexpr int VE = Row<T>::VE;
   uint64_t lo = 0, hi = ~0ull, before_mass = 0;
@@ -524,7 +524,7 @@ __device__ __noinline__ void count_block(Shared& sh, Scale sc, uint4 u, unsigned
 
 // Counts of the table's values and the cut by them. False: the cut lies among the smaller values.
 template <int THREADS>
-__device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16>& row, const Scale& sc, int top_k,
+__device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16> row, const Scale sc, int top_k,
                                        float top_p, bool by_k, bool by_p) {
   const int tid = threadIdx.x;
   for_blocks<__nv_bfloat16, THREADS, true>(
@@ -628,7 +628,7 @@ __device__ __noinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16>& row
 
 // The lowest key kept by top-k and top-p, of any values.
 template <typename T, int THREADS>
-__device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T>& row, const Scale& sc, int top_k, float top_p,
+__device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const Scale sc, int top_k, float top_p,
                                              bool by_k, bool by_p) {
   constexpr int VE = Row<T>::VE;
   const int tid = threadIdx.x;
@@ -763,7 +763,7 @@ __device__ __forceinline__ uint64_t key_weight(const Shared& sh, const Scale& sc
 }
 // The choice among what stays.
 template <typename T, int THREADS>
-__device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T>& row, const Scale& sc, int64_t r,
+__device__ __noinline__ void choose(const SampleArgs& a, Shared& sh, const Row<T> row, const Scale sc, int64_t r,
                                     float u, float temp) {
   constexpr int VE = Row<T>::VE, WARPS = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -945,7 +945,7 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 }
 // The row's largest logit, a NaN if it holds one. Every thread has it.
 template <typename T, int THREADS>
-__device__ __noinline__ float row_top(Shared& sh, const Row<T>& row) {
+__device__ __noinline__ float row_top(Shared& sh, const Row<T> row) {
   constexpr int VE = Row<T>::VE;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float top = -INFINITY;
@@ -983,7 +983,7 @@ __device__ __noinline__ float row_top(Shared& sh, const Row<T>& row) {
 }
 // The first token whose logit is `top`.
 template <typename T, int THREADS>
-__device__ __noinline__ int first_token(Shared& sh, const Row<T>& row, float top) {
+__device__ __noinline__ int first_token(Shared& sh, const Row<T> row, float top) {
   constexpr int VE = Row<T>::VE;
   if (threadIdx.x == 0) sh.n = row.V;
   __syncthreads();
