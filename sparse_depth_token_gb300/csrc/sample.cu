@@ -1,5 +1,14 @@
 // A token for each row of logits from a given uniform number, with temperature, top-k, top-p
 // and min-p.
+//
+// A CTA has a row: its largest logit, the counts of its values (bf16) or bins' counts and masses
+// (fp32) by atomics in shared memory, the cut that top-k, top-p and min-p make, the kept weights
+// of a slice of the row for each warp, the token in the slice that the uniform number falls in. Weights
+// and sums are whole numbers, so that a sum does not depend on its order. The row is read from
+// memory once and from L2 twice or three times. Bound by shared memory's turns (13 us of a
+// 27-us pair of bf16 rows an SM are counts and sums), by the code's way into the instruction
+// cache and by the barriers between phases, not by the reads: 4096 rows of 50257 bf16 logits with
+// top-p 503 us (816 GB/s), 256 rows of fp32 with all settings 113, eight rows of bf16 29.
 
 #include <cuda_bf16.h>
 #include <math.h>
@@ -127,7 +136,7 @@ __device__ __noinline__ uint64_t weight_of(const Shared& sh, Scale s, float x) {
   return weight_inline(sh, s, x);
 }
 
-// Elements of 16-byte block v of a row, -infinity for those outside it.
+// 16-byte blocks of a row.
 template <typename T> struct Row {
   static constexpr int VE = 16 / sizeof(T);
   const T* base;    // aligned
@@ -142,45 +151,52 @@ template <typename T> struct Row {
     first = off ? 1 : 0;
     last = (off + V) / VE;
   }
-  __device__ __forceinline__ uint4 raw(int v) const {
-    return *reinterpret_cast<const uint4*>(base + (int64_t)v * VE);
-  }
-  __device__ __forceinline__ void load(int v, float (&x)[VE]) const {
-    const int e0 = v * VE - off;   // token of the block's first element
-    if (e0 >= 0 && e0 + VE <= V) {
-      const uint4 raw = *reinterpret_cast<const uint4*>(base + (int64_t)v * VE);
-#pragma unroll
-      for (int i = 0; i < VE / 2; ++i) {
-        const float2 f = vec_pair<T>(raw, i);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-        x[i] = e0 + i >= 0 && e0 + i < V ? ld_f(base + (int64_t)v * VE + i) : -INFINITY;
-    }
-  }
 };
-
-// f(v, raw) for this thread's blocks v = from, from + STEP, .. below `to` that lie within the row
-// whole; edge(v) for those that do not (the row's first and last block at most). f's code stands
-// once and nothing is loaded ahead: several copies, or blocks that stay in registers while the rare
-// cases are called, cost more than the other warps leave of a load's wait (four blocks ahead 786 us
-// for 4096 rows of bf16 and 144 for 256 of fp32, two 712 and 159, one 577 and 121, none 562 and 124).
-template <typename T, int STEP, typename F, typename G>
-__device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, F&& f, G&& edge) {
-  int v = from;
-  if (v < row.first && v < to) {
-    edge(v);
-    v += STEP;
-  }
-  const int end = min(to, row.last);
+// A block that the row's first or last token lies in: -infinity in the others' place.
+template <typename T> __device__ __noinline__ uint4 edge_block(const T* base, int off, int V, int v) {
+  constexpr int VE = 16 / sizeof(T);
+  uint4 r = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-  for (; v < end; v += STEP) f(v, row.raw(v));
-  // the block past the last whole one, if it is this thread's
-  if (row.last < to && row.last >= from && row.last < row.blocks && row.last >= row.first && (row.last - from) % STEP == 0)
-    edge(row.last);
+  for (int i = VE - 1; i >= 0; --i) {
+    const int token = v * VE - off + i;
+    const uint32_t x = __float_as_uint(token >= 0 && token < V ? ld_f(base + (int64_t)v * VE + i) : -INFINITY);
+    if constexpr (sizeof(T) == 2)
+      r = make_uint4(r.x << 16 | x >> 16, __funnelshift_l(r.x, r.y, 16), __funnelshift_l(r.y, r.z, 16),
+                     __funnelshift_l(r.z, r.w, 16));
+    else
+      r = make_uint4(x, r.x, r.y, r.z);
+  }
+  return r;
+}
+template <typename T> __device__ __forceinline__ uint4 block_of(const Row<T>& row, int v) {
+  return v >= row.first && v < row.last ? *reinterpret_cast<const uint4*>(row.base + (int64_t)v * Row<T>::VE)
+                                        : edge_block<T>(row.base, row.off, row.V, v);
+}
+// Element i of a block.
+template <typename T> __device__ __forceinline__ float element(const uint4& u, int i) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w = i < 4 ? i < 2 ? u.x : u.y : i < 6 ? u.z : u.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  } else {
+    return __uint_as_float(i < 2 ? i == 0 ? u.x : u.y : i == 2 ? u.z : u.w);
+  }
+}
+
+// f(v, block) for this thread's blocks v = from, from + STEP, .. below `to`, the next one on its
+// way. f's code stands once, rare cases and a row's ends stand out of line: all of a row's phases
+// pass through the instruction cache once a row, so longer code costs more than it saves (four
+// copies with four loads on their way 786 us for 4096 rows of bf16, one copy 562, that without the
+// ends' and the scans' copies 509, with one load ahead 504).
+template <typename T, int STEP, typename F>
+__device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, F&& f) {
+  if (from >= to) return;
+  uint4 next = block_of(row, from);
+#pragma unroll 1
+  for (int v = from; v < to; v += STEP) {
+    const uint4 now = next;
+    if (v + STEP < to) next = block_of(row, v + STEP);
+    f(v, now);
+  }
 }
 
 __device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
@@ -190,7 +206,7 @@ template <int THREADS>
 __device__ __forceinline__ ulonglong2 block_scan2(Shared& sh, uint64_t a, uint64_t b, ulonglong2* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t ia = a, ib = b;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t ua = shfl_up64(ia, o), ub = shfl_up64(ib, o);
     if (lane >= o) {
@@ -208,7 +224,7 @@ __device__ __forceinline__ ulonglong2 block_scan2(Shared& sh, uint64_t a, uint64
   constexpr int WARPS = THREADS / 32;
   uint64_t wa = lane < WARPS ? sh.scan[lane] : 0, wb = lane < WARPS ? sh.scan2[lane] : 0;
   const uint64_t ma = wa, mb = wb;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < WARPS; o <<= 1) {
     const uint64_t ua = shfl_up64(wa, o), ub = shfl_up64(wb, o);
     if (lane >= o) {
@@ -244,23 +260,11 @@ __device__ __forceinline__ void add_mass(Shared& sh, int b, uint64_t w) {
 }
 
 template <int THREADS> __device__ __forceinline__ void clear_bins(Shared& sh) {
+#pragma unroll 1
   for (int b = threadIdx.x; b < kBins; b += THREADS) sh.mass_lo[b] = sh.mass_hi[b] = sh.count[b] = 0;
   __syncthreads();
 }
 
-// Block v with elements outside the row at -infinity, and which are inside.
-template <typename T>
-__device__ __forceinline__ unsigned block_at(const Row<T>& row, int v, float (&x)[Row<T>::VE]) {
-  constexpr int VE = Row<T>::VE;
-  row.load(v, x);
-  unsigned live = 0;
-#pragma unroll
-  for (int i = 0; i < VE; ++i) {
-    const int token = v * VE - row.off + i;
-    if (token >= 0 && token < row.V) live |= 1u << i;
-  }
-  return live;
-}
 // First bin at which the running sum of counts (by_mass: masses) reaches `need` (bin kBins: none),
 // what lies before it, and the whole sums.
 struct Crossing {
@@ -272,6 +276,7 @@ template <int THREADS>
 __device__ __forceinline__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t need) {
   constexpr int PER = kBins / THREADS;
   uint64_t c = 0, m = 0, total, total_c;
+#pragma unroll 1
   for (int i = 0; i < PER; ++i) {
     const int b = threadIdx.x * PER + i;
     c += sh.count[b];
@@ -289,6 +294,7 @@ __device__ __forceinline__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t 
   __syncthreads();
   const uint64_t before = by_mass ? mb : cb, mine = by_mass ? m : c;
   if (before < need && need <= before + mine) {
+#pragma unroll 1
     for (int i = 0; i < PER; ++i) {
       const int b = threadIdx.x * PER + i;
       const uint64_t bc = sh.count[b], bm = (uint64_t)sh.mass_hi[b] << 32 | sh.mass_lo[b];
@@ -317,25 +323,25 @@ __device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T> row, const Sc
   uint64_t lo = 0, hi = ~0ull, before_mass = 0;
   bool ranged = false;   // members are those with keys in lo .. hi, else those of the bin
   auto visit = [&](auto&& f) {
+    uint4 next = threadIdx.x < row.blocks ? block_of(row, threadIdx.x) : make_uint4(0, 0, 0, 0);
 #pragma unroll 1
     for (int v = threadIdx.x; v < row.blocks; v += THREADS) {
-      float x[VE];
-      const unsigned live = block_at<T>(row, v, x);
+      const uint4 u = next;
+      if (v + THREADS < row.blocks) next = block_of(row, v + THREADS);
       unsigned in = 0;
-#pragma unroll
+#pragma unroll (sizeof(T) == 4 ? 4 : 1)
       for (int i = 0; i < VE; ++i) {
-        const uint64_t key = key_of(x[i], v * VE - row.off + i);
+        const float x = element<T>(u, i);
+        const uint64_t key = key_of(x, v * VE - row.off + i);
         float z;
-        in |= (ranged ? key >= lo && key <= hi : min(kBins - 1, -step_of(sc, x[i], z) >> 4) == bin) ? 1u << i : 0u;
+        in |= (ranged ? key >= lo && key <= hi : min(kBins - 1, -step_of(sc, x, z) >> 4) == bin) ? 1u << i : 0u;
       }
-      // few are members
+      // few are members, and none of those outside the row
 #pragma unroll 1
-      for (in &= live; in; in &= in - 1) {
+      for (; in; in &= in - 1) {
         const int i = __ffs(in) - 1;
-        float y = x[0];
-#pragma unroll
-        for (int j = 1; j < VE; ++j) y = j == i ? x[j] : y;
-        f(key_of(y, v * VE - row.off + i), y);
+        const float x = element<T>(u, i);
+        f(key_of(x, v * VE - row.off + i), x);
       }
     }
   };
@@ -459,18 +465,6 @@ __device__ __forceinline__ unsigned half_of(const uint4& u, int i) {
   const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
   return i & 1 ? w >> 16 : w & 0xffffu;
 }
-// The same block with clamped elements, those outside the row as they are told.
-__device__ __forceinline__ unsigned clamped_bits(float x) { return __float_as_uint(fmaxf(x, -127.5f)) >> 16; }
-
-__device__ __forceinline__ uint4 packed(const float (&x)[8]) {
-  uint4 u;
-  u.x = clamped_bits(x[0]) | clamped_bits(x[1]) << 16;
-  u.y = clamped_bits(x[2]) | clamped_bits(x[3]) << 16;
-  u.z = clamped_bits(x[4]) | clamped_bits(x[5]) << 16;
-  u.w = clamped_bits(x[6]) | clamped_bits(x[7]) << 16;
-  return u;
-}
-
 // Byte offsets of the places of a word's two values in a table of entries of 2^SHIFT bytes.
 template <int SHIFT> __device__ __forceinline__ uint32_t offsets(uint32_t w) {
   return (w & 0x07ff07ffu) << SHIFT | (w >> (4 - SHIFT) & 0x08000800u << SHIFT);
@@ -479,7 +473,8 @@ template <typename E> __device__ __forceinline__ E& entry(E* table, uint32_t byt
   return *reinterpret_cast<E*>(reinterpret_cast<char*>(table) + bytes);
 }
 // The entry at `bytes` past a table's address in shared memory, 0 unless `on`. Lanes that do not
-// read cost no bank's turn: with an eighth of the values above the cut, and plain loads 818 -> 786 us for 4096 rows.
+// read cost no bank's turn: with an eighth of the values above the cut 818 -> 786 us
+// for 4096 rows.
 __device__ __forceinline__ uint64_t load_if(uint32_t table, uint32_t bytes, unsigned on) {
   uint64_t r;
   asm volatile(
@@ -506,17 +501,13 @@ __device__ __forceinline__ uint4 lowest_for(const uint4& u, unsigned beside) {
                     lowest_for(u.w, beside >> 6));
 }
 
-// Counts the clamped values u that `live` tells, in the table or beside it.
+// Counts the clamped values u that `live` tells, which lie beside the table.
 __device__ __noinline__ void count_block(Shared& sh, Scale sc, uint4 u, unsigned live) {
 #pragma unroll 1
   for (; live; live &= live - 1) {
     const unsigned bits = half_of(u, __ffs(live) - 1);
-    if (in_table(bits)) {
-      atomicAdd(&sh.count[place_of(bits)], 1u);
-    } else {
-      atomicAdd(&sh.small_n, 1u);
-      atomicAdd(&sh.small_mass, (unsigned long long)weight_of(sh, sc, __uint_as_float(bits << 16)));
-    }
+    atomicAdd(&sh.small_n, 1u);
+    atomicAdd(&sh.small_mass, (unsigned long long)weight_of(sh, sc, __uint_as_float(bits << 16)));
   }
 }
 
@@ -525,27 +516,20 @@ template <int THREADS>
 __device__ __forceinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16> row, const Scale sc, int top_k,
                                        float top_p, bool by_k, bool by_p) {
   const int tid = threadIdx.x;
-  for_blocks<__nv_bfloat16, THREADS>(
-      row, tid, row.blocks,
-      [&](int, const uint4& raw) {
-        uint4 u = clamped(raw);
-        if (!all_in_table(u)) {
-          const unsigned beside = beside_table(u);
-          count_block(sh, sc, u, beside);
-          u = lowest_for(u, beside);
-        }
+  for_blocks<__nv_bfloat16, THREADS>(row, tid, row.blocks, [&](int, const uint4& raw) {
+    uint4 u = clamped(raw);
+    if (!all_in_table(u)) {
+      const unsigned beside = beside_table(u);
+      count_block(sh, sc, u, beside);
+      u = lowest_for(u, beside);
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t at = offsets<2>((&u.x)[i]);
-          atomicAdd(&entry(sh.count, at & 0xffffu), 1u);
-          atomicAdd(&entry(sh.count, at >> 16), 1u);
-        }
-      },
-      [&](int v) {
-        float x[8];
-        const unsigned live = block_at<__nv_bfloat16>(row, v, x);
-        count_block(sh, sc, packed(x), live);
-      });
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = offsets<2>((&u.x)[i]);
+      atomicAdd(&entry(sh.count, at & 0xffffu), 1u);
+      atomicAdd(&entry(sh.count, at >> 16), 1u);
+    }
+  });
   __syncthreads();
   // running sums in rank order; the small values lie between the signs
   constexpr int PER = kBins / THREADS;
@@ -629,53 +613,42 @@ __device__ __forceinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16> r
   return true;
 }
 
-// The lowest key kept by top-k and top-p, of any values.
+// Counts and masses of a row's bins below `region`; the mass of the others is returned unless by_k
+// (what is kept then lies in the bins): small weights are summed aside, not by atomics, unless the
+// cut lies among them.
 template <typename T, int THREADS>
-__device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const Scale sc, int top_k, float top_p,
-                                             bool by_k, bool by_p) {
-  constexpr int VE = Row<T>::VE;
-  const int tid = threadIdx.x;
-  uint64_t cut = 0, rest_mass = 0;
-  // Tokens whose weights are below 2^-24 are summed aside, not by atomics, unless the cut lies
-  // among them.
-  auto fill = [&](int region) {
-    clear_bins<THREADS>(sh);
-    uint64_t mass = 0;
-    auto meet = [&](float x) {
+__device__ __noinline__ uint64_t fill_bins(Shared& sh, const Row<T> row, const Scale sc, bool by_k, bool by_p,
+                                           int region) {
+  clear_bins<THREADS>(sh);
+  uint64_t mass = 0;
+  for_blocks<T, THREADS>(row, threadIdx.x, row.blocks, [&](int, const uint4& u) {
+// fp32 comes this way alone: 122 us for 256 rows with four copies, 129 with one
+#pragma unroll (sizeof(T) == 4 ? 4 : 1)
+    for (int i = 0; i < Row<T>::VE; ++i) {
+      const float x = element<T>(u, i);
       float z;
       const int b = min(kBins - 1, -step_of(sc, x, z) >> 4);
-      const uint64_t w = by_p ? weight_inline(sh, sc, x) : 0;
+      const uint64_t w = by_p && (b < region || !by_k) ? weight_inline(sh, sc, x) : 0;
       if (b < region) {
         if (by_k) atomicAdd(&sh.count[b], 1u);
         if (w) add_mass(sh, b, w);
       } else {
         mass += w;
       }
-    };
-    for_blocks<T, THREADS>(
-        row, tid, row.blocks,
-        [&](int, const uint4& raw) {
-#pragma unroll
-          for (int i = 0; i < VE / 2; ++i) {
-            const float2 f = vec_pair<T>(raw, i);
-            meet(f.x);
-            meet(f.y);
-          }
-        },
-        [&](int v) {
-          float x[VE];
-          row.load(v, x);
-#pragma unroll 1
-          for (int i = 0; i < VE; ++i) {
-            const int token = v * VE - row.off + i;
-            if (token >= 0 && token < row.V) meet(x[i]);
-          }
-        });
-    ulonglong2 all;
-    block_scan2<THREADS>(sh, mass, 0, &all);
-    rest_mass = all.x;
-    __syncthreads();
-  };
+    }
+  });
+  ulonglong2 all;
+  block_scan2<THREADS>(sh, mass, 0, &all);
+  __syncthreads();
+  return all.x;
+}
+
+// The lowest key kept by top-k and top-p, of any values.
+template <typename T, int THREADS>
+__device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const Scale sc, int top_k, float top_p,
+                                             bool by_k, bool by_p) {
+  uint64_t cut = 0, rest_mass = 0;
+  auto fill = [&](int region) { rest_mass = fill_bins<T, THREADS>(sh, row, sc, by_k, by_p, region); };
   int region = 24 * 64;
   fill(region);
   uint64_t kept = 0;
@@ -683,9 +656,8 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const
   if (by_k) {
     uint64_t to;
     Crossing at = find_bin<THREADS>(sh, false, top_k);
-    if (at.bin == kBins) {
-      region = kBins;
-      fill(region);
+    if (at.bin == kBins && region < kBins) {
+      fill(region = kBins);
       at = find_bin<THREADS>(sh, false, top_k);
     }
     kept = at.mass;
@@ -705,8 +677,7 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const
     uint64_t to;
     Crossing at = find_bin<THREADS>(sh, true, need);
     if (at.bin == kBins && region < kBins) {
-      region = kBins;
-      fill(region);
+      fill(region = kBins);
       at = find_bin<THREADS>(sh, true, need);
     }
     const uint64_t key = find_key<T, THREADS>(sh, row, sc, at.bin, true, need - at.mass, &to, &clobbered);
@@ -715,53 +686,31 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const
   return cut;
 }
 
-// Weights of block v's tokens that are kept for sure, and how many are of the last value kept.
-// bf16 by the table: eight clamped values u, those outside the row left out by `live`.
-__device__ __forceinline__ unsigned table_weights(const Shared& sh, const Scale& sc, const Cut& cut, const uint4& u,
-                                                  unsigned live, uint64_t (&w)[8]) {
-  unsigned tied = 0;
-  if (live == 0xffu && all_in_table(u)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const unsigned place = place_of(half_of(u, i));
-      w[i] = sh.value[place];
-      tied += place == cut.place;
-    }
-    return tied;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned bits = half_of(u, i), place = place_of(bits);
-    w[i] = 0;
-    if (!(live >> i & 1)) continue;
-    if (in_table(bits)) {
-      w[i] = sh.value[place];
-      tied += place == cut.place;
-    } else if (cut.small) {
-      const uint64_t t = weight_of(sh, sc, __uint_as_float(bits << 16));
-      w[i] = t >= cut.least ? t : 0;
-    }
-  }
-  return tied;
-}
-// Their sum, one by one.
+// Weights of the clamped values u that `live` tells, which lie beside the table, summed.
 __device__ __noinline__ uint64_t sum_block(const Shared& sh, Scale sc, uint4 u, unsigned live) {
   uint64_t sum = 0;
 #pragma unroll 1
   for (; live; live &= live - 1) {
-    const unsigned bits = half_of(u, __ffs(live) - 1), place = place_of(bits);
-    if (in_table(bits)) {
-      sum += sh.value[place];
-    } else if (sh.cut.small) {
-      const uint64_t t = weight_of(sh, sc, __uint_as_float(bits << 16));
-      sum += t >= sh.cut.least ? t : 0;
-    }
+    const uint64_t t = weight_of(sh, sc, __uint_as_float(half_of(u, __ffs(live) - 1) << 16));
+    sum += t >= sh.cut.least ? t : 0;
   }
   return sum;
 }
+// Weight of a token if it stays for sure, in the general way.
 __device__ __forceinline__ uint64_t key_weight(const Shared& sh, const Scale& sc, const Cut& cut, int token, float x) {
   if (!(x > cut.x || (x == cut.x && token <= cut.token))) return 0;
   const uint64_t t = weight_inline(sh, sc, x);
+  return t >= cut.least ? t : 0;
+}
+// In any way; *tied: it is of the last value kept.
+template <typename T>
+__device__ __noinline__ uint64_t token_weight(const Shared& sh, Scale sc, int token, float x) {
+  const Cut& cut = sh.cut;
+  if (sizeof(T) != 2 || !cut.table) return key_weight(sh, sc, cut, token, x);
+  const unsigned bits = __float_as_uint(fmaxf(x, -127.5f)) >> 16;
+  if (in_table(bits)) return sh.value[place_of(bits)];   // 0 if it goes or is tied
+  if (!cut.small) return 0;
+  const uint64_t t = weight_of(sh, sc, x);
   return t >= cut.least ? t : 0;
 }
 // The choice among what stays.
@@ -775,6 +724,9 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
   const int per = (row.blocks + WARPS - 1) / WARPS;
   uint64_t sum = 0;
   unsigned tied = 0;
+  // equal to no logit without a cut by the table
+  const bool ranked = sizeof(T) == 2 && cut.table && cut.place < kBins;
+  const float cut_value = ranked ? place_value(cut.place) : __int_as_float(0x7fc00000);
   const int slice_end = min(row.blocks, (warp + 1) * per);
   if (sizeof(T) == 2 && cut.table) {
     if constexpr (sizeof(T) == 2) {
@@ -783,59 +735,29 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
       const uint32_t value = (uint32_t)__cvta_generic_to_shared(sh.value);
       const uint32_t pattern = cut_bits | cut_bits >> 16;
       unsigned ties = 0;
-      for_blocks<T, 32>(
-          row, warp * per + lane, slice_end,
-          [&](int, const uint4& raw) {
-            uint4 u = clamped(raw);
-            if (!all_in_table(u)) {
-              const unsigned beside = beside_table(u);
-              if (cut.small) sum += sum_block(sh, sc, u, beside);
-              u = lowest_for(u, beside);
-            }
+      for_blocks<T, 32>(row, warp * per + lane, slice_end, [&](int, const uint4& raw) {
+        uint4 u = clamped(raw);
+        if (!all_in_table(u)) {
+          const unsigned beside = beside_table(u);
+          if (cut.small) sum += sum_block(sh, sc, u, beside);
+          u = lowest_for(u, beside);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t w = (&u.x)[i], at = offsets<3>(w);
-              const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w);
-              const unsigned above = __hgt2_mask(x2, *reinterpret_cast<const __nv_bfloat162*>(&pattern));
-              sum += load_if(value, at & 0xffffu, above & 0xffffu) + load_if(value, at >> 16, above >> 16);
-              ties += __heq2_mask(x2, *reinterpret_cast<const __nv_bfloat162*>(&pattern)) & 0x00010001u;
-            }
-          },
-          [&](int v) {
-            float x[8];
-            const unsigned live = block_at<T>(row, v, x);
-            const uint4 u = packed(x);
-            sum += sum_block(sh, sc, u, live);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              tied += (live >> i & 1) && half_of(u, i) == (pattern & 0xffffu);
-          });
-      tied += (ties & 0xffffu) + (ties >> 16);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = (&u.x)[i], at = offsets<3>(w);
+          const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w);
+          const unsigned above = __hgt2_mask(x2, *reinterpret_cast<const __nv_bfloat162*>(&pattern));
+          sum += load_if(value, at & 0xffffu, above & 0xffffu) + load_if(value, at >> 16, above >> 16);
+          ties += __heq2_mask(x2, *reinterpret_cast<const __nv_bfloat162*>(&pattern)) & 0x00010001u;
+        }
+      });
+      tied = (ties & 0xffffu) + (ties >> 16);
     }
   } else {
-    for_blocks<T, 32>(
-        row, warp * per + lane, slice_end,
-        [&](int v, const uint4& raw) {
-          const int token0 = v * VE - row.off;
-          if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < VE; ++i) sum += key_weight(sh, sc, cut, token0 + i, __uint_as_float((&raw.x)[i]));
-          } else {
-#pragma unroll 1
-            for (int i = 0; i < VE; ++i)
-              sum += key_weight(sh, sc, cut, token0 + i, __uint_as_float(half_of(raw, i) << 16));
-          }
-        },
-        [&](int v) {
-          float x[VE];
-          block_at<T>(row, v, x);
-#pragma unroll
-          for (int i = 0; i < VE; ++i)
-            if (x[i] > -INFINITY && x[i] >= cut.x && (x[i] > cut.x || v * VE - row.off + i <= cut.token)) {
-              const uint64_t t = weight_of(sh, sc, x[i]);
-              sum += t >= cut.least ? t : 0;
-            }
-        });
+    for_blocks<T, 32>(row, warp * per + lane, slice_end, [&](int v, const uint4& u) {
+#pragma unroll (sizeof(T) == 4 ? 4 : 1)
+      for (int i = 0; i < VE; ++i) sum += key_weight(sh, sc, cut, v * VE - row.off + i, element<T>(u, i));
+    });
   }
   tied = __reduce_add_sync(0xffffffffu, tied);
 #pragma unroll
@@ -869,57 +791,40 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
 #pragma unroll 1
   for (int v0 = slice * per; v0 < min(row.blocks, (slice + 1) * per); v0 += THREADS) {
     const int v = v0 + tid;
-    uint64_t w[VE], mine = 0;
-    unsigned met = 0;
-    float x[VE];
+    // the block's weights and its tokens of the last value kept
     const bool live = v < min(row.blocks, (slice + 1) * per);
+    uint64_t sure = 0;
+    unsigned met = 0;
+    uint4 block = make_uint4(0, 0, 0, 0);
     if (live) {
-      const unsigned inside = block_at<T>(row, v, x);
-      if constexpr (sizeof(T) == 2) {
-        if (cut.table) met = table_weights(sh, sc, cut, packed(x), inside, w);
-      }
-      if (sizeof(T) != 2 || !cut.table) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          w[i] = 0;
-          if (x[i] > -INFINITY && x[i] >= cut.x && (x[i] > cut.x || v * VE - row.off + i <= cut.token)) {
-            const uint64_t t = weight_of(sh, sc, x[i]);
-            w[i] = t >= cut.least ? t : 0;
-          }
-        }
+      block = block_of(row, v);
+#pragma unroll 1
+      for (int i = 0; i < VE; ++i) {
+        const float x = element<T>(block, i);
+        sure += token_weight<T>(sh, sc, v * VE - row.off + i, x);
+        met += sizeof(T) == 2 && x == cut_value;
       }
     }
-    ulonglong2 all2;
-    if (cut.ties) {   // the block's ties that stay
-      uint64_t stay = block_scan2<THREADS>(sh, met, 0, &all2).x;
-      stay = left > stay ? left - stay : 0;
-      left = left > all2.x ? left - all2.x : 0;
-      if (live && met) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const unsigned bits = clamped_bits(x[i]);
-          if (stay && in_table(bits) && place_of(bits) == cut.place) {
-            w[i] = cut.weight;
-            --stay;
-          }
-        }
-      }
-    }
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < VE; ++i) mine += w[i];
-    }
-    const uint64_t before = block_scan2<THREADS>(sh, mine, 0, &all2).x, all = all2.x;
+    ulonglong2 all;
+    const ulonglong2 before2 = block_scan2<THREADS>(sh, sure, met, &all);
+    // the first `left` ties stay
+    const uint64_t ties_before = min((uint64_t)before2.y, left), ties_here = min((uint64_t)met, left - ties_before);
+    const uint64_t before = before2.x + ties_before * cut.weight, mine = sure + ties_here * cut.weight;
     if (before <= target && target < before + mine) {
-      uint64_t cum = before;
+      uint64_t cum = before, stay = ties_here;
       int at = -1;
       float x_at = 0.f;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        cum += w[i];
-        if (at < 0 && cum > target) {
-          at = i;
-          x_at = x[i];
+#pragma unroll 1
+      for (int i = 0; i < VE && cum <= target; ++i) {
+        x_at = element<T>(block, i);
+        at = i;
+        if (sizeof(T) == 2 && x_at == cut_value) {
+          if (stay) {
+            cum += cut.weight;
+            --stay;
+          }
+        } else {
+          cum += token_weight<T>(sh, sc, v * VE - row.off + i, x_at);
         }
       }
       a.token[r] = v * VE - row.off + at;
@@ -935,10 +840,11 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
         a.logp[r] = big + (rest2 + ((qq - n * kLn2Lo) - log1pf(f)));
       }
     }
-    if (target < all) break;
-    target -= all;
+    const uint64_t ties_all = min((uint64_t)all.y, left), whole_here = all.x + ties_all * cut.weight;
+    if (target < whole_here) break;
+    target -= whole_here;
+    left -= ties_all;
   }
-  __syncthreads();
 }
 
 // The largest of two, a NaN if one is.
@@ -950,27 +856,18 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 // The row's largest logit, a NaN if it holds one. Every thread has it.
 template <typename T, int THREADS>
 __device__ __forceinline__ float row_top(Shared& sh, const Row<T> row) {
-  constexpr int VE = Row<T>::VE;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float top = -INFINITY;
   __nv_bfloat162 top2 = __float2bfloat162_rn(-INFINITY);
-  for_blocks<T, THREADS>(
-      row, tid, row.blocks,
-      [&](int, const uint4& raw) {
-        if constexpr (sizeof(T) == 2) {
-          const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
-          top2 = __hmax2_nan(top2, __hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3])));
-        } else {
-          top = max_nan(top, max_nan(max_nan(__uint_as_float(raw.x), __uint_as_float(raw.y)),
-                                     max_nan(__uint_as_float(raw.z), __uint_as_float(raw.w))));
-        }
-      },
-      [&](int v) {
-        float x[VE];
-        row.load(v, x);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) top = max_nan(top, x[i]);
-      });
+  for_blocks<T, THREADS>(row, tid, row.blocks, [&](int, const uint4& raw) {
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
+      top2 = __hmax2_nan(top2, __hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3])));
+    } else {
+      top = max_nan(top, max_nan(max_nan(__uint_as_float(raw.x), __uint_as_float(raw.y)),
+                                 max_nan(__uint_as_float(raw.z), __uint_as_float(raw.w))));
+    }
+  });
   const float2 f = __bfloat1622float2(top2);
   top = max_nan(top, max_nan(f.x, f.y));
 #pragma unroll
@@ -993,11 +890,10 @@ __device__ __noinline__ int first_token(Shared& sh, const Row<T> row, float top)
   __syncthreads();
 #pragma unroll 1
   for (int v = threadIdx.x; v < row.blocks; v += THREADS) {
-    float x[VE];
-    row.load(v, x);
+    const uint4 u = block_of(row, v);
     unsigned at = 0;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) at |= x[i] == top ? 1u << i : 0u;
+    for (int i = 0; i < VE; ++i) at |= element<T>(u, i) == top ? 1u << i : 0u;
     if (at) {
       atomicMin(&sh.n, v * VE - row.off + __ffs(at) - 1);
       break;   // the thread's others come later
@@ -1083,6 +979,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
         if (by_k || by_p) table = table_cut<THREADS>(sh, row, sc, top_k, top_p, by_k, by_p);
         if (table && least) {
           __syncthreads();
+#pragma unroll 1
           for (int i = tid; i < kBins; i += THREADS)
             if (sh.value[i] < least) sh.value[i] = 0;
         }
