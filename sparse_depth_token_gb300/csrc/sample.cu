@@ -831,7 +831,7 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
       if (a.logp) {
         // (x - top) / temp - ln(whole 2^-unit), each with its rounding errors
         const float d = x_at - sc.top, t = d - x_at, dd = (x_at - (d - t)) + (-sc.top - t);
-        const float q = d / temp, qq = (fmaf(-q, temp, d) + dd) / temp;
+        const float q = d / temp, qq = temp < INFINITY ? (fmaf(-q, temp, d) + dd) / temp : 0.0f;
         const int e = 63 - __clzll(whole);
         const float f = (float)(whole - (1ull << e)) * __uint_as_float((unsigned)(127 - e) << 23);
         const float n = (float)(e - a.unit);
@@ -947,7 +947,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
     {   // log2(e) / temp, the division's remainder in the second part
       constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;   // log2(e)
       sc.hi = kHi / temp;
-      sc.lo = (fmaf(-sc.hi, temp, kHi) + kLo) / temp;
+      sc.lo = temp < INFINITY ? (fmaf(-sc.hi, temp, kHi) + kLo) / temp : 0.0f;
       if (!(sc.hi < 0x1p120f)) {   // any difference between logits is then beyond the last weight
         sc.hi = 0x1p120f;
         sc.lo = 0.0f;

@@ -169,6 +169,40 @@ def test_borders(X, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_infinite_temperature(X, dtype):
+    """Every logit above -infinity weighs the same, whatever the filters rank them by."""
+    V, live = 1000, 700
+    g = torch.Generator().manual_seed(31)
+    logits = (torch.randn(8, V, generator=g) * 3).cuda().to(DT[dtype])
+    logits[:, live:] = -math.inf
+    # the token is u times 700 rounded down: 0.5 and the like are exact, the others no closer than
+    # 0.3 to a border
+    u, at = f32([0.0, 0.25, 0.5, 0.75, 0.1234, 0.9, 0.999, 0.6]), [0, 175, 350, 525, 86, 629, 699, 420]
+    u[5] = 0.8995
+    u[7] = 0.6005
+    t = f32([math.inf] * 8)
+    token, logp, status = _run(X, logits, u, temperature=t)
+    assert status == X.OK and token.tolist() == at
+    assert bool(((logp + math.log(live)).abs() < 1e-6).all())
+    token, logp, status = _run(X, logits, u, temperature=t, top_k=ints([70] * 8))
+    order = torch.sort(logits.float(), dim=1, descending=True, stable=True).indices[:, :70].sort(dim=1).values
+    assert status == X.OK and token.tolist() == [int(order[i, int(float(u[i]) * 70)]) for i in range(8)]
+    assert bool(((logp + math.log(70)).abs() < 1e-6).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_largest_vocabulary(X, dtype):
+    V = X.MAX_VOCAB
+    g = torch.Generator(device="cuda").manual_seed(8)
+    logits = (torch.randn(3, V + 3, generator=g, device="cuda") * 2.5).to(DT[dtype])[:, 1: V + 1]
+    u = f32([0.3, 0.71, 0.999])
+    for kw in (dict(), dict(top_p=f32([0.9, 0.5, 0.99])), dict(top_k=ints([50, 100000, 3])),
+               dict(temperature=f32([1.7, 0.0, 0.6]), min_p=f32([1e-6, 0.1, 1e-3]))):
+        # 2^22 borders lie 2^-22 apart, so that one row in 128 has its u within 2^-30 of one
+        _check(X, logits, u, skip_close=True, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_temperature_zero_is_the_first_largest(X, dtype):
     logits = torch.zeros(3, 50, device="cuda", dtype=DT[dtype])
     logits[0, 7] = logits[0, 30] = 2.0
