@@ -504,7 +504,8 @@ XMOD_API size_t xmod_cache_attention_chunk_workspace_bytes(const xmod_dims* dims
  * sequence, the row before it to one less, and so on:
  *   o[m, h] = sum_i p_i V[i, g],  p = softmax over i < lim(m) of q[m, h] . K[i, g] / sqrt(head_dim)
  *   lim(m) = len[c] - (start[c + 1] - 1 - m),  g = h / (n_heads / n_kv_heads)
- *   M       rows of q, o and lse; those of no chunk keep their values in o and lse
+ *   M       rows of q, o and lse, at most XMOD_MAX_CHUNK_ROWS; those of no chunk keep their
+ *           values in o and lse
  *   q       [M, n_heads * head_dim], row stride ldq (dtype): rotated queries
  *   start   [n_chunks + 1] int32, not descending, within 0 .. M; a chunk may be empty
  *   seq     [n_chunks] int32, or NULL (chunk c reads sequence c). A negative entry skips its
@@ -525,6 +526,8 @@ XMOD_API size_t xmod_cache_attention_chunk_workspace_bytes(const xmod_dims* dims
  *   ws      xmod_cache_attention_chunk_workspace_bytes(dims, n_chunks, M) bytes; concurrent
  *           calls need one each. head_dim must be 32, 64 or 128. M = 0 or n_chunks = 0 does
  *           nothing. */
+#define XMOD_MAX_CHUNK_ROWS (1 << 30)
+
 XMOD_API int xmod_cache_attention_chunk(const xmod_dims* dims, const xmod_kv_cache* cache,
                                         int n_chunks, int M, const void* q, int ldq,
                                         const int32_t* start, const int32_t* seq,
@@ -667,7 +670,9 @@ XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const v
  * Weights are integers in units of at most 2^-39 (2^(bits of V) - 62), computed to a relative
  * error of 2^-32, and sums are exact: the choice depends on neither order nor launch, and
  * differs from the real numbers' only where u, top_p or min_p lies that close to a border.
- * Weights below the unit count as 0.
+ * Weights below the unit count as 0. T may be infinite (every logit above -infinity has the
+ * weight 1); a positive T below 1.1e-36 counts as that. A difference of logits beyond fp32's
+ * range counts as infinite.
  * Checked on the device and reported through status_out (a device int, or NULL; see
  * xmod_gather): a row that holds a NaN or +infinity, or nothing above -infinity, has no
  * distribution: token -1 and logp NaN; so does a row whose u, temperature, top_p or min_p is

@@ -122,6 +122,7 @@ int xmod_cache_attention_chunk(const xmod_dims* dm, const xmod_kv_cache* cache, 
   const int st = cache_status(dm, cache);
   if (st) return st;
   if (n_chunks < 0 || M < 0) return XMOD_ERR_INVALID_ARG;
+  if (M > XMOD_MAX_CHUNK_ROWS) return XMOD_ERR_UNSUPPORTED;
   if (n_chunks == 0 || M == 0) return XMOD_OK;
   const int qw = dm->n_heads * dm->head_dim;
   if (!ptr16(q) || ldq < qw || ldq % 8 || !start || !ptr4_or_null(start) || !ptr4_or_null(seq) || !len ||

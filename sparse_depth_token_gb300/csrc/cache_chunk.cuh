@@ -141,7 +141,8 @@ struct ChunkPlan {
   long long begin, end;       // this CTA's range
   long long each, tiles;      // of a CTA; of a KV head and pass of the chunk it begins in
   long long off;
-  unsigned long long found;
+  long long found_cost;
+  int found;                  // the last segment known to begin at or before the range, and the cost before it
   Chunk k;
   int more, chunk, hp, t, at;   // where the range begins: chunk, KV head and pass, segment, position in it
 };
@@ -198,6 +199,7 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
     plan->each = length;
     plan->more = more;
     plan->found = 0;
+    plan->found_cost = 0;
   }
   if (begin < end && begin >= before && begin < before + mine) {
     long long at = before;
@@ -230,20 +232,23 @@ __device__ __forceinline__ void make_chunk_plan(const ChunkArgs& a, ChunkPlan* p
   int lo = 0, hi = segments;   // within lo .. hi - 1
 #pragma unroll 1
   while (hi - lo > 1) {
-    const int step = (hi - lo + nthreads - 1) / nthreads, t = lo + tid * step;
+    const int step = (hi - lo - 1) / nthreads + 1;
+    const long long t = lo + (long long)tid * step;
+    long long n = 0;
     if (t < hi) {
-      const long long n = cost_before(a, k, segments, t);
-      if (n <= rem) atomicMax(&plan->found, (unsigned long long)t << 40 | (unsigned long long)n);
+      n = cost_before(a, k, segments, (int)t);
+      if (n <= rem) atomicMax(&plan->found, (int)t);
     }
     __syncthreads();
-    lo = (int)(plan->found >> 40);
+    lo = plan->found;
+    if (t == lo) plan->found_cost = n;
     hi = min(hi, lo + step);
     __syncthreads();
   }
   if (tid == 0) {
     plan->t = lo;
     plan->hp = hp;
-    plan->at = (int)(rem - (long long)(plan->found & 0xffffffffffull));
+    plan->at = (int)(rem - plan->found_cost);
   }
   __syncthreads();
 }

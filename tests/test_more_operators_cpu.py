@@ -48,6 +48,7 @@ def test_chunk_arguments():
     need = X.cache_attention_chunk_workspace_bytes(_dims(), 2, 3)
     assert need > 0 and _chunk(ws_bytes=need - 1) == X.ERR_WORKSPACE
     assert _chunk(n=0) == X.OK and _chunk(M=0) == X.OK
+    assert _chunk(M=(1 << 30) + 1) == X.ERR_UNSUPPORTED      # a segment's last token fits 32 bits
     for args in ((_dims(n_kv_heads=3), 2, 3), (_dims(), -1, 3), (_dims(), 2, -1), (_dims(head_dim=96), 2, 3)):
         assert X.cache_attention_chunk_workspace_bytes(*args) == 0
 
