@@ -14,7 +14,7 @@
 //   warps 4..7    softmax of A, a row a thread: scores from tensor memory, running maximum and
 //   warps 8..11   sum, P back over the scores as bf16; the same for B
 //   warps 12..15  (e4m3) codes to bf16, exactly
-// The running maximum only moves when it grows by more than 2^8 (weights stay below 256 and
+// The reference of the weights, a maximum, only moves when it grows by more than 2^8 (weights stay below 256 and
 // keep their relative rounding in bf16); O is then rescaled in tensor memory.
 //
 // V is used as the cache stores it, [slot, dimension], as an MN-major operand: nothing is
@@ -527,9 +527,24 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           for (int i = 3; i < 15; i += 2) t = max3(t, u[i], u[i + 1]);
           mc[r] = fmaxf(t, u[15]);
         }
-        const float m_cand = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]) * scale_log2;
+        const float top = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]), m_cand = top * scale_log2;
         const bool grow = m_cand > m + kRescale;
-        const float m_new = grow ? m_cand : m;
+        float m_new = grow ? m_cand : m;
+        if constexpr (FP8) {
+          // the largest weight, times its value's scale, becomes a power of two, which bf16 holds (without
+          // this a row of one or two keys is off by two roundings that every dimension shares: 1.9
+          // times the error of exact weights)
+          if (__any_sync(0xffffffffu, grow)) {
+            float s = 1.0f;
+#pragma unroll
+            for (int i = 0; i < KB; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + KB + i);
+              s = v[i] == top ? f.x : v[i + 1] == top ? f.y : v[i + 2] == top ? f.z : v[i + 3] == top ? f.w : s;
+            }
+            // any shift will do: it cancels from the sums
+            if (grow) m_new += log2f(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u));
+          }
+        }
         const float alpha = grow ? exp2f(m - m_new) : 1.0f;
         if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
           // O holds the tiles before: the last of their products has to have landed
