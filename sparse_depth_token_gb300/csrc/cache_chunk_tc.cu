@@ -164,6 +164,27 @@ __device__ __forceinline__ void codes_bf16(const uint4& u, uint4& lo, uint4& hi)
   hi = make_uint4(codes2_bf16(u.z & 0xffffu), codes2_bf16(u.z >> 16), codes2_bf16(u.w & 0xffffu), codes2_bf16(u.w >> 16));
 }
 
+// log2 of the significand of the value's scale that belongs to the largest of a row's scores (in
+// tensor memory; sc: the keys' scales, then the values'; those below `seen`).
+__device__ __noinline__ float scale_shift(uint32_t scores, const float* sc, int seen) {
+  float top = -INFINITY, s = 1.0f;
+#pragma unroll 1
+  for (int c = 0; c < KB; c += 32) {
+    float v[32];
+    tmem_ld32(scores + c, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float x = v[i] * sc[c + i];
+      if (c + i < seen && x > top) {
+        top = x;
+        s = sc[KB + c + i];
+      }
+    }
+  }
+  return log2f(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u));
+}
+
 template <int HD, bool FP8>
 __global__ void __launch_bounds__((Tc<HD, FP8>::THREADS), 1)
 cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
@@ -527,7 +548,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           for (int i = 3; i < 15; i += 2) t = max3(t, u[i], u[i + 1]);
           mc[r] = fmaxf(t, u[15]);
         }
-        const float top = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]), m_cand = top * scale_log2;
+        const float m_cand = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]) * scale_log2;
         const bool grow = m_cand > m + kRescale;
         float m_new = grow ? m_cand : m;
         if constexpr (FP8) {
@@ -535,14 +556,8 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           // this a row of one or two keys is off by two roundings that every dimension shares: 1.9
           // times the error of exact weights)
           if (__any_sync(0xffffffffu, grow)) {
-            float s = 1.0f;
-#pragma unroll
-            for (int i = 0; i < KB; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + KB + i);
-              s = v[i] == top ? f.x : v[i + 1] == top ? f.y : v[i + 2] == top ? f.z : v[i + 3] == top ? f.w : s;
-            }
-            // any shift will do: it cancels from the sums
-            if (grow) m_new += log2f(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u));
+            const float shift = scale_shift(tS + b * KB, sc, seen);
+            if (grow) m_new += shift;   // any would do: it cancels from the sums
           }
         }
         const float alpha = grow ? exp2f(m - m_new) : 1.0f;
