@@ -5,10 +5,11 @@
 // (fp32) by atomics in shared memory, the cut that top-k, top-p and min-p make, the kept weights
 // of a slice of the row for each warp, the token in the slice that the uniform number falls in. Weights
 // and sums are whole numbers, so that a sum does not depend on its order. The row is read from
-// memory once and from L2 twice or three times. Bound by shared memory's turns (13 us of a
-// 27-us pair of bf16 rows an SM are counts and sums), by the code's way into the instruction
-// cache and by the barriers between phases, not by the reads: 4096 rows of 50257 bf16 logits with
-// top-p 503 us (816 GB/s), 256 rows of fp32 with all settings 113, eight rows of bf16 29.
+// memory once and from L2 twice or three times. Bound by issue (bf16: 80 thousand instructions a
+// row, of all its warps, half of them the counts' and the slices' loops), shared memory's turns, the
+// code's way into the instruction cache and the barriers between phases, not by the reads: 4096
+// rows of 50257 bf16 logits with top-p 434 us (947 GB/s), 256 rows of fp32 with all settings 111,
+// eight rows of bf16 23.
 
 #include <cuda_bf16.h>
 #include <math.h>
@@ -472,17 +473,18 @@ template <int SHIFT> __device__ __forceinline__ uint32_t offsets(uint32_t w) {
 template <typename E> __device__ __forceinline__ E& entry(E* table, uint32_t bytes) {
   return *reinterpret_cast<E*>(reinterpret_cast<char*>(table) + bytes);
 }
-// The entry at `bytes` past a table's address in shared memory, 0 unless `on`. Lanes that do not
-// read cost no bank's turn: with an eighth of the values above the cut 818 -> 786 us
-// for 4096 rows.
-__device__ __forceinline__ uint64_t load_if(uint32_t table, uint32_t bytes, unsigned on) {
-  uint64_t r;
+// Sum of the entries at two byte offsets past a table's address in shared memory, each if its half
+// of x (bf16) is above that of cut. Lanes that do not read cost no bank's turn: with an eighth of
+// the values above the cut 818 -> 786 us for 4096 rows.
+__device__ __forceinline__ uint64_t sum_above(uint32_t table, uint32_t offsets, uint32_t x, uint32_t cut) {
+  uint64_t a, b;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b64 %0, 0;\n\t@p ld.shared.b64 %0, [%1];\n\t}"
-      : "=l"(r)
-      : "r"(table + bytes), "r"(on)
+      "{\n\t.reg .pred p, q;\n\tsetp.gt.bf16x2 p|q, %4, %5;\n\tmov.b64 %0, 0;\n\tmov.b64 %1, 0;\n\t"
+      "@p ld.shared.b64 %0, [%2];\n\t@q ld.shared.b64 %1, [%3];\n\t}"
+      : "=&l"(a), "=&l"(b)
+      : "r"(table + (offsets & 0xffffu)), "r"(table + (offsets >> 16)), "r"(x), "r"(cut)
       : "memory");
-  return r;
+  return a + b;
 }
 // The values beside the table, a bit each, and the block with the lowest value in their place: its
 // weight is 0 and it ranks last, so that it may be counted without harm.
@@ -736,18 +738,20 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
       const uint32_t pattern = cut_bits | cut_bits >> 16;
       unsigned ties = 0;
       for_blocks<T, 32>(row, warp * per + lane, slice_end, [&](int, const uint4& raw) {
-        uint4 u = clamped(raw);
-        if (!all_in_table(u)) {
-          const unsigned beside = beside_table(u);
-          if (cut.small) sum += sum_block(sh, sc, u, beside);
-          u = lowest_for(u, beside);
+        uint4 u = raw;
+        if (cut.small) {   // else nothing outside the table is above the cut or equal to it
+          u = clamped(raw);
+          if (!all_in_table(u)) {
+            const unsigned beside = beside_table(u);
+            sum += sum_block(sh, sc, u, beside);
+            u = lowest_for(u, beside);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = (&u.x)[i], at = offsets<3>(w);
           const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w);
-          const unsigned above = __hgt2_mask(x2, *reinterpret_cast<const __nv_bfloat162*>(&pattern));
-          sum += load_if(value, at & 0xffffu, above & 0xffffu) + load_if(value, at >> 16, above >> 16);
+          sum += sum_above(value, at, w, pattern);
           ties += __heq2_mask(x2, *reinterpret_cast<const __nv_bfloat162*>(&pattern)) & 0x00010001u;
         }
       });
@@ -768,24 +772,29 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
     sh.scan2[warp] = tied;
   }
   __syncthreads();
-  uint64_t whole = 0, left = cut.ties;   // ties not yet met
+  // a lane a slice: the ties before it, what is kept of it, and up to it
+  const unsigned ties_all = (unsigned)cut.ties, here = lane < WARPS ? (unsigned)sh.scan2[lane] : 0u;
+  unsigned met_before = here;
 #pragma unroll 1
-  for (int w = 0; w < WARPS; ++w) {
-    const uint64_t t = min(left, sh.scan2[w]);
-    whole += sh.scan[w] + t * cut.weight;
-    left -= t;
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const unsigned up = __shfl_up_sync(0xffffffffu, met_before, o);
+    if (lane >= o) met_before += up;
   }
+  met_before -= here;
+  const uint64_t mass =
+      (lane < WARPS ? sh.scan[lane] : 0) + min(here, ties_all - min(ties_all, met_before)) * cut.weight;
+  uint64_t upto = mass;
+#pragma unroll 1
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const uint64_t up = shfl_up64(upto, o);
+    if (lane >= o) upto += up;
+  }
+  const uint64_t whole = __shfl_sync(0xffffffffu, upto, WARPS - 1);
   bool rest;
-  uint64_t target = scaled(u, whole, &rest);   // the running sum has to exceed it
-  int slice = 0;
-  left = cut.ties;
-#pragma unroll 1
-  for (; slice < WARPS - 1; ++slice) {
-    const uint64_t t = min(left, sh.scan2[slice]), mass = sh.scan[slice] + t * cut.weight;
-    if (target < mass) break;
-    target -= mass;
-    left -= t;
-  }
+  uint64_t target = scaled(u, whole, &rest);   // the running sum has to exceed it, as the whole does
+  const int slice = min(__ffs(__ballot_sync(0xffffffffu, target < upto)) - 1, WARPS - 1);
+  target -= __shfl_sync(0xffffffffu, upto - mass, slice);
+  uint64_t left = ties_all - min(ties_all, __shfl_sync(0xffffffffu, met_before, slice));   // ties not yet met
   __syncthreads();
   // ---- the token within the slice, a block a thread
 #pragma unroll 1
@@ -840,10 +849,10 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
         a.logp[r] = big + (rest2 + ((qq - n * kLn2Lo) - log1pf(f)));
       }
     }
-    const uint64_t ties_all = min((uint64_t)all.y, left), whole_here = all.x + ties_all * cut.weight;
+    const uint64_t ties_here_all = min((uint64_t)all.y, left), whole_here = all.x + ties_here_all * cut.weight;
     if (target < whole_here) break;
     target -= whole_here;
-    left -= ties_all;
+    left -= ties_here_all;
   }
 }
 
