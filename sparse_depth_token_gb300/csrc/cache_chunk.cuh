@@ -46,7 +46,7 @@ struct ChunkArgs {
   int group;              // query heads of a KV head
   int hpt, tpt, passes;   // heads and tokens of a segment, passes over a KV head's query heads
   int block_tokens;       // tokens of a block of rows
-  int lead;               // what a segment costs beside its tiles, in tiles
+  int lead;               // what a segment costs beside its tiles, in tiles (six prompts with 0: 1291 us, with 4: 993)
   int hpt_inverse;        // ceil(2^16 / hpt): r / hpt for r, hpt <= 256 (their product is below 2^16)
   int page_shift;         // log2 of the page size, -1: not a power of two
   int box;                // rows of a TMA box: divides the page size and a tile

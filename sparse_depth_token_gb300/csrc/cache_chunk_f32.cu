@@ -1,4 +1,7 @@
-// Attention of a chunk of new tokens over the paged cache on FFMA: fp32 throughout.
+// Attention of a chunk of new tokens over the paged cache on FFMA: fp32 throughout (tf32 would keep
+// ten bits of q, K and the weights). Bound: FFMA, of which 64 x 64 tiles reach 36 TFLOP/s (500
+// tokens at 8192 of 16 and 4 heads of 128 910 us, eight chunks of 512 at 4096 of 64 889); small calls
+// by the latency of one to three tiles a CTA and the join (six of 100 at 1000 35 us).
 
 #include <math.h>
 

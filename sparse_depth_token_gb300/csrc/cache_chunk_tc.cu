@@ -23,6 +23,12 @@
 // only in part, the softmax warps look at V first: slots past the segment's end become zeros;
 // and if another slot that some row does not see holds such a value, those values are added by
 // hand to the rows that see them and then replaced by zeros.
+//
+// Bound by the tensor pipe and its issue beside the softmax warps: 500 tokens at 131072 of 16
+// and 4 heads of 128 384 us (1.39 PFLOP/s, 0.73 of the measured burst), six prompts of up to
+// 8192 tokens 990 us (1.36; a segment's start and end cost about four of its tiles). Over e4m3
+// by issue: 16 ragged chunks at up to 16384 238 us (0.68 PFLOP/s). Small calls by latency: eight
+// chunks of 4 tokens over 4096 29 us with the join, whose plan takes 3.
 
 #include <cuda.h>
 #include <cuda_fp16.h>

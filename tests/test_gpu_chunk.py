@@ -114,6 +114,20 @@ def test_matches_the_plain_form(X, kind, hq, hkv, hd, shape):
     _check(s)
 
 
+def test_one_key_over_e4m3_is_its_value(X):
+    """The largest weight times its value's scale is a power of two, which bf16 holds: what is left
+    of a single key are the output's rounding and the exponent's (log2, ex2 and a product, each
+    within 2^-21)."""
+    for hq, hkv, hd in HEADS:
+        s = _setup(X, "e4m3", hq, hkv, hd, 16, [(1, 1)] * 40, seed=hd + hq)
+        _call(s)
+        for i in range(40):
+            at = s["first"][i]
+            ref, _, bound, _ = R.chunk_ref(s["c"], s["q"][at: at + 1].reshape(1, hq, hd), i, 1, 3 * 2.0 ** -21)
+            err = (s["o"][at].view(1, hq, hd).double() - ref).abs() - bound - C.HALF["bf16"] * (ref.abs() + bound)
+            assert float(err.max()) <= 0, (hq, hd, i, float(err.max()))
+
+
 @pytest.mark.parametrize("kind", sorted(KINDS))
 def test_wide_groups(X, kind):
     """More query heads on a KV head than a tile has rows."""
