@@ -365,6 +365,29 @@ def test_captured_and_on_streams(X, kind):
         assert torch.equal(s["o"], o)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_small_heads_at_once(X, kind):
+    """Calls on two streams whose CTAs fit an SM together but for the tensor memory, which one
+    waits for until the other is done: the same bits as alone."""
+    sets = [_setup(X, kind, 12, 4, 32, 16, shape, seed=i) for i, shape in
+            enumerate([[(300, 2000), (9, 60)], [(200, 3000)]])]
+    alone = []
+    for s in sets:
+        _call(s)
+        alone.append(s["o"].clone())
+        s["o"].fill_(-3.0)
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                _call(s)
+    torch.cuda.synchronize()
+    for s, o in zip(sets, alone):
+        _check(s)
+        assert torch.equal(s["o"], o)
+
+
 def test_binding_refusals(X):
     s = _setup(X, "bf16", 4, 2, 64, 16, [(3, 5), (2, 9)])
     bad = [dict(q=s["q"].float()), dict(q=s["q"][:, :-8]), dict(q=s["q"].cpu()), dict(start=s["start"][:-1]),
