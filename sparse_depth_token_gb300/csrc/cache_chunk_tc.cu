@@ -231,7 +231,6 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(FULL + 8 * i, FP8 ? 128 : 1);
@@ -267,6 +266,9 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;   // S of A, S of B (two buffers each), O of A, O of B
+  // Not before the allocation: a successor that got the columns which a CTA of this grid waits for
+  // would hold them while it waits for this grid to end.
+  pdl_trigger();
   pdl_wait();
   make_chunk_plan(a, plan, scratch);
   if (tid == 0) a.join[blockIdx.x].first = -1;
