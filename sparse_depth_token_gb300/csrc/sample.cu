@@ -240,7 +240,7 @@ __device__ __forceinline__ ulonglong2 block_scan2(Shared& sh, uint64_t a, uint64
 
 // f * w rounded down for f >= 0, and whether something was cut off.
 __device__ __forceinline__ uint64_t scaled(float f, uint64_t w, bool* cut) {
-  const uint32_t b = __float_as_uint(f);
+  const uint32_t b = __float_as_uint(f) & 0x7fffffffu;   // -0 is 0
   const int ex = (int)(b >> 23);
   const uint64_t m = (b & 0x7fffffu) | (ex ? 0x800000u : 0u);
   const int right = 150 - (ex ? ex : 1);   // f = m 2^-right, right >= 24 below 1
