@@ -930,7 +930,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
   for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
     const Row<T> row(a.logits, r * a.ld, a.V);
     const float top = row_top<T, THREADS>(sh, row);
-    const float temp = a.temperature ? a.temperature[r] : 1.0f;
+    float temp = a.temperature ? a.temperature[r] : 1.0f;
     const float u = a.u[r], min_p = a.min_p ? a.min_p[r] : 0.0f, top_p = a.top_p ? a.top_p[r] : 1.0f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
     if (!(top > -INFINITY && top < INFINITY) || !(u >= 0.0f && u < 1.0f) || temp != temp ||
@@ -955,12 +955,9 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
     sc.unit = a.unit;
     {   // log2(e) / temp, the division's remainder in the second part
       constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;   // log2(e)
+      temp = fmaxf(temp, kHi * 0x1p-120f);   // below it sc.hi would pass fp32's range
       sc.hi = kHi / temp;
       sc.lo = temp < INFINITY ? (fmaf(-sc.hi, temp, kHi) + kLo) / temp : 0.0f;
-      if (!(sc.hi < 0x1p120f)) {   // any difference between logits is then beyond the last weight
-        sc.hi = 0x1p120f;
-        sc.lo = 0.0f;
-      }
     }
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.0f;
     uint64_t least = 0;

@@ -35,3 +35,25 @@ def test_negative_zeros(X, dtype, V):
         a, b = _run(X, logits, none + 0.4, **{name: none}), _run(X, logits, none + 0.4, **{name: -none})
         assert a[2] == b[2] == X.OK
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("t", [1e-45, 1e-38, 1.0e-36, 2.0e-36])
+def test_log_probability_at_tiny_temperatures(X, t):
+    """Logits 1e-36 apart: a temperature below 2^-120 log2(e) counts as that, for the choice and for
+    its log probability."""
+    least = float(f32([1.44269502])) * 2.0 ** -120
+    logits = torch.full((64, 300), -1.0, device="cuda")
+    logits[:, 3], logits[:, 7], logits[:, 200] = -1e-36, 0.0, -4e-37
+    u = (torch.arange(64, device="cuda") + 0.5) / 64
+    # 64-bit: the three weights of tokens 3, 7 and 200
+    x = logits[0, [3, 7, 200]].double()
+    p = torch.softmax(x / max(float(f32([t])), least), 0)
+    ends = p.cumsum(0)
+    assert float((u.double()[:, None] - ends[None, :2]).abs().min()) > 1e-4
+    want = (u.double()[:, None] > ends[None, :2]).sum(1)
+    token, logp, status = _run(X, logits, u, temperature=f32([t] * 64))
+    assert status == X.OK
+    assert token.tolist() == [[3, 7, 200][int(i)] for i in want]
+    lp = p.log()[want]
+    # the sum's error and fp32's of the difference over the temperature
+    assert bool(((logp.double() - lp).abs() <= 2.0 ** -22 * lp.abs() + 3e-7).all())
