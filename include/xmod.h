@@ -667,12 +667,13 @@ XMOD_API int xmod_token_logprobs_bwd(xmod_dtype dtype, int64_t N, int V, const v
  *   token   [N] int32
  *   logp    [N] fp32: ln of the probability with which the token was chosen, w_token over the
  *           kept weights' sum; or NULL
- * Weights are integers in units of at most 2^-39 (2^(bits of V) - 62), computed to a relative
- * error of 2^-32, and sums are exact: the choice depends on neither order nor launch, and
- * differs from the real numbers' only where u, top_p or min_p lies that close to a border.
- * Weights below the unit count as 0. T may be infinite (every logit above -infinity has the
- * weight 1); a positive T below 1.0854e-36 (2^-120 log2(e)) counts as that, for the choice and
- * for logp. A difference of logits beyond fp32's range counts as infinite.
+ * Weights are integers in units of 2^-62, computed to a relative error of 2^-32 (at temperatures
+ * above 1e33 of 2^-22) and rounded down, and their sums are exact: the choice depends on neither
+ * order nor launch, and differs from the real numbers' only where u or top_p lies within twice
+ * that error of a border, relative to the sums compared, or min_p within it of a weight, relative
+ * to that, and 2^-62 more. Weights below the unit count as 0. T may be infinite (every logit above
+ * -infinity has the weight 1); a positive T below 1.0854e-36 (2^-120 log2(e)) counts as that, for
+ * the choice and for logp. A difference of logits beyond fp32's range counts as infinite.
  * Checked on the device and reported through status_out (a device int, or NULL; see
  * xmod_gather): a row that holds a NaN or +infinity, or nothing above -infinity, has no
  * distribution: token -1 and logp NaN; so does a row whose u, temperature, top_p or min_p is

@@ -4,12 +4,14 @@
 // A CTA has a row: its largest logit, the counts of its values (bf16) or bins' counts and masses
 // (fp32) by atomics in shared memory, the cut that top-k, top-p and min-p make, the kept weights
 // of a slice of the row for each warp, the token in the slice that the uniform number falls in. Weights
-// and sums are whole numbers, so that a sum does not depend on its order. The row is read from
+// and sums are whole numbers, so that a sum does not depend on its order; weights have units of
+// 2^-62 of the largest and sums 96 bits (in 64 bits, with units that leave room for V weights, 4096 rows
+// take 434 us, but 2^22 logits 27 below one were off by 2^-19 of the row's sum). The row is read from
 // memory once and from L2 twice or three times. Bound by issue (bf16: 80 thousand instructions a
 // row, of all its warps, half of them the counts' and the slices' loops), shared memory's turns, the
 // code's way into the instruction cache and the barriers between phases, not by the reads: 4096
-// rows of 50257 bf16 logits with top-p 434 us (947 GB/s), 256 rows of fp32 with all settings 111,
-// eight rows of bf16 23.
+// rows of 50257 bf16 logits with top-p 445 us (924 GB/s), 256 rows of fp32 with all settings 114,
+// eight rows of bf16 24.
 
 #include <cuda_bf16.h>
 #include <math.h>
@@ -40,8 +42,13 @@ const PowerTables& power_tables() {
   return tables;
 }
 
+// Weights are whole numbers in units of 2^-62, the largest 2^62; sums of up to 2^22 of them have 96 bits.
+constexpr int kUnit = 62;
+using wide = unsigned __int128;
+static_assert(kUnit + 22 < 96 && XMOD_MAX_VOCAB <= 1 << 22, "");
+
 struct SampleArgs {
-  int V, unit;     // weights in units of 2^-unit
+  int V;
   int64_t N, ld;
   const void* logits;
   const float *temperature, *top_p, *min_p, *u;
@@ -66,12 +73,19 @@ struct Cut {
   int token;
 };
 
+// The slice that the token lies in: what is left of the target and of the ties there, the kept sum.
+struct Choice {
+  uint64_t target_lo, target_hi, whole_lo, whole_hi;
+  unsigned left;
+  int slice;
+};
+
 struct Shared {
-  uint64_t power[1024];     // 2^(i / 1024) in units of 2^-unit, less kRound's bits
+  uint64_t power[1024];     // 2^(i / 1024) in units of 2^-62, less kRound's bits
   float powerf[1024];       // the same times 2^32
   union {
     struct {
-      unsigned mass_lo[kBins], mass_hi[kBins];
+      unsigned mass_lo[kBins], mass_hi[kBins], mass_top[kBins];
     };
     uint64_t value[kBins];  // weights of bf16 values
   };
@@ -79,10 +93,11 @@ struct Shared {
   uint64_t key[kList], weight[kList];
   uint64_t scan[33], scan2[33];
   uint64_t found[4];
-  unsigned long long small_mass;
+  unsigned long long small_lo, small_hi;   // their mass: small_lo + small_hi 2^32
   unsigned small_n;
   int n;
   Cut cut;
+  Choice choice;
 };
 
 // Order of a logit as an unsigned number (larger value, larger number; -0 equals +0), above
@@ -100,7 +115,6 @@ __device__ __forceinline__ int key_token(uint64_t key) { return (int)(0xffffffff
 // A row's scale: weights are 2^((x - top) c), c = log2(e) / T in two parts.
 struct Scale {
   float top, hi, lo;
-  int unit;
 };
 
 // Where the weight of x lies on a grid of 1/1024 in log2 (0 at the top, descending with x), and
@@ -119,7 +133,7 @@ __device__ __forceinline__ int step_of(const Scale& s, float x, float& z) {
   return p > -63.0f ? __float_as_int(n) - __float_as_int(kMagic) : kNone;   // -infinity too
 }
 
-// Weight in units of 2^-unit: the table's entry for the grid point and a second-order series
+// Weight in units of 2^-62: the table's entry for the grid point and a second-order series
 // of what is left (at most 2^-11: the next term is below 2^-37), rounded to 2^-32 by adding
 // kRound, whose bits the table's entry has less.
 constexpr float kRound = 12582912.0f;
@@ -129,7 +143,7 @@ __device__ __forceinline__ uint64_t weight_inline(const Shared& sh, const Scale&
   const int j = step & 1023, shift = -(step >> 10);   // 63 at most, or none
   const float q = z * fmaf(z, 0.24022651f, 0.69314718f);
   const int corr = __float_as_int(fmaf(sh.powerf[j], q, kRound));
-  const int64_t w = (int64_t)sh.power[j] + (int64_t)corr * (1ll << (s.unit - 32));
+  const int64_t w = (int64_t)sh.power[j] + (int64_t)corr * (1ll << (kUnit - 32));
   return step == kNone ? 0 : (uint64_t)w >> shift;
 }
 
@@ -200,69 +214,101 @@ __device__ __forceinline__ void for_blocks(const Row<T>& row, int from, int to, 
   }
 }
 
-__device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
+// Sums of weights. A count of tokens rides in the top 32 bits where both are summed.
+struct Sum96 {
+  uint64_t lo;
+  uint32_t hi;
+  __device__ __forceinline__ void add(uint64_t w) {
+    asm("add.cc.u64 %0, %0, %2;\n\taddc.u32 %1, %1, 0;" : "+l"(lo), "+r"(hi) : "l"(w));
+  }
+  __device__ __forceinline__ wide get() const { return (wide)hi << 64 | lo; }
+};
+__device__ __forceinline__ wide times(uint64_t w, uint32_t n) {   // w below 2^64, n any
+  return ((wide)((w >> 32) * n) << 32) + (uint64_t)(uint32_t)w * n;
+}
+__device__ __forceinline__ wide with_count(uint32_t count, wide mass) { return (wide)count << 96 | mass; }
+__device__ __forceinline__ uint32_t count_in(wide v) { return (uint32_t)(v >> 96); }
+__device__ __forceinline__ wide mass_in(wide v) { return v & (((wide)1 << 96) - 1); }
 
-// Sums over the CTA of each thread's a and b before it; *total the whole sums.
-template <int THREADS>
-__device__ __forceinline__ ulonglong2 block_scan2(Shared& sh, uint64_t a, uint64_t b, ulonglong2* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t ia = a, ib = b;
+__device__ __forceinline__ wide shfl(wide v, int lane) {
+  return (wide)__shfl_sync(0xffffffffu, (uint64_t)(v >> 64), lane) << 64 | __shfl_sync(0xffffffffu, (uint64_t)v, lane);
+}
+// Sum over the lanes up to this one's, of the first `lanes`.
+__device__ __forceinline__ wide warp_scan(wide v, int lanes) {
 #pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t ua = shfl_up64(ia, o), ub = shfl_up64(ib, o);
-    if (lane >= o) {
-      ia += ua;
-      ib += ub;
-    }
+  for (int o = 1; o < lanes; o <<= 1) {
+    const wide up = (wide)__shfl_up_sync(0xffffffffu, (uint64_t)(v >> 64), o) << 64 |
+                    __shfl_up_sync(0xffffffffu, (uint64_t)v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += up;
   }
-  __syncthreads();
-  if (lane == 31) {
-    sh.scan[warp] = ia;
-    sh.scan2[warp] = ib;
-  }
-  __syncthreads();
-  // a lane a warp
-  constexpr int WARPS = THREADS / 32;
-  uint64_t wa = lane < WARPS ? sh.scan[lane] : 0, wb = lane < WARPS ? sh.scan2[lane] : 0;
-  const uint64_t ma = wa, mb = wb;
-#pragma unroll 1
-  for (int o = 1; o < WARPS; o <<= 1) {
-    const uint64_t ua = shfl_up64(wa, o), ub = shfl_up64(wb, o);
-    if (lane >= o) {
-      wa += ua;
-      wb += ub;
-    }
-  }
-  total->x = __shfl_sync(0xffffffffu, wa, WARPS - 1);
-  total->y = __shfl_sync(0xffffffffu, wb, WARPS - 1);
-  return make_ulonglong2(__shfl_sync(0xffffffffu, wa - ma, warp) + ia - a, __shfl_sync(0xffffffffu, wb - mb, warp) + ib - b);
+  return v;
 }
 
-// f * w rounded down for f >= 0, and whether something was cut off.
-__device__ __forceinline__ uint64_t scaled(float f, uint64_t w, bool* cut) {
+// Sum over the warp of v below 2^80, by pieces of 27 bits.
+__device__ __forceinline__ wide warp_sum96(const Sum96& v) {
+  const uint32_t p0 = __reduce_add_sync(0xffffffffu, (uint32_t)v.lo & 0x7ffffffu);
+  const uint32_t p1 = __reduce_add_sync(0xffffffffu, (uint32_t)(v.lo >> 27) & 0x7ffffffu);
+  const uint32_t p2 = __reduce_add_sync(0xffffffffu, (uint32_t)(v.lo >> 54) | v.hi << 10);
+  return ((wide)p2 << 54) + (((uint64_t)p1 << 27) + p0);
+}
+
+// Sum over the CTA of each thread's v before it; *total the whole sum.
+template <int THREADS>
+__device__ __forceinline__ wide block_scan(Shared& sh, wide v, wide* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const wide incl = warp_scan(v, 32);
+  __syncthreads();
+  if (lane == 31) {
+    sh.scan[warp] = (uint64_t)incl;
+    sh.scan2[warp] = (uint64_t)(incl >> 64);
+  }
+  __syncthreads();
+  // a lane a warp, by one warp: by all of them it costs more than the barrier
+  constexpr int WARPS = THREADS / 32;
+  if (warp == 0) {
+    const wide mine = lane < WARPS ? (wide)sh.scan2[lane] << 64 | sh.scan[lane] : 0;
+    const wide upto = warp_scan(mine, WARPS), before = upto - mine;
+    __syncwarp();
+    if (lane < WARPS) {
+      sh.scan[lane] = (uint64_t)before;
+      sh.scan2[lane] = (uint64_t)(before >> 64);
+    }
+    if (lane == WARPS - 1) {
+      sh.scan[32] = (uint64_t)upto;
+      sh.scan2[32] = (uint64_t)(upto >> 64);
+    }
+  }
+  __syncthreads();
+  *total = (wide)sh.scan2[32] << 64 | sh.scan[32];
+  return ((wide)sh.scan2[warp] << 64 | sh.scan[warp]) + (incl - v);
+}
+
+// f * w rounded down for f >= 0 (w below 2^96), and whether something was cut off.
+__device__ __forceinline__ wide scaled(float f, wide w, bool* cut) {
   const uint32_t b = __float_as_uint(f) & 0x7fffffffu;   // -0 is 0
   const int ex = (int)(b >> 23);
-  const uint64_t m = (b & 0x7fffffu) | (ex ? 0x800000u : 0u);
-  const int right = 150 - (ex ? ex : 1);   // f = m 2^-right, right >= 24 below 1
-  const uint64_t lo = m * w, hi = __umul64hi(m, w);
-  if (right < 64) {
-    *cut = (lo & ((1ull << right) - 1)) != 0;
-    return hi << (64 - right) | lo >> right;
-  }
-  const int r = right - 64;
-  *cut = lo != 0 || (r < 64 ? (hi & ((1ull << r) - 1)) != 0 : hi != 0);
-  return r < 64 ? hi >> r : 0;
+  const int right = 150 - (ex ? ex : 1);   // f = m 2^-right, right >= 23 up to 1
+  const wide v = w * ((b & 0x7fffffu) | (ex ? 0x800000u : 0u));
+  const wide r = right < 128 ? v >> right : 0;
+  *cut = right < 128 ? r << right != v : v != 0;
+  return r;
 }
 
 __device__ __forceinline__ void add_mass(Shared& sh, int b, uint64_t w) {
   const unsigned lo = (unsigned)w, old = atomicAdd(&sh.mass_lo[b], lo);
   const unsigned hi = (unsigned)(w >> 32) + (old + lo < old ? 1u : 0u);
-  if (hi) atomicAdd(&sh.mass_hi[b], hi);
+  if (hi) {
+    const unsigned before = atomicAdd(&sh.mass_hi[b], hi);
+    if (before + hi < before) atomicAdd(&sh.mass_top[b], 1u);
+  }
+}
+__device__ __forceinline__ wide bin_of(const Shared& sh, int b) {   // count and mass
+  return (wide)((uint64_t)sh.count[b] << 32 | sh.mass_top[b]) << 64 | ((uint64_t)sh.mass_hi[b] << 32 | sh.mass_lo[b]);
 }
 
 template <int THREADS> __device__ __forceinline__ void clear_bins(Shared& sh) {
 #pragma unroll 1
-  for (int b = threadIdx.x; b < kBins; b += THREADS) sh.mass_lo[b] = sh.mass_hi[b] = sh.count[b] = 0;
+  for (int b = threadIdx.x; b < kBins; b += THREADS) sh.mass_lo[b] = sh.mass_hi[b] = sh.mass_top[b] = sh.count[b] = 0;
   __syncthreads();
 }
 
@@ -270,47 +316,40 @@ template <int THREADS> __device__ __forceinline__ void clear_bins(Shared& sh) {
 // what lies before it, and the whole sums.
 struct Crossing {
   int bin;
-  uint64_t count, mass;   // before the bin
-  uint64_t all_count, all_mass;
+  uint32_t count;   // before the bin
+  wide mass;        // the same
+  wide all_mass;
 };
 template <int THREADS>
-__device__ __forceinline__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t need) {
+__device__ __forceinline__ Crossing find_bin(Shared& sh, bool by_mass, wide need) {
   constexpr int PER = kBins / THREADS;
-  uint64_t c = 0, m = 0, total, total_c;
+  wide mine = 0, total;
 #pragma unroll 1
-  for (int i = 0; i < PER; ++i) {
-    const int b = threadIdx.x * PER + i;
-    c += sh.count[b];
-    m += (uint64_t)sh.mass_hi[b] << 32 | sh.mass_lo[b];
-  }
-  ulonglong2 totals;
-  const ulonglong2 befores = block_scan2<THREADS>(sh, c, m, &totals);
-  uint64_t cb = befores.x, mb = befores.y;
-  total_c = totals.x;
-  total = totals.y;
+  for (int i = 0; i < PER; ++i) mine += bin_of(sh, threadIdx.x * PER + i);
+  wide before = block_scan<THREADS>(sh, mine, &total);
   if (threadIdx.x == 0) {   // what a sum that never reaches `need` would leave
     sh.found[0] = kBins;
-    sh.found[1] = sh.found[2] = 0;
+    sh.found[1] = sh.found[2] = sh.found[3] = 0;
   }
   __syncthreads();
-  const uint64_t before = by_mass ? mb : cb, mine = by_mass ? m : c;
-  if (before < need && need <= before + mine) {
+  auto of = [&](wide v) { return by_mass ? mass_in(v) : (wide)count_in(v); };
+  if (of(before) < need && need <= of(before + mine)) {
 #pragma unroll 1
     for (int i = 0; i < PER; ++i) {
       const int b = threadIdx.x * PER + i;
-      const uint64_t bc = sh.count[b], bm = (uint64_t)sh.mass_hi[b] << 32 | sh.mass_lo[b];
-      if (need <= (by_mass ? mb + bm : cb + bc)) {
+      const wide upto = before + bin_of(sh, b);
+      if (need <= of(upto)) {
         sh.found[0] = b;
-        sh.found[1] = cb;
-        sh.found[2] = mb;
+        sh.found[1] = count_in(before);
+        sh.found[2] = (uint64_t)before;
+        sh.found[3] = (uint64_t)(mass_in(before) >> 64);
         break;
       }
-      cb += bc;
-      mb += bm;
+      before = upto;
     }
   }
   __syncthreads();
-  const Crossing r{(int)sh.found[0], sh.found[1], sh.found[2], total_c, total};
+  const Crossing r{(int)sh.found[0], (uint32_t)sh.found[1], (wide)sh.found[3] << 64 | sh.found[2], mass_in(total)};
   __syncthreads();
   return r;
 }
@@ -319,9 +358,10 @@ __device__ __forceinline__ Crossing find_bin(Shared& sh, bool by_mass, uint64_t 
 // order reaches `need`, and the mass up to it. `clobbered`: the bins were used for finer ones.
 template <typename T, int THREADS>
 __device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T> row, const Scale sc, int bin, bool by_mass,
-                                          uint64_t need, uint64_t* mass_to, bool* clobbered) {
+                                          wide need, wide* mass_to, bool* clobbered) {
   constexpr int VE = Row<T>::VE;
-  uint64_t lo = 0, hi = ~0ull, before_mass = 0;
+  uint64_t lo = 0, hi = ~0ull;
+  wide before_mass = 0;
   bool ranged = false;   // members are those with keys in lo .. hi, else those of the bin
   auto visit = [&](auto&& f) {
     uint4 next = threadIdx.x < row.blocks ? block_of(row, threadIdx.x) : make_uint4(0, 0, 0, 0);
@@ -389,7 +429,7 @@ __device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T> row, const Sc
     __syncthreads();
     const Crossing at = find_bin<THREADS>(sh, by_mass, need);
     const int sub = min(at.bin, kBins - 1);
-    need -= by_mass ? at.mass : at.count;
+    need -= by_mass ? at.mass : (wide)at.count;
     before_mass += at.mass;
     hi -= (uint64_t)sub << shift;
     const uint64_t width = (1ull << shift) - 1;
@@ -398,26 +438,29 @@ __device__ __noinline__ uint64_t find_key(Shared& sh, const Row<T> row, const Sc
   }
   const int n = min(sh.n, kList);
   __syncthreads();
-  if (threadIdx.x == 0) sh.found[0] = sh.found[1] = 0;
+  if (threadIdx.x == 0) sh.found[0] = sh.found[1] = sh.found[2] = 0;
   __syncthreads();
 #pragma unroll 1
   for (int i = threadIdx.x; i < n; i += THREADS) {
     const uint64_t key = sh.key[i], w = sh.weight[i];
-    uint64_t above = 0, above_mass = 0;
+    unsigned above = 0;
+    Sum96 sum{0, 0};
 #pragma unroll 4
     for (int j = 0; j < n; ++j)
       if (sh.key[j] > key) {
         ++above;
-        above_mass += sh.weight[j];
+        sum.add(sh.weight[j]);
       }
+    const wide above_mass = sum.get();
     if (by_mass ? above_mass < need && need <= above_mass + w : above + 1 == need) {
       sh.found[0] = key;
-      sh.found[1] = above_mass + w;
+      sh.found[1] = (uint64_t)(above_mass + w);
+      sh.found[2] = (uint64_t)((above_mass + w) >> 64);
     }
   }
   __syncthreads();
   const uint64_t key = sh.found[0];
-  *mass_to = before_mass + sh.found[1];
+  *mass_to = before_mass + ((wide)sh.found[2] << 64 | sh.found[1]);
   __syncthreads();
   return key;
 }
@@ -505,13 +548,18 @@ __device__ __forceinline__ uint4 lowest_for(const uint4& u, unsigned beside) {
 
 // Counts the clamped values u that `live` tells, which lie beside the table.
 __device__ __noinline__ void count_block(Shared& sh, Scale sc, uint4 u, unsigned live) {
+  atomicAdd(&sh.small_n, (unsigned)__popc(live));
+  uint64_t lo = 0, hi = 0;
 #pragma unroll 1
   for (; live; live &= live - 1) {
-    const unsigned bits = half_of(u, __ffs(live) - 1);
-    atomicAdd(&sh.small_n, 1u);
-    atomicAdd(&sh.small_mass, (unsigned long long)weight_of(sh, sc, __uint_as_float(bits << 16)));
+    const uint64_t w = weight_of(sh, sc, __uint_as_float(half_of(u, __ffs(live) - 1) << 16));
+    lo += (uint32_t)w;
+    hi += w >> 32;
   }
+  atomicAdd(&sh.small_lo, (unsigned long long)lo);
+  atomicAdd(&sh.small_hi, (unsigned long long)hi);
 }
+__device__ __forceinline__ wide small_mass(const Shared& sh) { return ((wide)sh.small_hi << 32) + sh.small_lo; }
 
 // Counts of the table's values and the cut by them. False: the cut lies among the smaller values.
 template <int THREADS>
@@ -536,7 +584,8 @@ __device__ __forceinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16> r
   // running sums in rank order; the small values lie between the signs
   constexpr int PER = kBins / THREADS;
   const int r0 = tid * PER;
-  uint64_t c = 0, m = 0;
+  unsigned c = 0;
+  uint64_t m_lo = 0, m_hi = 0;   // of the weights' low and high words: at most 2^57
   {   // the thread's ranks are PER places in a row, from a multiple of PER on
     const int at = min(place_at(r0), place_at(r0 + PER - 1));
 #pragma unroll
@@ -545,53 +594,77 @@ __device__ __forceinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16> r
       const ulonglong2 v0 = *reinterpret_cast<const ulonglong2*>(&sh.value[at + i]);
       const ulonglong2 v1 = *reinterpret_cast<const ulonglong2*>(&sh.value[at + i + 2]);
       c += n.x + n.y + n.z + n.w;
-      m += n.x * v0.x + n.y * v0.y + n.z * v1.x + n.w * v1.y;
+      m_lo += (v0.x & 0xffffffffu) * n.x + (v0.y & 0xffffffffu) * n.y + (v1.x & 0xffffffffu) * n.z + (v1.y & 0xffffffffu) * n.w;
+      m_hi += (v0.x >> 32) * n.x + (v0.y >> 32) * n.y + (v1.x >> 32) * n.z + (v1.y >> 32) * n.w;
     }
   }
-  ulonglong2 all;
-  const ulonglong2 before2 = block_scan2<THREADS>(sh, c, m, &all);
-  const uint64_t cb = before2.x + (r0 >= kValues ? sh.small_n : 0);
-  const uint64_t mb = before2.y + (r0 >= kValues ? sh.small_mass : 0);
+  const wide m = ((wide)m_hi << 32) + m_lo;
+  wide all;
+  const wide before2 = block_scan<THREADS>(sh, with_count(c, m), &all);
+  const unsigned cb = count_in(before2) + (r0 >= kValues ? sh.small_n : 0u);
+  const wide mb = mass_in(before2) + (r0 >= kValues ? small_mass(sh) : 0);
   // where a sum reaches `need`: found = {place, tokens of it, sum up to it}
-  auto reach = [&](bool by_mass, uint64_t need) {
+  auto reach = [&](bool by_mass, wide need) {
     __syncthreads();
-    if (tid == 0) sh.found[0] = kBins;
+    if (tid < 32) {
+      if (by_mass) {   // top_p of what is kept, rounded up, by one warp
+        bool more;
+        need = scaled(top_p, need, &more);
+        need += more;
+        if (need == 0) need = 1;
+      }
+      if (tid == 0) {
+        sh.found[0] = kBins;
+        sh.choice.target_lo = (uint64_t)need;
+        sh.choice.target_hi = (uint64_t)(need >> 64);
+      }
+    }
     __syncthreads();
-    const uint64_t before = by_mass ? mb : cb;
-    if (before < need && need <= before + (by_mass ? m : c)) {
-      uint64_t count = cb, mass = mb;
+    need = (wide)sh.choice.target_hi << 64 | sh.choice.target_lo;
+    const wide before = by_mass ? mb : (wide)cb;
+    if (before < need && need <= before + (by_mass ? m : (wide)c)) {
+      unsigned count = cb;
+      wide mass = mb;
 #pragma unroll 1
       for (int i = 0; i < PER; ++i) {
         const int at = place_at(r0 + i);
-        const uint64_t n = sh.count[at], w = sh.value[at];
-        if (by_mass ? need <= mass + n * w : need <= count + n) {
-          const uint64_t keep = by_mass ? (need - mass + w - 1) / w : need - count;
+        const unsigned n = sh.count[at];
+        const uint64_t w = sh.value[at];
+        if (by_mass ? need <= mass + times(w, n) : need <= count + n) {
+          unsigned keep = (unsigned)need - count;
+          if (by_mass) {   // need - mass over w, rounded up: about, then exactly
+            const wide rest = need - mass;
+            keep = (unsigned)__fdividef((float)(uint64_t)(rest >> 64) * 0x1p64f + (float)(uint64_t)rest, (float)w);
+#pragma unroll 1
+            while (times(w, keep) < rest) ++keep;
+#pragma unroll 1
+            while (keep > 1 && times(w, keep - 1) >= rest) --keep;
+          }
+          mass += times(w, keep);
           sh.found[0] = at;
           sh.found[1] = keep;
-          sh.found[2] = mass + keep * w;
+          sh.found[2] = (uint64_t)mass;
+          sh.found[3] = (uint64_t)(mass >> 64);
           break;
         }
         count += n;
-        mass += n * w;
+        mass += times(w, n);
       }
     }
     __syncthreads();
   };
-  uint64_t kept = all.y + sh.small_mass, ties = 0;
+  wide kept = mass_in(all) + small_mass(sh);
+  uint64_t ties = 0;
   unsigned place = kBins;
   if (by_k) {
     reach(false, top_k);
     place = (unsigned)sh.found[0];
     if (place == kBins) return false;
     ties = sh.found[1];
-    kept = sh.found[2];
+    kept = (wide)sh.found[3] << 64 | sh.found[2];
   }
   if (by_p) {
-    bool more;
-    uint64_t need = scaled(top_p, kept, &more);
-    need += more;
-    if (need == 0) need = 1;
-    reach(true, need);
+    reach(true, kept);
     const unsigned at = (unsigned)sh.found[0];
     if (at == kBins) return false;
     // of one place p's cut is within k's
@@ -619,10 +692,10 @@ __device__ __forceinline__ bool table_cut(Shared& sh, const Row<__nv_bfloat16> r
 // (what is kept then lies in the bins): small weights are summed aside, not by atomics, unless the
 // cut lies among them.
 template <typename T, int THREADS>
-__device__ __noinline__ uint64_t fill_bins(Shared& sh, const Row<T> row, const Scale sc, bool by_k, bool by_p,
+__device__ __noinline__ wide fill_bins(Shared& sh, const Row<T> row, const Scale sc, bool by_k, bool by_p,
                                            int region) {
   clear_bins<THREADS>(sh);
-  uint64_t mass = 0;
+  Sum96 mass{0, 0};
   for_blocks<T, THREADS>(row, threadIdx.x, row.blocks, [&](int, const uint4& u) {
 // fp32 comes this way alone: 122 us for 256 rows with four copies, 129 with one
 #pragma unroll (sizeof(T) == 4 ? 4 : 1)
@@ -635,28 +708,29 @@ __device__ __noinline__ uint64_t fill_bins(Shared& sh, const Row<T> row, const S
         if (by_k) atomicAdd(&sh.count[b], 1u);
         if (w) add_mass(sh, b, w);
       } else {
-        mass += w;
+        mass.add(w);
       }
     }
   });
-  ulonglong2 all;
-  block_scan2<THREADS>(sh, mass, 0, &all);
+  wide all;
+  block_scan<THREADS>(sh, mass.get(), &all);
   __syncthreads();
-  return all.x;
+  return all;
 }
 
 // The lowest key kept by top-k and top-p, of any values.
 template <typename T, int THREADS>
 __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const Scale sc, int top_k, float top_p,
                                              bool by_k, bool by_p) {
-  uint64_t cut = 0, rest_mass = 0;
+  uint64_t cut = 0;
+  wide rest_mass = 0;
   auto fill = [&](int region) { rest_mass = fill_bins<T, THREADS>(sh, row, sc, by_k, by_p, region); };
   int region = 24 * 64;
   fill(region);
-  uint64_t kept = 0;
+  wide kept = 0;
   bool clobbered = false;
   if (by_k) {
-    uint64_t to;
+    wide to;
     Crossing at = find_bin<THREADS>(sh, false, top_k);
     if (at.bin == kBins && region < kBins) {
       fill(region = kBins);
@@ -668,15 +742,15 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const
       kept += to;
     }
   } else {
-    kept = find_bin<THREADS>(sh, true, ~0ull).all_mass + rest_mass;
+    kept = find_bin<THREADS>(sh, true, ~(wide)0).all_mass + rest_mass;
   }
   if (by_p) {
     if (clobbered) fill(region);
     bool more;
-    uint64_t need = scaled(top_p, kept, &more);
+    wide need = scaled(top_p, kept, &more);
     need += more;
     if (need == 0) need = 1;
-    uint64_t to;
+    wide to;
     Crossing at = find_bin<THREADS>(sh, true, need);
     if (at.bin == kBins && region < kBins) {
       fill(region = kBins);
@@ -689,14 +763,14 @@ __device__ __noinline__ uint64_t general_cut(Shared& sh, const Row<T> row, const
 }
 
 // Weights of the clamped values u that `live` tells, which lie beside the table, summed.
-__device__ __noinline__ uint64_t sum_block(const Shared& sh, Scale sc, uint4 u, unsigned live) {
-  uint64_t sum = 0;
+__device__ __noinline__ wide sum_block(const Shared& sh, Scale sc, uint4 u, unsigned live) {
+  Sum96 sum{0, 0};
 #pragma unroll 1
   for (; live; live &= live - 1) {
     const uint64_t t = weight_of(sh, sc, __uint_as_float(half_of(u, __ffs(live) - 1) << 16));
-    sum += t >= sh.cut.least ? t : 0;
+    sum.add(t >= sh.cut.least ? t : 0);
   }
-  return sum;
+  return sum.get();
 }
 // Weight of a token if it stays for sure, in the general way.
 __device__ __forceinline__ uint64_t key_weight(const Shared& sh, const Scale& sc, const Cut& cut, int token, float x) {
@@ -724,7 +798,7 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
   const Cut cut = sh.cut;
   // ---- kept weights by slices of the row, a warp each
   const int per = (row.blocks + WARPS - 1) / WARPS;
-  uint64_t sum = 0;
+  Sum96 sum{0, 0};   // a lane's slice
   unsigned tied = 0;
   // equal to no logit without a cut by the table
   const bool ranked = sizeof(T) == 2 && cut.table && cut.place < kBins;
@@ -743,7 +817,9 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
           u = clamped(raw);
           if (!all_in_table(u)) {
             const unsigned beside = beside_table(u);
-            sum += sum_block(sh, sc, u, beside);
+            const wide t = sum_block(sh, sc, u, beside);
+            sum.add((uint64_t)t);
+            sum.hi += (uint32_t)(t >> 64);
             u = lowest_for(u, beside);
           }
         }
@@ -751,7 +827,7 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = (&u.x)[i], at = offsets<3>(w);
           const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w);
-          sum += sum_above(value, at, w, pattern);
+          sum.add(sum_above(value, at, w, pattern));
           ties += __heq2_mask(x2, *reinterpret_cast<const __nv_bfloat162*>(&pattern)) & 0x00010001u;
         }
       });
@@ -760,49 +836,50 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
   } else {
     for_blocks<T, 32>(row, warp * per + lane, slice_end, [&](int v, const uint4& u) {
 #pragma unroll (sizeof(T) == 4 ? 4 : 1)
-      for (int i = 0; i < VE; ++i) sum += key_weight(sh, sc, cut, v * VE - row.off + i, element<T>(u, i));
+      for (int i = 0; i < VE; ++i) sum.add(key_weight(sh, sc, cut, v * VE - row.off + i, element<T>(u, i)));
     });
   }
-  tied = __reduce_add_sync(0xffffffffu, tied);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const wide slice_sum = with_count(__reduce_add_sync(0xffffffffu, tied), warp_sum96(sum));
   __syncthreads();
   if (lane == 0) {
-    sh.scan[warp] = sum;
-    sh.scan2[warp] = tied;
+    sh.scan[warp] = (uint64_t)slice_sum;
+    sh.scan2[warp] = (uint64_t)(slice_sum >> 64);
   }
   __syncthreads();
-  // a lane a slice: the ties before it, what is kept of it, and up to it
-  const unsigned ties_all = (unsigned)cut.ties, here = lane < WARPS ? (unsigned)sh.scan2[lane] : 0u;
-  unsigned met_before = here;
+  if (warp == 0) {
+    // a lane a slice: the ties before it, what is kept of it, and up to it
+    const wide slice_of = lane < WARPS ? (wide)sh.scan2[lane] << 64 | sh.scan[lane] : 0;
+    const unsigned ties_all = (unsigned)cut.ties, here = count_in(slice_of);
+    unsigned met_before = here;
 #pragma unroll 1
-  for (int o = 1; o < WARPS; o <<= 1) {
-    const unsigned up = __shfl_up_sync(0xffffffffu, met_before, o);
-    if (lane >= o) met_before += up;
+    for (int o = 1; o < WARPS; o <<= 1) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, met_before, o);
+      if (lane >= o) met_before += up;
+    }
+    met_before -= here;
+    const unsigned ties_left = ties_all - min(ties_all, met_before);
+    const wide mass = mass_in(slice_of) + times(cut.weight, min(here, ties_left));
+    const wide upto = warp_scan(mass, WARPS);
+    const wide whole = shfl(upto, WARPS - 1);
+    bool rest;
+    const wide target = scaled(u, whole, &rest);   // the running sum has to exceed it, as the whole does
+    const int slice = min(__ffs(__ballot_sync(0xffffffffu, target < upto)) - 1, WARPS - 1);
+    if (lane == slice) {
+      const wide within = target - (upto - mass);
+      sh.choice = Choice{(uint64_t)within, (uint64_t)(within >> 64), (uint64_t)whole, (uint64_t)(whole >> 64), ties_left, slice};
+    }
   }
-  met_before -= here;
-  const uint64_t mass =
-      (lane < WARPS ? sh.scan[lane] : 0) + min(here, ties_all - min(ties_all, met_before)) * cut.weight;
-  uint64_t upto = mass;
-#pragma unroll 1
-  for (int o = 1; o < WARPS; o <<= 1) {
-    const uint64_t up = shfl_up64(upto, o);
-    if (lane >= o) upto += up;
-  }
-  const uint64_t whole = __shfl_sync(0xffffffffu, upto, WARPS - 1);
-  bool rest;
-  uint64_t target = scaled(u, whole, &rest);   // the running sum has to exceed it, as the whole does
-  const int slice = min(__ffs(__ballot_sync(0xffffffffu, target < upto)) - 1, WARPS - 1);
-  target -= __shfl_sync(0xffffffffu, upto - mass, slice);
-  uint64_t left = ties_all - min(ties_all, __shfl_sync(0xffffffffu, met_before, slice));   // ties not yet met
   __syncthreads();
+  const int slice = sh.choice.slice;
+  wide target = (wide)sh.choice.target_hi << 64 | sh.choice.target_lo;
+  unsigned left = sh.choice.left;   // ties not yet met
   // ---- the token within the slice, a block a thread
 #pragma unroll 1
   for (int v0 = slice * per; v0 < min(row.blocks, (slice + 1) * per); v0 += THREADS) {
     const int v = v0 + tid;
     // the block's weights and its tokens of the last value kept
     const bool live = v < min(row.blocks, (slice + 1) * per);
-    uint64_t sure = 0;
+    Sum96 sure{0, 0};
     unsigned met = 0;
     uint4 block = make_uint4(0, 0, 0, 0);
     if (live) {
@@ -810,17 +887,19 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
 #pragma unroll 1
       for (int i = 0; i < VE; ++i) {
         const float x = element<T>(block, i);
-        sure += token_weight<T>(sh, sc, v * VE - row.off + i, x);
+        sure.add(token_weight<T>(sh, sc, v * VE - row.off + i, x));
         met += sizeof(T) == 2 && x == cut_value;
       }
     }
-    ulonglong2 all;
-    const ulonglong2 before2 = block_scan2<THREADS>(sh, sure, met, &all);
+    wide all;
+    const wide before2 = block_scan<THREADS>(sh, with_count(met, sure.get()), &all);
     // the first `left` ties stay
-    const uint64_t ties_before = min((uint64_t)before2.y, left), ties_here = min((uint64_t)met, left - ties_before);
-    const uint64_t before = before2.x + ties_before * cut.weight, mine = sure + ties_here * cut.weight;
+    const unsigned ties_before = min(count_in(before2), left), ties_here = min(met, left - ties_before);
+    const wide before = mass_in(before2) + times(cut.weight, ties_before);
+    const wide mine = sure.get() + times(cut.weight, ties_here);
     if (before <= target && target < before + mine) {
-      uint64_t cum = before, stay = ties_here;
+      wide cum = before;
+      unsigned stay = ties_here;
       int at = -1;
       float x_at = 0.f;
 #pragma unroll 1
@@ -838,18 +917,23 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
       }
       a.token[r] = v * VE - row.off + at;
       if (a.logp) {
-        // (x - top) / temp - ln(whole 2^-unit), each with its rounding errors
+        // (x - top) / temp - ln(whole 2^-62), each with its rounding errors
         const float d = x_at - sc.top, t = d - x_at, dd = (x_at - (d - t)) + (-sc.top - t);
         const float q = d / temp, qq = temp < INFINITY ? (fmaf(-q, temp, d) + dd) / temp : 0.0f;
-        const int e = 63 - __clzll(whole);
-        const float f = (float)(whole - (1ull << e)) * __uint_as_float((unsigned)(127 - e) << 23);
-        const float n = (float)(e - a.unit);
+        // whole = 2^e (1 + f); it has the largest weight or, at least, the chosen one
+        const uint64_t high = sh.choice.whole_hi;
+        const wide whole = (wide)high << 64 | sh.choice.whole_lo;
+        const int e = high ? 127 - __clzll(high) : 63 - __clzll((uint64_t)whole);
+        const uint64_t head = (uint64_t)(e > 63 ? whole >> (e - 63) : whole << (63 - e));
+        const float f = (float)(head & 0x7fffffffffffffffull) * 0x1p-63f;
+        const float n = (float)(e - kUnit);
         constexpr float kLn2Hi = 0.693145752f, kLn2Lo = 1.42860677e-6f;   // the first of 17 bits
         const float big = q - n * kLn2Hi, rest2 = (q - big) - n * kLn2Hi;
         a.logp[r] = big + (rest2 + ((qq - n * kLn2Lo) - log1pf(f)));
       }
     }
-    const uint64_t ties_here_all = min((uint64_t)all.y, left), whole_here = all.x + ties_here_all * cut.weight;
+    const unsigned ties_here_all = min(count_in(all), left);
+    const wide whole_here = mass_in(all) + times(cut.weight, ties_here_all);
     if (target < whole_here) break;
     target -= whole_here;
     left -= ties_here_all;
@@ -921,8 +1005,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
   pdl_trigger();
   for (int i = tid; i < 1024; i += THREADS) {
     const uint64_t p = __umul64hi(tables.coarse[i >> 5], tables.fine[i & 31]);   // 60-bit fraction
-    sh.power[i] = (a.unit >= 60 ? p << (a.unit - 60) : p >> (60 - a.unit)) -
-                  ((uint64_t)__float_as_int(kRound) << (a.unit - 32));
+    sh.power[i] = (p << (kUnit - 60)) - ((uint64_t)__float_as_int(kRound) << (kUnit - 32));
     sh.powerf[i] = (float)(p >> 28);
   }
   pdl_wait();
@@ -952,7 +1035,6 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
     }
     Scale sc;
     sc.top = top;
-    sc.unit = a.unit;
     {   // log2(e) / temp, the division's remainder in the second part
       constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;   // log2(e)
       temp = fmaxf(temp, kHi * 0x1p-120f);   // below it sc.hi would pass fp32's range
@@ -963,15 +1045,14 @@ sample_kernel(const SampleArgs a, const __grid_constant__ PowerTables tables) {
     uint64_t least = 0;
     if (min_p > 0.0f) {
       bool more;
-      least = scaled(fminf(min_p, 1.0f), 1ull << a.unit, &more);
-      least += more;
+      least = (uint64_t)scaled(fminf(min_p, 1.0f), (wide)1 << kUnit, &more) + more;
     }
     // -127.5 at (-127.5 - top) sc.hi: none of its weight is left 62 below
     bool table = sizeof(T) == 2 && in_table(__float_as_uint(top) >> 16) && (-127.5f - top) * sc.hi < -64.0f;
     if (tid == 0) {
       sh.cut = Cut{table, true, kBins, 0, 0, least, -INFINITY, a.V};
       sh.small_n = 0;
-      sh.small_mass = 0;
+      sh.small_lo = sh.small_hi = 0;
     }
     if constexpr (sizeof(T) == 2) {
       if (table) {
@@ -1037,9 +1118,6 @@ int xmod_sample_tokens(xmod_dtype dt, int64_t N, int V, const void* logits, int6
   if (device_sms() <= 0) return XMOD_ERR_CUDA;
   SampleArgs a{};
   a.V = V;
-  int bits = 1;
-  while ((1 << bits) < V) ++bits;
-  a.unit = 62 - bits;
   a.N = N;
   a.ld = ld;
   a.logits = logits;
