@@ -17,12 +17,22 @@ struct PairTurns {
   uint64_t f[64];
 };
 
+// |freq| / (2 pi) with the product's rounding error and 1 / (2 pi) in two doubles, its fraction rounded
+// to 2^-64 and negated for a negative freq: a small negative number rounded up to a turn would
+// keep no more than 2^-54 of it.
 void pair_turns(const xmod_rope& r, PairTurns& t) {
-  constexpr double kInvTwoPi = 0.15915494309189535;
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
   for (int c = 0; c < r.rot_dim / 2; ++c) {
-    const double turns = r.freq[c] * kInvTwoPi;
-    const double frac = turns - floor(turns);   // may round to 1
-    t.f[c] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;
+    const double f = fabs(r.freq[c]), turns = f * kHi;
+    const double rest = fma(f, kHi, -turns) + f * kLo;
+    // units of 2^-64, and what is left of them
+    const double at = (turns - floor(turns)) * 0x1p64, more = (rest - rint(rest)) * 0x1p64;
+    const double at_units = floor(at), more_units = floor(more);   // 0 .. 2^64 - 1, -2^63 .. 2^63
+    const double left = (at - at_units) + (more - more_units);
+    const uint64_t frac = (uint64_t)at_units +
+                          (more_units < 0.0 ? 0 - (uint64_t)-more_units : (uint64_t)more_units) +
+                          (uint64_t)(left + 0.5);
+    t.f[c] = r.freq[c] < 0.0 ? 0 - frac : frac;
   }
 }
 
