@@ -3,6 +3,7 @@
 // tokens at 8192 of 16 and 4 heads of 128 910 us, eight chunks of 512 at 4096 of 64 889); small calls
 // by the latency of one to three tiles a CTA and the join (six of 100 at 1000 35 us).
 
+#include <limits.h>
 #include <math.h>
 
 #include <atomic>
@@ -75,8 +76,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
     auto pages_of = [&](int tile, int (&page)[N]) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int slot = tile * kChunkKeys + key_in + STEP * j;
-        page[j] = tile < last && slot < w.limit ? chunk_page(a, w.k, slot) : 0;
+        // tiles past the last one may lie past 2^31
+        const int slot = tile < last ? tile * kChunkKeys + key_in + STEP * j : INT_MAX;
+        page[j] = slot < w.limit ? chunk_page(a, w.k, slot) : 0;
       }
     };
     auto copy = [&](const float* cache, float* to, int tile, const int (&page)[N]) {
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_chunk_f32_kernel(const Chun
           if (key0 + tx + 16 * j >= row[i].limit) sc[i][j] = -INFINITY;
           top = fmaxf(top, sc[i][j]);
         }
-        masked |= key0 + kChunkKeys > row[i].limit;
+        masked |= row[i].limit - key0 < kChunkKeys;
 #pragma unroll
         for (int of = 8; of > 0; of >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, of));
         const float low = top == -INFINITY ? 0.f : top, keep = exp2f(mx[i] - low);

@@ -361,8 +361,9 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     const int nbox = KB / a.box;
     int page = 0, y_prev = 0, boxes_prev = 0;
     auto page_of = [&](int tile) {   // lane b: the page of box b
+      if (lane >= nbox) return 0;   // nor may the sum pass 2^31, which the last tile reaches
       const int key = tile * KB + lane * a.box;
-      return lane < nbox && key < w.limit ? chunk_page(a, w.k, key) : 0;
+      return key < w.limit ? chunk_page(a, w.k, key) : 0;
     };
     auto load_v = [&](int i, int y, int boxes) {   // V of the i-th tile of the range
       const int st = i % NK;
@@ -387,7 +388,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
           report_status(a.status, XMOD_ERR_DEVICE_CHECK);
           pg = 0;
         }
-        const int key = tile * KB + lane * a.box;
+        const int key = tile * KB + (lane < nbox ? lane * a.box : 0);
         const int y = (int)(((int64_t)pg * a.hkv + g) * a.page_size + chunk_in_page(a, key));
         if constexpr (!FP8) {
           const int st = it % NK;
@@ -536,7 +537,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             v[i + 3] = s1.y;
           }
         }
-        const bool masked = key0 + KB > least;   // some row of the segment does not see all of it
+        const bool masked = least - key0 < KB;   // some row of the segment does not see all of it
         const int seen = limit - key0;   // of this row
         if (masked) {
 #pragma unroll
