@@ -51,10 +51,36 @@ constexpr int KB = kChunkKeys;
 constexpr int QR = kChunkTcRows;
 constexpr float kRescale = 8.0f;   // log2 units
 
+// Whether a wait that ran out has to give up. Some roles wait as long as a segment takes, which has no
+// bound (2 s at 146 million slots): not if the loads, of which the word after the abort flag counts
+// 1024 tiles at a time, went on since this thread asked last, a limit's time ago; behind it every
+// thread has what it saw then. (Kept in the wait's own registers this costs 2 % of the kernel's time.)
+__device__ __noinline__ bool stalled(volatile int* abort_flag, int* status) {
+  volatile uint16_t* const seen = reinterpret_cast<volatile uint16_t*>(abort_flag + 2) + threadIdx.x;
+  const uint16_t now = (uint16_t)(abort_flag[1] | 0x8000);   // 0: has not asked yet
+  if (*seen != now) {
+    *seen = now;
+    return false;
+  }
+  report_status(status, XMOD_ERR_TIMEOUT);
+  *abort_flag = 1;
+  return true;
+}
 // The bounded wait with everything but its first test out of line: it stands in every loop here,
 // whose code has to stay small.
 __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return mbar_wait(bar, parity, abort_flag, status);
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (stalled(abort_flag, status)) return false;
+        t0 = global_timer_ns();
+      }
+    }
+  }
 }
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
   bool ok = mbar_try_wait(bar, parity);
@@ -75,7 +101,7 @@ template <int HD, bool FP8> struct Tc {
   // where a warp turns its rows of the output: 32 rows of OUT columns, padded
   static constexpr int OUT = FP8 && HD == 128 ? 16 : 32, OUT_LD = OUT * 2 + 16, TURN = 8 * 32 * OUT_LD;
   static constexpr int DATA = 2 * Q_TILE + 2 * NK * K_TILE + NC * (2 * CODES + SCALES) + NK * SCALES + TURN;
-  static constexpr int MISC = 2048;
+  static constexpr int MISC = 2048 + 512;
   static constexpr int SMEM = DATA + MISC + 1024;
   static constexpr int THREADS = FP8 ? 512 : 384;
   static constexpr int TMEM_COLS = 512;                     // S: 4 x 64, O: 2 x HD
@@ -224,13 +250,14 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
   ChunkPlan* const plan = reinterpret_cast<ChunkPlan*>(misc + 640);
   long long* const scratch = reinterpret_cast<long long*>(misc + 768);                      // [16]
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc + 896);
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 904);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 1408);            // what stalled() tells
   unsigned long long* const bad_keys = reinterpret_cast<unsigned long long*>(misc + 912);   // [2][3]
   Segment* const segs = reinterpret_cast<Segment*>(misc + 960);
-  static_assert(sizeof(ChunkPlan) <= 128 && 960 + kSegments * sizeof(Segment) <= C::MISC, "");
+  static_assert(sizeof(ChunkPlan) <= 128 && 960 + kSegments * sizeof(Segment) <= 1408 && 1408 + 8 + 2 * C::THREADS <= C::MISC, "");
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  reinterpret_cast<volatile uint16_t*>(abort_flag + 2)[tid] = 0;
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(FULL + 8 * i, FP8 ? 128 : 1);
@@ -254,7 +281,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       mbar_init(C_FULL + 8 * i, 1);
       mbar_init(C_EMPTY + 8 * i, 128);
     }
-    *abort_flag = 0;
+    abort_flag[0] = abort_flag[1] = 0;
     for (int i = 0; i < 6; ++i) bad_keys[i] = 0;
     fence_barrier_init();
     prefetch_tensormap(&mQ);
@@ -381,6 +408,7 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       const int first = w.first, last = w.last, g = chunk_kv_head(a, w.hp);
       page = page_of(first);
       for (int tile = first; tile < last && ok; ++tile, ++it) {
+        if (lane == 0 && (it & 1023) == 0) abort_flag[1] = it >> 10;
         const int next = tile + 1 < last ? page_of(tile + 1) : 0;
         const int valid = max(0, min(KB, w.limit - tile * KB)), boxes = (valid + a.box - 1) / a.box;
         int pg = page;

@@ -74,3 +74,41 @@ def test_last_slots_of_the_longest_cache(X, kind, after):
         err = (o[m].double() - ref).abs() - bound - half * (ref.abs() + bound)
         assert float(err.max()) <= 0, (m, float(err.max()))
         assert abs(float(lse[m]) - float(torch.logsumexp(z, 0))) <= rel + 1e-6 * abs(float(lse[m]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_segments_that_take_longer_than_a_wait(X, kind):
+    """Two chunks of one token for each SM, all of one sequence: 180 million slots and 64 by turns, so that
+    every CTA works on a long segment, whose end another warp of it waits for with the next one's
+    query, for longer than the limit of a wait without progress."""
+    hd, P, pages = 32, 8176, 22016
+    n = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(6)
+    k, v = (torch.randn(1, 1, P, hd, generator=g).cuda() for _ in range(2))
+    if kind == "e4m3":
+        k, v = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)
+        scales = {name: torch.ones(1, 1, P, device="cuda") for name in ("k_scale", "v_scale")}
+    else:
+        k, v, scales = k.to(torch.bfloat16), v.to(torch.bfloat16), {}
+    cache = X.kv_cache(k, v, torch.zeros(1, pages, dtype=torch.int32, device="cuda"), **scales)
+    dm = C.dims(X, 1, 1, hd, "bf16")
+    q = torch.randn(n, hd, generator=g).cuda().to(torch.bfloat16)
+    o, lse = torch.zeros(n, hd, device="cuda", dtype=torch.bfloat16), torch.zeros(n, 1, device="cuda")
+    ws = torch.zeros(X.cache_attention_chunk_workspace_bytes(dm, n, n), dtype=torch.uint8, device="cuda")
+    start = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([P * pages, 64] * (n // 2), dtype=torch.int32, device="cuda")
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    X.cache_attention_chunk(dm, cache, q, start, torch.zeros(n, dtype=torch.int32, device="cuda"), lens, o, ws, lse=lse)
+    end.record()
+    assert X.sync_status(ws) == X.OK
+    print("ms:", begin.elapsed_time(end))
+    # the long sequence is one page 22016 times over: its softmax is that page's. fp32 sums of 2.8
+    # million tiles: half a step, 2^-24, for each of them and of the four products of 16 keys, twice
+    # that if they are cut off; the weights' and the output's rounding
+    for rows, slots, times, adds in ((slice(0, n, 2), P, pages, 5 * P * pages / 64), (slice(1, n, 2), 64, 1, 5)):
+        z = q[rows].double() @ k[0, 0, :slots].double().T / math.sqrt(hd)
+        w, rel = torch.softmax(z, 1), adds * 2.0 ** -23 + 2.0 ** -16
+        ref, spread = w @ v[0, 0, :slots].double(), w @ v[0, 0, :slots].double().abs()
+        assert float(((o[rows].double() - ref).abs() - spread * (rel + 2.0 ** -7)).max()) <= 0
+        assert float((lse[rows, 0].double() - torch.logsumexp(z, 1) - math.log(times)).abs().max()) <= math.log1p(rel)
