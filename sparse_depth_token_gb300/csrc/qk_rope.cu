@@ -176,6 +176,8 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
   }
   const T* gain = (const T*)(is_k ? a.k_gain : a.q_gain);
   const bool norm = gain != nullptr, live = h0 < heads;
+  // lanes without a head have zeros, and add to the gains' sums: with eps 0 they would have no inverse root
+  const float eps = live ? a.eps : 1.0f;
   float2 dg0[V / 2], dg1[V / 2];
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) dg0[e] = dg1[e] = make_float2(0.f, 0.f);
@@ -231,7 +233,7 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
           float sum = ss.x + ss.y;
 #pragma unroll
           for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float inv = rsqrtf(fmaf(sum, 1.0f / (float)HD, a.eps));
+          const float inv = rsqrtf(fmaf(sum, 1.0f / (float)HD, eps));
           const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
           for (int e = 0; e < V / 2; ++e) {
@@ -257,7 +259,7 @@ qk_rope_kernel(const RopeArgs a, const __grid_constant__ PairTurns turns) {
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
             dot += __shfl_xor_sync(0xffffffffu, dot, o);
           }
-          const float inv = rsqrtf(fmaf(sum, 1.0f / (float)HD, a.eps));
+          const float inv = rsqrtf(fmaf(sum, 1.0f / (float)HD, eps));
           const float2 inv2 = make_float2(inv, inv);
           const float back = -(inv * dot) * (1.0f / (float)HD) * inv * inv;
           const float2 back2 = make_float2(back, back);
