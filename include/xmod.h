@@ -517,7 +517,9 @@ XMOD_API size_t xmod_cache_attention_chunk_workspace_bytes(const xmod_dims* dims
  * Slots at or after lim(m) have no influence on row m, whatever they hold (NaN and infinities
  * included; tokens of the chunk after row m among them). Products are accumulated in fp32 and
  * the softmax's sums are fp32. In bf16 and over E4M3 the weights of the values (with E4M3 times
- * the values' scales) are rounded to bf16. Scores beyond fp32's range give NaN.
+ * the values' scales) are rounded to bf16, 8 bits, where xmod_cache_attention keeps 16 (11 at
+ * least with E4M3). Scores beyond fp32's range give NaN. Sums are divided by the weights' at the
+ * end: rows for which 2^8 sum_i (p_i / max p) |V_i| passes fp32's range are infinite or NaN.
  * Device checks (status word of ws): a chunk whose sequence is not below n_seqs, or whose start
  * entries lie outside 0 .. M or descend, is skipped; a len outside its range is clamped into
  * it; a page outside [0, n_pages) is read as page 0.

@@ -46,7 +46,9 @@ struct ChunkArgs {
   int group;              // query heads of a KV head
   int hpt, tpt, passes;   // heads and tokens of a segment, passes over a KV head's query heads
   int block_tokens;       // tokens of a block of rows
-  int lead;               // what a segment costs beside its tiles, in tiles (six prompts with 0: 1291 us, with 4: 993)
+  int lead;               // what a segment costs beside its tiles, in tiles: tensor cores 4 (six prompts 993 us,
+                          // with 0 1291), FFMA 1 (six of 100 at 1000 34.6 us, with 0 39.2, with 2 41.0;
+                          // six prompts of up to 2048, 16 and 4 heads of 64: 662, 745, 688)
   int hpt_inverse;        // ceil(2^16 / hpt): r / hpt for r, hpt <= 256 (their product is below 2^16)
   int page_shift;         // log2 of the page size, -1: not a power of two
   int box;                // rows of a TMA box: divides the page size and a tile

@@ -25,10 +25,15 @@
 // hand to the rows that see them and then replaced by zeros.
 //
 // Bound by the tensor pipe and its issue beside the softmax warps: 500 tokens at 131072 of 16
-// and 4 heads of 128 384 us (1.39 PFLOP/s, 0.73 of the measured burst), six prompts of up to
-// 8192 tokens 990 us (1.36; a segment's start and end cost about four of its tiles). Over e4m3
-// by issue: 16 ragged chunks at up to 16384 238 us (0.68 PFLOP/s). Small calls by latency: eight
-// chunks of 4 tokens over 4096 29 us with the join, whose plan takes 3.
+// and 4 heads of 128 380 us (1.41 PFLOP/s, 0.74 of the measured burst; at the power cap 414), six
+// prompts of up to 8192 tokens 990 us (1.40; at the cap 1060; a segment's start and end cost about four
+// of its tiles). Over e4m3 by issue: 16 ragged chunks at up to 16384 238 us (0.68 PFLOP/s). Small
+// calls by latency: eight chunks of 4 tokens over 4096 29 us with the join, whose plan takes 3.
+//
+// The weights are rounded to bf16 (8 bits): P is an operand of the same MMA as V and kind::f16 takes
+// one type for both. Two bf16 parts of P would keep 16 bits, as the attention of single tokens does, at
+// half again the MMAs (twice P V), of the pipe that bounds long chunks. The sums l take the weights
+// before the rounding.
 
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -185,7 +190,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // Two e4m3 codes to bf16, exactly, by way of f16 and fp32 (NaN included; moving the bits to their
-// places by hand takes more instructions).
+// places by hand takes more instructions). The conversion itself ends at f16; the operands are bf16
+// because the queries are, whose range f16 has not.
 __device__ __forceinline__ uint32_t codes2_bf16(uint32_t codes) {
   const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3));
   const float2 f = __half22float2(h);

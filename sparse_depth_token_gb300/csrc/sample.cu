@@ -7,7 +7,7 @@
 // and sums are whole numbers, so that a sum does not depend on its order; weights have units of
 // 2^-62 of the largest and sums 96 bits (in 64 bits, with units that leave room for V weights, 4096 rows
 // take 434 us, but 2^22 logits 27 below one were off by 2^-19 of the row's sum). The row is read from
-// memory once and from L2 twice or three times. Bound by issue (bf16: 80 thousand instructions a
+// memory once and from L2 twice or three times. Bound by issue (bf16: 73 thousand instructions a
 // row, of all its warps, half of them the counts' and the slices' loops), shared memory's turns, the
 // code's way into the instruction cache and the barriers between phases, not by the reads: 4096
 // rows of 50257 bf16 logits with top-p 445 us (924 GB/s), 256 rows of fp32 with all settings 114,
@@ -927,7 +927,7 @@ __device__ __forceinline__ void choose(const SampleArgs& a, Shared& sh, const Ro
         const uint64_t head = (uint64_t)(e > 63 ? whole >> (e - 63) : whole << (63 - e));
         const float f = (float)(head & 0x7fffffffffffffffull) * 0x1p-63f;
         const float n = (float)(e - kUnit);
-        constexpr float kLn2Hi = 0.693145752f, kLn2Lo = 1.42860677e-6f;   // the first of 17 bits
+        constexpr float kLn2Hi = 0.693145752f, kLn2Lo = 1.42860677e-6f;   // the first of 15 bits: exact times n
         const float big = q - n * kLn2Hi, rest2 = (q - big) - n * kLn2Hi;
         a.logp[r] = big + (rest2 + ((qq - n * kLn2Lo) - log1pf(f)));
       }
@@ -1130,7 +1130,10 @@ int xmod_sample_tokens(xmod_dtype dt, int64_t N, int V, const void* logits, int6
   a.logp = logp;
   a.status = status_out;
   const Ctx c{(cudaStream_t)stream, status_out};
-  // few rows: one CTA an SM with twice the threads
+  // A row an SM: twice the threads (152 rows of 50257 with top-p, us: bf16 23.1, with 512 threads 24.3;
+  // fp32 60 and 80; rows of 1000 13.3 and 11.8, 17.3 and 16.9). More: two CTAs an SM (153 rows of
+  // bf16 33.0, with 1024 threads 40.1, 608 rows 70 and 92; fp32 111 and 110, 234 and 244; rows of 1000
+  // 15 and 22).
   if (N <= device_sms())
     XMOD_LAUNCH(c, "sample_tokens", (dt == XMOD_BF16 ? launch_sample<__nv_bfloat16, 1024>(c, a)
                                                      : launch_sample<float, 1024>(c, a)));
