@@ -416,7 +416,9 @@ cache_chunk_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
       for (int tile = first; tile < last && ok; ++tile, ++it) {
         if (lane == 0 && (it & 1023) == 0) abort_flag[1] = it >> 10;
         const int next = tile + 1 < last ? page_of(tile + 1) : 0;
-        const int valid = max(0, min(KB, w.limit - tile * KB)), boxes = (valid + a.box - 1) / a.box;
+        // A tile without keys loads a box as well (of page 0, seen by no row): there at once, it would
+        // complete FULL again before the softmax of the tile that had its stage waited for that.
+        const int valid = max(1, min(KB, w.limit - tile * KB)), boxes = (valid + a.box - 1) / a.box;
         int pg = page;
         if (lane < boxes && (pg < 0 || pg >= a.n_pages)) {
           report_status(a.status, XMOD_ERR_DEVICE_CHECK);
