@@ -15,14 +15,14 @@ def X():
     return xmod
 
 
-@pytest.mark.parametrize("kind", sorted(T.KINDS))
+@pytest.mark.parametrize("kind,some,none", [("bf16", 1, 4), ("bf16", 1, 6), ("bf16", 1, 8), ("bf16", 2, 3), ("bf16", 3, 17),
+                                            ("e4m3", 1, 6), ("fp32", 1, 6)])
 @pytest.mark.parametrize("hq,hkv,hd", [(48, 4, 128), (8, 4, 64), (4, 4, 32)])
-@pytest.mark.parametrize("some,none", [(1, 4), (1, 6), (1, 8), (2, 3), (3, 17), (1, 40)])
 def test_runs_of_segments_without_keys(X, kind, hq, hkv, hd, some, none):
     """Segments with keys, all of them masked, then as many without as a ring has stages, more or
     fewer: each is a tile that is there without a load."""
     shape = []
-    while len(shape) * hkv < 152 * 3 * (some + none):
+    while len(shape) * hkv < 152 * 2 * (some + none):
         shape += [(1 + (len(shape) + i) % 3, (30, 64, 2, 75)[(len(shape) + i) % 4]) for i in range(some)]
         shape += [(1 + i % 2, 0) for i in range(-(-none // hkv))]
     s = T._setup(X, kind, hq, hkv, hd, 16, shape)
