@@ -25,8 +25,8 @@
 // hand to the rows that see them and then replaced by zeros.
 //
 // Bound by the tensor pipe and its issue beside the softmax warps: 500 tokens at 131072 of 16
-// and 4 heads of 128 380 us (1.41 PFLOP/s, 0.74 of the measured burst; at the power cap 414), six
-// prompts of up to 8192 tokens 990 us (1.40; at the cap 1060; a segment's start and end cost about four
+// and 4 heads of 128 380 us (1.41 PFLOP/s, 0.74 of the measured burst; at the power cap 406-423), six
+// prompts of up to 8192 tokens 990 us (1.40; at the cap 1057-1082; a segment's start and end cost about four
 // of its tiles). Over e4m3 by issue: 16 ragged chunks at up to 16384 238 us (0.68 PFLOP/s). Small
 // calls by latency: eight chunks of 4 tokens over 4096 29 us with the join, whose plan takes 3.
 //
